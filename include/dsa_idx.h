@@ -73,7 +73,9 @@ typedef enum {
                               defect, never an input error) */
 } dsa_status_t;
 
-typedef enum { DSA_DTYPE_F32 = 0, DSA_DTYPE_BF16 = 1 } dsa_dtype_t;
+/* DSA_DTYPE_OPERAND (dsa_idx_cache_write only): rows that are scoring operands
+ * already, codes with their scales, in the format of the cache. */
+typedef enum { DSA_DTYPE_F32 = 0, DSA_DTYPE_BF16 = 1, DSA_DTYPE_OPERAND = 2 } dsa_dtype_t;
 
 /* Scoring precision.  DSA_PREC_FP8: E4M3 with one UE8M0 scale per vector
  * (the SM90 path's per-vector FP8 scoring, [P1] "What does this PR do?"):
@@ -334,8 +336,121 @@ dsa_status_t dsa_idx_score_topk_noalloc(
  * dsa_idx_read_status; do not call it while capturing a graph. */
 dsa_status_t dsa_idx_score_topk_noalloc_status(dsa_stream_t stream, dsa_status_t* out);
 
+/* ---------------------------------------------------------------------------
+ * Paged cache: writing new tokens, reading back, attention.
+ *
+ * The serving side of the indexer.  Index keys (a cache of keys alone, one
+ * head) and the keys and values that are attended to live in pages; a chunk of
+ * new tokens (or one token) of every sequence enters the cache, is scored
+ * against the sequence's index keys so far (dsa_idx_cache_read gives
+ * dsa_idx_score_topk_kv its key operand) and attends to the selected rows.
+ *
+ *   pages        device [num_pages, n_kv_heads, page_size, head_dim]: bf16
+ *                (BF16) or e4m3 codes (MXFP8, FP8); page_size a power of two
+ *                in [8, 1024], head_dim 64 or 128, fewer than 2^32 rows in all
+ *   page scales  device u8 [num_pages, n_kv_heads, page_size, head_dim/32]
+ *                (MXFP8) or [num_pages, n_kv_heads, page_size] (FP8), else NULL
+ *   page_table   device int32 [num_seqs, max_pages]: position p of sequence d
+ *                is slot p % page_size of page page_table[d, p / page_size].
+ *                Entries behind a sequence's last page are never read;
+ *                sequences may share pages that are not written
+ *   cu_seqlens_q device int32 [num_seqs+1]: prefix of the new tokens T_d
+ *   cu_seqlens_k device int32 [num_seqs+1]: prefix of the cached tokens S_d,
+ *                the new ones included: the T_d new tokens of a sequence are
+ *                its last (the convention of dsa_idx_score_topk_kv), T_d >= 0
+ *   total_q, total_k  rows of the packed tensors.  cu_seqlens[num_seqs] may be
+ *                smaller (a padded batch): rows behind it are left as they were
+ *   v, v_pages   NULL for a cache of keys alone
+ *   ws           device workspace, 256-byte aligned; its status is read with
+ *                dsa_idx_read_status.  Calls that may overlap on the GPU need
+ *                a workspace each
+ * T_d > S_d, a position behind max_pages, a page outside [0, num_pages) and a
+ * prefix that ends above its total are found on the device:
+ * DSA_ERR_INVALID_ARG in the status; nothing outside the caller's tensors is
+ * touched, and the rows concerned are not written (write, read) or
+ * unspecified (attention).
+ * ------------------------------------------------------------------------- */
+
+/* Workspace bytes of dsa_idx_cache_write and dsa_idx_cache_read. */
+size_t dsa_idx_cache_workspace_size(void);
+
+/* Store the new tokens' rows at their positions, in the format of the cache
+ * (quantised as by dsa_idx_quantize_mxfp8 / dsa_idx_quantize_fp8_rows; BF16:
+ * rounded to nearest even).
+ *   k, v       device [total_q, n_kv_heads, head_dim] in_dtype, 16-byte
+ *              aligned; k_stride, v_stride: elements from one token to the
+ *              next (0 = packed; a multiple of 16 bytes), heads packed inside
+ *   k_scale, v_scale  DSA_DTYPE_OPERAND with an 8-bit cache: the packed rows'
+ *              scale bytes, as dsa_idx_preprocess writes them; else NULL
+ * Two tokens of one call must not share a slot (the result is one of the two).
+ * Non-finite elements give unspecified codes, as in the quantisers.
+ * total_q * n_kv_heads < 2^30. */
+dsa_status_t dsa_idx_cache_write(
+    const void* k, int64_t k_stride, const uint8_t* k_scale,
+    const void* v, int64_t v_stride, const uint8_t* v_scale,
+    dsa_dtype_t in_dtype, dsa_mx_scale_rule_t scale_rule,
+    const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int num_seqs,
+    int total_q, const int32_t* page_table, int max_pages,
+    void* k_pages, uint8_t* k_page_scale, void* v_pages, uint8_t* v_page_scale,
+    int num_pages, int page_size, int n_kv_heads, int head_dim,
+    dsa_precision_t prec, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* Rows 0 .. S_d - 1 of every sequence, packed in cu_seqlens_k's order.
+ *   dequantize  0: as stored (codes and scales: with n_kv_heads = 1 the key
+ *               operand of dsa_idx_score_topk_kv); 1: BF16 values code * 2^e
+ *               (exact while the value is in BF16's range)
+ *   k_out, v_out  device [total_k, n_kv_heads, head_dim], codes or bf16;
+ *               v_out NULL: keys alone
+ *   k_scale_out, v_scale_out  device u8 [total_k, n_kv_heads, head_dim/32] or
+ *               [total_k, n_kv_heads]; not used with BF16 or dequantize
+ * total_k * n_kv_heads < 2^30. */
+dsa_status_t dsa_idx_cache_read(
+    const void* k_pages, const uint8_t* k_page_scale, const void* v_pages,
+    const uint8_t* v_page_scale, int num_pages, int page_size, int n_kv_heads,
+    int head_dim, dsa_precision_t prec, const int32_t* page_table,
+    int max_pages, const int32_t* cu_seqlens_k, int num_seqs, int total_k,
+    int dequantize, void* k_out, uint8_t* k_scale_out, void* v_out,
+    uint8_t* v_scale_out, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* Workspace bytes of dsa_idx_paged_attention for these sizes (status, partial
+ * results of long key ranges).  0 for invalid sizes. */
+size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqlen_q, int n_heads,
+                                        int n_kv_heads, int head_dim, int topk_width);
+
+/* Attention of the new tokens over the cache: with G = n_heads / n_kv_heads,
+ *   out[t, h] = sum_s softmax_s(sm_scale * q[t, h] . k[s, h / G]) v[s, h / G]
+ * over the keys s that query t of sequence d (position P = S_d - T_d + t) sees:
+ * 0 .. P, or with topk_idx the listed ones of them.
+ *   q           device bf16 [total_q, n_heads, head_dim], 16-byte aligned;
+ *               q_stride: elements from one token to the next (0 = packed)
+ *   topk_idx    device int32 [total_q, topk_width] or NULL: positions as
+ *               dsa_idx_score_topk / _kv write them, in any order.  Entries
+ *               < 0 and entries > P are not seen; a position listed twice
+ *               counts twice
+ *   topk_len    device int32 [total_q] or NULL: only the first topk_len
+ *               entries of a row are looked at
+ *   out         device bf16 [total_q, n_heads, head_dim]
+ *   lse         device fp32 [total_q, n_heads] or NULL: log of the sum of
+ *               exp(sm_scale q.k) over the seen keys
+ * A query that sees no key gets out = 0 and lse = -inf.  sm_scale is finite and
+ * not negative; n_heads a multiple of n_kv_heads, at most 128 heads to one;
+ * max_seqlen_q and max_seqlen_k bound T_d and S_d (a longer sequence is
+ * reported in the status and not computed).  Rows 0 .. S_d - 1 of a sequence
+ * must be finite; what other slots of its pages hold does not matter.
+ * The same inputs give the same bits. */
+dsa_status_t dsa_idx_paged_attention(
+    const void* q, int64_t q_stride, const void* k_pages,
+    const uint8_t* k_page_scale, const void* v_pages,
+    const uint8_t* v_page_scale, int num_pages, int page_size, int n_heads,
+    int n_kv_heads, int head_dim, dsa_precision_t prec,
+    const int32_t* page_table, int max_pages, const int32_t* cu_seqlens_q,
+    const int32_t* cu_seqlens_k, int num_seqs, int total_q, int max_seqlen_q,
+    int max_seqlen_k, float sm_scale, const int32_t* topk_idx,
+    const int32_t* topk_len, int topk_width, void* out, float* lse,
+    void* ws, size_t ws_bytes, dsa_stream_t stream);
+
 /* Synchronise `stream` and return the device status word recorded in `ws` by
- * the last dsa_idx_score_topk call on it (DSA_OK if none).  Eager helper; do
+ * the last call that was given it (DSA_OK if none).  Eager helper; do
  * not call it while capturing a graph. */
 dsa_status_t dsa_idx_read_status(const void* ws, dsa_stream_t stream,
                                  dsa_status_t* out);

@@ -17,10 +17,14 @@ from . import _abi
 from ._abi import (DSA_FLAG_COMPRESSED_KEYS, DSA_FLAG_DETERMINISTIC, DSA_FLAG_KPOOL_TAIL,  # noqa: F401
                    DSA_FLAG_SORT_BY_SCORE,
                    DSA_PREC_BF16, DSA_PREC_FP8, DSA_PREC_MXFP8)
+from .paged import (PagedCache, attention_workspace, cache_read, cache_workspace, cache_write,  # noqa: F401
+                    paged_attention, paged_cache)
 
 __all__ = [
     "DsaError", "preprocess", "quantize_mxfp8", "quantize_fp8_rows", "kpool_compress", "score_topk", "score_topk_kv", "workspace",
     "read_status", "debug_mma_tile", "output_width",
+    "PagedCache", "paged_cache", "cache_write", "cache_read", "paged_attention", "cache_workspace",
+    "attention_workspace",
 ]
 
 

@@ -23,6 +23,7 @@ DSA_ERR_BOUNDS = 6
 # dsa_dtype_t
 DSA_DTYPE_F32 = 0
 DSA_DTYPE_BF16 = 1
+DSA_DTYPE_OPERAND = 2
 # dsa_precision_t
 DSA_PREC_BF16 = 0
 DSA_PREC_MXFP8 = 1
@@ -35,6 +36,9 @@ DSA_FLAG_DETERMINISTIC = 0x1
 DSA_FLAG_SORT_BY_SCORE = 0x2
 DSA_FLAG_KPOOL_TAIL = 0x4
 DSA_FLAG_COMPRESSED_KEYS = 0x8
+
+# dsa_idx_cache_workspace_size() (checked by the library)
+DSA_CACHE_WS_BYTES = 8192
 
 _c_int, _c_i64, _c_f, _c_size, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
 
@@ -62,6 +66,16 @@ SIGNATURES = {
                                             _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
                                             _vp, _vp, _vp, _vp]),
     "dsa_idx_score_topk_noalloc_status": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
+    "dsa_idx_cache_workspace_size": (_c_size, []),
+    "dsa_idx_cache_write": (_c_int, [_vp, _c_i64, _vp, _vp, _c_i64, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int,
+                                     _vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                     _vp, _c_size, _vp]),
+    "dsa_idx_cache_read": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp,
+                                    _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "dsa_idx_attention_workspace_size": (_c_size, [_c_int] * 7),
+    "dsa_idx_paged_attention": (_c_int, [_vp, _c_i64, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                         _c_int, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_f, _vp,
+                                         _vp, _c_int, _vp, _vp, _vp, _c_size, _vp]),
     "dsa_idx_read_status": (_c_int, [_vp, _vp, ctypes.POINTER(_c_int)]),
     "dsa_idx_debug_mma_tile": (_c_int, [_vp, _vp, _c_i64, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_int,
                                         _c_int, _c_int, _vp, _vp, _c_size, _vp]),

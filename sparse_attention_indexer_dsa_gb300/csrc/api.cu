@@ -16,6 +16,7 @@
 #include "dsa_idx_testing.h"
 #include "dsa_status_codes.h"
 #include "dsa_params.h"
+#include "host_util.h"
 
 
 using namespace dsa;
@@ -27,13 +28,10 @@ thread_local std::string g_last_error;
 }  // namespace
 
 namespace dsa {
+
 // Set the message dsa_idx_last_error() returns (for entry points in other files).
 void set_last_error(const std::string& msg) { g_last_error = msg; }
-}  // namespace dsa
 
-namespace {
-
-dsa_status_t fail(dsa_status_t s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 dsa_status_t fail(dsa_status_t s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -48,13 +46,7 @@ dsa_status_t cuda_fail(cudaError_t e, const char* what) {
   return fail(DSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Device facts, cached per device ordinal.
-struct DevInfo {
-  int sm_count = 0, major = 0, minor = 0;
-};
-
 dsa_status_t device_info(DevInfo* out) {
   static std::mutex mu;
   static DevInfo cache[64];
@@ -76,6 +68,10 @@ dsa_status_t device_info(DevInfo* out) {
     return fail(DSA_ERR_UNSUPPORTED, "built for sm_103a; device is sm_%d%d", out->major, out->minor);
   return DSA_OK;
 }
+
+}  // namespace dsa
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -147,6 +143,11 @@ unsigned long long g_timeout_ns = 2000000000ull;
 int g_fault_inject = 0;
 
 }  // namespace
+
+namespace dsa {
+unsigned long long wait_timeout_ns() { return g_timeout_ns; }
+int fault_inject_mode() { return g_fault_inject; }
+}  // namespace dsa
 
 extern "C" {
 
@@ -474,6 +475,13 @@ dsa_status_t dsa_idx_read_status(const void* ws, dsa_stream_t stream, dsa_status
   int h = 0;
   e = cudaMemcpy(&h, ws, sizeof(int), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
+  if (h == DSA_DEV_STATUS_PER_BLOCK) {   // one word per block: the first that is not 0
+    static thread_local int hdr[DSA_DEV_STATUS_HEADER_BYTES / 4];
+    e = cudaMemcpy(hdr, ws, sizeof(hdr), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail(e, "status read");
+    h = 0;
+    for (int b = 0; b < hdr[1] && b < DSA_DEV_STATUS_MAX_BLOCKS && h == 0; ++b) h = hdr[DSA_DEV_STATUS_FIRST + b];
+  }
   *out = (dsa_status_t)h;
   return DSA_OK;
 }

@@ -1,0 +1,218 @@
+// C ABI of the paged-cache operators (include/dsa_idx.h): host-side validation
+// and launches.  Never allocates, frees or synchronises.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "dsa_idx.h"
+#include "dsa_status_codes.h"
+#include "host_util.h"
+#include "paged_params.h"
+
+using namespace dsa;
+
+namespace {
+
+// Checks shared by the three operators; fills the device view.
+dsa_status_t check_cache(PagedCacheView* c, const void* k_pages, const uint8_t* k_page_scale, const void* v_pages,
+                         const uint8_t* v_page_scale, int num_pages, int page_size, int n_kv_heads, int head_dim,
+                         dsa_precision_t prec, const int32_t* page_table, int max_pages, int num_seqs,
+                         const int32_t* cu_seqlens_k) {
+  if (!k_pages || !page_table || !cu_seqlens_k) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (prec != DSA_PREC_BF16 && prec != DSA_PREC_MXFP8 && prec != DSA_PREC_FP8) return fail(DSA_ERR_INVALID_ARG, "prec");
+  if (head_dim != 64 && head_dim != 128) return fail(DSA_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (num_pages < 1 || n_kv_heads < 1 || max_pages < 1 || num_seqs < 1) return fail(DSA_ERR_INVALID_ARG, "sizes");
+  if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+    return fail(DSA_ERR_UNSUPPORTED, "page_size must be a power of two in [8, 1024]");
+  if ((int64_t)num_pages * n_kv_heads >= (int64_t)0xFFFFFFFF / page_size)
+    return fail(DSA_ERR_UNSUPPORTED, "a cache holds fewer than 2^32 rows");
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return fail(DSA_ERR_INVALID_ARG, "pages must be 16-byte aligned");
+  if (prec != DSA_PREC_BF16) {
+    if (!k_page_scale || (v_pages && !v_page_scale)) return fail(DSA_ERR_INVALID_ARG, "8-bit caches need their scales");
+    if (!aligned16(k_page_scale) || !aligned16(v_page_scale))
+      return fail(DSA_ERR_INVALID_ARG, "page scales must be 16-byte aligned");
+  }
+  c->k = const_cast<void*>(k_pages);
+  c->k_scale = const_cast<uint8_t*>(k_page_scale);
+  c->v = const_cast<void*>(v_pages);
+  c->v_scale = const_cast<uint8_t*>(v_page_scale);
+  c->table = page_table;
+  c->num_pages = num_pages;
+  c->page_shift = 0;
+  while ((1 << c->page_shift) < page_size) ++c->page_shift;
+  c->n_kv = n_kv_heads;
+  c->max_pages = max_pages;
+  c->fmt = (int)prec;
+  c->sw = prec == DSA_PREC_MXFP8 ? head_dim / 32 : (prec == DSA_PREC_FP8 ? 1 : 0);
+  return DSA_OK;
+}
+
+dsa_status_t check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (!ws) return fail(DSA_ERR_WORKSPACE, "workspace is NULL");
+  if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, need);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(DSA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return DSA_OK;
+}
+
+// Token stride of a [tokens, heads, head_dim] tensor: 0 = packed.
+dsa_status_t check_stride(int64_t* stride, int heads, int head_dim, int elem_bytes, const char* name) {
+  const int64_t packed = (int64_t)heads * head_dim;
+  if (*stride == 0) *stride = packed;
+  if (*stride < packed || (*stride * elem_bytes) % 16 != 0)
+    return fail(DSA_ERR_INVALID_ARG, "%s: a token stride covers its heads and is a multiple of 16 bytes", name);
+  return DSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dsa_idx_cache_workspace_size(void) { return DSA_DEV_STATUS_HEADER_BYTES; }
+
+dsa_status_t dsa_idx_cache_write(const void* k, int64_t k_stride, const uint8_t* k_scale, const void* v, int64_t v_stride,
+                                 const uint8_t* v_scale, dsa_dtype_t in_dtype, dsa_mx_scale_rule_t scale_rule,
+                                 const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int num_seqs, int total_q,
+                                 const int32_t* page_table, int max_pages, void* k_pages, uint8_t* k_page_scale,
+                                 void* v_pages, uint8_t* v_page_scale, int num_pages, int page_size, int n_kv_heads,
+                                 int head_dim, dsa_precision_t prec, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  CacheWriteParams p{};
+  dsa_status_t s = check_cache(&p.c, k_pages, k_page_scale, v_pages, v_page_scale, num_pages, page_size, n_kv_heads,
+                               head_dim, prec, page_table, max_pages, num_seqs, cu_seqlens_k);
+  if (s != DSA_OK) return s;
+  if ((!k && total_q > 0) || !cu_seqlens_q) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (total_q > 0 && (v != nullptr) != (v_pages != nullptr))
+    return fail(DSA_ERR_INVALID_ARG, "v and v_pages must both be given or both be NULL");
+  if (total_q < 0) return fail(DSA_ERR_INVALID_ARG, "sizes");
+  if ((int64_t)total_q * n_kv_heads >= (int64_t)1 << 30) return fail(DSA_ERR_UNSUPPORTED, "total_q * n_kv_heads above 2^30");
+  if (scale_rule != DSA_MX_SCALE_NOSAT && scale_rule != DSA_MX_SCALE_FLOOR) return fail(DSA_ERR_INVALID_ARG, "scale_rule");
+  int elem;
+  if (in_dtype == DSA_DTYPE_OPERAND && prec != DSA_PREC_BF16) {
+    if (!k_scale || (v && !v_scale)) return fail(DSA_ERR_INVALID_ARG, "codes come with their scales");
+    p.src = 2;
+    elem = 1;
+  } else if (in_dtype == DSA_DTYPE_F32) {
+    p.src = 0;
+    elem = 4;
+  } else if (in_dtype == DSA_DTYPE_BF16 || in_dtype == DSA_DTYPE_OPERAND) {   // a BF16 cache stores the operand itself
+    p.src = 1;
+    elem = 2;
+  } else {
+    return fail(DSA_ERR_INVALID_ARG, "in_dtype");
+  }
+  if (!aligned16(k) || !aligned16(v)) return fail(DSA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+  if ((s = check_stride(&k_stride, n_kv_heads, head_dim, elem, "k")) != DSA_OK) return s;
+  if (v && (s = check_stride(&v_stride, n_kv_heads, head_dim, elem, "v")) != DSA_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, DSA_DEV_STATUS_HEADER_BYTES)) != DSA_OK) return s;
+  DevInfo di;
+  if ((s = device_info(&di)) != DSA_OK) return s;
+  p.k = k;
+  p.v = v;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.num_seqs = num_seqs;
+  p.total_q = total_q;
+  p.rule = (int)scale_rule;
+  p.hdr = reinterpret_cast<int*>(ws);
+  cudaError_t e = launch_cache_write(p, head_dim, di.sm_count, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
+  return DSA_OK;
+}
+
+dsa_status_t dsa_idx_cache_read(const void* k_pages, const uint8_t* k_page_scale, const void* v_pages,
+                                const uint8_t* v_page_scale, int num_pages, int page_size, int n_kv_heads, int head_dim,
+                                dsa_precision_t prec, const int32_t* page_table, int max_pages,
+                                const int32_t* cu_seqlens_k, int num_seqs, int total_k, int dequantize, void* k_out,
+                                uint8_t* k_scale_out, void* v_out, uint8_t* v_scale_out, void* ws, size_t ws_bytes,
+                                dsa_stream_t stream) {
+  CacheReadParams p{};
+  dsa_status_t s = check_cache(&p.c, k_pages, k_page_scale, v_pages, v_page_scale, num_pages, page_size, n_kv_heads,
+                               head_dim, prec, page_table, max_pages, num_seqs, cu_seqlens_k);
+  if (s != DSA_OK) return s;
+  if (!k_out && total_k > 0) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (v_out && !v_pages) return fail(DSA_ERR_INVALID_ARG, "the cache has no values");
+  if (total_k < 0) return fail(DSA_ERR_INVALID_ARG, "sizes");
+  if ((int64_t)total_k * n_kv_heads >= (int64_t)1 << 30) return fail(DSA_ERR_UNSUPPORTED, "total_k * n_kv_heads above 2^30");
+  if (prec != DSA_PREC_BF16 && !dequantize && (!k_scale_out || (v_out && !v_scale_out)))
+    return fail(DSA_ERR_INVALID_ARG, "codes come with their scales");
+  if (!aligned16(k_out) || !aligned16(v_out)) return fail(DSA_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
+  if ((s = check_ws(ws, ws_bytes, DSA_DEV_STATUS_HEADER_BYTES)) != DSA_OK) return s;
+  DevInfo di;
+  if ((s = device_info(&di)) != DSA_OK) return s;
+  p.cu_k = cu_seqlens_k;
+  p.num_seqs = num_seqs;
+  p.total_k = total_k;
+  p.dequant = dequantize && prec != DSA_PREC_BF16;
+  p.k = k_out;
+  p.k_scale = k_scale_out;
+  p.v = v_out;
+  p.v_scale = v_scale_out;
+  p.hdr = reinterpret_cast<int*>(ws);
+  cudaError_t e = launch_cache_read(p, head_dim, di.sm_count, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
+  return DSA_OK;
+}
+
+size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqlen_q, int n_heads, int n_kv_heads,
+                                        int head_dim, int topk_width) {
+  if (total_q < 0 || num_seqs < 1 || max_seqlen_q < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 ||
+      topk_width < 0)
+    return 0;
+  (void)head_dim;
+  return DSA_DEV_STATUS_HEADER_BYTES;
+}
+
+dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void* k_pages, const uint8_t* k_page_scale,
+                                     const void* v_pages, const uint8_t* v_page_scale, int num_pages, int page_size,
+                                     int n_heads, int n_kv_heads, int head_dim, dsa_precision_t prec,
+                                     const int32_t* page_table, int max_pages, const int32_t* cu_seqlens_q,
+                                     const int32_t* cu_seqlens_k, int num_seqs, int total_q, int max_seqlen_q,
+                                     int max_seqlen_k, float sm_scale, const int32_t* topk_idx, const int32_t* topk_len,
+                                     int topk_width, void* out, float* lse, void* ws, size_t ws_bytes,
+                                     dsa_stream_t stream) {
+  AttnParams p{};
+  dsa_status_t s = check_cache(&p.c, k_pages, k_page_scale, v_pages, v_page_scale, num_pages, page_size, n_kv_heads,
+                               head_dim, prec, page_table, max_pages, num_seqs, cu_seqlens_k);
+  if (s != DSA_OK) return s;
+  if (!v_pages || !cu_seqlens_q || (total_q > 0 && (!q || !out))) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0) return fail(DSA_ERR_INVALID_ARG, "sizes");
+  if (n_heads < 1 || n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 128)
+    return fail(DSA_ERR_UNSUPPORTED, "n_heads must be a multiple of n_kv_heads, at most 128 heads to one");
+  if ((int64_t)total_q * n_heads >= (int64_t)1 << 31) return fail(DSA_ERR_UNSUPPORTED, "total_q * n_heads above 2^31");
+  if (!(sm_scale >= 0.f) || std::isinf(sm_scale)) return fail(DSA_ERR_INVALID_ARG, "sm_scale must be finite and >= 0");
+  if (topk_idx ? topk_width < 1 : (topk_width != 0 || topk_len != nullptr))
+    return fail(DSA_ERR_INVALID_ARG, "topk_width and topk_len belong to topk_idx");
+  if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if ((s = check_stride(&q_stride, n_heads, head_dim, 2, "q")) != DSA_OK) return s;
+  const size_t need = dsa_idx_attention_workspace_size(total_q, num_seqs, max_seqlen_q, n_heads, n_kv_heads, head_dim,
+                                                       topk_width);
+  if ((s = check_ws(ws, ws_bytes, need)) != DSA_OK) return s;
+  DevInfo di;
+  if ((s = device_info(&di)) != DSA_OK) return s;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.topk_idx = topk_idx;
+  p.topk_len = topk_len;
+  p.topk_width = topk_width;
+  p.num_seqs = num_seqs;
+  p.total_q = total_q;
+  p.max_seqlen_q = max_seqlen_q;
+  p.max_seqlen_k = max_seqlen_k;
+  p.n_heads = n_heads;
+  p.group = n_heads / n_kv_heads;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.out = out;
+  p.lse = lse;
+  p.hdr = reinterpret_cast<int*>(ws);
+  p.timeout_ns = wait_timeout_ns();
+  cudaError_t e = launch_paged_attention(p, head_dim, di.sm_count, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  return DSA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,104 @@
+// Parameter blocks and launchers of the paged-cache operators (paged_cache.cu,
+// paged_attn.cu) and the device view of a paged cache.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dsa_status_codes.h"
+
+namespace dsa {
+
+// Pages [num_pages][n_kv][page_size][D]; the rows of one (page, head) are
+// contiguous.  Scales follow the same order, `sw` bytes per row.
+struct PagedCacheView {
+  void* k;
+  uint8_t* k_scale;
+  void* v;            // null: a cache of keys alone
+  uint8_t* v_scale;
+  const int32_t* table;   // [num_seqs][max_pages]
+  int num_pages, page_shift, n_kv, max_pages;
+  int fmt;            // dsa_precision_t
+  int sw;             // scale bytes per row (0 for BF16)
+};
+
+struct CacheWriteParams {
+  PagedCacheView c;
+  const void* k;
+  const void* v;
+  const uint8_t* k_scale;   // source in operand form: its scale bytes
+  const uint8_t* v_scale;
+  int64_t k_stride, v_stride;   // elements from one token to the next
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int num_seqs, total_q;
+  int src;            // 0 FP32, 1 BF16, 2 operand form (codes and scales)
+  int rule;
+  int* hdr;
+};
+
+struct CacheReadParams {
+  PagedCacheView c;
+  const int32_t* cu_k;
+  int num_seqs, total_k;
+  int dequant;        // 0: rows and scales as stored, 1: BF16 values
+  void* k;
+  uint8_t* k_scale;
+  void* v;
+  uint8_t* v_scale;
+  int* hdr;
+};
+
+struct AttnParams {
+  PagedCacheView c;
+  const void* q;
+  int64_t q_stride;   // elements from one token to the next
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* topk_idx;   // null: every visible key
+  const int32_t* topk_len;
+  int topk_width;
+  int num_seqs, total_q, max_seqlen_q, max_seqlen_k, n_heads, group;
+  float scale_log2;   // sm_scale * log2(e)
+  void* out;
+  float* lse;
+  int* hdr;
+  unsigned long long timeout_ns;
+};
+
+cudaError_t launch_cache_write(const CacheWriteParams& p, int D, int sm_count, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheReadParams& p, int D, int sm_count, cudaStream_t stream);
+cudaError_t launch_paged_attention(const AttnParams& p, int D, int sm_count, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// Sequence of packed row `r`: the last d with cu[d] <= r (cu[0] = 0).
+__device__ __forceinline__ int find_seq(const int32_t* __restrict__ cu, int num_seqs, int r) {
+  int lo = 0, hi = num_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(cu + mid) <= r) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Row of the cache (in rows of D elements) that holds position `pos` of
+// sequence `d`, head `h`; -1 where the table or the page list does not cover it.
+__device__ __forceinline__ int64_t cache_row(const PagedCacheView& c, int d, int pos, int h) {
+  const int pi = pos >> c.page_shift;
+  if (pos < 0 || pi >= c.max_pages) return -1;
+  const int page = __ldg(c.table + (int64_t)d * c.max_pages + pi);
+  if ((unsigned)page >= (unsigned)c.num_pages) return -1;
+  return (((int64_t)page * c.n_kv + h) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
+}
+
+// Every block of a launch records its status (0 or an error code).
+__device__ __forceinline__ void put_block_status(int* hdr, int code) {
+  hdr[DSA_DEV_STATUS_FIRST + blockIdx.x] = code;
+  if (blockIdx.x == 0) {
+    hdr[0] = DSA_DEV_STATUS_PER_BLOCK;
+    hdr[1] = gridDim.x;
+  }
+}
+#endif
+
+}  // namespace dsa

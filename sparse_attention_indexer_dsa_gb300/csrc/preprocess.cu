@@ -27,6 +27,7 @@
 
 #include "dsa_device.cuh"
 #include "dsa_params.h"
+#include "mx_scale.cuh"
 
 namespace dsa {
 
@@ -40,24 +41,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-
-// UE8M0 exponent of a block from the bit pattern of its max magnitude
-// (sign cleared).  With amax = m * 2^E, m in [1, 2), the smallest e with
-// amax <= 448 * 2^e = 1.75 * 2^(e+8) is E - 8, plus one when m > 1.75 (mantissa
-// field above 0x600000).  Adding 0x1FFFFF to the bit pattern carries into the
-// exponent field exactly in that case, so the NOSAT exponent is
-// ((bits + 0x1FFFFF) >> 23) - 135 and the FLOOR exponent (bits >> 23) - 135.
-// Zero, subnormal and tiny magnitudes land at or below -127 and clamp there;
-// the largest pattern (NaN) gives 121, so no upper clamp is needed.
-__device__ __forceinline__ int mx_exponent_bits(uint32_t amax_bits, uint32_t carry) {
-  return max((int)((amax_bits + carry) >> 23) - 135, -127);
-}
-
-// mantissa carry for the rule: 0 = NOSAT, 1 = FLOOR
-__device__ __forceinline__ uint32_t mx_carry(int rule) { return rule == 1 ? 0u : 0x1FFFFFu; }
-
-// 2^-e as a float for e in [-127, 121] (always a normal number)
-__device__ __forceinline__ float exp2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 
 // Quantise one block of 4*GL elements spread over GL consecutive lanes (4
 // values per lane): GL = 8 is an MXFP8 block of 32, GL = 32 a whole 128-element
