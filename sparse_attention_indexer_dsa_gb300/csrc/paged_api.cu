@@ -63,7 +63,78 @@ dsa_status_t check_stride(int64_t* stride, int heads, int head_dim, int elem_byt
   return DSA_OK;
 }
 
+uint32_t round16(uint32_t x) { return (x + 15) / 16 * 16; }
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
 }  // namespace
+
+namespace dsa {
+
+// Two query tiles to a block when the average sequence fills more than one
+// 128-row tile: its keys are then read once for both.  Otherwise the two
+// streams of a block work on their own.  Key ranges are divided only while
+// there are at most four units to a stream (more balance themselves), and a
+// call's workspace has room for four more units to a stream.
+bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, bool eight_bit,
+               int topk_width) {
+  *pl = AttnPlan{};
+  const int group = n_heads / n_kv;
+  pl->tq = topk_width > 0 ? 1 : kAttnRows / group;
+  pl->pair = topk_width == 0 && max_seqlen_q > pl->tq && (int64_t)total_q * group > (int64_t)kAttnRows * num_seqs;
+  const int tok = pl->tq < max_seqlen_q ? pl->tq : (max_seqlen_q > 0 ? max_seqlen_q : 1);
+  pl->rows_cap = tok * group;
+  const int per = pl->pair ? 2 * pl->tq : pl->tq;
+  // every tile but a sequence's last is full, and a tile holds a token at least
+  int64_t tiles = (int64_t)total_q / per + num_seqs;
+  if (tiles > total_q) tiles = total_q;
+  const int64_t base = tiles * n_kv;
+  const int64_t streams = pl->pair ? kAttnSms : 2 * kAttnSms;
+  const int64_t few = pl->pair ? 2 : 4;
+  pl->max_units = base <= few * streams ? (int)(base + few * streams) : 0;
+  const int qrows = pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
+  pl->q_bytes = (uint32_t)qrows * D * 2;
+  const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys * D;
+  for (pl->streams = 2; pl->streams >= 1; --pl->streams) {
+    const uint32_t rings = pl->pair ? 1 : pl->streams;
+    const uint32_t rows = rings * (eight_bit ? 4 : 2) * kAttnKeys * 4, scale = eight_bit ? rings * 4 * 2 * kAttnKeys * 4 : 0;
+    const uint32_t mask = 2 * 8 * 4 * 4, bars = 512, tab = round16((128 + 1) * 4);
+    const uint32_t q = 2 * pl->q_bytes, tail = rows + scale + mask + bars + tab;
+    if (q + tail > kAttnSmemMax) continue;
+    const uint32_t avail = kAttnSmemMax - q - tail;
+    if (eight_bit) {
+      pl->nst = pl->pair || rings == 1 ? 3 : 2;
+      if (avail < rings * (pl->nst * stage + raw)) continue;
+      pl->nraw = (int)((avail - rings * pl->nst * stage) / (rings * raw));
+      if (pl->nraw > 4) pl->nraw = 4;
+    } else {
+      pl->nst = (int)(avail / (rings * stage));
+      if (pl->nst < 2) continue;
+      if (pl->nst > 8) pl->nst = 8;
+      pl->nraw = 0;
+    }
+    pl->off_ring = q;
+    pl->off_raw = pl->off_ring + rings * pl->nst * stage;
+    pl->off_rows = pl->off_raw + rings * pl->nraw * raw;
+    pl->off_scale = pl->off_rows + rows;
+    pl->off_mask = pl->off_scale + scale;
+    pl->off_bars = pl->off_mask + mask;
+    pl->off_tab = pl->off_bars + bars;
+    pl->smem = pl->off_tab + tab;
+    return true;
+  }
+  return false;
+}
+
+size_t attn_workspace_bytes(const AttnPlan& pl, int num_seqs, int D) {
+  size_t n = DSA_DEV_STATUS_HEADER_BYTES;
+  if (pl.max_units > 0) {
+    const size_t slots = (size_t)pl.max_units * (pl.pair ? 2 : 1) * pl.rows_cap;
+    n += round256((size_t)num_seqs * 4) + round256(slots * 8) + round256(slots * D * 4);
+  }
+  return n;
+}
+
+}  // namespace dsa
 
 extern "C" {
 
@@ -159,10 +230,11 @@ dsa_status_t dsa_idx_cache_read(const void* k_pages, const uint8_t* k_page_scale
 size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqlen_q, int n_heads, int n_kv_heads,
                                         int head_dim, int topk_width) {
   if (total_q < 0 || num_seqs < 1 || max_seqlen_q < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 ||
-      topk_width < 0)
+      n_heads / n_kv_heads > kAttnRows || (head_dim != 64 && head_dim != 128) || topk_width < 0)
     return 0;
-  (void)head_dim;
-  return DSA_DEV_STATUS_HEADER_BYTES;
+  AttnPlan pl;   // the workspace does not depend on the cache's format
+  if (!attn_plan(&pl, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, false, topk_width)) return 0;
+  return attn_workspace_bytes(pl, num_seqs, head_dim);
 }
 
 dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void* k_pages, const uint8_t* k_page_scale,
@@ -187,8 +259,10 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
     return fail(DSA_ERR_INVALID_ARG, "topk_width and topk_len belong to topk_idx");
   if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if ((s = check_stride(&q_stride, n_heads, head_dim, 2, "q")) != DSA_OK) return s;
-  const size_t need = dsa_idx_attention_workspace_size(total_q, num_seqs, max_seqlen_q, n_heads, n_kv_heads, head_dim,
-                                                       topk_width);
+  if (!attn_plan(&p.plan, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, prec != DSA_PREC_BF16,
+                 topk_width))
+    return fail(DSA_ERR_UNSUPPORTED, "no kernel configuration fits");
+  const size_t need = attn_workspace_bytes(p.plan, num_seqs, head_dim);
   if ((s = check_ws(ws, ws_bytes, need)) != DSA_OK) return s;
   DevInfo di;
   if ((s = device_info(&di)) != DSA_OK) return s;
@@ -205,12 +279,34 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
   p.max_seqlen_k = max_seqlen_k;
   p.n_heads = n_heads;
   p.group = n_heads / n_kv_heads;
-  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  // a masked logit is -inf times the scale: 0 is stood in for by a scale that no finite logit survives
+  p.scale_log2 = fmaxf(sm_scale * 1.4426950408889634f, 1e-37f);
   p.out = out;
   p.lse = lse;
   p.hdr = reinterpret_cast<int*>(ws);
   p.timeout_ns = wait_timeout_ns();
-  cudaError_t e = launch_paged_attention(p, head_dim, di.sm_count, reinterpret_cast<cudaStream_t>(stream));
+  p.fault_inject = fault_inject_mode();
+  if (p.plan.max_units > 0) {
+    const size_t slots = (size_t)p.plan.max_units * (p.plan.pair ? 2 : 1) * p.plan.rows_cap;
+    uint8_t* w = reinterpret_cast<uint8_t*>(ws) + DSA_DEV_STATUS_HEADER_BYTES;
+    p.doc_base = reinterpret_cast<int*>(w);
+    w += round256((size_t)num_seqs * 4);
+    p.part_ml = reinterpret_cast<float2*>(w);
+    w += round256(slots * 8);
+    p.part_o = reinterpret_cast<float*>(w);
+  }
+  // no more blocks than there can be units
+  const int per = p.plan.pair ? 2 * p.plan.tq : p.plan.tq;
+  const int64_t keys = topk_idx ? topk_width : max_seqlen_k;
+  int64_t bound = ((int64_t)total_q / per + num_seqs) * n_kv_heads * (p.plan.max_units > 0 ? keys / (2 * kAttnKeys) + 1 : 1);
+  if (bound > di.sm_count) bound = di.sm_count;
+  if (bound > DSA_DEV_STATUS_MAX_BLOCKS) bound = DSA_DEV_STATUS_MAX_BLOCKS;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool q8 = prec != DSA_PREC_BF16;
+  cudaError_t e = head_dim == 128 ? (q8 ? launch_paged_attention_128_q8(p, (int)bound, di.sm_count, st)
+                                        : launch_paged_attention_128(p, (int)bound, di.sm_count, st))
+                                  : (q8 ? launch_paged_attention_64_q8(p, (int)bound, di.sm_count, st)
+                                        : launch_paged_attention_64(p, (int)bound, di.sm_count, st));
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return DSA_OK;
 }

@@ -1,0 +1,986 @@
+// Attention of new tokens over a paged cache on the tensor cores:
+//   o[t, h] = sum_s softmax_s(sm_scale q[t, h] . k[s, h / G]) v[s, h / G]
+// over the keys s that token t sees (all positions up to its own, or the
+// listed ones among them).
+//
+// Tiles.  A query tile is 128 rows: tq tokens x the G heads that share a key
+// head (one token when every token has its own list).  Keys come in tiles of
+// 128.  Per tile S = Q K^T (K = head_dim) goes to TMEM, the softmax warps turn
+// it into P = 2^(c S - m) in BF16 in the same TMEM columns, and O += P V reads
+// P from TMEM.  m is the running row maximum (log2 domain), raised only when a
+// row exceeds it by more than 8, so the accumulator in TMEM is rescaled a few
+// times per row instead of once per tile; the sums and O stay in FP32, and 2^8
+// is far inside BF16's range.  P is rounded to BF16 because the PV product has
+// BF16 operands; the sum l adds the unrounded weights.
+//
+// Streams.  One block per SM with two streams, each a TMEM half (S/P 128
+// columns, O head_dim columns), a softmax warpgroup and an MMA warp: while one
+// stream's softmax runs, the tensor core works for the other.
+//   PAIR: the streams hold two neighbouring query tiles and share one ring of
+//         key/value stages (long chunks: the keys are read half as often);
+//   else: the streams are independent, each with its own units and ring
+//         (single tokens, short chunks, selected rows).
+// Four loader warps fill the rings: they resolve position -> page -> row once
+// per tile (one row per thread) and copy the rows with cp.async into the
+// 128-byte swizzled layout the MMA reads; rows that are not there are
+// zero-filled, so nothing outside a sequence's own rows enters a product.
+// 8-bit rows are fetched as stored (cp.async into a thread-private ring) and
+// widened to BF16 on the way into the stage; E4M3 x 2^e is exact in BF16.
+//
+// Units.  (sequence, key head, query tile, range of key tiles).  Every block
+// derives the same list from the prefixes: the number of key tiles per range is
+// the one of eight candidates with the shortest estimated schedule.  Divided
+// ranges leave (O, m, l) in the workspace and a second kernel joins them.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "dsa_device.cuh"
+#include "paged_params.h"
+
+namespace dsa {
+
+namespace attn {
+
+constexpr int kGroups = 128;        // sequences are counted in this many groups
+constexpr int kOverhead = 4;        // start and end of a unit, in key tiles
+constexpr int kSplitOverhead = 6;   // ... when its result is joined later
+constexpr int kMinChunk = 2;
+constexpr int kMaskRing = 8;
+constexpr float kRaise = 8.f;       // log2 of the largest weight before the maximum is raised
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Arrives (without raising the count) once this thread's earlier cp.async have landed.
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The loads' destination registers named, so that no use moves above the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_tied(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16 (BF16 operands, FP32 accumulate)
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Wait while draining after an abort: ignores the abort flag, still bounded.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, kWaitHintNs) && globaltimer_ns() - t0 < timeout_ns) {
+  }
+}
+
+struct Doc {
+  int q0, T, S;
+};
+
+// A sequence's sizes; T = 0 (and false) when they are inconsistent.
+__device__ __forceinline__ bool doc_info(const AttnParams& p, int d, Doc* o) {
+  const int q0 = __ldg(p.cu_q + d), q1 = __ldg(p.cu_q + d + 1);
+  const int k0 = __ldg(p.cu_k + d), k1 = __ldg(p.cu_k + d + 1);
+  o->q0 = q0;
+  o->T = q1 - q0;
+  o->S = k1 - k0;
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.total_q && k1 >= k0 && o->S >= o->T && o->T <= p.max_seqlen_q &&
+                  o->S <= p.max_seqlen_k && (int64_t)o->S <= ((int64_t)p.c.max_pages << p.c.page_shift);
+  if (!ok) o->T = 0;
+  return ok;
+}
+
+// Query tiles (pairs of them with PAIR) and key tiles of a sequence.
+template <bool PAIR>
+__device__ __forceinline__ void doc_tiles(const AttnParams& p, const Doc& o, int* mt, int* kt) {
+  const int per = PAIR ? 2 * p.plan.tq : p.plan.tq;
+  *mt = (o.T + per - 1) / per;
+  *kt = ((p.topk_idx ? p.topk_width : o.S) + kAttnKeys - 1) / kAttnKeys;
+}
+
+__device__ __forceinline__ int splits_of(int kt, int chunk) { return kt <= chunk ? 1 : (kt + chunk - 1) / chunk; }
+
+// One unit as one stream sees it.
+struct Unit {
+  int d, h, split, ns;
+  int q0, P0;        // first packed query row of the sequence, keys before its first query
+  int i0, i1;        // tokens of this stream's tile
+  int last;          // end of the unit's tokens (PAIR: of both tiles)
+  int lo, n;         // first key tile, number of key tiles of this stream
+  int n_shared;      // key tiles the loader brings (PAIR: the longer of the two)
+};
+
+// tab: first unit of each of the kGroups groups of sequences (+ the total).
+template <bool PAIR>
+__device__ __forceinline__ Unit decode_unit(const AttnParams& p, const int* tab, int gsz, int chunk, int u, int w) {
+  int lo = 0, hi = kGroups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tab[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  int rem = u - tab[lo];
+  int d = lo * gsz;
+  Doc o;
+  int mt, kt, ns;
+  for (;;) {
+    doc_info(p, d, &o);
+    doc_tiles<PAIR>(p, o, &mt, &kt);
+    ns = splits_of(kt, chunk);
+    const int units = mt * ns * p.c.n_kv;
+    if (rem < units || d + 1 >= p.num_seqs) break;
+    rem -= units;
+    ++d;
+  }
+  Unit x;
+  x.d = d;
+  x.ns = ns;
+  x.q0 = o.q0;
+  x.P0 = o.S - o.T;
+  x.split = rem % ns;
+  rem /= ns;
+  const int tile = mt - 1 - rem % mt;   // the longest first
+  x.h = rem / mt;
+  const int t = PAIR ? 2 * tile + w : tile;
+  x.i0 = min(t * p.plan.tq, o.T);
+  x.i1 = min(x.i0 + p.plan.tq, o.T);
+  x.last = PAIR ? min((2 * tile + 2) * p.plan.tq, o.T) : x.i1;
+  int kt_own, kt_all;
+  if (p.topk_idx) {
+    int n = p.topk_width;
+    if (p.topk_len) n = max(0, min(n, __ldg(p.topk_len + o.q0 + x.i0)));
+    kt_own = (n + kAttnKeys - 1) / kAttnKeys;
+    kt_all = kt;
+  } else {
+    kt_own = x.i0 < x.i1 ? (x.P0 + x.i1 + kAttnKeys - 1) / kAttnKeys : 0;
+    kt_all = (x.P0 + x.last + kAttnKeys - 1) / kAttnKeys;
+  }
+  const int per = (kt_all + ns - 1) / ns;
+  x.lo = x.split * per;
+  x.n = max(0, min(x.lo + per, kt_own) - x.lo);
+  x.n_shared = PAIR ? max(0, min(x.lo + per, kt_all) - x.lo) : x.n;
+  return x;
+}
+
+__device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+
+template <int D, bool Q8, bool PAIR>
+__global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const __grid_constant__ AttnParams p) {
+  constexpr uint32_t kStage = kAttnKeys * D * 2;     // one tile of keys or values
+  constexpr uint32_t kChunk = kAttnKeys * 128;       // 64 of its columns
+  constexpr int kRings = PAIR ? 1 : 2;
+  constexpr int kLoaders = PAIR ? 128 : 64;          // loader threads per ring
+  constexpr int kRowsPer = kAttnKeys / kLoaders;     // rows a loader thread resolves per tile
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const AttnPlan& pl = p.plan;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_u32(smem);
+  const uint64_t tmo = p.timeout_ns;
+
+  // barriers: per ring full/empty; per stream q_full, q_empty, s_full, p_full, o_full, o_free, drain
+  const uint32_t bars = sbase + pl.off_bars;
+  int* const ctl = reinterpret_cast<int*>(smem + pl.off_bars + 8 * (2 * 8 * 2 + 2 * 8));   // status, abort, tmem base, chunk, units
+  int* const status = ctl;
+  volatile int* const abort_flag = ctl + 1;
+  int* const tab = reinterpret_cast<int*>(smem + pl.off_tab);
+  auto bar_full = [&](int ring, int s) { return bars + 8u * (ring * 16 + s); };
+  auto bar_empty = [&](int ring, int s) { return bars + 8u * (ring * 16 + 8 + s); };
+  auto bar_st = [&](int w, int i) { return bars + 8u * (32 + w * 8 + i); };
+  enum { Q_FULL, Q_EMPTY, S_FULL, P_FULL, O_FULL, O_FREE, DRAIN };
+
+  if (tid == 0) {
+    ctl[0] = (sbase & 1023u) ? DSA_DEV_ERR_BOUNDS : 0;   // the swizzle needs a 1024-byte base
+    ctl[1] = (sbase & 1023u) ? 1 : 0;
+    for (int r = 0; r < kRings; ++r)
+      for (int s = 0; s < pl.nst; ++s) {
+        mbar_init(bar_full(r, s), kLoaders);
+        mbar_init(bar_empty(r, s), PAIR ? 2 : 1);
+      }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(bar_st(w, Q_FULL), kLoaders);
+      mbar_init(bar_st(w, Q_EMPTY), 1);
+      mbar_init(bar_st(w, S_FULL), 1);
+      mbar_init(bar_st(w, P_FULL), 4);
+      mbar_init(bar_st(w, O_FULL), 1);
+      mbar_init(bar_st(w, O_FREE), 4);
+      mbar_init(bar_st(w, DRAIN), 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 12) tmem_alloc(smem_u32(ctl + 2), 512);
+
+  // ---- the unit list (every block the same) ----
+  const int gsz = (p.num_seqs + kGroups - 1) / kGroups;
+  const int n_streams = PAIR ? (int)gridDim.x : pl.streams * (int)gridDim.x;
+  {
+    float* const red = reinterpret_cast<float*>(smem);   // scratch before any tile is loaded
+    long long work = 0;
+    int kmax = 0;
+    bool bad = tid == 0 && (__ldg(p.cu_q + p.num_seqs) > p.total_q);
+    if (tid < kGroups) {
+      for (int i = 0; i < gsz; ++i) {
+        const int d = tid * gsz + i;
+        if (d >= p.num_seqs) break;
+        Doc o;
+        int mt, kt;
+        bad |= !doc_info(p, d, &o);
+        doc_tiles<PAIR>(p, o, &mt, &kt);
+        work += (long long)mt * kt * p.c.n_kv;
+        if (mt > 0) kmax = max(kmax, kt);
+      }
+    }
+    float wsum = (float)work;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+      kmax = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, o));
+    }
+    if (lane == 0 && warp < 4) {
+      red[warp] = wsum;
+      red[4 + warp] = (float)kmax;
+    }
+    const int any_bad = __syncthreads_or(bad);
+    if (any_bad && tid == 0) set_status(status, DSA_DEV_ERR_INVALID_ARG);
+    wsum = red[0] + red[1] + red[2] + red[3];
+    kmax = (int)fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7]));
+    int chunk = max(kmax, 1);
+    if (pl.max_units > 0 && kmax > kMinChunk) {
+      int cand[8];
+      int units[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        units[i] = 0;
+        cand[i] = i == 0 ? kmax : min(kmax, max(kMinChunk, (int)ceilf(wsum / (float)(n_streams * i))));
+      }
+      if (tid < kGroups) {
+        for (int i = 0; i < gsz; ++i) {
+          const int d = tid * gsz + i;
+          if (d >= p.num_seqs) break;
+          Doc o;
+          int mt, kt;
+          doc_info(p, d, &o);
+          doc_tiles<PAIR>(p, o, &mt, &kt);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) units[c] += mt * p.c.n_kv * splits_of(kt, cand[c]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) units[c] = __reduce_add_sync(0xffffffffu, units[c]);
+      if (lane == 0 && warp < 4) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) reinterpret_cast<int*>(red)[16 + warp * 8 + c] = units[c];
+      }
+      __syncthreads();
+      float best = 3e38f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int* r = reinterpret_cast<const int*>(red) + 16 + c;
+        const int n = r[0] + r[8] + r[16] + r[24];
+        if (c > 0 && (cand[c] >= kmax || n > pl.max_units)) continue;
+        const float rounds = (float)((n + n_streams - 1) / n_streams);
+        const float est = rounds * (float)(cand[c] + (c == 0 ? kOverhead : kSplitOverhead));
+        if (est < best) {
+          best = est;
+          chunk = cand[c];
+        }
+      }
+    }
+    int mine = 0;
+    if (tid < kGroups) {
+      for (int i = 0; i < gsz; ++i) {
+        const int d = tid * gsz + i;
+        if (d >= p.num_seqs) break;
+        Doc o;
+        int mt, kt;
+        doc_info(p, d, &o);
+        doc_tiles<PAIR>(p, o, &mt, &kt);
+        mine += mt * p.c.n_kv * splits_of(kt, chunk);
+      }
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31 && warp < 4) reinterpret_cast<int*>(red)[8 + warp] = incl;
+    __syncthreads();
+    if (tid < kGroups) {
+      int before = incl - mine;
+      for (int i = 0; i < warp; ++i) before += reinterpret_cast<int*>(red)[8 + i];
+      tab[tid] = before;
+      if (tid == kGroups - 1) tab[kGroups] = before + mine;
+      if (blockIdx.x == 0 && pl.max_units > 0) {   // for the joining kernel
+        for (int i = 0; i < gsz; ++i) {
+          const int d = tid * gsz + i;
+          if (d >= p.num_seqs) break;
+          Doc o;
+          int mt, kt;
+          doc_info(p, d, &o);
+          doc_tiles<PAIR>(p, o, &mt, &kt);
+          p.doc_base[d] = before;
+          before += mt * p.c.n_kv * splits_of(kt, chunk);
+        }
+      }
+    }
+    if (tid == 0) {
+      ctl[3] = chunk;
+      if (blockIdx.x == 0) p.hdr[kAttnHdrChunk] = chunk;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  const uint32_t tmem = (uint32_t)ctl[2];
+  const int chunk = ctl[3];
+  const int n_units = tab[kGroups];
+  const int wg = warp >> 2;
+  // Independent streams: all first streams of the grid before the second ones, so few units spread over all SMs.
+  auto first_unit = [&](int w) {
+    return PAIR ? (int)blockIdx.x : (w < pl.streams ? w * (int)gridDim.x + (int)blockIdx.x : n_units);
+  };
+
+  if (wg == 2) {
+    // ======================= loaders =======================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(96));
+    const int ring = PAIR ? 0 : (warp - 8) >> 1;
+    const int lt = tid - 256 - ring * 64;            // thread of this ring
+    const int bar_id = 1 + ring;
+    const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
+    uint32_t* const rowtab = reinterpret_cast<uint32_t*>(smem + pl.off_rows) + ring * (Q8 ? 4 : 2) * kAttnKeys;
+    uint32_t* const masks = reinterpret_cast<uint32_t*>(smem + pl.off_mask) + ring * kMaskRing * 4;
+    constexpr int kBufs = Q8 ? 4 : 2;
+    bool bad_page = false, ok = true;
+
+    // Rows of key tile `kt` of a unit: the cache row or ~0, and (selected keys) the mask of those seen.
+    auto resolve = [&](const Unit& x, int kt, uint32_t (&row)[kRowsPer], uint32_t (&sck)[kRowsPer],
+                       uint32_t (&scv)[kRowsPer], uint32_t (&seen)[kRowsPer]) {
+#pragma unroll
+      for (int i = 0; i < kRowsPer; ++i) {
+        const int r = (PAIR ? 0 : (warp & 1) * 64) + (PAIR ? lt : i * 32 + lane);
+        int pos = kt * kAttnKeys + r;
+        bool there;
+        if (p.topk_idx) {
+          int n = p.topk_width;
+          const int t = x.q0 + x.i0;
+          if (p.topk_len) n = min(n, __ldg(p.topk_len + t));
+          const int j = pos;
+          pos = j < n ? __ldg(p.topk_idx + (int64_t)t * p.topk_width + j) : -1;
+          there = pos >= 0 && pos <= x.P0 + x.i0;
+        } else {
+          there = pos < x.P0 + x.last;   // keys behind the last visible one are never read
+        }
+        row[i] = ~0u;
+        sck[i] = scv[i] = 0;
+        if (there) {
+          const int64_t cr = cache_row(p.c, x.d, pos, x.h);
+          if (cr < 0) {
+            bad_page = true;
+          } else {
+            row[i] = (uint32_t)cr;
+            if constexpr (Q8) {
+              if (p.c.sw == 1) {
+                sck[i] = __ldg(p.c.k_scale + cr) * 0x01010101u;
+                scv[i] = __ldg(p.c.v_scale + cr) * 0x01010101u;
+              } else if constexpr (D == 128) {
+                sck[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_scale) + cr);
+                scv[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_scale) + cr);
+              } else {
+                sck[i] = __ldg(reinterpret_cast<const uint16_t*>(p.c.k_scale) + cr);
+                scv[i] = __ldg(reinterpret_cast<const uint16_t*>(p.c.v_scale) + cr);
+              }
+            }
+          }
+        }
+        seen[i] = __ballot_sync(0xffffffffu, row[i] != ~0u);
+      }
+    };
+    uint32_t* const sctab = reinterpret_cast<uint32_t*>(smem + pl.off_scale) + ring * 4 * 2 * kAttnKeys;
+    auto publish = [&](int tc, const uint32_t (&row)[kRowsPer], const uint32_t (&sck)[kRowsPer],
+                       const uint32_t (&scv)[kRowsPer], const uint32_t (&seen)[kRowsPer]) {
+      const int buf = tc % kBufs;
+#pragma unroll
+      for (int i = 0; i < kRowsPer; ++i) {
+        const int r = (PAIR ? 0 : (warp & 1) * 64) + (PAIR ? lt : i * 32 + lane);
+        rowtab[buf * kAttnKeys + r] = row[i];
+        if constexpr (Q8) {
+          sctab[(buf * 2) * kAttnKeys + r] = sck[i];
+          sctab[(buf * 2 + 1) * kAttnKeys + r] = scv[i];
+        }
+        if (!PAIR && lane == 0) masks[(tc % kMaskRing) * 4 + (r >> 5)] = seen[i];
+      }
+    };
+    // Query tile of stream w.
+    auto load_q = [&](const Unit& x, int w) {
+      const uint32_t qb = sbase + (uint32_t)w * pl.q_bytes;
+      constexpr int PPR = D / 8;
+      const int live = (x.i1 - x.i0) * p.group;
+      const int rows = (int)(pl.q_bytes / (D * 2));
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q);
+      for (int i = lt; i < rows * PPR; i += kLoaders) {
+        const int r = i / PPR, c = i % PPR;
+        const int tok = r / p.group, g = r - tok * p.group;
+        const bool there = r < live;
+        const uint16_t* src =
+            there ? q + (int64_t)(x.q0 + x.i0 + tok) * p.q_stride + (int64_t)(x.h * p.group + g) * D + c * 8 : q;
+        cp_async16(qb + (c >> 3) * (uint32_t)(rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, there);
+      }
+      cp_arrive(bar_st(w, Q_FULL));
+    };
+    int st = 0;
+    uint32_t ph = 0;
+    auto advance = [&] {
+      if (++st == pl.nst) {
+        st = 0;
+        ph ^= 1u;
+      }
+    };
+    bool wrapped = false;   // every stage has been used once
+    auto wait_empty = [&] {
+      if (wrapped) ok = mbar_wait(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo);
+      return ok;
+    };
+    uint32_t qph[2] = {0, 0};   // query tiles loaded so far, per stream
+    auto q_phase = [&](const Unit& x, const Unit& y) {
+      // x: stream `ring` (PAIR: stream 0), y: stream 1 with PAIR
+      for (int i = 0; i < (PAIR ? 2 : 1) && ok; ++i) {
+        const int w = PAIR ? i : ring;
+        const Unit& z = i == 0 ? x : y;
+        if (z.n == 0) continue;
+        if (qph[i] > 0) ok = mbar_wait(bar_st(w, Q_EMPTY), (qph[i] - 1) & 1u, abort_flag, status, tmo);
+        if (ok) load_q(z, w);
+        ++qph[i];
+      }
+    };
+    const int u0 = first_unit(ring);
+
+    if constexpr (!Q8) {
+      constexpr int PPR = D / 8;                   // 16-byte pieces per row
+      constexpr int RPP = kLoaders / PPR;          // rows per pass
+      const int c = lt % PPR, rsub = lt / PPR;
+      const uint32_t dcol = (uint32_t)(c >> 3) * kChunk;
+      int tc = 0;
+      bool stop = false;
+      for (int u = u0; u < n_units && !stop; u += n_streams) {
+        const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, PAIR ? 0 : ring);
+        Unit y = x;
+        if constexpr (PAIR) y = decode_unit<PAIR>(p, tab, gsz, chunk, u, 1);
+        const int n = x.n_shared;
+        uint32_t row[kRowsPer], sa[kRowsPer], sb[kRowsPer], seen[kRowsPer];
+        if (n > 0) {
+          resolve(x, x.lo, row, sa, sb, seen);
+          publish(tc, row, sa, sb, seen);
+        }
+        for (int j = 0; j < n; ++j, ++tc) {
+          stop = named_bar_or(bar_id, kLoaders, !ok);   // all give up together
+          if (stop) break;
+          if (j + 1 < n) resolve(x, x.lo + j + 1, row, sa, sb, seen);
+          const uint32_t* rt = rowtab + (tc % kBufs) * kAttnKeys;
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!wait_empty()) break;
+            const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(kv ? p.c.v : p.c.k) + c * 8;
+            if (p.fault_inject != 1 || tc > 0 || kv > 0) {   // the tests' withheld first stage
+#pragma unroll 8
+              for (int i = 0; i < kAttnKeys / RPP; ++i) {
+                const int r = i * RPP + rsub;
+                const uint32_t cr = rt[r];
+                cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + (cr == ~0u ? 0 : (size_t)cr * D), cr != ~0u);
+              }
+              cp_arrive(bar_full(ring, st));
+            }
+            advance();
+            if (st == 0) wrapped = true;
+          }
+          if (j == 0 && ok) q_phase(x, y);
+          if (j + 1 < n) publish(tc + 1, row, sa, sb, seen);
+        }
+      }
+    } else {
+      constexpr int PPR = D / 16;                  // 16-code pieces per row
+      constexpr int RPP = kLoaders / PPR;
+      constexpr int kPasses = kAttnKeys / RPP;
+      const int c = lt % PPR, rsub = lt / PPR;
+      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * (kAttnKeys * D) + lt * 16;
+      const uint32_t dcol = (uint32_t)(c >> 2) * kChunk;
+      const int c0 = (c & 3) * 2;                  // first of the two 16-byte pieces in its 128-byte span
+      // the fetch runs nraw items (keys, values, keys, ...) ahead of the conversion, across units
+      int fu = u0, fj = 0, fkv = 0, ftc = 0, fslot = 0;
+      Unit fx{};
+      fx.n_shared = 0;
+      bool fnew = true, fend = false;
+      auto fetch = [&] {
+        uint32_t row[kRowsPer], sa[kRowsPer], sb[kRowsPer], seen[kRowsPer];
+        if (!fend && fkv == 0) {
+          while (!fend && (fnew || fj >= fx.n_shared)) {
+            if (!fnew) fu += n_streams;
+            fnew = false;
+            if (fu >= n_units) {
+              fend = true;
+              break;
+            }
+            fx = decode_unit<PAIR>(p, tab, gsz, chunk, fu, PAIR ? 0 : ring);
+            fj = 0;
+            if (fx.n_shared > 0) {
+              resolve(fx, fx.lo, row, sa, sb, seen);
+              publish(ftc, row, sa, sb, seen);
+            }
+          }
+          if (!fend && named_bar_or(bar_id, kLoaders, !ok)) {   // all give up together
+            ok = false;
+            fend = true;
+          }
+        }
+        if (!fend) {
+          const bool more = fkv == 1 && fj + 1 < fx.n_shared;
+          const uint8_t* src = reinterpret_cast<const uint8_t*>(fkv ? p.c.v : p.c.k) + c * 16;
+          const uint32_t* rt = rowtab + (ftc % kBufs) * kAttnKeys;
+          const uint32_t dst = raw_base + (uint32_t)fslot * (kAttnKeys * D);
+#pragma unroll
+          for (int i = 0; i < kPasses; ++i) {
+            const uint32_t cr = rt[i * RPP + rsub];
+            cp_async16(dst + i * (kLoaders * 16), src + (cr == ~0u ? 0 : (size_t)cr * D), cr != ~0u);
+          }
+          if (more) {
+            resolve(fx, fx.lo + fj + 1, row, sa, sb, seen);
+            publish(ftc + 1, row, sa, sb, seen);
+          }
+          if (fkv == 1) {
+            ++fj;
+            ++ftc;
+          }
+          fkv ^= 1;
+          fslot = fslot + 1 == pl.nraw ? 0 : fslot + 1;
+        }
+        cp_commit();
+      };
+      for (int i = 0; i < pl.nraw; ++i) fetch();
+      int tc = 0, slot = 0;
+      for (int u = u0; u < n_units && (ok || !fend); u += n_streams) {
+        const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, PAIR ? 0 : ring);
+        Unit y = x;
+        if constexpr (PAIR) y = decode_unit<PAIR>(p, tab, gsz, chunk, u, 1);
+        for (int j = 0; j < x.n_shared && (ok || !fend); ++j, ++tc) {
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!ok) {   // on to the next vote
+              fetch();
+              continue;
+            }
+            switch (pl.nraw) {
+              case 1: cp_wait<0>(); break;
+              case 2: cp_wait<1>(); break;
+              case 3: cp_wait<2>(); break;
+              default: cp_wait<3>(); break;
+            }
+            if (!wait_empty()) {
+              fetch();
+              continue;
+            }
+            const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
+            const uint32_t src = raw_base + (uint32_t)slot * (kAttnKeys * D);
+            const uint32_t* sct = sctab + ((tc % kBufs) * 2 + kv) * kAttnKeys;
+#pragma unroll 4
+            for (int i = 0; i < kPasses; ++i) {
+              const int r = i * RPP + rsub;
+              uint32_t w4[4];
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(w4[0]), "=r"(w4[1]), "=r"(w4[2]), "=r"(w4[3])
+                           : "r"(src + i * (kLoaders * 16)));
+              // E4M3 bits s.eeee.mmm placed at a BF16's sign, low exponent and high mantissa bits read
+              // as value * 2^-120 (subnormals included); one exact product with 2^(120 + e) restores it
+              const uint32_t e8 = (sct[r] >> (8 * (c >> 1))) & 0xFFu;      // 2^(e8 - 127)
+              const uint32_t first = e8 > 134u ? 254u : e8 + 120u;         // 2^(first - 127): BF16 ends at 2^127
+              __nv_bfloat162 f;
+              *reinterpret_cast<uint32_t*>(&f) = (first << 7) * 0x00010001u;
+              uint32_t o[8];
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+                for (int hlf = 0; hlf < 2; ++hlf) {
+                  const uint32_t t = __byte_perm(w4[q4], 0, hlf ? 0x3424 : 0x1404);
+                  uint32_t b = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
+                  __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&b), f);
+                  o[2 * q4 + hlf] = *reinterpret_cast<uint32_t*>(&v);
+                }
+              }
+              if (e8 > 134u) {                                             // values beyond 2^16: a second factor
+                const uint32_t second = e8 - 134u + 127u;
+                __nv_bfloat162 f2;
+                *reinterpret_cast<uint32_t*>(&f2) = (min(second, 254u) << 7) * 0x00010001u;
+#pragma unroll
+                for (int q8 = 0; q8 < 8; ++q8) {
+                  __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[q8]), f2);
+                  o[q8] = *reinterpret_cast<uint32_t*>(&v);
+                }
+              }
+              const uint32_t rowd = dst + r * 128;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(rowd + ((uint32_t)(c0 ^ (r & 7)) << 4)), "r"(o[0]),
+                           "r"(o[1]), "r"(o[2]), "r"(o[3])
+                           : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(rowd + ((uint32_t)((c0 + 1) ^ (r & 7)) << 4)),
+                           "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                           : "memory");
+            }
+            fence_proxy_async_smem();
+            if (p.fault_inject != 1 || tc > 0 || kv > 0) mbar_arrive(bar_full(ring, st));
+            advance();
+            if (st == 0) wrapped = true;
+            slot = slot + 1 == pl.nraw ? 0 : slot + 1;
+            fetch();
+          }
+          if (j == 0 && ok) q_phase(x, y);
+        }
+      }
+    }
+    cp_wait<0>();
+    if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
+  } else if (wg == 3) {
+    // ======================= MMA warps =======================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(64));
+    const int w = warp - 12;
+    if (w < 2) {
+      const int ring = PAIR ? 0 : w;
+      const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
+      const uint32_t t_s = tmem + (uint32_t)w * 128, t_o = tmem + 256 + (uint32_t)w * 128;
+      constexpr uint32_t idesc_qk = idesc_bf16(kAttnRows, kAttnKeys);
+      constexpr uint32_t idesc_pv = idesc_bf16(kAttnRows, D) | (1u << 16);   // V: rows of keys, N contiguous
+      if (lane == 0) {
+        const uint32_t q_rows_bytes = pl.q_bytes / (D / 64);   // one 64-column chunk of the query tile
+        const uint64_t qd0 = sw128_kmajor_desc(sbase + (uint32_t)w * pl.q_bytes, 0);
+        int st = 0;
+        uint32_t ph = 0, nq = 0, nt = 0;
+        bool ok = true;
+        auto advance = [&] {
+          if (++st == pl.nst) {
+            st = 0;
+            ph ^= 1u;
+          }
+        };
+        const int u0 = first_unit(w);
+        for (int u = u0; u < n_units && ok; u += n_streams) {
+          const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, w);
+          if (x.n > 0) {
+            ok = mbar_wait(bar_st(w, Q_FULL), nq & 1u, abort_flag, status, tmo);
+          }
+          for (int j = 0; j < x.n && ok; ++j) {
+            // S = Q K^T
+            ok = mbar_wait(bar_full(ring, st), ph, abort_flag, status, tmo);
+            if (!ok) break;
+            fence_proxy_async_smem();   // the loaders' cp.async writes, seen through the barrier
+            tc_fence_after();
+            {
+              const uint64_t kd0 = sw128_kmajor_desc(ring_base + (uint32_t)st * kStage, 0);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t ko = (k & 3) * 2;   // 32 bytes, in 16-byte units
+                mma_bf16(t_s, qd0 + ko + (uint64_t)((k >> 2) * q_rows_bytes >> 4), kd0 + ko + (k >> 2) * (kChunk >> 4),
+                         idesc_qk, k > 0);
+              }
+            }
+            tc_commit(bar_st(w, S_FULL));
+            tc_commit(bar_empty(ring, st));
+            if (j == x.n - 1) tc_commit(bar_st(w, Q_EMPTY));
+            advance();
+            // O += P V
+            ok = mbar_wait(bar_full(ring, st), ph, abort_flag, status, tmo) &&
+                 mbar_wait(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
+            if (ok && j == 0 && nq > 0) ok = mbar_wait(bar_st(w, O_FREE), (nq - 1) & 1u, abort_flag, status, tmo);
+            if (!ok) break;
+            fence_proxy_async_smem();
+            tc_fence_after();
+            {
+              // N-major operand: 64-column chunks kChunk apart, groups of 8 keys 1024 bytes apart
+              const uint64_t vd0 = smem_desc(ring_base + (uint32_t)st * kStage, kChunk, 1024, 2);
+#pragma unroll
+              for (int k = 0; k < kAttnKeys / 16; ++k)
+                mma_bf16_ts(t_o, t_s + k * 8, vd0 + k * (2048 >> 4), idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
+            }
+            tc_commit(bar_empty(ring, st));
+            advance();
+            ++nt;
+          }
+          if (x.n > 0 && ok) {
+            tc_commit(bar_st(w, O_FULL));
+            ++nq;
+          }
+          if constexpr (PAIR) {   // stages only the other stream needs
+            for (int j = 2 * x.n; j < 2 * x.n_shared && ok; ++j) {
+              ok = mbar_wait(bar_full(ring, st), ph, abort_flag, status, tmo);
+              if (ok) mbar_arrive(bar_empty(ring, st));
+              advance();
+            }
+          }
+        }
+        if (!ok) {   // what was issued completes before the tensor memory is given back
+          tc_commit(bar_st(w, DRAIN));
+          drain_wait(bar_st(w, DRAIN), 0, tmo);
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    // ======================= softmax warpgroups =======================
+    // shares of the launch's 512 x 128 registers: 2 x 176 + 96 + 64 = 4 x 128
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(176));
+    const int w = wg;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)quarter << 21;    // TMEM lane 32 * quarter
+    const uint32_t t_s = tmem + (uint32_t)w * 128 + lane_off, t_o = tmem + 256 + (uint32_t)w * 128 + lane_off;
+    const uint32_t* const masks = reinterpret_cast<const uint32_t*>(smem + pl.off_mask) + w * kMaskRing * 4;
+    const float scale = p.scale_log2;
+    const int u0 = first_unit(w);
+    uint32_t nt = 0, nq = 0;
+    bool ok = true;
+    for (int u = u0; u < n_units && ok; u += n_streams) {
+      const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, w);
+      const int live = (x.i1 - x.i0) * p.group;
+      const bool warp_live = quarter * 32 < live;
+      const int tok = r / p.group, g = r - tok * p.group;
+      const int vis = r < live ? x.P0 + x.i0 + tok + 1 : 0x7FFFFFFF;   // visible keys of this row
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < x.n; ++j, ++nt) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_st(w, S_FULL), nt & 1u, abort_flag, status, tmo));
+        if (!ok) break;
+        if (warp_live) {
+          tc_fence_after();
+          uint32_t s[128];
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) tmem_ld_x32(t_s + c, s + c);
+          tmem_ld_wait_tied<128>(s);
+          if (!p.topk_idx) {
+            const int lim = vis - (x.lo + j) * kAttnKeys;
+            if (__any_sync(0xffffffffu, lim < kAttnKeys)) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c) s[c] = c < lim ? s[c] : 0xFF800000u;
+            }
+          } else {
+            const uint4 mk = *reinterpret_cast<const uint4*>(masks + (nt % kMaskRing) * 4);
+            if ((mk.x & mk.y & mk.z & mk.w) != 0xFFFFFFFFu) {
+              const uint32_t mw[4] = {mk.x, mk.y, mk.z, mk.w};
+#pragma unroll
+              for (int c = 0; c < 128; ++c) s[c] = (mw[c >> 5] >> (c & 31)) & 1u ? s[c] : 0xFF800000u;
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mx[i] = fmaxf(mx[i], fmaxf(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])));
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const float mt = top == -INFINITY ? -INFINITY : top * scale;
+          const bool raise = r < live && mt > m + kRaise;      // m = -inf: any finite maximum
+          if (__any_sync(0xffffffffu, raise)) {
+            const float alpha = raise ? ex2(m - mt) : 1.f;     // 0 when m = -inf
+            if (raise) m = mt;
+            l *= alpha;
+            if (j > 0) {   // the previous tile's PV completed before this S
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld_x32(t_o + c, o);
+                tmem_ld_wait_tied<32>(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st_x16(t_o + c, o);
+                tmem_st_x16(t_o + c + 16, o + 16);
+              }
+            }
+          }
+          const float mref = m == -INFINITY ? 0.f : m;
+          const float2 sc2 = make_float2(scale, scale), mm2 = make_float2(-mref, -mref);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 e = ffma2(as_f2(s[c + 2 * i], s[c + 2 * i + 1]), sc2, mm2);
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              sum[i & 1] = __fadd2_rn(sum[i & 1], e);
+              pk[i] = pack_bf16(e.x, e.y);
+            }
+            tmem_st_x16(t_s + c / 2, pk);
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_st(w, P_FULL));
+      }
+      if (!ok) break;
+      if (x.n > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_st(w, O_FULL), nq & 1u, abort_flag, status, tmo));
+        if (!ok) break;
+        ++nq;
+        tc_fence_after();
+      }
+      if (warp_live) {
+        const bool mine = r < live;
+        const int64_t orow = (int64_t)(x.q0 + x.i0 + tok) * p.n_heads + x.h * p.group + g;
+        const int64_t prow = (int64_t)(PAIR ? 2 * u + w : u) * pl.rows_cap + r;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (x.n > 0) {
+            tmem_ld_x32(t_o + c, o);
+            tmem_ld_wait_tied<32>(o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+          }
+          if (mine) {
+            if (x.ns == 1) {
+              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow * D + c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4 v;
+                uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  pv[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                dst[i] = l > 0.f || l != l ? v : make_uint4(0, 0, 0, 0);
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                     __uint_as_float(o[4 * i + 3]));
+            }
+          }
+        }
+        if (mine) {
+          if (x.ns == 1) {
+            if (p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          } else {
+            p.part_ml[prow] = make_float2(m, l);
+          }
+        }
+      }
+      if (x.n > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_st(w, O_FREE));
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (tid == 0) put_block_status(p.hdr, *status);
+}
+
+// Joins the partial results of divided key ranges: one warp per (token, head).
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(256) paged_attention_join_kernel(const AttnParams p) {
+  constexpr int VEC = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = (int64_t)p.total_q * p.n_heads;
+  const int chunk = p.hdr[kAttnHdrChunk];
+  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (int64_t)gridDim.x * 8) {
+    const int t = (int)(row / p.n_heads), hh = (int)(row % p.n_heads);
+    const int d = find_seq(p.cu_q, p.num_seqs, t);
+    Doc o;
+    if (!doc_info(p, d, &o) || t < o.q0 || t >= o.q0 + o.T) continue;
+    int mt, kt;
+    doc_tiles<PAIR>(p, o, &mt, &kt);
+    const int ns = splits_of(kt, chunk);
+    if (ns == 1) continue;
+    const int i = t - o.q0, tile = i / p.plan.tq;
+    const int ut = PAIR ? tile >> 1 : tile;
+    const int u0 = p.doc_base[d] + ((hh / p.group) * mt + (mt - 1 - ut)) * ns;
+    const int r = (i - tile * p.plan.tq) * p.group + hh % p.group;
+    auto slot = [&](int s) { return (int64_t)(PAIR ? 2 * (u0 + s) + (tile & 1) : u0 + s) * p.plan.rows_cap + r; };
+    float m = -INFINITY;
+    for (int s = lane; s < ns; s += 32) {
+      const float2 ml = p.part_ml[slot(s)];
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    float l = 0.f, acc[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < ns; ++s) {
+      const float2 ml = p.part_ml[slot(s)];
+      const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - m);
+      const float* src = p.part_o + slot(s) * D + lane * VEC;
+      l = fmaf(ml.y, f, l);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = f == 0.f ? acc[e] : fmaf(src[e], f, acc[e]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + row * D + lane * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+template <int D, bool Q8, bool PAIR>
+cudaError_t launch(const AttnParams& p, int grid, int sm_count, cudaStream_t stream) {
+  auto kernel = paged_attention_kernel<D, Q8, PAIR>;
+  // The warpgroups' register shares add up to 128 a thread: fewer at launch would leave them waiting.
+  static const int regs = [&] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs < 128) return cudaErrorInvalidDeviceFunction;
+  // per device, and always the same value: calls of several threads do not disturb one another
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAttnSmemMax);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kAttnThreads, p.plan.smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.plan.max_units == 0 || p.total_q == 0) return e;
+  const int64_t blocks = ((int64_t)p.total_q * p.n_heads + 7) / 8;
+  paged_attention_join_kernel<D, PAIR><<<(unsigned)(blocks < 8 * sm_count ? blocks : 8 * sm_count), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace attn
+
+}  // namespace dsa

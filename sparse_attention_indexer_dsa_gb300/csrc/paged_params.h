@@ -49,8 +49,28 @@ struct CacheReadParams {
   int* hdr;
 };
 
+constexpr int kAttnKeys = 128;      // keys per tile
+constexpr int kAttnRows = 128;      // query rows (token, head of the group) per tile
+constexpr int kAttnThreads = 512;
+constexpr uint32_t kAttnSmemMax = 232448;   // 227 KB
+constexpr int kAttnSms = 152;       // the grid's upper bound, for workspace sizes
+
+// How one call is laid out (attn_plan): tiles, shared memory and splits.
+struct AttnPlan {
+  int pair;        // two query tiles share one key stream (long chunks); else two independent streams
+  int streams;     // independent streams per block (1 where two do not fit)
+  int tq;          // tokens per query tile
+  int rows_cap;    // rows of a tile that can be live
+  int nst;         // key/value stages per ring
+  int nraw;        // stages of stored 8-bit rows per ring
+  int max_units;   // units with room for a partial result; 0: key ranges are never divided
+  uint32_t q_bytes;                                        // query tile in shared memory
+  uint32_t off_ring, off_raw, off_rows, off_scale, off_mask, off_bars, off_tab, smem;
+};
+
 struct AttnParams {
   PagedCacheView c;
+  AttnPlan plan;
   const void* q;
   int64_t q_stride;   // elements from one token to the next
   const int32_t* cu_q;
@@ -63,12 +83,28 @@ struct AttnParams {
   void* out;
   float* lse;
   int* hdr;
+  int* doc_base;      // [num_seqs] first unit of each sequence
+  float* part_o;      // [units (x 2)][rows_cap][D] sums not yet divided
+  float2* part_ml;    // [units (x 2)][rows_cap] running maximum (log2) and sum
+  int fault_inject;
   unsigned long long timeout_ns;
 };
 
+// Header words of an attention workspace beside the status words.
+constexpr int kAttnHdrChunk = 8;    // key tiles per split
+
+// False: these sizes need more shared memory than a block has.
+bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, bool eight_bit,
+               int topk_width);
+size_t attn_workspace_bytes(const AttnPlan& pl, int num_seqs, int D);
+
 cudaError_t launch_cache_write(const CacheWriteParams& p, int D, int sm_count, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheReadParams& p, int D, int sm_count, cudaStream_t stream);
-cudaError_t launch_paged_attention(const AttnParams& p, int D, int sm_count, cudaStream_t stream);
+// One launcher per head size and width of the cached elements (a file each).
+cudaError_t launch_paged_attention_128(const AttnParams& p, int grid, int sm_count, cudaStream_t stream);
+cudaError_t launch_paged_attention_64(const AttnParams& p, int grid, int sm_count, cudaStream_t stream);
+cudaError_t launch_paged_attention_128_q8(const AttnParams& p, int grid, int sm_count, cudaStream_t stream);
+cudaError_t launch_paged_attention_64_q8(const AttnParams& p, int grid, int sm_count, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Sequence of packed row `r`: the last d with cu[d] <= r (cu[0] = 0).
