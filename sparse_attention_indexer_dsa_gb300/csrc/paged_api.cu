@@ -93,11 +93,11 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   pl->max_units = base <= few * streams ? (int)(base + few * streams) : 0;
   const int qrows = pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
   pl->q_bytes = (uint32_t)qrows * D * 2;
-  const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys * D;
+  const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys / 2 * D;
   for (pl->streams = 2; pl->streams >= 1; --pl->streams) {
     const uint32_t rings = pl->pair ? 1 : pl->streams;
-    const uint32_t rows = rings * (eight_bit ? 4 : 2) * kAttnKeys * 4, scale = eight_bit ? rings * 4 * 2 * kAttnKeys * 4 : 0;
-    const uint32_t mask = 2 * 8 * 4 * 4, bars = 512, tab = round16((128 + 1) * 4);
+    const uint32_t rows = rings * (eight_bit ? 2 : 1) * kAttnKeys * 4, scale = eight_bit ? rings * 4 * 2 * kAttnKeys * 4 : 0;
+    const uint32_t mask = pl->pair ? 0 : 2 * 8 * 4 * 4, bars = 400, tab = round16((64 + 1) * 4);
     const uint32_t q = 2 * pl->q_bytes, tail = rows + scale + mask + bars + tab;
     if (q + tail > kAttnSmemMax) continue;
     const uint32_t avail = kAttnSmemMax - q - tail;
@@ -105,7 +105,7 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
       pl->nst = pl->pair || rings == 1 ? 3 : 2;
       if (avail < rings * (pl->nst * stage + raw)) continue;
       pl->nraw = (int)((avail - rings * pl->nst * stage) / (rings * raw));
-      if (pl->nraw > 4) pl->nraw = 4;
+      if (pl->nraw > 6) pl->nraw = 6;
     } else {
       pl->nst = (int)(avail / (rings * stage));
       if (pl->nst < 2) continue;
@@ -298,7 +298,8 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
   // no more blocks than there can be units
   const int per = p.plan.pair ? 2 * p.plan.tq : p.plan.tq;
   const int64_t keys = topk_idx ? topk_width : max_seqlen_k;
-  int64_t bound = ((int64_t)total_q / per + num_seqs) * n_kv_heads * (p.plan.max_units > 0 ? keys / (2 * kAttnKeys) + 1 : 1);
+  if (keys <= kAttnMinChunk * kAttnKeys) p.plan.max_units = 0;   // nothing to divide: no joining launch
+  int64_t bound = ((int64_t)total_q / per + num_seqs) * n_kv_heads * (p.plan.max_units > 0 ? keys / (kAttnMinChunk * kAttnKeys) + 1 : 1);
   if (bound > di.sm_count) bound = di.sm_count;
   if (bound > DSA_DEV_STATUS_MAX_BLOCKS) bound = DSA_DEV_STATUS_MAX_BLOCKS;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

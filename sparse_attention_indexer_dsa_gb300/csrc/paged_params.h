@@ -51,7 +51,7 @@ struct CacheReadParams {
 
 constexpr int kAttnKeys = 128;      // keys per tile
 constexpr int kAttnRows = 128;      // query rows (token, head of the group) per tile
-constexpr int kAttnThreads = 512;
+constexpr int kAttnMinChunk = 2;    // key tiles of a divided range, at least
 constexpr uint32_t kAttnSmemMax = 232448;   // 227 KB
 constexpr int kAttnSms = 152;       // the grid's upper bound, for workspace sizes
 
@@ -62,7 +62,7 @@ struct AttnPlan {
   int tq;          // tokens per query tile
   int rows_cap;    // rows of a tile that can be live
   int nst;         // key/value stages per ring
-  int nraw;        // stages of stored 8-bit rows per ring
+  int nraw;        // half tiles of stored 8-bit rows per ring
   int max_units;   // units with room for a partial result; 0: key ranges are never divided
   uint32_t q_bytes;                                        // query tile in shared memory
   uint32_t off_ring, off_raw, off_rows, off_scale, off_mask, off_bars, off_tab, smem;

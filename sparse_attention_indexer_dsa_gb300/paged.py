@@ -12,8 +12,6 @@ indexer is, per layer:
 """
 from __future__ import annotations
 
-import contextlib
-import math
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -23,6 +21,22 @@ from . import _abi
 
 _PREC = {"bf16": _abi.DSA_PREC_BF16, "mxfp8": _abi.DSA_PREC_MXFP8, "fp8": _abi.DSA_PREC_FP8}
 _NAME = {v: n for n, v in _PREC.items()}
+_RULE = {"nosat": _abi.DSA_MX_SCALE_NOSAT, "floor": _abi.DSA_MX_SCALE_FLOOR}
+_SOURCES = {torch.float32: _abi.DSA_DTYPE_F32, torch.bfloat16: _abi.DSA_DTYPE_BF16,
+            torch.uint8: _abi.DSA_DTYPE_OPERAND}
+
+
+def _rule(r) -> int:
+    if isinstance(r, str):
+        if r not in _RULE:
+            raise ValueError(f"scale_rule must be 'nosat' or 'floor', not {r!r}")
+        return _RULE[r]
+    return r
+
+
+def _error(code: int, where: str) -> Exception:
+    from . import DsaError
+    return DsaError(code, where)
 
 
 @dataclass
@@ -96,27 +110,46 @@ def paged_cache(num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, 
     return PagedCache(k, ks, v, vs, prec)
 
 
-def _on(device: torch.device):
-    """The tensors' device as the current one, for the launch and its stream."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# The checks of one call run in a few microseconds of host time, a good part of
+# a single-token call: one comparison per property, and the message only when one fails.
+_stream = torch._C._cuda_getCurrentRawStream        # of a device index
 
 
-def _arg(t: Optional[torch.Tensor], name: str, device: torch.device, dtype, shape=None) -> Optional[int]:
-    """Address of a contiguous tensor of this type and shape on this device."""
-    if t is None:
-        return None
+class _Current:
+    """Makes the tensors' device the current one for a launch, where it is not."""
+    __slots__ = ("device", "was")
+
+    def __init__(self, device: torch.device):
+        self.device = device.index
+
+    def __enter__(self):
+        self.was = torch.cuda.current_device()
+        if self.was != self.device:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.was != self.device:
+            torch.cuda.set_device(self.was)
+
+
+def _refuse(t: torch.Tensor, name: str, device: torch.device, dtype, shape):
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the CUDA device")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t: Optional[torch.Tensor], name: str, device: torch.device, dtype, shape=None) -> Optional[int]:
+    """Address of a contiguous tensor of this type and shape on this device."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _refuse(t, name, device, dtype, shape)
     return t.data_ptr() or None
 
 
@@ -124,44 +157,34 @@ def _tokens(t: Optional[torch.Tensor], name: str, device: torch.device, dtypes, 
     """Address and token stride of a [tokens, heads, head_dim] tensor whose tokens may be apart."""
     if t is None:
         return None, 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on the CUDA device")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: unsupported dtype {t.dtype}")
     if t.dim() != 3 or t.shape[1:] != (heads, head_dim):
         raise ValueError(f"{name} must be [tokens, {heads}, {head_dim}], not {tuple(t.shape)}")
-    if (t.stride(2) != 1 and head_dim > 1) or (t.stride(1) != head_dim and heads > 1):
+    if t.device != device:
+        _refuse(t, name, device, t.dtype, None)
+    if t.is_contiguous():
+        return t.data_ptr() or None, 0
+    if t.stride(2) != 1 or (t.stride(1) != head_dim and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
     return t.data_ptr() or None, (t.stride(0) if t.shape[0] > 1 else 0)
 
 
-def _cache_args(c: PagedCache):
-    return (c.k.data_ptr(), c.k_scale.data_ptr() if c.k_scale is not None else None,
-            c.v.data_ptr() if c.v is not None else None, c.v_scale.data_ptr() if c.v_scale is not None else None)
-
-
-def _batch(cache: PagedCache, page_table: torch.Tensor, cu_seqlens_k: torch.Tensor,
-           cu_seqlens_q: Optional[torch.Tensor] = None):
-    """Addresses of the page table and the prefixes, and the number of sequences."""
-    dev = cache.k.device
-    if not cache.k.is_cuda:
+def _pages(c: PagedCache):
+    """Addresses of the pages and scales, device, and (num_pages, n_kv_heads, page_size, head_dim)."""
+    k, ks, v, vs = c.k, c.k_scale, c.v, c.v_scale
+    if not k.is_cuda:
         raise ValueError("tensors must live on the CUDA device")
+    return ((k.data_ptr(), None if ks is None else ks.data_ptr(), None if v is None else v.data_ptr(),
+             None if vs is None else vs.data_ptr()), k.device, k.shape)
+
+
+def _table(page_table: torch.Tensor, device: torch.device):
+    """Address of the page table, its width, the number of sequences."""
     if page_table.dim() != 2:
         raise ValueError("page_table must be [num_seqs, max_pages]")
-    B = page_table.shape[0]
-    table = _arg(page_table, "page_table", dev, torch.int32)
-    ck = _arg(cu_seqlens_k, "cu_seqlens_k", dev, torch.int32, (B + 1,))
-    cq = _arg(cu_seqlens_q, "cu_seqlens_q", dev, torch.int32, (B + 1,))
-    return table, ck, cq, B
-
-
-def _workspace(ws: Optional[torch.Tensor], need: int, device: torch.device) -> torch.Tensor:
-    if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    _arg(ws, "ws", device, torch.uint8)
-    return ws
+    B, width = page_table.shape
+    return _arg(page_table, "page_table", device, torch.int32), width, B
 
 
 def cache_workspace(device=None) -> torch.Tensor:
@@ -179,36 +202,38 @@ def cache_write(cache: PagedCache, k: torch.Tensor, v: Optional[torch.Tensor], c
     stride are taken as they are); v None for a cache of keys alone.  With an
     8-bit cache, uint8 k and v are E4M3 codes in operand form (as preprocess
     gives them) and k_scale, v_scale their UE8M0 bytes."""
-    from . import _check, _rule, _stream
-    dev = cache.k.device
-    table, ck, cq, B = _batch(cache, page_table, cu_seqlens_k, cu_seqlens_q)
-    Hk, D = cache.n_kv_heads, cache.head_dim
-    kinds = (torch.float32, torch.bfloat16) + ((torch.uint8,) if cache.prec != "bf16" else ())
-    kp, kst = _tokens(k, "k", dev, kinds, Hk, D)
-    vp, vst = _tokens(v, "v", dev, (k.dtype,), Hk, D)
+    a, dev, (N, Hk, ps, D) = _pages(cache)
+    table, width, B = _table(page_table, dev)
+    T, dt = k.shape[0], k.dtype
+    codes = dt is torch.uint8
+    if codes and cache.prec == "bf16":
+        raise ValueError("k: a bf16 cache stores fp32 or bf16 rows")
+    kp, kst = _tokens(k, "k", dev, _SOURCES, Hk, D)
+    vp, vst = _tokens(v, "v", dev, (dt,), Hk, D)
     if (v is None) != (cache.v is None):
         raise ValueError("v and the cache's values must both be given or both be None")
-    if v is not None and v.shape[0] != k.shape[0]:
+    if v is not None and v.shape[0] != T:
         raise ValueError("k and v must have the same tokens")
-    T = k.shape[0]
     ksp = vsp = None
-    if k.dtype == torch.uint8:
+    if codes:
         if k_scale is None or (v is not None and v_scale is None):
             raise ValueError("codes come with their scales")
-        n = cache.k_scale.shape[3]
-        ksp = _arg(k_scale, "k_scale", dev, torch.uint8, (T, Hk, n))
-        vsp = _arg(v_scale, "v_scale", dev, torch.uint8, (T, Hk, n))
+        shape = (T, Hk, cache.k_scale.shape[3])
+        ksp = _arg(k_scale, "k_scale", dev, torch.uint8, shape)
+        vsp = _arg(v_scale, "v_scale", dev, torch.uint8, shape)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to uint8 codes")
-    dt = {torch.float32: _abi.DSA_DTYPE_F32, torch.bfloat16: _abi.DSA_DTYPE_BF16,
-          torch.uint8: _abi.DSA_DTYPE_OPERAND}[k.dtype]
-    with _on(dev):
-        ws = _workspace(ws, _abi.DSA_CACHE_WS_BYTES, dev)
-        a = _cache_args(cache)
+    cq = _arg(cu_seqlens_q, "cu_seqlens_q", dev, torch.int32, (B + 1,))
+    ck = _arg(cu_seqlens_k, "cu_seqlens_k", dev, torch.int32, (B + 1,))
+    if ws is None:
+        ws = torch.empty(_abi.DSA_CACHE_WS_BYTES, dtype=torch.uint8, device=dev)
+    wp = _arg(ws, "ws", dev, torch.uint8)
+    with _Current(dev):
         code = _abi.load().dsa_idx_cache_write(
-            kp, kst, ksp, vp, vst, vsp, dt, _rule(scale_rule), cq, ck, B, T, table, page_table.shape[1], a[0], a[1],
-            a[2], a[3], cache.num_pages, cache.page_size, Hk, D, _PREC[cache.prec], ws.data_ptr(), ws.numel(), _stream())
-    _check(code, "dsa_idx_cache_write")
+            kp, kst, ksp, vp, vst, vsp, _SOURCES[dt], _rule(scale_rule), cq, ck, B, T, table, width, *a,
+            N, ps, Hk, D, _PREC[cache.prec], wp, ws.numel(), _stream(dev.index))
+    if code:
+        raise _error(code, "dsa_idx_cache_write")
 
 
 def cache_read(cache: PagedCache, cu_seqlens_k: torch.Tensor, page_table: torch.Tensor, total_k: int, out_prec=None,
@@ -221,38 +246,43 @@ def cache_read(cache: PagedCache, cu_seqlens_k: torch.Tensor, page_table: torch.
     bf16; v and v_scale None for a cache of keys alone), or with
     out_prec="bf16" the values as bfloat16 and no scales.  `out` is such a
     tuple to write into; rows behind the last sequence stay as they were."""
-    from . import _check, _stream
-    dev = cache.k.device
-    table, ck, _, B = _batch(cache, page_table, cu_seqlens_k)
+    a, dev, (N, Hk, ps, D) = _pages(cache)
+    table, width, B = _table(page_table, dev)
     if out_prec not in (None, "bf16", cache.prec):
         raise ValueError(f"out_prec must be None or 'bf16' for a {cache.prec} cache, not {out_prec!r}")
     deq = out_prec == "bf16" and cache.prec != "bf16"
-    Hk, D = cache.n_kv_heads, cache.head_dim
-    dt = torch.bfloat16 if deq or cache.prec == "bf16" else torch.uint8
-    n = 0 if dt == torch.bfloat16 else cache.k_scale.shape[3]
-    with _on(dev):
-        if out is None:
-            def rows():
-                t = torch.empty((total_k, Hk, D), dtype=dt, device=dev)
-                return t, (torch.empty((total_k, Hk, n), dtype=torch.uint8, device=dev) if n else None)
-            k, ks = rows()
-            v, vs = rows() if cache.v is not None else (None, None)
-        else:
-            k, ks, v, vs = out
-            if k is None or (n and (ks is None or (v is not None and vs is None))):
-                raise ValueError("out lacks a tensor of this result")
-            if v is not None and cache.v is None:
-                raise ValueError("the cache has no values")
-        ws = _workspace(ws, _abi.DSA_CACHE_WS_BYTES, dev)
-        a = _cache_args(cache)
-        code = _abi.load().dsa_idx_cache_read(
-            a[0], a[1], a[2], a[3], cache.num_pages, cache.page_size, Hk, D, _PREC[cache.prec], table,
-            page_table.shape[1], ck, B, total_k, int(deq), _arg(k, "out k", dev, dt, (total_k, Hk, D)),
-            _arg(ks, "out k_scale", dev, torch.uint8, (total_k, Hk, n)) if n else None,
-            _arg(v, "out v", dev, dt, (total_k, Hk, D)),
-            _arg(vs, "out v_scale", dev, torch.uint8, (total_k, Hk, n)) if n else None, ws.data_ptr(), ws.numel(),
-            _stream())
-    _check(code, "dsa_idx_cache_read")
+    values = deq or cache.prec == "bf16"
+    dt = torch.bfloat16 if values else torch.uint8
+    shape = (total_k, Hk, D)
+    sshape = None if values else (total_k, Hk, cache.k_scale.shape[3])
+    ck = _arg(cu_seqlens_k, "cu_seqlens_k", dev, torch.int32, (B + 1,))
+    ks = v = vs = None
+    if out is None:
+        k = torch.empty(shape, dtype=dt, device=dev)
+        if cache.v is not None:
+            v = torch.empty(shape, dtype=dt, device=dev)
+        if not values:
+            ks = torch.empty(sshape, dtype=torch.uint8, device=dev)
+            vs = None if v is None else torch.empty(sshape, dtype=torch.uint8, device=dev)
+        kp, vp = k.data_ptr() or None, None if v is None else v.data_ptr()
+    else:
+        k, ks, v, vs = out
+        if k is None or (not values and (ks is None or (v is not None and vs is None))):
+            raise ValueError("out lacks a tensor of this result")
+        if v is not None and cache.v is None:
+            raise ValueError("the cache has no values")
+        kp, vp = _arg(k, "out k", dev, dt, shape), _arg(v, "out v", dev, dt, shape)
+    ksp = vsp = None
+    if not values:
+        ksp, vsp = _arg(ks, "out k_scale", dev, torch.uint8, sshape), _arg(vs, "out v_scale", dev, torch.uint8, sshape)
+    if ws is None:
+        ws = torch.empty(_abi.DSA_CACHE_WS_BYTES, dtype=torch.uint8, device=dev)
+    wp = _arg(ws, "ws", dev, torch.uint8)
+    with _Current(dev):
+        code = _abi.load().dsa_idx_cache_read(*a, N, ps, Hk, D, _PREC[cache.prec], table, width, ck, B, total_k, int(deq),
+                                              kp, ksp, vp, vsp, wp, ws.numel(), _stream(dev.index))
+    if code:
+        raise _error(code, "dsa_idx_cache_read")
     return k, ks, v, vs
 
 
@@ -279,46 +309,46 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, cu_seqlens_q: torch.Tens
     n_heads, head_dim] bf16, or (out, lse fp32 [tokens, n_heads]); `out` is
     such a tensor (or pair) to write into: rows behind the last sequence stay
     as they were."""
-    from . import _check, _stream
     if cache.v is None:
         raise ValueError("the cache has no values")
-    dev = cache.k.device
-    table, ck, cq, B = _batch(cache, page_table, cu_seqlens_k, cu_seqlens_q)
+    a, dev, (N, Hk, ps, D) = _pages(cache)
+    table, width, B = _table(page_table, dev)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, n_heads, head_dim]")
-    T, H, D = q.shape
-    Hk = cache.n_kv_heads
-    qp, qst = _tokens(q, "q", dev, (torch.bfloat16,), H, cache.head_dim)
-    W = 0
+    T, H, _ = shape = q.shape
+    qp, qst = _tokens(q, "q", dev, (torch.bfloat16,), H, D)
+    cq = _arg(cu_seqlens_q, "cu_seqlens_q", dev, torch.int32, (B + 1,))
+    ck = _arg(cu_seqlens_k, "cu_seqlens_k", dev, torch.int32, (B + 1,))
+    W, ip, lp = 0, None, None
     if topk_idx is not None:
         if topk_idx.dim() != 2:
             raise ValueError("topk_idx must be [tokens, width]")
         W = topk_idx.shape[1]
+        ip = _arg(topk_idx, "topk_idx", dev, torch.int32, (T, W))
+        lp = _arg(topk_len, "topk_len", dev, torch.int32, (T,))
     elif topk_len is not None:
         raise ValueError("topk_len belongs to topk_idx")
-    ip = _arg(topk_idx, "topk_idx", dev, torch.int32, (T, W))
-    lp = _arg(topk_len, "topk_len", dev, torch.int32, (T,))
-    lib = _abi.load()
-    with _on(dev):
-        lse = None
-        if out is not None:
-            out, lse = out if isinstance(out, (tuple, list)) else (out, None)
-            if return_lse and lse is None:
-                raise ValueError("out must be a pair (out, lse) with return_lse")
-        else:
-            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
-            if return_lse:
-                lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = attention_workspace(T, B, max_seqlen_q, H, Hk, D, W, dev)
-        else:
-            _arg(ws, "ws", dev, torch.uint8)
-        a = _cache_args(cache)
-        code = lib.dsa_idx_paged_attention(
-            qp, qst, a[0], a[1], a[2], a[3], cache.num_pages, cache.page_size, H, Hk, D, _PREC[cache.prec], table,
-            page_table.shape[1], cq, ck, B, T, max_seqlen_q, max_seqlen_k,
-            1.0 / math.sqrt(D) if sm_scale is None else sm_scale, ip, lp, W,
-            _arg(out, "out", dev, torch.bfloat16, (T, H, D)), _arg(lse, "lse", dev, torch.float32, (T, H)),
-            ws.data_ptr(), ws.numel(), _stream())
-    _check(code, "dsa_idx_paged_attention")
+    lse = lsep = None
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        op = out.data_ptr() or None
+        if return_lse:
+            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+            lsep = lse.data_ptr() or None
+    else:
+        if isinstance(out, (tuple, list)):
+            out, lse = out
+        if return_lse and lse is None:
+            raise ValueError("out must be a pair (out, lse) with return_lse")
+        op = _arg(out, "out", dev, torch.bfloat16, shape)
+        lsep = _arg(lse, "lse", dev, torch.float32, (T, H))
+    if ws is None:
+        ws = attention_workspace(T, B, max_seqlen_q, H, Hk, D, W, dev)
+    wp = _arg(ws, "ws", dev, torch.uint8)
+    with _Current(dev):
+        code = _abi.load().dsa_idx_paged_attention(
+            qp, qst, *a, N, ps, H, Hk, D, _PREC[cache.prec], table, width, cq, ck, B, T, max_seqlen_q, max_seqlen_k,
+            D ** -0.5 if sm_scale is None else sm_scale, ip, lp, W, op, lsep, wp, ws.numel(), _stream(dev.index))
+    if code:
+        raise _error(code, "dsa_idx_paged_attention")
     return (out, lse) if return_lse else out
