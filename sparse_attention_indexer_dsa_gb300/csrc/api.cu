@@ -105,6 +105,29 @@ dsa_status_t make_operand_map(CUtensorMap* m, const void* base, int64_t rows, in
   return DSA_OK;
 }
 
+}  // namespace
+
+namespace dsa {
+
+// BF16 pages [groups][rows][D]: boxes of box_rows x 64 columns, 128-byte swizzle.
+dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, int rows, int D, int box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)groups};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * rows};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled(pages) failed: %d", (int)r);
+  return DSA_OK;
+}
+
+}  // namespace dsa
+
+namespace {
+
 // Scale words: rows of 4 UE8M0 bytes viewed as u32 [rows], box 132 words.
 dsa_status_t make_scale_map(CUtensorMap* m, const void* base, int64_t rows) {
   auto enc = encode_fn();

@@ -2,6 +2,7 @@
 // dsa_idx_last_error() and the device facts.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -18,6 +19,8 @@ dsa_status_t fail(dsa_status_t s, const char* fmt, ...) __attribute__((format(pr
 dsa_status_t cuda_fail(cudaError_t e, const char* what);
 // Facts of the current device; refuses anything but sm_103.
 dsa_status_t device_info(DevInfo* out);
+
+dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, int rows, int D, int box_rows);
 
 // Limit of the kernels' bounded waits, and the fault injection of the tests.
 unsigned long long wait_timeout_ns();

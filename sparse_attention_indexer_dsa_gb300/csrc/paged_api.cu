@@ -295,6 +295,12 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
     w += round256(slots * 8);
     p.part_o = reinterpret_cast<float*>(w);
   }
+  if (prec == DSA_PREC_BF16 && !topk_idx) {
+    const int64_t groups = (int64_t)num_pages * n_kv_heads;
+    const int box = page_size < kAttnKeys ? page_size : kAttnKeys;
+    if ((s = make_pages_map(&p.tm_k, k_pages, groups, page_size, head_dim, box)) != DSA_OK) return s;
+    if ((s = make_pages_map(&p.tm_v, v_pages, groups, page_size, head_dim, box)) != DSA_OK) return s;
+  }
   // no more blocks than there can be units
   const int per = p.plan.pair ? 2 * p.plan.tq : p.plan.tq;
   const int64_t keys = topk_idx ? topk_width : max_seqlen_k;

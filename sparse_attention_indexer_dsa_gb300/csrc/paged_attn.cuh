@@ -8,9 +8,11 @@
 // 128.  Per tile S = Q K^T (K = head_dim) goes to TMEM, the softmax warps turn
 // it into P = 2^(c S - m) in BF16 in the same TMEM columns, and O += P V reads
 // P from TMEM.  m is the running row maximum (log2 domain), raised only when a
-// row exceeds it by more than 8, so the accumulator in TMEM is rescaled a few
-// times per row instead of once per tile; the sums and O stay in FP32, and 2^8
-// is far inside BF16's range.  P is rounded to BF16 because the PV product has
+// row exceeds it by more than 20, so the accumulator in TMEM is hardly ever
+// rescaled: weights up to 2^20 keep their relative precision in BF16, and the
+// sums and O in FP32 are far from its range.  (A warp rescales when one of its
+// 32 rows must: at a margin of 8 that was every fourth tile of N(0, 1) inputs
+// with outliers.)  P is rounded to BF16 because the PV product has
 // BF16 operands; the sum l adds the unrounded weights.
 //
 // Streams.  One block per SM with two streams, each a TMEM half (S/P 128
@@ -22,13 +24,14 @@
 //         key/value stages (long chunks: the keys are read half as often);
 //   else: the streams are independent, each with its own units and ring
 //         (single tokens, short chunks, selected rows).
-// Loader warps fill the rings.  Listed position -> page -> row is resolved a
-// step per tile, three tiles ahead (one row per thread), so its dependent loads
-// are off the path; the rows are copied with cp.async into the 128-byte
-// swizzled layout the MMA reads.  Rows that are not there are zero-filled, so
-// nothing outside a sequence's own rows enters a product.  8-bit rows are
-// fetched as stored (cp.async into a thread-private ring) and widened to BF16
-// on the way into the stage; E4M3 x 2^e is exact in BF16.  One more warp per
+// Loaders.  All visible keys of a BF16 cache come by TMA, a box per page, from
+// one warp.  Listed rows and 8-bit caches: loader warps resolve listed position
+// -> page -> row a step per tile, three tiles ahead (one row per thread), so its
+// dependent loads are off the path, and copy the rows with cp.async into the
+// 128-byte swizzled layout the MMA reads.  Rows that are not there are
+// zero-filled, so nothing outside a sequence's own rows enters a product.  8-bit
+// rows are fetched as stored (cp.async into a thread-private ring) and widened to
+// BF16 on the way into the stage; E4M3 x 2^e is exact in BF16.  One more warp per
 // stream loads its query tiles.
 //
 // Units.  (sequence, key head, query tile, range of key tiles).  Every block
@@ -52,7 +55,7 @@ constexpr int kGroups = 64;         // sequences are counted in this many groups
 constexpr int kOverhead = 4;        // start and end of a unit, in key tiles
 constexpr int kSplitOverhead = 6;   // ... when its result is joined later
 constexpr int kMaskRing = 8;
-constexpr float kRaise = 8.f;       // log2 of the largest weight before the maximum is raised
+constexpr float kRaise = 20.f;      // log2 of the largest weight before the maximum is raised
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -68,6 +71,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -120,7 +129,7 @@ __device__ __forceinline__ bool poll_bar(uint32_t bar, uint32_t parity, uint32_t
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
       "mov.u32 n, %3;\n"
       "POLL_%=:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE_%=;\n\t"
       "sub.u32 n, n, 1;\n\t"
       "setp.ne.u32 q, n, 0;\n\t"
@@ -281,6 +290,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
   const uint64_t tmo = p.timeout_ns;
+  const bool tma = !Q8 && (PAIR || !p.topk_idx);
 
   // barriers: per ring full/empty; per stream q_full, q_empty, s_full, p_full, o_full, o_free, drain
   const uint32_t bars = sbase + pl.off_bars;
@@ -300,7 +310,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
     ctl[4] = 0;
     for (int r = 0; r < kRings; ++r)
       for (int s = 0; s < pl.nst; ++s) {
-        mbar_init(bar_full(r, s), kLoaders);
+        mbar_init(bar_full(r, s), tma ? 1 : kLoaders);
         mbar_init(bar_empty(r, s), PAIR ? 2 : 1);
       }
     for (int w = 0; w < 2; ++w) {
@@ -454,6 +464,81 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
     const int lt = (tid - 256) % kLoaders;           // thread of this ring
     const int bar_id = 1 + ring;
     const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
+    // Every visible key of a BF16 cache: TMA, a box per page, issued by one warp (a lane to a page).
+    // The unit's last tile may end inside a page whose other slots hold anything: the warp copies
+    // that one row by row, with zeros behind the last visible key.
+    auto load_tma = [&] {
+      const int shift = p.c.page_shift;
+      const int box = min(kAttnKeys, 1 << shift);               // keys per box
+      const int boxes = kAttnKeys / box;
+      int st = 0;
+      uint32_t ph = 0;
+      bool wrapped = false, bad_page = false;
+      for (int u = first_unit(ring); u < n_units; u += n_streams) {
+        const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, PAIR ? 0 : ring);
+        const int32_t* table = p.c.table + (int64_t)x.d * p.c.max_pages;
+        const int last = x.P0 + x.last;                         // keys visible to the unit
+        auto page_of = [&](int key) {
+          return key < last ? __ldg(table + (key >> shift)) : 0;   // (doc_info: within max_pages)
+        };
+        int page = x.n_shared > 0 && lane < boxes ? page_of(x.lo * kAttnKeys + lane * box) : 0;
+        for (int j = 0; j < x.n_shared; ++j) {
+          const int key0 = (x.lo + j) * kAttnKeys;
+          const int now = page;
+          if (j + 1 < x.n_shared && lane < boxes) page = page_of(key0 + kAttnKeys + lane * box);
+          const bool whole = key0 + kAttnKeys <= last;
+          const bool good = (unsigned)now < (unsigned)p.c.num_pages;
+          const bool mine = whole && lane < boxes && good;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * (uint32_t)box * D * 2;
+          if (whole && lane < boxes && !good) bad_page = true;
+          for (int kv = 0; kv < 2; ++kv) {
+            if (wrapped && !__all_sync(0xffffffffu, wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo))) {
+              cp_wait<0>();
+              return;
+            }
+            const uint32_t dst = ring_base + (uint32_t)st * kStage;
+            const bool withheld = p.fault_inject == 1 && u == first_unit(ring) && j == 0 && kv == 0;   // (tests)
+            if (whole) {
+              if (!withheld) {
+                if (lane == 0) mbar_arrive_expect_tx(bar_full(ring, st), bytes);
+                __syncwarp();
+                if (mine) {
+#pragma unroll
+                  for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(dst + c * kChunk + lane * box * 128, kv ? &p.tm_v : &p.tm_k, bar_full(ring, st), c * 64,
+                                (key0 + lane * box) & ((1 << shift) - 1), now * p.c.n_kv + x.h);
+                }
+              }
+            } else {
+              constexpr int PPR = D / 8;
+              const int c = lane % PPR;
+              const uint16_t* src = reinterpret_cast<const uint16_t*>(kv ? p.c.v : p.c.k) + c * 8;
+#pragma unroll 4
+              for (int r = lane / PPR; r < kAttnKeys; r += 32 / PPR) {
+                const int64_t cr = key0 + r < last ? cache_row(p.c, x.d, key0 + r, x.h) : -1;
+                if (key0 + r < last && cr < 0) bad_page = true;
+                cp_async16(dst + (uint32_t)(c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           src + (cr < 0 ? 0 : cr * D), cr >= 0);
+              }
+              cp_commit();
+              cp_wait<0>();
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && !withheld) mbar_arrive(bar_full(ring, st));
+            }
+            if (++st == pl.nst) {
+              st = 0;
+              ph ^= 1u;
+              wrapped = true;
+            }
+          }
+        }
+      }
+      if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
+    };
+    if (tma) {
+      if (lt < 32) load_tma();
+    } else {
     constexpr int kRowBufs = Q8 ? 2 : 1;   // (BF16: the next tile's rows wait for a second barrier)
     uint32_t* const rowtab = reinterpret_cast<uint32_t*>(smem + pl.off_rows) + ring * kRowBufs * kAttnKeys;
     uint32_t* const sctab = reinterpret_cast<uint32_t*>(smem + pl.off_scale) + ring * 4 * 2 * kAttnKeys;
@@ -723,6 +808,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
     }
     cp_wait<0>();
     if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
+    }
   } else if (wg >= 2) {
     // ======================= MMA and query-loader warps =======================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kMmaRegs));
@@ -790,6 +876,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
           const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, w);
           if (x.n > 0) {
             ok = wait_bar(bar_st(w, Q_FULL), nq & 1u, abort_flag, status, tmo);
+            fence_proxy_async_smem();   // the query tile's cp.async writes
           }
           auto issue_qk = [&](bool last) {   // S = Q K^T with the keys of stage st
             const uint64_t kd0 = sw128_kmajor_desc(ring_base + (uint32_t)st * kStage, 0);
@@ -807,7 +894,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
           if (x.n > 0 && ok) {
             ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
             if (!ok) break;
-            fence_proxy_async_smem();   // the loaders' cp.async writes, seen through the barrier
+            if (!tma) fence_proxy_async_smem();   // the loaders' cp.async writes, seen through the barrier
             tc_fence_after();
             take_turn();
             issue_qk(x.n == 1);
@@ -824,7 +911,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
             advance();
             bool next = j + 1 < x.n;
             const bool have_k = next && mbar_try_wait(bar_full(ring, st), ph);
-            fence_proxy_async_smem();
+            if (!tma) fence_proxy_async_smem();
             ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
             if (!ok) break;
             tc_fence_after();
@@ -840,7 +927,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
             if (next && !have_k) {
               ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
               if (!ok) break;
-              fence_proxy_async_smem();
+              if (!tma) fence_proxy_async_smem();
               take_turn();
               issue_qk(j + 2 == x.n);
               end_turn();
@@ -905,11 +992,14 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
               for (int c = 0; c < kAttnKeys; ++c) s[c] = (mw[c >> 5] >> (c & 31)) & 1u ? s[c] : 0xFF800000u;
             }
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx[8];
 #pragma unroll
-          for (int c = 0; c < kAttnKeys; c += 2)
-            mx[(c >> 1) & 3] = fmaxf(mx[(c >> 1) & 3], fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int c = 0; c < 8; ++c) mx[c] = fmaxf(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+#pragma unroll
+          for (int c = 16; c < kAttnKeys; c += 2)
+            mx[(c >> 1) & 7] = fmaxf(mx[(c >> 1) & 7], fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
           const float mt = top == -INFINITY ? -INFINITY : top * scale;
           const bool raise = r < live && mt > m + kRaise;      // m = -inf: any finite maximum
           if (__any_sync(0xffffffffu, raise)) {

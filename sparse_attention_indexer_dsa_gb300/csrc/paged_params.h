@@ -2,6 +2,7 @@
 // paged_attn.cu) and the device view of a paged cache.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -69,6 +70,7 @@ struct AttnPlan {
 };
 
 struct AttnParams {
+  CUtensorMap tm_k, tm_v;   // BF16 pages as [pages * heads][page_size][D], boxes of up to 128 rows x 64 columns
   PagedCacheView c;
   AttnPlan plan;
   const void* q;
