@@ -129,7 +129,7 @@ __device__ __forceinline__ bool poll_bar(uint32_t bar, uint32_t parity, uint32_t
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
       "mov.u32 n, %3;\n"
       "POLL_%=:\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE_%=;\n\t"
       "sub.u32 n, n, 1;\n\t"
       "setp.ne.u32 q, n, 0;\n\t"
@@ -501,12 +501,15 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
             if (whole) {
               if (!withheld) {
                 if (lane == 0) mbar_arrive_expect_tx(bar_full(ring, st), bytes);
-                __syncwarp();
-                if (mine) {
+#pragma unroll 1
+                for (int i = 0; i < boxes; ++i) {   // (one lane and uniform coordinates: a lane to a box issues slower)
+                  const int pg = __shfl_sync(0xffffffffu, now, i);
+                  if (lane == 0 && (unsigned)pg < (unsigned)p.c.num_pages) {
+                    const int slot = (key0 + i * box) & ((1 << shift) - 1), z = pg * p.c.n_kv + x.h;
 #pragma unroll
-                  for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(dst + c * kChunk + lane * box * 128, kv ? &p.tm_v : &p.tm_k, bar_full(ring, st), c * 64,
-                                (key0 + lane * box) & ((1 << shift) - 1), now * p.c.n_kv + x.h);
+                    for (int c = 0; c < D / 64; ++c)
+                      tma_load_3d(dst + c * kChunk + i * box * 128, kv ? &p.tm_v : &p.tm_k, bar_full(ring, st), c * 64, slot, z);
+                  }
                 }
               }
             } else {
