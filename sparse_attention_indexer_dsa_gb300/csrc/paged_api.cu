@@ -75,12 +75,15 @@ namespace dsa {
 // streams of a block work on their own.  Key ranges are divided only while
 // there are at most four units to a stream (more balance themselves), and a
 // call's workspace has room for four more units to a stream.
-bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, bool eight_bit,
-               int topk_width) {
+bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,
+               int page_size, int topk_width) {
   *pl = AttnPlan{};
+  const bool eight_bit = sw > 0;
   const int group = n_heads / n_kv;
+  // a page's part of a half tile must have scales in whole 16 bytes for the bulk copy
+  pl->gather = topk_width > 0 || (eight_bit && ((page_size < 64 ? page_size : 64) * sw) % 16 != 0);
   pl->tq = topk_width > 0 ? 1 : kAttnRows / group;
-  pl->pair = topk_width == 0 && max_seqlen_q > pl->tq && (int64_t)total_q * group > (int64_t)kAttnRows * num_seqs;
+  pl->pair = !pl->gather && max_seqlen_q > pl->tq && (int64_t)total_q * group > (int64_t)kAttnRows * num_seqs;
   const int tok = pl->tq < max_seqlen_q ? pl->tq : (max_seqlen_q > 0 ? max_seqlen_q : 1);
   pl->rows_cap = tok * group;
   const int per = pl->pair ? 2 * pl->tq : pl->tq;
@@ -93,11 +96,12 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   pl->max_units = base <= few * streams ? (int)(base + few * streams) : 0;
   const int qrows = pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
   pl->q_bytes = (uint32_t)qrows * D * 2;
-  const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys / 2 * D;
+  const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys / 2 * D + (pl->gather ? 0 : 256);
   for (pl->streams = 2; pl->streams >= 1; --pl->streams) {
     const uint32_t rings = pl->pair ? 1 : pl->streams;
-    const uint32_t rows = rings * (eight_bit ? 2 : 1) * kAttnKeys * 4, scale = eight_bit ? rings * 4 * 2 * kAttnKeys * 4 : 0;
-    const uint32_t mask = pl->pair ? 0 : 2 * 8 * 4 * 4, bars = 400, tab = round16((64 + 1) * 4);
+    const uint32_t rows = pl->gather ? rings * (eight_bit ? 2 : 1) * kAttnKeys * 4 : 64;   // else: rows of a half tile
+    const uint32_t scale = pl->gather && eight_bit ? rings * 4 * 2 * kAttnKeys * 4 : 0;
+    const uint32_t mask = pl->gather ? 2 * 8 * 4 * 4 : 0, bars = 8 * (2 * 32 + 2 * 6) + 32, tab = round16((64 + 1) * 4);
     const uint32_t q = 2 * pl->q_bytes, tail = rows + scale + mask + bars + tab;
     if (q + tail > kAttnSmemMax) continue;
     const uint32_t avail = kAttnSmemMax - q - tail;
@@ -232,9 +236,16 @@ size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqle
   if (total_q < 0 || num_seqs < 1 || max_seqlen_q < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 ||
       n_heads / n_kv_heads > kAttnRows || (head_dim != 64 && head_dim != 128) || topk_width < 0)
     return 0;
-  AttnPlan pl;   // the workspace does not depend on the cache's format
-  if (!attn_plan(&pl, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, false, topk_width)) return 0;
-  return attn_workspace_bytes(pl, num_seqs, head_dim);
+  // the largest of the cache's formats
+  size_t most = 0;
+  for (int sw : {0, 1, head_dim / 32})
+    for (int page_size : {8, 64}) {
+      AttnPlan pl;
+      if (!attn_plan(&pl, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, sw, page_size, topk_width)) return 0;
+      const size_t n = attn_workspace_bytes(pl, num_seqs, head_dim);
+      most = n > most ? n : most;
+    }
+  return most;
 }
 
 dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void* k_pages, const uint8_t* k_page_scale,
@@ -259,8 +270,7 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
     return fail(DSA_ERR_INVALID_ARG, "topk_width and topk_len belong to topk_idx");
   if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if ((s = check_stride(&q_stride, n_heads, head_dim, 2, "q")) != DSA_OK) return s;
-  if (!attn_plan(&p.plan, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, prec != DSA_PREC_BF16,
-                 topk_width))
+  if (!attn_plan(&p.plan, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, p.c.sw, page_size, topk_width))
     return fail(DSA_ERR_UNSUPPORTED, "no kernel configuration fits");
   const size_t need = attn_workspace_bytes(p.plan, num_seqs, head_dim);
   if ((s = check_ws(ws, ws_bytes, need)) != DSA_OK) return s;
@@ -295,11 +305,13 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
     w += round256(slots * 8);
     p.part_o = reinterpret_cast<float*>(w);
   }
-  if (prec == DSA_PREC_BF16 && !topk_idx) {
+  if (!p.plan.gather) {
     const int64_t groups = (int64_t)num_pages * n_kv_heads;
-    const int box = page_size < kAttnKeys ? page_size : kAttnKeys;
-    if ((s = make_pages_map(&p.tm_k, k_pages, groups, page_size, head_dim, box)) != DSA_OK) return s;
-    if ((s = make_pages_map(&p.tm_v, v_pages, groups, page_size, head_dim, box)) != DSA_OK) return s;
+    const int keys = prec == DSA_PREC_BF16 ? kAttnKeys : kAttnKeys / 2;   // of a tile, or half a tile as stored
+    const int box = page_size < keys ? page_size : keys;
+    const bool b8 = prec != DSA_PREC_BF16;
+    if ((s = make_pages_map(&p.tm_k, k_pages, groups, page_size, head_dim, box, b8)) != DSA_OK) return s;
+    if ((s = make_pages_map(&p.tm_v, v_pages, groups, page_size, head_dim, box, b8)) != DSA_OK) return s;
   }
   // no more blocks than there can be units
   const int per = p.plan.pair ? 2 * p.plan.tq : p.plan.tq;

@@ -187,9 +187,9 @@ __device__ __forceinline__ bool doc_info(const AttnParams& p, int d, Doc* o) {
 }
 
 // Query tiles (pairs of them with PAIR) and key tiles of a sequence.
-template <bool PAIR>
+template <bool kPair>
 __device__ __forceinline__ void doc_tiles(const AttnParams& p, const Doc& o, int* mt, int* kt) {
-  const int per = PAIR ? 2 * p.plan.tq : p.plan.tq;
+  const int per = kPair ? 2 * p.plan.tq : p.plan.tq;
   *mt = (o.T + per - 1) / per;
   *kt = ((p.topk_idx ? p.topk_width : o.S) + kAttnKeys - 1) / kAttnKeys;
 }
@@ -208,7 +208,7 @@ struct Unit {
 };
 
 // tab: first unit of each of the kGroups groups of sequences (+ the total).
-template <bool PAIR>
+template <bool kPair>
 __device__ __forceinline__ Unit decode_unit(const AttnParams& p, const int* tab, int gsz, int chunk, int u, int w) {
   int lo = 0, hi = kGroups - 1;
   while (lo < hi) {
@@ -221,7 +221,7 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams& p, const int* tab,
   int mt, kt, ns;
   for (;;) {
     doc_info(p, d, &o);
-    doc_tiles<PAIR>(p, o, &mt, &kt);
+    doc_tiles<kPair>(p, o, &mt, &kt);
     ns = splits_of(kt, chunk);
     const int units = mt * ns * p.c.n_kv;
     if (rem < units || d + 1 >= p.num_seqs) break;
@@ -237,10 +237,10 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams& p, const int* tab,
   rem /= ns;
   const int tile = mt - 1 - rem % mt;   // the longest first
   x.h = rem / mt;
-  const int t = PAIR ? 2 * tile + w : tile;
+  const int t = kPair ? 2 * tile + w : tile;
   x.i0 = min(t * p.plan.tq, o.T);
   x.i1 = min(x.i0 + p.plan.tq, o.T);
-  x.last = PAIR ? min((2 * tile + 2) * p.plan.tq, o.T) : x.i1;
+  x.last = kPair ? min((2 * tile + 2) * p.plan.tq, o.T) : x.i1;
   int kt_own, kt_all;
   if (p.topk_idx) {
     int n = p.topk_width;
@@ -256,7 +256,7 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams& p, const int* tab,
   const int per = (kt_all + ns - 1) / ns;
   x.lo = x.split * per;
   x.n = max(0, min(x.lo + per, kt_own) - x.lo);
-  x.n_shared = PAIR ? max(0, min(x.lo + per, kt_all) - x.lo) : x.n;
+  x.n_shared = kPair ? max(0, min(x.lo + per, kt_all) - x.lo) : x.n;
   return x;
 }
 
@@ -264,62 +264,118 @@ __device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 
-// Warps: 8 softmax, then 4 or 8 loaders, then MMA 0, MMA 1, query loader 0, 1.
-template <bool Q8>
+// Sixteen E4M3 codes to BF16, times 2^(e8 - 127).  Code bits s.eeee.mmm placed at a BF16's sign, low
+// exponent and high mantissa bits read as value * 2^-120 (subnormals included); one exact product with
+// 2^(120 + e) restores it.
+__device__ __forceinline__ void widen16(const uint32_t (&w4)[4], uint32_t e8, uint32_t (&o)[8]) {
+  const uint32_t first = e8 > 134u ? 254u : e8 + 120u;         // 2^(first - 127): BF16 ends at 2^127
+  __nv_bfloat162 f;
+  *reinterpret_cast<uint32_t*>(&f) = (first << 7) * 0x00010001u;
+#pragma unroll
+  for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+    for (int hlf = 0; hlf < 2; ++hlf) {
+      const uint32_t t = __byte_perm(w4[q4], 0, hlf ? 0x3424 : 0x1404);
+      uint32_t b = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
+      __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&b), f);
+      o[2 * q4 + hlf] = *reinterpret_cast<uint32_t*>(&v);
+    }
+  }
+  if (e8 > 134u) {                                             // values beyond 2^16: a second factor
+    __nv_bfloat162 f2;
+    *reinterpret_cast<uint32_t*>(&f2) = ((e8 - 134u + 127u) << 7) * 0x00010001u;
+#pragma unroll
+    for (int q8 = 0; q8 < 8; ++q8) {
+      __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[q8]), f2);
+      o[q8] = *reinterpret_cast<uint32_t*>(&v);
+    }
+  }
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+}
+
+// Kernel kinds: two query tiles on one stream of keys; independent streams that see every key up to
+// their own; independent streams with rows gathered one by one (listed keys, and caches whose page
+// scales are too short for a bulk copy).
+enum { PAIR = 0, SOLO = 1, GATHER = 2 };
+
+// Warps: 8 softmax; workers (8-bit caches: 8 that widen rows; BF16 rows gathered: 4 that copy); the
+// rest: key loaders (TMA), query loaders, MMA 0 and 1 last.  (The four warps of an SM's sub-partition
+// are those of equal number modulo 4; loaders and MMA warps are kept on different ones.)
+template <bool Q8, int MODE>
 struct Roles {
-  static constexpr int kLoadWarps = Q8 ? 8 : 4;   // widening 8-bit rows takes twice the threads
-  static constexpr int kThreads = 256 + 32 * kLoadWarps + 128;
+  static constexpr int kWorkWarps = Q8 ? 8 : (MODE == GATHER ? 4 : 0);
+  static constexpr int kWarps = Q8 ? 20 : 16;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kQueryWarp = MODE != GATHER && !Q8 ? 10 : kWarps - 4;   // and the next one
+  static constexpr int kKeyWarp = Q8 ? kWarps - 4 : 8;                        // TMA: and the next one
   // registers: shares of what the launch holds (threads x the launch's count, a multiple of 8)
   static constexpr int kLaunchRegs = Q8 ? 96 : 128;
-  static constexpr int kSoftmaxRegs = Q8 ? 160 : 192;
-  static constexpr int kLoadRegs = Q8 ? 56 : 72;
-  static constexpr int kMmaRegs = Q8 ? 48 : 56;
-  static_assert(2 * kSoftmaxRegs + kLoadWarps / 4 * kLoadRegs + kMmaRegs <= kThreads / 128 * kLaunchRegs, "shares");
+  static constexpr int kSoftmaxRegs = Q8 ? 112 : 192;
+  static constexpr int kWorkRegs = Q8 ? 80 : 72;
+  static constexpr int kAuxRegs = Q8 ? 96 : (MODE == GATHER ? 56 : 64);
+  static_assert(2 * kSoftmaxRegs + kWorkWarps / 4 * kWorkRegs + (kWarps - 8 - kWorkWarps) / 4 * kAuxRegs <=
+                    kWarps / 4 * kLaunchRegs, "shares");
 };
 
-template <int D, bool Q8, bool PAIR>
-__global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel(const __grid_constant__ AttnParams p) {
-  using R = Roles<Q8>;
+template <int D, bool Q8, int MODE>
+__global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_kernel(const __grid_constant__ AttnParams p) {
+  using R = Roles<Q8, MODE>;
+  constexpr bool kPair = MODE == PAIR;
+  constexpr bool kWorkerCopies = MODE == GATHER && !Q8;   // stages written by cp.async: fenced by the MMA warp
   constexpr uint32_t kStage = kAttnKeys * D * 2;     // one tile of keys or values
   constexpr uint32_t kChunk = kAttnKeys * 128;       // 64 of its columns
-  constexpr int kRings = PAIR ? 1 : 2;
-  constexpr int kLoaders = 32 * R::kLoadWarps / kRings;              // loader threads per ring
-  constexpr int kRowsPer = kLoaders < kAttnKeys ? kAttnKeys / kLoaders : 1;   // rows a loader thread resolves per tile
+  constexpr int kRings = kPair ? 1 : 2;
+  constexpr int kLoaders = R::kWorkWarps > 0 ? 32 * R::kWorkWarps / kRings : 32;   // worker threads per ring
+  constexpr int kRowsPer = kLoaders < kAttnKeys ? kAttnKeys / kLoaders : 1;   // rows a worker resolves per tile
+  constexpr uint32_t kRawItem = kAttnKeys / 2 * D + (MODE == GATHER ? 0 : 256);   // half a tile as stored (+ scales)
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnPlan& pl = p.plan;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
   const uint64_t tmo = p.timeout_ns;
-  const bool tma = !Q8 && (PAIR || !p.topk_idx);
+  const bool listed = MODE == GATHER && p.topk_idx != nullptr;
 
-  // barriers: per ring full/empty; per stream q_full, q_empty, s_full, p_full, o_full, o_free, drain
+  // barriers: per ring full/empty (BF16 tiles) and raw full/empty (stored 8-bit half tiles); per stream
+  // q_full, q_empty, s_full, p_full, o_full, drain
   const uint32_t bars = sbase + pl.off_bars;
-  int* const ctl = reinterpret_cast<int*>(smem + pl.off_bars + 8 * (2 * 16 + 2 * 7));   // status, abort, tmem base, chunk, turn
+  int* const ctl = reinterpret_cast<int*>(smem + pl.off_bars + 8 * (2 * 32 + 2 * 6));   // status, abort, tmem base, chunk, turn
   int* const status = ctl;
   volatile int* const abort_flag = ctl + 1;
   int* const tab = reinterpret_cast<int*>(smem + pl.off_tab);
-  auto bar_full = [&](int ring, int s) { return bars + 8u * (ring * 16 + s); };
-  auto bar_empty = [&](int ring, int s) { return bars + 8u * (ring * 16 + 8 + s); };
-  auto bar_st = [&](int w, int i) { return bars + 8u * (32 + w * 7 + i); };
-  enum { Q_FULL, Q_EMPTY, S_FULL, P_FULL, O_FULL, O_FREE, DRAIN };
-  constexpr int kMmaWarp = 8 + R::kLoadWarps;
+  auto bar_full = [&](int ring, int s) { return bars + 8u * (ring * 32 + s); };
+  auto bar_empty = [&](int ring, int s) { return bars + 8u * (ring * 32 + 8 + s); };
+  auto bar_raw_full = [&](int ring, int s) { return bars + 8u * (ring * 32 + 16 + s); };
+  auto bar_raw_empty = [&](int ring, int s) { return bars + 8u * (ring * 32 + 24 + s); };
+  auto bar_st = [&](int w, int i) { return bars + 8u * (64 + w * 6 + i); };
+  enum { Q_FULL, Q_EMPTY, S_FULL, P_FULL, O_FULL, DRAIN };
+  constexpr int kMmaWarp = R::kWarps - 2;
 
   if (tid == 0) {
     ctl[0] = (sbase & 1023u) ? DSA_DEV_ERR_BOUNDS : 0;   // the swizzle needs a 1024-byte base
     ctl[1] = (sbase & 1023u) ? 1 : 0;
     ctl[4] = 0;
-    for (int r = 0; r < kRings; ++r)
+    for (int r = 0; r < kRings; ++r) {
       for (int s = 0; s < pl.nst; ++s) {
-        mbar_init(bar_full(r, s), tma ? 1 : kLoaders);
-        mbar_init(bar_empty(r, s), PAIR ? 2 : 1);
+        mbar_init(bar_full(r, s), R::kWorkWarps > 0 ? kLoaders : 1);
+        mbar_init(bar_empty(r, s), kPair ? 2 : 1);
       }
+      for (int s = 0; s < pl.nraw; ++s) {
+        mbar_init(bar_raw_full(r, s), 1);
+        mbar_init(bar_raw_empty(r, s), kLoaders / 32);
+      }
+    }
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar_st(w, Q_FULL), 32);
       mbar_init(bar_st(w, Q_EMPTY), 1);
       mbar_init(bar_st(w, S_FULL), 1);
       mbar_init(bar_st(w, P_FULL), 4);
       mbar_init(bar_st(w, O_FULL), 1);
-      mbar_init(bar_st(w, O_FREE), 4);
       mbar_init(bar_st(w, DRAIN), 1);
     }
     fence_mbar_init();
@@ -328,7 +384,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
 
   // ---- the unit list (every block the same) ----
   const int gsz = (p.num_seqs + kGroups - 1) / kGroups;
-  const int n_streams = PAIR ? (int)gridDim.x : pl.streams * (int)gridDim.x;
+  const int n_streams = kPair ? (int)gridDim.x : pl.streams * (int)gridDim.x;
   {
     float* const red = reinterpret_cast<float*>(smem);   // scratch before any tile is loaded
     long long work = 0;
@@ -341,7 +397,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
         Doc o;
         int mt, kt;
         bad |= !doc_info(p, d, &o);
-        doc_tiles<PAIR>(p, o, &mt, &kt);
+        doc_tiles<kPair>(p, o, &mt, &kt);
         work += (long long)mt * kt * p.c.n_kv;
         if (mt > 0) kmax = max(kmax, kt);
       }
@@ -376,7 +432,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
           Doc o;
           int mt, kt;
           doc_info(p, d, &o);
-          doc_tiles<PAIR>(p, o, &mt, &kt);
+          doc_tiles<kPair>(p, o, &mt, &kt);
 #pragma unroll
           for (int c = 0; c < 8; ++c) units[c] += mt * p.c.n_kv * splits_of(kt, cand[c]);
         }
@@ -410,7 +466,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
         Doc o;
         int mt, kt;
         doc_info(p, d, &o);
-        doc_tiles<PAIR>(p, o, &mt, &kt);
+        doc_tiles<kPair>(p, o, &mt, &kt);
         mine += mt * p.c.n_kv * splits_of(kt, chunk);
       }
     }
@@ -434,7 +490,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
           Doc o;
           int mt, kt;
           doc_info(p, d, &o);
-          doc_tiles<PAIR>(p, o, &mt, &kt);
+          doc_tiles<kPair>(p, o, &mt, &kt);
           p.doc_base[d] = before;
           before += mt * p.c.n_kv * splits_of(kt, chunk);
         }
@@ -454,99 +510,101 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
   const int wg = warp >> 2;
   // Independent streams: all first streams of the grid before the second ones, so few units spread over all SMs.
   auto first_unit = [&](int w) {
-    return PAIR ? (int)blockIdx.x : (w < pl.streams ? w * (int)gridDim.x + (int)blockIdx.x : n_units);
+    return kPair ? (int)blockIdx.x : (w < pl.streams ? w * (int)gridDim.x + (int)blockIdx.x : n_units);
+  };
+  // The query tile of a unit, by one warp (zeros behind its last row).
+  auto load_q = [&](const Unit& x, int w) {
+    constexpr int PPR = D / 8;
+    constexpr int RPP = 32 / PPR;
+    const int rows = (int)(pl.q_bytes / (D * 2));
+    const int c = lane % PPR, rsub = lane / PPR;
+    const uint32_t qb = sbase + (uint32_t)w * pl.q_bytes + (uint32_t)(c >> 3) * (uint32_t)(rows * 128);
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + c * 8;
+    const int tokens = x.i1 - x.i0;
+    const uint16_t* src = q + (int64_t)(x.q0 + x.i0) * p.q_stride + (int64_t)(x.h * p.group) * D;
+    int tok = 0, g = rsub;
+    for (int r = rsub; r < rows; r += RPP, g += RPP) {
+      while (g >= p.group) {
+        g -= p.group;
+        ++tok;
+      }
+      const bool there = tok < tokens;
+      cp_async16(qb + r * 128 + (((c & 7) ^ (r & 7)) << 4), there ? src + tok * p.q_stride + g * D : q, there);
+    }
+    cp_arrive(bar_st(w, Q_FULL));
   };
 
-  if (wg >= 2 && wg < 2 + R::kLoadWarps / 4) {
-    // ======================= loaders =======================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kLoadRegs));
-    const int ring = PAIR ? 0 : (tid - 256) / kLoaders;
+  if (R::kWorkWarps > 0 && wg >= 2 && wg < 2 + R::kWorkWarps / 4) {
+    // ======================= workers =======================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kWorkRegs));
+    const int ring = kPair ? 0 : (tid - 256) / kLoaders;
     const int lt = (tid - 256) % kLoaders;           // thread of this ring
     const int bar_id = 1 + ring;
     const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
-    // Every visible key of a BF16 cache: TMA, a box per page, issued by one warp (a lane to a page).
-    // The unit's last tile may end inside a page whose other slots hold anything: the warp copies
-    // that one row by row, with zeros behind the last visible key.
-    auto load_tma = [&] {
-      const int shift = p.c.page_shift;
-      const int box = min(kAttnKeys, 1 << shift);               // keys per box
-      const int boxes = kAttnKeys / box;
-      int st = 0;
-      uint32_t ph = 0;
-      bool wrapped = false, bad_page = false;
-      for (int u = first_unit(ring); u < n_units; u += n_streams) {
-        const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, PAIR ? 0 : ring);
-        const int32_t* table = p.c.table + (int64_t)x.d * p.c.max_pages;
-        const int last = x.P0 + x.last;                         // keys visible to the unit
-        auto page_of = [&](int key) {
-          return key < last ? __ldg(table + (key >> shift)) : 0;   // (doc_info: within max_pages)
-        };
-        int page = x.n_shared > 0 && lane < boxes ? page_of(x.lo * kAttnKeys + lane * box) : 0;
-        for (int j = 0; j < x.n_shared; ++j) {
-          const int key0 = (x.lo + j) * kAttnKeys;
-          const int now = page;
-          if (j + 1 < x.n_shared && lane < boxes) page = page_of(key0 + kAttnKeys + lane * box);
-          const bool whole = key0 + kAttnKeys <= last;
-          const bool good = (unsigned)now < (unsigned)p.c.num_pages;
-          const bool mine = whole && lane < boxes && good;
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * (uint32_t)box * D * 2;
-          if (whole && lane < boxes && !good) bad_page = true;
-          for (int kv = 0; kv < 2; ++kv) {
-            if (wrapped && !__all_sync(0xffffffffu, wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo))) {
-              cp_wait<0>();
-              return;
-            }
-            const uint32_t dst = ring_base + (uint32_t)st * kStage;
-            const bool withheld = p.fault_inject == 1 && u == first_unit(ring) && j == 0 && kv == 0;   // (tests)
-            if (whole) {
-              if (!withheld) {
-                if (lane == 0) mbar_arrive_expect_tx(bar_full(ring, st), bytes);
-#pragma unroll 1
-                for (int i = 0; i < boxes; ++i) {   // (one lane and uniform coordinates: a lane to a box issues slower)
-                  const int pg = __shfl_sync(0xffffffffu, now, i);
-                  if (lane == 0 && (unsigned)pg < (unsigned)p.c.num_pages) {
-                    const int slot = (key0 + i * box) & ((1 << shift) - 1), z = pg * p.c.n_kv + x.h;
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                      tma_load_3d(dst + c * kChunk + i * box * 128, kv ? &p.tm_v : &p.tm_k, bar_full(ring, st), c * 64, slot, z);
-                  }
-                }
-              }
-            } else {
-              constexpr int PPR = D / 8;
-              const int c = lane % PPR;
-              const uint16_t* src = reinterpret_cast<const uint16_t*>(kv ? p.c.v : p.c.k) + c * 8;
-#pragma unroll 4
-              for (int r = lane / PPR; r < kAttnKeys; r += 32 / PPR) {
-                const int64_t cr = key0 + r < last ? cache_row(p.c, x.d, key0 + r, x.h) : -1;
-                if (key0 + r < last && cr < 0) bad_page = true;
-                cp_async16(dst + (uint32_t)(c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                           src + (cr < 0 ? 0 : cr * D), cr >= 0);
-              }
-              cp_commit();
-              cp_wait<0>();
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0 && !withheld) mbar_arrive(bar_full(ring, st));
-            }
-            if (++st == pl.nst) {
-              st = 0;
-              ph ^= 1u;
-              wrapped = true;
-            }
+    bool ok = true;
+    int st = 0;
+    uint32_t ph = 0;
+    bool wrapped = false;   // every stage has been used once
+    auto advance = [&] {
+      if (++st == pl.nst) {
+        st = 0;
+        ph ^= 1u;
+        wrapped = true;
+      }
+    };
+    if constexpr (MODE != GATHER) {
+      // Stored half tiles (keys 0-63, 64-127, values 0-63, 64-127 of a tile) to BF16 stages.
+      constexpr int PPR = D / 16;                  // 16-code pieces per row
+      constexpr int RPP = kLoaders / PPR;
+      const int c = lt % PPR, rsub = lt / PPR;
+      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem;
+      const int* const meta = reinterpret_cast<const int*>(smem + pl.off_rows) + ring * 8;
+      const uint32_t dcol = (uint32_t)(c >> 2) * kChunk;
+      const int c0 = (c & 3) * 2;                  // first of the two 16-byte pieces in its 128-byte span
+      const int sw = p.c.sw, blk = sw == 1 ? 0 : c >> 1;
+      int slot = 0;
+      uint32_t rph = 0;
+      for (int u = first_unit(ring); u < n_units && ok; u += n_streams) {
+        const int n = decode_unit<kPair>(p, tab, gsz, chunk, u, kPair ? 0 : ring).n_shared;
+        for (int it = 0; it < 4 * n && ok; ++it) {
+          if (!(it & 1) && wrapped) ok = wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo);
+          ok = __all_sync(0xffffffffu, ok && wait_bar(bar_raw_full(ring, slot), rph, abort_flag, status, tmo));
+          if (!ok) break;
+          const uint32_t raw = raw_base + (uint32_t)slot * kRawItem;
+          const uint8_t* scales = smem + (raw - sbase) + kAttnKeys / 2 * D;
+          const int valid = meta[slot];
+          const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
+#pragma unroll 2
+          for (int r = rsub; r < kAttnKeys / 2; r += RPP) {
+            uint32_t w4[4], o[8];
+            ld_shared_v4(raw + r * D + c * 16, w4);
+            const uint32_t e8 = scales[r * sw + blk];
+            if (r >= valid) w4[0] = w4[1] = w4[2] = w4[3] = 0;   // nothing of the page's other slots
+            widen16(w4, r < valid ? e8 : 0, o);
+            const int row = (it & 1) * (kAttnKeys / 2) + r;
+            const uint32_t rowd = dst + row * 128;
+            st_shared_v4(rowd + ((uint32_t)(c0 ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+            st_shared_v4(rowd + ((uint32_t)((c0 + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_raw_empty(ring, slot));
+          if (++slot == pl.nraw) {
+            slot = 0;
+            rph ^= 1u;
+          }
+          if (it & 1) {
+            fence_proxy_async_smem();
+            mbar_arrive(bar_full(ring, st));
+            advance();
           }
         }
       }
-      if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
-    };
-    if (tma) {
-      if (lt < 32) load_tma();
     } else {
     constexpr int kRowBufs = Q8 ? 2 : 1;   // (BF16: the next tile's rows wait for a second barrier)
     uint32_t* const rowtab = reinterpret_cast<uint32_t*>(smem + pl.off_rows) + ring * kRowBufs * kAttnKeys;
     uint32_t* const sctab = reinterpret_cast<uint32_t*>(smem + pl.off_scale) + ring * 4 * 2 * kAttnKeys;
     uint32_t* const masks = reinterpret_cast<uint32_t*>(smem + pl.off_mask) + ring * kMaskRing * 4;
-    bool bad_page = false, ok = true;
+    bool bad_page = false;
 
     // ---- position -> page -> row, a step per tile; `fu`, `fj`, `fx`: the tile that enters ----
     int fu = first_unit(ring), fj = -1;
@@ -616,10 +674,8 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
               sctab[((pubs & 3) * 2) * kAttnKeys + r] = out.sck[i];
               sctab[((pubs & 3) * 2 + 1) * kAttnKeys + r] = out.scv[i];
             }
-            if constexpr (!PAIR) {
-              const uint32_t seen = __ballot_sync(0xffffffffu, out.row[i] != ~0u);
-              if (lane == 0) masks[(pubs % kMaskRing) * 4 + (r >> 5)] = seen;
-            }
+            const uint32_t seen = __ballot_sync(0xffffffffu, out.row[i] != ~0u);
+            if (lane == 0) masks[(pubs % kMaskRing) * 4 + (r >> 5)] = seen;
           }
         }
         ++pubs;
@@ -640,7 +696,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
         fj = 0;
         if (fx.n_shared > 0) fu += n_streams;   // (0: nothing decoded yet)
         for (; fu < n_units; fu += n_streams) {
-          fx = decode_unit<PAIR>(p, tab, gsz, chunk, fu, PAIR ? 0 : ring);
+          fx = decode_unit<false>(p, tab, gsz, chunk, fu, ring);
           if (fx.n_shared > 0) break;
         }
       }
@@ -659,18 +715,12 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
       }
     };
 
-    int st = 0;
-    uint32_t ph = 0;
-    bool wrapped = false;   // every stage has been used once
-    auto advance = [&] {
-      if (++st == pl.nst) {
-        st = 0;
-        ph ^= 1u;
-        wrapped = true;
+    // A free stage, for all of the ring's workers (the vote makes them give up together).
+    auto wait_empty = [&](int s, uint32_t parity, bool used) {
+      if (used) {
+        if (lt < 32 && ok) ok = wait_bar(bar_empty(ring, s), parity, abort_flag, status, tmo);
+        ok = !named_bar_or(bar_id, kLoaders, !ok);
       }
-    };
-    auto wait_empty = [&] {
-      if (wrapped && ok) ok = wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo);
       return ok;
     };
 
@@ -680,26 +730,31 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
     if constexpr (Q8) step();
     if constexpr (!Q8) {
       constexpr int PPR = D / 8;                   // 16-byte pieces per row
-      constexpr int RPP = kLoaders / PPR;          // rows per pass
+      constexpr int RPP = kLoaders / PPR;          // rows per pass: 4 or 8
       const int c = lt % PPR, rsub = lt / PPR;
-      const uint32_t dcol = (uint32_t)(c >> 3) * kChunk;
+      const uint32_t dcol = (uint32_t)(c >> 3) * kChunk + rsub * 128;
+      const uint32_t col = (c & 7) ^ rsub;         // rows of a pass differ in their low bits by rsub only
+      const uint16_t* kb = reinterpret_cast<const uint16_t*>(p.c.k) + c * 8;
+      const uint16_t* vb = reinterpret_cast<const uint16_t*>(p.c.v) + c * 8;
       for (int t = 0; t < pubs; ++t) {
-        if (named_bar_or(bar_id, kLoaders, !ok)) break;   // all give up together
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!wait_empty()) break;
-          const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(kv ? p.c.v : p.c.k) + c * 8;
-          if (p.fault_inject != 1 || t > 0 || kv > 0) {   // the tests' withheld first stage
+        named_bar_sync(bar_id, kLoaders);          // the tile's rows are in the table
+        const int ks = st;
+        if (!wait_empty(st, ph ^ 1u, wrapped)) break;   // (every worker at the same place)
+        advance();
+        if (!wait_empty(st, ph ^ 1u, wrapped)) break;
+        const uint32_t kd = ring_base + (uint32_t)ks * kStage + dcol, vd = ring_base + (uint32_t)st * kStage + dcol;
 #pragma unroll 8
-            for (int i = 0; i < kAttnKeys / RPP; ++i) {
-              const int r = i * RPP + rsub;
-              const uint32_t cr = rowtab[r];
-              cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + (cr == ~0u ? 0 : (size_t)cr * D), cr != ~0u);
-            }
-            cp_arrive(bar_full(ring, st));
-          }
-          advance();
+        for (int i = 0; i < kAttnKeys / RPP; ++i) {
+          const uint32_t e = rowtab[i * RPP + rsub];
+          const bool there = e != ~0u;
+          const size_t off = (size_t)(there ? e : 0) * D;
+          const uint32_t at = i * RPP * 128 + ((col ^ ((i * RPP) & 7)) << 4);
+          cp_async16(kd + at, kb + off, there);
+          cp_async16(vd + at, vb + off, there);
         }
+        if (p.fault_inject != 1 || t > 0) cp_arrive(bar_full(ring, ks));   // (the tests' withheld first stage)
+        cp_arrive(bar_full(ring, st));
+        advance();
         named_bar_sync(bar_id, kLoaders);
         step();
       }
@@ -707,9 +762,8 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
       constexpr int PPR = D / 16;                  // 16-code pieces per row
       constexpr int RPP = kLoaders / PPR;
       constexpr int kPasses = kAttnKeys / 2 / RPP; // half a tile is one item of the fetch ring
-      constexpr uint32_t kItem = kAttnKeys / 2 * D;
       const int c = lt % PPR, rsub = lt / PPR;
-      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kItem + lt * 16;
+      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem + lt * 16;
       const uint32_t dcol = (uint32_t)(c >> 2) * kChunk;
       const int c0 = (c & 3) * 2;                  // first of the two 16-byte pieces in its 128-byte span
       // items: keys 0-63, keys 64-127, values 0-63, values 64-127 of a tile
@@ -719,17 +773,17 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
         if (!fend && fi == 0) {
           if (ft >= pubs) {
             fend = true;
-          } else if (named_bar_or(bar_id, kLoaders, !ok)) {   // all give up together
-            ok = false;
+          } else if (!ok) {
             fend = true;
           } else {
+            named_bar_sync(bar_id, kLoaders);      // the tile's rows are in the table
             step();
           }
         }
         if (!fend) {
           const uint8_t* src = reinterpret_cast<const uint8_t*>(fi >> 1 ? p.c.v : p.c.k) + c * 16;
           const uint32_t* rt = rowtab + (ft & 1) * kAttnKeys + (fi & 1) * (kAttnKeys / 2);
-          const uint32_t dst = raw_base + (uint32_t)fslot * kItem;
+          const uint32_t dst = raw_base + (uint32_t)fslot * kRawItem;
 #pragma unroll
           for (int i = 0; i < kPasses; ++i) {
             const uint32_t cr = rt[i * RPP + rsub];
@@ -745,7 +799,8 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
       for (int i = 0; i < pl.nraw; ++i) fetch();
       int slot = 0;
       for (int it = 0; it < fetched; ++it) {
-        if (it & 1 ? ok : wait_empty()) {
+        if (!(it & 1) && !wait_empty(st, ph ^ 1u, wrapped)) break;   // (every worker at the same place)
+        {
           switch (pl.nraw) {   // the oldest item has landed
             case 1: cp_wait<0>(); break;
             case 2: cp_wait<1>(); break;
@@ -755,49 +810,18 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
             default: cp_wait<5>(); break;
           }
           const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
-          const uint32_t src = raw_base + (uint32_t)slot * kItem;
+          const uint32_t src = raw_base + (uint32_t)slot * kRawItem;
           const uint32_t* sct = sctab + (((it >> 2) & 3) * 2 + ((it >> 1) & 1)) * kAttnKeys;
           const int sshift = p.c.sw == 1 ? 0 : 8 * (c >> 1);
 #pragma unroll 2
           for (int i = 0; i < kPasses; ++i) {
             const int r = (it & 1) * (kAttnKeys / 2) + i * RPP + rsub;
-            uint32_t w4[4];
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w4[0]), "=r"(w4[1]), "=r"(w4[2]), "=r"(w4[3])
-                         : "r"(src + i * (kLoaders * 16)));
-            // E4M3 bits s.eeee.mmm placed at a BF16's sign, low exponent and high mantissa bits read
-            // as value * 2^-120 (subnormals included); one exact product with 2^(120 + e) restores it
-            const uint32_t e8 = (sct[r] >> sshift) & 0xFFu;              // 2^(e8 - 127)
-            const uint32_t first = e8 > 134u ? 254u : e8 + 120u;         // 2^(first - 127): BF16 ends at 2^127
-            __nv_bfloat162 f;
-            *reinterpret_cast<uint32_t*>(&f) = (first << 7) * 0x00010001u;
-            uint32_t o[8];
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-#pragma unroll
-              for (int hlf = 0; hlf < 2; ++hlf) {
-                const uint32_t t = __byte_perm(w4[q4], 0, hlf ? 0x3424 : 0x1404);
-                uint32_t b = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
-                __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&b), f);
-                o[2 * q4 + hlf] = *reinterpret_cast<uint32_t*>(&v);
-              }
-            }
-            if (e8 > 134u) {                                             // values beyond 2^16: a second factor
-              __nv_bfloat162 f2;
-              *reinterpret_cast<uint32_t*>(&f2) = ((e8 - 134u + 127u) << 7) * 0x00010001u;
-#pragma unroll
-              for (int q8 = 0; q8 < 8; ++q8) {
-                __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[q8]), f2);
-                o[q8] = *reinterpret_cast<uint32_t*>(&v);
-              }
-            }
+            uint32_t w4[4], o[8];
+            ld_shared_v4(src + i * (kLoaders * 16), w4);
+            widen16(w4, (sct[r] >> sshift) & 0xFFu, o);
             const uint32_t rowd = dst + r * 128;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(rowd + ((uint32_t)(c0 ^ (r & 7)) << 4)), "r"(o[0]),
-                         "r"(o[1]), "r"(o[2]), "r"(o[3])
-                         : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(rowd + ((uint32_t)((c0 + 1) ^ (r & 7)) << 4)),
-                         "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                         : "memory");
+            st_shared_v4(rowd + ((uint32_t)(c0 ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+            st_shared_v4(rowd + ((uint32_t)((c0 + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
           }
           if (it & 1) {
             fence_proxy_async_smem();
@@ -813,42 +837,186 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
     if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
     }
   } else if (wg >= 2) {
-    // ======================= MMA and query-loader warps =======================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kMmaRegs));
-    const int w = warp & 1;
-    if (warp >= kMmaWarp + 2) {
-      // query tiles of stream w, each as soon as the last product with the one before has been done
-      constexpr int PPR = D / 8;
-      constexpr int RPP = 32 / PPR;
-      const uint32_t qb = sbase + (uint32_t)w * pl.q_bytes;
-      const int rows = (int)(pl.q_bytes / (D * 2));
-      const int c = lane % PPR, rsub = lane / PPR;
-      const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + c * 8;
-      const uint32_t dcol = (uint32_t)(c >> 3) * (uint32_t)(rows * 128);
-      uint32_t nq = 0;
-      bool ok = true;
-      for (int u = first_unit(w); u < n_units && ok; u += n_streams) {
-        const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, w);
-        if (x.n == 0) continue;
-        if (nq > 0) ok = mbar_wait(bar_st(w, Q_EMPTY), (nq - 1) & 1u, abort_flag, status, tmo);
-        if (!ok) break;
-        ++nq;
-        const int tokens = x.i1 - x.i0;
-        const uint16_t* src = q + (int64_t)(x.q0 + x.i0) * p.q_stride + (int64_t)(x.h * p.group) * D;
-        int tok = 0, g = rsub;
-        for (int r = rsub; r < rows; r += RPP, g += RPP) {
-          while (g >= p.group) {
-            g -= p.group;
-            ++tok;
+    // ======================= loaders and MMA =======================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kAuxRegs));
+    // Every visible key of a BF16 cache: TMA, a box per page, issued by one warp.  The unit's last
+    // tile may end inside a page whose other slots hold anything: the warp copies that one row by
+    // row, with zeros behind the last visible key.
+    auto load_tma = [&](int ring) {
+      const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
+      const int shift = p.c.page_shift;
+      const int box = min(kAttnKeys, 1 << shift);               // keys per box
+      const int boxes = kAttnKeys / box;
+      int st = 0;
+      uint32_t ph = 0;
+      bool wrapped = false, bad_page = false;
+      for (int u = first_unit(ring); u < n_units; u += n_streams) {
+        const Unit x = decode_unit<kPair>(p, tab, gsz, chunk, u, kPair ? 0 : ring);
+        const int32_t* table = p.c.table + (int64_t)x.d * p.c.max_pages;
+        const int last = x.P0 + x.last;                         // keys visible to the unit
+        auto page_of = [&](int key) {
+          return key < last ? __ldg(table + (key >> shift)) : 0;   // (doc_info: within max_pages)
+        };
+        int page = x.n_shared > 0 && lane < boxes ? page_of(x.lo * kAttnKeys + lane * box) : 0;
+        for (int j = 0; j < x.n_shared; ++j) {
+          const int key0 = (x.lo + j) * kAttnKeys;
+          const int now = page;
+          if (j + 1 < x.n_shared && lane < boxes) page = page_of(key0 + kAttnKeys + lane * box);
+          const bool whole = key0 + kAttnKeys <= last;
+          const bool good = (unsigned)now < (unsigned)p.c.num_pages;
+          const bool mine = whole && lane < boxes && good;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * (uint32_t)box * D * 2;
+          if (whole && lane < boxes && !good) bad_page = true;
+          for (int kv = 0; kv < 2; ++kv) {
+            if (wrapped && !__all_sync(0xffffffffu, wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo))) {
+              cp_wait<0>();
+              return;
+            }
+            const uint32_t dst = ring_base + (uint32_t)st * kStage;
+            const bool withheld = p.fault_inject == 1 && u == first_unit(ring) && j == 0 && kv == 0;   // (tests)
+            if (whole) {
+              if (!withheld) {
+                if (lane == 0) mbar_arrive_expect_tx(bar_full(ring, st), bytes);
+#pragma unroll 1
+                for (int i = 0; i < boxes; ++i) {   // (one lane and uniform coordinates: a lane to a box issues slower)
+                  const int pg = __shfl_sync(0xffffffffu, now, i);
+                  if (lane == 0 && (unsigned)pg < (unsigned)p.c.num_pages) {
+                    const int slot = (key0 + i * box) & ((1 << shift) - 1), z = pg * p.c.n_kv + x.h;
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                      tma_load_3d(dst + c * kChunk + i * box * 128, kv ? &p.tm_v : &p.tm_k, bar_full(ring, st), c * 64, slot, z);
+                  }
+                }
+              }
+            } else {
+              constexpr int PPR = D / 8;
+              const int c = lane % PPR;
+              const uint16_t* src = reinterpret_cast<const uint16_t*>(kv ? p.c.v : p.c.k) + c * 8;
+#pragma unroll 4
+              for (int r = lane / PPR; r < kAttnKeys; r += 32 / PPR) {
+                const int64_t cr = key0 + r < last ? cache_row(p.c, x.d, key0 + r, x.h) : -1;
+                if (key0 + r < last && cr < 0) bad_page = true;
+                cp_async16(dst + (uint32_t)(c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           src + (cr < 0 ? 0 : cr * D), cr >= 0);
+              }
+              cp_commit();
+              cp_wait<0>();
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && !withheld) mbar_arrive(bar_full(ring, st));
+            }
+            if (++st == pl.nst) {
+              st = 0;
+              ph ^= 1u;
+              wrapped = true;
+            }
           }
-          const bool there = tok < tokens;
-          cp_async16(qb + dcol + r * 128 + (((c & 7) ^ (r & 7)) << 4), there ? src + tok * p.q_stride + g * D : q, there);
         }
-        cp_arrive(bar_st(w, Q_FULL));
+      }
+      if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
+    };
+    // Every visible key of an 8-bit cache, as stored: half tiles of codes (a TMA box per page) and their
+    // scales (a bulk copy per page); the workers learn how many rows of a half tile are visible.  The
+    // stream's query tile is loaded on the way.
+    auto load_raw = [&](int ring) {
+      constexpr int kHalf = kAttnKeys / 2;
+      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem;
+      int* const meta = reinterpret_cast<int*>(smem + pl.off_rows) + ring * 8;
+      const int shift = p.c.page_shift, sw = p.c.sw;
+      const int box = min(kHalf, 1 << shift), boxes = kHalf / box;
+      int slot = 0;
+      uint32_t rph = 0, nq = 0;
+      bool wrapped = false, bad_page = false;
+      for (int u = first_unit(ring); u < n_units; u += n_streams) {
+        const Unit x = decode_unit<kPair>(p, tab, gsz, chunk, u, kPair ? 0 : ring);
+        const int32_t* table = p.c.table + (int64_t)x.d * p.c.max_pages;
+        const int last = x.P0 + x.last;                         // keys visible to the unit
+        auto page_of = [&](int key) {
+          return key < last ? __ldg(table + (key >> shift)) : -1;   // (doc_info: within max_pages)
+        };
+        int page = x.n_shared > 0 && lane < 2 * boxes ? page_of(x.lo * kAttnKeys + lane * box) : 0;
+        for (int j = 0; j < x.n_shared; ++j) {
+          const int key0 = (x.lo + j) * kAttnKeys;
+          const int now = page;
+          if (j + 1 < x.n_shared && lane < 2 * boxes) page = page_of(key0 + kAttnKeys + lane * box);
+          const bool good = (unsigned)now < (unsigned)p.c.num_pages;
+          if (lane < 2 * boxes && key0 + lane * box < last && !good) bad_page = true;
+          const uint32_t have = __ballot_sync(0xffffffffu, lane < 2 * boxes && good);
+#pragma unroll 1
+          for (int it = 0; it < 4; ++it) {
+            if (wrapped &&
+                !__all_sync(0xffffffffu, wait_bar(bar_raw_empty(ring, slot), rph ^ 1u, abort_flag, status, tmo))) {
+              cp_wait<0>();
+              return;
+            }
+            const uint32_t bar = bar_raw_full(ring, slot), dst = raw_base + (uint32_t)slot * kRawItem;
+            const int k0 = key0 + (it & 1) * kHalf, b0 = (it & 1) * boxes;
+            const uint32_t mine = (have >> b0) & ((1u << boxes) - 1u);
+            const bool withheld = p.fault_inject == 1 && u == first_unit(ring) && j == 0 && it == 0;   // (tests)
+            if (lane == 0 && !withheld) {
+              meta[slot] = min(kHalf, max(0, last - k0));
+              mbar_arrive_expect_tx(bar, __popc(mine) * (uint32_t)(box * (D + sw)));
+            }
+            const uint8_t* sc = it >> 1 ? p.c.v_scale : p.c.k_scale;
+#pragma unroll 1
+            for (int i = 0; i < boxes; ++i) {
+              const int pg = __shfl_sync(0xffffffffu, now, b0 + i);
+              if (lane == 0 && !withheld && ((mine >> i) & 1u)) {
+                const int in_page = (k0 + i * box) & ((1 << shift) - 1), z = pg * p.c.n_kv + x.h;
+                tma_load_3d(dst + i * box * D, it >> 1 ? &p.tm_v : &p.tm_k, bar, 0, in_page, z);
+                bulk_load(dst + kHalf * D + i * box * sw, sc + ((((int64_t)z << shift) + in_page) * sw), box * sw, bar);
+              }
+            }
+            if (++slot == pl.nraw) {
+              slot = 0;
+              rph ^= 1u;
+              wrapped = true;
+            }
+          }
+          if (!kPair && j == 0) {
+            if (nq > 0 &&
+                !__all_sync(0xffffffffu, wait_bar(bar_st(ring, Q_EMPTY), (nq - 1) & 1u, abort_flag, status, tmo)))
+              break;
+            ++nq;
+            load_q(x, ring);
+          }
+        }
       }
       cp_wait<0>();
+      if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
+    };
+    // Query tiles of streams w0 .. w1 - 1, each as soon as its stream's last product with the one before is done.
+    auto load_queries = [&](int w0, int w1) {
+      uint32_t nq[2] = {0, 0};
+      for (int u = first_unit(w0); u < n_units; u += n_streams) {
+        for (int w = w0; w < w1; ++w) {
+          const Unit x = decode_unit<kPair>(p, tab, gsz, chunk, u, w);
+          if (x.n == 0) continue;
+          if (nq[w - w0] > 0 && !__all_sync(0xffffffffu, mbar_wait(bar_st(w, Q_EMPTY), (nq[w - w0] - 1) & 1u, abort_flag,
+                                                                    status, tmo))) {
+            cp_wait<0>();
+            return;
+          }
+          ++nq[w - w0];
+          load_q(x, w);
+        }
+      }
+      cp_wait<0>();
+    };
+    if (warp < kMmaWarp) {
+      if constexpr (MODE != GATHER && Q8) {
+        if (warp == R::kKeyWarp) load_raw(0);
+        else if (warp == R::kKeyWarp + 1 && kPair) load_queries(0, 2);
+        else if (warp == R::kKeyWarp + 1) load_raw(1);
+      } else {
+        if (MODE != GATHER && warp >= R::kKeyWarp && warp < R::kKeyWarp + kRings) load_tma(warp - R::kKeyWarp);
+        else if (warp == R::kQueryWarp) load_queries(0, 1);
+        else if (warp == R::kQueryWarp + 1) load_queries(1, 2);
+      }
+      __syncwarp();
     } else {
-      const int ring = PAIR ? 0 : w;
+      const int w = warp - kMmaWarp;
+      const int ring = kPair ? 0 : w;
       const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
       const uint32_t t_s = tmem + (uint32_t)w * 128, t_o = tmem + 256 + (uint32_t)w * 128;
       constexpr uint32_t idesc_qk = idesc_bf16(kAttnRows, kAttnKeys);
@@ -876,7 +1044,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
           }
         };
         for (int u = first_unit(w); u < n_units && ok; u += n_streams) {
-          const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, w);
+          const Unit x = decode_unit<kPair>(p, tab, gsz, chunk, u, w);
           if (x.n > 0) {
             ok = wait_bar(bar_st(w, Q_FULL), nq & 1u, abort_flag, status, tmo);
             fence_proxy_async_smem();   // the query tile's cp.async writes
@@ -897,7 +1065,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
           if (x.n > 0 && ok) {
             ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
             if (!ok) break;
-            if (!tma) fence_proxy_async_smem();   // the loaders' cp.async writes, seen through the barrier
+            if (kWorkerCopies) fence_proxy_async_smem();   // the loaders' cp.async writes, seen through the barrier
             tc_fence_after();
             take_turn();
             issue_qk(x.n == 1);
@@ -906,7 +1074,6 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
           for (int j = 0; j < x.n && ok; ++j) {
             // everything but P is waited for first
             ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
-            if (ok && j == 0 && nq > 0) ok = wait_bar(bar_st(w, O_FREE), (nq - 1) & 1u, abort_flag, status, tmo);
             if (!ok) break;
             // N-major operand: 64-column chunks kChunk apart, groups of 8 keys 1024 bytes apart
             const uint64_t vd0 = smem_desc(ring_base + (uint32_t)st * kStage, kChunk, 1024, 2);
@@ -914,7 +1081,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
             advance();
             bool next = j + 1 < x.n;
             const bool have_k = next && mbar_try_wait(bar_full(ring, st), ph);
-            if (!tma) fence_proxy_async_smem();
+            if (kWorkerCopies) fence_proxy_async_smem();
             ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
             if (!ok) break;
             tc_fence_after();
@@ -930,14 +1097,14 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
             if (next && !have_k) {
               ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
               if (!ok) break;
-              if (!tma) fence_proxy_async_smem();
+              if (kWorkerCopies) fence_proxy_async_smem();
               take_turn();
               issue_qk(j + 2 == x.n);
               end_turn();
             }
           }
           if (x.n > 0) ++nq;
-          if constexpr (PAIR) {   // stages only the other stream needs
+          if constexpr (kPair) {   // stages only the other stream needs
             for (int j = 2 * x.n; j < 2 * x.n_shared && ok; ++j) {
               ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
               if (ok) mbar_arrive(bar_empty(ring, st));
@@ -954,6 +1121,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
     }
   } else {
     // ======================= softmax warpgroups =======================
+    // (shares of the launch's registers: Roles)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmaxRegs));
     const int w = wg;
     const int quarter = warp & 3;
@@ -964,8 +1132,9 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
     const float scale = p.scale_log2;
     uint32_t nt = 0, nq = 0;
     bool ok = true;
-    for (int u = first_unit(w); u < n_units && ok; u += n_streams) {
-      const Unit x = decode_unit<PAIR>(p, tab, gsz, chunk, u, w);
+    Unit x{}, nx{};
+    if (first_unit(w) < n_units) x = decode_unit<kPair>(p, tab, gsz, chunk, first_unit(w), w);
+    for (int u = first_unit(w); u < n_units && ok; u += n_streams, x = nx) {
       const int live = (x.i1 - x.i0) * p.group;
       const bool warp_live = quarter * 32 < live;
       const int tok = r / p.group, g = r - tok * p.group;
@@ -976,31 +1145,41 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
         if (!ok) break;
         if (warp_live) {
           tc_fence_after();
-          uint32_t s[kAttnKeys];
+          // BF16: the row's 128 logits stay in registers.  8-bit caches: the worker warps need the
+          // registers; 32 at a time are read from TMEM, twice (a second read of 64 KB a tile).
+          constexpr int kHeld = Q8 ? 32 : kAttnKeys;
+          uint32_t s[kHeld];
+          const int lim = vis - (x.lo + j) * kAttnKeys;
+          auto load_s = [&](int c0) {   // logits c0 .., those of keys not seen replaced by -inf
 #pragma unroll
-          for (int c = 0; c < kAttnKeys; c += 32) tmem_ld_x32(t_s + c, s + c);
-          tmem_ld_wait_tied<kAttnKeys>(s);
-          // keys not seen: -inf
-          if (!p.topk_idx) {
-            const int lim = vis - (x.lo + j) * kAttnKeys;
-            if (__any_sync(0xffffffffu, lim < kAttnKeys)) {
+            for (int c = 0; c < kHeld; c += 32) tmem_ld_x32(t_s + c0 + c, s + c);
+            tmem_ld_wait_tied<kHeld>(s);
+            if (!listed) {
+              if (__any_sync(0xffffffffu, lim < c0 + kHeld)) {
 #pragma unroll
-              for (int c = 0; c < kAttnKeys; ++c) s[c] = c < lim ? s[c] : 0xFF800000u;
+                for (int c = 0; c < kHeld; ++c) s[c] = c0 + c < lim ? s[c] : 0xFF800000u;
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kHeld; c += 32) {
+                const uint32_t mk = masks[(nt % kMaskRing) * 4 + ((c0 + c) >> 5)];
+                if (mk != 0xFFFFFFFFu) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) s[c + i] = (mk >> i) & 1u ? s[c + i] : 0xFF800000u;
+                }
+              }
             }
-          } else {
-            const uint4 mk = *reinterpret_cast<const uint4*>(masks + (nt % kMaskRing) * 4);
-            if ((mk.x & mk.y & mk.z & mk.w) != 0xFFFFFFFFu) {
-              const uint32_t mw[4] = {mk.x, mk.y, mk.z, mk.w};
-#pragma unroll
-              for (int c = 0; c < kAttnKeys; ++c) s[c] = (mw[c >> 5] >> (c & 31)) & 1u ? s[c] : 0xFF800000u;
-            }
-          }
+          };
           float mx[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) mx[c] = fmaxf(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+          for (int c = 0; c < 8; ++c) mx[c] = -INFINITY;
 #pragma unroll
-          for (int c = 16; c < kAttnKeys; c += 2)
-            mx[(c >> 1) & 7] = fmaxf(mx[(c >> 1) & 7], fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+          for (int c0 = kAttnKeys - kHeld; c0 >= 0; c0 -= kHeld) {   // (the first ones stay)
+            load_s(c0);
+#pragma unroll
+            for (int c = 0; c < kHeld; c += 2)
+              mx[(c >> 1) & 7] = fmaxf(mx[(c >> 1) & 7], fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+          }
           const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                   fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
           const float mt = top == -INFINITY ? -INFINITY : top * scale;
@@ -1025,17 +1204,21 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
           const float2 sc2 = make_float2(scale, scale), mm2 = make_float2(-mref, -mref);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < kAttnKeys; c += 16) {
-            uint32_t pk[8];
+          for (int c0 = 0; c0 < kAttnKeys; c0 += kHeld) {
+            if (c0 > 0) load_s(c0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float2 e = ffma2(as_f2(s[c + 2 * i], s[c + 2 * i + 1]), sc2, mm2);
-              e.x = ex2(e.x);
-              e.y = ex2(e.y);
-              sum[i & 1] = __fadd2_rn(sum[i & 1], e);
-              pk[i] = pack_bf16(e.x, e.y);
+            for (int c = 0; c < kHeld; c += 16) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float2 e = ffma2(as_f2(s[c + 2 * i], s[c + 2 * i + 1]), sc2, mm2);
+                e.x = ex2(e.x);
+                e.y = ex2(e.y);
+                sum[i & 1] = __fadd2_rn(sum[i & 1], e);
+                pk[i] = pack_bf16(e.x, e.y);
+              }
+              tmem_st_x8(t_s + (c0 + c) / 2, pk);   // over logits already read
             }
-            tmem_st_x8(t_s + c / 2, pk);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_st_wait();
@@ -1045,14 +1228,15 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
         if (lane == 0) mbar_arrive(bar_st(w, P_FULL));
       }
       if (!ok) break;
+      if (u + n_streams < n_units) nx = decode_unit<kPair>(p, tab, gsz, chunk, u + n_streams, w);   // (while O is formed)
       const bool mine = r < live;
       const int64_t orow = (int64_t)(x.q0 + x.i0 + tok) * p.n_heads + x.h * p.group + g;
-      const int64_t prow = (int64_t)(PAIR ? 2 * u + w : u) * pl.rows_cap + r;
+      const int64_t prow = (int64_t)(kPair ? 2 * u + w : u) * pl.rows_cap + r;
       if (x.n > 0) {
         ok = __all_sync(0xffffffffu, wait_bar(bar_st(w, O_FULL), nq & 1u, abort_flag, status, tmo));
         if (!ok) break;
         ++nq;
-        tc_fence_after();
+        tc_fence_after();   // (the next unit's first PV waits for its P, which follows these reads)
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -1060,11 +1244,6 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
           if (warp_live) {
             tmem_ld_x32(t_o + c, o);
             tmem_ld_wait_tied<32>(o);
-          }
-          if (c + 32 == D) {   // all read: the next unit's products may start
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_st(w, O_FREE));
           }
           if (mine) {
             if (x.ns == 1) {
@@ -1101,7 +1280,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_attention_kernel
 }
 
 // Joins the partial results of divided key ranges: one warp per (token, head).
-template <int D, bool PAIR>
+template <int D, bool kPair>
 __global__ void __launch_bounds__(256) paged_attention_join_kernel(const AttnParams p) {
   constexpr int VEC = D / 32;
   const int lane = threadIdx.x & 31;
@@ -1113,14 +1292,14 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const AttnPar
     Doc o;
     if (!doc_info(p, d, &o) || t < o.q0 || t >= o.q0 + o.T) continue;
     int mt, kt;
-    doc_tiles<PAIR>(p, o, &mt, &kt);
+    doc_tiles<kPair>(p, o, &mt, &kt);
     const int ns = splits_of(kt, chunk);
     if (ns == 1) continue;
     const int i = t - o.q0, tile = i / p.plan.tq;
-    const int ut = PAIR ? tile >> 1 : tile;
+    const int ut = kPair ? tile >> 1 : tile;
     const int u0 = p.doc_base[d] + ((hh / p.group) * mt + (mt - 1 - ut)) * ns;
     const int r = (i - tile * p.plan.tq) * p.group + hh % p.group;
-    auto slot = [&](int s) { return (int64_t)(PAIR ? 2 * (u0 + s) + (tile & 1) : u0 + s) * p.plan.rows_cap + r; };
+    auto slot = [&](int s) { return (int64_t)(kPair ? 2 * (u0 + s) + (tile & 1) : u0 + s) * p.plan.rows_cap + r; };
     float m = -INFINITY;
     for (int s = lane; s < ns; s += 32) {
       const float2 ml = p.part_ml[slot(s)];
@@ -1148,9 +1327,9 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const AttnPar
   }
 }
 
-template <int D, bool Q8, bool PAIR>
+template <int D, bool Q8, int MODE>
 cudaError_t launch(const AttnParams& p, int grid, int sm_count, cudaStream_t stream) {
-  auto kernel = paged_attention_kernel<D, Q8, PAIR>;
+  auto kernel = paged_attention_kernel<D, Q8, MODE>;
   cudaError_t e;
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -1159,17 +1338,17 @@ cudaError_t launch(const AttnParams& p, int grid, int sm_count, cudaStream_t str
     // The warpgroups' register shares add up to kLaunchRegs a thread: fewer at launch would leave them waiting.
     cudaFuncAttributes a;
     if ((e = cudaFuncGetAttributes(&a, kernel)) != cudaSuccess) return e;
-    if (a.numRegs < Roles<Q8>::kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+    if (a.numRegs < Roles<Q8, MODE>::kLaunchRegs) return cudaErrorInvalidDeviceFunction;
     // always the same value: calls of several threads do not disturb one another
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAttnSmemMax);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
   }
-  kernel<<<grid, Roles<Q8>::kThreads, p.plan.smem, stream>>>(p);
+  kernel<<<grid, Roles<Q8, MODE>::kThreads, p.plan.smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.plan.max_units == 0 || p.total_q == 0) return e;
   const int64_t blocks = ((int64_t)p.total_q * p.n_heads + 7) / 8;
-  paged_attention_join_kernel<D, PAIR><<<(unsigned)(blocks < 8 * sm_count ? blocks : 8 * sm_count), 256, 0, stream>>>(p);
+  paged_attention_join_kernel<D, MODE == PAIR><<<(unsigned)(blocks < 8 * sm_count ? blocks : 8 * sm_count), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -4,8 +4,9 @@
 namespace dsa {
 
 cudaError_t launch_paged_attention_64_q8(const AttnParams& p, int grid, int sm_count, cudaStream_t stream) {
-  return p.plan.pair ? attn::launch<64, true, true>(p, grid, sm_count, stream)
-                     : attn::launch<64, true, false>(p, grid, sm_count, stream);
+  if (p.plan.pair) return attn::launch<64, true, attn::PAIR>(p, grid, sm_count, stream);
+  if (p.plan.gather) return attn::launch<64, true, attn::GATHER>(p, grid, sm_count, stream);
+  return attn::launch<64, true, attn::SOLO>(p, grid, sm_count, stream);
 }
 
 }  // namespace dsa

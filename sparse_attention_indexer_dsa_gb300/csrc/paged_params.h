@@ -59,6 +59,7 @@ constexpr int kAttnSms = 152;       // the grid's upper bound, for workspace siz
 // How one call is laid out (attn_plan): tiles, shared memory and splits.
 struct AttnPlan {
   int pair;        // two query tiles share one key stream (long chunks); else two independent streams
+  int gather;      // rows resolved and copied one by one (listed keys, short page scales)
   int streams;     // independent streams per block (1 where two do not fit)
   int tq;          // tokens per query tile
   int rows_cap;    // rows of a tile that can be live
@@ -70,7 +71,7 @@ struct AttnPlan {
 };
 
 struct AttnParams {
-  CUtensorMap tm_k, tm_v;   // BF16 pages as [pages * heads][page_size][D], boxes of up to 128 rows x 64 columns
+  CUtensorMap tm_k, tm_v;   // pages as [pages * heads][page_size][D]: a box per page and tile
   PagedCacheView c;
   AttnPlan plan;
   const void* q;
@@ -96,8 +97,8 @@ struct AttnParams {
 constexpr int kAttnHdrChunk = 8;    // key tiles per split
 
 // False: these sizes need more shared memory than a block has.
-bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, bool eight_bit,
-               int topk_width);
+bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,
+               int page_size, int topk_width);
 size_t attn_workspace_bytes(const AttnPlan& pl, int num_seqs, int D);
 
 cudaError_t launch_cache_write(const CacheWriteParams& p, int D, int sm_count, cudaStream_t stream);
