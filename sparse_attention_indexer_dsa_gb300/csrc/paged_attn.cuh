@@ -304,21 +304,21 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&w)[4]) {
 // scales are too short for a bulk copy).
 enum { PAIR = 0, SOLO = 1, GATHER = 2 };
 
-// Warps: 8 softmax; workers (8-bit caches: 8 that widen rows; BF16 rows gathered: 4 that copy); the
+// Warps: 8 softmax; workers (8: they widen 8-bit rows, or copy gathered ones: four copy at half the rate); the
 // rest: key loaders (TMA), query loaders, MMA 0 and 1 last.  (The four warps of an SM's sub-partition
 // are those of equal number modulo 4; loaders and MMA warps are kept on different ones.)
 template <bool Q8, int MODE>
 struct Roles {
-  static constexpr int kWorkWarps = Q8 ? 8 : (MODE == GATHER ? 4 : 0);
-  static constexpr int kWarps = Q8 ? 20 : 16;
+  static constexpr int kWorkWarps = Q8 || MODE == GATHER ? 8 : 0;
+  static constexpr int kWarps = kWorkWarps > 0 ? 20 : 16;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kQueryWarp = MODE != GATHER && !Q8 ? 10 : kWarps - 4;   // and the next one
-  static constexpr int kKeyWarp = Q8 ? kWarps - 4 : 8;                        // TMA: and the next one
+  static constexpr int kQueryWarp = kWorkWarps > 0 ? kWarps - 4 : 10;         // and the next one
+  static constexpr int kKeyWarp = kWorkWarps > 0 ? kWarps - 4 : 8;            // TMA: and the next one
   // registers: shares of what the launch holds (threads x the launch's count, a multiple of 8)
-  static constexpr int kLaunchRegs = Q8 ? 96 : 128;
-  static constexpr int kSoftmaxRegs = Q8 ? 112 : 192;
-  static constexpr int kWorkRegs = Q8 ? 80 : 72;
-  static constexpr int kAuxRegs = Q8 ? 96 : (MODE == GATHER ? 56 : 64);
+  static constexpr int kLaunchRegs = kWorkWarps > 0 ? 96 : 128;
+  static constexpr int kSoftmaxRegs = kWorkWarps > 0 ? 112 : 192;
+  static constexpr int kWorkRegs = 80;
+  static constexpr int kAuxRegs = kWorkWarps > 0 ? 96 : 64;
   static_assert(2 * kSoftmaxRegs + kWorkWarps / 4 * kWorkRegs + (kWarps - 8 - kWorkWarps) / 4 * kAuxRegs <=
                     kWarps / 4 * kLaunchRegs, "shares");
 };
@@ -730,31 +730,29 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     if constexpr (Q8) step();
     if constexpr (!Q8) {
       constexpr int PPR = D / 8;                   // 16-byte pieces per row
-      constexpr int RPP = kLoaders / PPR;          // rows per pass: 4 or 8
+      constexpr int RPP = kLoaders / PPR;          // rows per pass: 8 or 16
       const int c = lt % PPR, rsub = lt / PPR;
       const uint32_t dcol = (uint32_t)(c >> 3) * kChunk + rsub * 128;
-      const uint32_t col = (c & 7) ^ rsub;         // rows of a pass differ in their low bits by rsub only
+      const uint32_t col = (c & 7) ^ (rsub & 7);   // (a pass is a multiple of 8 rows)
       const uint16_t* kb = reinterpret_cast<const uint16_t*>(p.c.k) + c * 8;
       const uint16_t* vb = reinterpret_cast<const uint16_t*>(p.c.v) + c * 8;
       for (int t = 0; t < pubs; ++t) {
         named_bar_sync(bar_id, kLoaders);          // the tile's rows are in the table
-        const int ks = st;
-        if (!wait_empty(st, ph ^ 1u, wrapped)) break;   // (every worker at the same place)
-        advance();
-        if (!wait_empty(st, ph ^ 1u, wrapped)) break;
-        const uint32_t kd = ring_base + (uint32_t)ks * kStage + dcol, vd = ring_base + (uint32_t)st * kStage + dcol;
-#pragma unroll 8
-        for (int i = 0; i < kAttnKeys / RPP; ++i) {
-          const uint32_t e = rowtab[i * RPP + rsub];
-          const bool there = e != ~0u;
-          const size_t off = (size_t)(there ? e : 0) * D;
-          const uint32_t at = i * RPP * 128 + ((col ^ ((i * RPP) & 7)) << 4);
-          cp_async16(kd + at, kb + off, there);
-          cp_async16(vd + at, vb + off, there);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!wait_empty(st, ph ^ 1u, wrapped)) break;   // (every worker at the same place)
+          const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
+          const uint16_t* src = kv ? vb : kb;
+#pragma unroll
+          for (int i = 0; i < kAttnKeys / RPP; ++i) {
+            const uint32_t e = rowtab[i * RPP + rsub];
+            const bool there = e != ~0u;
+            cp_async16(dst + i * RPP * 128 + (col << 4), src + (size_t)(there ? e : 0) * D, there);
+          }
+          if (p.fault_inject != 1 || t > 0 || kv > 0) cp_arrive(bar_full(ring, st));   // (the tests' withheld first stage)
+          advance();
         }
-        if (p.fault_inject != 1 || t > 0) cp_arrive(bar_full(ring, ks));   // (the tests' withheld first stage)
-        cp_arrive(bar_full(ring, st));
-        advance();
+        if (!ok) break;
         named_bar_sync(bar_id, kLoaders);
         step();
       }
@@ -1049,59 +1047,54 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
             ok = wait_bar(bar_st(w, Q_FULL), nq & 1u, abort_flag, status, tmo);
             fence_proxy_async_smem();   // the query tile's cp.async writes
           }
-          auto issue_qk = [&](bool last) {   // S = Q K^T with the keys of stage st
-            const uint64_t kd0 = sw128_kmajor_desc(ring_base + (uint32_t)st * kStage, 0);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t ko = (k & 3) * 2;   // 32 bytes, in 16-byte units
-              mma_bf16(t_s, qd0 + ko + (uint64_t)((k >> 2) * q_rows_bytes >> 4), kd0 + ko + (k >> 2) * (kChunk >> 4),
-                       idesc_qk, k > 0);
-            }
-            tc_commit(bar_st(w, S_FULL));
-            tc_commit(bar_empty(ring, st));
-            if (last) tc_commit(bar_st(w, Q_EMPTY));
-            advance();
-          };
-          if (x.n > 0 && ok) {
-            ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
-            if (!ok) break;
-            if (kWorkerCopies) fence_proxy_async_smem();   // the loaders' cp.async writes, seen through the barrier
-            tc_fence_after();
-            take_turn();
-            issue_qk(x.n == 1);
-            end_turn();
-          }
-          for (int j = 0; j < x.n && ok; ++j) {
-            // everything but P is waited for first
-            ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
-            if (!ok) break;
-            // N-major operand: 64-column chunks kChunk apart, groups of 8 keys 1024 bytes apart
-            const uint64_t vd0 = smem_desc(ring_base + (uint32_t)st * kStage, kChunk, 1024, 2);
-            const uint32_t v_empty = bar_empty(ring, st);
-            advance();
-            bool next = j + 1 < x.n;
-            const bool have_k = next && mbar_try_wait(bar_full(ring, st), ph);
-            if (kWorkerCopies) fence_proxy_async_smem();
-            ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
-            if (!ok) break;
-            tc_fence_after();
-            take_turn();
-#pragma unroll
-            for (int k = 0; k < kAttnKeys / 16; ++k)   // O += P V
-              mma_bf16_ts(t_o, t_s + k * 8, vd0 + k * (2048 >> 4), idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
-            tc_commit(v_empty);
-            ++nt;
-            if (have_k) issue_qk(j + 2 == x.n);
-            else if (!next) tc_commit(bar_st(w, O_FULL));
-            end_turn();
-            if (next && !have_k) {
+          // iteration j: O += P V of tile j - 1, S = Q K^T of tile j
+#pragma unroll 1
+          for (int j = 0; x.n > 0 && j <= x.n; ++j) {
+            const bool next = j < x.n;
+            bool have_k = false;
+            if (j > 0) {
+              // everything but P is waited for first
               ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
               if (!ok) break;
-              if (kWorkerCopies) fence_proxy_async_smem();
+              // N-major operand: 64-column chunks kChunk apart, groups of 8 keys 1024 bytes apart
+              uint64_t vd = smem_desc(ring_base + (uint32_t)st * kStage, kChunk, 1024, 2);
+              const uint32_t v_empty = bar_empty(ring, st);
+              advance();
+              have_k = next && mbar_try_wait(bar_full(ring, st), ph);
+              if (kWorkerCopies) fence_proxy_async_smem();   // the workers' cp.async writes, seen through the barriers
+              // (P of a unit's first tile also says that the softmax warps have read the last unit's O)
+              ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
+              if (!ok) break;
+              ++nt;
+              tc_fence_after();
               take_turn();
-              issue_qk(j + 2 == x.n);
-              end_turn();
+#pragma unroll
+              for (int k = 0; k < kAttnKeys / 16; ++k, vd += 2048 >> 4)
+                mma_bf16_ts(t_o, t_s + k * 8, vd, idesc_pv, (j > 1 || k > 0) ? 1u : 0u);
+              tc_commit(v_empty);
+              if (!next) tc_commit(bar_st(w, O_FULL));
             }
+            if (next) {
+              if (!have_k) {
+                if (j > 0) end_turn();
+                ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
+                if (!ok) break;
+                if (kWorkerCopies) fence_proxy_async_smem();
+                tc_fence_after();
+                take_turn();
+              }
+              uint64_t qd = qd0, kd = sw128_kmajor_desc(ring_base + (uint32_t)st * kStage, 0);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c, qd += q_rows_bytes >> 4, kd += kChunk >> 4) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_bf16(t_s, qd + 2 * k, kd + 2 * k, idesc_qk, c + k > 0);   // 32 bytes a step
+              }
+              tc_commit(bar_st(w, S_FULL));
+              tc_commit(bar_empty(ring, st));
+              if (j + 1 == x.n) tc_commit(bar_st(w, Q_EMPTY));
+              advance();
+            }
+            end_turn();
           }
           if (x.n > 0) ++nq;
           if constexpr (kPair) {   // stages only the other stream needs
@@ -1145,11 +1138,13 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         if (!ok) break;
         if (warp_live) {
           tc_fence_after();
-          // BF16: the row's 128 logits stay in registers.  8-bit caches: the worker warps need the
-          // registers; 32 at a time are read from TMEM, twice (a second read of 64 KB a tile).
-          constexpr int kHeld = Q8 ? 32 : kAttnKeys;
+          // Pages by TMA in BF16: the row's 128 logits stay in registers.  With worker warps beside
+          // them: 32 at a time, read from TMEM twice, for the maximum and for the weights (fewer
+          // registers, a fifth of the code).
+          constexpr int kHeld = R::kWorkWarps > 0 ? 32 : kAttnKeys;
           uint32_t s[kHeld];
           const int lim = vis - (x.lo + j) * kAttnKeys;
+          const uint32_t* const mask = masks + (nt % kMaskRing) * 4;
           auto load_s = [&](int c0) {   // logits c0 .., those of keys not seen replaced by -inf
 #pragma unroll
             for (int c = 0; c < kHeld; c += 32) tmem_ld_x32(t_s + c0 + c, s + c);
@@ -1160,21 +1155,18 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
                 for (int c = 0; c < kHeld; ++c) s[c] = c0 + c < lim ? s[c] : 0xFF800000u;
               }
             } else {
+              const uint32_t mk = mask[c0 >> 5];   // (listed keys: kHeld is 32)
+              if (mk != 0xFFFFFFFFu) {
 #pragma unroll
-              for (int c = 0; c < kHeld; c += 32) {
-                const uint32_t mk = masks[(nt % kMaskRing) * 4 + ((c0 + c) >> 5)];
-                if (mk != 0xFFFFFFFFu) {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) s[c + i] = (mk >> i) & 1u ? s[c + i] : 0xFF800000u;
-                }
+                for (int c = 0; c < kHeld; ++c) s[c] = (mk >> (c & 31)) & 1u ? s[c] : 0xFF800000u;
               }
             }
           };
           float mx[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) mx[c] = -INFINITY;
-#pragma unroll
-          for (int c0 = kAttnKeys - kHeld; c0 >= 0; c0 -= kHeld) {   // (the first ones stay)
+#pragma unroll 1
+          for (int c0 = 0; c0 < kAttnKeys; c0 += kHeld) {
             load_s(c0);
 #pragma unroll
             for (int c = 0; c < kHeld; c += 2)
@@ -1190,34 +1182,34 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
             l *= alpha;
             if (j > 0) {   // the previous tile's PV completed before this S
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
+              for (int d = 0; d < D; d += 16) {
                 uint32_t o[16];
-                tmem_ld_x16(t_o + c, o);
+                tmem_ld_x16(t_o + d, o);
                 tmem_ld_wait_tied<16>(o);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st_x16(t_o + c, o);
+                tmem_st_x16(t_o + d, o);
               }
             }
           }
           const float mref = m == -INFINITY ? 0.f : m;
           const float2 sc2 = make_float2(scale, scale), mm2 = make_float2(-mref, -mref);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
           for (int c0 = 0; c0 < kAttnKeys; c0 += kHeld) {
-            if (c0 > 0) load_s(c0);
+            if (kHeld < kAttnKeys) load_s(c0);
 #pragma unroll
-            for (int c = 0; c < kHeld; c += 16) {
-              uint32_t pk[8];
+            for (int c = 0; c < kHeld; c += 32) {
+              uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < 16; ++i) {
                 float2 e = ffma2(as_f2(s[c + 2 * i], s[c + 2 * i + 1]), sc2, mm2);
                 e.x = ex2(e.x);
                 e.y = ex2(e.y);
                 sum[i & 1] = __fadd2_rn(sum[i & 1], e);
                 pk[i] = pack_bf16(e.x, e.y);
               }
-              tmem_st_x8(t_s + (c0 + c) / 2, pk);   // over logits already read
+              tmem_st_x16(t_s + (c0 + c) / 2, pk);   // over logits already read
             }
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
