@@ -80,8 +80,8 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   *pl = AttnPlan{};
   const bool eight_bit = sw > 0;
   const int group = n_heads / n_kv;
-  // a page's part of a half tile must have scales in whole 16 bytes for the bulk copy
-  pl->gather = topk_width > 0 || (eight_bit && ((page_size < 64 ? page_size : 64) * sw) % 16 != 0);
+  // a page's part of a tile must have scales in whole 16 bytes for the bulk copy
+  pl->gather = topk_width > 0 || (eight_bit && ((page_size < kAttnKeys ? page_size : kAttnKeys) * sw) % 16 != 0);
   pl->tq = topk_width > 0 ? 1 : kAttnRows / group;
   pl->pair = !pl->gather && max_seqlen_q > pl->tq && (int64_t)total_q * group > (int64_t)kAttnRows * num_seqs;
   const int tok = pl->tq < max_seqlen_q ? pl->tq : (max_seqlen_q > 0 ? max_seqlen_q : 1);
@@ -96,10 +96,10 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   pl->max_units = base <= few * streams ? (int)(base + few * streams) : 0;
   const int qrows = pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
   pl->q_bytes = (uint32_t)qrows * D * 2;
-  const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys / 2 * D + (pl->gather ? 0 : 256);
+  const uint32_t stage = kAttnKeys * D * 2, raw = pl->gather ? kAttnKeys / 2 * D : kAttnKeys * D + 512;
   for (pl->streams = 2; pl->streams >= 1; --pl->streams) {
     const uint32_t rings = pl->pair ? 1 : pl->streams;
-    const uint32_t rows = pl->gather ? rings * (eight_bit ? 2 : 1) * kAttnKeys * 4 : 64;   // else: rows of a half tile
+    const uint32_t rows = pl->gather ? rings * (eight_bit ? 2 : 1) * kAttnKeys * 4 : 64;   // else: visible rows of a stored tile
     const uint32_t scale = pl->gather && eight_bit ? rings * 4 * 2 * kAttnKeys * 4 : 0;
     const uint32_t mask = pl->gather ? 2 * 8 * 4 * 4 : 0, bars = 8 * (2 * 32 + 2 * 6) + 32, tab = round16((64 + 1) * 4);
     const uint32_t q = 2 * pl->q_bytes, tail = rows + scale + mask + bars + tab;
@@ -307,8 +307,7 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
   }
   if (!p.plan.gather) {
     const int64_t groups = (int64_t)num_pages * n_kv_heads;
-    const int keys = prec == DSA_PREC_BF16 ? kAttnKeys : kAttnKeys / 2;   // of a tile, or half a tile as stored
-    const int box = page_size < keys ? page_size : keys;
+    const int box = page_size < kAttnKeys ? page_size : kAttnKeys;
     const bool b8 = prec != DSA_PREC_BF16;
     if ((s = make_pages_map(&p.tm_k, k_pages, groups, page_size, head_dim, box, b8)) != DSA_OK) return s;
     if ((s = make_pages_map(&p.tm_v, v_pages, groups, page_size, head_dim, box, b8)) != DSA_OK) return s;

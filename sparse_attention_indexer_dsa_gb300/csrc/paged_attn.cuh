@@ -304,21 +304,21 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&w)[4]) {
 // scales are too short for a bulk copy).
 enum { PAIR = 0, SOLO = 1, GATHER = 2 };
 
-// Warps: 8 softmax; workers (8: they widen 8-bit rows, or copy gathered ones: four copy at half the rate); the
+// Warps: 8 softmax; workers (16 widen 8-bit tiles; 8 copy gathered rows: four do at half the rate); the
 // rest: key loaders (TMA), query loaders, MMA 0 and 1 last.  (The four warps of an SM's sub-partition
 // are those of equal number modulo 4; loaders and MMA warps are kept on different ones.)
 template <bool Q8, int MODE>
 struct Roles {
-  static constexpr int kWorkWarps = Q8 || MODE == GATHER ? 8 : 0;
-  static constexpr int kWarps = kWorkWarps > 0 ? 20 : 16;
+  static constexpr int kWorkWarps = MODE == GATHER ? 8 : (Q8 ? 16 : 0);
+  static constexpr int kWarps = kWorkWarps > 0 ? 12 + kWorkWarps : 16;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kQueryWarp = kWorkWarps > 0 ? kWarps - 4 : 10;         // and the next one
   static constexpr int kKeyWarp = kWorkWarps > 0 ? kWarps - 4 : 8;            // TMA: and the next one
   // registers: shares of what the launch holds (threads x the launch's count, a multiple of 8)
-  static constexpr int kLaunchRegs = kWorkWarps > 0 ? 96 : 128;
+  static constexpr int kLaunchRegs = kWorkWarps == 16 ? 72 : (kWorkWarps == 8 ? 96 : 128);
   static constexpr int kSoftmaxRegs = kWorkWarps > 0 ? 112 : 192;
-  static constexpr int kWorkRegs = 80;
-  static constexpr int kAuxRegs = kWorkWarps > 0 ? 96 : 64;
+  static constexpr int kWorkRegs = kWorkWarps == 16 ? 56 : 80;
+  static constexpr int kAuxRegs = kWorkWarps == 16 ? 56 : (kWorkWarps == 8 ? 96 : 64);
   static_assert(2 * kSoftmaxRegs + kWorkWarps / 4 * kWorkRegs + (kWarps - 8 - kWorkWarps) / 4 * kAuxRegs <=
                     kWarps / 4 * kLaunchRegs, "shares");
 };
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
   constexpr int kRings = kPair ? 1 : 2;
   constexpr int kLoaders = R::kWorkWarps > 0 ? 32 * R::kWorkWarps / kRings : 32;   // worker threads per ring
   constexpr int kRowsPer = kLoaders < kAttnKeys ? kAttnKeys / kLoaders : 1;   // rows a worker resolves per tile
-  constexpr uint32_t kRawItem = kAttnKeys / 2 * D + (MODE == GATHER ? 0 : 256);   // half a tile as stored (+ scales)
+  constexpr uint32_t kRawItem = MODE == GATHER ? kAttnKeys / 2 * D : kAttnKeys * D + 512;   // (half) a tile as stored (+ scales)
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnPlan& pl = p.plan;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
   const uint64_t tmo = p.timeout_ns;
   const bool listed = MODE == GATHER && p.topk_idx != nullptr;
 
-  // barriers: per ring full/empty (BF16 tiles) and raw full/empty (stored 8-bit half tiles); per stream
+  // barriers: per ring full/empty (BF16 tiles) and raw full/empty (stored 8-bit tiles); per stream
   // q_full, q_empty, s_full, p_full, o_full, drain
   const uint32_t bars = sbase + pl.off_bars;
   int* const ctl = reinterpret_cast<int*>(smem + pl.off_bars + 8 * (2 * 32 + 2 * 6));   // status, abort, tmem base, chunk, turn
@@ -553,38 +553,47 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       }
     };
     if constexpr (MODE != GATHER) {
-      // Stored half tiles (keys 0-63, 64-127, values 0-63, 64-127 of a tile) to BF16 stages.
+      // Stored tiles (keys, values, keys, ...) to BF16 stages.
       constexpr int PPR = D / 16;                  // 16-code pieces per row
       constexpr int RPP = kLoaders / PPR;
+      constexpr int kPasses = kAttnKeys / RPP;
       const int c = lt % PPR, rsub = lt / PPR;
-      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem;
+      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem + rsub * D + c * 16;
       const int* const meta = reinterpret_cast<const int*>(smem + pl.off_rows) + ring * 8;
-      const uint32_t dcol = (uint32_t)(c >> 2) * kChunk;
-      const int c0 = (c & 3) * 2;                  // first of the two 16-byte pieces in its 128-byte span
-      const int sw = p.c.sw, blk = sw == 1 ? 0 : c >> 1;
+      const uint32_t dcol = (uint32_t)(c >> 2) * kChunk + rsub * 128;
+      // the two 16-byte pieces in their 128-byte span (a pass is a multiple of 8 rows)
+      static_assert(!Q8 || RPP % 8 == 0, "swizzle");
+      const uint32_t at0 = dcol + ((uint32_t)(((c & 3) * 2) ^ (rsub & 7)) << 4), at1 = at0 ^ 16u;
+      const int sw = p.c.sw, s0 = rsub * sw + (sw == 1 ? 0 : c >> 1);
       int slot = 0;
       uint32_t rph = 0;
       for (int u = first_unit(ring); u < n_units && ok; u += n_streams) {
         const int n = decode_unit<kPair>(p, tab, gsz, chunk, u, kPair ? 0 : ring).n_shared;
-        for (int it = 0; it < 4 * n && ok; ++it) {
-          if (!(it & 1) && wrapped) ok = wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo);
-          ok = __all_sync(0xffffffffu, ok && wait_bar(bar_raw_full(ring, slot), rph, abort_flag, status, tmo));
+        for (int it = 0; it < 2 * n; ++it) {
+          ok = __all_sync(0xffffffffu, wait_bar(bar_raw_full(ring, slot), rph, abort_flag, status, tmo) &&
+                                           (!wrapped || wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo)));
           if (!ok) break;
           const uint32_t raw = raw_base + (uint32_t)slot * kRawItem;
-          const uint8_t* scales = smem + (raw - sbase) + kAttnKeys / 2 * D;
-          const int valid = meta[slot];
-          const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
-#pragma unroll 2
-          for (int r = rsub; r < kAttnKeys / 2; r += RPP) {
-            uint32_t w4[4], o[8];
-            ld_shared_v4(raw + r * D + c * 16, w4);
-            const uint32_t e8 = scales[r * sw + blk];
-            if (r >= valid) w4[0] = w4[1] = w4[2] = w4[3] = 0;   // nothing of the page's other slots
-            widen16(w4, r < valid ? e8 : 0, o);
-            const int row = (it & 1) * (kAttnKeys / 2) + r;
-            const uint32_t rowd = dst + row * 128;
-            st_shared_v4(rowd + ((uint32_t)(c0 ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-            st_shared_v4(rowd + ((uint32_t)((c0 + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+          const uint8_t* scales = smem + pl.off_raw + (size_t)(ring * pl.nraw + slot) * kRawItem + kAttnKeys * D + s0;
+          const int valid = meta[slot] - rsub;
+          const uint32_t dst = ring_base + (uint32_t)st * kStage;
+          uint32_t w4[kPasses][4], e8[kPasses];
+#pragma unroll
+          for (int i = 0; i < kPasses; ++i) {
+            ld_shared_v4(raw + i * RPP * D, w4[i]);
+            e8[i] = scales[i * RPP * sw];
+          }
+#pragma unroll
+          for (int i = 0; i < kPasses; ++i) {
+            uint32_t o[8];
+            if (i * RPP >= valid) {   // nothing of the page's other slots
+              e8[i] = 0;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) w4[i][q] = 0;
+            }
+            widen16(w4[i], e8[i], o);
+            st_shared_v4(dst + at0 + i * RPP * 128, o[0], o[1], o[2], o[3]);
+            st_shared_v4(dst + at1 + i * RPP * 128, o[4], o[5], o[6], o[7]);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_raw_empty(ring, slot));
@@ -592,11 +601,9 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
             slot = 0;
             rph ^= 1u;
           }
-          if (it & 1) {
-            fence_proxy_async_smem();
-            mbar_arrive(bar_full(ring, st));
-            advance();
-          }
+          fence_proxy_async_smem();
+          mbar_arrive(bar_full(ring, st));
+          advance();
         }
       }
     } else {
@@ -913,15 +920,14 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       }
       if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
     };
-    // Every visible key of an 8-bit cache, as stored: half tiles of codes (a TMA box per page) and their
-    // scales (a bulk copy per page); the workers learn how many rows of a half tile are visible.  The
+    // Every visible key of an 8-bit cache, as stored: tiles of codes (a TMA box per page) and their
+    // scales (a bulk copy per page); the workers learn how many rows of a tile are visible.  The
     // stream's query tile is loaded on the way.
     auto load_raw = [&](int ring) {
-      constexpr int kHalf = kAttnKeys / 2;
       const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem;
       int* const meta = reinterpret_cast<int*>(smem + pl.off_rows) + ring * 8;
       const int shift = p.c.page_shift, sw = p.c.sw;
-      const int box = min(kHalf, 1 << shift), boxes = kHalf / box;
+      const int box = min(kAttnKeys, 1 << shift), boxes = kAttnKeys / box;
       int slot = 0;
       uint32_t rph = 0, nq = 0;
       bool wrapped = false, bad_page = false;
@@ -932,37 +938,35 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         auto page_of = [&](int key) {
           return key < last ? __ldg(table + (key >> shift)) : -1;   // (doc_info: within max_pages)
         };
-        int page = x.n_shared > 0 && lane < 2 * boxes ? page_of(x.lo * kAttnKeys + lane * box) : 0;
+        int page = x.n_shared > 0 && lane < boxes ? page_of(x.lo * kAttnKeys + lane * box) : 0;
         for (int j = 0; j < x.n_shared; ++j) {
           const int key0 = (x.lo + j) * kAttnKeys;
           const int now = page;
-          if (j + 1 < x.n_shared && lane < 2 * boxes) page = page_of(key0 + kAttnKeys + lane * box);
+          if (j + 1 < x.n_shared && lane < boxes) page = page_of(key0 + kAttnKeys + lane * box);
           const bool good = (unsigned)now < (unsigned)p.c.num_pages;
-          if (lane < 2 * boxes && key0 + lane * box < last && !good) bad_page = true;
-          const uint32_t have = __ballot_sync(0xffffffffu, lane < 2 * boxes && good);
+          if (lane < boxes && key0 + lane * box < last && !good) bad_page = true;
+          const uint32_t have = __ballot_sync(0xffffffffu, lane < boxes && good);
 #pragma unroll 1
-          for (int it = 0; it < 4; ++it) {
+          for (int kv = 0; kv < 2; ++kv) {
             if (wrapped &&
                 !__all_sync(0xffffffffu, wait_bar(bar_raw_empty(ring, slot), rph ^ 1u, abort_flag, status, tmo))) {
               cp_wait<0>();
               return;
             }
             const uint32_t bar = bar_raw_full(ring, slot), dst = raw_base + (uint32_t)slot * kRawItem;
-            const int k0 = key0 + (it & 1) * kHalf, b0 = (it & 1) * boxes;
-            const uint32_t mine = (have >> b0) & ((1u << boxes) - 1u);
-            const bool withheld = p.fault_inject == 1 && u == first_unit(ring) && j == 0 && it == 0;   // (tests)
+            const bool withheld = p.fault_inject == 1 && u == first_unit(ring) && j == 0 && kv == 0;   // (tests)
             if (lane == 0 && !withheld) {
-              meta[slot] = min(kHalf, max(0, last - k0));
-              mbar_arrive_expect_tx(bar, __popc(mine) * (uint32_t)(box * (D + sw)));
+              meta[slot] = min(kAttnKeys, last - key0);
+              mbar_arrive_expect_tx(bar, __popc(have) * (uint32_t)(box * (D + sw)));
             }
-            const uint8_t* sc = it >> 1 ? p.c.v_scale : p.c.k_scale;
+            const uint8_t* sc = kv ? p.c.v_scale : p.c.k_scale;
 #pragma unroll 1
-            for (int i = 0; i < boxes; ++i) {
-              const int pg = __shfl_sync(0xffffffffu, now, b0 + i);
-              if (lane == 0 && !withheld && ((mine >> i) & 1u)) {
-                const int in_page = (k0 + i * box) & ((1 << shift) - 1), z = pg * p.c.n_kv + x.h;
-                tma_load_3d(dst + i * box * D, it >> 1 ? &p.tm_v : &p.tm_k, bar, 0, in_page, z);
-                bulk_load(dst + kHalf * D + i * box * sw, sc + ((((int64_t)z << shift) + in_page) * sw), box * sw, bar);
+            for (int i = 0; i < boxes; ++i) {   // (one lane and uniform coordinates: a lane to a box issues slower)
+              const int pg = __shfl_sync(0xffffffffu, now, i);
+              if (lane == 0 && !withheld && ((have >> i) & 1u)) {
+                const int in_page = (key0 + i * box) & ((1 << shift) - 1), z = pg * p.c.n_kv + x.h;
+                tma_load_3d(dst + i * box * D, kv ? &p.tm_v : &p.tm_k, bar, 0, in_page, z);
+                bulk_load(dst + kAttnKeys * D + i * box * sw, sc + ((((int64_t)z << shift) + in_page) * sw), box * sw, bar);
               }
             }
             if (++slot == pl.nraw) {
