@@ -512,11 +512,15 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
   auto first_unit = [&](int w) {
     return kPair ? (int)blockIdx.x : (w < pl.streams ? w * (int)gridDim.x + (int)blockIdx.x : n_units);
   };
+  // Independent streams with at most 64 live rows: the second stream's rows are TMEM lanes (and so
+  // warps and sub-partitions of the SM) that the first one's do not use.
+  const int q_rows = (int)(pl.q_bytes / (D * 2));
+  auto first_row = [&](int w) { return !kPair && w == 1 && q_rows <= kAttnRows / 2 ? q_rows : 0; };
   // The query tile of a unit, by one warp (zeros behind its last row).
   auto load_q = [&](const Unit& x, int w) {
     constexpr int PPR = D / 8;
     constexpr int RPP = 32 / PPR;
-    const int rows = (int)(pl.q_bytes / (D * 2));
+    const int rows = q_rows;
     const int c = lane % PPR, rsub = lane / PPR;
     const uint32_t qb = sbase + (uint32_t)w * pl.q_bytes + (uint32_t)(c >> 3) * (uint32_t)(rows * 128);
     const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + c * 8;
@@ -639,9 +643,8 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           bad_page = true;
       }
     };
-    auto step = [&] {
-      // rows (and scales) of the tile furthest on become readable
-      Last out;
+    Last out;       // rows (and scales) of the tile furthest on, next to become readable
+    auto prepare = [&] {
       if constexpr (Q8) {
         out = s3;
         s3.live = s2.live;
@@ -670,22 +673,6 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
             }
           }
         }
-      }
-      if (out.live) {
-        if (resolver) {
-#pragma unroll
-          for (int i = 0; i < kRowsPer; ++i) {
-            const int r = row_of(i);
-            rowtab[(pubs % kRowBufs) * kAttnKeys + r] = out.row[i];
-            if constexpr (Q8) {
-              sctab[((pubs & 3) * 2) * kAttnKeys + r] = out.sck[i];
-              sctab[((pubs & 3) * 2 + 1) * kAttnKeys + r] = out.scv[i];
-            }
-            const uint32_t seen = __ballot_sync(0xffffffffu, out.row[i] != ~0u);
-            if (lane == 0) masks[(pubs % kMaskRing) * 4 + (r >> 5)] = seen;
-          }
-        }
-        ++pubs;
       }
       // listed positions have arrived: request the pages
       s2 = s1;
@@ -720,6 +707,28 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
             s1.v[i] = j < fx.n_list ? __ldg(p.topk_idx + (int64_t)(fx.q0 + fx.i0) * p.topk_width + j) : -1;
         }
       }
+    };
+    auto publish = [&] {
+      if (out.live) {
+        if (resolver) {
+#pragma unroll
+          for (int i = 0; i < kRowsPer; ++i) {
+            const int r = row_of(i);
+            rowtab[(pubs % kRowBufs) * kAttnKeys + r] = out.row[i];
+            if constexpr (Q8) {
+              sctab[((pubs & 3) * 2) * kAttnKeys + r] = out.sck[i];
+              sctab[((pubs & 3) * 2 + 1) * kAttnKeys + r] = out.scv[i];
+            }
+            const uint32_t seen = __ballot_sync(0xffffffffu, out.row[i] != ~0u);
+            if (lane == 0) masks[(pubs % kMaskRing) * 4 + (r >> 5)] = seen;
+          }
+        }
+        ++pubs;
+      }
+    };
+    auto step = [&] {
+      prepare();
+      publish();
     };
 
     // A free stage, for all of the ring's workers (the vote makes them give up together).
@@ -758,10 +767,11 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           }
           if (p.fault_inject != 1 || t > 0 || kv > 0) cp_arrive(bar_full(ring, st));   // (the tests' withheld first stage)
           advance();
+          if (kv == 0) prepare();                  // (the next tile's rows, while the values' stage may still be in use)
         }
         if (!ok) break;
         named_bar_sync(bar_id, kLoaders);
-        step();
+        publish();
       }
     } else {
       constexpr int PPR = D / 16;                  // 16-code pieces per row
@@ -1035,7 +1045,9 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           }
         };
         auto end_turn = [&] { atomicExch_block(turn, 0); };
-        const uint64_t qd0 = sw128_kmajor_desc(sbase + (uint32_t)w * pl.q_bytes, 0);
+        // (the 128 rows that the products read begin before the tile when its rows are not the first:
+        // with 32 or 64 rows a tile, still inside the first stream's)
+        const uint64_t qd0 = sw128_kmajor_desc(sbase + (uint32_t)w * pl.q_bytes - first_row(w) * 128, 0);
         int st = 0;
         uint32_t ph = 0, nq = 0, nt = 0;
         bool ok = true;
@@ -1070,6 +1082,10 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
               ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
               if (!ok) break;
               ++nt;
+              if (next && !have_k) {   // once more: the next QK without giving up the turn
+                have_k = mbar_try_wait(bar_full(ring, st), ph);
+                if (kWorkerCopies && have_k) fence_proxy_async_smem();
+              }
               tc_fence_after();
               take_turn();
 #pragma unroll
@@ -1122,7 +1138,8 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmaxRegs));
     const int w = wg;
     const int quarter = warp & 3;
-    const int r = quarter * 32 + lane;
+    const int r0 = quarter * 32 - first_row(w);   // this warp's first row of the tile (below 0: none)
+    const int r = r0 + lane;
     const uint32_t lane_off = (uint32_t)quarter << 21;    // TMEM lane 32 * quarter
     const uint32_t t_s = tmem + (uint32_t)w * 128 + lane_off, t_o = tmem + 256 + (uint32_t)w * 128 + lane_off;
     const uint32_t* const masks = reinterpret_cast<const uint32_t*>(smem + pl.off_mask) + w * kMaskRing * 4;
@@ -1133,9 +1150,9 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     if (first_unit(w) < n_units) x = decode_unit<kPair>(p, tab, gsz, chunk, first_unit(w), w);
     for (int u = first_unit(w); u < n_units && ok; u += n_streams, x = nx) {
       const int live = (x.i1 - x.i0) * p.group;
-      const bool warp_live = quarter * 32 < live;
+      const bool warp_live = r0 >= 0 && r0 < live;
       const int tok = r / p.group, g = r - tok * p.group;
-      const int vis = r < live ? x.P0 + x.i0 + tok + 1 : 0x7FFFFFFF;   // visible keys of this row
+      const int vis = r0 >= 0 && r < live ? x.P0 + x.i0 + tok + 1 : 0x7FFFFFFF;   // visible keys of this row
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < x.n; ++j, ++nt) {
         ok = __all_sync(0xffffffffu, wait_bar(bar_st(w, S_FULL), nt & 1u, abort_flag, status, tmo));
@@ -1225,7 +1242,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       }
       if (!ok) break;
       if (u + n_streams < n_units) nx = decode_unit<kPair>(p, tab, gsz, chunk, u + n_streams, w);   // (while O is formed)
-      const bool mine = r < live;
+      const bool mine = r0 >= 0 && r < live;
       const int64_t orow = (int64_t)(x.q0 + x.i0 + tok) * p.n_heads + x.h * p.group + g;
       const int64_t prow = (int64_t)(kPair ? 2 * u + w : u) * pl.rows_cap + r;
       if (x.n > 0) {
