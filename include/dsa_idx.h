@@ -347,7 +347,7 @@ dsa_status_t dsa_idx_score_topk_noalloc_status(dsa_stream_t stream, dsa_status_t
  *
  *   pages        device [num_pages, n_kv_heads, page_size, head_dim]: bf16
  *                (BF16) or e4m3 codes (MXFP8, FP8); page_size a power of two
- *                in [8, 1024], head_dim 64 or 128, fewer than 2^32 rows in all
+ *                in [8, 1024], head_dim 64 or 128, fewer than 2^31 rows in all
  *   page scales  device u8 [num_pages, n_kv_heads, page_size, head_dim/32]
  *                (MXFP8) or [num_pages, n_kv_heads, page_size] (FP8), else NULL
  *   page_table   device int32 [num_seqs, max_pages]: position p of sequence d

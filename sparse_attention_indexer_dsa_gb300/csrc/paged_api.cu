@@ -24,8 +24,8 @@ dsa_status_t check_cache(PagedCacheView* c, const void* k_pages, const uint8_t* 
   if (num_pages < 1 || n_kv_heads < 1 || max_pages < 1 || num_seqs < 1) return fail(DSA_ERR_INVALID_ARG, "sizes");
   if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
     return fail(DSA_ERR_UNSUPPORTED, "page_size must be a power of two in [8, 1024]");
-  if ((int64_t)num_pages * n_kv_heads >= (int64_t)0xFFFFFFFF / page_size)
-    return fail(DSA_ERR_UNSUPPORTED, "a cache holds fewer than 2^32 rows");
+  if ((int64_t)num_pages * n_kv_heads >= ((int64_t)1 << 31) / page_size)
+    return fail(DSA_ERR_UNSUPPORTED, "a cache holds fewer than 2^31 rows");
   if (!aligned16(k_pages) || !aligned16(v_pages)) return fail(DSA_ERR_INVALID_ARG, "pages must be 16-byte aligned");
   if (prec != DSA_PREC_BF16) {
     if (!k_page_scale || (v_pages && !v_page_scale)) return fail(DSA_ERR_INVALID_ARG, "8-bit caches need their scales");
@@ -96,13 +96,12 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   pl->max_units = base <= few * streams ? (int)(base + few * streams) : 0;
   const int qrows = pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
   pl->q_bytes = (uint32_t)qrows * D * 2;
-  const uint32_t stage = kAttnKeys * D * 2, raw = pl->gather ? kAttnKeys / 2 * D : kAttnKeys * D + 512;
+  const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys * D + 512;
   for (pl->streams = 2; pl->streams >= 1; --pl->streams) {
     const uint32_t rings = pl->pair ? 1 : pl->streams;
-    const uint32_t rows = pl->gather ? rings * (eight_bit ? 2 : 1) * kAttnKeys * 4 : 64;   // else: visible rows of a stored tile
-    const uint32_t scale = pl->gather && eight_bit ? rings * 4 * 2 * kAttnKeys * 4 : 0;
+    const uint32_t rows = 64;   // visible rows of a stored tile
     const uint32_t mask = pl->gather ? 2 * 8 * 4 * 4 : 0, bars = 8 * (2 * 32 + 2 * 6) + 32, tab = round16((64 + 1) * 4);
-    const uint32_t q = 2 * pl->q_bytes, tail = rows + scale + mask + bars + tab;
+    const uint32_t q = 2 * pl->q_bytes, tail = rows + mask + bars + tab;
     if (q + tail > kAttnSmemMax) continue;
     const uint32_t avail = kAttnSmemMax - q - tail;
     if (eight_bit) {
@@ -119,8 +118,7 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
     pl->off_ring = q;
     pl->off_raw = pl->off_ring + rings * pl->nst * stage;
     pl->off_rows = pl->off_raw + rings * pl->nraw * raw;
-    pl->off_scale = pl->off_rows + rows;
-    pl->off_mask = pl->off_scale + scale;
+    pl->off_mask = pl->off_rows + rows;
     pl->off_bars = pl->off_mask + mask;
     pl->off_tab = pl->off_bars + bars;
     pl->smem = pl->off_tab + tab;
@@ -305,7 +303,12 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
     w += round256(slots * 8);
     p.part_o = reinterpret_cast<float*>(w);
   }
-  if (!p.plan.gather) {
+  if (p.plan.gather) {
+    const int64_t rows = (int64_t)num_pages * n_kv_heads * page_size;
+    const bool b8 = prec != DSA_PREC_BF16;
+    if ((s = make_pages_map(&p.tm_k, k_pages, 0, rows, head_dim, 1, b8)) != DSA_OK) return s;
+    if ((s = make_pages_map(&p.tm_v, v_pages, 0, rows, head_dim, 1, b8)) != DSA_OK) return s;
+  } else {
     const int64_t groups = (int64_t)num_pages * n_kv_heads;
     const int box = page_size < kAttnKeys ? page_size : kAttnKeys;
     const bool b8 = prec != DSA_PREC_BF16;

@@ -24,15 +24,13 @@
 //         key/value stages (long chunks: the keys are read half as often);
 //   else: the streams are independent, each with its own units and ring
 //         (single tokens, short chunks, selected rows).
-// Loaders.  All visible keys of a BF16 cache come by TMA, a box per page, from
-// one warp.  Listed rows and 8-bit caches: loader warps resolve listed position
-// -> page -> row a step per tile, three tiles ahead (one row per thread), so its
-// dependent loads are off the path, and copy the rows with cp.async into the
-// 128-byte swizzled layout the MMA reads.  Rows that are not there are
-// zero-filled, so nothing outside a sequence's own rows enters a product.  8-bit
-// rows are fetched as stored (cp.async into a thread-private ring) and widened to
-// BF16 on the way into the stage; E4M3 x 2^e is exact in BF16.  One more warp per
-// stream loads its query tiles.
+// Loaders.  TMA brings everything: all visible keys as a box per page, listed
+// keys four rows at a time, into the 128-byte swizzled layout the MMA reads.
+// Listed position -> page -> row is resolved a step per tile, ahead of the
+// copies, so its dependent loads are off the path.  Rows that are not there are
+// zero-filled, so nothing outside a sequence's own rows enters a product.  Tiles
+// of 8-bit caches are fetched as stored and widened to BF16 by worker warps on
+// the way into a stage; E4M3 x 2^e is exact in BF16.
 //
 // Units.  (sequence, key head, query tile, range of key tiles).  Every block
 // derives the same list from the prefixes: the number of key tiles per range is
@@ -43,6 +41,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "dsa_device.cuh"
 #include "paged_params.h"
@@ -76,6 +75,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Four rows of a two-dimensional map (its box one row high).
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y0, int y1, int y2,
+                                            int y3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
       : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -304,21 +312,21 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&w)[4]) {
 // scales are too short for a bulk copy).
 enum { PAIR = 0, SOLO = 1, GATHER = 2 };
 
-// Warps: 8 softmax; workers (16 widen 8-bit tiles; 8 copy gathered rows: four do at half the rate); the
+// Warps: 8 softmax; workers (16 widen 8-bit tiles; 8 bring gathered BF16 rows); the
 // rest: key loaders (TMA), query loaders, MMA 0 and 1 last.  (The four warps of an SM's sub-partition
 // are those of equal number modulo 4; loaders and MMA warps are kept on different ones.)
 template <bool Q8, int MODE>
 struct Roles {
-  static constexpr int kWorkWarps = MODE == GATHER ? 8 : (Q8 ? 16 : 0);
+  static constexpr int kWorkWarps = Q8 ? 16 : (MODE == GATHER ? 8 : 0);
   static constexpr int kWarps = kWorkWarps > 0 ? 12 + kWorkWarps : 16;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kQueryWarp = kWorkWarps > 0 ? kWarps - 4 : 10;         // and the next one
   static constexpr int kKeyWarp = kWorkWarps > 0 ? kWarps - 4 : 8;            // TMA: and the next one
   // registers: shares of what the launch holds (threads x the launch's count, a multiple of 8)
   static constexpr int kLaunchRegs = kWorkWarps == 16 ? 72 : (kWorkWarps == 8 ? 96 : 128);
-  static constexpr int kSoftmaxRegs = kWorkWarps > 0 ? 112 : 192;
+  static constexpr int kSoftmaxRegs = kWorkWarps == 16 ? 104 : (kWorkWarps == 8 ? 112 : 192);
   static constexpr int kWorkRegs = kWorkWarps == 16 ? 56 : 80;
-  static constexpr int kAuxRegs = kWorkWarps == 16 ? 56 : (kWorkWarps == 8 ? 96 : 64);
+  static constexpr int kAuxRegs = kWorkWarps == 16 ? 72 : (kWorkWarps == 8 ? 96 : 64);
   static_assert(2 * kSoftmaxRegs + kWorkWarps / 4 * kWorkRegs + (kWarps - 8 - kWorkWarps) / 4 * kAuxRegs <=
                     kWarps / 4 * kLaunchRegs, "shares");
 };
@@ -327,13 +335,11 @@ template <int D, bool Q8, int MODE>
 __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_kernel(const __grid_constant__ AttnParams p) {
   using R = Roles<Q8, MODE>;
   constexpr bool kPair = MODE == PAIR;
-  constexpr bool kWorkerCopies = MODE == GATHER && !Q8;   // stages written by cp.async: fenced by the MMA warp
   constexpr uint32_t kStage = kAttnKeys * D * 2;     // one tile of keys or values
   constexpr uint32_t kChunk = kAttnKeys * 128;       // 64 of its columns
   constexpr int kRings = kPair ? 1 : 2;
   constexpr int kLoaders = R::kWorkWarps > 0 ? 32 * R::kWorkWarps / kRings : 32;   // worker threads per ring
-  constexpr int kRowsPer = kLoaders < kAttnKeys ? kAttnKeys / kLoaders : 1;   // rows a worker resolves per tile
-  constexpr uint32_t kRawItem = MODE == GATHER ? kAttnKeys / 2 * D : kAttnKeys * D + 512;   // (half) a tile as stored (+ scales)
+  constexpr uint32_t kRawItem = kAttnKeys * D + 512;   // a tile as stored, with its scales
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnPlan& pl = p.plan;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     ctl[4] = 0;
     for (int r = 0; r < kRings; ++r) {
       for (int s = 0; s < pl.nst; ++s) {
-        mbar_init(bar_full(r, s), R::kWorkWarps > 0 ? kLoaders : 1);
+        mbar_init(bar_full(r, s), Q8 ? kLoaders : (MODE == GATHER ? kLoaders / 32 : 1));
         mbar_init(bar_empty(r, s), kPair ? 2 : 1);
       }
       for (int s = 0; s < pl.nraw; ++s) {
@@ -538,12 +544,119 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     cp_arrive(bar_st(w, Q_FULL));
   };
 
+  // Listed keys (or, without a list, all of them) as cache rows, tile by tile, for one warp: position ->
+  // page -> row, a step per tile, so that the dependent loads of a tile are spread over the tiles before
+  // it.  kRowsPer rows a lane from row row0 of the tile on; use(rows) returns false to give up.
+  const int no_row = (p.c.num_pages * p.c.n_kv) << p.c.page_shift;   // behind the last row: TMA fills zeros
+  auto gather = [&](int ring, int row0, auto rows_per, auto use) {
+    constexpr int kRowsPer = decltype(rows_per)::value;
+    int fu = first_unit(ring), fj = -1;
+    Unit fx{};
+    struct Step {
+      bool live = false;          // holds a tile
+      int d = 0, h = 0, lim = 0;  // its sequence, key head, keys visible to the unit
+      int u = -1;                 // its unit, where it is the first tile (else -1)
+      int v[kRowsPer];            // listed position, then page
+      int pos[kRowsPer];
+    } s1, s2;
+    struct Last {
+      bool live = false;
+      int u = -1;
+      uint32_t row[kRowsPer], sck[kRowsPer], scv[kRowsPer];
+    } s3;
+    bool bad_page = false;
+    auto row_of = [&](int i) { return row0 + i * 32 + lane; };
+    auto row_from = [&](const Step& s, int i, uint32_t* row) {
+      *row = ~0u;
+      if (s.pos[i] >= 0) {
+        if ((unsigned)s.v[i] < (unsigned)p.c.num_pages)
+          *row = (uint32_t)((((int64_t)s.v[i] * p.c.n_kv + s.h) << p.c.page_shift) +
+                            (s.pos[i] & ((1 << p.c.page_shift) - 1)));
+        else
+          bad_page = true;
+      }
+    };
+    Last out;       // rows (and scales) of the tile furthest on, next to become readable
+    auto prepare = [&] {
+      if constexpr (Q8) {
+        out = s3;
+        s3.live = s2.live;
+        s3.u = s2.u;
+      } else {
+        out.live = s2.live;
+        out.u = s2.u;
+      }
+      if (s2.live) {
+        Last& l = Q8 ? s3 : out;
+#pragma unroll
+        for (int i = 0; i < kRowsPer; ++i) {
+          row_from(s2, i, &l.row[i]);
+          if constexpr (Q8) {
+            l.sck[i] = l.scv[i] = 0;
+            const uint32_t cr = l.row[i];
+            if (cr != ~0u) {
+              if (p.c.sw == 1) {
+                l.sck[i] = __ldg(p.c.k_scale + cr);
+                l.scv[i] = __ldg(p.c.v_scale + cr);
+              } else if constexpr (D == 128) {
+                l.sck[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_scale) + cr);
+                l.scv[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_scale) + cr);
+              } else {
+                l.sck[i] = __ldg(reinterpret_cast<const uint16_t*>(p.c.k_scale) + cr);
+                l.scv[i] = __ldg(reinterpret_cast<const uint16_t*>(p.c.v_scale) + cr);
+              }
+            }
+          }
+        }
+      }
+      // listed positions have arrived: request the pages
+      s2 = s1;
+      if (s2.live) {
+#pragma unroll
+        for (int i = 0; i < kRowsPer; ++i) {
+          const int pos = s1.v[i];
+          s2.pos[i] = pos >= 0 && pos < s2.lim ? pos : -1;
+          const int pi = pos >> p.c.page_shift;
+          s2.v[i] = s2.pos[i] >= 0 && pi < p.c.max_pages ? __ldg(p.c.table + (int64_t)s2.d * p.c.max_pages + pi) : -1;
+        }
+      }
+      // the next tile enters: request its listed positions
+      if (fu < n_units && ++fj >= fx.n_shared) {
+        fj = 0;
+        if (fx.n_shared > 0) fu += n_streams;   // (0: nothing decoded yet)
+        for (; fu < n_units; fu += n_streams) {
+          fx = decode_unit<false>(p, tab, gsz, chunk, fu, ring);
+          if (fx.n_shared > 0) break;
+        }
+      }
+      s1.live = fu < n_units;
+      if (s1.live) {
+        s1.d = fx.d;
+        s1.u = fj == 0 ? fu : -1;
+        s1.h = fx.h;
+        s1.lim = fx.P0 + (p.topk_idx ? fx.i0 + 1 : fx.last);   // keys behind the last visible one are never read
+#pragma unroll
+        for (int i = 0; i < kRowsPer; ++i) {
+          const int j = (fx.lo + fj) * kAttnKeys + row_of(i);
+          s1.v[i] = j;
+          if (p.topk_idx)
+            s1.v[i] = j < fx.n_list ? __ldg(p.topk_idx + (int64_t)(fx.q0 + fx.i0) * p.topk_width + j) : -1;
+        }
+      }
+    };
+    prepare();
+    prepare();
+    prepare();
+    if constexpr (Q8) prepare();
+    while (out.live && use(out)) prepare();
+    if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
+  };
+
   if (R::kWorkWarps > 0 && wg >= 2 && wg < 2 + R::kWorkWarps / 4) {
     // ======================= workers =======================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kWorkRegs));
     const int ring = kPair ? 0 : (tid - 256) / kLoaders;
     const int lt = (tid - 256) % kLoaders;           // thread of this ring
-    const int bar_id = 1 + ring;
     const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
     bool ok = true;
     int st = 0;
@@ -556,7 +669,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         wrapped = true;
       }
     };
-    if constexpr (MODE != GATHER) {
+    if constexpr (Q8) {
       // Stored tiles (keys, values, keys, ...) to BF16 stages.
       constexpr int PPR = D / 16;                  // 16-code pieces per row
       constexpr int RPP = kLoaders / PPR;
@@ -611,245 +724,35 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         }
       }
     } else {
-    constexpr int kRowBufs = Q8 ? 2 : 1;   // (BF16: the next tile's rows wait for a second barrier)
-    uint32_t* const rowtab = reinterpret_cast<uint32_t*>(smem + pl.off_rows) + ring * kRowBufs * kAttnKeys;
-    uint32_t* const sctab = reinterpret_cast<uint32_t*>(smem + pl.off_scale) + ring * 4 * 2 * kAttnKeys;
-    uint32_t* const masks = reinterpret_cast<uint32_t*>(smem + pl.off_mask) + ring * kMaskRing * 4;
-    bool bad_page = false;
-
-    // ---- position -> page -> row, a step per tile; `fu`, `fj`, `fx`: the tile that enters ----
-    int fu = first_unit(ring), fj = -1;
-    Unit fx{};
-    struct Step {
-      bool live = false;          // holds a tile
-      int d = 0, h = 0, lim = 0;  // its sequence, key head, keys visible to the unit
-      int v[kRowsPer];            // listed position, then page
-      int pos[kRowsPer];
-    } s1, s2;
-    struct Last {
-      bool live = false;
-      uint32_t row[kRowsPer], sck[kRowsPer], scv[kRowsPer];
-    } s3;
-    int pubs = 0;   // tiles whose rows are in rowtab
-    const bool resolver = lt * kRowsPer < kAttnKeys;
-    auto row_of = [&](int i) { return (lt >> 5) * (32 * kRowsPer) + i * 32 + lane; };
-    auto row_from = [&](const Step& s, int i, uint32_t* row) {
-      *row = ~0u;
-      if (s.pos[i] >= 0) {
-        if ((unsigned)s.v[i] < (unsigned)p.c.num_pages)
-          *row = (uint32_t)((((int64_t)s.v[i] * p.c.n_kv + s.h) << p.c.page_shift) +
-                            (s.pos[i] & ((1 << p.c.page_shift) - 1)));
-        else
-          bad_page = true;
-      }
-    };
-    Last out;       // rows (and scales) of the tile furthest on, next to become readable
-    auto prepare = [&] {
-      if constexpr (Q8) {
-        out = s3;
-        s3.live = s2.live;
-      } else {
-        out.live = s2.live;
-      }
-      if (s2.live && resolver) {
-        Last& l = Q8 ? s3 : out;
-#pragma unroll
-        for (int i = 0; i < kRowsPer; ++i) {
-          row_from(s2, i, &l.row[i]);
-          if constexpr (Q8) {
-            l.sck[i] = l.scv[i] = 0;
-            const uint32_t cr = l.row[i];
-            if (cr != ~0u) {
-              if (p.c.sw == 1) {
-                l.sck[i] = __ldg(p.c.k_scale + cr);
-                l.scv[i] = __ldg(p.c.v_scale + cr);
-              } else if constexpr (D == 128) {
-                l.sck[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_scale) + cr);
-                l.scv[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_scale) + cr);
-              } else {
-                l.sck[i] = __ldg(reinterpret_cast<const uint16_t*>(p.c.k_scale) + cr);
-                l.scv[i] = __ldg(reinterpret_cast<const uint16_t*>(p.c.v_scale) + cr);
-              }
-            }
-          }
-        }
-      }
-      // listed positions have arrived: request the pages
-      s2 = s1;
-      if (s2.live && resolver) {
-#pragma unroll
-        for (int i = 0; i < kRowsPer; ++i) {
-          const int pos = s1.v[i];
-          s2.pos[i] = pos >= 0 && pos < s2.lim ? pos : -1;
-          const int pi = pos >> p.c.page_shift;
-          s2.v[i] = s2.pos[i] >= 0 && pi < p.c.max_pages ? __ldg(p.c.table + (int64_t)s2.d * p.c.max_pages + pi) : -1;
-        }
-      }
-      // the next tile enters: request its listed positions
-      if (fu < n_units && ++fj >= fx.n_shared) {
-        fj = 0;
-        if (fx.n_shared > 0) fu += n_streams;   // (0: nothing decoded yet)
-        for (; fu < n_units; fu += n_streams) {
-          fx = decode_unit<false>(p, tab, gsz, chunk, fu, ring);
-          if (fx.n_shared > 0) break;
-        }
-      }
-      s1.live = fu < n_units;
-      if (s1.live && resolver) {
-        s1.d = fx.d;
-        s1.h = fx.h;
-        s1.lim = fx.P0 + (p.topk_idx ? fx.i0 + 1 : fx.last);   // keys behind the last visible one are never read
-#pragma unroll
-        for (int i = 0; i < kRowsPer; ++i) {
-          const int j = (fx.lo + fj) * kAttnKeys + row_of(i);
-          s1.v[i] = j;
-          if (p.topk_idx)
-            s1.v[i] = j < fx.n_list ? __ldg(p.topk_idx + (int64_t)(fx.q0 + fx.i0) * p.topk_width + j) : -1;
-        }
-      }
-    };
-    auto publish = [&] {
-      if (out.live) {
-        if (resolver) {
-#pragma unroll
-          for (int i = 0; i < kRowsPer; ++i) {
-            const int r = row_of(i);
-            rowtab[(pubs % kRowBufs) * kAttnKeys + r] = out.row[i];
-            if constexpr (Q8) {
-              sctab[((pubs & 3) * 2) * kAttnKeys + r] = out.sck[i];
-              sctab[((pubs & 3) * 2 + 1) * kAttnKeys + r] = out.scv[i];
-            }
-            const uint32_t seen = __ballot_sync(0xffffffffu, out.row[i] != ~0u);
-            if (lane == 0) masks[(pubs % kMaskRing) * 4 + (r >> 5)] = seen;
-          }
-        }
-        ++pubs;
-      }
-    };
-    auto step = [&] {
-      prepare();
-      publish();
-    };
-
-    // A free stage, for all of the ring's workers (the vote makes them give up together).
-    auto wait_empty = [&](int s, uint32_t parity, bool used) {
-      if (used) {
-        if (lt < 32 && ok) ok = wait_bar(bar_empty(ring, s), parity, abort_flag, status, tmo);
-        ok = !named_bar_or(bar_id, kLoaders, !ok);
-      }
-      return ok;
-    };
-
-    step();
-    step();
-    step();
-    if constexpr (Q8) step();
-    if constexpr (!Q8) {
-      constexpr int PPR = D / 8;                   // 16-byte pieces per row
-      constexpr int RPP = kLoaders / PPR;          // rows per pass: 8 or 16
-      const int c = lt % PPR, rsub = lt / PPR;
-      const uint32_t dcol = (uint32_t)(c >> 3) * kChunk + rsub * 128;
-      const uint32_t col = (c & 7) ^ (rsub & 7);   // (a pass is a multiple of 8 rows)
-      const uint16_t* kb = reinterpret_cast<const uint16_t*>(p.c.k) + c * 8;
-      const uint16_t* vb = reinterpret_cast<const uint16_t*>(p.c.v) + c * 8;
-      for (int t = 0; t < pubs; ++t) {
-        named_bar_sync(bar_id, kLoaders);          // the tile's rows are in the table
-#pragma unroll 1
+      // BF16 rows gathered four at a time by TMA; a warp brings a quarter of a tile.
+      const int wq = lt >> 5;
+      int t = 0;
+      gather(ring, wq * 32, std::integral_constant<int, 1>{}, [&](const auto& out) {
+        const uint32_t seen = __ballot_sync(0xffffffffu, out.row[0] != ~0u);
+        if (lane == 0) reinterpret_cast<uint32_t*>(smem + pl.off_mask)[(ring * kMaskRing + t % kMaskRing) * 4 + wq] = seen;
+        const int y = out.row[0] != ~0u ? (int)out.row[0] : no_row;
         for (int kv = 0; kv < 2; ++kv) {
-          if (!wait_empty(st, ph ^ 1u, wrapped)) break;   // (every worker at the same place)
-          const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
-          const uint16_t* src = kv ? vb : kb;
-#pragma unroll
-          for (int i = 0; i < kAttnKeys / RPP; ++i) {
-            const uint32_t e = rowtab[i * RPP + rsub];
-            const bool there = e != ~0u;
-            cp_async16(dst + i * RPP * 128 + (col << 4), src + (size_t)(there ? e : 0) * D, there);
-          }
-          if (p.fault_inject != 1 || t > 0 || kv > 0) cp_arrive(bar_full(ring, st));   // (the tests' withheld first stage)
-          advance();
-          if (kv == 0) prepare();                  // (the next tile's rows, while the values' stage may still be in use)
-        }
-        if (!ok) break;
-        named_bar_sync(bar_id, kLoaders);
-        publish();
-      }
-    } else {
-      constexpr int PPR = D / 16;                  // 16-code pieces per row
-      constexpr int RPP = kLoaders / PPR;
-      constexpr int kPasses = kAttnKeys / 2 / RPP; // half a tile is one item of the fetch ring
-      const int c = lt % PPR, rsub = lt / PPR;
-      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem + lt * 16;
-      const uint32_t dcol = (uint32_t)(c >> 2) * kChunk;
-      const int c0 = (c & 3) * 2;                  // first of the two 16-byte pieces in its 128-byte span
-      // items: keys 0-63, keys 64-127, values 0-63, values 64-127 of a tile
-      int ft = 0, fi = 0, fslot = 0, fetched = 0;
-      bool fend = false;
-      auto fetch = [&] {
-        if (!fend && fi == 0) {
-          if (ft >= pubs) {
-            fend = true;
-          } else if (!ok) {
-            fend = true;
-          } else {
-            named_bar_sync(bar_id, kLoaders);      // the tile's rows are in the table
-            step();
-          }
-        }
-        if (!fend) {
-          const uint8_t* src = reinterpret_cast<const uint8_t*>(fi >> 1 ? p.c.v : p.c.k) + c * 16;
-          const uint32_t* rt = rowtab + (ft & 1) * kAttnKeys + (fi & 1) * (kAttnKeys / 2);
-          const uint32_t dst = raw_base + (uint32_t)fslot * kRawItem;
-#pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const uint32_t cr = rt[i * RPP + rsub];
-            cp_async16(dst + i * (kLoaders * 16), src + (cr == ~0u ? 0 : (size_t)cr * D), cr != ~0u);
-          }
-          fslot = fslot + 1 == pl.nraw ? 0 : fslot + 1;
-          fi = (fi + 1) & 3;
-          if (fi == 0) ++ft;
-          ++fetched;
-        }
-        cp_commit();
-      };
-      for (int i = 0; i < pl.nraw; ++i) fetch();
-      int slot = 0;
-      for (int it = 0; it < fetched; ++it) {
-        if (!(it & 1) && !wait_empty(st, ph ^ 1u, wrapped)) break;   // (every worker at the same place)
-        {
-          switch (pl.nraw) {   // the oldest item has landed
-            case 1: cp_wait<0>(); break;
-            case 2: cp_wait<1>(); break;
-            case 3: cp_wait<2>(); break;
-            case 4: cp_wait<3>(); break;
-            case 5: cp_wait<4>(); break;
-            default: cp_wait<5>(); break;
-          }
-          const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
-          const uint32_t src = raw_base + (uint32_t)slot * kRawItem;
-          const uint32_t* sct = sctab + (((it >> 2) & 3) * 2 + ((it >> 1) & 1)) * kAttnKeys;
-          const int sshift = p.c.sw == 1 ? 0 : 8 * (c >> 1);
+          if (wrapped) ok = __all_sync(0xffffffffu, wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo));
+          if (!ok) return false;
+          const bool withheld = p.fault_inject == 1 && t == 0 && kv == 0;   // (tests)
+          const uint32_t bar = bar_full(ring, st), dst = ring_base + (uint32_t)st * kStage + wq * 32 * 128;
+          if (lane == 0 && !withheld) mbar_arrive_expect_tx(bar, 32 * D * 2);
+          __syncwarp();
 #pragma unroll 2
-          for (int i = 0; i < kPasses; ++i) {
-            const int r = (it & 1) * (kAttnKeys / 2) + i * RPP + rsub;
-            uint32_t w4[4], o[8];
-            ld_shared_v4(src + i * (kLoaders * 16), w4);
-            widen16(w4, (sct[r] >> sshift) & 0xFFu, o);
-            const uint32_t rowd = dst + r * 128;
-            st_shared_v4(rowd + ((uint32_t)(c0 ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-            st_shared_v4(rowd + ((uint32_t)((c0 + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+          for (int g = 0; g < 32; g += 4) {
+            const int y0 = __shfl_sync(0xffffffffu, y, g), y1 = __shfl_sync(0xffffffffu, y, g + 1);
+            const int y2 = __shfl_sync(0xffffffffu, y, g + 2), y3 = __shfl_sync(0xffffffffu, y, g + 3);
+            if (lane == 0 && !withheld) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_gather4(dst + c * kChunk + g * 128, kv ? &p.tm_v : &p.tm_k, bar, c * 64, y0, y1, y2, y3);
+            }
           }
-          if (it & 1) {
-            fence_proxy_async_smem();
-            if (p.fault_inject != 1 || it > 1) mbar_arrive(bar_full(ring, st));
-          }
+          advance();
         }
-        if (it & 1) advance();
-        slot = slot + 1 == pl.nraw ? 0 : slot + 1;
-        fetch();
-      }
-    }
-    cp_wait<0>();
-    if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
+        ++t;
+        return true;
+      });
     }
   } else if (wg >= 2) {
     // ======================= loaders and MMA =======================
@@ -997,6 +900,69 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       cp_wait<0>();
       if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
     };
+    // Listed rows of an 8-bit cache, as stored: four rows at a time by TMA, their scales by plain loads.
+    auto load_raw_rows = [&](int ring) {
+      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem;
+      int* const meta = reinterpret_cast<int*>(smem + pl.off_rows) + ring * 8;
+      uint32_t* const masks = reinterpret_cast<uint32_t*>(smem + pl.off_mask) + ring * kMaskRing * 4;
+      int slot = 0, t = 0;
+      uint32_t rph = 0, nq = 0;
+      bool wrapped = false;
+      gather(ring, 0, std::integral_constant<int, 4>{}, [&](const auto& out) {
+        int y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t seen = __ballot_sync(0xffffffffu, out.row[i] != ~0u);
+          if (lane == 0) masks[(t % kMaskRing) * 4 + i] = seen;
+          y[i] = out.row[i] != ~0u ? (int)out.row[i] : no_row;
+        }
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          if (wrapped && !__all_sync(0xffffffffu, wait_bar(bar_raw_empty(ring, slot), rph ^ 1u, abort_flag, status, tmo)))
+            return false;
+          const uint32_t bar = bar_raw_full(ring, slot), dst = raw_base + (uint32_t)slot * kRawItem;
+          uint8_t* sc = smem + (dst - sbase) + kAttnKeys * D;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 32 + lane;
+            const uint32_t e = kv ? out.scv[i] : out.sck[i];
+            if (p.c.sw == 1) sc[r] = (uint8_t)e;
+            else if constexpr (D == 128) reinterpret_cast<uint32_t*>(sc)[r] = e;
+            else reinterpret_cast<uint16_t*>(sc)[r] = (uint16_t)e;
+          }
+          const bool withheld = p.fault_inject == 1 && t == 0 && kv == 0;   // (tests)
+          if (lane == 0) meta[slot] = kAttnKeys;
+          __syncwarp();
+          if (lane == 0 && !withheld) mbar_arrive_expect_tx(bar, kAttnKeys * D);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll 1
+            for (int g = 0; g < 32; g += 4) {
+              const int y0 = __shfl_sync(0xffffffffu, y[i], g), y1 = __shfl_sync(0xffffffffu, y[i], g + 1);
+              const int y2 = __shfl_sync(0xffffffffu, y[i], g + 2), y3 = __shfl_sync(0xffffffffu, y[i], g + 3);
+              if (lane == 0 && !withheld)
+                tma_gather4(dst + (i * 32 + g) * D, kv ? &p.tm_v : &p.tm_k, bar, 0, y0, y1, y2, y3);
+            }
+          }
+          if (++slot == pl.nraw) {
+            slot = 0;
+            rph ^= 1u;
+            wrapped = true;
+          }
+        }
+        if (out.u >= 0) {   // a unit's first tile: its queries
+          if (nq > 0 &&
+              !__all_sync(0xffffffffu, wait_bar(bar_st(ring, Q_EMPTY), (nq - 1) & 1u, abort_flag, status, tmo)))
+            return false;
+          ++nq;
+          load_q(decode_unit<false>(p, tab, gsz, chunk, out.u, ring), ring);
+        }
+        ++t;
+        return true;
+      });
+      cp_wait<0>();
+    };
     // Query tiles of streams w0 .. w1 - 1, each as soon as its stream's last product with the one before is done.
     auto load_queries = [&](int w0, int w1) {
       uint32_t nq[2] = {0, 0};
@@ -1016,7 +982,9 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       cp_wait<0>();
     };
     if (warp < kMmaWarp) {
-      if constexpr (MODE != GATHER && Q8) {
+      if constexpr (MODE == GATHER && Q8) {
+        if (warp < R::kKeyWarp + 2) load_raw_rows(warp - R::kKeyWarp);
+      } else if constexpr (Q8) {
         if (warp == R::kKeyWarp) load_raw(0);
         else if (warp == R::kKeyWarp + 1 && kPair) load_queries(0, 2);
         else if (warp == R::kKeyWarp + 1) load_raw(1);
@@ -1077,15 +1045,11 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
               const uint32_t v_empty = bar_empty(ring, st);
               advance();
               have_k = next && mbar_try_wait(bar_full(ring, st), ph);
-              if (kWorkerCopies) fence_proxy_async_smem();   // the workers' cp.async writes, seen through the barriers
               // (P of a unit's first tile also says that the softmax warps have read the last unit's O)
               ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
               if (!ok) break;
               ++nt;
-              if (next && !have_k) {   // once more: the next QK without giving up the turn
-                have_k = mbar_try_wait(bar_full(ring, st), ph);
-                if (kWorkerCopies && have_k) fence_proxy_async_smem();
-              }
+              if (next && !have_k) have_k = mbar_try_wait(bar_full(ring, st), ph);   // once more: the next QK in this turn
               tc_fence_after();
               take_turn();
 #pragma unroll
@@ -1099,7 +1063,6 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
                 if (j > 0) end_turn();
                 ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
                 if (!ok) break;
-                if (kWorkerCopies) fence_proxy_async_smem();
                 tc_fence_after();
                 take_turn();
               }

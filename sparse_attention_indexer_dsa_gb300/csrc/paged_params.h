@@ -64,10 +64,10 @@ struct AttnPlan {
   int tq;          // tokens per query tile
   int rows_cap;    // rows of a tile that can be live
   int nst;         // key/value stages per ring
-  int nraw;        // tiles (gathered: half tiles) of stored 8-bit rows per ring
+  int nraw;        // tiles of stored 8-bit rows per ring
   int max_units;   // units with room for a partial result; 0: key ranges are never divided
   uint32_t q_bytes;                                        // query tile in shared memory
-  uint32_t off_ring, off_raw, off_rows, off_scale, off_mask, off_bars, off_tab, smem;
+  uint32_t off_ring, off_raw, off_rows, off_mask, off_bars, off_tab, smem;
 };
 
 struct AttnParams {
