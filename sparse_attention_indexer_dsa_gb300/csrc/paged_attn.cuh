@@ -24,8 +24,9 @@
 //         key/value stages (long chunks: the keys are read half as often);
 //   else: the streams are independent, each with its own units and ring
 //         (single tokens, short chunks, selected rows).
-// Loaders.  TMA brings everything: all visible keys as a box per page, listed
-// keys four rows at a time, into the 128-byte swizzled layout the MMA reads.
+// Loaders.  TMA brings all visible keys as a box per page and listed 8-bit rows
+// four at a time; listed BF16 rows are copied with cp.async; all of it in the
+// 128-byte swizzled layout the MMA reads.
 // Listed position -> page -> row is resolved a step per tile, ahead of the
 // copies, so its dependent loads are off the path.  Rows that are not there are
 // zero-filled, so nothing outside a sequence's own rows enters a product.  Tiles
@@ -324,9 +325,9 @@ struct Roles {
   static constexpr int kKeyWarp = kWorkWarps > 0 ? kWarps - 4 : 8;            // TMA: and the next one
   // registers: shares of what the launch holds (threads x the launch's count, a multiple of 8)
   static constexpr int kLaunchRegs = kWorkWarps == 16 ? 72 : (kWorkWarps == 8 ? 96 : 128);
-  static constexpr int kSoftmaxRegs = kWorkWarps == 16 ? 104 : (kWorkWarps == 8 ? 112 : 192);
-  static constexpr int kWorkRegs = kWorkWarps == 16 ? 56 : 80;
-  static constexpr int kAuxRegs = kWorkWarps == 16 ? 72 : (kWorkWarps == 8 ? 96 : 64);
+  static constexpr int kSoftmaxRegs = kWorkWarps == 16 ? 104 : (kWorkWarps == 8 ? 128 : 192);
+  static constexpr int kWorkRegs = kWorkWarps == 16 ? 56 : 72;
+  static constexpr int kAuxRegs = kWorkWarps == 16 ? 72 : (kWorkWarps == 8 ? 80 : 64);
   static_assert(2 * kSoftmaxRegs + kWorkWarps / 4 * kWorkRegs + (kWarps - 8 - kWorkWarps) / 4 * kAuxRegs <=
                     kWarps / 4 * kLaunchRegs, "shares");
 };
@@ -335,6 +336,7 @@ template <int D, bool Q8, int MODE>
 __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_kernel(const __grid_constant__ AttnParams p) {
   using R = Roles<Q8, MODE>;
   constexpr bool kPair = MODE == PAIR;
+  constexpr bool kWorkerCopies = MODE == GATHER && !Q8;   // stages written by cp.async: fenced by the MMA warp
   constexpr uint32_t kStage = kAttnKeys * D * 2;     // one tile of keys or values
   constexpr uint32_t kChunk = kAttnKeys * 128;       // 64 of its columns
   constexpr int kRings = kPair ? 1 : 2;
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     ctl[4] = 0;
     for (int r = 0; r < kRings; ++r) {
       for (int s = 0; s < pl.nst; ++s) {
-        mbar_init(bar_full(r, s), Q8 ? kLoaders : (MODE == GATHER ? kLoaders / 32 : 1));
+        mbar_init(bar_full(r, s), R::kWorkWarps > 0 ? kLoaders : 1);
         mbar_init(bar_empty(r, s), kPair ? 2 : 1);
       }
       for (int s = 0; s < pl.nraw; ++s) {
@@ -724,35 +726,34 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         }
       }
     } else {
-      // BF16 rows gathered four at a time by TMA; a warp brings a quarter of a tile.
-      const int wq = lt >> 5;
+      // BF16 rows copied one by one; a warp brings a quarter of a tile.  (TMA row gathers of four come to
+      // 27 bytes a cycle and SM, cp.async from eight warps to 60.)
+      constexpr int PPR = D / 8;                   // 16-byte pieces per row
+      constexpr int RPP = 32 / PPR;                // rows per pass
+      const int wq = lt >> 5, c = lane % PPR, rsub = lane / PPR;
+      const uint32_t dcol = (uint32_t)(c >> 3) * kChunk + (wq * 32 + rsub) * 128;
       int t = 0;
       gather(ring, wq * 32, std::integral_constant<int, 1>{}, [&](const auto& out) {
         const uint32_t seen = __ballot_sync(0xffffffffu, out.row[0] != ~0u);
         if (lane == 0) reinterpret_cast<uint32_t*>(smem + pl.off_mask)[(ring * kMaskRing + t % kMaskRing) * 4 + wq] = seen;
-        const int y = out.row[0] != ~0u ? (int)out.row[0] : no_row;
         for (int kv = 0; kv < 2; ++kv) {
           if (wrapped) ok = __all_sync(0xffffffffu, wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo));
           if (!ok) return false;
-          const bool withheld = p.fault_inject == 1 && t == 0 && kv == 0;   // (tests)
-          const uint32_t bar = bar_full(ring, st), dst = ring_base + (uint32_t)st * kStage + wq * 32 * 128;
-          if (lane == 0 && !withheld) mbar_arrive_expect_tx(bar, 32 * D * 2);
-          __syncwarp();
-#pragma unroll 2
-          for (int g = 0; g < 32; g += 4) {
-            const int y0 = __shfl_sync(0xffffffffu, y, g), y1 = __shfl_sync(0xffffffffu, y, g + 1);
-            const int y2 = __shfl_sync(0xffffffffu, y, g + 2), y3 = __shfl_sync(0xffffffffu, y, g + 3);
-            if (lane == 0 && !withheld) {
+          const uint32_t dst = ring_base + (uint32_t)st * kStage + dcol;
+          const uint16_t* src = reinterpret_cast<const uint16_t*>(kv ? p.c.v : p.c.k) + c * 8;
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_gather4(dst + c * kChunk + g * 128, kv ? &p.tm_v : &p.tm_k, bar, c * 64, y0, y1, y2, y3);
-            }
+          for (int i = 0; i < 32; i += RPP) {
+            const uint32_t e = __shfl_sync(0xffffffffu, out.row[0], i + rsub);
+            const bool there = e != ~0u;
+            cp_async16(dst + i * 128 + (((c & 7) ^ ((i + rsub) & 7)) << 4), src + (size_t)(there ? e : 0) * D, there);
           }
+          if (p.fault_inject != 1 || t > 0 || kv > 0) cp_arrive(bar_full(ring, st));   // (the tests' withheld first stage)
           advance();
         }
         ++t;
         return true;
       });
+      cp_wait<0>();
     }
   } else if (wg >= 2) {
     // ======================= loaders and MMA =======================
@@ -1045,11 +1046,15 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
               const uint32_t v_empty = bar_empty(ring, st);
               advance();
               have_k = next && mbar_try_wait(bar_full(ring, st), ph);
+              if (kWorkerCopies) fence_proxy_async_smem();   // the workers' cp.async writes, seen through the barriers
               // (P of a unit's first tile also says that the softmax warps have read the last unit's O)
               ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
               if (!ok) break;
               ++nt;
-              if (next && !have_k) have_k = mbar_try_wait(bar_full(ring, st), ph);   // once more: the next QK in this turn
+              if (next && !have_k) {   // once more: the next QK in this turn
+                have_k = mbar_try_wait(bar_full(ring, st), ph);
+                if (kWorkerCopies && have_k) fence_proxy_async_smem();
+              }
               tc_fence_after();
               take_turn();
 #pragma unroll
@@ -1063,6 +1068,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
                 if (j > 0) end_turn();
                 ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
                 if (!ok) break;
+                if (kWorkerCopies) fence_proxy_async_smem();
                 tc_fence_after();
                 take_turn();
               }
@@ -1122,10 +1128,11 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         if (!ok) break;
         if (warp_live) {
           tc_fence_after();
-          // Pages by TMA in BF16: the row's 128 logits stay in registers.  With worker warps beside
-          // them: 32 at a time, read from TMEM twice, for the maximum and for the weights (fewer
-          // registers, a fifth of the code).
-          constexpr int kHeld = R::kWorkWarps > 0 ? 32 : kAttnKeys;
+          // Pages by TMA in BF16: the row's 128 logits stay in registers.  With copying workers beside
+          // them: 64, the others being read from TMEM twice, for the maximum and for the weights; with
+          // widening ones, 32 in a rolled loop (slower on its own, but it leaves them the registers).
+          constexpr int kHeld = R::kWorkWarps == 16 ? 32 : (R::kWorkWarps > 0 ? 64 : kAttnKeys);
+          constexpr int kUnroll = kHeld == 32 ? 1 : kAttnKeys / kHeld;
           uint32_t s[kHeld];
           const int lim = vis - (x.lo + j) * kAttnKeys;
           const uint32_t* const mask = masks + (nt % kMaskRing) * 4;
@@ -1139,18 +1146,21 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
                 for (int c = 0; c < kHeld; ++c) s[c] = c0 + c < lim ? s[c] : 0xFF800000u;
               }
             } else {
-              const uint32_t mk = mask[c0 >> 5];   // (listed keys: kHeld is 32)
-              if (mk != 0xFFFFFFFFu) {
 #pragma unroll
-                for (int c = 0; c < kHeld; ++c) s[c] = (mk >> (c & 31)) & 1u ? s[c] : 0xFF800000u;
+              for (int c = 0; c < kHeld; c += 32) {
+                const uint32_t mk = mask[(c0 + c) >> 5];
+                if (mk != 0xFFFFFFFFu) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) s[c + i] = (mk >> i) & 1u ? s[c + i] : 0xFF800000u;
+                }
               }
             }
           };
           float mx[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) mx[c] = -INFINITY;
-#pragma unroll 1
-          for (int c0 = 0; c0 < kAttnKeys; c0 += kHeld) {
+#pragma unroll kUnroll
+          for (int c0 = kAttnKeys - kHeld; c0 >= 0; c0 -= kHeld) {   // (the first ones stay)
             load_s(c0);
 #pragma unroll
             for (int c = 0; c < kHeld; c += 2)
@@ -1179,9 +1189,9 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           const float mref = m == -INFINITY ? 0.f : m;
           const float2 sc2 = make_float2(scale, scale), mm2 = make_float2(-mref, -mref);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
+#pragma unroll kUnroll
           for (int c0 = 0; c0 < kAttnKeys; c0 += kHeld) {
-            if (kHeld < kAttnKeys) load_s(c0);
+            if (c0 > 0) load_s(c0);
 #pragma unroll
             for (int c = 0; c < kHeld; c += 32) {
               uint32_t pk[16];
