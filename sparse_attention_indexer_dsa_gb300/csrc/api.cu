@@ -110,8 +110,8 @@ dsa_status_t make_operand_map(CUtensorMap* m, const void* base, int64_t rows, in
 namespace dsa {
 
 // Pages [groups][rows][D]: BF16 in boxes of box_rows x 64 columns with the 128-byte swizzle, or 8-bit
-// codes in boxes of box_rows whole rows; groups 0: a two-dimensional map [rows][D], for row gathers.
-dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, int64_t rows, int D, int box_rows, bool b8) {
+// codes in boxes of box_rows whole rows.
+dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, int rows, int D, int box_rows, bool b8) {
   auto enc = encode_fn();
   if (!enc) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   const cuuint64_t row = (cuuint64_t)D * (b8 ? 1 : 2);
@@ -119,7 +119,7 @@ dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, in
   cuuint64_t strides[2] = {row, row * rows};
   cuuint32_t box[3] = {(cuuint32_t)(b8 ? D : 64), (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(m, b8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups > 0 ? 3 : 2, const_cast<void*>(base),
+  CUresult r = enc(m, b8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    b8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -20,7 +20,7 @@ dsa_status_t cuda_fail(cudaError_t e, const char* what);
 // Facts of the current device; refuses anything but sm_103.
 dsa_status_t device_info(DevInfo* out);
 
-dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, int64_t rows, int D, int box_rows, bool b8);
+dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, int rows, int D, int box_rows, bool b8);
 
 // Limit of the kernels' bounded waits, and the fault injection of the tests.
 unsigned long long wait_timeout_ns();

@@ -303,12 +303,7 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
     w += round256(slots * 8);
     p.part_o = reinterpret_cast<float*>(w);
   }
-  if (p.plan.gather) {
-    const int64_t rows = (int64_t)num_pages * n_kv_heads * page_size;
-    const bool b8 = prec != DSA_PREC_BF16;
-    if ((s = make_pages_map(&p.tm_k, k_pages, 0, rows, head_dim, 1, b8)) != DSA_OK) return s;
-    if ((s = make_pages_map(&p.tm_v, v_pages, 0, rows, head_dim, 1, b8)) != DSA_OK) return s;
-  } else {
+  if (!p.plan.gather) {
     const int64_t groups = (int64_t)num_pages * n_kv_heads;
     const int box = page_size < kAttnKeys ? page_size : kAttnKeys;
     const bool b8 = prec != DSA_PREC_BF16;

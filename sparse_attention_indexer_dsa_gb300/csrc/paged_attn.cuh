@@ -24,9 +24,10 @@
 //         key/value stages (long chunks: the keys are read half as often);
 //   else: the streams are independent, each with its own units and ring
 //         (single tokens, short chunks, selected rows).
-// Loaders.  TMA brings all visible keys as a box per page and listed 8-bit rows
-// four at a time; listed BF16 rows are copied with cp.async; all of it in the
-// 128-byte swizzled layout the MMA reads.
+// Loaders.  TMA brings all visible keys as a box per page; listed rows are copied
+// one by one with cp.async (TMA row gathers of four came to 27 bytes a cycle and
+// SM, cp.async from eight warps to 60); BF16 in the 128-byte swizzled layout the
+// MMA reads.
 // Listed position -> page -> row is resolved a step per tile, ahead of the
 // copies, so its dependent loads are off the path.  Rows that are not there are
 // zero-filled, so nothing outside a sequence's own rows enters a product.  Tiles
@@ -78,20 +79,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// Four rows of a two-dimensional map (its box one row high).
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y0, int y1, int y2,
-                                            int y3) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
-      : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrives (without raising the count) once this thread's earlier cp.async have landed.
 __device__ __forceinline__ void cp_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -313,22 +301,25 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&w)[4]) {
 // scales are too short for a bulk copy).
 enum { PAIR = 0, SOLO = 1, GATHER = 2 };
 
-// Warps: 8 softmax; workers (16 widen 8-bit tiles; 8 bring gathered BF16 rows); the
-// rest: key loaders (TMA), query loaders, MMA 0 and 1 last.  (The four warps of an SM's sub-partition
+// Warps: 8 softmax; workers (16, or 12 of gathered rows, widen 8-bit tiles; 8 bring gathered BF16
+// rows); 4 that bring gathered 8-bit rows; the rest: key loaders (TMA), query loaders, MMA 0 and 1 last.  (The four warps of an SM's sub-partition
 // are those of equal number modulo 4; loaders and MMA warps are kept on different ones.)
 template <bool Q8, int MODE>
 struct Roles {
-  static constexpr int kWorkWarps = Q8 ? 16 : (MODE == GATHER ? 8 : 0);
-  static constexpr int kWarps = kWorkWarps > 0 ? 12 + kWorkWarps : 16;
+  static constexpr int kWorkWarps = MODE == GATHER ? (Q8 ? 12 : 8) : (Q8 ? 16 : 0);
+  static constexpr int kBringWarps = MODE == GATHER && Q8 ? 4 : 0;
+  static constexpr int kWarps = kWorkWarps > 0 ? 12 + kWorkWarps + kBringWarps : 16;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kQueryWarp = kWorkWarps > 0 ? kWarps - 4 : 10;         // and the next one
   static constexpr int kKeyWarp = kWorkWarps > 0 ? kWarps - 4 : 8;            // TMA: and the next one
   // registers: shares of what the launch holds (threads x the launch's count, a multiple of 8)
-  static constexpr int kLaunchRegs = kWorkWarps == 16 ? 72 : (kWorkWarps == 8 ? 96 : 128);
-  static constexpr int kSoftmaxRegs = kWorkWarps == 16 ? 104 : (kWorkWarps == 8 ? 128 : 192);
-  static constexpr int kWorkRegs = kWorkWarps == 16 ? 56 : 72;
-  static constexpr int kAuxRegs = kWorkWarps == 16 ? 72 : (kWorkWarps == 8 ? 80 : 64);
-  static_assert(2 * kSoftmaxRegs + kWorkWarps / 4 * kWorkRegs + (kWarps - 8 - kWorkWarps) / 4 * kAuxRegs <=
+  static constexpr int kLaunchRegs = Q8 ? 72 : (MODE == GATHER ? 96 : 128);
+  static constexpr int kSoftmaxRegs = Q8 ? 104 : (MODE == GATHER ? 128 : 192);
+  static constexpr int kWorkRegs = Q8 ? 56 : 72;
+  static constexpr int kBringRegs = 64;
+  static constexpr int kAuxRegs = Q8 ? (MODE == GATHER ? 64 : 72) : (MODE == GATHER ? 80 : 64);
+  static_assert(2 * kSoftmaxRegs + kWorkWarps / 4 * kWorkRegs + kBringWarps / 4 * kBringRegs +
+                        (kWarps - 8 - kWorkWarps - kBringWarps) / 4 * kAuxRegs <=
                     kWarps / 4 * kLaunchRegs, "shares");
 };
 
@@ -374,7 +365,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         mbar_init(bar_empty(r, s), kPair ? 2 : 1);
       }
       for (int s = 0; s < pl.nraw; ++s) {
-        mbar_init(bar_raw_full(r, s), 1);
+        mbar_init(bar_raw_full(r, s), MODE == GATHER ? 128 : 1);   // (two warps, each thread twice)
         mbar_init(bar_raw_empty(r, s), kLoaders / 32);
       }
     }
@@ -549,7 +540,6 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
   // Listed keys (or, without a list, all of them) as cache rows, tile by tile, for one warp: position ->
   // page -> row, a step per tile, so that the dependent loads of a tile are spread over the tiles before
   // it.  kRowsPer rows a lane from row row0 of the tile on; use(rows) returns false to give up.
-  const int no_row = (p.c.num_pages * p.c.n_kv) << p.c.page_shift;   // behind the last row: TMA fills zeros
   auto gather = [&](int ring, int row0, auto rows_per, auto use) {
     constexpr int kRowsPer = decltype(rows_per)::value;
     int fu = first_unit(ring), fj = -1;
@@ -675,7 +665,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       // Stored tiles (keys, values, keys, ...) to BF16 stages.
       constexpr int PPR = D / 16;                  // 16-code pieces per row
       constexpr int RPP = kLoaders / PPR;
-      constexpr int kPasses = kAttnKeys / RPP;
+      constexpr int kPasses = (kAttnKeys + RPP - 1) / RPP;   // (12 workers: the last pass is not whole)
       const int c = lt % PPR, rsub = lt / PPR;
       const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem + rsub * D + c * 16;
       const int* const meta = reinterpret_cast<const int*>(smem + pl.off_rows) + ring * 8;
@@ -699,11 +689,14 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           uint32_t w4[kPasses][4], e8[kPasses];
 #pragma unroll
           for (int i = 0; i < kPasses; ++i) {
-            ld_shared_v4(raw + i * RPP * D, w4[i]);
-            e8[i] = scales[i * RPP * sw];
+            if (kAttnKeys % RPP == 0 || i * RPP + rsub < kAttnKeys) {
+              ld_shared_v4(raw + i * RPP * D, w4[i]);
+              e8[i] = scales[i * RPP * sw];
+            }
           }
 #pragma unroll
           for (int i = 0; i < kPasses; ++i) {
+            if (kAttnKeys % RPP != 0 && i * RPP + rsub >= kAttnKeys) break;
             uint32_t o[8];
             if (i * RPP >= valid) {   // nothing of the page's other slots
               e8[i] = 0;
@@ -726,8 +719,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         }
       }
     } else {
-      // BF16 rows copied one by one; a warp brings a quarter of a tile.  (TMA row gathers of four come to
-      // 27 bytes a cycle and SM, cp.async from eight warps to 60.)
+      // BF16 rows copied one by one; a warp brings a quarter of a tile.
       constexpr int PPR = D / 8;                   // 16-byte pieces per row
       constexpr int RPP = 32 / PPR;                // rows per pass
       const int wq = lt >> 5, c = lane % PPR, rsub = lane / PPR;
@@ -753,8 +745,63 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         ++t;
         return true;
       });
-      cp_wait<0>();
+      cp_wait_all();
     }
+  } else if (R::kBringWarps > 0 && wg >= 2 && wg < 2 + (R::kWorkWarps + R::kBringWarps) / 4) {
+    // ======================= gathered rows of an 8-bit cache, as stored =======================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kBringRegs));
+    const int ring = (warp >> 1) & 1, part = warp & 1;   // two warps to a ring, half a tile each
+    constexpr int PPR = D / 16;                          // 16-byte pieces per row
+    constexpr int RPP = 32 / PPR;                        // rows per pass
+    const int c = lane % PPR, rsub = lane / PPR;
+    const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem;
+    int* const meta = reinterpret_cast<int*>(smem + pl.off_rows) + ring * 8;
+    uint32_t* const masks = reinterpret_cast<uint32_t*>(smem + pl.off_mask) + ring * kMaskRing * 4 + part * 2;
+    int slot = 0, t = 0;
+    uint32_t rph = 0;
+    bool wrapped = false;
+    gather(ring, part * 64, std::integral_constant<int, 2>{}, [&](const auto& out) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t seen = __ballot_sync(0xffffffffu, out.row[i] != ~0u);
+        if (lane == 0) masks[(t % kMaskRing) * 4 + i] = seen;
+      }
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        if (wrapped && !__all_sync(0xffffffffu, wait_bar(bar_raw_empty(ring, slot), rph ^ 1u, abort_flag, status, tmo)))
+          return false;
+        const uint32_t bar = bar_raw_full(ring, slot), dst = raw_base + (uint32_t)slot * kRawItem;
+        uint8_t* sc = smem + (dst - sbase) + kAttnKeys * D;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(kv ? p.c.v : p.c.k) + c * 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = part * 64 + i * 32 + lane;
+          const uint32_t e = kv ? out.scv[i] : out.sck[i];
+          if (p.c.sw == 1) sc[r] = (uint8_t)e;
+          else if constexpr (D == 128) reinterpret_cast<uint32_t*>(sc)[r] = e;
+          else reinterpret_cast<uint16_t*>(sc)[r] = (uint16_t)e;
+#pragma unroll 4
+          for (int g = 0; g < 32; g += RPP) {
+            const uint32_t cr = __shfl_sync(0xffffffffu, out.row[i], g + rsub);
+            const bool there = cr != ~0u;
+            cp_async16(dst + (part * 64 + i * 32 + g + rsub) * D + c * 16, src + (size_t)(there ? cr : 0) * D, there);
+          }
+        }
+        if (part == 0 && lane == 0) meta[slot] = kAttnKeys;
+        if (p.fault_inject != 1 || t > 0 || kv > 0) {   // (the tests' withheld first tile)
+          mbar_arrive(bar);     // the scales
+          cp_arrive(bar);       // the codes, when they have landed
+        }
+        if (++slot == pl.nraw) {
+          slot = 0;
+          rph ^= 1u;
+          wrapped = true;
+        }
+      }
+      ++t;
+      return true;
+    });
+    cp_wait_all();
   } else if (wg >= 2) {
     // ======================= loaders and MMA =======================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kAuxRegs));
@@ -788,7 +835,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           if (whole && lane < boxes && !good) bad_page = true;
           for (int kv = 0; kv < 2; ++kv) {
             if (wrapped && !__all_sync(0xffffffffu, wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo))) {
-              cp_wait<0>();
+              cp_wait_all();
               return;
             }
             const uint32_t dst = ring_base + (uint32_t)st * kStage;
@@ -818,8 +865,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
                 cp_async16(dst + (uint32_t)(c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                            src + (cr < 0 ? 0 : cr * D), cr >= 0);
               }
-              cp_commit();
-              cp_wait<0>();
+              cp_wait_all();
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0 && !withheld) mbar_arrive(bar_full(ring, st));
@@ -864,7 +910,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           for (int kv = 0; kv < 2; ++kv) {
             if (wrapped &&
                 !__all_sync(0xffffffffu, wait_bar(bar_raw_empty(ring, slot), rph ^ 1u, abort_flag, status, tmo))) {
-              cp_wait<0>();
+              cp_wait_all();
               return;
             }
             const uint32_t bar = bar_raw_full(ring, slot), dst = raw_base + (uint32_t)slot * kRawItem;
@@ -898,71 +944,8 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           }
         }
       }
-      cp_wait<0>();
+      cp_wait_all();
       if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
-    };
-    // Listed rows of an 8-bit cache, as stored: four rows at a time by TMA, their scales by plain loads.
-    auto load_raw_rows = [&](int ring) {
-      const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem;
-      int* const meta = reinterpret_cast<int*>(smem + pl.off_rows) + ring * 8;
-      uint32_t* const masks = reinterpret_cast<uint32_t*>(smem + pl.off_mask) + ring * kMaskRing * 4;
-      int slot = 0, t = 0;
-      uint32_t rph = 0, nq = 0;
-      bool wrapped = false;
-      gather(ring, 0, std::integral_constant<int, 4>{}, [&](const auto& out) {
-        int y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t seen = __ballot_sync(0xffffffffu, out.row[i] != ~0u);
-          if (lane == 0) masks[(t % kMaskRing) * 4 + i] = seen;
-          y[i] = out.row[i] != ~0u ? (int)out.row[i] : no_row;
-        }
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          if (wrapped && !__all_sync(0xffffffffu, wait_bar(bar_raw_empty(ring, slot), rph ^ 1u, abort_flag, status, tmo)))
-            return false;
-          const uint32_t bar = bar_raw_full(ring, slot), dst = raw_base + (uint32_t)slot * kRawItem;
-          uint8_t* sc = smem + (dst - sbase) + kAttnKeys * D;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = i * 32 + lane;
-            const uint32_t e = kv ? out.scv[i] : out.sck[i];
-            if (p.c.sw == 1) sc[r] = (uint8_t)e;
-            else if constexpr (D == 128) reinterpret_cast<uint32_t*>(sc)[r] = e;
-            else reinterpret_cast<uint16_t*>(sc)[r] = (uint16_t)e;
-          }
-          const bool withheld = p.fault_inject == 1 && t == 0 && kv == 0;   // (tests)
-          if (lane == 0) meta[slot] = kAttnKeys;
-          __syncwarp();
-          if (lane == 0 && !withheld) mbar_arrive_expect_tx(bar, kAttnKeys * D);
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-#pragma unroll 1
-            for (int g = 0; g < 32; g += 4) {
-              const int y0 = __shfl_sync(0xffffffffu, y[i], g), y1 = __shfl_sync(0xffffffffu, y[i], g + 1);
-              const int y2 = __shfl_sync(0xffffffffu, y[i], g + 2), y3 = __shfl_sync(0xffffffffu, y[i], g + 3);
-              if (lane == 0 && !withheld)
-                tma_gather4(dst + (i * 32 + g) * D, kv ? &p.tm_v : &p.tm_k, bar, 0, y0, y1, y2, y3);
-            }
-          }
-          if (++slot == pl.nraw) {
-            slot = 0;
-            rph ^= 1u;
-            wrapped = true;
-          }
-        }
-        if (out.u >= 0) {   // a unit's first tile: its queries
-          if (nq > 0 &&
-              !__all_sync(0xffffffffu, wait_bar(bar_st(ring, Q_EMPTY), (nq - 1) & 1u, abort_flag, status, tmo)))
-            return false;
-          ++nq;
-          load_q(decode_unit<false>(p, tab, gsz, chunk, out.u, ring), ring);
-        }
-        ++t;
-        return true;
-      });
-      cp_wait<0>();
     };
     // Query tiles of streams w0 .. w1 - 1, each as soon as its stream's last product with the one before is done.
     auto load_queries = [&](int w0, int w1) {
@@ -973,19 +956,17 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           if (x.n == 0) continue;
           if (nq[w - w0] > 0 && !__all_sync(0xffffffffu, mbar_wait(bar_st(w, Q_EMPTY), (nq[w - w0] - 1) & 1u, abort_flag,
                                                                     status, tmo))) {
-            cp_wait<0>();
+            cp_wait_all();
             return;
           }
           ++nq[w - w0];
           load_q(x, w);
         }
       }
-      cp_wait<0>();
+      cp_wait_all();
     };
     if (warp < kMmaWarp) {
-      if constexpr (MODE == GATHER && Q8) {
-        if (warp < R::kKeyWarp + 2) load_raw_rows(warp - R::kKeyWarp);
-      } else if constexpr (Q8) {
+      if constexpr (MODE != GATHER && Q8) {
         if (warp == R::kKeyWarp) load_raw(0);
         else if (warp == R::kKeyWarp + 1 && kPair) load_queries(0, 2);
         else if (warp == R::kKeyWarp + 1) load_raw(1);
