@@ -686,26 +686,30 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           const uint8_t* scales = smem + pl.off_raw + (size_t)(ring * pl.nraw + slot) * kRawItem + kAttnKeys * D + s0;
           const int valid = meta[slot] - rsub;
           const uint32_t dst = ring_base + (uint32_t)st * kStage;
-          uint32_t w4[kPasses][4], e8[kPasses];
+          constexpr int kBatch = kPasses % 4 == 0 ? 4 : (kPasses % 2 == 0 ? 2 : 1);   // passes whose loads go first
 #pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            if (kAttnKeys % RPP == 0 || i * RPP + rsub < kAttnKeys) {
-              ld_shared_v4(raw + i * RPP * D, w4[i]);
-              e8[i] = scales[i * RPP * sw];
+          for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
+            uint32_t w4[kBatch][4], e8[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              if (kAttnKeys % RPP == 0 || (i0 + i) * RPP + rsub < kAttnKeys) {
+                ld_shared_v4(raw + (i0 + i) * RPP * D, w4[i]);
+                e8[i] = scales[(i0 + i) * RPP * sw];
+              }
             }
-          }
 #pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            if (kAttnKeys % RPP != 0 && i * RPP + rsub >= kAttnKeys) break;
-            uint32_t o[8];
-            if (i * RPP >= valid) {   // nothing of the page's other slots
-              e8[i] = 0;
+            for (int i = 0; i < kBatch; ++i) {
+              if (kAttnKeys % RPP != 0 && (i0 + i) * RPP + rsub >= kAttnKeys) break;
+              uint32_t o[8];
+              if ((i0 + i) * RPP >= valid) {   // nothing of the page's other slots
+                e8[i] = 0;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) w4[i][q] = 0;
+                for (int q = 0; q < 4; ++q) w4[i][q] = 0;
+              }
+              widen16(w4[i], e8[i], o);
+              st_shared_v4(dst + at0 + (i0 + i) * RPP * 128, o[0], o[1], o[2], o[3]);
+              st_shared_v4(dst + at1 + (i0 + i) * RPP * 128, o[4], o[5], o[6], o[7]);
             }
-            widen16(w4[i], e8[i], o);
-            st_shared_v4(dst + at0 + i * RPP * 128, o[0], o[1], o[2], o[3]);
-            st_shared_v4(dst + at1 + i * RPP * 128, o[4], o[5], o[6], o[7]);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_raw_empty(ring, slot));

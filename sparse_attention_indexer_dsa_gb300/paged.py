@@ -113,23 +113,15 @@ def paged_cache(num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, 
 # The checks of one call run in a few microseconds of host time, a good part of
 # a single-token call: one comparison per property, and the message only when one fails.
 _stream = torch._C._cuda_getCurrentRawStream        # of a device index
+_current = torch._C._cuda_getDevice
 
 
-class _Current:
-    """Makes the tensors' device the current one for a launch, where it is not."""
-    __slots__ = ("device", "was")
-
-    def __init__(self, device: torch.device):
-        self.device = device.index
-
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.was != self.device:
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.was != self.device:
-            torch.cuda.set_device(self.was)
+def _call(fn, device: torch.device, args) -> int:
+    """The call with the tensors' device as the current one (changed only where it is not)."""
+    if _current() == device.index:
+        return fn(*args, _stream(device.index))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(device.index))
 
 
 def _refuse(t: torch.Tensor, name: str, device: torch.device, dtype, shape):
@@ -227,11 +219,12 @@ def cache_write(cache: PagedCache, k: torch.Tensor, v: Optional[torch.Tensor], c
     ck = _arg(cu_seqlens_k, "cu_seqlens_k", dev, torch.int32, (B + 1,))
     if ws is None:
         ws = torch.empty(_abi.DSA_CACHE_WS_BYTES, dtype=torch.uint8, device=dev)
-    wp = _arg(ws, "ws", dev, torch.uint8)
-    with _Current(dev):
-        code = _abi.load().dsa_idx_cache_write(
-            kp, kst, ksp, vp, vst, vsp, _SOURCES[dt], _rule(scale_rule), cq, ck, B, T, table, width, *a,
-            N, ps, Hk, D, _PREC[cache.prec], wp, ws.numel(), _stream(dev.index))
+        wp = ws.data_ptr()
+    else:
+        wp = _arg(ws, "ws", dev, torch.uint8)
+    code = _call(_abi.load().dsa_idx_cache_write, dev, (
+        kp, kst, ksp, vp, vst, vsp, _SOURCES[dt], _rule(scale_rule), cq, ck, B, T, table, width, *a, N, ps, Hk, D,
+        _PREC[cache.prec], wp, ws.numel()))
     if code:
         raise _error(code, "dsa_idx_cache_write")
 
@@ -277,10 +270,11 @@ def cache_read(cache: PagedCache, cu_seqlens_k: torch.Tensor, page_table: torch.
         ksp, vsp = _arg(ks, "out k_scale", dev, torch.uint8, sshape), _arg(vs, "out v_scale", dev, torch.uint8, sshape)
     if ws is None:
         ws = torch.empty(_abi.DSA_CACHE_WS_BYTES, dtype=torch.uint8, device=dev)
-    wp = _arg(ws, "ws", dev, torch.uint8)
-    with _Current(dev):
-        code = _abi.load().dsa_idx_cache_read(*a, N, ps, Hk, D, _PREC[cache.prec], table, width, ck, B, total_k, int(deq),
-                                              kp, ksp, vp, vsp, wp, ws.numel(), _stream(dev.index))
+        wp = ws.data_ptr()
+    else:
+        wp = _arg(ws, "ws", dev, torch.uint8)
+    code = _call(_abi.load().dsa_idx_cache_read, dev, (
+        *a, N, ps, Hk, D, _PREC[cache.prec], table, width, ck, B, total_k, int(deq), kp, ksp, vp, vsp, wp, ws.numel()))
     if code:
         raise _error(code, "dsa_idx_cache_read")
     return k, ks, v, vs
@@ -345,10 +339,9 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, cu_seqlens_q: torch.Tens
     if ws is None:
         ws = attention_workspace(T, B, max_seqlen_q, H, Hk, D, W, dev)
     wp = _arg(ws, "ws", dev, torch.uint8)
-    with _Current(dev):
-        code = _abi.load().dsa_idx_paged_attention(
-            qp, qst, *a, N, ps, H, Hk, D, _PREC[cache.prec], table, width, cq, ck, B, T, max_seqlen_q, max_seqlen_k,
-            D ** -0.5 if sm_scale is None else sm_scale, ip, lp, W, op, lsep, wp, ws.numel(), _stream(dev.index))
+    code = _call(_abi.load().dsa_idx_paged_attention, dev, (
+        qp, qst, *a, N, ps, H, Hk, D, _PREC[cache.prec], table, width, cq, ck, B, T, max_seqlen_q, max_seqlen_k,
+        D ** -0.5 if sm_scale is None else sm_scale, ip, lp, W, op, lsep, wp, ws.numel()))
     if code:
         raise _error(code, "dsa_idx_paged_attention")
     return (out, lse) if return_lse else out
