@@ -7,9 +7,11 @@
 //
 // A row is handled by D / 8 consecutive lanes, eight elements each, so a lane
 // moves 16 bytes of BF16 and an E4M3 row of 128 is one full line.  A warp takes
-// kUnroll steps of consecutive (token, head) rows at a time and requests all of
-// them before it looks up where they go, so the loads and the page lookups
-// overlap.  Keys and values are two halves of one row range: one launch.
+// consecutive tokens of one head: their rows, and their scales, are neighbours in
+// a page.  (Token by token, eight heads a warp, the rows of a line's neighbours
+// came from other blocks: 62 against 43 us for 32768 tokens x 8 heads x 128 of K
+// and V into MXFP8.)  U steps of rows are requested before it is looked up where
+// they go; where is looked up once per page.  Keys and values are one launch.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -22,17 +24,27 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
 
-// Position of a packed row's token: the sequence it was in last time, or a
-// search when it has left it.
-struct SeqCursor {
-  int d = -1, lo = 0, hi = 0;   // rows [lo, hi) of sequence d
-  __device__ __forceinline__ void seek(const int32_t* cu, int num_seqs, int t) {
-    if (d >= 0 && t >= lo && t < hi) return;
-    d = find_seq(cu, num_seqs, t);
-    lo = __ldg(cu + d);
-    hi = __ldg(cu + d + 1);
+// Where packed tokens' rows are in the cache, looked up once per page.
+struct Place {
+  int lo = 0, hi = -1;   // packed tokens [lo, hi): of one sequence and in one page
+  int64_t base = -1;     // cache row of token lo, head 0; -1: not there
+  bool fits = true;      // false: the sequence or the page does not fit (reported)
+  // cu packs the tokens; TAIL: they are the last of the sequence's positions in cu_k.
+  template <bool TAIL>
+  __device__ __forceinline__ void seek(const PagedCacheView& c, const int32_t* cu, const int32_t* cu_k, int num_seqs, int t) {
+    if (t >= lo && t < hi) return;
+    const int d = find_seq(cu, num_seqs, t);
+    const int s0 = __ldg(cu + d), s1 = __ldg(cu + d + 1);
+    lo = t;
+    hi = t + 1;
+    base = -1;
+    fits = true;
+    if (t < s0 || t >= s1) return;   // behind the last sequence: left alone
+    const int first = TAIL ? __ldg(cu_k + d + 1) - __ldg(cu_k + d) - (s1 - s0) : 0;
+    if (first >= 0) base = cache_row(c, d, first + (t - s0), 0);   // else more new tokens than cached ones
+    fits = base >= 0;
+    if (fits) hi = min(s1, t + (1 << c.page_shift) - ((first + (t - s0)) & ((1 << c.page_shift) - 1)));
   }
 };
 
@@ -86,48 +98,38 @@ __device__ __forceinline__ uint2 quant8(const float (&x)[8], uint32_t carry, int
 }
 
 // FMT: 0 BF16, 1 MXFP8, 2 FP8 (dsa_precision_t).  SRC: 0 FP32, 1 BF16, 2 codes.
-template <int D, int FMT, int SRC>
+template <int D, int FMT, int SRC, int U>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteParams p) {
   constexpr int LPR = D / 8;          // lanes per row
-  constexpr int RPS = 32 / LPR;       // rows per warp step
+  constexpr int RPS = 32 / LPR;       // rows per step
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, li = lane % LPR;
-  const uint32_t n_kv = p.c.n_kv;               // rows stay below 2^31 (checked by the caller)
-  const uint32_t half = p.total_q * n_kv;
-  const uint32_t rows = p.v ? 2 * half : half;
+  const uint32_t n_kv = p.c.n_kv, heads = p.v ? 2 * n_kv : n_kv;   // key heads, then value heads
+  const uint32_t items = ((p.total_q + RPS * U - 1) / (RPS * U)) * heads;   // below 2^31 (checked by the caller)
   const uint32_t carry = mx_carry(p.rule);
-  const uint32_t step = gridDim.x * (kThreads / 32) * (RPS * kUnroll);
   bool bad = blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.cu_q + p.num_seqs) > p.total_q;
-  SeqCursor cur;
-  for (uint32_t r0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * (RPS * kUnroll); r0 < rows;
-       r0 += step) {
-    Piece<SRC> x[kUnroll];
+  Place at;
+  for (uint32_t it = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += gridDim.x * (kThreads / 32)) {
+    const uint32_t block = it / heads, hh = it - block * heads;
+    const bool isv = hh >= n_kv;
+    const uint32_t h = isv ? hh - n_kv : hh;
+    const void* src = isv ? p.v : p.k;
+    const int64_t stride = isv ? p.v_stride : p.k_stride;
+    const int t0 = (int)(block * (RPS * U)) + sub;
+    Piece<SRC> x[U];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t r = r0 + u * RPS + sub;
+    for (int u = 0; u < U; ++u) {
       x[u] = Piece<SRC>{};
-      if (r < rows) {
-        const bool isv = r >= half;
-        const uint32_t rr = isv ? r - half : r;
-        const uint32_t t = rr / n_kv, h = rr - t * n_kv;
-        load_piece<SRC>(x[u], isv ? p.v : p.k, (int64_t)t * (isv ? p.v_stride : p.k_stride) + (int)(h * D + li * 8));
-      }
+      if (t0 + u * RPS < p.total_q) load_piece<SRC>(x[u], src, (t0 + u * RPS) * stride + (int)(h * D + li * 8));
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t r = r0 + u * RPS + sub;
-      const bool isv = r >= half;
-      const uint32_t rr = isv ? r - half : r;
-      const int t = (int)(rr / n_kv), h = (int)(rr - (uint32_t)t * n_kv);
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * RPS;
       int64_t row = -1;
-      if (r < rows) {
-        cur.seek(p.cu_q, p.num_seqs, t);
-        if (t >= cur.lo && t < cur.hi) {   // rows behind the last sequence are left alone
-          const int s = __ldg(p.cu_k + cur.d + 1) - __ldg(p.cu_k + cur.d);
-          row = cache_row(p.c, cur.d, s - (cur.hi - t), h);
-          if (s < cur.hi - cur.lo) row = -1;   // more new tokens than cached ones
-          bad |= row < 0;
-        }
+      if (t < p.total_q) {
+        at.seek<true>(p.c, p.cu_q, p.cu_k, p.num_seqs, t);
+        bad |= !at.fits;
+        if (at.base >= 0) row = at.base + (t - at.lo) + ((int64_t)h << p.c.page_shift);
       }
       uint8_t* dst = reinterpret_cast<uint8_t*>(isv ? p.c.v : p.c.k);
       uint8_t* dsc = isv ? p.c.v_scale : p.c.k_scale;
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
         if (row >= 0) {
           *reinterpret_cast<uint2*>(dst + row * D + li * 8) = x[u].codes;
           constexpr int SW = FMT == 1 ? D / 32 : 1;
-          if (li < SW) dsc[row * SW + li] = __ldg((isv ? p.v_scale : p.k_scale) + (size_t)rr * SW + li);
+          if (li < SW) dsc[row * SW + li] = __ldg((isv ? p.v_scale : p.k_scale) + ((size_t)t * n_kv + h) * SW + li);
         }
       } else {
         constexpr int GL = FMT == 1 ? 4 : LPR;
@@ -161,8 +163,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
   if (threadIdx.x == 0) put_block_status(p.hdr, any ? DSA_DEV_ERR_INVALID_ARG : 0);
 }
 
-// Rows of ROWB bytes (stored) copied 16 bytes a lane.
-template <int D, int FMT, bool DEQ>
+template <int D, int FMT, bool DEQ, int U>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadParams p) {
   constexpr int ESZ = FMT == 0 ? 2 : 1;
   constexpr int BPL = DEQ ? 8 : 16;           // stored bytes per lane: eight codes widen to 16 bytes
@@ -171,62 +172,55 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
   constexpr int SW = FMT == 1 ? D / 32 : (FMT == 2 ? 1 : 0);
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, li = lane % LPR;
-  const uint32_t n_kv = p.c.n_kv;               // rows stay below 2^31 (checked by the caller)
-  const uint32_t half = p.total_k * n_kv;
-  const uint32_t rows = p.v ? 2 * half : half;
-  const uint32_t step = gridDim.x * (kThreads / 32) * (RPS * kUnroll);
+  const uint32_t n_kv = p.c.n_kv, heads = p.v ? 2 * n_kv : n_kv;   // key heads, then value heads
+  const uint32_t items = ((p.total_k + RPS * U - 1) / (RPS * U)) * heads;   // below 2^31 (checked by the caller)
   bool bad = blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.cu_k + p.num_seqs) > p.total_k;
-  SeqCursor cur;
-  for (uint32_t r0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * (RPS * kUnroll); r0 < rows;
-       r0 += step) {
-    uint4 x[kUnroll];
-    uint32_t sc[kUnroll];
-    bool ok[kUnroll];
+  Place at;
+  for (uint32_t it = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += gridDim.x * (kThreads / 32)) {
+    const uint32_t block = it / heads, hh = it - block * heads;
+    const bool isv = hh >= n_kv;
+    const uint32_t h = isv ? hh - n_kv : hh;
+    const uint8_t* pages = reinterpret_cast<const uint8_t*>(isv ? p.c.v : p.c.k) + li * BPL;
+    const uint8_t* page_scales = isv ? p.c.v_scale : p.c.k_scale;
+    const int t0 = (int)(block * (RPS * U)) + sub;
+    uint4 x[U];
+    uint32_t sc[U];
+    bool ok[U];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t r = r0 + u * RPS + sub;
-      const bool isv = r >= half;
-      const uint32_t rr = isv ? r - half : r;
-      const int t = (int)(rr / n_kv), h = (int)(rr - (uint32_t)t * n_kv);
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * RPS;
       ok[u] = false;
       x[u] = make_uint4(0, 0, 0, 0);
       sc[u] = 0;
-      if (r < rows) {
-        cur.seek(p.cu_k, p.num_seqs, t);
-        if (t >= cur.lo && t < cur.hi) {
-          const int64_t row = cache_row(p.c, cur.d, t - cur.lo, h);
-          if (row < 0) {
-            bad = true;
-          } else {
-            ok[u] = true;
-            const uint8_t* src = reinterpret_cast<const uint8_t*>(isv ? p.c.v : p.c.k) + row * (D * ESZ) + li * BPL;
-            const uint8_t* ssc = isv ? p.c.v_scale : p.c.k_scale;
-            if constexpr (BPL == 16) {
-              x[u] = __ldg(reinterpret_cast<const uint4*>(src));
-              if constexpr (SW > 0) {
-                if (li < SW) sc[u] = __ldg(ssc + row * SW + li);
-              }
-            } else {
-              const uint2 c = __ldg(reinterpret_cast<const uint2*>(src));
-              x[u].x = c.x;
-              x[u].y = c.y;
-              sc[u] = __ldg(ssc + row * SW + (SW > 1 ? li / 4 : 0));
+      if (t < p.total_k) {
+        at.seek<false>(p.c, p.cu_k, p.cu_k, p.num_seqs, t);
+        bad |= !at.fits;
+        if (at.base >= 0) {
+          const int64_t row = at.base + (t - at.lo) + ((int64_t)h << p.c.page_shift);
+          ok[u] = true;
+          if constexpr (BPL == 16) {
+            x[u] = __ldg(reinterpret_cast<const uint4*>(pages + row * (D * ESZ)));
+            if constexpr (SW > 0) {
+              if (li < SW) sc[u] = __ldg(page_scales + row * SW + li);
             }
+          } else {
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(pages + row * (D * ESZ)));
+            x[u].x = c.x;
+            x[u].y = c.y;
+            sc[u] = __ldg(page_scales + row * SW + (SW > 1 ? li / 4 : 0));
           }
         }
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       if (!ok[u]) continue;
-      const uint32_t r = r0 + u * RPS + sub;
-      const bool isv = r >= half;
-      const uint32_t rr = isv ? r - half : r;
+      const size_t rr = (size_t)(t0 + u * RPS) * n_kv + h;
       uint8_t* dst = reinterpret_cast<uint8_t*>(isv ? p.v : p.k);
       if constexpr (!DEQ) {
-        *reinterpret_cast<uint4*>(dst + (size_t)rr * (D * ESZ) + li * 16) = x[u];
+        *reinterpret_cast<uint4*>(dst + rr * (D * ESZ) + li * 16) = x[u];
         if constexpr (SW > 0) {
-          if (li < SW) (isv ? p.v_scale : p.k_scale)[(size_t)rr * SW + li] = (uint8_t)sc[u];
+          if (li < SW) (isv ? p.v_scale : p.k_scale)[rr * SW + li] = (uint8_t)sc[u];
         }
       } else {
         // code * 2^e is exact in FP32, and in BF16 unless it is below BF16's range
@@ -240,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
           const __nv_bfloat162 b = __floats2bfloat162_rn(v.x * f, v.y * f);
           reinterpret_cast<uint32_t*>(&o)[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        *reinterpret_cast<uint4*>(dst + ((size_t)rr * D + li * 8) * 2) = o;
+        *reinterpret_cast<uint4*>(dst + (rr * D + li * 8) * 2) = o;
       }
     }
   }
@@ -248,55 +242,77 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
   if (threadIdx.x == 0) put_block_status(p.hdr, any ? DSA_DEV_ERR_INVALID_ARG : 0);
 }
 
-// Blocks for `rows` rows at `rps` rows a block, at most eight per SM (the
-// header has a status word for each).
-unsigned blocks_for(int64_t rows, int rows_per_block, int sm_count) {
-  int64_t b = (rows + rows_per_block - 1) / rows_per_block;
-  int64_t cap = (int64_t)sm_count * 8;
+// Blocks for `items` warp items, at most twelve per SM (the header has a status
+// word for each).
+unsigned blocks_for(int64_t items, int sm_count) {
+  int64_t b = (items + kThreads / 32 - 1) / (kThreads / 32);
+  int64_t cap = (int64_t)sm_count * 12;
   if (cap > DSA_DEV_STATUS_MAX_BLOCKS) cap = DSA_DEV_STATUS_MAX_BLOCKS;
   if (b > cap) b = cap;
   return (unsigned)(b < 1 ? 1 : b);
 }
 
+// Steps of rows a warp requests at once: four, and one where four would leave SMs
+// without work (the lookups of a few tokens then run side by side).
+constexpr int kUnroll = 4;
+bool few(int64_t steps, int sm_count) { return steps < (int64_t)sm_count * (kThreads / 32) * kUnroll; }
+
+template <int D, int FMT, int SRC>
+void write_u(const CacheWriteParams& p, int sm_count, cudaStream_t st) {
+  constexpr int RPS = 32 / (D / 8);
+  const int64_t heads = (int64_t)p.c.n_kv * (p.v ? 2 : 1), steps = ((int64_t)p.total_q + RPS - 1) / RPS;
+  if (few(steps * heads, sm_count))
+    cache_write_kernel<D, FMT, SRC, 1><<<blocks_for(steps * heads, sm_count), kThreads, 0, st>>>(p);
+  else
+    cache_write_kernel<D, FMT, SRC, kUnroll>
+        <<<blocks_for((steps + kUnroll - 1) / kUnroll * heads, sm_count), kThreads, 0, st>>>(p);
+}
+
 template <int D, int FMT>
-void write_src(const CacheWriteParams& p, unsigned blocks, cudaStream_t st) {
-  if (p.src == 0) cache_write_kernel<D, FMT, 0><<<blocks, kThreads, 0, st>>>(p);
-  else if (p.src == 1) cache_write_kernel<D, FMT, 1><<<blocks, kThreads, 0, st>>>(p);
-  else if constexpr (FMT != 0) cache_write_kernel<D, FMT, 2><<<blocks, kThreads, 0, st>>>(p);
+void write_src(const CacheWriteParams& p, int sm_count, cudaStream_t st) {
+  if (p.src == 0) write_u<D, FMT, 0>(p, sm_count, st);
+  else if (p.src == 1) write_u<D, FMT, 1>(p, sm_count, st);
+  else if constexpr (FMT != 0) write_u<D, FMT, 2>(p, sm_count, st);
 }
 
 template <int D>
-void write_fmt(const CacheWriteParams& p, unsigned blocks, cudaStream_t st) {
-  if (p.c.fmt == 0) write_src<D, 0>(p, blocks, st);
-  else if (p.c.fmt == 1) write_src<D, 1>(p, blocks, st);
-  else write_src<D, 2>(p, blocks, st);
+void write_fmt(const CacheWriteParams& p, int sm_count, cudaStream_t st) {
+  if (p.c.fmt == 0) write_src<D, 0>(p, sm_count, st);
+  else if (p.c.fmt == 1) write_src<D, 1>(p, sm_count, st);
+  else write_src<D, 2>(p, sm_count, st);
+}
+
+template <int D, int FMT, bool DEQ>
+void read_u(const CacheReadParams& p, int sm_count, cudaStream_t st) {
+  constexpr int RPS = 32 / (D * (FMT == 0 ? 2 : 1) / (DEQ ? 8 : 16));
+  const int64_t heads = (int64_t)p.c.n_kv * (p.v ? 2 : 1), steps = ((int64_t)p.total_k + RPS - 1) / RPS;
+  if (few(steps * heads, sm_count))
+    cache_read_kernel<D, FMT, DEQ, 1><<<blocks_for(steps * heads, sm_count), kThreads, 0, st>>>(p);
+  else
+    cache_read_kernel<D, FMT, DEQ, kUnroll>
+        <<<blocks_for((steps + kUnroll - 1) / kUnroll * heads, sm_count), kThreads, 0, st>>>(p);
 }
 
 template <int D>
-void read_fmt(const CacheReadParams& p, unsigned blocks, cudaStream_t st) {
-  if (p.c.fmt == 0) cache_read_kernel<D, 0, false><<<blocks, kThreads, 0, st>>>(p);
-  else if (p.c.fmt == 1 && p.dequant) cache_read_kernel<D, 1, true><<<blocks, kThreads, 0, st>>>(p);
-  else if (p.c.fmt == 1) cache_read_kernel<D, 1, false><<<blocks, kThreads, 0, st>>>(p);
-  else if (p.dequant) cache_read_kernel<D, 2, true><<<blocks, kThreads, 0, st>>>(p);
-  else cache_read_kernel<D, 2, false><<<blocks, kThreads, 0, st>>>(p);
+void read_fmt(const CacheReadParams& p, int sm_count, cudaStream_t st) {
+  if (p.c.fmt == 0) read_u<D, 0, false>(p, sm_count, st);
+  else if (p.c.fmt == 1 && p.dequant) read_u<D, 1, true>(p, sm_count, st);
+  else if (p.c.fmt == 1) read_u<D, 1, false>(p, sm_count, st);
+  else if (p.dequant) read_u<D, 2, true>(p, sm_count, st);
+  else read_u<D, 2, false>(p, sm_count, st);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_write(const CacheWriteParams& p, int D, int sm_count, cudaStream_t stream) {
-  const int64_t rows = (int64_t)p.total_q * p.c.n_kv * (p.v ? 2 : 1);
-  const unsigned blocks = blocks_for(rows, kThreads / (D / 8) * kUnroll, sm_count);
-  if (D == 128) write_fmt<128>(p, blocks, stream);
-  else write_fmt<64>(p, blocks, stream);
+  if (D == 128) write_fmt<128>(p, sm_count, stream);
+  else write_fmt<64>(p, sm_count, stream);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const CacheReadParams& p, int D, int sm_count, cudaStream_t stream) {
-  const int64_t rows = (int64_t)p.total_k * p.c.n_kv * (p.v ? 2 : 1);
-  const int lanes = p.c.fmt == 0 || p.dequant ? D / 8 : D / 16;
-  const unsigned blocks = blocks_for(rows, kThreads / lanes * kUnroll, sm_count);
-  if (D == 128) read_fmt<128>(p, blocks, stream);
-  else read_fmt<64>(p, blocks, stream);
+  if (D == 128) read_fmt<128>(p, sm_count, stream);
+  else read_fmt<64>(p, sm_count, stream);
   return cudaGetLastError();
 }
 
