@@ -412,8 +412,10 @@ dsa_status_t dsa_idx_cache_read(
     int dequantize, void* k_out, uint8_t* k_scale_out, void* v_out,
     uint8_t* v_scale_out, void* ws, size_t ws_bytes, dsa_stream_t stream);
 
-/* Workspace bytes of dsa_idx_paged_attention for these sizes (status, partial
- * results of long key ranges).  0 for invalid sizes. */
+/* Workspace bytes of dsa_idx_paged_attention (status, partial results of long
+ * key ranges), enough for every call of at most total_q, num_seqs and
+ * max_seqlen_q with these heads and a topk_width that is 0, or not, as here.
+ * 0 for invalid sizes. */
 size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqlen_q, int n_heads,
                                         int n_kv_heads, int head_dim, int topk_width);
 
@@ -435,9 +437,12 @@ size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqle
  * A query that sees no key gets out = 0 and lse = -inf.  sm_scale is finite and
  * not negative; n_heads a multiple of n_kv_heads, at most 128 heads to one;
  * max_seqlen_q and max_seqlen_k bound T_d and S_d (a longer sequence is
- * reported in the status and not computed).  Rows 0 .. S_d - 1 of a sequence
- * must be finite; what other slots of its pages hold does not matter.
- * The same inputs give the same bits. */
+ * reported in the status and not computed; nothing is computed when
+ * cu_seqlens_q falls).  Rows 0 .. S_d - 1 of a sequence (with topk_idx: the
+ * listed ones) must be finite; what other slots of its pages hold does not
+ * matter.  out and lse share no memory with the inputs.  total_q * n_heads <
+ * 2^30, max_seqlen_k and topk_width at most 2^30.  With total_q = 0 topk_idx
+ * may be NULL whatever topk_width is.  The same inputs give the same bits. */
 dsa_status_t dsa_idx_paged_attention(
     const void* q, int64_t q_stride, const void* k_pages,
     const uint8_t* k_page_scale, const void* v_pages,

@@ -66,6 +66,15 @@ dsa_status_t check_stride(int64_t* stride, int heads, int head_dim, int elem_byt
 uint32_t round16(uint32_t x) { return (x + 15) / 16 * 16; }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Streams of a launch, and units of one query tile (or pair) up to which key ranges are divided.
+int64_t all_streams(bool pair) { return pair ? kAttnSms : 2 * kAttnSms; }
+int64_t most_undivided(bool pair) { return (pair ? 2 : 4) * all_streams(pair); }
+
+// Workspace bytes with `slots` rows of partial results.
+size_t with_partials(int num_seqs, size_t slots, int D) {
+  return DSA_DEV_STATUS_HEADER_BYTES + round256((size_t)num_seqs * 4) + round256(slots * 8) + round256(slots * D * 4);
+}
+
 }  // namespace
 
 namespace dsa {
@@ -91,9 +100,8 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   int64_t tiles = (int64_t)total_q / per + num_seqs;
   if (tiles > total_q) tiles = total_q;
   const int64_t base = tiles * n_kv;
-  const int64_t streams = pl->pair ? kAttnSms : 2 * kAttnSms;
-  const int64_t few = pl->pair ? 2 : 4;
-  pl->max_units = base <= few * streams ? (int)(base + few * streams) : 0;
+  const int64_t most = most_undivided(pl->pair);
+  pl->max_units = base <= most ? (int)(base + most) : 0;
   const int qrows = pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
   pl->q_bytes = (uint32_t)qrows * D * 2;
   const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys * D + 512;
@@ -128,12 +136,8 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
 }
 
 size_t attn_workspace_bytes(const AttnPlan& pl, int num_seqs, int D) {
-  size_t n = DSA_DEV_STATUS_HEADER_BYTES;
-  if (pl.max_units > 0) {
-    const size_t slots = (size_t)pl.max_units * (pl.pair ? 2 : 1) * pl.rows_cap;
-    n += round256((size_t)num_seqs * 4) + round256(slots * 8) + round256(slots * D * 4);
-  }
-  return n;
+  if (pl.max_units == 0) return DSA_DEV_STATUS_HEADER_BYTES;
+  return with_partials(num_seqs, (size_t)pl.max_units * (pl.pair ? 2 : 1) * pl.rows_cap, D);
 }
 
 }  // namespace dsa
@@ -234,16 +238,21 @@ size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqle
   if (total_q < 0 || num_seqs < 1 || max_seqlen_q < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 ||
       n_heads / n_kv_heads > kAttnRows || (head_dim != 64 && head_dim != 128) || topk_width < 0)
     return 0;
-  // the largest of the cache's formats
-  size_t most = 0;
-  for (int sw : {0, 1, head_dim / 32})
-    for (int page_size : {8, 64}) {
-      AttnPlan pl;
-      if (!attn_plan(&pl, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, sw, page_size, topk_width)) return 0;
-      const size_t n = attn_workspace_bytes(pl, num_seqs, head_dim);
-      most = n > most ? n : most;
-    }
-  return most;
+  // The most that attn_plan asks for at any format and at any sizes up to these: fewer tokens may need
+  // more, as the key ranges of many tiles are not divided.
+  const int group = n_heads / n_kv_heads, tq = topk_width > 0 ? 1 : kAttnRows / group;
+  const int tok = max_seqlen_q < 1 ? 1 : (max_seqlen_q < tq ? max_seqlen_q : tq);
+  size_t slots = 0;
+  for (bool pair : {false, true}) {
+    if (pair && (topk_width > 0 || max_seqlen_q <= tq)) continue;
+    int64_t tiles = (int64_t)total_q / (pair ? 2 * tq : tq) + num_seqs;
+    if (tiles > total_q) tiles = total_q;
+    int64_t base = tiles * n_kv_heads;
+    if (base > most_undivided(pair)) base = most_undivided(pair);
+    const size_t n = (size_t)(base + most_undivided(pair)) * (pair ? 2 : 1) * (size_t)(tok * group);
+    slots = n > slots ? n : slots;
+  }
+  return with_partials(num_seqs, slots, head_dim);
 }
 
 dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void* k_pages, const uint8_t* k_page_scale,
@@ -262,9 +271,13 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
   if (total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0) return fail(DSA_ERR_INVALID_ARG, "sizes");
   if (n_heads < 1 || n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 128)
     return fail(DSA_ERR_UNSUPPORTED, "n_heads must be a multiple of n_kv_heads, at most 128 heads to one");
-  if ((int64_t)total_q * n_heads >= (int64_t)1 << 31) return fail(DSA_ERR_UNSUPPORTED, "total_q * n_heads above 2^31");
+  if ((int64_t)total_q * n_heads >= (int64_t)1 << 30) return fail(DSA_ERR_UNSUPPORTED, "total_q * n_heads above 2^30");
+  // (key tiles are counted in 32 bits)
+  if (max_seqlen_k > (1 << 30) || topk_width > (1 << 30))
+    return fail(DSA_ERR_UNSUPPORTED, "max_seqlen_k and topk_width are at most 2^30");
   if (!(sm_scale >= 0.f) || std::isinf(sm_scale)) return fail(DSA_ERR_INVALID_ARG, "sm_scale must be finite and >= 0");
-  if (topk_idx ? topk_width < 1 : (topk_width != 0 || topk_len != nullptr))
+  // (an empty list tensor has no address)
+  if (topk_width < 0 || (topk_idx && topk_width < 1) || (!topk_idx && total_q > 0 && (topk_width > 0 || topk_len)))
     return fail(DSA_ERR_INVALID_ARG, "topk_width and topk_len belong to topk_idx");
   if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if ((s = check_stride(&q_stride, n_heads, head_dim, 2, "q")) != DSA_OK) return s;

@@ -302,8 +302,9 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&w)[4]) {
 enum { PAIR = 0, SOLO = 1, GATHER = 2 };
 
 // Warps: 8 softmax; workers (16, or 12 of gathered rows, widen 8-bit tiles; 8 bring gathered BF16
-// rows); 4 that bring gathered 8-bit rows; the rest: key loaders (TMA), query loaders, MMA 0 and 1 last.  (The four warps of an SM's sub-partition
-// are those of equal number modulo 4; loaders and MMA warps are kept on different ones.)
+// rows); 4 that bring gathered 8-bit rows; the rest: key loaders (TMA), query loaders, MMA 0 and 1
+// last.  (The four warps of an SM's sub-partition are those of equal number modulo 4; loaders and MMA
+// warps are kept on different ones.)
 template <bool Q8, int MODE>
 struct Roles {
   static constexpr int kWorkWarps = MODE == GATHER ? (Q8 ? 12 : 8) : (Q8 ? 16 : 0);
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     ctl[4] = 0;
     for (int r = 0; r < kRings; ++r) {
       for (int s = 0; s < pl.nst; ++s) {
-        mbar_init(bar_full(r, s), R::kWorkWarps > 0 ? kLoaders : 1);
+        mbar_init(bar_full(r, s), R::kWorkWarps > 0 ? kLoaders + (kWorkerCopies ? R::kWorkWarps / 2 : 0) : 1);
         mbar_init(bar_empty(r, s), kPair ? 2 : 1);
       }
       for (int s = 0; s < pl.nraw; ++s) {
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     long long work = 0;
     int kmax = 0;
     bool bad = tid == 0 && (__ldg(p.cu_q + p.num_seqs) > p.total_q);
+    bool broken = false;   // cu_q falls: tokens could count for several sequences, so nothing is computed
     if (tid < kGroups) {
       for (int i = 0; i < gsz; ++i) {
         const int d = tid * gsz + i;
@@ -396,6 +398,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         Doc o;
         int mt, kt;
         bad |= !doc_info(p, d, &o);
+        broken |= __ldg(p.cu_q + d) < 0 || __ldg(p.cu_q + d + 1) < __ldg(p.cu_q + d);
         doc_tiles<kPair>(p, o, &mt, &kt);
         work += (long long)mt * kt * p.c.n_kv;
         if (mt > 0) kmax = max(kmax, kt);
@@ -413,10 +416,11 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     }
     const int any_bad = __syncthreads_or(bad);
     if (any_bad && tid == 0) set_status(status, DSA_DEV_ERR_INVALID_ARG);
+    const bool none = any_bad && __syncthreads_or(broken);
     wsum = red[0] + red[1];
     kmax = (int)fmaxf(red[4], red[5]);
-    int chunk = max(kmax, 1);
-    if (pl.max_units > 0 && kmax > kAttnMinChunk) {
+    int chunk = none ? 0x7FFFFFFF : max(kmax, 1);
+    if (pl.max_units > 0 && !none && kmax > kAttnMinChunk) {
       int cand[8];
       int units[8];
 #pragma unroll
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       }
     }
     int mine = 0;
-    if (tid < kGroups) {
+    if (tid < kGroups && !none) {
       for (int i = 0; i < gsz; ++i) {
         const int d = tid * gsz + i;
         if (d >= p.num_seqs) break;
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       for (int i = 0; i < warp; ++i) before += reinterpret_cast<int*>(red)[8 + i];
       tab[tid] = before;
       if (tid == kGroups - 1) tab[kGroups] = before + mine;
-      if (blockIdx.x == 0 && pl.max_units > 0) {   // for the joining kernel
+      if (blockIdx.x == 0 && pl.max_units > 0 && !none) {   // for the joining kernel
         for (int i = 0; i < gsz; ++i) {
           const int d = tid * gsz + i;
           if (d >= p.num_seqs) break;
@@ -743,7 +747,10 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
             const bool there = e != ~0u;
             cp_async16(dst + i * 128 + (((c & 7) ^ ((i + rsub) & 7)) << 4), src + (size_t)(there ? e : 0) * D, there);
           }
-          if (p.fault_inject != 1 || t > 0 || kv > 0) cp_arrive(bar_full(ring, st));   // (the tests' withheld first stage)
+          if (p.fault_inject != 1 || t > 0 || kv > 0) {   // (the tests' withheld first stage)
+            if (lane == 0) mbar_arrive(bar_full(ring, st));   // the mask
+            cp_arrive(bar_full(ring, st));                    // the rows, when they have landed
+          }
           advance();
         }
         ++t;
@@ -812,6 +819,14 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     // Every visible key of a BF16 cache: TMA, a box per page, issued by one warp.  The unit's last
     // tile may end inside a page whose other slots hold anything: the warp copies that one row by
     // row, with zeros behind the last visible key.
+    // After an abort a loader waits (again with a limit) for the copies it has in flight: the last use
+    // of every stage, those from st on being of the round before.
+    auto drain_ring = [&](auto bar, int ring, int count, int st, uint32_t ph, bool wrapped) {
+      if (lane == 0) {
+        for (int s = 0; s < (wrapped ? count : st); ++s) drain_wait(bar(ring, s), s < st ? ph : ph ^ 1u, tmo);
+      }
+      __syncwarp();
+    };
     auto load_tma = [&](int ring) {
       const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
       const int shift = p.c.page_shift;
@@ -839,7 +854,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           if (whole && lane < boxes && !good) bad_page = true;
           for (int kv = 0; kv < 2; ++kv) {
             if (wrapped && !__all_sync(0xffffffffu, wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo))) {
-              cp_wait_all();
+              drain_ring(bar_full, ring, pl.nst, st, ph, wrapped);
               return;
             }
             const uint32_t dst = ring_base + (uint32_t)st * kStage;
@@ -882,6 +897,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           }
         }
       }
+      if (*abort_flag) drain_ring(bar_full, ring, pl.nst, st, ph, wrapped);
       if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
     };
     // Every visible key of an 8-bit cache, as stored: tiles of codes (a TMA box per page) and their
@@ -915,6 +931,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
             if (wrapped &&
                 !__all_sync(0xffffffffu, wait_bar(bar_raw_empty(ring, slot), rph ^ 1u, abort_flag, status, tmo))) {
               cp_wait_all();
+              drain_ring(bar_raw_full, ring, pl.nraw, slot, rph, wrapped);
               return;
             }
             const uint32_t bar = bar_raw_full(ring, slot), dst = raw_base + (uint32_t)slot * kRawItem;
@@ -941,14 +958,18 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           }
           if (!kPair && j == 0) {
             if (nq > 0 &&
-                !__all_sync(0xffffffffu, wait_bar(bar_st(ring, Q_EMPTY), (nq - 1) & 1u, abort_flag, status, tmo)))
-              break;
+                !__all_sync(0xffffffffu, wait_bar(bar_st(ring, Q_EMPTY), (nq - 1) & 1u, abort_flag, status, tmo))) {
+              cp_wait_all();
+              drain_ring(bar_raw_full, ring, pl.nraw, slot, rph, wrapped);
+              return;
+            }
             ++nq;
             load_q(x, ring);
           }
         }
       }
       cp_wait_all();
+      if (*abort_flag) drain_ring(bar_raw_full, ring, pl.nraw, slot, rph, wrapped);
       if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
     };
     // Query tiles of streams w0 .. w1 - 1, each as soon as its stream's last product with the one before is done.
@@ -992,10 +1013,10 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         // The streams issue PV and the next QK as one block, in turns: their softmax phases then
         // alternate with the other's products.  Left to themselves both streams' products queue
         // up together, and so do the softmax phases (5300 against 3300 cycles per key tile).
-        // Nothing is waited for inside a turn, so a turn always comes.
+        // Nothing is waited for inside a turn, so a turn always comes; only the times depend on it.
         int* const turn = ctl + 4;
         auto take_turn = [&] {
-          while (atomicCAS_block(turn, 0, 1) != 0) {
+          for (int i = 0; i < (1 << 20) && atomicCAS_block(turn, 0, 1) != 0; ++i) {
           }
         };
         auto end_turn = [&] { atomicExch_block(turn, 0); };

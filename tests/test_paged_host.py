@@ -126,3 +126,32 @@ def test_reference_forms_agree_with_themselves():
             pg = b.table[d, pos // 8]
             got = values(b.pages["v"][pg, :, pos % 8], b.scales["v"][pg, :, pos % 8], "fp8")
             np.testing.assert_array_equal(got, b.rows["v"][b.cu_k[d] + pos])
+
+
+@pytest.mark.parametrize("kw", [dict(max_k=(1 << 30) + 1), dict(idx=A, W=(1 << 30) + 1), dict(total_q=1 << 26)])
+def test_attention_counts_in_32_bits(lib, kw):
+    assert _attend(lib, **kw) == 2
+
+
+def test_an_empty_list_tensor_is_no_error(lib):
+    """total_q = 0: a list of no rows has no address (what is left to fail here is the missing device)."""
+    assert _attend(lib, total_q=0, q=None, out=None, idx=None, W=4) not in (1, 2, 4)
+    assert _attend(lib, total_q=0, q=None, out=None, idx=None, W=-1) == 1
+    assert _attend(lib, total_q=4, idx=None, W=4) == 1
+
+
+def test_a_workspace_serves_smaller_calls(lib):
+    rng = np.random.default_rng(7)
+    size = lib.dsa_idx_attention_workspace_size
+    for _ in range(300):
+        kv, group, D = int(rng.integers(1, 9)), int(rng.integers(1, 129)), int(rng.choice([64, 128]))
+        W = int(rng.choice([0, 0, 64, 2048]))
+        total = [int(2 ** rng.uniform(0, 16)) for _ in range(2)]
+        seqs = [int(2 ** rng.uniform(0, 9)) for _ in range(2)]
+        mq = [int(2 ** rng.uniform(0, 14)) for _ in range(2)]
+        n = size(max(total), max(seqs), max(mq), kv * group, kv, D, W)
+        for total_q, s, q in ((total[0], seqs[0], mq[0]), (max(total), max(seqs), max(mq)), (min(total), max(seqs), 1)):
+            for prec in (0, 1, 2):
+                code = _attend(lib, H=kv * group, kv=kv, D=D, prec=prec, seqs=s, total_q=total_q, max_q=q, max_k=1 << 20,
+                               idx=A if W else None, W=W, ws_bytes=n)
+                assert code not in (1, 2, 4), (kv, group, D, W, total_q, s, q, prec)
