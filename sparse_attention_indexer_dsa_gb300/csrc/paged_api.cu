@@ -102,14 +102,16 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   const int64_t base = tiles * n_kv;
   const int64_t most = most_undivided(pl->pair);
   pl->max_units = base <= most ? (int)(base + most) : 0;
-  const int qrows = pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
+  pl->narrow = !pl->pair && D == 128 && pl->rows_cap <= kAttnNarrow;
+  const int qrows = pl->narrow ? kAttnNarrow : pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
   pl->q_bytes = (uint32_t)qrows * D * 2;
   const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys * D + 512;
   for (pl->streams = 2; pl->streams >= 1; --pl->streams) {
     const uint32_t rings = pl->pair ? 1 : pl->streams;
     const uint32_t rows = 64;   // visible rows of a stored tile
-    const uint32_t mask = pl->gather ? 2 * 8 * 4 * 4 : 0, bars = 8 * (2 * 32 + 2 * 6) + 32, tab = round16((64 + 1) * 4);
-    const uint32_t q = 2 * pl->q_bytes, tail = rows + mask + bars + tab;
+    const uint32_t mask = pl->gather ? 2 * 8 * 4 * 4 : 0, bars = 8 * kAttnBars + 32, tab = round16((64 + 1) * 4);
+    const uint32_t red = pl->narrow ? 2 * 9 * kAttnNarrow * 4 : 0;
+    const uint32_t q = 2 * pl->q_bytes + (pl->narrow ? 4 * kAttnNarrowP : 0), tail = rows + red + mask + bars + tab;
     if (q + tail > kAttnSmemMax) continue;
     const uint32_t avail = kAttnSmemMax - q - tail;
     if (eight_bit) {
@@ -123,10 +125,12 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
       if (pl->nst > 8) pl->nst = 8;
       pl->nraw = 0;
     }
+    pl->off_p = 2 * pl->q_bytes;
     pl->off_ring = q;
     pl->off_raw = pl->off_ring + rings * pl->nst * stage;
     pl->off_rows = pl->off_raw + rings * pl->nraw * raw;
-    pl->off_mask = pl->off_rows + rows;
+    pl->off_red = pl->off_rows + rows;
+    pl->off_mask = pl->off_red + red;
     pl->off_bars = pl->off_mask + mask;
     pl->off_tab = pl->off_bars + bars;
     pl->smem = pl->off_tab + tab;

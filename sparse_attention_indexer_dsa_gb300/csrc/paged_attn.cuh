@@ -79,6 +79,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// True for one lane of the warp (lane 0), in a form that tells the compiler that it is one: the
+// operands of TMA and MMA instructions then go to uniform registers without a loop over lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrives (without raising the count) once this thread's earlier cp.async have landed.
 __device__ __forceinline__ void cp_arrive(uint32_t bar) {
@@ -135,6 +146,19 @@ __device__ __forceinline__ bool poll_bar(uint32_t bar, uint32_t parity, uint32_t
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity), "r"(polls)
+      : "memory");
+  return ok != 0;
+}
+
+// Whether a phase is over, at once (try_wait may suspend the thread while it is not).
+__device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -292,6 +316,10 @@ __device__ __forceinline__ void widen16(const uint32_t (&w4)[4], uint32_t e8, ui
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t x) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(x) : "memory");
+}
+__device__ __forceinline__ uint16_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&w)[4]) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
 }
@@ -305,7 +333,7 @@ enum { PAIR = 0, SOLO = 1, GATHER = 2 };
 // rows); 4 that bring gathered 8-bit rows; the rest: key loaders (TMA), query loaders, MMA 0 and 1
 // last.  (The four warps of an SM's sub-partition are those of equal number modulo 4; loaders and MMA
 // warps are kept on different ones.)
-template <bool Q8, int MODE>
+template <bool Q8, int MODE, bool NARROW>
 struct Roles {
   static constexpr int kWorkWarps = MODE == GATHER ? (Q8 ? 12 : 8) : (Q8 ? 16 : 0);
   static constexpr int kBringWarps = MODE == GATHER && Q8 ? 4 : 0;
@@ -324,15 +352,52 @@ struct Roles {
                     kWarps / 4 * kLaunchRegs, "shares");
 };
 
-template <int D, bool Q8, int MODE>
-__global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_kernel(const __grid_constant__ AttnParams p) {
-  using R = Roles<Q8, MODE>;
+// Sums (or maxima) over a warp's lanes of N values a lane: half of the values change hands in every step, so it takes
+// N - 1 + log2(32 / N) exchanges; lanes 32 / N * r end with value r's result.
+template <int N, class F>
+__device__ __forceinline__ float warp_join(float (&v)[N], int lane, F f) {
+  int bit = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n >>= 1, bit >>= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = f(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+    }
+  }
+  for (; bit >= 1; bit >>= 1) v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
+  return v[0];
+}
+
+// True for all 128 threads of a named barrier when it is for one of them (orders their shared memory).
+__device__ __forceinline__ bool any_of_128(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+template <int D, bool Q8, int MODE, bool NARROW>
+__global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ AttnParams p) {
+  using R = Roles<Q8, MODE, NARROW>;
+  static_assert(!NARROW || (D == 128 && MODE != PAIR), "a narrow tile's values are the 128 rows of its second product");
   constexpr bool kPair = MODE == PAIR;
   constexpr bool kWorkerCopies = MODE == GATHER && !Q8;   // stages written by cp.async: fenced by the MMA warp
   constexpr uint32_t kStage = kAttnKeys * D * 2;     // one tile of keys or values
   constexpr uint32_t kChunk = kAttnKeys * 128;       // 64 of its columns
   constexpr int kRings = kPair ? 1 : 2;
-  constexpr int kLoaders = R::kWorkWarps > 0 ? 32 * R::kWorkWarps / kRings : 32;   // worker threads per ring
+  // One ring's workers are two teams, one widening the keys' tiles and one the values': most of a
+  // tile's time is latency (waits, fences), which then overlaps.
+  constexpr int kTeams = Q8 && kRings == 1 ? 2 : 1;
+  constexpr int kLoaders = R::kWorkWarps > 0 ? 32 * R::kWorkWarps / (kRings * kTeams) : 32;   // threads of a team
   constexpr uint32_t kRawItem = kAttnKeys * D + 512;   // a tile as stored, with its scales
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnPlan& pl = p.plan;
@@ -342,9 +407,9 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
   const bool listed = MODE == GATHER && p.topk_idx != nullptr;
 
   // barriers: per ring full/empty (BF16 tiles) and raw full/empty (stored 8-bit tiles); per stream
-  // q_full, q_empty, s_full, p_full, o_full, drain
+  // q_full, q_empty, o_full, drain, and s_full, p_full, p_empty (two of each with NARROW)
   const uint32_t bars = sbase + pl.off_bars;
-  int* const ctl = reinterpret_cast<int*>(smem + pl.off_bars + 8 * (2 * 32 + 2 * 6));   // status, abort, tmem base, chunk, turn
+  int* const ctl = reinterpret_cast<int*>(smem + pl.off_bars + 8 * kAttnBars);   // status, abort, tmem base, chunk, turn
   int* const status = ctl;
   volatile int* const abort_flag = ctl + 1;
   int* const tab = reinterpret_cast<int*>(smem + pl.off_tab);
@@ -352,8 +417,8 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
   auto bar_empty = [&](int ring, int s) { return bars + 8u * (ring * 32 + 8 + s); };
   auto bar_raw_full = [&](int ring, int s) { return bars + 8u * (ring * 32 + 16 + s); };
   auto bar_raw_empty = [&](int ring, int s) { return bars + 8u * (ring * 32 + 24 + s); };
-  auto bar_st = [&](int w, int i) { return bars + 8u * (64 + w * 6 + i); };
-  enum { Q_FULL, Q_EMPTY, S_FULL, P_FULL, O_FULL, DRAIN };
+  auto bar_st = [&](int w, int i) { return bars + 8u * (64 + w * 10 + i); };
+  enum { Q_FULL, Q_EMPTY, O_FULL, DRAIN, S_FULL, P_FULL = S_FULL + 2, P_EMPTY = P_FULL + 2 };
   constexpr int kMmaWarp = R::kWarps - 2;
 
   if (tid == 0) {
@@ -362,19 +427,22 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
     ctl[4] = 0;
     for (int r = 0; r < kRings; ++r) {
       for (int s = 0; s < pl.nst; ++s) {
-        mbar_init(bar_full(r, s), R::kWorkWarps > 0 ? kLoaders + (kWorkerCopies ? R::kWorkWarps / 2 : 0) : 1);
+        mbar_init(bar_full(r, s), kWorkerCopies ? kLoaders + kLoaders / 32 : (R::kWorkWarps > 0 ? kLoaders / 32 : 1));
         mbar_init(bar_empty(r, s), kPair ? 2 : 1);
       }
       for (int s = 0; s < pl.nraw; ++s) {
-        mbar_init(bar_raw_full(r, s), MODE == GATHER ? 128 : 1);   // (two warps, each thread twice)
+        mbar_init(bar_raw_full(r, s), MODE == GATHER ? 64 + 2 : 1);   // (two warps: their threads' copies, their scales)
         mbar_init(bar_raw_empty(r, s), kLoaders / 32);
       }
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar_st(w, Q_FULL), 32);
       mbar_init(bar_st(w, Q_EMPTY), 1);
-      mbar_init(bar_st(w, S_FULL), 1);
-      mbar_init(bar_st(w, P_FULL), 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(bar_st(w, S_FULL + b), 1);
+        mbar_init(bar_st(w, P_FULL + b), 4);
+        mbar_init(bar_st(w, P_EMPTY + b), 1);
+      }
       mbar_init(bar_st(w, O_FULL), 1);
       mbar_init(bar_st(w, DRAIN), 1);
     }
@@ -651,16 +719,17 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
   if (R::kWorkWarps > 0 && wg >= 2 && wg < 2 + R::kWorkWarps / 4) {
     // ======================= workers =======================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kWorkRegs));
-    const int ring = kPair ? 0 : (tid - 256) / kLoaders;
-    const int lt = (tid - 256) % kLoaders;           // thread of this ring
+    const int ring = kRings == 1 ? 0 : (tid - 256) / kLoaders, team = kTeams == 1 ? 0 : (tid - 256) / kLoaders;
+    const int lt = (tid - 256) % kLoaders;           // thread of this team
     const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
     bool ok = true;
-    int st = 0;
+    int st = team;          // (at least two stages and stored tiles to a ring of two teams)
     uint32_t ph = 0;
     bool wrapped = false;   // every stage has been used once
     auto advance = [&] {
-      if (++st == pl.nst) {
-        st = 0;
+      st += kTeams;
+      if (st >= pl.nst) {
+        st -= pl.nst;
         ph ^= 1u;
         wrapped = true;
       }
@@ -670,7 +739,9 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       constexpr int PPR = D / 16;                  // 16-code pieces per row
       constexpr int RPP = kLoaders / PPR;
       constexpr int kPasses = (kAttnKeys + RPP - 1) / RPP;   // (12 workers: the last pass is not whole)
-      const int c = lt % PPR, rsub = lt / PPR;
+      // (of two neighbouring rows, one's first half beside the other's second in eight lanes: a 64-column
+      // chunk's pieces of one row alone would be 2-way bank conflicts of the stores)
+      const int c = lt % PPR, rsub = D == 128 ? ((lt / PPR) & ~1) | (((lt / PPR) ^ (c >> 2)) & 1) : lt / PPR;
       const uint32_t raw_base = sbase + pl.off_raw + (uint32_t)ring * pl.nraw * kRawItem + rsub * D + c * 16;
       const int* const meta = reinterpret_cast<const int*>(smem + pl.off_rows) + ring * 8;
       const uint32_t dcol = (uint32_t)(c >> 2) * kChunk + rsub * 128;
@@ -678,11 +749,11 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       static_assert(!Q8 || RPP % 8 == 0, "swizzle");
       const uint32_t at0 = dcol + ((uint32_t)(((c & 3) * 2) ^ (rsub & 7)) << 4), at1 = at0 ^ 16u;
       const int sw = p.c.sw, s0 = rsub * sw + (sw == 1 ? 0 : c >> 1);
-      int slot = 0;
+      int slot = team;
       uint32_t rph = 0;
       for (int u = first_unit(ring); u < n_units && ok; u += n_streams) {
         const int n = decode_unit<kPair>(p, tab, gsz, chunk, u, kPair ? 0 : ring).n_shared;
-        for (int it = 0; it < 2 * n; ++it) {
+        for (int it = team; it < 2 * n; it += kTeams) {
           ok = __all_sync(0xffffffffu, wait_bar(bar_raw_full(ring, slot), rph, abort_flag, status, tmo) &&
                                            (!wrapped || wait_bar(bar_empty(ring, st), ph ^ 1u, abort_flag, status, tmo)));
           if (!ok) break;
@@ -717,12 +788,15 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_raw_empty(ring, slot));
-          if (++slot == pl.nraw) {
-            slot = 0;
+          slot += kTeams;
+          if (slot >= pl.nraw) {
+            slot -= pl.nraw;
             rph ^= 1u;
           }
+          // (one arrival a warp: 32 lanes' arrivals at one barrier are worked off one after the other)
           fence_proxy_async_smem();
-          mbar_arrive(bar_full(ring, st));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_full(ring, st));
           advance();
         }
       }
@@ -800,8 +874,9 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
         }
         if (part == 0 && lane == 0) meta[slot] = kAttnKeys;
         if (p.fault_inject != 1 || t > 0 || kv > 0) {   // (the tests' withheld first tile)
-          mbar_arrive(bar);     // the scales
-          cp_arrive(bar);       // the codes, when they have landed
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);   // the scales
+          cp_arrive(bar);                    // the codes, when they have landed
         }
         if (++slot == pl.nraw) {
           slot = 0;
@@ -865,7 +940,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
 #pragma unroll 1
                 for (int i = 0; i < boxes; ++i) {   // (one lane and uniform coordinates: a lane to a box issues slower)
                   const int pg = __shfl_sync(0xffffffffu, now, i);
-                  if (lane == 0 && (unsigned)pg < (unsigned)p.c.num_pages) {
+                  if ((unsigned)pg < (unsigned)p.c.num_pages && elect_one()) {
                     const int slot = (key0 + i * box) & ((1 << shift) - 1), z = pg * p.c.n_kv + x.h;
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c)
@@ -944,7 +1019,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
 #pragma unroll 1
             for (int i = 0; i < boxes; ++i) {   // (one lane and uniform coordinates: a lane to a box issues slower)
               const int pg = __shfl_sync(0xffffffffu, now, i);
-              if (lane == 0 && !withheld && ((have >> i) & 1u)) {
+              if (!withheld && ((have >> i) & 1u) && elect_one()) {
                 const int in_page = (key0 + i * box) & ((1 << shift) - 1), z = pg * p.c.n_kv + x.h;
                 tma_load_3d(dst + i * box * D, kv ? &p.tm_v : &p.tm_k, bar, 0, in_page, z);
                 bulk_load(dst + kAttnKeys * D + i * box * sw, sc + ((((int64_t)z << shift) + in_page) * sw), box * sw, bar);
@@ -1005,10 +1080,90 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
       const int w = warp - kMmaWarp;
       const int ring = kPair ? 0 : w;
       const uint32_t ring_base = sbase + pl.off_ring + (uint32_t)ring * pl.nst * kStage;
+      if constexpr (NARROW) {
+        // S^T = K Q^T into one of two buffers, O^T += V^T P^T with P from shared memory: the next tile's
+        // S^T is formed while the softmax warps are at this one.
+        constexpr int N = kAttnNarrow;
+        const uint32_t t_s = tmem + (uint32_t)w * 2 * N, t_o = tmem + 4 * N + (uint32_t)w * N;
+        constexpr uint32_t idesc_qk = idesc_bf16(kAttnKeys, N);
+        constexpr uint32_t idesc_pv = idesc_bf16(D, N) | (1u << 15);   // V: rows of keys, M contiguous
+        if (elect_one()) {
+          const uint64_t qd0 = sw128_kmajor_desc(sbase + (uint32_t)w * pl.q_bytes, 0);
+          const uint64_t pd0 = sw128_kmajor_desc(sbase + pl.off_p + (uint32_t)w * 2 * kAttnNarrowP, 0);
+          int st[2] = {0, 1};   // stage and phase of the next keys and of the next values
+          uint32_t ph[2] = {0, 0}, nq = 0, nt = 0;
+          bool ok = true;
+          auto advance = [&](int i) {
+            st[i] += 2;
+            if (st[i] >= pl.nst) {
+              st[i] -= pl.nst;
+              ph[i] ^= 1u;
+            }
+          };
+          for (int u = first_unit(w); u < n_units && ok; u += n_streams) {
+            const Unit x = decode_unit<false>(p, tab, gsz, chunk, u, w);
+            if (x.n == 0) continue;
+            ok = wait_bar(bar_st(w, Q_FULL), nq & 1u, abort_flag, status, tmo);
+            if (!ok) break;
+            ++nq;
+            // Whichever product's operands are there: S^T of tile jk (P of tile jk - 2 has been waited for,
+            // so that buffer's S^T is read), PV of tile jv.
+            int jk = 0, jv = 0;
+            uint32_t polls = 0;
+            uint64_t t0 = 0;
+            while (jv < x.n) {
+              const uint32_t t = nt + jv, bv = t & 1u, bk = (nt + jk) & 1u;
+              if (jk < x.n && jk <= jv + 1 && test_bar(bar_full(ring, st[0]), ph[0])) {
+                fence_proxy_async_smem();   // cp.async's writes (query tile, copied rows), seen through the barriers
+                tc_fence_after();
+                uint64_t qd = qd0, kd = sw128_kmajor_desc(ring_base + (uint32_t)st[0] * kStage, 0);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c, qd += (N * 128) >> 4, kd += kChunk >> 4) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) mma_bf16(t_s + bk * N, kd + 2 * k, qd + 2 * k, idesc_qk, c + k > 0);
+                }
+                tc_commit(bar_st(w, S_FULL + bk));
+                tc_commit(bar_empty(ring, st[0]));
+                if (++jk == x.n) tc_commit(bar_st(w, Q_EMPTY));
+                advance(0);
+                polls = 0;
+              } else if (jv < jk && test_bar(bar_st(w, P_FULL + bv), (t >> 1) & 1u) &&
+                         test_bar(bar_full(ring, st[1]), ph[1])) {
+                if (kWorkerCopies) fence_proxy_async_smem();
+                tc_fence_after();
+                uint64_t vd = smem_desc(ring_base + (uint32_t)st[1] * kStage, kChunk, 1024, 2), pd = pd0 + bv * (kAttnNarrowP >> 4);
+#pragma unroll
+                for (int k = 0; k < kAttnKeys / 16; ++k, vd += 2048 >> 4)
+                  mma_bf16(t_o, vd, pd + (k >> 2) * ((N * 128) >> 4) + (k & 3) * 2, idesc_pv, (jv > 0 || k > 0) ? 1u : 0u);
+                tc_commit(bar_empty(ring, st[1]));
+                tc_commit(bar_st(w, P_EMPTY + bv));
+                if (++jv == x.n) tc_commit(bar_st(w, O_FULL));
+                advance(1);
+                polls = 0;
+              } else if ((++polls & 1023u) == 0) {   // bounded, as wait_bar
+                if (polls == 1024u) t0 = globaltimer_ns();
+                if (*abort_flag) {
+                  ok = false;
+                } else if (globaltimer_ns() - t0 > tmo) {
+                  set_status(status, DSA_DEV_ERR_TIMEOUT);
+                  *abort_flag = 1;
+                  ok = false;
+                }
+                if (!ok) break;
+              }
+            }
+            nt += x.n;
+          }
+          if (!ok) {   // what was issued completes before the tensor memory is given back
+            tc_commit(bar_st(w, DRAIN));
+            drain_wait(bar_st(w, DRAIN), 0, tmo);
+          }
+        }
+      } else {
       const uint32_t t_s = tmem + (uint32_t)w * 128, t_o = tmem + 256 + (uint32_t)w * 128;
       constexpr uint32_t idesc_qk = idesc_bf16(kAttnRows, kAttnKeys);
       constexpr uint32_t idesc_pv = idesc_bf16(kAttnRows, D) | (1u << 16);   // V: rows of keys, N contiguous
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t q_rows_bytes = pl.q_bytes / (D / 64);   // one 64-column chunk of the query tile
         // The streams issue PV and the next QK as one block, in turns: their softmax phases then
         // alternate with the other's products.  Left to themselves both streams' products queue
@@ -1051,14 +1206,14 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
               uint64_t vd = smem_desc(ring_base + (uint32_t)st * kStage, kChunk, 1024, 2);
               const uint32_t v_empty = bar_empty(ring, st);
               advance();
-              have_k = next && mbar_try_wait(bar_full(ring, st), ph);
+              have_k = next && test_bar(bar_full(ring, st), ph);
               if (kWorkerCopies) fence_proxy_async_smem();   // the workers' cp.async writes, seen through the barriers
               // (P of a unit's first tile also says that the softmax warps have read the last unit's O)
               ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
               if (!ok) break;
               ++nt;
               if (next && !have_k) {   // once more: the next QK in this turn
-                have_k = mbar_try_wait(bar_full(ring, st), ph);
+                have_k = test_bar(bar_full(ring, st), ph);
                 if (kWorkerCopies && have_k) fence_proxy_async_smem();
               }
               tc_fence_after();
@@ -1105,7 +1260,170 @@ __global__ void __launch_bounds__(Roles<Q8, MODE>::kThreads, 1) paged_attention_
           drain_wait(bar_st(w, DRAIN), 0, tmo);
         }
       }
+      }
       __syncwarp();
+    }
+  } else if constexpr (NARROW) {
+    // ======================= softmax warpgroups, a key to a thread =======================
+    // The rows' maxima are the block's: the warpgroup votes whether a logit exceeds its row's, and raises
+    // them together.  Whatever a warp has waited for in vain, it takes part in every vote: all leave at one.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmaxRegs));
+    constexpr int N = kAttnNarrow;
+    const int w = wg, quarter = warp & 3, key = quarter * 32 + lane, bar_id = 1 + w;
+    const uint32_t lane_off = (uint32_t)quarter << 21;    // TMEM lane 32 * quarter
+    const uint32_t t_s = tmem + (uint32_t)w * 2 * N + lane_off, t_o = tmem + 4 * N + (uint32_t)w * N + lane_off;
+    float* const m_tab = reinterpret_cast<float*>(smem + pl.off_red) + w * 9 * N;   // running maximum of each row
+    float* const m_of = m_tab + N;                                                  // [4][N] a warp's maxima
+    float* const l_of = m_tab + 5 * N;                                              // [4][N] a warp's sums
+    const uint32_t* const masks = reinterpret_cast<const uint32_t*>(smem + pl.off_mask) + w * kMaskRing * 4;
+    // this key's 2 bytes of each row of P (K-major, 64 keys to a 128-byte row, swizzled)
+    const uint32_t p_at = sbase + pl.off_p + (uint32_t)w * 2 * kAttnNarrowP + (uint32_t)(key >> 6) * (N * 128) + (key & 7) * 2;
+    const uint32_t piece = (key & 63) >> 3;
+    const float scale = p.scale_log2;
+    constexpr int kLanesPerRow = 32 / N;
+    uint32_t nt = 0, nq = 0;
+    bool ok = true;
+    Unit x{}, nx{};
+    if (first_unit(w) < n_units) x = decode_unit<false>(p, tab, gsz, chunk, first_unit(w), w);
+    for (int u = first_unit(w); u < n_units && ok; u += n_streams, x = nx) {
+      const int live = (x.i1 - x.i0) * p.group;
+      const int vis0 = x.P0 + x.i0 + 1;   // keys that the first token sees
+      float l[N];
+#pragma unroll
+      for (int r = 0; r < N; ++r) l[r] = 0.f;
+      if (x.n > 0) {
+        any_of_128(bar_id, false);        // (the last unit's maxima and sums have been read)
+        if (key < N) m_tab[key] = key < live ? -INFINITY : INFINITY;
+        any_of_128(bar_id, false);
+      }
+      for (int j = 0; j < x.n; ++j, ++nt) {
+        const uint32_t b = nt & 1u;
+        if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_st(w, S_FULL + b), (nt >> 1) & 1u, abort_flag, status, tmo));
+        float s[N];
+        bool over = false;
+        if (ok) {
+          tc_fence_after();
+          uint32_t raw[N];
+          tmem_ld_x16(t_s + b * N, raw);
+          tmem_ld_wait_tied<N>(raw);
+          const int at = (x.lo + j) * kAttnKeys + key;
+          const bool hidden = listed ? ((masks[(nt % kMaskRing) * 4 + quarter] >> lane) & 1u) == 0 : false;
+          if (__any_sync(0xffffffffu, hidden || (!listed && at >= vis0))) {
+            int tok = 0, g = 0;
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+              if (hidden || (!listed && at >= vis0 + tok)) raw[r] = 0xFF800000u;
+              if (++g == p.group) {
+                g = 0;
+                ++tok;
+              }
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < N; ++r) s[r] = __uint_as_float(raw[r]);
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            if (r % 8 == 0 && r >= live) break;
+            over |= s[r] * scale > m_tab[r] + kRaise;   // (rows that are not live: never)
+          }
+        }
+        if (any_of_128(bar_id, over || !ok)) {
+          if (ok) {
+            float v[N];
+#pragma unroll
+            for (int r = 0; r < N; ++r) v[r] = s[r];
+            const float mx = warp_join<N>(v, lane, [](float a, float c) { return fmaxf(a, c); });
+            if (lane % kLanesPerRow == 0) m_of[quarter * N + lane / kLanesPerRow] = mx;
+            if (j > 0)   // O so far
+              ok = __all_sync(0xffffffffu, wait_bar(bar_st(w, P_EMPTY + (b ^ 1u)), ((nt - 1) >> 1) & 1u, abort_flag, status, tmo));
+          }
+          ok = !any_of_128(bar_id, !ok);
+          if (!ok) break;
+          float alpha[N], mine = 0.f;
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            const float top = fmaxf(fmaxf(m_of[r], m_of[N + r]), fmaxf(m_of[2 * N + r], m_of[3 * N + r]));
+            const float mt = top == -INFINITY ? -INFINITY : top * scale, m = m_tab[r];
+            const bool raise = mt > m + kRaise;
+            alpha[r] = raise ? ex2(m - mt) : 1.f;      // 0 when m = -inf
+            l[r] *= alpha[r];
+            if (r == key) mine = raise ? mt : m;
+          }
+          if (j > 0) {
+            tc_fence_after();
+            uint32_t o[N];
+            tmem_ld_x16(t_o, o);
+            tmem_ld_wait_tied<N>(o);
+#pragma unroll
+            for (int r = 0; r < N; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
+            tmem_st_x16(t_o, o);
+            tmem_st_wait();
+          }
+          any_of_128(bar_id, false);
+          if (key < N) m_tab[key] = mine;
+          any_of_128(bar_id, false);
+        }
+        if (nt >= 2)
+          ok = __all_sync(0xffffffffu, wait_bar(bar_st(w, P_EMPTY + b), ((nt >> 1) - 1u) & 1u, abort_flag, status, tmo));
+        if (ok) {
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            if (r % 8 == 0 && r >= live) break;   // (columns of the product that nobody reads)
+            const float m = m_tab[r];
+            s[r] = ex2(fmaf(s[r], scale, m == -INFINITY ? 0.f : -m));   // (m = inf where no row is live: 0)
+            l[r] += s[r];
+          }
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            if (r % 8 == 0 && r >= live) break;
+            st_shared_u16(p_at + b * kAttnNarrowP + (r >> 3) * 1024 + (r & 7) * 128 + ((piece ^ (r & 7)) << 4), bf16_bits(s[r]));
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar_st(w, P_FULL + b));
+      }
+      if (u + n_streams < n_units) nx = decode_unit<false>(p, tab, gsz, chunk, u + n_streams, w);   // (while O is formed)
+      uint32_t o[N];
+      if (x.n > 0) {
+        if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_st(w, O_FULL), nq & 1u, abort_flag, status, tmo));
+        ++nq;
+        const float sum = warp_join<N>(l, lane, [](float a, float c) { return a + c; });
+        if (lane % kLanesPerRow == 0) l_of[quarter * N + lane / kLanesPerRow] = sum;
+        ok = !any_of_128(bar_id, !ok);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld_x16(t_o, o);   // (the next unit's first PV waits for its P, which follows these reads)
+        tmem_ld_wait_tied<N>(o);
+      }
+      // thread `key` has element `key` of every row's result
+      int64_t orow = (int64_t)(x.q0 + x.i0) * p.n_heads + x.h * p.group;
+      const int64_t prow = (int64_t)u * pl.rows_cap;
+      int g = 0;
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        if (r < live) {
+          float lr = 0.f, m = -INFINITY, v = 0.f;
+          if (x.n > 0) {
+            lr = (l_of[r] + l_of[N + r]) + (l_of[2 * N + r] + l_of[3 * N + r]);
+            m = m_tab[r];
+            v = __uint_as_float(o[r]);
+          }
+          if (x.ns == 1) {
+            reinterpret_cast<uint16_t*>(p.out)[orow * D + key] = bf16_bits(lr == 0.f ? 0.f : v * (1.f / lr));
+            if (p.lse && key == r) p.lse[orow] = lr == 0.f ? -INFINITY : (m + log2f(lr)) * 0.6931471805599453f;
+          } else {
+            if (x.n > 0) p.part_o[(prow + r) * D + key] = v;   // (else (m, l) = (-inf, 0) tells as much)
+            if (key == r) p.part_ml[prow + r] = make_float2(m, lr);
+          }
+        }
+        ++orow;
+        if (++g == p.group) {
+          g = 0;
+          orow += p.n_heads - p.group;
+        }
+      }
     }
   } else {
     // ======================= softmax warpgroups =======================
@@ -1319,9 +1637,9 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const AttnPar
   }
 }
 
-template <int D, bool Q8, int MODE>
+template <int D, bool Q8, int MODE, bool NARROW = false>
 cudaError_t launch(const AttnParams& p, int grid, int sm_count, cudaStream_t stream) {
-  auto kernel = paged_attention_kernel<D, Q8, MODE>;
+  auto kernel = paged_attention_kernel<D, Q8, MODE, NARROW>;
   cudaError_t e;
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -1330,13 +1648,13 @@ cudaError_t launch(const AttnParams& p, int grid, int sm_count, cudaStream_t str
     // The warpgroups' register shares add up to kLaunchRegs a thread: fewer at launch would leave them waiting.
     cudaFuncAttributes a;
     if ((e = cudaFuncGetAttributes(&a, kernel)) != cudaSuccess) return e;
-    if (a.numRegs < Roles<Q8, MODE>::kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+    if (a.numRegs < Roles<Q8, MODE, NARROW>::kLaunchRegs) return cudaErrorInvalidDeviceFunction;
     // always the same value: calls of several threads do not disturb one another
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAttnSmemMax);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
   }
-  kernel<<<grid, Roles<Q8, MODE>::kThreads, p.plan.smem, stream>>>(p);
+  kernel<<<grid, Roles<Q8, MODE, NARROW>::kThreads, p.plan.smem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.plan.max_units == 0 || p.total_q == 0) return e;
   const int64_t blocks = ((int64_t)p.total_q * p.n_heads + 7) / 8;

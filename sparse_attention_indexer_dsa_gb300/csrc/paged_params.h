@@ -53,6 +53,9 @@ struct CacheReadParams {
 constexpr int kAttnKeys = 128;      // keys per tile
 constexpr int kAttnRows = 128;      // query rows (token, head of the group) per tile
 constexpr int kAttnMinChunk = 2;    // key tiles of a divided range, at least
+constexpr int kAttnNarrow = 16;              // query rows of a narrow tile (columns of its products)
+constexpr int kAttnNarrowP = kAttnNarrow * kAttnKeys * 2;   // bytes of its weights
+constexpr int kAttnBars = 2 * 32 + 2 * 10;   // barriers of a block
 constexpr uint32_t kAttnSmemMax = 232448;   // 227 KB
 constexpr int kAttnSms = 152;       // the grid's upper bound, for workspace sizes
 
@@ -65,9 +68,10 @@ struct AttnPlan {
   int rows_cap;    // rows of a tile that can be live
   int nst;         // key/value stages per ring
   int nraw;        // tiles of stored 8-bit rows per ring
+  int narrow;      // at most kAttnNarrow rows to a tile: the products have the keys as rows, the queries as columns
   int max_units;   // units with room for a partial result; 0: key ranges are never divided
   uint32_t q_bytes;                                        // query tile in shared memory
-  uint32_t off_ring, off_raw, off_rows, off_mask, off_bars, off_tab, smem;
+  uint32_t off_p, off_ring, off_raw, off_rows, off_red, off_mask, off_bars, off_tab, smem;
 };
 
 struct AttnParams {
