@@ -81,7 +81,8 @@ namespace dsa {
 
 // Two query tiles to a block when the average sequence fills more than one
 // 128-row tile: its keys are then read once for both.  Otherwise the two
-// streams of a block work on their own.  Key ranges are divided only while
+// streams of a block work on their own; tiles of at most 16 rows are narrow
+// (the figures are with the kernel).  Key ranges are divided only while
 // there are at most four units to a stream (more balance themselves), and a
 // call's workspace has room for four more units to a stream.
 bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,

@@ -24,6 +24,18 @@
 //         key/value stages (long chunks: the keys are read half as often);
 //   else: the streams are independent, each with its own units and ring
 //         (single tokens, short chunks, selected rows).
+// Narrow tiles.  At most 16 query rows (single tokens of few heads; head_dim
+// 128) would leave seven eighths of the 128 TMEM lanes, and three of four
+// softmax warps, to rows that are not there.  There the keys are the products'
+// rows: S^T = K Q^T (128 keys x 16), a key to a softmax thread, P^T through
+// shared memory, O^T += V^T P^T (head_dim x 16).  S and P have two buffers, so
+// the next tile's logits are formed meanwhile.  One token of each of 64
+// sequences, 64 heads, 8 key heads, 2048 - 16384 keys, against tiles of 128
+// rows: 418 us against 425 over MXFP8 (1.2 GB), 376 against 385 over BF16
+// (2.4 GB: 93 % of the copy rate); 2048 listed keys of 4 tokens of each: 496
+// against 605 over MXFP8, 277 against 338 over BF16.  Over 8-bit caches the
+// latency of a stored tile (its load, its widening, the hand-overs) bounds it:
+// shared memory holds two stored tiles to a ring beside the widened ones.
 // Loaders.  TMA brings all visible keys as a box per page; listed rows are copied
 // one by one with cp.async (TMA row gathers of four came to 27 bytes a cycle and
 // SM, cp.async from eight warps to 60); BF16 in the 128-byte swizzled layout the
@@ -33,6 +45,10 @@
 // zero-filled, so nothing outside a sequence's own rows enters a product.  Tiles
 // of 8-bit caches are fetched as stored and widened to BF16 by worker warps on
 // the way into a stage; E4M3 x 2^e is exact in BF16.
+// Issue.  TMA and MMA instructions take their operands from uniform registers:
+// issued under `lane == 0` each was a loop over lanes (some 400 cycles to a TMA
+// copy beside busy workers), from an elected lane it is not: 4096 tokens over
+// 32768 BF16 keys 3.13 -> 2.88 ms, ragged chunks over FP8 0.57 -> 0.50 ms.
 //
 // Units.  (sequence, key head, query tile, range of key tiles).  Every block
 // derives the same list from the prefixes: the number of key tiles per range is
@@ -103,11 +119,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -373,6 +384,7 @@ __device__ __forceinline__ float warp_join(float (&v)[N], int lane, F f) {
 // True for all 128 threads of a named barrier when it is for one of them (orders their shared memory).
 __device__ __forceinline__ bool any_of_128(int id, bool x) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
@@ -1160,106 +1172,107 @@ __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
           }
         }
       } else {
-      const uint32_t t_s = tmem + (uint32_t)w * 128, t_o = tmem + 256 + (uint32_t)w * 128;
-      constexpr uint32_t idesc_qk = idesc_bf16(kAttnRows, kAttnKeys);
-      constexpr uint32_t idesc_pv = idesc_bf16(kAttnRows, D) | (1u << 16);   // V: rows of keys, N contiguous
-      if (elect_one()) {
-        const uint32_t q_rows_bytes = pl.q_bytes / (D / 64);   // one 64-column chunk of the query tile
-        // The streams issue PV and the next QK as one block, in turns: their softmax phases then
-        // alternate with the other's products.  Left to themselves both streams' products queue
-        // up together, and so do the softmax phases (5300 against 3300 cycles per key tile).
-        // Nothing is waited for inside a turn, so a turn always comes; only the times depend on it.
-        int* const turn = ctl + 4;
-        auto take_turn = [&] {
-          for (int i = 0; i < (1 << 20) && atomicCAS_block(turn, 0, 1) != 0; ++i) {
-          }
-        };
-        auto end_turn = [&] { atomicExch_block(turn, 0); };
-        // (the 128 rows that the products read begin before the tile when its rows are not the first:
-        // with 32 or 64 rows a tile, still inside the first stream's)
-        const uint64_t qd0 = sw128_kmajor_desc(sbase + (uint32_t)w * pl.q_bytes - first_row(w) * 128, 0);
-        int st = 0;
-        uint32_t ph = 0, nq = 0, nt = 0;
-        bool ok = true;
-        auto advance = [&] {
-          if (++st == pl.nst) {
-            st = 0;
-            ph ^= 1u;
-          }
-        };
-        for (int u = first_unit(w); u < n_units && ok; u += n_streams) {
-          const Unit x = decode_unit<kPair>(p, tab, gsz, chunk, u, w);
-          if (x.n > 0) {
-            ok = wait_bar(bar_st(w, Q_FULL), nq & 1u, abort_flag, status, tmo);
-            fence_proxy_async_smem();   // the query tile's cp.async writes
-          }
-          // iteration j: O += P V of tile j - 1, S = Q K^T of tile j
-#pragma unroll 1
-          for (int j = 0; x.n > 0 && j <= x.n; ++j) {
-            const bool next = j < x.n;
-            bool have_k = false;
-            if (j > 0) {
-              // everything but P is waited for first
-              ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
-              if (!ok) break;
-              // N-major operand: 64-column chunks kChunk apart, groups of 8 keys 1024 bytes apart
-              uint64_t vd = smem_desc(ring_base + (uint32_t)st * kStage, kChunk, 1024, 2);
-              const uint32_t v_empty = bar_empty(ring, st);
-              advance();
-              have_k = next && test_bar(bar_full(ring, st), ph);
-              if (kWorkerCopies) fence_proxy_async_smem();   // the workers' cp.async writes, seen through the barriers
-              // (P of a unit's first tile also says that the softmax warps have read the last unit's O)
-              ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
-              if (!ok) break;
-              ++nt;
-              if (next && !have_k) {   // once more: the next QK in this turn
-                have_k = test_bar(bar_full(ring, st), ph);
-                if (kWorkerCopies && have_k) fence_proxy_async_smem();
-              }
-              tc_fence_after();
-              take_turn();
-#pragma unroll
-              for (int k = 0; k < kAttnKeys / 16; ++k, vd += 2048 >> 4)
-                mma_bf16_ts(t_o, t_s + k * 8, vd, idesc_pv, (j > 1 || k > 0) ? 1u : 0u);
-              tc_commit(v_empty);
-              if (!next) tc_commit(bar_st(w, O_FULL));
+        // ---- tiles of 128 query rows ----
+        const uint32_t t_s = tmem + (uint32_t)w * 128, t_o = tmem + 256 + (uint32_t)w * 128;
+        constexpr uint32_t idesc_qk = idesc_bf16(kAttnRows, kAttnKeys);
+        constexpr uint32_t idesc_pv = idesc_bf16(kAttnRows, D) | (1u << 16);   // V: rows of keys, N contiguous
+        if (elect_one()) {
+          const uint32_t q_rows_bytes = pl.q_bytes / (D / 64);   // one 64-column chunk of the query tile
+          // The streams issue PV and the next QK as one block, in turns: their softmax phases then
+          // alternate with the other's products.  Left to themselves both streams' products queue
+          // up together, and so do the softmax phases (5300 against 3300 cycles per key tile).
+          // Nothing is waited for inside a turn, so a turn always comes; only the times depend on it.
+          int* const turn = ctl + 4;
+          auto take_turn = [&] {
+            for (int i = 0; i < (1 << 20) && atomicCAS_block(turn, 0, 1) != 0; ++i) {
             }
-            if (next) {
-              if (!have_k) {
-                if (j > 0) end_turn();
+          };
+          auto end_turn = [&] { atomicExch_block(turn, 0); };
+          // (the 128 rows that the products read begin before the tile when its rows are not the first:
+          // with 32 or 64 rows a tile, still inside the first stream's)
+          const uint64_t qd0 = sw128_kmajor_desc(sbase + (uint32_t)w * pl.q_bytes - first_row(w) * 128, 0);
+          int st = 0;
+          uint32_t ph = 0, nq = 0, nt = 0;
+          bool ok = true;
+          auto advance = [&] {
+            if (++st == pl.nst) {
+              st = 0;
+              ph ^= 1u;
+            }
+          };
+          for (int u = first_unit(w); u < n_units && ok; u += n_streams) {
+            const Unit x = decode_unit<kPair>(p, tab, gsz, chunk, u, w);
+            if (x.n > 0) {
+              ok = wait_bar(bar_st(w, Q_FULL), nq & 1u, abort_flag, status, tmo);
+              fence_proxy_async_smem();   // the query tile's cp.async writes
+            }
+            // iteration j: O += P V of tile j - 1, S = Q K^T of tile j
+#pragma unroll 1
+            for (int j = 0; x.n > 0 && j <= x.n; ++j) {
+              const bool next = j < x.n;
+              bool have_k = false;
+              if (j > 0) {
+                // everything but P is waited for first
                 ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
                 if (!ok) break;
-                if (kWorkerCopies) fence_proxy_async_smem();
+                // N-major operand: 64-column chunks kChunk apart, groups of 8 keys 1024 bytes apart
+                uint64_t vd = smem_desc(ring_base + (uint32_t)st * kStage, kChunk, 1024, 2);
+                const uint32_t v_empty = bar_empty(ring, st);
+                advance();
+                have_k = next && test_bar(bar_full(ring, st), ph);
+                if (kWorkerCopies) fence_proxy_async_smem();   // the workers' cp.async writes, seen through the barriers
+                // (P of a unit's first tile also says that the softmax warps have read the last unit's O)
+                ok = wait_bar(bar_st(w, P_FULL), nt & 1u, abort_flag, status, tmo);
+                if (!ok) break;
+                ++nt;
+                if (next && !have_k) {   // once more: the next QK in this turn
+                  have_k = test_bar(bar_full(ring, st), ph);
+                  if (kWorkerCopies && have_k) fence_proxy_async_smem();
+                }
                 tc_fence_after();
                 take_turn();
-              }
-              uint64_t qd = qd0, kd = sw128_kmajor_desc(ring_base + (uint32_t)st * kStage, 0);
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c, qd += q_rows_bytes >> 4, kd += kChunk >> 4) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_bf16(t_s, qd + 2 * k, kd + 2 * k, idesc_qk, c + k > 0);   // 32 bytes a step
+                for (int k = 0; k < kAttnKeys / 16; ++k, vd += 2048 >> 4)
+                  mma_bf16_ts(t_o, t_s + k * 8, vd, idesc_pv, (j > 1 || k > 0) ? 1u : 0u);
+                tc_commit(v_empty);
+                if (!next) tc_commit(bar_st(w, O_FULL));
               }
-              tc_commit(bar_st(w, S_FULL));
-              tc_commit(bar_empty(ring, st));
-              if (j + 1 == x.n) tc_commit(bar_st(w, Q_EMPTY));
-              advance();
+              if (next) {
+                if (!have_k) {
+                  if (j > 0) end_turn();
+                  ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
+                  if (!ok) break;
+                  if (kWorkerCopies) fence_proxy_async_smem();
+                  tc_fence_after();
+                  take_turn();
+                }
+                uint64_t qd = qd0, kd = sw128_kmajor_desc(ring_base + (uint32_t)st * kStage, 0);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c, qd += q_rows_bytes >> 4, kd += kChunk >> 4) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) mma_bf16(t_s, qd + 2 * k, kd + 2 * k, idesc_qk, c + k > 0);   // 32 bytes a step
+                }
+                tc_commit(bar_st(w, S_FULL));
+                tc_commit(bar_empty(ring, st));
+                if (j + 1 == x.n) tc_commit(bar_st(w, Q_EMPTY));
+                advance();
+              }
+              end_turn();
             }
-            end_turn();
+            if (x.n > 0) ++nq;
+            if constexpr (kPair) {   // stages only the other stream needs
+              for (int j = 2 * x.n; j < 2 * x.n_shared && ok; ++j) {
+                ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
+                if (ok) mbar_arrive(bar_empty(ring, st));
+                advance();
+              }
+            }
           }
-          if (x.n > 0) ++nq;
-          if constexpr (kPair) {   // stages only the other stream needs
-            for (int j = 2 * x.n; j < 2 * x.n_shared && ok; ++j) {
-              ok = wait_bar(bar_full(ring, st), ph, abort_flag, status, tmo);
-              if (ok) mbar_arrive(bar_empty(ring, st));
-              advance();
-            }
+          if (!ok) {   // what was issued completes before the tensor memory is given back
+            tc_commit(bar_st(w, DRAIN));
+            drain_wait(bar_st(w, DRAIN), 0, tmo);
           }
         }
-        if (!ok) {   // what was issued completes before the tensor memory is given back
-          tc_commit(bar_st(w, DRAIN));
-          drain_wait(bar_st(w, DRAIN), 0, tmo);
-        }
-      }
       }
       __syncwarp();
     }

@@ -7,7 +7,7 @@ import torch
 import sparse_attention_indexer_dsa_gb300 as dsa
 from sparse_attention_indexer_dsa_gb300 import _abi
 from tests.gpu_util import dev, host
-from tests.paged_ref import Batch, attention
+from tests.paged_ref import Batch, attention, quantise, values
 from tests.test_gpu_paged_attention import _close, _queries, _run, _selection
 
 pytestmark = pytest.mark.gpu
@@ -158,3 +158,36 @@ def test_captured_calls_that_share_a_workspace():
     torch.cuda.synchronize()
     for _, out, _, (want, _, tol, _) in runs:
         _close(host(out.double()), want, tol)
+
+
+@pytest.mark.parametrize("group", [1, 4, 5])
+@pytest.mark.parametrize("prec,D,page", [("bf16", 128, 16), ("mxfp8", 128, 32), ("fp8", 128, 8), ("mxfp8", 64, 32)])
+def test_tiles_of_few_rows(prec, D, page, group):
+    """A few tokens of few heads each: at most 16 rows to a tile, of several tokens."""
+    rng = np.random.default_rng(61)
+    b = Batch(rng, [(3, 700), (2, 129), (0, 5), (1, 1), (3, 3), (3, 257)], 2, D, page, prec)
+    _run(b, rng, 2 * group, group)
+    sel, lens = _selection(rng, b, 300, "wild")
+    _run(b, rng, 2 * group, group, sel, lens)
+
+
+@pytest.mark.parametrize("step", [0.05, -0.05, 0.4])
+@pytest.mark.parametrize("group", [4, 16, 24])
+def test_rising_and_falling_logits_of_few_rows(group, step):
+    """Keys whose logits grow (or fall) along the sequence by 2 ** 0.5 .. 2 ** 5 in every one: the
+    running maximum is raised over and over while products are in flight, within split ranges too."""
+    rng = np.random.default_rng(62)
+    b = Batch(rng, [(1, 1500), (1, 640), (1, 90)], 1, 128, 16, "bf16")
+    for d, (_, s) in enumerate(b.lens):
+        for pos in range(s):
+            bits, _ = quantise(np.concatenate([[step * pos], 0.2 * rng.standard_normal(127)])[None], "bf16")
+            b.pages["k"][b.table[d, pos // 16], 0, pos % 16] = bits
+            b.rows["k"][b.cu_k[d] + pos, 0] = values(bits, None, "bf16")
+    q, qd = _queries(rng, 3, group, 128)
+    q[:, :, 0], qd[:, :, 0] = 8.0, 8.0
+    for sel in (None, np.stack([np.concatenate([rng.permutation(s)[:80], np.full(max(0, 80 - s), -1)]) for _, s in b.lens]).astype(np.int32)):
+        out, lse = dsa.paged_attention(qd, b.cache(dsa), b.dev("cu_q"), b.dev("cu_k"), b.dev("table"), 1, 1500, sm_scale=1.0,
+                                       topk_idx=None if sel is None else dev(sel), return_lse=True)
+        want, wl, tol, ltol = attention(b, q, group, 1.0, sel)
+        _close(host(out.double()), want, tol)
+        _close(host(lse.double()), wl, ltol)
