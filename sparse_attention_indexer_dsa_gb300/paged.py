@@ -282,7 +282,7 @@ def cache_read(cache: PagedCache, cu_seqlens_k: torch.Tensor, page_table: torch.
 
 def attention_workspace(total_q: int, num_seqs: int, max_seqlen_q: int, n_heads: int, n_kv_heads: int, head_dim: int,
                         topk_width: int = 0, device=None) -> torch.Tensor:
-    """Device workspace (uint8, 256-byte aligned) for paged_attention."""
+    """Device workspace (uint8, 256-byte aligned) for every paged_attention call of at most these sizes."""
     n = _abi.load().dsa_idx_attention_workspace_size(total_q, num_seqs, max_seqlen_q, n_heads, n_kv_heads, head_dim,
                                                      topk_width)
     if n == 0:
@@ -302,7 +302,9 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, cu_seqlens_q: torch.Tens
     entries.  sm_scale defaults to head_dim ** -0.5.  Returns out [tokens,
     n_heads, head_dim] bf16, or (out, lse fp32 [tokens, n_heads]); `out` is
     such a tensor (or pair) to write into: rows behind the last sequence stay
-    as they were."""
+    as they were.  Forward only: no gradient is recorded.  `ws` from
+    attention_workspace may be of a larger call; calls that may overlap need
+    one each."""
     if cache.v is None:
         raise ValueError("the cache has no values")
     a, dev, (N, Hk, ps, D) = _pages(cache)

@@ -16,16 +16,17 @@ pytestmark = pytest.mark.gpu
 KINDS = {"pair": ([(300, 900)], 0), "solo": ([(1, 900), (1, 300)], 0), "list": ([(3, 900)], 400)}
 
 
+@pytest.mark.parametrize("heads", [8, 24])   # narrow tiles, tiles of 128 rows
 @pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
-def test_a_withheld_tile_times_out_and_the_next_call_is_clean(prec, kind):
+def test_a_withheld_tile_times_out_and_the_next_call_is_clean(prec, kind, heads):
     rng = np.random.default_rng(51)
     lens, W = KINDS[kind]
     b = Batch(rng, lens, 1, 128, 64, prec)
     sel, _ = _selection(rng, b, W, "sorted") if W else (None, None)
-    q, qd = _queries(rng, b.total_q, 8, 128)
+    q, qd = _queries(rng, b.total_q, heads, 128)
     max_q, max_k = max(t for t, _ in lens), max(s for _, s in lens)
-    ws = dsa.attention_workspace(b.total_q, len(lens), max_q, 8, 1, 128, W)
+    ws = dsa.attention_workspace(b.total_q, len(lens), max_q, heads, 1, 128, W)
     lib = _abi.load()
     args = (qd, b.cache(dsa), b.dev("cu_q"), b.dev("cu_k"), b.dev("table"), max_q, max_k)
     lst = None if sel is None else dev(sel)
@@ -39,7 +40,7 @@ def test_a_withheld_tile_times_out_and_the_next_call_is_clean(prec, kind):
         lib.dsa_idx_test_set_timeout_ns(2_000_000_000)
     out = dsa.paged_attention(*args, topk_idx=lst, ws=ws)
     assert dsa.read_status(ws) == 0
-    want, _, tol, _ = attention(b, q, 8, 128 ** -0.5, sel)
+    want, _, tol, _ = attention(b, q, heads, 128 ** -0.5, sel)
     _close(host(out.double()), want, tol)
 
 
