@@ -81,8 +81,8 @@ namespace dsa {
 
 // Two query tiles to a block when the average sequence fills more than one
 // 128-row tile: its keys are then read once for both.  Otherwise the two
-// streams of a block work on their own; tiles of at most 16 rows are narrow
-// (the figures are with the kernel).  Key ranges are divided only while
+// streams of a block work on their own; tiles of at most 16 rows with
+// gathered keys are narrow (the figures are with the kernel).  Key ranges are divided only while
 // there are at most four units to a stream (more balance themselves), and a
 // call's workspace has room for four more units to a stream.
 bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,
@@ -103,7 +103,7 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   const int64_t base = tiles * n_kv;
   const int64_t most = most_undivided(pl->pair);
   pl->max_units = base <= most ? (int)(base + most) : 0;
-  pl->narrow = !pl->pair && D == 128 && pl->rows_cap <= kAttnNarrow;
+  pl->narrow = pl->gather && D == 128 && pl->rows_cap <= kAttnNarrow;
   const int qrows = pl->narrow ? kAttnNarrow : pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
   pl->q_bytes = (uint32_t)qrows * D * 2;
   const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys * D + 512;

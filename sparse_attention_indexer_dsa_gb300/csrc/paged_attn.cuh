@@ -29,13 +29,16 @@
 // softmax warps, to rows that are not there.  There the keys are the products'
 // rows: S^T = K Q^T (128 keys x 16), a key to a softmax thread, P^T through
 // shared memory, O^T += V^T P^T (head_dim x 16).  S and P have two buffers, so
-// the next tile's logits are formed meanwhile.  One token of each of 64
-// sequences, 64 heads, 8 key heads, 2048 - 16384 keys, against tiles of 128
-// rows: 418 us against 425 over MXFP8 (1.2 GB), 376 against 385 over BF16
-// (2.4 GB: 93 % of the copy rate); 2048 listed keys of 4 tokens of each: 496
-// against 605 over MXFP8, 277 against 338 over BF16.  Over 8-bit caches the
-// latency of a stored tile (its load, its widening, the hand-overs) bounds it:
-// shared memory holds two stored tiles to a ring beside the widened ones.
+// the next tile's logits are formed meanwhile.  4 tokens of each of 64
+// sequences, 64 heads, 8 key heads, 2048 listed keys, against tiles of 128 rows:
+// 495 us against 556 over MXFP8, 279 against 321 over BF16; one token and every
+// key, FP8 in pages of 8: 550 against 639.  Rows that TMA brings stay with tiles
+// of 128 rows, which are as fast: a token of each of the 64 over 2048 - 16384
+// keys 379 us over BF16 (2.4 GB, 93 % of the copy rate) either way, 429 against
+// 427 over MXFP8 (1.2 GB), with 8 sequences 75 against 81 and 75 against 77.
+// Over 8-bit caches the latency of a stored tile (its load, its widening, the
+// hand-overs) bounds them: shared memory holds two stored tiles to a ring beside
+// the widened ones.
 // Loaders.  TMA brings all visible keys as a box per page; listed rows are copied
 // one by one with cp.async (TMA row gathers of four came to 27 bytes a cycle and
 // SM, cp.async from eight warps to 60); BF16 in the 128-byte swizzled layout the
@@ -400,7 +403,7 @@ template <int D, bool Q8, int MODE, bool NARROW>
 __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ AttnParams p) {
   using R = Roles<Q8, MODE, NARROW>;
-  static_assert(!NARROW || (D == 128 && MODE != PAIR), "a narrow tile's values are the 128 rows of its second product");
+  static_assert(!NARROW || (D == 128 && MODE == GATHER), "a narrow tile's values are the 128 rows of its second product");
   constexpr bool kPair = MODE == PAIR;
   constexpr bool kWorkerCopies = MODE == GATHER && !Q8;   // stages written by cp.async: fenced by the MMA warp
   constexpr uint32_t kStage = kAttnKeys * D * 2;     // one tile of keys or values
@@ -1178,17 +1181,18 @@ __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
         constexpr uint32_t idesc_pv = idesc_bf16(kAttnRows, D) | (1u << 16);   // V: rows of keys, N contiguous
         if (elect_one()) {
           const uint32_t q_rows_bytes = pl.q_bytes / (D / 64);   // one 64-column chunk of the query tile
-          // Two tiles of one stream of keys issue PV and the next QK as one block, in turns, so that one's
-          // softmax runs beside the other's products: 4096 tokens over 32768 BF16 keys 2.89 against 2.92 ms.
-          // (Independent streams are as fast or faster without: selected rows 596 against 604 us.)  Nothing
-          // is waited for inside a turn, so a turn always comes; only the times depend on it.
+          // The streams issue PV and the next QK as one block, in turns, so that one's softmax runs beside
+          // the other's products: 4096 tokens over 32768 BF16 keys 2.89 against 2.92 ms, a token of each
+          // sequence over MXFP8 425 against 451 us.  (Gathered rows are faster without: 596 against 604 us.)
+          // Nothing is waited for inside a turn, so a turn always comes; only the times depend on it.
+          constexpr bool kTurns = MODE != GATHER;
           int* const turn = ctl + 4;
           auto take_turn = [&] {
-            for (int i = 0; kPair && i < (1 << 20) && atomicCAS_block(turn, 0, 1) != 0; ++i) {
+            for (int i = 0; kTurns && i < (1 << 20) && atomicCAS_block(turn, 0, 1) != 0; ++i) {
             }
           };
           auto end_turn = [&] {
-            if (kPair) atomicExch_block(turn, 0);
+            if (kTurns) atomicExch_block(turn, 0);
           };
           // (the 128 rows that the products read begin before the tile when its rows are not the first:
           // with 32 or 64 rows a tile, still inside the first stream's)

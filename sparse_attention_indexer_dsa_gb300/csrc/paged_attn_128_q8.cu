@@ -5,9 +5,7 @@ namespace dsa {
 
 cudaError_t launch_paged_attention_128_q8(const AttnParams& p, int grid, int sm_count, cudaStream_t stream) {
   if (p.plan.pair) return attn::launch<128, true, attn::PAIR>(p, grid, sm_count, stream);
-  if (p.plan.narrow)
-    return p.plan.gather ? attn::launch<128, true, attn::GATHER, true>(p, grid, sm_count, stream)
-                         : attn::launch<128, true, attn::SOLO, true>(p, grid, sm_count, stream);
+  if (p.plan.narrow) return attn::launch<128, true, attn::GATHER, true>(p, grid, sm_count, stream);
   if (p.plan.gather) return attn::launch<128, true, attn::GATHER>(p, grid, sm_count, stream);
   return attn::launch<128, true, attn::SOLO>(p, grid, sm_count, stream);
 }
