@@ -159,7 +159,11 @@ def _tokens(t: Optional[torch.Tensor], name: str, device: torch.device, dtypes, 
         return t.data_ptr() or None, 0
     if t.stride(2) != 1 or (t.stride(1) != head_dim and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.data_ptr() or None, (t.stride(0) if t.shape[0] > 1 else 0)
+    if t.shape[0] < 2:
+        return t.data_ptr() or None, 0
+    if t.stride(0) < heads * head_dim:   # (an expanded tensor's 0 would be taken for packed tokens)
+        raise ValueError(f"{name}: tokens must not share memory (an expanded tensor is copied first)")
+    return t.data_ptr() or None, t.stride(0)
 
 
 def _pages(c: PagedCache):
@@ -191,7 +195,7 @@ def cache_write(cache: PagedCache, k: torch.Tensor, v: Optional[torch.Tensor], c
     """Store the new tokens' rows in the cache's format (dsa_idx_cache_write).
 
     k, v [tokens, n_kv_heads, head_dim], fp32 or bf16 (views with a token
-    stride are taken as they are); v None for a cache of keys alone.  With an
+    stride are taken as they are, tokens that share memory are refused); v None for a cache of keys alone.  With an
     8-bit cache, uint8 k and v are E4M3 codes in operand form (as preprocess
     gives them) and k_scale, v_scale their UE8M0 bytes."""
     a, dev, (N, Hk, ps, D) = _pages(cache)
@@ -297,7 +301,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, cu_seqlens_q: torch.Tens
     """Attention of the new tokens over the cache (dsa_idx_paged_attention).
 
     q [tokens, n_heads, head_dim] bf16 (a view with a token stride is taken as
-    it is).  topk_idx int32 [tokens, W] restricts every query to the listed
+    it is, tokens that share memory are refused).  topk_idx int32 [tokens, W] restricts every query to the listed
     positions (score_topk's rows), topk_len int32 [tokens] to a row's first
     entries.  sm_scale defaults to head_dim ** -0.5.  Returns out [tokens,
     n_heads, head_dim] bf16, or (out, lse fp32 [tokens, n_heads]); `out` is
