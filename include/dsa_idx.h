@@ -364,6 +364,8 @@ dsa_status_t dsa_idx_score_topk_noalloc_status(dsa_stream_t stream, dsa_status_t
  *   ws           device workspace, 256-byte aligned; its status is read with
  *                dsa_idx_read_status.  Calls that may overlap on the GPU need
  *                a workspace each
+ * With total_q (total_k) = 0 the packed tensors may be NULL: empty ones have no
+ * address.
  * T_d > S_d, a position behind max_pages, a page outside [0, num_pages) and a
  * prefix that ends above its total are found on the device:
  * DSA_ERR_INVALID_ARG in the status; nothing outside the caller's tensors is

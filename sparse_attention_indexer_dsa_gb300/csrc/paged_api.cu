@@ -169,7 +169,7 @@ dsa_status_t dsa_idx_cache_write(const void* k, int64_t k_stride, const uint8_t*
   if (scale_rule != DSA_MX_SCALE_NOSAT && scale_rule != DSA_MX_SCALE_FLOOR) return fail(DSA_ERR_INVALID_ARG, "scale_rule");
   int elem;
   if (in_dtype == DSA_DTYPE_OPERAND && prec != DSA_PREC_BF16) {
-    if (!k_scale || (v && !v_scale)) return fail(DSA_ERR_INVALID_ARG, "codes come with their scales");
+    if (total_q > 0 && (!k_scale || (v && !v_scale))) return fail(DSA_ERR_INVALID_ARG, "codes come with their scales");
     p.src = 2;
     elem = 1;
   } else if (in_dtype == DSA_DTYPE_F32) {
@@ -218,7 +218,7 @@ dsa_status_t dsa_idx_cache_read(const void* k_pages, const uint8_t* k_page_scale
   if (v_out && !v_pages) return fail(DSA_ERR_INVALID_ARG, "the cache has no values");
   if (total_k < 0) return fail(DSA_ERR_INVALID_ARG, "sizes");
   if ((int64_t)total_k * n_kv_heads >= (int64_t)1 << 30) return fail(DSA_ERR_UNSUPPORTED, "total_k * n_kv_heads above 2^30");
-  if (prec != DSA_PREC_BF16 && !dequantize && (!k_scale_out || (v_out && !v_scale_out)))
+  if (total_k > 0 && prec != DSA_PREC_BF16 && !dequantize && (!k_scale_out || (v_out && !v_scale_out)))
     return fail(DSA_ERR_INVALID_ARG, "codes come with their scales");
   if (!aligned16(k_out) || !aligned16(v_out)) return fail(DSA_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
   if ((s = check_ws(ws, ws_bytes, DSA_DEV_STATUS_HEADER_BYTES)) != DSA_OK) return s;

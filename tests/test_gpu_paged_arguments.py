@@ -26,3 +26,24 @@ def test_expanded_tokens_are_refused():
         dsa.paged_attention(q.expand(8, 4, 64), c, *args, 5, 40)
     torch.cuda.synchronize()
     _check_pages(c, b, b.pages, b.scales)
+
+
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8", "fp8"])
+def test_no_tokens_at_all(prec):
+    """Empty tensors in every form that a call takes: nothing is refused, nothing is touched."""
+    b = Batch(np.random.default_rng(72), [(0, 0), (0, 0)], 1, 128, 16, prec)
+    c, ws = b.cache(dsa), dsa.cache_workspace()
+    args = (b.dev("cu_q"), b.dev("cu_k"), b.dev("table"))
+    rows = lambda dt: torch.empty((0, 1, 128), dtype=dt, device="cuda")
+    for dt in (torch.float32, torch.bfloat16):
+        dsa.cache_write(c, rows(dt), rows(dt), *args, ws=ws)
+        assert dsa.read_status(ws) == 0
+    if prec != "bf16":
+        sc = torch.empty((0, 1, 4 if prec == "mxfp8" else 1), dtype=torch.uint8, device="cuda")
+        dsa.cache_write(c, rows(torch.uint8), rows(torch.uint8), *args, k_scale=sc, v_scale=sc, ws=ws)
+        assert dsa.read_status(ws) == 0
+    for to in (None, "bf16"):
+        k, ks, v, vs = dsa.cache_read(c, *args[1:], 0, out_prec=to, ws=ws)
+        assert dsa.read_status(ws) == 0 and k.shape == v.shape == (0, 1, 128)
+        assert (ks is None) == (vs is None) == (prec == "bf16" or to == "bf16")
+    _check_pages(c, b, b.pages, b.scales)

@@ -3,7 +3,8 @@ that they have to take: nothing here reaches a GPU."""
 import pytest
 import torch
 
-from sparse_attention_indexer_dsa_gb300 import paged
+from sparse_attention_indexer_dsa_gb300 import _abi, paged
+from tests.test_paged_host import _read, _write, lib  # noqa: F401
 
 CPU = torch.device("cpu")
 
@@ -40,3 +41,19 @@ def test_tokens_that_share_memory_are_refused(view):
 def test_one_head_expanded_over_tokens_is_refused():
     with pytest.raises(ValueError):
         _tokens(torch.zeros((1, 1, 64), dtype=torch.bfloat16).expand(5, 1, 64), heads=1)
+
+
+@pytest.mark.parametrize("prec", [0, 1, 2])
+@pytest.mark.parametrize("v", [True, False])
+def test_no_tokens_have_no_addresses(lib, prec, v):  # noqa: F811
+    """Empty tensors have no address, of rows, codes and scales alike: no argument is missing then (what
+    is left to fail here is the missing device)."""
+    refused = (_abi.DSA_ERR_INVALID_ARG, _abi.DSA_ERR_UNSUPPORTED, _abi.DSA_ERR_WORKSPACE)
+    pages = {} if v else dict(vp=None, vps=None)
+    for src in (_abi.DSA_DTYPE_F32, _abi.DSA_DTYPE_BF16, _abi.DSA_DTYPE_OPERAND):
+        assert _write(lib, total_q=0, k=None, v=None, k_scale=None, v_scale=None, in_dtype=src, prec=prec, **pages) not in refused
+    for deq in (0, 1):
+        assert _read(lib, total_k=0, k=None, v=None, ks=None, vs=None, deq=deq, prec=prec, **pages) not in refused
+    if prec:
+        assert _write(lib, total_q=1, k_scale=None, in_dtype=_abi.DSA_DTYPE_OPERAND, prec=prec) == _abi.DSA_ERR_INVALID_ARG
+        assert _read(lib, total_k=1, ks=None, prec=prec) == _abi.DSA_ERR_INVALID_ARG
