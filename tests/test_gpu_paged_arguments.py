@@ -31,9 +31,10 @@ def test_expanded_tokens_are_refused():
 @pytest.mark.parametrize("prec", ["bf16", "mxfp8", "fp8"])
 def test_no_tokens_at_all(prec):
     """Empty tensors in every form that a call takes: nothing is refused, nothing is touched."""
-    b = Batch(np.random.default_rng(72), [(0, 0), (0, 0)], 1, 128, 16, prec)
+    b = Batch(np.random.default_rng(72), [(0, 5), (0, 0)], 1, 128, 16, prec)
     c, ws = b.cache(dsa), dsa.cache_workspace()
-    args = (b.dev("cu_q"), b.dev("cu_k"), b.dev("table"))
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    args = (none, none, b.dev("table"))
     rows = lambda dt: torch.empty((0, 1, 128), dtype=dt, device="cuda")
     for dt in (torch.float32, torch.bfloat16):
         dsa.cache_write(c, rows(dt), rows(dt), *args, ws=ws)
