@@ -43,6 +43,7 @@ def test_one_head_expanded_over_tokens_is_refused():
         _tokens(torch.zeros((1, 1, 64), dtype=torch.bfloat16).expand(5, 1, 64), heads=1)
 
 
+@pytest.mark.no_device
 @pytest.mark.parametrize("prec", [0, 1, 2])
 @pytest.mark.parametrize("v", [True, False])
 def test_no_tokens_have_no_addresses(lib, prec, v):  # noqa: F811
@@ -57,3 +58,23 @@ def test_no_tokens_have_no_addresses(lib, prec, v):  # noqa: F811
     if prec:
         assert _write(lib, total_q=1, k_scale=None, in_dtype=_abi.DSA_DTYPE_OPERAND, prec=prec) == _abi.DSA_ERR_INVALID_ARG
         assert _read(lib, total_k=1, ks=None, prec=prec) == _abi.DSA_ERR_INVALID_ARG
+
+
+def test_made_up_addresses_stay_off_a_gpu(monkeypatch):
+    """Where there is a GPU, the collection skips every test that would hand a kernel a made-up address."""
+    from tests import conftest
+
+    class Item:
+        def __init__(self, name, *keywords):
+            self.originalname, self.keywords, self.marks = name, set(keywords), []
+
+        def add_marker(self, m):
+            self.marks.append(m)
+
+    items = [Item(n) for n in sorted(conftest.MADE_UP_ADDRESSES)] + [Item("x", "no_device"), Item("y"), Item("z", "gpu")]
+    monkeypatch.setattr(conftest, "gpu_available", lambda: True)
+    conftest.pytest_collection_modifyitems(None, items)
+    assert [len(i.marks) for i in items] == [1] * len(conftest.MADE_UP_ADDRESSES) + [1, 0, 0]
+    from tests import test_abi, test_paged_host
+    for n in conftest.MADE_UP_ADDRESSES:
+        assert hasattr(test_abi, n) or hasattr(test_paged_host, n)
