@@ -366,11 +366,12 @@ dsa_status_t dsa_idx_score_topk_noalloc_status(dsa_stream_t stream, dsa_status_t
  *                a workspace each
  * With total_q (total_k) = 0 the packed tensors may be NULL: empty ones have no
  * address.
- * T_d > S_d, a position behind max_pages, a page outside [0, num_pages) and a
- * prefix that ends above its total are found on the device:
+ * T_d > S_d, a position behind max_pages, a page outside [0, num_pages), a
+ * prefix that falls and one that ends above its total are found on the device:
  * DSA_ERR_INVALID_ARG in the status; nothing outside the caller's tensors is
  * touched, and the rows concerned are not written (write, read) or
- * unspecified (attention).
+ * unspecified (attention).  Where a prefix falls, write and read take a packed
+ * row for a row of one of the sequences that hold it, or leave it.
  * ------------------------------------------------------------------------- */
 
 /* Workspace bytes of dsa_idx_cache_write and dsa_idx_cache_read. */

@@ -51,6 +51,18 @@ struct Place {
   }
 };
 
+// Whether a prefix falls, or (packed rows) starts below 0: tokens would count for several sequences or
+// for none.  The grid's threads look at a sequence each; what one finds goes to its block's status.
+template <bool PACKED>
+__device__ __forceinline__ bool falls(const int32_t* cu, int num_seqs) {
+  bool bad = false;
+  for (uint32_t d = blockIdx.x * kThreads + threadIdx.x; d < (uint32_t)num_seqs; d += gridDim.x * kThreads) {
+    const int a = __ldg(cu + d);
+    bad |= __ldg(cu + d + 1) < a || (PACKED && a < 0);
+  }
+  return bad;
+}
+
 // Eight elements of a source row, as FP32 bits or as two words of codes.
 template <int SRC>
 struct Piece {
@@ -111,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
   const uint32_t items = ((p.total_q + RPS * U - 1) / (RPS * U)) * heads;   // below 2^31 (checked by the caller)
   const uint32_t carry = mx_carry(p.rule);
   bool bad = blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.cu_q + p.num_seqs) > p.total_q;
+  bad |= falls<true>(p.cu_q, p.num_seqs) | falls<false>(p.cu_k, p.num_seqs);
   Place at;
   for (uint32_t it = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += gridDim.x * (kThreads / 32)) {
     const uint32_t block = it / heads, hh = it - block * heads;
@@ -178,6 +191,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
   const uint32_t n_kv = p.c.n_kv, heads = p.v ? 2 * n_kv : n_kv;   // key heads, then value heads
   const uint32_t items = ((p.total_k + RPS * U - 1) / (RPS * U)) * heads;   // below 2^31 (checked by the caller)
   bool bad = blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.cu_k + p.num_seqs) > p.total_k;
+  bad |= falls<true>(p.cu_k, p.num_seqs);
   Place at;
   for (uint32_t it = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += gridDim.x * (kThreads / 32)) {
     const uint32_t block = it / heads, hh = it - block * heads;
