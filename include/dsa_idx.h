@@ -386,8 +386,8 @@ size_t dsa_idx_cache_workspace_size(void);
  *   k_scale, v_scale  DSA_DTYPE_OPERAND with an 8-bit cache: the packed rows'
  *              scale bytes, as dsa_idx_preprocess writes them; else NULL
  * Two tokens of one call must not share a slot (the result is one of the two).
- * Non-finite elements give unspecified codes, as in the quantisers.
- * total_q * n_kv_heads < 2^30. */
+ * Non-finite elements give unspecified codes, as in the quantisers (a NaN stays
+ * one).  total_q * n_kv_heads < 2^30. */
 dsa_status_t dsa_idx_cache_write(
     const void* k, int64_t k_stride, const uint8_t* k_scale,
     const void* v, int64_t v_stride, const uint8_t* v_scale,
@@ -401,7 +401,8 @@ dsa_status_t dsa_idx_cache_write(
 /* Rows 0 .. S_d - 1 of every sequence, packed in cu_seqlens_k's order.
  *   dequantize  0: as stored (codes and scales: with n_kv_heads = 1 the key
  *               operand of dsa_idx_score_topk_kv); 1: BF16 values code * 2^e
- *               (exact while the value is in BF16's range)
+ *               (exact while the value is in BF16's range; NaN for the NaN
+ *               code and for scale byte 255)
  *   k_out, v_out  device [total_k, n_kv_heads, head_dim], codes or bf16;
  *               v_out NULL: keys alone
  *   k_scale_out, v_scale_out  device u8 [total_k, n_kv_heads, head_dim/32] or
@@ -443,7 +444,10 @@ size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqle
  * reported in the status and not computed; nothing is computed when
  * cu_seqlens_q falls).  Rows 0 .. S_d - 1 of a sequence (with topk_idx: the
  * listed ones) must be finite; what other slots of its pages hold does not
- * matter.  out and lse share no memory with the inputs.  total_q * n_heads <
+ * matter.  A NaN among them makes the result of the queries that see it NaN
+ * (8-bit: as the quantisers store it, or under scale byte 255; a NaN code under
+ * a scale byte up to 134, which none of them writes, reads as 480 * 2^e), and
+ * that of the sequence's other queries unspecified.  out and lse share no memory with the inputs.  total_q * n_heads <
  * 2^30, max_seqlen_k and topk_width at most 2^30.  With total_q = 0 topk_idx
  * may be NULL whatever topk_width is.  The same inputs give the same bits. */
 dsa_status_t dsa_idx_paged_attention(

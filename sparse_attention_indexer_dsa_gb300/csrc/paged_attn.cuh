@@ -301,9 +301,13 @@ __device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
 
 // Sixteen E4M3 codes to BF16, times 2^(e8 - 127).  Code bits s.eeee.mmm placed at a BF16's sign, low
 // exponent and high mantissa bits read as value * 2^-120 (subnormals included); one exact product with
-// 2^(120 + e) restores it.
+// 2^(120 + e) restores it.  That is a BF16 up to e8 = 134; FAR: beyond it (values over 2^16) there is a
+// second factor.  The NaN code reads as 480 that way.  The quantisers' scale of a block with a NaN is at
+// least 247 (the bits of its magnitude are the largest), so every NaN that they stored is FAR, and is put
+// back there; so is scale 255, which is NaN.
+template <bool FAR>
 __device__ __forceinline__ void widen16(const uint32_t (&w4)[4], uint32_t e8, uint32_t (&o)[8]) {
-  const uint32_t first = e8 > 134u ? 254u : e8 + 120u;         // 2^(first - 127): BF16 ends at 2^127
+  const uint32_t first = FAR ? 254u : e8 + 120u;               // 2^(first - 127): BF16 ends at 2^127
   __nv_bfloat162 f;
   *reinterpret_cast<uint32_t*>(&f) = (first << 7) * 0x00010001u;
 #pragma unroll
@@ -316,13 +320,15 @@ __device__ __forceinline__ void widen16(const uint32_t (&w4)[4], uint32_t e8, ui
       o[2 * q4 + hlf] = *reinterpret_cast<uint32_t*>(&v);
     }
   }
-  if (e8 > 134u) {                                             // values beyond 2^16: a second factor
+  if constexpr (FAR) {
     __nv_bfloat162 f2;
     *reinterpret_cast<uint32_t*>(&f2) = ((e8 - 134u + 127u) << 7) * 0x00010001u;
+    const __nv_bfloat162 most = __float2bfloat162_rn(e8 == 255u ? -1.f : 57344.f);   // 448 * 2^7: of the numbers
 #pragma unroll
     for (int q8 = 0; q8 < 8; ++q8) {
-      __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[q8]), f2);
-      o[q8] = *reinterpret_cast<uint32_t*>(&v);
+      const __nv_bfloat162 w = *reinterpret_cast<__nv_bfloat162*>(&o[q8]);
+      __nv_bfloat162 v = __hmul2(w, f2);
+      o[q8] = *reinterpret_cast<uint32_t*>(&v) | __hgt2_mask(__habs2(w), most);
     }
   }
 }
@@ -776,6 +782,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
           const uint8_t* scales = smem + pl.off_raw + (size_t)(ring * pl.nraw + slot) * kRawItem + kAttnKeys * D + s0;
           const int valid = meta[slot] - rsub;
           const uint32_t dst = ring_base + (uint32_t)st * kStage;
+          uint32_t top = 0;   // of the tile's scales
           constexpr int kBatch = kPasses % 4 == 0 ? 4 : (kPasses % 2 == 0 ? 2 : 1);   // passes whose loads go first
 #pragma unroll
           for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
@@ -796,9 +803,24 @@ __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) w4[i][q] = 0;
               }
-              widen16(w4[i], e8[i], o);
+              top = max(top, e8[i]);
+              widen16<false>(w4[i], e8[i], o);
               st_shared_v4(dst + at0 + (i0 + i) * RPP * 128, o[0], o[1], o[2], o[3]);
               st_shared_v4(dst + at1 + (i0 + i) * RPP * 128, o[4], o[5], o[6], o[7]);
+            }
+          }
+          // Far scales once more, in a loop of its own: as code of every unrolled pass it cost all tiles
+          // (a token of each of 64 sequences over MXFP8 441 against 416 us).
+          if (top > 134u) {
+#pragma unroll 1
+            for (int r = 0; r < kAttnKeys - rsub; r += RPP) {
+              const uint32_t e = scales[r * sw];
+              if (e <= 134u || r >= valid) continue;
+              uint32_t w4[4], o[8];
+              ld_shared_v4(raw + r * D, w4);
+              widen16<true>(w4, e, o);
+              st_shared_v4(dst + at0 + r * 128, o[0], o[1], o[2], o[3]);
+              st_shared_v4(dst + at1 + r * 128, o[4], o[5], o[6], o[7]);
             }
           }
           __syncwarp();

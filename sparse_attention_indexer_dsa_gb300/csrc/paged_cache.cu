@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
         }
       } else {
         // code * 2^e is exact in FP32, and in BF16 unless it is below BF16's range
-        const float f = sc[u] == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(sc[u] << 23);
+        const float f = __uint_as_float(max(sc[u] << 23, 0x00400000u) | (sc[u] + 1) >> 8 << 22);   // (255: NaN)
         const uint32_t w[2] = {x[u].x, x[u].y};
         uint4 o;
 #pragma unroll

@@ -7,8 +7,8 @@ import torch
 import sparse_attention_indexer_dsa_gb300 as dsa
 from sparse_attention_indexer_dsa_gb300 import _abi
 from tests.gpu_util import dev, host
-from tests.paged_ref import Batch
-from tests.test_gpu_paged_attention import _queries
+from tests.paged_ref import Batch, attention
+from tests.test_gpu_paged_attention import _close, _queries, _selection
 from tests.test_gpu_paged_cache import _check_pages
 
 pytestmark = pytest.mark.gpu
@@ -104,3 +104,58 @@ def test_many_sequences_prefixes_are_looked_at_to_the_end():
             cu[at + 1] += 2                            # above its right neighbour
         dsa.cache_write(c, x, x, dev(cu), ck, tb, ws=ws)
         assert dsa.read_status(ws) == (0 if at is None else _abi.DSA_ERR_INVALID_ARG), at
+
+
+# (tokens, cached) of the first sequence, heads to a key head, width of the lists: pairs of query tiles,
+# single tiles, lists over tiles of 128 rows and narrow ones
+NAN_KINDS = {"pair": ((300, 700), 8, 0), "solo": ((1, 700), 8, 0), "list": ((3, 700), 24, 300), "narrow": ((3, 700), 4, 300)}
+
+
+@pytest.mark.parametrize("how", ["written", "stored", "scale 255"])
+@pytest.mark.parametrize("kind", list(NAN_KINDS))
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8", "fp8"])
+def test_a_nan_stays_a_nan(prec, kind, how):
+    """A NaN in a row that every query of sequence 0 sees: written with the new tokens, or among the
+    stored rows.  In K the results of its key head's queries are NaN, in V those of the element; the
+    other key head and the other sequence have their own results, bit by bit within the bound."""
+    if how == "scale 255" and prec == "bf16":
+        pytest.skip("no scales")
+    rng = np.random.default_rng(76)
+    (t, s), group, W = NAN_KINDS[kind]
+    b = Batch(rng, [(t, s), (1, 200)], 2, 128, 16, prec)
+    sel = None
+    if W:
+        sel = _selection(rng, b, W, "sorted")[0]
+        sel[:t, 0] = s - t
+    q, qd = _queries(rng, b.total_q, 2 * group, 128)
+    cu_q, cu_k, tb = b.dev("cu_q"), b.dev("cu_k"), b.dev("table")
+    pos, dim = s - t, 70                       # the first new token: visible to all of them
+    pg, sl = int(b.table[0, pos // 16]), pos % 16
+    for n in b.names:
+        c = b.cache(dsa)
+        if how == "written":
+            new = {m: np.concatenate([b.rows[m][e - u:e] for e, (u, _) in zip(b.cu_k[1:], b.lens)]) for m in b.names}
+            new[n][0, 1, dim] = np.nan
+            dsa.cache_write(c, dev(new["k"].astype(np.float32)), dev(new["v"].astype(np.float32)), cu_q, cu_k, tb)
+        elif prec == "bf16":
+            getattr(c, n)[pg, 1, sl, dim] = float("nan")
+        elif how == "stored":
+            getattr(c, n)[pg, 1, sl, dim] = 0xFF
+            getattr(c, n + "_scale")[pg, 1, sl] = 248
+        else:
+            getattr(c, n + "_scale")[pg, 1, sl] = 255
+        back = dsa.cache_read(c, cu_k, tb, b.total_k, out_prec="bf16")[0 if n == "k" else 2]
+        gone = torch.isnan(back)
+        assert bool(gone[pos, 1, dim]) and not bool(gone[:, 0].any()) and int(gone[:, 1].any(1).sum()) == 1
+        out, lse = dsa.paged_attention(qd, c, cu_q, cu_k, tb, t, s, topk_idx=None if sel is None else dev(sel),
+                                       return_lse=True)
+        want, wl, tol, ltol = attention(b, q, group, 128 ** -0.5, sel)
+        got, gl = host(out.double()), host(lse.double())
+        if n == "k":
+            assert np.isnan(got[:t, group:]).all() and np.isnan(gl[:t, group:]).all()
+        else:
+            assert np.isnan(got[:t, group:, dim]).all()
+            _close(gl[:t, group:], wl[:t, group:], ltol[:t, group:])
+        _close(got[:, :group], want[:, :group], tol[:, :group])
+        _close(got[t:], want[t:], tol[t:])
+        _close(gl[:, :group], wl[:, :group], ltol[:, :group])
