@@ -438,8 +438,8 @@ size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqle
  *   out         device bf16 [total_q, n_heads, head_dim]
  *   lse         device fp32 [total_q, n_heads] or NULL: log of the sum of
  *               exp(sm_scale q.k) over the seen keys
- * A query that sees no key gets out = 0 and lse = -inf.  sm_scale is finite and
- * not negative; n_heads a multiple of n_kv_heads, at most 128 heads to one;
+ * A query that sees no key gets out = 0 and lse = -inf.  sm_scale is finite
+ * (as is sm_scale * log2(e)) and not negative; n_heads a multiple of n_kv_heads, at most 128 heads to one;
  * max_seqlen_q and max_seqlen_k bound T_d and S_d (a longer sequence is
  * reported in the status and not computed; nothing is computed when
  * cu_seqlens_q falls).  Rows 0 .. S_d - 1 of a sequence (with topk_idx: the

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <limits>
 
 #include "dsa_idx.h"
 #include "dsa_status_codes.h"
@@ -280,7 +281,9 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
   // (key tiles are counted in 32 bits)
   if (max_seqlen_k > (1 << 30) || topk_width > (1 << 30))
     return fail(DSA_ERR_UNSUPPORTED, "max_seqlen_k and topk_width are at most 2^30");
-  if (!(sm_scale >= 0.f) || std::isinf(sm_scale)) return fail(DSA_ERR_INVALID_ARG, "sm_scale must be finite and >= 0");
+  const float scale_log2 = sm_scale * 1.4426950408889634f;
+  if (!(sm_scale >= 0.f) || std::isinf(scale_log2))
+    return fail(DSA_ERR_INVALID_ARG, "sm_scale and sm_scale * log2(e) must be finite and >= 0");
   // (an empty list tensor has no address)
   if (topk_width < 0 || (topk_idx && topk_width < 1) || (!topk_idx && total_q > 0 && (topk_width > 0 || topk_len)))
     return fail(DSA_ERR_INVALID_ARG, "topk_width and topk_len belong to topk_idx");
@@ -305,8 +308,9 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
   p.max_seqlen_k = max_seqlen_k;
   p.n_heads = n_heads;
   p.group = n_heads / n_kv_heads;
-  // a masked logit is -inf times the scale: 0 is stood in for by a scale that no finite logit survives
-  p.scale_log2 = fmaxf(sm_scale * 1.4426950408889634f, 1e-37f);
+  // a masked logit is -inf times the scale: 0 is stood in for by the least number, times which the
+  // largest logit is 2^-21
+  p.scale_log2 = fmaxf(scale_log2, std::numeric_limits<float>::denorm_min());
   p.out = out;
   p.lse = lse;
   p.hdr = reinterpret_cast<int*>(ws);

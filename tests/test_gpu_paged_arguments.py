@@ -7,7 +7,7 @@ import torch
 import sparse_attention_indexer_dsa_gb300 as dsa
 from sparse_attention_indexer_dsa_gb300 import _abi
 from tests.gpu_util import dev, host
-from tests.paged_ref import Batch, attention
+from tests.paged_ref import Batch, attention, quantise, values
 from tests.test_gpu_paged_attention import _close, _queries, _selection
 from tests.test_gpu_paged_cache import _check_pages
 
@@ -159,3 +159,31 @@ def test_a_nan_stays_a_nan(prec, kind, how):
         _close(got[:, :group], want[:, :group], tol[:, :group])
         _close(got[t:], want[t:], tol[t:])
         _close(gl[:, :group], wl[:, :group], ltol[:, :group])
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -126, 2.0 ** -140])
+@pytest.mark.parametrize("kind", list(NAN_KINDS))
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+def test_the_smallest_scales_on_the_largest_logits(prec, kind, scale):
+    """Products of +-2^126: a scale of 0 gives every seen key the same weight, one of 2^-126 the
+    logits +-1, one below FP32's normal numbers next to none."""
+    rng = np.random.default_rng(77)
+    (t, s), group, W = NAN_KINDS[kind]
+    b = Batch(rng, [(t, s)], 1, 128, 16, prec)
+    row = np.zeros((s, 1, 128))
+    row[:, 0, 0] = rng.choice([-1.0, 1.0], s) * 2.0 ** 63
+    st, sc = quantise(row, prec)
+    b.rows["k"] = values(st, sc, prec)
+    for pos in range(s):
+        b.pages["k"][b.table[0, pos // 16], :, pos % 16] = st[pos]
+        if sc is not None:
+            b.scales["k"][b.table[0, pos // 16], :, pos % 16] = sc[pos]
+    q = np.zeros((t, group, 128))
+    q[:, :, 0] = 2.0 ** 63
+    sel = _selection(rng, b, W, "sorted")[0] if W else None
+    out, lse = dsa.paged_attention(dev(q.astype(np.float32)).to(torch.bfloat16), b.cache(dsa), b.dev("cu_q"), b.dev("cu_k"),
+                                   b.dev("table"), t, s, sm_scale=scale, topk_idx=None if sel is None else dev(sel),
+                                   return_lse=True)
+    want, wl, tol, ltol = attention(b, q, group, scale, sel)
+    _close(host(out.double()), want, tol)
+    _close(host(lse.double()), wl, ltol)

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from sparse_attention_indexer_dsa_gb300 import _abi, paged
-from tests.test_paged_host import _read, _write, lib  # noqa: F401
+from tests.test_paged_host import _attend, _read, _write, lib  # noqa: F401
 
 CPU = torch.device("cpu")
 
@@ -78,3 +78,9 @@ def test_made_up_addresses_stay_off_a_gpu(monkeypatch):
     from tests import test_abi, test_paged_host
     for n in conftest.MADE_UP_ADDRESSES:
         assert hasattr(test_abi, n) or hasattr(test_paged_host, n)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38, float("inf"), -1e-45, float("nan")])
+def test_scales_that_no_logit_takes(lib, scale):  # noqa: F811
+    """sm_scale is multiplied by log2(e) on its way: what overflows there is refused as an infinity is."""
+    assert _attend(lib, scale=scale) == _abi.DSA_ERR_INVALID_ARG
