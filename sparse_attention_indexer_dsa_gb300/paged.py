@@ -112,8 +112,10 @@ def paged_cache(num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, 
 
 # The checks of one call run in a few microseconds of host time, a good part of
 # a single-token call: one comparison per property, and the message only when one fails.
-_stream = torch._C._cuda_getCurrentRawStream        # of a device index
-_current = torch._C._cuda_getDevice
+# (torch's own lookups behind its public functions; a torch without CUDA lacks them, and is imported all the same)
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, device: torch.device, args) -> int:

@@ -1,5 +1,9 @@
 """Arguments of the paged-cache binding that the kernels must never see, and those
 that they have to take: nothing here reaches a GPU."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -84,3 +88,17 @@ def test_made_up_addresses_stay_off_a_gpu(monkeypatch):
 def test_scales_that_no_logit_takes(lib, scale):  # noqa: F811
     """sm_scale is multiplied by log2(e) on its way: what overflows there is refused as an infinity is."""
     assert _attend(lib, scale=scale) == _abi.DSA_ERR_INVALID_ARG
+
+
+def test_the_package_is_imported_without_cuda_in_torch():
+    """A torch built without CUDA has no such names in torch._C; the paged cache's handle still works there."""
+    code = ("import torch\n"
+            "for n in [n for n in vars(torch._C) if n.startswith('_cuda_')]: delattr(torch._C, n)\n"
+            "import sparse_attention_indexer_dsa_gb300 as dsa\n"
+            "k = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16)\n"
+            "assert dsa.PagedCache(k, None, k, None).page_size == 16\n"
+            "from sparse_attention_indexer_dsa_gb300 import paged\n"
+            "assert callable(paged._stream) and callable(paged._current)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
