@@ -85,7 +85,7 @@ def workspace(total_tokens: int, num_seqs: int, max_seqlen: int, n_heads: int, h
                                            index_topk, kpool_size, _prec(prec))
     if n == 0:
         raise ValueError("invalid workspace sizes")
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def preprocess(q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tensor, max_seqlen: int,

@@ -99,7 +99,7 @@ def paged_cache(num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, 
     dt = torch.bfloat16 if prec == "bf16" else torch.uint8
 
     def pages():
-        t = torch.zeros(shape, dtype=dt, device=device or "cuda")
+        t = torch.zeros(shape, dtype=dt, device="cuda" if device is None else device)
         if prec == "bf16":
             return t, None
         n = head_dim // 32 if prec == "mxfp8" else 1
@@ -187,7 +187,7 @@ def _table(page_table: torch.Tensor, device: torch.device):
 
 def cache_workspace(device=None) -> torch.Tensor:
     """Device workspace for cache_write and cache_read (read_status reads it)."""
-    return torch.empty(_abi.load().dsa_idx_cache_workspace_size(), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(_abi.load().dsa_idx_cache_workspace_size(), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def cache_write(cache: PagedCache, k: torch.Tensor, v: Optional[torch.Tensor], cu_seqlens_q: torch.Tensor,
@@ -293,7 +293,7 @@ def attention_workspace(total_q: int, num_seqs: int, max_seqlen_q: int, n_heads:
                                                      topk_width)
     if n == 0:
         raise ValueError("invalid workspace sizes")
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def paged_attention(q: torch.Tensor, cache: PagedCache, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,

@@ -7,6 +7,7 @@ import sys
 import pytest
 import torch
 
+import sparse_attention_indexer_dsa_gb300 as dsa
 from sparse_attention_indexer_dsa_gb300 import _abi, paged
 from tests.test_paged_host import _attend, _read, _write, lib  # noqa: F401
 
@@ -102,3 +103,19 @@ def test_the_package_is_imported_without_cuda_in_torch():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_device_0_is_device_0(monkeypatch, lib):  # noqa: F811
+    """A device given by its number is that device, number 0 too; None is the current one."""
+    seen = []
+    for name in ("empty", "zeros"):
+        make = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, device, _make=make, **k: (seen.append(device), _make(*a, device="cpu", **k))[1])
+    calls = (lambda d: dsa.paged_cache(2, 16, 1, 64, device=d).k, lambda d: dsa.cache_workspace(d),
+             lambda d: dsa.attention_workspace(4, 1, 4, 16, 2, 128, device=d),
+             lambda d: dsa.workspace(8, 1, 8, 64, 128, 16, device=d))
+    for call in calls:
+        for given, want in ((0, 0), (1, 1), ("cuda:0", "cuda:0"), (None, "cuda")):
+            seen.clear()
+            call(given)
+            assert set(seen) == {want}, (given, seen)
