@@ -64,7 +64,7 @@ dsa_status_t check_stride(int64_t* stride, int heads, int head_dim, int elem_byt
   return DSA_OK;
 }
 
-uint32_t round16(uint32_t x) { return (x + 15) / 16 * 16; }
+constexpr uint32_t round16(uint32_t x) { return (x + 15) / 16 * 16; }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Streams of a launch, and units of one query tile (or pair) up to which key ranges are divided.
@@ -86,7 +86,7 @@ namespace dsa {
 // gathered keys are narrow (the figures are with the kernel).  Key ranges are divided only while
 // there are at most four units to a stream (more balance themselves), and a
 // call's workspace has room for four more units to a stream.
-bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,
+void attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,
                int page_size, int topk_width) {
   *pl = AttnPlan{};
   const bool eight_bit = sw > 0;
@@ -107,38 +107,36 @@ bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   pl->narrow = pl->gather && D == 128 && pl->rows_cap <= kAttnNarrow;
   const int qrows = pl->narrow ? kAttnNarrow : pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
   pl->q_bytes = (uint32_t)qrows * D * 2;
-  const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys * D + 512;
-  for (pl->streams = 2; pl->streams >= 1; --pl->streams) {
-    const uint32_t rings = pl->pair ? 1 : pl->streams;
-    const uint32_t rows = 64;   // visible rows of a stored tile
-    const uint32_t mask = pl->gather ? 2 * 8 * 4 * 4 : 0, bars = 8 * kAttnBars + 32, tab = round16((64 + 1) * 4);
-    const uint32_t red = pl->narrow ? 2 * 9 * kAttnNarrow * 4 : 0;
-    const uint32_t q = 2 * pl->q_bytes + (pl->narrow ? 4 * kAttnNarrowP : 0), tail = rows + red + mask + bars + tab;
-    if (q + tail > kAttnSmemMax) continue;
-    const uint32_t avail = kAttnSmemMax - q - tail;
-    if (eight_bit) {
-      pl->nst = pl->pair || rings == 1 ? 3 : 2;
-      if (avail < rings * (pl->nst * stage + raw)) continue;
-      pl->nraw = (int)((avail - rings * pl->nst * stage) / (rings * raw));
-      if (pl->nraw > 6) pl->nraw = 6;
-    } else {
-      pl->nst = (int)(avail / (rings * stage));
-      if (pl->nst < 2) continue;
-      if (pl->nst > 8) pl->nst = 8;
-      pl->nraw = 0;
-    }
-    pl->off_p = 2 * pl->q_bytes;
-    pl->off_ring = q;
-    pl->off_raw = pl->off_ring + rings * pl->nst * stage;
-    pl->off_rows = pl->off_raw + rings * pl->nraw * raw;
-    pl->off_red = pl->off_rows + rows;
-    pl->off_mask = pl->off_red + red;
-    pl->off_bars = pl->off_mask + mask;
-    pl->off_tab = pl->off_bars + bars;
-    pl->smem = pl->off_tab + tab;
-    return true;
+  constexpr uint32_t kRows = 64;   // (visible rows of a stored tile)
+  constexpr uint32_t kMask = 2 * 8 * 4 * 4, kBars = 8 * kAttnBars + 32, kTab = round16((64 + 1) * 4);
+  // The largest plans fit: 128 rows of 128 elements to a query tile, with a stored tile (a pair: one for
+  // each team of workers) and two stages to a ring (a pair of an 8-bit cache: three).
+  constexpr uint32_t kStageMax = kAttnKeys * 128 * 2, kRawMax = kAttnKeys * 128 + 512;
+  constexpr uint32_t kFixedMax = 2 * kAttnRows * 128 * 2 + kRows + kMask + kBars + kTab;
+  static_assert(kFixedMax + 2 * (2 * kStageMax + kRawMax) <= kAttnSmemMax, "two streams");
+  static_assert(kFixedMax + 3 * kStageMax + 2 * kRawMax <= kAttnSmemMax, "a pair");
+  const uint32_t stage = kAttnKeys * D * 2, raw = kAttnKeys * D + 512, rings = pl->pair ? 1 : 2;
+  const uint32_t mask = pl->gather ? kMask : 0, red = pl->narrow ? 2 * 9 * kAttnNarrow * 4 : 0;
+  const uint32_t q = 2 * pl->q_bytes + (pl->narrow ? 4 * kAttnNarrowP : 0);
+  const uint32_t avail = kAttnSmemMax - q - (kRows + red + mask + kBars + kTab);
+  if (eight_bit) {
+    pl->nst = pl->pair ? 3 : 2;
+    pl->nraw = (int)((avail - rings * pl->nst * stage) / (rings * raw));
+    if (pl->nraw > 6) pl->nraw = 6;
+  } else {
+    pl->nst = (int)(avail / (rings * stage));
+    if (pl->nst > 8) pl->nst = 8;
+    pl->nraw = 0;
   }
-  return false;
+  pl->off_p = 2 * pl->q_bytes;
+  pl->off_ring = q;
+  pl->off_raw = pl->off_ring + rings * pl->nst * stage;
+  pl->off_rows = pl->off_raw + rings * pl->nraw * raw;
+  pl->off_red = pl->off_rows + kRows;
+  pl->off_mask = pl->off_red + red;
+  pl->off_bars = pl->off_mask + mask;
+  pl->off_tab = pl->off_bars + kBars;
+  pl->smem = pl->off_tab + kTab;
 }
 
 size_t attn_workspace_bytes(const AttnPlan& pl, int num_seqs, int D) {
@@ -289,8 +287,7 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
     return fail(DSA_ERR_INVALID_ARG, "topk_width and topk_len belong to topk_idx");
   if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if ((s = check_stride(&q_stride, n_heads, head_dim, 2, "q")) != DSA_OK) return s;
-  if (!attn_plan(&p.plan, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, p.c.sw, page_size, topk_width))
-    return fail(DSA_ERR_UNSUPPORTED, "no kernel configuration fits");
+  attn_plan(&p.plan, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, p.c.sw, page_size, topk_width);
   const size_t need = attn_workspace_bytes(p.plan, num_seqs, head_dim);
   if ((s = check_ws(ws, ws_bytes, need)) != DSA_OK) return s;
   DevInfo di;

@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
 
   // ---- the unit list (every block the same) ----
   const int gsz = (p.num_seqs + kGroups - 1) / kGroups;
-  const int n_streams = kPair ? (int)gridDim.x : pl.streams * (int)gridDim.x;
+  const int n_streams = (kPair ? 1 : 2) * (int)gridDim.x;
   {
     float* const red = reinterpret_cast<float*>(smem);   // scratch before any tile is loaded
     long long work = 0;
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
   const int wg = warp >> 2;
   // Independent streams: all first streams of the grid before the second ones, so few units spread over all SMs.
   auto first_unit = [&](int w) {
-    return kPair ? (int)blockIdx.x : (w < pl.streams ? w * (int)gridDim.x + (int)blockIdx.x : n_units);
+    return kPair ? (int)blockIdx.x : w * (int)gridDim.x + (int)blockIdx.x;
   };
   // Independent streams with at most 64 live rows: the second stream's rows are TMEM lanes (and so
   // warps and sub-partitions of the SM) that the first one's do not use.

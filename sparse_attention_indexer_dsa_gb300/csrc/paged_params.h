@@ -1,5 +1,5 @@
 // Parameter blocks and launchers of the paged-cache operators (paged_cache.cu,
-// paged_attn.cu) and the device view of a paged cache.
+// paged_attn.cuh) and the device view of a paged cache.
 #pragma once
 
 #include <cuda.h>
@@ -63,7 +63,6 @@ constexpr int kAttnSms = 152;       // the grid's upper bound, for workspace siz
 struct AttnPlan {
   int pair;        // two query tiles share one key stream (long chunks); else two independent streams
   int gather;      // rows resolved and copied one by one (listed keys, short page scales)
-  int streams;     // independent streams per block (1 where two do not fit)
   int tq;          // tokens per query tile
   int rows_cap;    // rows of a tile that can be live
   int nst;         // key/value stages per ring
@@ -100,8 +99,7 @@ struct AttnParams {
 // Header words of an attention workspace beside the status words.
 constexpr int kAttnHdrChunk = 8;    // key tiles per split
 
-// False: these sizes need more shared memory than a block has.
-bool attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,
+void attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,
                int page_size, int topk_width);
 size_t attn_workspace_bytes(const AttnPlan& pl, int num_seqs, int D);
 
