@@ -423,6 +423,15 @@ dsa_status_t dsa_idx_cache_read(
 size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqlen_q, int n_heads,
                                         int n_kv_heads, int head_dim, int topk_width);
 
+/* Workspace bytes of one dsa_idx_paged_attention call with exactly these
+ * arguments: never more than the above, and the status header alone where its
+ * plan divides no key range (many query tiles, or short ranges).  0 for invalid
+ * sizes. */
+size_t dsa_idx_attention_call_workspace_size(int total_q, int num_seqs, int max_seqlen_q,
+                                             int max_seqlen_k, int n_heads, int n_kv_heads,
+                                             int head_dim, int page_size, dsa_precision_t prec,
+                                             int topk_width);
+
 /* Attention of the new tokens over the cache: with G = n_heads / n_kv_heads,
  *   out[t, h] = sum_s softmax_s(sm_scale * q[t, h] . k[s, h / G]) v[s, h / G]
  * over the keys s that query t of sequence d (position P = S_d - T_d + t) sees:

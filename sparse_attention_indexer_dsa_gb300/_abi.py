@@ -73,6 +73,7 @@ SIGNATURES = {
     "dsa_idx_cache_read": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp,
                                     _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
     "dsa_idx_attention_workspace_size": (_c_size, [_c_int] * 7),
+    "dsa_idx_attention_call_workspace_size": (_c_size, [_c_int] * 10),
     "dsa_idx_paged_attention": (_c_int, [_vp, _c_i64, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                                          _c_int, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_f, _vp,
                                          _vp, _c_int, _vp, _vp, _vp, _c_size, _vp]),

@@ -14,6 +14,11 @@ using namespace dsa;
 
 namespace {
 
+// Scale bytes of a row.
+int scale_width(dsa_precision_t prec, int head_dim) {
+  return prec == DSA_PREC_MXFP8 ? head_dim / 32 : (prec == DSA_PREC_FP8 ? 1 : 0);
+}
+
 // Checks shared by the three operators; fills the device view.
 dsa_status_t check_cache(PagedCacheView* c, const void* k_pages, const uint8_t* k_page_scale, const void* v_pages,
                          const uint8_t* v_page_scale, int num_pages, int page_size, int n_kv_heads, int head_dim,
@@ -44,7 +49,7 @@ dsa_status_t check_cache(PagedCacheView* c, const void* k_pages, const uint8_t* 
   c->n_kv = n_kv_heads;
   c->max_pages = max_pages;
   c->fmt = (int)prec;
-  c->sw = prec == DSA_PREC_MXFP8 ? head_dim / 32 : (prec == DSA_PREC_FP8 ? 1 : 0);
+  c->sw = scale_width(prec, head_dim);
   return DSA_OK;
 }
 
@@ -86,8 +91,8 @@ namespace dsa {
 // gathered keys are narrow (the figures are with the kernel).  Key ranges are divided only while
 // there are at most four units to a stream (more balance themselves), and a
 // call's workspace has room for four more units to a stream.
-void attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,
-               int page_size, int topk_width) {
+void attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int max_seqlen_k, int n_heads, int n_kv, int D,
+               int sw, int page_size, int topk_width) {
   *pl = AttnPlan{};
   const bool eight_bit = sw > 0;
   const int group = n_heads / n_kv;
@@ -103,7 +108,9 @@ void attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_
   if (tiles > total_q) tiles = total_q;
   const int64_t base = tiles * n_kv;
   const int64_t most = most_undivided(pl->pair);
-  pl->max_units = base <= most ? (int)(base + most) : 0;
+  // (a range of kAttnMinChunk tiles is not divided: no partial results, no joining launch)
+  const bool divide = base <= most && (topk_width > 0 ? topk_width : max_seqlen_k) > kAttnMinChunk * kAttnKeys;
+  pl->max_units = divide ? (int)(base + most) : 0;
   pl->narrow = pl->gather && D == 128 && pl->rows_cap <= kAttnNarrow;
   const int qrows = pl->narrow ? kAttnNarrow : pl->pair || pl->rows_cap > 64 ? 128 : (pl->rows_cap > 32 ? 64 : 32);
   pl->q_bytes = (uint32_t)qrows * D * 2;
@@ -145,6 +152,15 @@ size_t attn_workspace_bytes(const AttnPlan& pl, int num_seqs, int D) {
 }
 
 }  // namespace dsa
+
+namespace {
+
+bool sizes_ok(int total_q, int num_seqs, int max_seqlen_q, int n_heads, int n_kv, int D, int topk_width) {
+  return total_q >= 0 && num_seqs >= 1 && max_seqlen_q >= 0 && n_heads >= 1 && n_kv >= 1 && n_heads % n_kv == 0 &&
+         n_heads / n_kv <= kAttnRows && (D == 64 || D == 128) && topk_width >= 0;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -239,9 +255,7 @@ dsa_status_t dsa_idx_cache_read(const void* k_pages, const uint8_t* k_page_scale
 
 size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqlen_q, int n_heads, int n_kv_heads,
                                         int head_dim, int topk_width) {
-  if (total_q < 0 || num_seqs < 1 || max_seqlen_q < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 ||
-      n_heads / n_kv_heads > kAttnRows || (head_dim != 64 && head_dim != 128) || topk_width < 0)
-    return 0;
+  if (!sizes_ok(total_q, num_seqs, max_seqlen_q, n_heads, n_kv_heads, head_dim, topk_width)) return 0;
   // The most that attn_plan asks for at any format and at any sizes up to these: fewer tokens may need
   // more, as the key ranges of many tiles are not divided.
   const int group = n_heads / n_kv_heads, tq = topk_width > 0 ? 1 : kAttnRows / group;
@@ -257,6 +271,18 @@ size_t dsa_idx_attention_workspace_size(int total_q, int num_seqs, int max_seqle
     slots = n > slots ? n : slots;
   }
   return with_partials(num_seqs, slots, head_dim);
+}
+
+size_t dsa_idx_attention_call_workspace_size(int total_q, int num_seqs, int max_seqlen_q, int max_seqlen_k, int n_heads,
+                                             int n_kv_heads, int head_dim, int page_size, dsa_precision_t prec,
+                                             int topk_width) {
+  if (!sizes_ok(total_q, num_seqs, max_seqlen_q, n_heads, n_kv_heads, head_dim, topk_width) || max_seqlen_k < 0 ||
+      page_size < 1)
+    return 0;
+  AttnPlan pl;
+  attn_plan(&pl, num_seqs, total_q, max_seqlen_q, max_seqlen_k, n_heads, n_kv_heads, head_dim, scale_width(prec, head_dim),
+            page_size, topk_width);
+  return attn_workspace_bytes(pl, num_seqs, head_dim);
 }
 
 dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void* k_pages, const uint8_t* k_page_scale,
@@ -287,7 +313,8 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
     return fail(DSA_ERR_INVALID_ARG, "topk_width and topk_len belong to topk_idx");
   if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if ((s = check_stride(&q_stride, n_heads, head_dim, 2, "q")) != DSA_OK) return s;
-  attn_plan(&p.plan, num_seqs, total_q, max_seqlen_q, n_heads, n_kv_heads, head_dim, p.c.sw, page_size, topk_width);
+  attn_plan(&p.plan, num_seqs, total_q, max_seqlen_q, max_seqlen_k, n_heads, n_kv_heads, head_dim, p.c.sw, page_size,
+            topk_width);
   const size_t need = attn_workspace_bytes(p.plan, num_seqs, head_dim);
   if ((s = check_ws(ws, ws_bytes, need)) != DSA_OK) return s;
   DevInfo di;
@@ -332,7 +359,6 @@ dsa_status_t dsa_idx_paged_attention(const void* q, int64_t q_stride, const void
   // no more blocks than there can be units
   const int per = p.plan.pair ? 2 * p.plan.tq : p.plan.tq;
   const int64_t keys = topk_idx ? topk_width : max_seqlen_k;
-  if (keys <= kAttnMinChunk * kAttnKeys) p.plan.max_units = 0;   // nothing to divide: no joining launch
   int64_t bound = ((int64_t)total_q / per + num_seqs) * n_kv_heads * (p.plan.max_units > 0 ? keys / (kAttnMinChunk * kAttnKeys) + 1 : 1);
   if (bound > di.sm_count) bound = di.sm_count;
   if (bound > DSA_DEV_STATUS_MAX_BLOCKS) bound = DSA_DEV_STATUS_MAX_BLOCKS;

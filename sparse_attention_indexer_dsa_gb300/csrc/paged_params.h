@@ -99,8 +99,8 @@ struct AttnParams {
 // Header words of an attention workspace beside the status words.
 constexpr int kAttnHdrChunk = 8;    // key tiles per split
 
-void attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int n_heads, int n_kv, int D, int sw,
-               int page_size, int topk_width);
+void attn_plan(AttnPlan* pl, int num_seqs, int total_q, int max_seqlen_q, int max_seqlen_k, int n_heads, int n_kv, int D,
+               int sw, int page_size, int topk_width);
 size_t attn_workspace_bytes(const AttnPlan& pl, int num_seqs, int D);
 
 cudaError_t launch_cache_write(const CacheWriteParams& p, int D, int sm_count, cudaStream_t stream);

@@ -288,7 +288,8 @@ def cache_read(cache: PagedCache, cu_seqlens_k: torch.Tensor, page_table: torch.
 
 def attention_workspace(total_q: int, num_seqs: int, max_seqlen_q: int, n_heads: int, n_kv_heads: int, head_dim: int,
                         topk_width: int = 0, device=None) -> torch.Tensor:
-    """Device workspace (uint8, 256-byte aligned) for every paged_attention call of at most these sizes."""
+    """Device workspace (uint8, 256-byte aligned) for every paged_attention call of at most these sizes,
+    with a list of any width if topk_width is not 0, without one if it is."""
     n = _abi.load().dsa_idx_attention_workspace_size(total_q, num_seqs, max_seqlen_q, n_heads, n_kv_heads, head_dim,
                                                      topk_width)
     if n == 0:
@@ -310,7 +311,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, cu_seqlens_q: torch.Tens
     such a tensor (or pair) to write into: rows behind the last sequence stay
     as they were.  Forward only: no gradient is recorded.  `ws` from
     attention_workspace may be of a larger call; calls that may overlap need
-    one each."""
+    one each.  Without it the call allocates what it needs itself."""
     if cache.v is None:
         raise ValueError("the cache has no values")
     a, dev, (N, Hk, ps, D) = _pages(cache)
@@ -345,7 +346,11 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, cu_seqlens_q: torch.Tens
         op = _arg(out, "out", dev, torch.bfloat16, shape)
         lsep = _arg(lse, "lse", dev, torch.float32, (T, H))
     if ws is None:
-        ws = attention_workspace(T, B, max_seqlen_q, H, Hk, D, W, dev)
+        n = _abi.load().dsa_idx_attention_call_workspace_size(T, B, max_seqlen_q, max_seqlen_k, H, Hk, D, ps,
+                                                              _PREC[cache.prec], W)
+        if n == 0:
+            raise ValueError("invalid sizes")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
     wp = _arg(ws, "ws", dev, torch.uint8)
     code = _call(_abi.load().dsa_idx_paged_attention, dev, (
         qp, qst, *a, N, ps, H, Hk, D, _PREC[cache.prec], table, width, cq, ck, B, T, max_seqlen_q, max_seqlen_k,

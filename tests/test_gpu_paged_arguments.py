@@ -187,3 +187,33 @@ def test_the_smallest_scales_on_the_largest_logits(prec, kind, scale):
     want, wl, tol, ltol = attention(b, q, group, scale, sel)
     _close(host(out.double()), want, tol)
     _close(host(lse.double()), wl, ltol)
+
+
+@pytest.mark.parametrize("kind", ["chunk", "steps", "list"])
+def test_a_call_without_a_workspace_allocates_its_own_alone(kind):
+    """Where the plan divides no key range that is the status header; the results are those of a call
+    with a workspace for every smaller one."""
+    rng = np.random.default_rng(78)
+    lens, W = {"chunk": ([(6000, 6400)], 0), "steps": ([(1, 200)] * 40, 0), "list": ([(700, 900)], 96)}[kind]
+    c = dsa.paged_cache(200, 64, 4, 128)
+    c.k.normal_()
+    c.v.normal_()
+    t, s = np.array(lens).T
+    cu_q, cu_k = (dev(np.concatenate([[0], np.cumsum(x)]).astype(np.int32)) for x in (t, s))
+    need = [-(-x // 64) for x in s]
+    table = np.full((len(lens), max(need)), -1, np.int32)
+    for d, n in enumerate(need):
+        table[d, :n] = rng.permutation(200)[:n]
+    T = int(t.sum())
+    q = torch.randn((T, 16, 128), device="cuda").to(torch.bfloat16)
+    sel = dev(rng.integers(0, 100, (T, W)).astype(np.int32)) if W else None
+    args = (q, c, cu_q, cu_k, dev(table), int(t.max()), int(s.max()))
+    out = torch.empty_like(q)
+    ws = dsa.attention_workspace(T, len(lens), int(t.max()), 16, 4, 128, W)
+    want = dsa.paged_attention(*args, topk_idx=sel, ws=ws)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    dsa.paged_attention(*args, topk_idx=sel, out=out)
+    assert torch.cuda.max_memory_allocated() - before <= 16384
+    assert torch.equal(out, want)

@@ -4,11 +4,13 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
 import sparse_attention_indexer_dsa_gb300 as dsa
 from sparse_attention_indexer_dsa_gb300 import _abi, paged
+from tests.test_paged_host import A as _A
 from tests.test_paged_host import _attend, _read, _write, lib  # noqa: F401
 
 CPU = torch.device("cpu")
@@ -119,3 +121,21 @@ def test_device_0_is_device_0(monkeypatch, lib):  # noqa: F811
             seen.clear()
             call(given)
             assert set(seen) == {want}, (given, seen)
+
+
+def test_what_a_call_needs_is_within_what_every_smaller_call_needs(lib):  # noqa: F811
+    rng = np.random.default_rng(8)
+    every, one = lib.dsa_idx_attention_workspace_size, lib.dsa_idx_attention_call_workspace_size
+    for _ in range(2000):
+        kv, group, D = int(rng.integers(1, 9)), int(rng.integers(1, 129)), int(rng.choice([64, 128]))
+        W, total, seqs, mq, mk = int(rng.choice([0, 0, 64, 2048])), *(int(2 ** rng.uniform(0, n)) for n in (16, 9, 14, 17))
+        page, prec = int(rng.choice([8, 16, 64, 1024])), int(rng.integers(0, 3))
+        need = one(total, seqs, mq, mk, kv * group, kv, D, page, prec, W)
+        assert _abi.DSA_CACHE_WS_BYTES <= need <= every(total, seqs, mq, kv * group, kv, D, W)
+        sizes = dict(H=kv * group, kv=kv, D=D, prec=prec, page=page, seqs=seqs, total_q=total, max_q=mq, max_k=mk, W=W,
+                     idx=_A if W else None)
+        assert _attend(lib, ws_bytes=need - 1, **sizes) == _abi.DSA_ERR_WORKSPACE
+    assert one(4096, 1, 4096, 32768, 64, 8, 128, 64, 0, 0) == _abi.DSA_CACHE_WS_BYTES     # undivided pairs
+    for bad in ((-1, 1, 4, 9, 16, 2, 128, 16, 0, 0), (4, 0, 4, 9, 16, 2, 128, 16, 0, 0), (4, 1, 4, -1, 16, 2, 128, 16, 0, 0),
+                (4, 1, 4, 9, 15, 2, 128, 16, 0, 0), (4, 1, 4, 9, 16, 2, 96, 16, 0, 0), (4, 1, 4, 9, 16, 2, 128, 0, 0, 0)):
+        assert one(*bad) == 0
