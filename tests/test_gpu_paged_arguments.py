@@ -8,7 +8,7 @@ import sparse_attention_indexer_dsa_gb300 as dsa
 from sparse_attention_indexer_dsa_gb300 import _abi
 from tests.gpu_util import dev, host
 from tests.paged_ref import Batch, attention, quantise, values
-from tests.test_gpu_paged_attention import _close, _queries, _selection
+from tests.test_gpu_paged_attention import _close, _queries, _run, _selection
 from tests.test_gpu_paged_cache import _check_pages
 
 pytestmark = pytest.mark.gpu
@@ -217,3 +217,54 @@ def test_a_call_without_a_workspace_allocates_its_own_alone(kind):
     dsa.paged_attention(*args, topk_idx=sel, out=out)
     assert torch.cuda.max_memory_allocated() - before <= 16384
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8", "fp8"])
+def test_a_chunk_beside_single_tokens(prec):
+    """One long chunk makes the call's tiles pairs; the single tokens beside it take a pair each, whose
+    second tile is empty."""
+    rng = np.random.default_rng(79)
+    b = Batch(rng, [(1, 1), (400, 900), (1, 300), (0, 70), (1, 1290)] + [(1, int(n)) for n in rng.integers(1, 500, 9)],
+              2, 128, 32, prec)
+    _run(b, rng, 16, 8)
+
+
+def test_two_host_threads():
+    """Calls from two threads at once, each with its stream, workspace and cache: the results are those
+    of the same calls one after the other, and an error is its own thread's."""
+    import threading
+    rng = np.random.default_rng(80)
+    jobs = []
+    for prec, lens, W in (("mxfp8", [(1, 3000), (1, 70)], 0), ("bf16", [(20, 600), (3, 90)], 64)):
+        b = Batch(rng, lens, 2, 128, 16, prec)
+        sel = dev(_selection(rng, b, W, "sorted")[0]) if W else None
+        _, qd = _queries(rng, b.total_q, 16, 128)
+        ws = dsa.attention_workspace(b.total_q, 2, max(t for t, _ in lens), 16, 2, 128, W)
+        args = (qd, b.cache(dsa), b.dev("cu_q"), b.dev("cu_k"), b.dev("table"), max(t for t, _ in lens), max(s for _, s in lens))
+        jobs.append((args, dict(topk_idx=sel, ws=ws)))
+    want = [dsa.paged_attention(*a, **k) for a, k in jobs]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            args, kw = jobs[i]
+            with torch.cuda.stream(torch.cuda.Stream()):
+                out = torch.empty_like(want[i])
+                for n in range(100):
+                    dsa.paged_attention(*args, out=out, **kw)
+                    if n % 10 == 0:
+                        with pytest.raises(dsa.DsaError) as e:
+                            dsa.paged_attention(*args, topk_idx=kw["topk_idx"], out=out, ws=kw["ws"][:256 * (i + 1)])
+                        assert f"workspace {256 * (i + 1)} bytes" in str(e.value)
+                assert dsa.read_status(kw["ws"]) == 0
+                assert torch.equal(out, want[i])
+        except BaseException as e:   # noqa: B902 (reported by the test's thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
