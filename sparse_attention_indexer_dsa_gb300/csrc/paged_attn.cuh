@@ -31,14 +31,14 @@
 // shared memory, O^T += V^T P^T (head_dim x 16).  S and P have two buffers, so
 // the next tile's logits are formed meanwhile.  4 tokens of each of 64
 // sequences, 64 heads, 8 key heads, 2048 listed keys, against tiles of 128 rows:
-// 495 us against 556 over MXFP8, 279 against 321 over BF16; one token and every
-// key, FP8 in pages of 8: 550 against 639.  Rows that TMA brings stay with tiles
-// of 128 rows, which are as fast: a token of each of the 64 over 2048 - 16384
-// keys 379 us over BF16 (2.4 GB, 93 % of the copy rate) either way, 429 against
-// 427 over MXFP8 (1.2 GB), with 8 sequences 75 against 81 and 75 against 77.
+// 482 us against 550 over MXFP8, 263 against 308 over BF16; one token and every
+// key, FP8 in pages of 8: 507 against 583.  Rows that TMA brings stay with tiles
+// of 128 rows, which were as fast when narrow ones were tried for them: a token
+// of each of the 64 over 2048 - 16384 keys 379 us over BF16 (2.4 GB, 93 % of the
+// copy rate) either way, 427 against 429 over MXFP8 (1.2 GB; 415 now).
 // Over 8-bit caches the latency of a stored tile (its load, its widening, the
 // hand-overs) bounds them: shared memory holds two stored tiles to a ring beside
-// the widened ones.
+// the widened ones, of more than 32 rows one.
 // Loaders.  TMA brings all visible keys as a box per page; listed rows are copied
 // one by one with cp.async (TMA row gathers of four came to 27 bytes a cycle and
 // SM, cp.async from eight warps to 60); BF16 in the 128-byte swizzled layout the
@@ -72,8 +72,12 @@ namespace dsa {
 namespace attn {
 
 constexpr int kGroups = 64;         // sequences are counted in this many groups
-constexpr int kOverhead = 4;        // start and end of a unit, in key tiles
-constexpr int kSplitOverhead = 6;   // ... when its result is joined later
+// Start and end of a unit, in key tiles, and the same when its result is joined later: what the estimate of
+// a schedule counts beside the tiles.  With 0 for the first 100 tokens over 700 listed rows take 30.7 against
+// 29.8 us, 12 changes nothing; with 4 for the second nothing changes, 12 takes 416 to 391 us for a token of each
+// of 64 sequences over MXFP8 and 29.8 to 30.4 for the listed rows.  (Other calls tried: within 1 %.)
+constexpr int kOverhead = 4;
+constexpr int kSplitOverhead = 6;
 constexpr int kMaskRing = 8;
 constexpr float kRaise = 20.f;      // log2 of the largest weight before the maximum is raised
 
@@ -352,7 +356,9 @@ enum { PAIR = 0, SOLO = 1, GATHER = 2 };
 // Warps: 8 softmax; workers (16, or 12 of gathered rows, widen 8-bit tiles; 8 bring gathered BF16
 // rows); 4 that bring gathered 8-bit rows; the rest: key loaders (TMA), query loaders, MMA 0 and 1
 // last.  (The four warps of an SM's sub-partition are those of equal number modulo 4; loaders and MMA
-// warps are kept on different ones.)
+// warps are kept on different ones.)  The shares of registers leave spills, most in the kernel of
+// gathered 8-bit rows (some 580 bytes of stores and 680 of loads in the code; the other kernels of
+// 128-row tiles 124 - 168 and 148 - 240).  What they cost has not been measured.
 template <bool Q8, int MODE, bool NARROW>
 struct Roles {
   static constexpr int kWorkWarps = MODE == GATHER ? (Q8 ? 12 : 8) : (Q8 ? 16 : 0);
@@ -1204,8 +1210,9 @@ __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
         if (elect_one()) {
           const uint32_t q_rows_bytes = pl.q_bytes / (D / 64);   // one 64-column chunk of the query tile
           // The streams issue PV and the next QK as one block, in turns, so that one's softmax runs beside
-          // the other's products: 4096 tokens over 32768 BF16 keys 2.89 against 2.92 ms, a token of each
-          // sequence over MXFP8 425 against 451 us.  (Gathered rows are faster without: 596 against 604 us.)
+          // the other's products: a token of each of 64 sequences over MXFP8 415 against 434 us, ragged
+          // chunks over FP8 492 against 495, 4096 tokens over 32768 BF16 keys 2.87 against 2.88 ms.  (Gathered
+          // rows take the same time either way.)
           // Nothing is waited for inside a turn, so a turn always comes; only the times depend on it.
           constexpr bool kTurns = MODE != GATHER;
           int* const turn = ctl + 4;

@@ -52,7 +52,9 @@ struct CacheReadParams {
 
 constexpr int kAttnKeys = 128;      // keys per tile
 constexpr int kAttnRows = 128;      // query rows (token, head of the group) per tile
-constexpr int kAttnMinChunk = 2;    // key tiles of a divided range, at least
+// Key tiles of a divided range, at least.  1 / 2 / 4: 16 tokens over 2048 keys of one head 24.1 / 20.8 / 21.2 us,
+// 2048 listed rows of one token 24.9 / 23.3 / 25.4, of 32 tokens over MXFP8 32.7 / 32.7 / 35.8.
+constexpr int kAttnMinChunk = 2;
 constexpr int kAttnNarrow = 16;              // query rows of a narrow tile (columns of its products)
 constexpr int kAttnNarrowP = kAttnNarrow * kAttnKeys * 2;   // bytes of its weights
 constexpr int kAttnBars = 2 * 32 + 2 * 10;   // barriers of a block
