@@ -17,6 +17,7 @@ from . import _abi
 from ._abi import (DSA_FLAG_COMPRESSED_KEYS, DSA_FLAG_DETERMINISTIC, DSA_FLAG_KPOOL_TAIL,  # noqa: F401
                    DSA_FLAG_SORT_BY_SCORE,
                    DSA_PREC_BF16, DSA_PREC_FP8, DSA_PREC_MXFP8)
+from .paged import _call
 from .paged import (PagedCache, attention_workspace, cache_read, cache_workspace, cache_write,  # noqa: F401
                     paged_attention, paged_cache)
 
@@ -241,9 +242,11 @@ def score_topk_kv(q_op: torch.Tensor, q_scale: Optional[torch.Tensor], k_op: tor
 
 
 def read_status(ws: torch.Tensor) -> int:
-    """Synchronise the current stream and return the device status word."""
+    """Synchronise the current stream of the workspace's device and return the device status word."""
     out = ctypes.c_int(0)
-    _check(_abi.load().dsa_idx_read_status(_ptr(ws), _stream(), ctypes.byref(out)), "dsa_idx_read_status")
+    lib, address = _abi.load(), _ptr(ws)
+    _check(_call(lambda stream: lib.dsa_idx_read_status(address, stream, ctypes.byref(out)), ws.device, ()),
+           "dsa_idx_read_status")
     return out.value
 
 

@@ -139,3 +139,39 @@ def test_what_a_call_needs_is_within_what_every_smaller_call_needs(lib):  # noqa
     for bad in ((-1, 1, 4, 9, 16, 2, 128, 16, 0, 0), (4, 0, 4, 9, 16, 2, 128, 16, 0, 0), (4, 1, 4, -1, 16, 2, 128, 16, 0, 0),
                 (4, 1, 4, 9, 15, 2, 128, 16, 0, 0), (4, 1, 4, 9, 16, 2, 96, 16, 0, 0), (4, 1, 4, 9, 16, 2, 128, 0, 0, 0)):
         assert one(*bad) == 0
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_the_status_is_read_on_the_workspace_s_device(monkeypatch, current):
+    """As the calls run on their tensors' device, whichever is the current one, so is their status read
+    behind that device's stream."""
+    class Ws:
+        is_cuda, device = True, torch.device("cuda", 1)
+        is_contiguous = staticmethod(lambda: True)
+        data_ptr = staticmethod(lambda: 4096)
+
+    class Lib:
+        @staticmethod
+        def dsa_idx_read_status(address, stream, out):
+            seen.append((address, stream, now[-1]))
+            out._obj.value = 5
+            return 0
+
+    class On:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            now.append(self.index)
+
+        def __exit__(self, *a):
+            now.pop()
+
+    seen, now = [], [current]
+    monkeypatch.setattr(_abi, "load", lambda: Lib)
+    monkeypatch.setattr(paged, "_stream", lambda index: 100 + index)
+    monkeypatch.setattr(paged, "_current", lambda: now[-1])
+    monkeypatch.setattr(dsa, "_stream", lambda: 100 + now[-1])
+    monkeypatch.setattr(torch.cuda, "device", On)
+    assert dsa.read_status(Ws) == 5
+    assert seen == [(4096, 101, 1)] and now == [current]
