@@ -311,7 +311,8 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, cu_seqlens_q: torch.Tens
     such a tensor (or pair) to write into: rows behind the last sequence stay
     as they were.  Forward only: no gradient is recorded.  `ws` from
     attention_workspace may be of a larger call; calls that may overlap need
-    one each.  Without it the call allocates what it needs itself."""
+    one each.  Without it the call allocates what it needs itself.  One plan
+    serves a call: a long chunk and many single tokens are faster as two."""
     if cache.v is None:
         raise ValueError("the cache has no values")
     a, dev, (N, Hk, ps, D) = _pages(cache)
