@@ -39,9 +39,10 @@ def _error(code: int, where: str) -> Exception:
     return DsaError(code, where)
 
 
-@dataclass
+@dataclass(frozen=True)
 class PagedCache:
-    """Pages of keys and, unless `v` is None, values.
+    """Pages of keys and, unless `v` is None, values: checked here, once, and so
+    not to be replaced afterwards (a new handle costs next to nothing).
 
     k, v [num_pages, n_kv_heads, page_size, head_dim]: bfloat16 (prec "bf16")
     or uint8 E4M3 codes; k_scale, v_scale uint8 UE8M0 bytes
@@ -55,7 +56,7 @@ class PagedCache:
 
     def __post_init__(self):
         if self.prec not in _PREC:
-            self.prec = _NAME[self.prec]
+            object.__setattr__(self, "prec", _NAME[self.prec])
         if self.k.dim() != 4:
             raise ValueError("pages are [num_pages, n_kv_heads, page_size, head_dim]")
         want = torch.bfloat16 if self.prec == "bf16" else torch.uint8

@@ -175,3 +175,14 @@ def test_the_status_is_read_on_the_workspace_s_device(monkeypatch, current):
     monkeypatch.setattr(torch.cuda, "device", On)
     assert dsa.read_status(Ws) == 5
     assert seen == [(4096, 101, 1)] and now == [current]
+
+
+def test_a_handle_stays_what_was_checked():
+    """The calls take sizes from the keys alone: values replaced by fewer pages would be read behind their end."""
+    k = torch.zeros((4, 1, 16, 64), dtype=torch.uint8)
+    sc = torch.zeros((4, 1, 16, 2), dtype=torch.uint8)
+    c = dsa.PagedCache(k, sc, k.clone(), sc.clone(), dsa.DSA_PREC_MXFP8)
+    assert c.prec == "mxfp8"
+    for name, t in (("k", k[:2]), ("v", k[:2]), ("k_scale", sc[:2]), ("v_scale", None), ("prec", "fp8")):
+        with pytest.raises(AttributeError):
+            setattr(c, name, t)
