@@ -447,18 +447,20 @@ size_t dsa_idx_attention_call_workspace_size(int total_q, int num_seqs, int max_
  *   out         device bf16 [total_q, n_heads, head_dim]
  *   lse         device fp32 [total_q, n_heads] or NULL: log of the sum of
  *               exp(sm_scale q.k) over the seen keys
- * A query that sees no key gets out = 0 and lse = -inf.  sm_scale is finite
- * (as is sm_scale * log2(e)) and not negative; n_heads a multiple of n_kv_heads, at most 128 heads to one;
- * max_seqlen_q and max_seqlen_k bound T_d and S_d (a longer sequence is
- * reported in the status and not computed; nothing is computed when
- * cu_seqlens_q falls).  Rows 0 .. S_d - 1 of a sequence (with topk_idx: the
- * listed ones) must be finite; what other slots of its pages hold does not
- * matter.  A NaN among them makes the result of the queries that see it NaN
- * (8-bit: as the quantisers store it, or under scale byte 255; a NaN code under
- * a scale byte up to 134, which none of them writes, reads as 480 * 2^e), and
- * that of the sequence's other queries unspecified.  out and lse share no memory with the inputs.  total_q * n_heads <
- * 2^30, max_seqlen_k and topk_width at most 2^30.  With total_q = 0 topk_idx
- * may be NULL whatever topk_width is.  The same inputs give the same bits. */
+ * A query that sees no key gets out = 0 and lse = -inf.  sm_scale is finite (as
+ * is sm_scale * log2(e)) and not negative; n_heads a multiple of n_kv_heads, at
+ * most 128 heads to one; max_seqlen_q and max_seqlen_k bound T_d and S_d (a
+ * longer sequence is reported in the status and not computed; nothing is
+ * computed when cu_seqlens_q falls).  Rows 0 .. S_d - 1 of a sequence (with
+ * topk_idx: the listed ones) must be finite; what other slots of its pages hold
+ * does not matter.  A NaN among them makes the result of the queries that see
+ * it NaN (8-bit: as the quantisers store it, or under scale byte 255; a NaN
+ * code under a scale byte up to 134, which none of them writes, reads as
+ * 480 * 2^e), and that of the sequence's other queries unspecified.  out and lse
+ * share no memory with the inputs.  total_q * n_heads < 2^30, max_seqlen_k and
+ * topk_width at most 2^30.  With total_q = 0 topk_idx may be NULL whatever
+ * topk_width is.  The same inputs give the same bits.  One plan serves a call: a
+ * batch of a long chunk and many single tokens is faster as two calls. */
 dsa_status_t dsa_idx_paged_attention(
     const void* q, int64_t q_stride, const void* k_pages,
     const uint8_t* k_page_scale, const void* v_pages,

@@ -198,8 +198,8 @@ def cache_write(cache: PagedCache, k: torch.Tensor, v: Optional[torch.Tensor], c
     """Store the new tokens' rows in the cache's format (dsa_idx_cache_write).
 
     k, v [tokens, n_kv_heads, head_dim], fp32 or bf16 (views with a token
-    stride are taken as they are, tokens that share memory are refused); v None for a cache of keys alone.  With an
-    8-bit cache, uint8 k and v are E4M3 codes in operand form (as preprocess
+    stride are taken as they are, tokens that share memory are refused); v None
+    for a cache of keys alone.  With an 8-bit cache, uint8 k and v are E4M3 codes in operand form (as preprocess
     gives them) and k_scale, v_scale their UE8M0 bytes."""
     a, dev, (N, Hk, ps, D) = _pages(cache)
     table, width, B = _table(page_table, dev)
@@ -305,8 +305,8 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, cu_seqlens_q: torch.Tens
     """Attention of the new tokens over the cache (dsa_idx_paged_attention).
 
     q [tokens, n_heads, head_dim] bf16 (a view with a token stride is taken as
-    it is, tokens that share memory are refused).  topk_idx int32 [tokens, W] restricts every query to the listed
-    positions (score_topk's rows), topk_len int32 [tokens] to a row's first
+    it is, tokens that share memory are refused).  topk_idx int32 [tokens, W]
+    restricts every query to the listed positions (score_topk's rows), topk_len int32 [tokens] to a row's first
     entries.  sm_scale defaults to head_dim ** -0.5.  Returns out [tokens,
     n_heads, head_dim] bf16, or (out, lse fp32 [tokens, n_heads]); `out` is
     such a tensor (or pair) to write into: rows behind the last sequence stay
