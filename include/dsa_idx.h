@@ -472,6 +472,143 @@ dsa_status_t dsa_idx_paged_attention(
     const int32_t* topk_len, int topk_width, void* out, float* lse,
     void* ws, size_t ws_bytes, dsa_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the attention: norms and rotation before it, a bounded cache behind it.
+ *
+ * A step of a layer whose cache holds at most `budget` rows of a sequence:
+ * dsa_idx_norm_rope, dsa_idx_cache_write, dsa_idx_paged_attention (with lse),
+ * dsa_idx_cache_weigh, and where caches have outgrown the budget
+ * dsa_idx_evict_select and dsa_idx_cache_compact.  Positions are given by the
+ * caller: once rows have left the cache its length is not the position.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { DSA_NORM_RMS = 0, DSA_NORM_LAYER = 1 } dsa_norm_t;
+
+/* Norms of queries and keys for each head, then the position rotation: for
+ * every row x of head_dim elements
+ *   n = x / sqrt(mean x^2 + eps)                      DSA_NORM_RMS
+ *   n = (x - mean x) / sqrt(var x + eps)              DSA_NORM_LAYER (biased variance)
+ *   y = R(pos) (n * weight + bias)
+ * in FP32, rounded once.  R turns pair i of the first rope_dim elements (i and
+ * i + rope_dim/2, or with rope_interleaved 2i and 2i + 1) by pos * freq_i,
+ * freq_i = rope_base^(-2i/rope_dim) or inv_freq[i]; angles are exact to 2^-32
+ * of a turn at every position.
+ *   q, k        device [total_tokens, n_heads (n_kv_heads), head_dim] in_dtype,
+ *               16-byte aligned; q_stride ..: elements from one token to the
+ *               next (0 = packed; a multiple of 16 bytes), heads packed inside
+ *   q_weight .. k_bias  device [head_dim] weight_dtype, or NULL: ones (zeros)
+ *   positions   device int32 [total_tokens] (any value); with rope_dim = 0 NULL
+ *   inv_freq    HOST array [rope_dim/2], or NULL
+ *   q_out, k_out  as q and k, in out_dtype, with strides of their own; may be q
+ *               and k themselves (same type and stride), else no shared memory
+ * n_kv_heads = 0: queries alone (k, k_out not used).  head_dim 64 or 128, at
+ * most 1024 heads each, rope_dim a multiple of 8 in [0, head_dim].  A row of
+ * zeros with eps = 0 gives NaN, a non-finite element makes its row non-finite;
+ * other rows are not touched by it. */
+dsa_status_t dsa_idx_norm_rope(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+    dsa_dtype_t in_dtype, const void* q_weight, const void* k_weight,
+    const void* q_bias, const void* k_bias, dsa_dtype_t weight_dtype,
+    dsa_norm_t norm, float eps, const int32_t* positions, int total_tokens,
+    int n_heads, int n_kv_heads, int head_dim, int rope_dim, double rope_base,
+    const double* inv_freq, int rope_interleaved, void* q_out,
+    int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+    dsa_dtype_t out_dtype, dsa_stream_t stream);
+
+/* Workspace bytes of dsa_idx_norm_rope_backward; 0 for an unsupported head_dim. */
+size_t dsa_idx_norm_rope_workspace_size(int head_dim);
+
+/* Gradients of dsa_idx_norm_rope: of its inputs (dq, dk, in_dtype, strides of
+ * their own) and of its weights and biases (FP32 [head_dim], summed over tokens
+ * and heads; NULL: not wanted), from the gradients dq_out, dk_out of its outputs
+ * (grad_dtype) and the forward's inputs; no other statistics are kept.  Weight
+ * gradients of a call without weights are those of weights of one.  Outputs
+ * share no memory with inputs.  ws as for the cache's operators.  The same
+ * inputs give the same bits. */
+dsa_status_t dsa_idx_norm_rope_backward(
+    const void* dq_out, int64_t dq_out_stride, const void* dk_out,
+    int64_t dk_out_stride, dsa_dtype_t grad_dtype, const void* q,
+    int64_t q_stride, const void* k, int64_t k_stride, dsa_dtype_t in_dtype,
+    const void* q_weight, const void* k_weight, dsa_dtype_t weight_dtype,
+    dsa_norm_t norm, float eps, const int32_t* positions, int total_tokens,
+    int n_heads, int n_kv_heads, int head_dim, int rope_dim, double rope_base,
+    const double* inv_freq, int rope_interleaved, void* dq, int64_t dq_stride,
+    void* dk, int64_t dk_stride, float* dq_weight, float* dk_weight,
+    float* dq_bias, float* dk_bias, void* ws, size_t ws_bytes,
+    dsa_stream_t stream);
+
+/* Workspace bytes of dsa_idx_cache_weigh, enough for every call of at most
+ * total_q, num_seqs and max_seqlen_q with these heads.  0 for invalid sizes. */
+size_t dsa_idx_weigh_workspace_size(int total_q, int num_seqs, int max_seqlen_q,
+                                    int n_heads, int n_kv_heads, int head_dim);
+
+/* Attention weight that cached rows gather: for every row s of a sequence with
+ * new tokens and key head h, G = n_heads / n_kv_heads,
+ *   weights[s, h] += sum_t sum_{j in group h} exp(sm_scale q[t, j] . k[s, h] - lse[t, j])
+ * over the new tokens t that see s (0 .. P of dsa_idx_paged_attention, whose
+ * conventions for pages, prefixes, q and sm_scale hold here), in FP32.  The
+ * rows of the new tokens themselves are set, not added to: what an earlier
+ * owner of the slot left does not count.  Rows of sequences without new tokens
+ * stay as they are.
+ *   lse         device fp32 [total_q, n_heads], as dsa_idx_paged_attention
+ *               gives it over every visible key; a row of -inf adds nothing
+ *   weights     device fp32 [num_pages, n_kv_heads, page_size], 16-byte
+ *               aligned: addressed by the page table like the pages' scales
+ * Sequences of one call share no pages.  Only keys are read (a cache of keys
+ * alone will do); they must be finite.  The same inputs give the same bits.
+ * T_d > S_d, a prefix that falls, positions and pages that do not fit are
+ * reported as by dsa_idx_paged_attention; where a prefix falls nothing is
+ * computed, and rows on pages that do not exist are left out. */
+dsa_status_t dsa_idx_cache_weigh(
+    const void* q, int64_t q_stride, const float* lse, const void* k_pages,
+    const uint8_t* k_page_scale, float* weights, int num_pages, int page_size,
+    int n_heads, int n_kv_heads, int head_dim, dsa_precision_t prec,
+    const int32_t* page_table, int max_pages, const int32_t* cu_seqlens_q,
+    const int32_t* cu_seqlens_k, int num_seqs, int total_q, int max_seqlen_q,
+    int max_seqlen_k, float sm_scale, void* ws, size_t ws_bytes,
+    dsa_stream_t stream);
+
+/* Which rows of each sequence stay: all where S_d <= budget, else the `budget`
+ * rows that come first by (one of the first `sinks` or last `recent` rows;
+ * weight, descending; position, ascending).
+ *   weights     as dsa_idx_cache_weigh keeps them (any float: NaN counts as less
+ *               than -inf, -0 as +0)
+ *   shared      0: every key head chooses its own rows; 1: one choice for all
+ *               heads, by the sum of their weights (FP32, head after head)
+ *   kept        device int32 [num_seqs, shared ? 1 : n_kv_heads, budget]:
+ *               positions in ascending order, then -1
+ *   kept_len    device int32 [num_seqs]: min(S_d, budget)
+ *   ws          dsa_idx_cache_workspace_size() bytes
+ * sinks + recent <= budget.  A sequence longer than max_seqlen_k, or than its
+ * pages, is reported in the status and keeps none (-1, 0); a row on a page that
+ * does not exist is reported and weighs NaN. */
+dsa_status_t dsa_idx_evict_select(
+    const float* weights, int num_pages, int page_size, int n_kv_heads,
+    const int32_t* page_table, int max_pages, const int32_t* cu_seqlens_k,
+    int num_seqs, int max_seqlen_k, int budget, int sinks, int recent,
+    int shared, int32_t* kept, int32_t* kept_len, void* ws, size_t ws_bytes,
+    dsa_stream_t stream);
+
+/* Moves the kept rows of every sequence to its first positions, in place: row j
+ * of head h becomes what row kept[d, h, j] was, for j < kept_len[d], in keys,
+ * values (v_pages NULL: keys alone), scales and, unless NULL, weights.  Rows
+ * from kept_len[d] on stay as they were; the caller's next cu_seqlens_k counts
+ * kept_len[d] rows, and whole pages behind them are free.
+ *   kept        device int32 [num_seqs, kept_heads, kept_width], ascending, as
+ *               dsa_idx_evict_select writes it; kept_heads n_kv_heads, or 1: the
+ *               same rows for every head (an index cache beside a shared choice)
+ *   ws          dsa_idx_cache_workspace_size() bytes
+ * Sequences share no pages.  An entry that is not above the one before it or is
+ * not a row of the sequence's pages, and a length outside [0, kept_width], are
+ * reported in the status; rows 0 .. kept_len[d] - 1 of that head (of that
+ * sequence) are then unspecified, and nothing else is touched. */
+dsa_status_t dsa_idx_cache_compact(
+    void* k_pages, uint8_t* k_page_scale, void* v_pages, uint8_t* v_page_scale,
+    float* weights, int num_pages, int page_size, int n_kv_heads, int head_dim,
+    dsa_precision_t prec, const int32_t* page_table, int max_pages,
+    const int32_t* kept, const int32_t* kept_len, int num_seqs, int kept_heads,
+    int kept_width, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
 /* Synchronise `stream` and return the device status word recorded in `ws` by
  * the last call that was given it (DSA_OK if none).  Eager helper; do
  * not call it while capturing a graph. */

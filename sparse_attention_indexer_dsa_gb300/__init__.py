@@ -17,6 +17,8 @@ from . import _abi
 from ._abi import (DSA_FLAG_COMPRESSED_KEYS, DSA_FLAG_DETERMINISTIC, DSA_FLAG_KPOOL_TAIL,  # noqa: F401
                    DSA_FLAG_SORT_BY_SCORE,
                    DSA_PREC_BF16, DSA_PREC_FP8, DSA_PREC_MXFP8)
+from .evict import cache_compact, cache_weigh, evict_select, paged_weights, weigh_workspace  # noqa: F401
+from .norms import NormRopeGrads, norm_rope, norm_rope_backward, norm_rope_workspace  # noqa: F401
 from .paged import _call
 from .paged import (PagedCache, attention_workspace, cache_read, cache_workspace, cache_write,  # noqa: F401
                     paged_attention, paged_cache)
@@ -26,6 +28,8 @@ __all__ = [
     "read_status", "debug_mma_tile", "output_width",
     "PagedCache", "paged_cache", "cache_write", "cache_read", "paged_attention", "cache_workspace",
     "attention_workspace",
+    "norm_rope", "norm_rope_backward", "norm_rope_workspace", "NormRopeGrads",
+    "cache_weigh", "weigh_workspace", "paged_weights", "evict_select", "cache_compact",
 ]
 
 

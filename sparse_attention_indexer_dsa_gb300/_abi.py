@@ -31,6 +31,9 @@ DSA_PREC_FP8 = 2
 # dsa_mx_scale_rule_t
 DSA_MX_SCALE_NOSAT = 0
 DSA_MX_SCALE_FLOOR = 1
+# dsa_norm_t
+DSA_NORM_RMS = 0
+DSA_NORM_LAYER = 1
 # flags
 DSA_FLAG_DETERMINISTIC = 0x1
 DSA_FLAG_SORT_BY_SCORE = 0x2
@@ -41,6 +44,7 @@ DSA_FLAG_COMPRESSED_KEYS = 0x8
 DSA_CACHE_WS_BYTES = 8192
 
 _c_int, _c_i64, _c_f, _c_size, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+_c_d = ctypes.c_double
 
 # name -> (restype, argtypes); every pointer is passed as an integer address
 SIGNATURES = {
@@ -77,6 +81,20 @@ SIGNATURES = {
     "dsa_idx_paged_attention": (_c_int, [_vp, _c_i64, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                                          _c_int, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_f, _vp,
                                          _vp, _c_int, _vp, _vp, _vp, _c_size, _vp]),
+    "dsa_idx_norm_rope": (_c_int, [_vp, _c_i64, _vp, _c_i64, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_f, _vp, _c_int,
+                                   _c_int, _c_int, _c_int, _c_int, _c_d, _vp, _c_int, _vp, _c_i64, _vp, _c_i64, _c_int,
+                                   _vp]),
+    "dsa_idx_norm_rope_workspace_size": (_c_size, [_c_int]),
+    "dsa_idx_norm_rope_backward": (_c_int, [_vp, _c_i64, _vp, _c_i64, _c_int, _vp, _c_i64, _vp, _c_i64, _c_int, _vp, _vp,
+                                            _c_int, _c_int, _c_f, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_d, _vp,
+                                            _c_int, _vp, _c_i64, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "dsa_idx_weigh_workspace_size": (_c_size, [_c_int] * 6),
+    "dsa_idx_cache_weigh": (_c_int, [_vp, _c_i64, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
+                                     _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_f, _vp, _c_size, _vp]),
+    "dsa_idx_evict_select": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                      _c_int, _vp, _vp, _vp, _c_size, _vp]),
+    "dsa_idx_cache_compact": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp,
+                                       _vp, _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
     "dsa_idx_read_status": (_c_int, [_vp, _vp, ctypes.POINTER(_c_int)]),
     "dsa_idx_debug_mma_tile": (_c_int, [_vp, _vp, _c_i64, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_int,
                                         _c_int, _c_int, _vp, _vp, _c_size, _vp]),

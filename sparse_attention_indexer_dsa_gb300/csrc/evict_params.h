@@ -1,0 +1,51 @@
+// Parameter blocks and launchers of the operators that bound a paged cache:
+// the attention weight of its rows (weigh.cuh), the choice of the rows that
+// stay and their moving together (evict.cu).
+#pragma once
+
+#include "paged_params.h"
+
+namespace dsa {
+
+struct WeighParams {
+  PagedCacheView c;
+  float* weights;     // [num_pages][n_kv][page_size]
+  const void* q;
+  int64_t q_stride;   // elements from one token to the next
+  const float* lse;   // [total_q][n_heads]
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int num_seqs, total_q, max_seqlen_q, max_seqlen_k, n_heads, group;
+  uint32_t group_mul; // 2^32 / group, rounded up (group 1: not used)
+  float scale_log2;   // sm_scale * log2(e)
+  int* hdr;
+};
+
+struct SelectParams {
+  const float* weights;
+  const int32_t* table;
+  int num_pages, page_shift, n_kv, max_pages;
+  const int32_t* cu_k;
+  int num_seqs, max_seqlen_k;
+  int budget, sinks, recent, shared;
+  int32_t* kept;       // [num_seqs][shared ? 1 : n_kv][budget]
+  int32_t* kept_len;   // [num_seqs]
+  int* hdr;
+};
+
+struct CompactParams {
+  PagedCacheView c;
+  float* weights;          // null: none
+  const int32_t* kept;     // [num_seqs][heads][width], ascending
+  const int32_t* kept_len; // [num_seqs]
+  int num_seqs, heads, width;
+  int row_bytes;           // of a row of keys or values
+  int slices;              // parts of a row that are moved by blocks of their own
+  int* hdr;
+};
+
+cudaError_t launch_weigh(const WeighParams& p, int D, int sm_count, cudaStream_t stream);
+cudaError_t launch_evict_select(const SelectParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_cache_compact(const CompactParams& p, int sm_count, cudaStream_t stream);
+
+}  // namespace dsa

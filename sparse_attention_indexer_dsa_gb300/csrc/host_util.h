@@ -22,6 +22,16 @@ dsa_status_t device_info(DevInfo* out);
 
 dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, int rows, int D, int box_rows, bool b8);
 
+// Checks that the paged-cache operators share.  The first fills the device view.
+struct PagedCacheView;
+dsa_status_t check_cache(PagedCacheView* c, const void* k_pages, const uint8_t* k_page_scale, const void* v_pages,
+                         const uint8_t* v_page_scale, int num_pages, int page_size, int n_kv_heads, int head_dim,
+                         dsa_precision_t prec, const int32_t* page_table, int max_pages, int num_seqs,
+                         const int32_t* cu_seqlens_k);
+dsa_status_t check_ws(const void* ws, size_t ws_bytes, size_t need);
+// Token stride of a [tokens, heads, head_dim] tensor: 0 = packed.
+dsa_status_t check_stride(int64_t* stride, int heads, int head_dim, int elem_bytes, const char* name);
+
 // Limit of the kernels' bounded waits, and the fault injection of the tests.
 unsigned long long wait_timeout_ns();
 int fault_inject_mode();

@@ -19,7 +19,10 @@ int scale_width(dsa_precision_t prec, int head_dim) {
   return prec == DSA_PREC_MXFP8 ? head_dim / 32 : (prec == DSA_PREC_FP8 ? 1 : 0);
 }
 
-// Checks shared by the three operators; fills the device view.
+}  // namespace
+
+namespace dsa {
+
 dsa_status_t check_cache(PagedCacheView* c, const void* k_pages, const uint8_t* k_page_scale, const void* v_pages,
                          const uint8_t* v_page_scale, int num_pages, int page_size, int n_kv_heads, int head_dim,
                          dsa_precision_t prec, const int32_t* page_table, int max_pages, int num_seqs,
@@ -60,7 +63,6 @@ dsa_status_t check_ws(const void* ws, size_t ws_bytes, size_t need) {
   return DSA_OK;
 }
 
-// Token stride of a [tokens, heads, head_dim] tensor: 0 = packed.
 dsa_status_t check_stride(int64_t* stride, int heads, int head_dim, int elem_bytes, const char* name) {
   const int64_t packed = (int64_t)heads * head_dim;
   if (*stride == 0) *stride = packed;
@@ -68,6 +70,10 @@ dsa_status_t check_stride(int64_t* stride, int heads, int head_dim, int elem_byt
     return fail(DSA_ERR_INVALID_ARG, "%s: a token stride covers its heads and is a multiple of 16 bytes", name);
   return DSA_OK;
 }
+
+}  // namespace dsa
+
+namespace {
 
 constexpr uint32_t round16(uint32_t x) { return (x + 15) / 16 * 16; }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }

@@ -65,6 +65,7 @@
 #include <type_traits>
 
 #include "dsa_device.cuh"
+#include "e4m3_widen.cuh"
 #include "paged_params.h"
 
 namespace dsa {
@@ -80,12 +81,6 @@ constexpr int kOverhead = 4;
 constexpr int kSplitOverhead = 6;
 constexpr int kMaskRing = 8;
 constexpr float kRaise = 20.f;      // log2 of the largest weight before the maximum is raised
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -301,40 +296,6 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams& p, const int* tab,
 
 __device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
-}
-
-// Sixteen E4M3 codes to BF16, times 2^(e8 - 127).  Code bits s.eeee.mmm placed at a BF16's sign, low
-// exponent and high mantissa bits read as value * 2^-120 (subnormals included); one exact product with
-// 2^(120 + e) restores it.  That is a BF16 up to e8 = 134; FAR: beyond it (values over 2^16) there is a
-// second factor.  The NaN code reads as 480 that way.  The quantisers' scale of a block with a NaN is at
-// least 247 (the bits of its magnitude are the largest), so every NaN that they stored is FAR, and is put
-// back there; so is scale 255, which is NaN.
-template <bool FAR>
-__device__ __forceinline__ void widen16(const uint32_t (&w4)[4], uint32_t e8, uint32_t (&o)[8]) {
-  const uint32_t first = FAR ? 254u : e8 + 120u;               // 2^(first - 127): BF16 ends at 2^127
-  __nv_bfloat162 f;
-  *reinterpret_cast<uint32_t*>(&f) = (first << 7) * 0x00010001u;
-#pragma unroll
-  for (int q4 = 0; q4 < 4; ++q4) {
-#pragma unroll
-    for (int hlf = 0; hlf < 2; ++hlf) {
-      const uint32_t t = __byte_perm(w4[q4], 0, hlf ? 0x3424 : 0x1404);
-      uint32_t b = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
-      __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&b), f);
-      o[2 * q4 + hlf] = *reinterpret_cast<uint32_t*>(&v);
-    }
-  }
-  if constexpr (FAR) {
-    __nv_bfloat162 f2;
-    *reinterpret_cast<uint32_t*>(&f2) = ((e8 - 134u + 127u) << 7) * 0x00010001u;
-    const __nv_bfloat162 most = __float2bfloat162_rn(e8 == 255u ? -1.f : 57344.f);   // 448 * 2^7: of the numbers
-#pragma unroll
-    for (int q8 = 0; q8 < 8; ++q8) {
-      const __nv_bfloat162 w = *reinterpret_cast<__nv_bfloat162*>(&o[q8]);
-      __nv_bfloat162 v = __hmul2(w, f2);
-      o[q8] = *reinterpret_cast<uint32_t*>(&v) | __hgt2_mask(__habs2(w), most);
-    }
-  }
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {

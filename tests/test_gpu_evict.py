@@ -1,0 +1,481 @@
+"""A paged cache of bounded length: gathered attention weights, the choice of rows and their moving, against the
+formulas in 64 bits (tests/evict_ref.py, whose bound of the FP32 sums is the tolerance) and together as they are used."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_indexer_dsa_gb300 as dsa
+from tests import evict_ref as E
+from tests.gpu_util import bf16_dev, dev, host
+from tests.paged_ref import Batch, quantise, values
+
+pytestmark = pytest.mark.gpu
+
+
+def queries(rng, T, H, D, std=1.0):
+    bits, _ = quantise(rng.standard_normal((T, H, D)) * std, "bf16")
+    return values(bits, None, "bf16"), bf16_dev(bits)
+
+
+def true_lse(b, q, group, scale):
+    out = np.full(q.shape[:2], -np.inf)
+    for d, (t, s) in enumerate(b.lens):
+        for i in range(t):
+            for hh in range(q.shape[1]):
+                lg = scale * (b.rows["k"][b.cu_k[d]:b.cu_k[d] + s - t + i + 1, hh // group] @ q[b.cu_q[d] + i, hh])
+                out[b.cu_q[d] + i, hh] = lg.max() + np.log(np.exp(lg - lg.max()).sum())
+    return out.astype(np.float32)
+
+
+def weigh(b, c, w, qd, lse, scale, max_q=None, max_k=None, ws=None, status=0):
+    max_q = max(t for t, _ in b.lens) if max_q is None else max_q
+    max_k = max(s for _, s in b.lens) if max_k is None else max_k
+    if ws is None:
+        ws = dsa.weigh_workspace(qd.shape[0], len(b.lens), max_q, qd.shape[1], b.n_kv, b.D)
+    dsa.cache_weigh(c, w, qd, lse, b.dev("cu_q"), b.dev("cu_k"), b.dev("table"), max_q, max_k, sm_scale=scale, ws=ws)
+    assert dsa.read_status(ws) == status
+    return w
+
+
+def close(got, want, tol, what=""):
+    got = host(got.double())
+    over = np.abs(got - want) - tol
+    assert np.isfinite(got).all() and (over <= 0).all(), (what, np.unravel_index(over.argmax(), over.shape), float(over.max()))
+
+
+def check_weigh(b, rng, group, std=2.0, scale=None, pad_q=0):
+    scale = b.D ** -0.5 if scale is None else scale
+    q, qd = queries(rng, b.total_q, b.n_kv * group, b.D, std)
+    lse = true_lse(b, q, group, scale)
+    w = E.random_weights(rng, b)
+    got = weigh(b, b.cache(dsa), dev(w), qd, dev(lse), scale)
+    want, tol = E.weigh(b, q, lse.astype(np.float64), w, group, scale)
+    close(got, want, tol)
+    return got
+
+
+LENS = {
+    "one": [(1, 1)],
+    "steps": [(1, 1), (1, 31), (1, 32), (0, 9), (1, 33), (1, 600)],
+    "chunk": [(33, 33), (0, 0), (17, 300), (1, 260), (130, 131)],
+    "prompt": [(257, 257)],
+}
+
+
+@pytest.mark.parametrize("lens", list(LENS))
+@pytest.mark.parametrize("kv,group", [(1, 1), (2, 8), (1, 64), (3, 5)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8", "fp8"])
+def test_weigh(lens, kv, group, D, prec):
+    rng = np.random.default_rng([sorted(LENS).index(lens), kv, group, D, len(prec)])
+    b = Batch(rng, LENS[lens], kv, D, 16, prec)
+    check_weigh(b, rng, group)
+
+
+@pytest.mark.parametrize("page", [8, 64, 1024])
+@pytest.mark.parametrize("lens", [[(1, 700), (3, 64), (1, 1025)], [(200, 900)], [(70, 70), (1, 2000), (0, 40), (40, 400)]])
+def test_weigh_pages(page, lens):
+    rng = np.random.default_rng([page, len(lens)])
+    b = Batch(rng, lens, 2, 128, page, "mxfp8", values_too=False, pad_q=5)
+    check_weigh(b, rng, 4)
+
+
+@pytest.mark.parametrize("group,T", [(128, 9), (1, 300), (7, 41), (2, 520)])
+def test_weigh_groups(group, T):
+    rng = np.random.default_rng([group, T])
+    b = Batch(rng, [(T, T + 77), (1, 300)], 1, 64, 32, "bf16", values_too=False)
+    check_weigh(b, rng, group)
+
+
+def test_weigh_far_scales():
+    """8-bit rows whose scales are far from one: the widened values span BF16's range."""
+    rng = np.random.default_rng(31)
+    for prec in ("mxfp8", "fp8"):
+        b = Batch(rng, [(1, 90), (40, 70)], 1, 128, 16, prec, std=3e5)
+        check_weigh(b, rng, 2, std=1e-6)
+
+
+def test_weigh_strange_lse():
+    """Rows that saw nothing add nothing; scale 0 weighs every row alike."""
+    rng = np.random.default_rng(32)
+    b = Batch(rng, [(2, 40), (80, 100)], 2, 64, 16, "bf16", values_too=False)
+    q, qd = queries(rng, b.total_q, 4, 64)
+    lse = true_lse(b, q, 2, 0.125)
+    lse[1] = -np.inf
+    lse[30:40, 1] = -np.inf
+    w = E.random_weights(rng, b)
+    got = weigh(b, b.cache(dsa), dev(w), qd, dev(lse), 0.125)
+    close(got, *E.weigh(b, q, lse.astype(np.float64), w, 2, 0.125))
+    lse = true_lse(b, q, 2, 0.0)
+    got = weigh(b, b.cache(dsa), dev(w), qd, dev(lse), 0.0)
+    close(got, *E.weigh(b, q, lse.astype(np.float64), w, 2, 0.0))
+
+
+def test_weigh_leaves_other_slots_and_repeats():
+    rng = np.random.default_rng(33)
+    b = Batch(rng, [(1, 50), (0, 33), (90, 131)], 2, 128, 16, "mxfp8", pad_q=7)
+    q, qd = queries(rng, b.total_q, 16, 128)
+    lse = true_lse(b, q, 8, 0.1)
+    w = E.random_weights(rng, b)
+    used = np.zeros(w.shape, bool)
+    for d in (0, 2):
+        used[E.rows_of(b, d)[0], :, E.rows_of(b, d)[1]] = True
+    w[~used] = np.nan
+    got = [host(weigh(b, b.cache(dsa), dev(w), qd, dev(lse), 0.1)) for _ in range(3)]
+    assert np.isnan(got[0][~used]).all() and np.isfinite(got[0][used]).all()
+    assert all(np.array_equal(got[0], g, equal_nan=True) for g in got[1:])
+    # a token adds its number of heads in all
+    added = got[0].astype(np.float64)
+    page, slot = E.rows_of(b, 0)
+    old = w[page, :, slot].astype(np.float64)
+    old[49:] = 0
+    assert np.allclose((added[page, :, slot] - old).sum(0), 8, atol=1e-4)
+
+
+def test_weigh_with_strided_queries_and_the_attentions_lse():
+    rng = np.random.default_rng(34)
+    b = Batch(rng, [(1, 500), (60, 333)], 2, 128, 32, "fp8")
+    wide = torch.randn(b.total_q, 8 + 3, 128, device="cuda").bfloat16()
+    qd = wide[:, :8]
+    c = b.cache(dsa)
+    _, lse = dsa.paged_attention(qd, c, b.dev("cu_q"), b.dev("cu_k"), b.dev("table"), 60, 500, return_lse=True)
+    w = dsa.paged_weights(c)
+    weigh(b, c, w, qd, lse, None)
+    want, tol = E.weigh(b, host(qd.double()), host(lse).astype(np.float64), np.zeros(w.shape, np.float32), 4, 128 ** -0.5)
+    close(w, want, tol)
+
+
+def test_weigh_reports():
+    rng = np.random.default_rng(35)
+    b = Batch(rng, [(1, 40), (3, 50)], 1, 64, 16, "bf16", values_too=False)
+    q, qd = queries(rng, b.total_q, 2, 64)
+    lse = dev(true_lse(b, q, 2, 0.1))
+    w = E.random_weights(rng, b)
+    c = b.cache(dsa)
+    want, tol = E.weigh(b, q, host(lse).astype(np.float64), w, 2, 0.1)
+    # a page that does not exist: its rows are left out
+    t = b.table[1, 1]
+    b.table[1, 1] = b.num_pages
+    got = weigh(b, c, dev(w), qd, lse, 0.1, status=1)
+    other = np.ones(w.shape, bool)
+    other[t] = False
+    assert np.array_equal(host(got)[t], w[t])
+    close(got, np.where(other, want, w), tol)
+    b.table[1, 1] = t
+    # a bound that is too small: that sequence is not computed
+    got = host(weigh(b, c, dev(w), qd, lse, 0.1, max_k=45, status=1))
+    page, slot = E.rows_of(b, 1)
+    assert np.array_equal(got[page, :, slot], w[page, :, slot])
+    # a prefix that falls: nothing is
+    for name, bad in (("cu_q", [0, 3, 1]), ("cu_k", [0, 50, 40])):
+        keep = getattr(b, name)
+        setattr(b, name, np.array(bad, np.int32))
+        assert np.array_equal(host(weigh(b, c, dev(w), qd, lse, 0.1, status=1)), w)
+        setattr(b, name, keep)
+    # more new tokens than rows, more tokens than there are
+    for name, bad in (("cu_k", [0, 40, 42]), ("cu_q", [0, 1, 9])):
+        keep = getattr(b, name)
+        setattr(b, name, np.array(bad, np.int32))
+        got = host(weigh(b, c, dev(w), qd, lse, 0.1, status=1))
+        assert np.array_equal(got[page, :, slot], w[page, :, slot])
+        setattr(b, name, keep)
+
+
+def test_weigh_empty():
+    rng = np.random.default_rng(36)
+    b = Batch(rng, [(0, 10), (0, 0)], 1, 64, 8, "bf16", values_too=False)
+    w = E.random_weights(rng, b)
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    got = weigh(b, b.cache(dsa), dev(w), q, torch.empty(0, 4, device="cuda"), 1.0)
+    assert np.array_equal(host(got), w)
+
+
+# ---------------------------------------------------------------- choice
+
+def check_select(b, w, budget, sinks, recent, shared, max_k=None):
+    ws = dsa.cache_workspace()
+    max_k = max(s for _, s in b.lens) if max_k is None else max_k
+    kept, n = dsa.evict_select(dev(w), b.dev("cu_k"), b.dev("table"), budget, max_k, sinks=sinks, recent=recent,
+                               shared=shared, ws=ws)
+    assert dsa.read_status(ws) == 0
+    want, wn = E.select(b, w, budget, sinks, recent, shared)
+    assert np.array_equal(host(n), wn) and np.array_equal(host(kept), want)
+
+
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (1, 1, 0), (64, 4, 16), (100, 0, 100), (127, 100, 27), (1500, 3, 0)])
+def test_select(ties, shared, budget, sinks, recent):
+    rng = np.random.default_rng([ties, shared, budget, sinks, recent])
+    b = Batch(rng, [(0, s) for s in (0, 1, 63, 64, 65, 127, 1023, 1025, 2100)], 3, 64, 16, "bf16", values_too=False)
+    check_select(b, E.random_weights(rng, b, ties), budget, sinks, recent, shared)
+
+
+@pytest.mark.parametrize("page", [8, 1024])
+def test_select_long(page):
+    """More rows than shared memory holds."""
+    rng = np.random.default_rng(page)
+    b = Batch(rng, [(0, 70001), (0, 300)], 1, 64, page, "fp8", values_too=False)
+    w = E.random_weights(rng, b)
+    for budget in (200, 4096, 70000):
+        check_select(b, w, budget, 4, 64, False)
+    check_select(b, E.random_weights(rng, b, True), 5000, 0, 0, True)
+
+
+def test_select_strange_weights():
+    rng = np.random.default_rng(41)
+    b = Batch(rng, [(0, 400), (0, 90)], 2, 64, 8, "bf16", values_too=False)
+    w = E.random_weights(rng, b)
+    flat = w.reshape(-1)
+    for v in (np.nan, -np.nan, np.inf, -np.inf, -0.0, 0.0, 1e-45, -1e-45, np.finfo(np.float32).max, np.finfo(np.float32).min):
+        flat[rng.random(flat.size) < 0.06] = v
+    for budget in (1, 5, 30, 80, 380):
+        check_select(b, w, budget, 1 if budget > 1 else 0, 2 if budget > 4 else 0, False)
+    for v in (0.0, np.nan, np.inf, -1.0):      # all alike: the first ones
+        check_select(b, np.full_like(w, v), 37, 2, 5, False)
+
+
+def test_select_wide_table_and_outputs():
+    rng = np.random.default_rng(42)
+    b = Batch(rng, [(0, 50), (0, 20)], 2, 64, 8, "bf16", values_too=False)
+    w = E.random_weights(rng, b)
+    check_select(b, w, 10, 1, 1, False, max_k=1 << 20)       # a bound far above the lengths
+    out = (torch.full((2, 2, 10), 9, dtype=torch.int32, device="cuda"), torch.full((2,), 9, dtype=torch.int32, device="cuda"))
+    got = dsa.evict_select(dev(w), b.dev("cu_k"), b.dev("table"), 10, 50, out=out)
+    assert got[0] is out[0] and np.array_equal(host(out[0]), E.select(b, w, 10, 0, 0, False)[0])
+
+
+def test_select_reports():
+    rng = np.random.default_rng(43)
+    b = Batch(rng, [(0, 50), (0, 40)], 1, 64, 8, "bf16", values_too=False)
+    w = E.random_weights(rng, b)
+    want, _ = E.select(b, w, 10, 0, 0, False)
+    ws = dsa.cache_workspace()
+
+    def run(max_k=50):
+        kept, n = dsa.evict_select(dev(w), b.dev("cu_k"), b.dev("table"), 10, max_k, ws=ws)
+        assert dsa.read_status(ws) == 1
+        return host(kept), host(n)
+
+    kept, n = run(max_k=45)
+    assert (kept[0] == -1).all() and np.array_equal(kept[1], want[1]) and list(n) == [0, 10]
+    keep, b.cu_k = b.cu_k, np.array([0, 50, 45], np.int32)
+    kept, n = run()
+    assert (kept[1] == -1).all() and np.array_equal(kept[0], want[0]) and list(n) == [10, 0]
+    b.cu_k = keep
+    b.table[0, 2] = -7
+    kept, n = run()
+    assert not ((kept[0] >= 16) & (kept[0] < 24)).any() and list(n) == [10, 10]
+
+
+# ---------------------------------------------------------------- moving
+
+def tensors_of(b, w=None):
+    t = {}
+    for nm in b.names:
+        t[nm] = b.pages[nm]
+        if b.scales[nm] is not None:
+            t[nm + "_scale"] = b.scales[nm]
+    if w is not None:
+        t["weights"] = w
+    return t
+
+
+def as_bits(t):
+    return host(t.view(torch.int16)).view(np.uint16) if t.dtype == torch.bfloat16 else host(t)
+
+
+def check_compact(b, rng, kept, kept_len, w=None, status=0):
+    c, ws = b.cache(dsa), dsa.cache_workspace()
+    wd = None if w is None else dev(w)
+    dsa.cache_compact(c, dev(kept), dev(kept_len), b.dev("table"), weights=wd, ws=ws)
+    assert dsa.read_status(ws) == status
+    want = E.compact(b, tensors_of(b, w), kept, kept_len)
+    got = {"k": c.k, "k_scale": c.k_scale, "v": c.v, "v_scale": c.v_scale, "weights": wd}
+    for name, x in want.items():
+        assert np.array_equal(as_bits(got[name]), x), name
+
+
+def some_rows(rng, b, heads, width, part=0.5):
+    kept = np.full((len(b.lens), heads, width), -1, np.int32)
+    n = np.array([min(width, int(round(s * part))) for _, s in b.lens], np.int32)
+    for d, (_, s) in enumerate(b.lens):
+        for h in range(heads):
+            kept[d, h, :n[d]] = np.sort(rng.choice(s, n[d], replace=False))
+    return kept, n
+
+
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kv,heads", [(1, 1), (3, 3), (3, 1)])
+@pytest.mark.parametrize("part", [0.1, 0.9, 1.0])
+def test_compact(prec, D, kv, heads, part):
+    rng = np.random.default_rng([len(prec), D, kv, heads, int(10 * part)])
+    b = Batch(rng, [(0, 0), (0, 1), (0, 17), (0, 700), (0, 2500)], kv, D, 16, prec)
+    kept, n = some_rows(rng, b, heads, 2600, part)
+    check_compact(b, rng, kept, n, E.random_weights(rng, b))
+
+
+@pytest.mark.parametrize("page", [8, 1024])
+@pytest.mark.parametrize("prec,values_too,weights", [("bf16", False, False), ("mxfp8", False, True), ("fp8", True, False)])
+def test_compact_parts(page, prec, values_too, weights):
+    rng = np.random.default_rng([page, len(prec)])
+    b = Batch(rng, [(0, 9000), (0, 1300)], 1, 128, page, prec, values_too=values_too)
+    kept, n = some_rows(rng, b, 1, 5000, 0.8)
+    check_compact(b, rng, kept, n, E.random_weights(rng, b) if weights else None)
+
+
+def test_compact_many_sequences():
+    rng = np.random.default_rng(51)
+    b = Batch(rng, [(0, int(s)) for s in rng.integers(0, 90, 300)], 4, 64, 8, "mxfp8")
+    kept, n = some_rows(rng, b, 4, 40)
+    check_compact(b, rng, kept, n, E.random_weights(rng, b))
+
+
+def test_compact_shifts_by_one():
+    """Every row but one stays: each chunk reads what the one before it has to leave alone."""
+    rng = np.random.default_rng(52)
+    for gone in (0, 1, 255, 256, 2999):
+        b = Batch(rng, [(0, 3000)], 2, 128, 64, "mxfp8")
+        kept = np.delete(np.arange(3000, dtype=np.int32), gone)[None, None]
+        check_compact(b, rng, kept, np.array([2999], np.int32), E.random_weights(rng, b))
+
+
+def test_compact_reports():
+    rng = np.random.default_rng(53)
+    b = Batch(rng, [(0, 100), (0, 80)], 2, 64, 8, "fp8")
+    kept, n = some_rows(rng, b, 2, 50)
+    good = E.compact(b, tensors_of(b), kept, n)
+    page1 = E.rows_of(b, 1)
+    for bad in ("falls", "twice", "behind", "before", "length", "width"):
+        k, m = kept.copy(), n.copy()
+        if bad == "falls":
+            k[0, 0, 10], k[0, 0, 20] = k[0, 0, 20], k[0, 0, 10]
+        elif bad == "twice":
+            k[0, 0, 11] = k[0, 0, 10]
+        elif bad == "behind":
+            k[0, 0, int(m[0]) - 1] = 1 << 29
+        elif bad == "before":
+            k[0, 0, 0] = -5
+        elif bad == "length":
+            m[0] = -1
+        else:
+            m[0] = 51
+        c, ws = b.cache(dsa), dsa.cache_workspace()
+        dsa.cache_compact(c, dev(k), dev(m), b.dev("table"), ws=ws)
+        assert dsa.read_status(ws) == 1, bad
+        for nm, t in (("k", c.k), ("v", c.v), ("v_scale", c.v_scale)):
+            got, start = as_bits(t), tensors_of(b)[nm]
+            assert np.array_equal(got[page1[0], :, page1[1]], good[nm][page1[0], :, page1[1]]), bad
+            outside = np.ones(start.shape[0], bool)
+            outside[b.table[0, :13]] = outside[b.table[1, :10]] = False
+            assert np.array_equal(got[outside], start[outside]), bad
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("shared", [False, True])
+def test_a_bounded_cache_step_by_step(prec, shared):
+    """A prompt in chunks, then single tokens, through norm_rope, cache_write, paged_attention, cache_weigh and, over
+    the budget, evict_select and cache_compact, with an index cache that keeps the same rows where the choice is shared:
+    the rows that a cache holds are those that a plain run of the choices keeps, bit for bit."""
+    torch.manual_seed(7)
+    kv, group, D, page, budget, B = 2, 4, 128, 16, 96, 3
+    pages = B * 12
+    table = torch.randperm(pages, device="cuda").to(torch.int32).view(B, 12)
+    cache = dsa.paged_cache(pages, page, kv, D, prec)
+    index = dsa.paged_cache(pages, page, 1, D, "bf16", values=False)
+    weights = dsa.paged_weights(cache)
+    lens = [0] * B
+    held = [[[] for _ in range(kv)] for _ in range(B)]        # positions of the rows that each head holds
+    qw, kw = torch.rand(D, device="cuda") + 0.5, torch.rand(D, device="cuda") + 0.5
+    seen = [0] * B
+    keys = [torch.empty(0, kv, D, device="cuda") for _ in range(B)]    # of every position, as written
+    for step in range(12):
+        new = [70, 33, 1] if step == 0 else ([40, 50, 64] if step == 1 else [1, 1, 1])
+        T = sum(new)
+        cu_q = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+        for d in range(B):
+            lens[d] += new[d]
+        cu_k = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+        pos = torch.cat([torch.arange(seen[d], seen[d] + new[d]) for d in range(B)]).to(torch.int32).cuda()
+        x = torch.randn(T, (group + 2) * kv, D, device="cuda").bfloat16()
+        q, k = dsa.norm_rope(x[:, :group * kv], x[:, group * kv:group * kv + kv], pos, qw, kw)
+        dsa.cache_write(cache, k, x[:, group * kv + kv:], cu_q, cu_k, table)
+        dsa.cache_write(index, k[:, :1], None, cu_q, cu_k, table)
+        max_q, max_k = max(new), max(lens)
+        out, lse = dsa.paged_attention(q, cache, cu_q, cu_k, table, max_q, max_k, return_lse=True)
+        dsa.cache_weigh(cache, weights, q, lse, cu_q, cu_k, table, max_q, max_k)
+        at = 0
+        for d in range(B):
+            keys[d] = torch.cat([keys[d], k[at:at + new[d]].float()])
+            at += new[d]
+            for h in range(kv):
+                held[d][h] += range(seen[d], seen[d] + new[d])
+            seen[d] += new[d]
+        before = host(weights)
+        kept, n = dsa.evict_select(weights, cu_k, table, budget, max_k, sinks=2, recent=8, shared=shared)
+        dsa.cache_compact(cache, kept, n, table, weights=weights)
+        if shared:
+            dsa.cache_compact(index, kept, n, table)
+        rows, m = host(kept), host(n)
+        for d in range(B):
+            for h in range(kv):
+                mine = rows[d, 0 if shared else h, :m[d]]
+                w = np.concatenate([before[p] for p in host(table)[d]], axis=1)[h] if not shared else None
+                if not shared and lens[d] > budget:      # the lightest that stays is no lighter than the heaviest that goes
+                    gone = np.setdiff1d(np.arange(2, lens[d] - 8), mine)
+                    free = mine[(mine >= 2) & (mine < lens[d] - 8)]
+                    assert w[free].min() >= w[gone].max()
+                held[d][h] = [held[d][h][i] for i in mine]
+            lens[d] = int(m[d])
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+        got, _, _, _ = dsa.cache_read(cache, cu, table, sum(lens), out_prec="bf16")
+        idx, _, _, _ = dsa.cache_read(index, cu, table, sum(lens))
+        at = 0
+        for d in range(B):
+            for h in range(kv):
+                want = keys[d][held[d][h], h]
+                have = got[at:at + lens[d], h].float()
+                if prec == "bf16":
+                    assert torch.equal(have, want)
+                else:       # half a step of E4M3 relative, or of its smallest under the block's scale
+                    amax = want.view(-1, D // 32, 32).abs().amax(-1, keepdim=True).expand(-1, -1, 32).reshape(want.shape)
+                    assert ((have - want).abs() <= torch.maximum(want.abs() * 2.0 ** -4, amax * 2.0 ** -16)).all()
+            if shared:
+                assert torch.equal(idx[at:at + lens[d], 0].float(), keys[d][held[d][0], 0])
+            at += lens[d]
+    assert lens == [96, 93, 75]
+
+
+def test_streams_and_graphs():
+    rng = np.random.default_rng(61)
+    b = Batch(rng, [(1, 300), (70, 200)], 2, 64, 16, "mxfp8")
+    q, qd = queries(rng, b.total_q, 8, 64)
+    lse = dev(true_lse(b, q, 4, 0.1))
+    w0 = E.random_weights(rng, b)
+    args = [b.dev(n) for n in ("cu_q", "cu_k", "table")]
+    ws = dsa.weigh_workspace(b.total_q, 2, 70, 8, 2, 64)
+    cw = dsa.cache_workspace()
+
+    def run(c, w):
+        dsa.cache_weigh(c, w, qd, lse, *args, 70, 300, sm_scale=0.1, ws=ws)
+        kept, n = dsa.evict_select(w, args[1], args[2], 128, 300, sinks=1, recent=9, ws=cw)
+        dsa.cache_compact(c, kept, n, args[2], weights=w, ws=cw)
+        return kept, n
+
+    c1, w1 = b.cache(dsa), dev(w0)
+    kept, n = run(c1, w1)
+    c2, w2 = b.cache(dsa), dev(w0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = run(c2, w2)
+        w2.copy_(dev(w0))          # nothing ran at capture
+        graph.replay()
+    s.synchronize()
+    assert torch.equal(got[0], kept) and torch.equal(got[1], n) and torch.equal(w1, w2)
+    assert torch.equal(c1.k, c2.k) and torch.equal(c1.v, c2.v) and torch.equal(c1.k_scale, c2.k_scale)

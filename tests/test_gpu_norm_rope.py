@@ -1,0 +1,241 @@
+"""Norms of queries and keys with the rotation, and their gradients, against their formulas in 64 bits.
+
+The tolerances are the bounds of tests/norm_ref.py: FP32 arithmetic, one rounding of what is stored."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_indexer_dsa_gb300 as dsa
+from tests import norm_ref as R
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+EPS = 1e-6
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def close(got, want, tol, what):
+    got = host(got) if torch.is_tensor(got) else got
+    assert np.isfinite(got).all(), what
+    over = np.abs(got - want) - tol
+    assert (over <= 0).all(), (what, np.unravel_index(over.argmax(), over.shape), float(over.max()))
+
+
+def inputs(rng, T, H, Hk, D, src, norm, wt="f32", strided=True, std=1.0, far=1 << 20):
+    x = rng.standard_normal((T, H + Hk, D)) * std
+    x[rng.random(x.shape) < 0.02] *= 9.0
+    x = torch.from_numpy(x).cuda().to(DT[src])
+    q, k = (x[:, :H], x[:, H:]) if strided else (x[:, :H].contiguous(), x[:, H:].contiguous())
+    def row(m, s):
+        return (m + s * torch.from_numpy(rng.standard_normal(D))).cuda().to(DT[wt])
+    w = [row(1.0, 0.2), row(1.0, 0.2)] + ([row(0.0, 0.2), row(0.0, 0.2)] if norm == "layer" else [None, None])
+    pos = torch.from_numpy(rng.integers(0, far, T).astype(np.int32)).cuda()
+    return q, k, pos, w
+
+
+def check_forward(q, k, pos, w, got, norm, rope_dim, inter, out, **kw):
+    for x, y, wi, bi, what in ((q, got[0], w[0], w[2], "q"), (k, got[1], w[1], w[3], "k")):
+        if x is None:
+            assert y is None
+            continue
+        a = (host(x), None if wi is None else host(wi), None if bi is None else host(bi), host(pos))
+        want = R.forward(*a, norm, EPS, rope_dim, inter, **kw)
+        close(y, want, R.forward_tol(*a, norm, EPS, rope_dim, inter, out, want), what)
+
+
+@pytest.mark.parametrize("norm,inter", [("rms", False), ("layer", False), ("rms", True), ("layer", True)])
+@pytest.mark.parametrize("D,rope_dim", [(64, 64), (64, 8), (128, 128), (128, 64), (128, 24), (128, 0)])
+@pytest.mark.parametrize("src,out", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_forward(norm, inter, D, rope_dim, src, out):
+    rng = np.random.default_rng([ord(norm[0]), inter, D, rope_dim, len(src), len(out)])
+    q, k, pos, w = inputs(rng, 13, 6, 3, D, src, norm)
+    got = dsa.norm_rope(q, k, pos, *w, norm=norm, eps=EPS, rope_dim=rope_dim, rope_interleaved=inter, out_dtype=DT[out])
+    check_forward(q, k, pos, w, got, norm, rope_dim, inter, out)
+
+
+@pytest.mark.parametrize("T,H,Hk", [(1, 1, 1), (1, 64, 8), (33, 1, 1), (200, 20, 5), (5, 128, 128), (3, 1, 0), (40, 3, 0),
+                                    (1000, 2, 1), (7, 1024, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_forward_shapes(T, H, Hk, D):
+    rng = np.random.default_rng([T, H, Hk, D])
+    q, k, pos, w = inputs(rng, T, H, max(Hk, 1), D, "bf16", "rms", wt="bf16", strided=Hk > 0)
+    if Hk == 0:
+        k, w = None, [w[0], None, None, None]
+    got = dsa.norm_rope(q, k, pos, *w, eps=EPS)
+    check_forward(q, k, pos, w, got, "rms", D, False, "bf16")
+
+
+def test_no_weights_in_place_and_given_outputs():
+    rng = np.random.default_rng(5)
+    q, k, pos, _ = inputs(rng, 50, 7, 2, 128, "bf16", "rms")
+    none = [None] * 4
+    got = dsa.norm_rope(q, k, pos, eps=EPS)
+    check_forward(q, k, pos, none, got, "rms", 128, False, "bf16")
+    wide = torch.full((50, 12, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = (wide[:, 1:8], wide[:, 9:11])
+    assert dsa.norm_rope(q, k, pos, eps=EPS, out=out)[0] is out[0]
+    assert torch.equal(out[0], got[0]) and torch.equal(out[1], got[1])
+    assert (wide[:, [0, 8, 11]] == 7.0).all()
+    dsa.norm_rope(q, k, pos, eps=EPS, out=(q, k))          # over the inputs
+    assert torch.equal(q, got[0]) and torch.equal(k, got[1])
+
+
+def test_frequencies_and_far_positions():
+    rng = np.random.default_rng(6)
+    q, k, _, w = inputs(rng, 9, 2, 1, 64, "f32", "rms")
+    pos = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1 << 20, 65535, -12345, 7], dtype=torch.int32, device="cuda")
+    freq = [float(f) for f in rng.uniform(-1.0, 1.0, 16)]
+    got = dsa.norm_rope(q, k, pos, *w, eps=EPS, rope_dim=32, inv_freq=freq)
+    # a frequency in turns is rounded to 2^-54 of a turn: 2^31 positions on, 2^-23 of one
+    near = [i for i in range(9) if abs(int(pos[i])) <= 1 << 20]
+    p = pos[near]
+    check_forward(q[near], k[near], p, w, (got[0][near], got[1][near]), "rms", 32, False, "f32", inv_freq=freq)
+    a = R.forward(host(q), host(w[0]), None, host(pos), "rms", EPS, 32, False, inv_freq=freq)
+    assert np.abs(host(got[0]) - a).max() < 1e-4
+
+
+def test_rows_do_not_touch_one_another():
+    rng = np.random.default_rng(7)
+    q, k, pos, w = inputs(rng, 11, 5, 2, 128, "f32", "layer", strided=False)
+    want = dsa.norm_rope(q, k, pos, *w, norm="layer", eps=EPS)
+    q2, k2 = q.clone(), k.clone()
+    q2[3, 1, 5] = float("nan")
+    k2[8, 0, 127] = float("inf")
+    got = dsa.norm_rope(q2, k2, pos, *w, norm="layer", eps=EPS)
+    bad = torch.zeros(11, 5, dtype=torch.bool, device="cuda")
+    bad[3, 1] = True
+    assert got[0][bad].isnan().all() and torch.equal(got[0][~bad], want[0][~bad])
+    bad = torch.zeros(11, 2, dtype=torch.bool, device="cuda")
+    bad[8, 0] = True
+    assert not got[1][bad].isfinite().any() and torch.equal(got[1][~bad], want[1][~bad])
+    zero = torch.zeros_like(q)
+    y, _ = dsa.norm_rope(zero, None, pos, w[0], q_bias=w[2], norm="layer", eps=EPS, rope_dim=0)
+    assert torch.equal(y, w[2].expand_as(y))
+
+
+def test_empty_and_ranges_of_values():
+    q = torch.empty(0, 4, 64, device="cuda")
+    pos = torch.empty(0, dtype=torch.int32, device="cuda")
+    a, b = dsa.norm_rope(q, q[:, :1], pos)
+    assert a.shape == (0, 4, 64) and b.shape == (0, 1, 64)
+    g = dsa.norm_rope_backward(q, q[:, :1], q, q[:, :1], pos, norm="layer")
+    assert g.q.shape == q.shape and all((t == 0).all() for t in g[2:])
+    rng = np.random.default_rng(8)
+    for std in (1e-12, 1e12):          # FP32 squares of 1e12 sum to 1e26; below eps the norm is linear
+        q, k, pos, w = inputs(rng, 20, 3, 1, 128, "f32", "rms", std=std)
+        check_forward(q, k, pos, w, dsa.norm_rope(q, k, pos, *w, eps=EPS), "rms", 128, False, "f32")
+
+
+def grads(q, k, pos, w, dq, dk, norm, rope_dim, inter, ws=None):
+    return dsa.norm_rope_backward(dq, dk, q, k, pos, w[0], w[1], norm=norm, eps=EPS, rope_dim=rope_dim,
+                                  rope_interleaved=inter, ws=ws)
+
+
+def check_backward(q, k, pos, w, dq, dk, g, norm, rope_dim, inter, src):
+    for x, d, wi, gx, gw, gb, what in ((q, dq, w[0], g.q, g.q_weight, g.q_bias, "q"), (k, dk, w[1], g.k, g.k_weight, g.k_bias, "k")):
+        if x is None:
+            assert gx is None and gw is None and gb is None
+            continue
+        a = (host(d), host(x), None if wi is None else host(wi), host(pos), norm, EPS, rope_dim, inter)
+        dx, dw, db = R.backward(*a)
+        tx, tw, tb = R.backward_tol(*a, src, dx)
+        close(gx, dx, tx, what)
+        close(gw, dw, tw, what + "_weight")
+        if norm == "layer":
+            close(gb, db, tb, what + "_bias")
+        else:
+            assert gb is None
+
+
+@pytest.mark.parametrize("norm,inter", [("rms", False), ("layer", False), ("rms", True), ("layer", True)])
+@pytest.mark.parametrize("D,rope_dim", [(64, 64), (64, 16), (128, 128), (128, 40), (128, 0)])
+@pytest.mark.parametrize("src,grad", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_backward(norm, inter, D, rope_dim, src, grad):
+    rng = np.random.default_rng([ord(norm[0]), inter, D, rope_dim, len(src), len(grad)])
+    q, k, pos, w = inputs(rng, 29, 5, 2, D, src, norm)
+    d = torch.from_numpy(rng.standard_normal((29, 7, D))).cuda().to(DT[grad])
+    dq, dk = d[:, :5], d[:, 5:]
+    g = grads(q, k, pos, w, dq, dk, norm, rope_dim, inter)
+    check_backward(q, k, pos, w, dq, dk, g, norm, rope_dim, inter, src)
+
+
+@pytest.mark.parametrize("T,H,Hk", [(1, 1, 1), (1, 64, 8), (700, 3, 1), (40, 128, 128), (9, 3, 0), (3000, 16, 2)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_backward_shapes_and_bits(T, H, Hk, D):
+    rng = np.random.default_rng([T, H, Hk, D, 1])
+    q, k, pos, w = inputs(rng, T, H, max(Hk, 1), D, "bf16", "rms", wt="bf16")
+    d = torch.from_numpy(rng.standard_normal((T, H + 1 + Hk, D))).cuda().to(torch.bfloat16)
+    dq, dk = d[:, :H], d[:, H:H + Hk]
+    if Hk == 0:
+        k, dk, w = None, None, [w[0], None, None, None]
+    ws = dsa.norm_rope_workspace(D)
+    g = grads(q, k, pos, w, dq, dk, "rms", D, False, ws)
+    assert dsa.read_status(ws) == 0
+    check_backward(q, k, pos, w, dq, dk, g, "rms", D, False, "bf16")
+    again = grads(q, k, pos, w, dq, dk, "rms", D, False, ws)
+    for a, b in zip(g, again):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("norm,inter", [("rms", False), ("layer", True)])
+def test_gradients_against_differences(norm, inter):
+    """d loss of the forward kernel itself, with loss = sum dy y in 64 bits: central differences of step h are off by
+    the forward's FP32 rounding over h and by h^2 third derivatives."""
+    rng = np.random.default_rng(12)
+    q, k, pos, w = inputs(rng, 3, 2, 1, 64, "f32", norm, strided=False, far=5000)
+    w = [t if t is None else t.float() for t in w]
+    dq, dk = (torch.from_numpy(rng.standard_normal(t.shape)).cuda().float() for t in (q, k))
+    g = grads(q, k, pos, w, dq, dk, norm, 32, inter)
+
+    def loss(q, k, w):
+        a, b = dsa.norm_rope(q, k, pos, *w, norm=norm, eps=EPS, rope_dim=32, rope_interleaved=inter)
+        return float((a.double() * dq.double()).sum() + (b.double() * dk.double()).sum())
+
+    h = 2.0 ** -6
+    # an output is off by at most some 40 half steps of the pair it is part of (norm_ref.lost, the turn): both losses by
+    # that of sum |dy| 2 |y|; third derivatives of a row of 64 normed values are below 50
+    y = dsa.norm_rope(q, k, pos, *w, norm=norm, eps=EPS, rope_dim=32, rope_interleaved=inter)
+    size = sum(float((a.double().abs() * b.double().abs()).sum()) for a, b in zip(y, (dq, dk)))
+    noise = 2 * 40 * 2.0 ** -24 * size / h
+    for i, (x, gx) in enumerate(((q, g.q), (k, g.k), (w[0], g.q_weight), (w[1], g.k_weight))):
+        for at in rng.integers(0, x.numel(), 6):
+            v = []
+            for s in (h, -h):
+                y = x.clone()
+                y.view(-1)[at] += s
+                args = [q, k, list(w)]
+                if i < 2:
+                    args[i] = y
+                else:
+                    args[2][i - 2] = y
+                v.append(loss(*args))
+            diff = (v[0] - v[1]) / (2 * h)
+            assert abs(diff - float(gx.view(-1)[at])) < noise + 50 * h * h, (i, int(at))
+
+
+def test_streams_and_graphs():
+    rng = np.random.default_rng(13)
+    q, k, pos, w = inputs(rng, 300, 8, 2, 128, "bf16", "rms")
+    d = torch.randn(300, 10, 128, device="cuda").bfloat16()
+    want, gw = dsa.norm_rope(q, k, pos, *w), grads(q, k, pos, w, d[:, :8], d[:, 8:], "rms", 128, False)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        out = [torch.zeros_like(t) for t in want]
+        ws = dsa.norm_rope_workspace(128)
+        dsa.norm_rope(q, k, pos, *w, out=tuple(out))
+    s.synchronize()
+    assert torch.equal(out[0], want[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = dsa.norm_rope(q, k, pos, *w)
+        g = grads(q, k, pos, w, d[:, :8], d[:, 8:], "rms", 128, False, ws)
+    for t in (*y, *(t for t in g if t is not None)):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], want[0]) and torch.equal(y[1], want[1])
+    assert all(torch.equal(a, b) for a, b in zip(g, gw) if a is not None)
