@@ -127,6 +127,21 @@ dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, in
   return DSA_OK;
 }
 
+dsa_status_t make_queries_map(CUtensorMap* m, const void* q, int tokens, int64_t stride, int heads, int D, int heads_per,
+                              int tokens_per) {
+  auto enc = encode_fn();
+  if (!enc) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads_per, (cuuint32_t)tokens_per};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled(queries) failed: %d", (int)r);
+  return DSA_OK;
+}
+
 }  // namespace dsa
 
 namespace {

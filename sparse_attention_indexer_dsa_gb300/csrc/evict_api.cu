@@ -18,7 +18,9 @@ size_t dsa_idx_weigh_workspace_size(int total_q, int num_seqs, int max_seqlen_q,
   if (total_q < 0 || num_seqs < 1 || max_seqlen_q < 0 || n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads != 0 ||
       n_heads / n_kv_heads > 128 || (head_dim != 64 && head_dim != 128))
     return 0;
-  return DSA_DEV_STATUS_HEADER_BYTES;
+  // the parts' sums where a sequence may have more query rows than the step kernel takes
+  const bool tiles = (int64_t)max_seqlen_q * (n_heads / n_kv_heads) > kWeighStepRows;
+  return DSA_DEV_STATUS_HEADER_BYTES + (tiles ? (size_t)kWeighUnits * kWeighKeys * sizeof(float) : 0);
 }
 
 dsa_status_t dsa_idx_cache_weigh(const void* q, int64_t q_stride, const float* lse, const void* k_pages,
@@ -61,7 +63,19 @@ dsa_status_t dsa_idx_cache_weigh(const void* q, int64_t q_stride, const float* l
   p.group = n_heads / n_kv_heads;
   p.group_mul = p.group > 1 ? (uint32_t)(((uint64_t)1 << 32) / p.group + 1) : 0;
   p.hdr = reinterpret_cast<int*>(ws);
-  cudaError_t e = launch_weigh(p, head_dim, di.sm_count, reinterpret_cast<cudaStream_t>(stream));
+  p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + DSA_DEV_STATUS_HEADER_BYTES);
+  p.timeout_ns = wait_timeout_ns();
+  p.fault_inject = fault_inject_mode();
+  // Long chunks have a kernel of their own; each of the two takes the sequences that are its own, by
+  // their lengths on the device.
+  const bool tiles = total_q > 0 && (int64_t)max_seqlen_q * p.group > kWeighStepRows;
+  p.step_blocks = weigh_step_blocks(p, di.sm_count);
+  p.tile_blocks = tiles ? di.sm_count : 0;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (tiles && (s = make_queries_map(&p.tm_q, q, total_q, q_stride, n_heads, head_dim, p.group, kWeighCols / p.group)) != DSA_OK)
+    return s;
+  cudaError_t e = launch_weigh_steps(p, head_dim, p.step_blocks, st);
+  if (e == cudaSuccess && tiles) e = launch_weigh_tiles(p, head_dim, di.sm_count, st);
   if (e != cudaSuccess) return cuda_fail(e, "cache weigh launch");
   return DSA_OK;
 }

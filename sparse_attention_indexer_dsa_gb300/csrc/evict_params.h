@@ -8,6 +8,7 @@
 namespace dsa {
 
 struct WeighParams {
+  CUtensorMap tm_q;   // queries as [tokens][heads][D]: a box per tile (weigh_tiles.cu)
   PagedCacheView c;
   float* weights;     // [num_pages][n_kv][page_size]
   const void* q;
@@ -18,8 +19,19 @@ struct WeighParams {
   int num_seqs, total_q, max_seqlen_q, max_seqlen_k, n_heads, group;
   uint32_t group_mul; // 2^32 / group, rounded up (group 1: not used)
   float scale_log2;   // sm_scale * log2(e)
+  int step_blocks, tile_blocks;
   int* hdr;
+  float* part;        // [kWeighUnits][kWeighKeys] sums over parts of the queries
+  int fault_inject;
+  unsigned long long timeout_ns;
 };
+
+// Query rows of a sequence up to which its keys stream past them.
+constexpr int kWeighStepRows = 64;
+constexpr int kWeighCols = 256;    // query rows of a tile
+constexpr int kWeighKeys = 256;    // keys of a unit
+constexpr int kWeighBalance = 8 * kAttnSms;       // units that a call is divided into, about
+constexpr int kWeighUnits = 2 * kWeighBalance;    // ... and at most, where parts are joined
 
 struct SelectParams {
   const float* weights;
@@ -44,7 +56,9 @@ struct CompactParams {
   int* hdr;
 };
 
-cudaError_t launch_weigh(const WeighParams& p, int D, int sm_count, cudaStream_t stream);
+int weigh_step_blocks(const WeighParams& p, int sm_count);
+cudaError_t launch_weigh_steps(const WeighParams& p, int D, int blocks, cudaStream_t stream);
+cudaError_t launch_weigh_tiles(const WeighParams& p, int D, int sm_count, cudaStream_t stream);
 cudaError_t launch_evict_select(const SelectParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_cache_compact(const CompactParams& p, int sm_count, cudaStream_t stream);
 

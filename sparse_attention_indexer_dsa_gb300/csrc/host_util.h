@@ -22,6 +22,10 @@ dsa_status_t device_info(DevInfo* out);
 
 dsa_status_t make_pages_map(CUtensorMap* m, const void* base, int64_t groups, int rows, int D, int box_rows, bool b8);
 
+// Queries [tokens][heads][D] BF16 as boxes of `tokens_per` tokens x `heads_per` heads x 64 elements.
+dsa_status_t make_queries_map(CUtensorMap* m, const void* q, int tokens, int64_t stride, int heads, int D, int heads_per,
+                              int tokens_per);
+
 // Checks that the paged-cache operators share.  The first fills the device view.
 struct PagedCacheView;
 dsa_status_t check_cache(PagedCacheView* c, const void* k_pages, const uint8_t* k_page_scale, const void* v_pages,

@@ -14,7 +14,7 @@
 
 #include "dsa_device.cuh"
 #include "e4m3_widen.cuh"
-#include "evict_params.h"
+#include "weigh.cuh"
 
 namespace dsa {
 
@@ -25,7 +25,6 @@ using attn::widen16;
 
 constexpr int kThreads = 256;
 constexpr int kKeys = 32;     // keys of a warp's step
-constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -41,24 +40,6 @@ __device__ __forceinline__ uint4 load_once(const void* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
-}
-
-struct Doc {
-  int q0, T, S;
-};
-
-// A sequence's sizes; T = 0 (and false) when they are inconsistent.
-__device__ __forceinline__ bool doc_info(const WeighParams& p, int d, Doc* o) {
-  const int q0 = __ldg(p.cu_q + d), q1 = __ldg(p.cu_q + d + 1);
-  const int k0 = __ldg(p.cu_k + d), k1 = __ldg(p.cu_k + d + 1);
-  o->q0 = q0;
-  o->T = q1 - q0;
-  o->S = k1 - k0;
-  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.total_q && k0 >= 0 && k1 >= k0 && o->S >= o->T &&
-                  o->T <= p.max_seqlen_q && o->S <= p.max_seqlen_k &&
-                  (int64_t)o->S <= ((int64_t)p.c.max_pages << p.c.page_shift);
-  if (!ok) o->T = 0;
-  return ok;
 }
 
 // First of the groups of kKeys keys of sequence d, in a numbering with room for all of each sequence.
@@ -131,12 +112,15 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
       base = group_base(p, d);
       next_base = group_base(p, d + 1);
       if (!doc_info(p, d, &doc)) code = DSA_DEV_ERR_INVALID_ARG;
-      n_rows = doc.T * p.group;
+      n_rows = by_steps(p, doc.T) ? doc.T * p.group : 0;
       P0 = doc.S - doc.T;
       if (n_rows > 0 && n_rows <= 8) load_q(0);
     }
     const int key0 = (gu - base) * kKeys;
-    if (n_rows == 0 || key0 >= doc.S) continue;
+    if (n_rows == 0 || key0 >= doc.S) {   // to the next sequence
+      u += next_base - 1 - gu;
+      continue;
+    }
     const int64_t mine = key0 + lane < doc.S ? cache_row(p.c, d, key0 + lane, h) : -1;   // this lane's key
     if (key0 + lane < doc.S && mine < 0) code = DSA_DEV_ERR_INVALID_ARG;
     const uint32_t row32 = mine < 0 ? ~0u : (uint32_t)mine;
@@ -227,25 +211,27 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     if (r != ~0u) p.weights[r] = key0 + mykey >= P0 ? got : p.weights[r] + got;
   }
   code = __syncthreads_or(code != 0) ? DSA_DEV_ERR_INVALID_ARG : 0;
-  if (tid == 0) put_block_status(p.hdr, code);
+  if (tid == 0) put_status(p, blockIdx.x, code);
 }
 
 }  // namespace weigh
 
-cudaError_t launch_weigh(const WeighParams& p, int D, int sm_count, cudaStream_t stream) {
-  using namespace weigh;
+int weigh_step_blocks(const WeighParams& p, int sm_count) {
   // no more blocks than there can be groups of keys
-  const int64_t groups = ((int64_t)p.max_seqlen_k / kKeys + 1) * p.num_seqs * p.c.n_kv;
-  int64_t blocks = (groups + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks > 2 * sm_count) blocks = 2 * sm_count;
-  if (blocks > DSA_DEV_STATUS_MAX_BLOCKS) blocks = DSA_DEV_STATUS_MAX_BLOCKS;
+  const int64_t groups = ((int64_t)p.max_seqlen_k / weigh::kKeys + 1) * p.num_seqs * p.c.n_kv;
+  const int64_t blocks = (groups + weigh::kThreads / 32 - 1) / (weigh::kThreads / 32);
+  return (int)(blocks < 2 * sm_count ? blocks : 2 * sm_count);
+}
+
+cudaError_t launch_weigh_steps(const WeighParams& p, int D, int blocks, cudaStream_t stream) {
+  using namespace weigh;
   const bool q8 = p.c.fmt != 0;
   if (D == 128) {
-    if (q8) weigh_kernel<128, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-    else weigh_kernel<128, false><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    if (q8) weigh_kernel<128, true><<<blocks, kThreads, 0, stream>>>(p);
+    else weigh_kernel<128, false><<<blocks, kThreads, 0, stream>>>(p);
   } else {
-    if (q8) weigh_kernel<64, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-    else weigh_kernel<64, false><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    if (q8) weigh_kernel<64, true><<<blocks, kThreads, 0, stream>>>(p);
+    else weigh_kernel<64, false><<<blocks, kThreads, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }

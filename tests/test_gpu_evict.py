@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import sparse_attention_indexer_dsa_gb300 as dsa
+from sparse_attention_indexer_dsa_gb300 import _abi
 from tests import evict_ref as E
 from tests.gpu_util import bf16_dev, dev, host
 from tests.paged_ref import Batch, quantise, values
@@ -85,6 +86,52 @@ def test_weigh_groups(group, T):
     rng = np.random.default_rng([group, T])
     b = Batch(rng, [(T, T + 77), (1, 300)], 1, 64, 32, "bf16", values_too=False)
     check_weigh(b, rng, group)
+
+
+@pytest.mark.parametrize("prec,D,page", [("bf16", 128, 64), ("mxfp8", 128, 16), ("fp8", 64, 8)])
+@pytest.mark.parametrize("kv,group,lens", [(1, 8, [(640, 700), (0, 5), (90, 95)]), (2, 5, [(1, 9), (900, 900)]),
+                                           (1, 128, [(40, 3000)])])
+def test_weigh_divided(kv, group, lens, prec, D, page):
+    """Few units of keys with many query rows: their tokens are divided and the parts joined."""
+    rng = np.random.default_rng([kv, group, D])
+    check_weigh(Batch(rng, lens, kv, D, page, prec, values_too=False, pad_q=3), rng, group)
+
+
+def test_weigh_other_rows_of_a_tile():
+    """A tile's last rows may be another sequence's tokens, or padding, that hold anything."""
+    rng = np.random.default_rng(37)
+    b = Batch(rng, [(70, 150), (20, 20), (65, 65)], 1, 64, 16, "bf16", values_too=False, pad_q=40)
+    q, qd = queries(rng, b.total_q, 4, 64)
+    lse = true_lse(b, q, 4, 0.1)
+    lse[155:] = np.nan
+    qd[155:] = float("nan")
+    qd[70:90] = float("nan")
+    w = E.random_weights(rng, b)
+    got = weigh(b, b.cache(dsa), dev(w), qd, dev(lse), 0.1)
+    want, tol = E.weigh(b, q, lse.astype(np.float64), w, 4, 0.1)
+    page, slot = E.rows_of(b, 1)
+    mine = np.ones(w.shape, bool)
+    mine[page, :, slot] = False
+    assert host(got)[page, :, slot].size and np.isnan(host(got)[page, :, slot]).all()
+    close(got[torch.from_numpy(mine).cuda()], want[mine], tol[mine])
+
+
+def test_weigh_a_wait_that_runs_out():
+    rng = np.random.default_rng(38)
+    b = Batch(rng, [(70, 150)], 1, 128, 16, "mxfp8", values_too=False)
+    q, qd = queries(rng, b.total_q, 4, 128)
+    lse = dev(true_lse(b, q, 4, 0.1))
+    w = E.random_weights(rng, b)
+    lib = _abi.load()
+    try:
+        lib.dsa_idx_test_set_timeout_ns(50_000_000)
+        lib.dsa_idx_test_set_fault_inject(1)
+        weigh(b, b.cache(dsa), dev(w), qd, lse, 0.1, status=_abi.DSA_ERR_TIMEOUT)
+    finally:
+        lib.dsa_idx_test_set_fault_inject(0)
+        lib.dsa_idx_test_set_timeout_ns(2_000_000_000)
+    got = weigh(b, b.cache(dsa), dev(w), qd, lse, 0.1)
+    close(got, *E.weigh(b, q, host(lse).astype(np.float64), w, 4, 0.1))
 
 
 def test_weigh_far_scales():
