@@ -520,7 +520,8 @@ size_t dsa_idx_norm_rope_workspace_size(int head_dim);
 
 /* Gradients of dsa_idx_norm_rope: of its inputs (dq, dk, in_dtype, strides of
  * their own) and of its weights and biases (FP32 [head_dim], summed over tokens
- * and heads; NULL: not wanted), from the gradients dq_out, dk_out of its outputs
+ * and heads; NULL: not wanted, biases of DSA_NORM_RMS always NULL), from the
+ * gradients dq_out, dk_out of its outputs
  * (grad_dtype) and the forward's inputs; no other statistics are kept.  Weight
  * gradients of a call without weights are those of weights of one.  Outputs
  * share no memory with inputs.  ws as for the cache's operators.  The same

@@ -42,6 +42,7 @@ struct SelectParams {
   int budget, sinks, recent, shared;
   int32_t* kept;       // [num_seqs][shared ? 1 : n_kv][budget]
   int32_t* kept_len;   // [num_seqs]
+  int cached;          // rows of a block whose bits its shared memory holds
   int* hdr;
 };
 

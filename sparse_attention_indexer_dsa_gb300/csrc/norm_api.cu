@@ -69,8 +69,6 @@ dsa_status_t fill(NormRopeParams* p, const void* q, int64_t q_stride, const void
   p->heads[0] = n_heads;
   p->heads[1] = n_kv_heads;
   p->tokens = total_tokens;
-  const int rows = n_heads + n_kv_heads;
-  p->row_mul = rows > 1 ? (uint32_t)(((uint64_t)1 << 32) / rows + 1) : 0;
   p->eps = eps;
   p->layer = norm == DSA_NORM_LAYER;
   p->in_bf16 = in_dtype == DSA_DTYPE_BF16;
@@ -97,8 +95,7 @@ dsa_status_t dsa_idx_norm_rope(const void* q, int64_t q_stride, const void* k, i
   if (s != DSA_OK) return s;
   DevInfo di;
   if ((s = device_info(&di)) != DSA_OK) return s;
-  p.tile = norm_tile(n_heads + n_kv_heads, head_dim, 4);
-  cudaError_t e = launch_norm_rope(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_norm_rope(p, head_dim, di.sm_count, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
   return DSA_OK;
 }
@@ -128,10 +125,10 @@ dsa_status_t dsa_idx_norm_rope_backward(const void* dq_out, int64_t dq_out_strid
   if ((s = check_stride(&dq_out_stride, n_heads, head_dim, elem_bytes(grad_dtype), "dq_out")) != DSA_OK) return s;
   if (n_kv_heads > 0 && (s = check_stride(&dk_out_stride, n_kv_heads, head_dim, elem_bytes(grad_dtype), "dk_out")) != DSA_OK)
     return s;
+  if (norm == DSA_NORM_RMS && (dq_bias || dk_bias)) return fail(DSA_ERR_INVALID_ARG, "biases of an RMS norm have no gradient here");
   if ((s = check_ws(ws, ws_bytes, dsa_idx_norm_rope_workspace_size(head_dim))) != DSA_OK) return s;
   DevInfo di;
   if ((s = device_info(&di)) != DSA_OK) return s;
-  p.f.tile = norm_tile(n_heads + n_kv_heads, head_dim, 4);
   p.dy[0] = dq_out;
   p.dy[1] = dk_out;
   p.dy_stride[0] = dq_out_stride;

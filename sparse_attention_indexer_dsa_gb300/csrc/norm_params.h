@@ -25,8 +25,8 @@ struct NormRopeParams {
   const void* b[2];          // null: zeros
   const int32_t* pos;
   int heads[2];
-  int tokens, tile;          // tile: tokens of a block's tile
-  uint32_t row_mul;          // 2^32 / rows of a token, rounded up (rows of a tile are far below 2^16)
+  int tokens;
+  int share, parts;          // rows of a token that a warp takes, such shares of a token
   float eps;
   int layer, in_bf16, out_bf16, w_bf16;
 };
@@ -43,17 +43,9 @@ struct NormRopeBackParams {
 };
 
 constexpr int kNormThreads = 256;
-constexpr int kNormTileMax = 32;        // tokens of a tile, at most
 constexpr int kNormBackBlocks = 1024;   // blocks of the backward kernel, at most
 
-// Tokens of a tile: about `steps` rows to a thread's group of lanes.
-inline int norm_tile(int rows_of_token, int D, int steps) {
-  const int rows = kNormThreads / (D / 8) * steps;
-  const int t = rows / rows_of_token;
-  return t < 1 ? 1 : (t > kNormTileMax ? kNormTileMax : t);
-}
-
-cudaError_t launch_norm_rope(const NormRopeParams& p, int D, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeParams& p, int D, int sm_count, cudaStream_t stream);
 cudaError_t launch_norm_rope_back(const NormRopeBackParams& p, int D, int sm_count, cudaStream_t stream);
 
 }  // namespace dsa

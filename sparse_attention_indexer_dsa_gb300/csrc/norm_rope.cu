@@ -9,10 +9,10 @@
 //
 // A row of D elements is handled by D / 8 lanes.  Each holds two groups of four
 // elements, chosen so that both elements of a pair are its own: the rotation
-// needs no exchange between lanes and half as many factors.  The rows of a
-// tile of tokens (one token of many heads, several of few) are spread over the
-// block; a token's cos and sin are formed once, in shared memory, while the
-// rows are on their way.
+// needs no exchange between lanes and half as many factors.  A warp takes some of
+// a token's rows (all of them where there are tokens enough) and forms the
+// token's cos and sin itself, each lane those of its pairs, while the first rows
+// are on their way; warps share nothing.
 //
 // An angle is pos * freq in turns, modulo one: 64-bit fixed point, so far
 // positions lose nothing (in FP32 a position of 2^20 would be off by 0.06 rad).
@@ -109,14 +109,11 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // x -> n; returns 1 / std.
-template <int D>
-__device__ __forceinline__ float normalise(float (&x)[8], bool layer, float eps) {
+template <int D, bool LAYER>
+__device__ __forceinline__ float normalise(float (&x)[8], float eps) {
   constexpr int LPR = D / 8;
-  if (layer) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s += x[e];
-    const float mean = row_sum<LPR>(s) * (1.f / D);
+  if (LAYER) {
+    const float mean = row_sum<LPR>(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]))) * (1.f / D);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] -= mean;
   }
@@ -148,265 +145,288 @@ __device__ __forceinline__ void turn(float (&y)[8], const float (&cs)[4], const 
   }
 }
 
-// cos and sin of the tile's tokens [tile][dim / 2], by the block's threads.
-__device__ __forceinline__ void fill_angles(const NormRopeParams& p, int t0, int n, float2* tab) {
-  const int half = p.rope.dim / 2;
-  for (int i = threadIdx.x; i < n * half; i += kNormThreads) {
-    const int t = i / half, f = i - t * half;
-    const uint64_t turns = (uint64_t)(int64_t)__ldg(p.pos + t0 + t) * p.rope.freq[f];
-    // the upper 32 bits as a signed part of a turn; sincospif takes half turns
-    const float x = (float)(int32_t)(uint32_t)(turns >> 32) * 0x1p-31f;
-    float sv, cv;
-    sincospif(x, &sv, &cv);
-    tab[i] = make_float2(cv, sv);
-  }
-}
-
-// A lane's factors of token t of the tile.
+// cos and sin of a lane's pairs at a position.
 template <int D>
-__device__ __forceinline__ void load_angles(const float2* tab, int half, int t, const Lane<D>& at, float (&cs)[4],
-                                            float (&sn)[4]) {
+__device__ __forceinline__ void angles(const RopeTable& r, int pos, const Lane<D>& at, float (&cs)[4], float (&sn)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float2 v = at.angle[e] >= 0 ? tab[t * half + at.angle[e]] : make_float2(1.f, 0.f);
-    cs[e] = v.x;
-    sn[e] = v.y;
+    cs[e] = 1.f;
+    sn[e] = 0.f;
+    if (at.angle[e] >= 0) {
+      const uint64_t turns = (uint64_t)(int64_t)pos * r.freq[at.angle[e]];
+      // the upper 32 bits as a signed part of a turn; sincospif takes half turns
+      sincospif((float)(int32_t)(uint32_t)(turns >> 32) * 0x1p-31f, &sn[e], &cs[e]);
+    }
   }
 }
 
-// Row r of a tile: token, head, and whether it is a key's.
-__device__ __forceinline__ void row_at(const NormRopeParams& p, int r, int* tok, int* head, int* kind) {
-  const int rows = p.heads[0] + p.heads[1];
-  *tok = rows == 1 ? r : (int)__umulhi((uint32_t)r, p.row_mul);   // r / rows
-  const int h = r - *tok * rows;
-  *kind = h >= p.heads[0];
-  *head = *kind ? h - p.heads[0] : h;
-}
+// A warp's share of a token: rows [lo, hi) of queries (kind 0) or keys (kind 1).
+struct Share {
+  int lo, hi;
+  __device__ __forceinline__ Share(const NormRopeParams& p, int part, int kind) {
+    const int rows = p.heads[0] + p.heads[1], a = part * p.share, b = min(a + p.share, rows);
+    lo = kind ? max(a - p.heads[0], 0) : a;
+    hi = kind ? b - p.heads[0] : min(b, p.heads[0]);
+  }
+};
 
 constexpr int kBatch = 4;   // rows of a lane that are requested together
 
-template <int D, bool IN, bool OUT>
+template <int D, bool IN, bool OUT, bool LAYER>
 __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int LPR = D / 8, RPS = kNormThreads / LPR;
-  extern __shared__ float2 tab[];
-  const int half = p.rope.dim / 2;
-  const int t0 = blockIdx.x * p.tile, n = min(p.tile, p.tokens - t0);
-  const int rows = n * (p.heads[0] + p.heads[1]);
-  const Lane<D> at(p.rope, threadIdx.x % LPR);
-  const int sub = threadIdx.x / LPR;
-  float cs[4], sn[4], w[8], b[8];
-  int cur_tok = -1, cur_kind = -1;
-  bool first = true;
-  for (int r0 = 0; r0 < rows; r0 += RPS * kBatch) {
-    Raw<IN> raw[kBatch][2];
-    int tok[kBatch], head[kBatch], kind[kBatch];
+  constexpr int LPR = D / 8, RPS = 32 / LPR;
+  const int64_t task = (int64_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
+  if (task >= (int64_t)p.tokens * p.parts) return;
+  const int tok = (int)(task / p.parts), part = (int)(task - (int64_t)tok * p.parts);
+  const int lane = threadIdx.x & 31, sub = lane / LPR;
+  const Lane<D> at(p.rope, lane % LPR);
+  float cs[4], sn[4];
+  bool turned = false;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + i * RPS + sub;
-      row_at(p, min(r, rows - 1), &tok[i], &head[i], &kind[i]);   // (all lanes take part in the sums)
-      const int64_t e = (int64_t)(t0 + tok[i]) * p.x_stride[kind[i]] + head[i] * D;
-      load4<IN>(raw[i][0], p.x[kind[i]], e + at.a);
-      load4<IN>(raw[i][1], p.x[kind[i]], e + at.b);
-    }
-    if (first) {
-      if (half > 0) fill_angles(p, t0, n, tab);
-      __syncthreads();
-      first = false;
-    }
+  for (int kind = 0; kind < 2; ++kind) {
+    const Share sh(p, part, kind);
+    if (sh.lo >= sh.hi) continue;
+    float w[8], b[8];
+    load_w<D>(p.w[kind], p.w_bf16, at, 1.f, w);
+    if (LAYER || p.b[kind]) load_w<D>(p.b[kind], p.w_bf16, at, 0.f, b);
+    const bool shift = p.b[kind] != nullptr;
+    const int64_t x0 = (int64_t)tok * p.x_stride[kind], y0 = (int64_t)tok * p.y_stride[kind];
+    for (int h0 = sh.lo + sub; h0 - sub < sh.hi; h0 += kBatch * RPS) {
+      Raw<IN> raw[kBatch][2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + i * RPS + sub;
-      if (r0 + i * RPS >= rows) break;
-      if (tok[i] != cur_tok) {
-        cur_tok = tok[i];
-        load_angles<D>(tab, half, cur_tok, at, cs, sn);
+      for (int i = 0; i < kBatch; ++i) {
+        const int64_t e = x0 + min(h0 + i * RPS, sh.hi - 1) * D;   // (all lanes take part in the sums)
+        load4<IN>(raw[i][0], p.x[kind], e + at.a);
+        load4<IN>(raw[i][1], p.x[kind], e + at.b);
       }
-      if (kind[i] != cur_kind) {
-        cur_kind = kind[i];
-        load_w<D>(p.w[cur_kind], p.w_bf16, at, 1.f, w);
-        load_w<D>(p.b[cur_kind], p.w_bf16, at, 0.f, b);
+      if (!turned) {
+        angles<D>(p.rope, p.rope.dim > 0 ? __ldg(p.pos + tok) : 0, at, cs, sn);
+        turned = true;
       }
-      float x[8];
-      widen4<IN>(raw[i][0], x);
-      widen4<IN>(raw[i][1], x + 4);
-      normalise<D>(x, p.layer, p.eps);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], w[e], b[e]);
-      turn(x, cs, sn, p.rope.interleaved);
-      if (r < rows) {
-        const int64_t o = (int64_t)(t0 + tok[i]) * p.y_stride[kind[i]] + head[i] * D;
-        store4<OUT>(p.y[kind[i]], o + at.a, x);
-        store4<OUT>(p.y[kind[i]], o + at.b, x + 4);
+      for (int i = 0; i < kBatch; ++i) {
+        if (h0 - sub + i * RPS >= sh.hi) break;
+        float x[8];
+        widen4<IN>(raw[i][0], x);
+        widen4<IN>(raw[i][1], x + 4);
+        normalise<D, LAYER>(x, p.eps);
+        if (shift) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], w[e], b[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= w[e];
+        }
+        turn(x, cs, sn, p.rope.interleaved);
+        const int h = h0 + i * RPS;
+        if (h < sh.hi) {
+          store4<OUT>(p.y[kind], y0 + h * D + at.a, x);
+          store4<OUT>(p.y[kind], y0 + h * D + at.b, x + 4);
+        }
       }
     }
   }
 }
 
-// Blocks take tiles in turn and keep the gradients of the weights in registers, each lane those of its
+// Warps take shares in turn and keep the gradients of the weights in registers, each lane those of its
 // own eight columns; what a block has gathered goes to the workspace, and a second kernel adds the
 // blocks' sums in their order, so that the same inputs give the same bits.
 constexpr int kBackBatch = 2;
 
-template <int D, bool IN, bool GRAD>
+template <int D, bool IN, bool GRAD, bool LAYER>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_back_kernel(const __grid_constant__ NormRopeBackParams q) {
-  constexpr int LPR = D / 8, RPS = kNormThreads / LPR;
-  extern __shared__ float2 tab[];
+  constexpr int LPR = D / 8, RPS = 32 / LPR, kRows = kNormThreads / LPR;
+  __shared__ float red[kRows * D];
   const NormRopeParams& p = q.f;
-  const int half = p.rope.dim / 2;
-  const Lane<D> at(p.rope, threadIdx.x % LPR);
-  const int sub = threadIdx.x / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR;
+  const Lane<D> at(p.rope, lane % LPR);
   float dw[2][8], db[2][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = db[0][e] = db[1][e] = 0.f;
-  const int tiles = (p.tokens + p.tile - 1) / p.tile;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int t0 = tile * p.tile, n = min(p.tile, p.tokens - t0);
-    __syncthreads();   // (the last tile's angles have been read)
-    if (half > 0) fill_angles(p, t0, n, tab);
-    __syncthreads();
+  const int64_t tasks = (int64_t)p.tokens * p.parts, warps = (int64_t)gridDim.x * (kNormThreads / 32);
+  for (int64_t task = (int64_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5); task < tasks; task += warps) {
+    const int tok = (int)(task / p.parts), part = (int)(task - (int64_t)tok * p.parts);
+    float cs[4], sn[4];
+    bool turned = false;
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
-      const int heads = p.heads[kind], rows = n * heads;
-      if (rows == 0) continue;
+      const Share sh(p, part, kind);
+      if (sh.lo >= sh.hi) continue;
       float w[8];
       load_w<D>(p.w[kind], p.w_bf16, at, 1.f, w);
-      for (int r0 = 0; r0 < rows; r0 += RPS * kBackBatch) {
-        Raw<IN> raw[kBackBatch][2];
-        Raw<GRAD> grad[kBackBatch][2];
-        int tok[kBackBatch], head[kBackBatch];
+      const int64_t x0 = (int64_t)tok * p.x_stride[kind], g0 = (int64_t)tok * q.dy_stride[kind];
+      const int64_t y0 = (int64_t)tok * p.y_stride[kind];
+      Raw<IN> raw[kBackBatch][2];
+      Raw<GRAD> grad[kBackBatch][2];
+      auto load = [&](int h0) {
 #pragma unroll
         for (int i = 0; i < kBackBatch; ++i) {
-          const int r = min(r0 + i * RPS + sub, rows - 1);
-          tok[i] = p.tile == 1 ? 0 : r / heads;
-          head[i] = r - tok[i] * heads;
-          const int64_t e = (int64_t)(t0 + tok[i]) * p.x_stride[kind] + head[i] * D;
-          const int64_t g = (int64_t)(t0 + tok[i]) * q.dy_stride[kind] + head[i] * D;
-          load4<IN>(raw[i][0], p.x[kind], e + at.a);
-          load4<IN>(raw[i][1], p.x[kind], e + at.b);
-          load4<GRAD>(grad[i][0], q.dy[kind], g + at.a);
-          load4<GRAD>(grad[i][1], q.dy[kind], g + at.b);
+          const int h = min(h0 + i * RPS, sh.hi - 1) * D;   // (all lanes take part in the sums)
+          load4<IN>(raw[i][0], p.x[kind], x0 + h + at.a);
+          load4<IN>(raw[i][1], p.x[kind], x0 + h + at.b);
+          load4<GRAD>(grad[i][0], q.dy[kind], g0 + h + at.a);
+          load4<GRAD>(grad[i][1], q.dy[kind], g0 + h + at.b);
         }
+      };
+      load(sh.lo + sub);
+      if (!turned) {
+        angles<D>(p.rope, p.rope.dim > 0 ? __ldg(p.pos + tok) : 0, at, cs, sn);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sn[e] = -sn[e];
+        turned = true;
+      }
+      for (int h0 = sh.lo + sub; h0 - sub < sh.hi; h0 += kBackBatch * RPS) {
+        float x[kBackBatch][8], g[kBackBatch][8];
 #pragma unroll
         for (int i = 0; i < kBackBatch; ++i) {
-          if (r0 + i * RPS >= rows) break;
-          const bool live = r0 + i * RPS + sub < rows;
-          float cs[4], sn[4], x[8], g[8];
-          load_angles<D>(tab, half, tok[i], at, cs, sn);
+          widen4<IN>(raw[i][0], x[i]);
+          widen4<IN>(raw[i][1], x[i] + 4);
+          widen4<GRAD>(grad[i][0], g[i]);
+          widen4<GRAD>(grad[i][1], g[i] + 4);
+        }
+        load(h0 + kBackBatch * RPS);   // (the next ones are on their way meanwhile; behind the last: the last once more)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sn[e] = -sn[e];
-          widen4<IN>(raw[i][0], x);
-          widen4<IN>(raw[i][1], x + 4);
-          widen4<GRAD>(grad[i][0], g);
-          widen4<GRAD>(grad[i][1], g + 4);
-          const float inv = normalise<D>(x, p.layer, p.eps);
-          turn(g, cs, sn, p.rope.interleaved);
+        for (int i = 0; i < kBackBatch; ++i) {
+          if (h0 - sub + i * RPS >= sh.hi) break;
+          const int h = h0 + i * RPS;
+          const bool live = h < sh.hi;
+          const float inv = normalise<D, LAYER>(x[i], p.eps);
+          turn(g[i], cs, sn, p.rope.interleaved);
           float dot = 0.f, sum = 0.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if (live) {
-              dw[kind][e] = fmaf(g[e], x[e], dw[kind][e]);
-              db[kind][e] += g[e];
+              dw[kind][e] = fmaf(g[i][e], x[i][e], dw[kind][e]);
+              if (LAYER) db[kind][e] += g[i][e];
             }
-            g[e] *= w[e];
-            dot = fmaf(g[e], x[e], dot);
-            sum += g[e];
+            g[i][e] *= w[e];
+            dot = fmaf(g[i][e], x[i][e], dot);
+            if (LAYER) sum += g[i][e];
           }
           dot = row_sum<LPR>(dot) * (1.f / D);
-          sum = p.layer ? row_sum<LPR>(sum) * (1.f / D) : 0.f;
+          if (LAYER) sum = row_sum<LPR>(sum) * (1.f / D);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = (g[e] - fmaf(x[e], dot, sum)) * inv;
+          for (int e = 0; e < 8; ++e) g[i][e] = (g[i][e] - (LAYER ? fmaf(x[i][e], dot, sum) : x[i][e] * dot)) * inv;
           if (live) {
-            const int64_t o = (int64_t)(t0 + tok[i]) * p.y_stride[kind] + head[i] * D;
-            store4<IN>(p.y[kind], o + at.a, g);
-            store4<IN>(p.y[kind], o + at.b, g + 4);
+            store4<IN>(p.y[kind], y0 + h * D + at.a, g[i]);
+            store4<IN>(p.y[kind], y0 + h * D + at.b, g[i] + 4);
           }
         }
       }
     }
   }
   // rows of lanes -> one row of columns, in their order
-  float* const red = reinterpret_cast<float*>(tab);
+  const int row = threadIdx.x / LPR;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < (LAYER ? 4 : 2); ++j) {
     const float(&v)[8] = j < 2 ? dw[j & 1] : db[j & 1];
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[sub * D + (e < 4 ? at.a : at.b) + (e & 3)] = v[e];
+    for (int e = 0; e < 8; ++e) red[row * D + (e < 4 ? at.a : at.b) + (e & 3)] = v[e];
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += kNormThreads) {
       float s = 0.f;
-      for (int r = 0; r < RPS; ++r) s += red[r * D + c];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) s += red[r * D + c];
       q.part[((int64_t)blockIdx.x * 4 + j) * D + c] = s;
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) q.hdr[0] = 0;
 }
 
-// Sums of the blocks' parts: a block to one of the four rows, 8 warps x 32 columns at a time.
-__global__ void __launch_bounds__(256) norm_rope_join_kernel(const __grid_constant__ NormRopeBackParams q, int D, int blocks) {
-  __shared__ float red[8][32];
-  const int j = blockIdx.x, c = blockIdx.y * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+// Sums of the blocks' parts: a block to 32 columns of one of the four rows.  Sums that the backward
+// kernel does not form (db of an rms norm) are not asked for.
+constexpr int kJoinWarps = 32;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) norm_rope_join_kernel(const __grid_constant__ NormRopeBackParams q, int D, int blocks) {
+  __shared__ float red[kJoinWarps][32];
+  const int j = blockIdx.x, lane = threadIdx.x & 31, c = blockIdx.y * 32 + lane, w = threadIdx.x >> 5;
   float* const out = j < 2 ? q.dw[j & 1] : q.db[j & 1];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && blocks == 0) q.hdr[0] = 0;
   if (!out) return;
   float s = 0.f;
-  for (int i = w; i < blocks; i += 8) s += q.part[((int64_t)i * 4 + j) * D + c];
-  red[w][threadIdx.x & 31] = s;
+  for (int i = w; i < blocks; i += kJoinWarps) s += q.part[((int64_t)i * 4 + j) * D + c];
+  red[w][lane] = s;
   __syncthreads();
   if (w == 0) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
+    for (int i = 0; i < kJoinWarps; ++i) t += red[i][lane];
     out[c] = t;
   }
 }
 
-template <int D>
-cudaError_t run(const NormRopeParams& p, cudaStream_t stream) {
-  const int blocks = (p.tokens + p.tile - 1) / p.tile;
-  const size_t smem = (size_t)p.tile * (p.rope.dim / 2) * sizeof(float2);
-  if (p.in_bf16) {
-    if (p.out_bf16) norm_rope_kernel<D, true, true><<<blocks, kNormThreads, smem, stream>>>(p);
-    else norm_rope_kernel<D, true, false><<<blocks, kNormThreads, smem, stream>>>(p);
-  } else {
-    if (p.out_bf16) norm_rope_kernel<D, false, true><<<blocks, kNormThreads, smem, stream>>>(p);
-    else norm_rope_kernel<D, false, false><<<blocks, kNormThreads, smem, stream>>>(p);
-  }
-  return cudaGetLastError();
+// Rows of a warp's share: a whole token where the tokens alone fill the GPU's warps, else fewer, down to
+// one batch of the loop.
+void divide(NormRopeParams* p, int D, int batch, int warps) {
+  const int rows = p->heads[0] + p->heads[1], least = 32 / (D / 8) * batch;
+  int parts = p->tokens > 0 ? (warps + p->tokens - 1) / p->tokens : 1;
+  if (parts > (rows + least - 1) / least) parts = (rows + least - 1) / least;
+  if (parts < 1) parts = 1;
+  p->share = ((rows + parts - 1) / parts + least - 1) / least * least;
+  p->parts = (rows + p->share - 1) / p->share;
 }
 
-template <int D>
-cudaError_t run_back(const NormRopeBackParams& q, int sm_count, cudaStream_t stream) {
-  const NormRopeParams& p = q.f;
-  int blocks = (p.tokens + p.tile - 1) / p.tile;
-  const int cap = 2 * sm_count < kNormBackBlocks ? 2 * sm_count : kNormBackBlocks;
-  if (blocks > cap) blocks = cap;
-  if (blocks > 0) {
-    size_t smem = (size_t)p.tile * (p.rope.dim / 2) * sizeof(float2);
-    const size_t red = (size_t)(kNormThreads / (D / 8)) * D * sizeof(float);
-    if (red > smem) smem = red;
-    if (p.in_bf16) {
-      if (q.dy_bf16) norm_rope_back_kernel<D, true, true><<<blocks, kNormThreads, smem, stream>>>(q);
-      else norm_rope_back_kernel<D, true, false><<<blocks, kNormThreads, smem, stream>>>(q);
-    } else {
-      if (q.dy_bf16) norm_rope_back_kernel<D, false, true><<<blocks, kNormThreads, smem, stream>>>(q);
-      else norm_rope_back_kernel<D, false, false><<<blocks, kNormThreads, smem, stream>>>(q);
-    }
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+template <int D, bool LAYER>
+void run(const NormRopeParams& p, cudaStream_t stream) {
+  const int64_t tasks = (int64_t)p.tokens * p.parts;
+  const unsigned blocks = (unsigned)((tasks + kNormThreads / 32 - 1) / (kNormThreads / 32));
+  if (p.in_bf16) {
+    if (p.out_bf16) norm_rope_kernel<D, true, true, LAYER><<<blocks, kNormThreads, 0, stream>>>(p);
+    else norm_rope_kernel<D, true, false, LAYER><<<blocks, kNormThreads, 0, stream>>>(p);
+  } else {
+    if (p.out_bf16) norm_rope_kernel<D, false, true, LAYER><<<blocks, kNormThreads, 0, stream>>>(p);
+    else norm_rope_kernel<D, false, false, LAYER><<<blocks, kNormThreads, 0, stream>>>(p);
   }
-  norm_rope_join_kernel<<<dim3(4, D / 32), 256, 0, stream>>>(q, D, blocks);
-  return cudaGetLastError();
+}
+
+template <int D, bool LAYER>
+void run_back(const NormRopeBackParams& q, int blocks, cudaStream_t stream) {
+  if (q.f.in_bf16) {
+    if (q.dy_bf16) norm_rope_back_kernel<D, true, true, LAYER><<<blocks, kNormThreads, 0, stream>>>(q);
+    else norm_rope_back_kernel<D, true, false, LAYER><<<blocks, kNormThreads, 0, stream>>>(q);
+  } else {
+    if (q.dy_bf16) norm_rope_back_kernel<D, false, true, LAYER><<<blocks, kNormThreads, 0, stream>>>(q);
+    else norm_rope_back_kernel<D, false, false, LAYER><<<blocks, kNormThreads, 0, stream>>>(q);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const NormRopeParams& p, int D, cudaStream_t stream) {
-  if (p.tokens == 0) return cudaSuccess;
-  return D == 128 ? run<128>(p, stream) : run<64>(p, stream);
+cudaError_t launch_norm_rope(const NormRopeParams& call, int D, int sm_count, cudaStream_t stream) {
+  if (call.tokens == 0) return cudaSuccess;
+  NormRopeParams p = call;
+  divide(&p, D, kBatch, 24 * sm_count);
+  if (D == 128) {
+    if (p.layer) run<128, true>(p, stream);
+    else run<128, false>(p, stream);
+  } else {
+    if (p.layer) run<64, true>(p, stream);
+    else run<64, false>(p, stream);
+  }
+  return cudaGetLastError();
 }
 
-cudaError_t launch_norm_rope_back(const NormRopeBackParams& p, int D, int sm_count, cudaStream_t stream) {
-  return D == 128 ? run_back<128>(p, sm_count, stream) : run_back<64>(p, sm_count, stream);
+cudaError_t launch_norm_rope_back(const NormRopeBackParams& call, int D, int sm_count, cudaStream_t stream) {
+  NormRopeBackParams q = call;
+  int cap = 2 * sm_count < kNormBackBlocks ? 2 * sm_count : kNormBackBlocks;
+  divide(&q.f, D, kBackBatch, 2 * cap * (kNormThreads / 32));   // (two shares to a warp: they differ in length)
+  const int64_t tasks = (int64_t)q.f.tokens * q.f.parts;
+  int blocks = cap;
+  if ((tasks + kNormThreads / 32 - 1) / (kNormThreads / 32) < cap) blocks = (int)((tasks + kNormThreads / 32 - 1) / (kNormThreads / 32));
+  if (blocks > 0) {
+    if (D == 128) {
+      if (q.f.layer) run_back<128, true>(q, blocks, stream);
+      else run_back<128, false>(q, blocks, stream);
+    } else {
+      if (q.f.layer) run_back<64, true>(q, blocks, stream);
+      else run_back<64, false>(q, blocks, stream);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  norm_rope_join_kernel<<<dim3(4, D / 32), 32 * kJoinWarps, 0, stream>>>(q, D, blocks);
+  return cudaGetLastError();
 }
 
 }  // namespace dsa

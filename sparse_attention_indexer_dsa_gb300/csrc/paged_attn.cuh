@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
                 for (int q = 0; q < 4; ++q) w4[i][q] = 0;
               }
               top = max(top, e8[i]);
-              widen16<false>(w4[i], e8[i], o);
+              widen<false>(w4[i], e8[i], o);
               st_shared_v4(dst + at0 + (i0 + i) * RPP * 128, o[0], o[1], o[2], o[3]);
               st_shared_v4(dst + at1 + (i0 + i) * RPP * 128, o[4], o[5], o[6], o[7]);
             }
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(Roles<Q8, MODE, NARROW>::kThreads, 1)
               if (e <= 134u || r >= valid) continue;
               uint32_t w4[4], o[8];
               ld_shared_v4(raw + r * D, w4);
-              widen16<true>(w4, e, o);
+              widen<true>(w4, e, o);
               st_shared_v4(dst + at0 + r * 128, o[0], o[1], o[2], o[3]);
               st_shared_v4(dst + at1 + r * 128, o[4], o[5], o[6], o[7]);
             }

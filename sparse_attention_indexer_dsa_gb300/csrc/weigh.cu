@@ -4,16 +4,26 @@
 // the new tokens themselves begin at 0.  With the lse of the attention the
 // summands are its softmax weights, so a token adds its number of heads in all.
 //
-// A warp takes 32 keys of one head at a time and forms their products with 8
-// query rows (token, head of the group) by mma.sync m16n8k16.  The operands go
-// from memory to registers as they lie: the sum over the head's elements has no
-// order, so a lane's 16 contiguous bytes of a row stand for the fragment's
-// elements, of queries and keys alike, and nothing passes through shared
-// memory.  8-bit rows are widened on the way; E4M3 x 2^e is exact in BF16.
+// A warp walks along the keys of one head, a step of 4 KB at a time: it copies the
+// steps ahead of it into shared memory of its own, and forms the products of a
+// step's keys with 8 query rows (token, head of the group) at a time by mma.sync
+// m16n8k16.  (The tensor memory of tcgen05 would have 128 rows of keys wait for
+// one another; here the keys are read once and the products are small.)  The sum
+// over the head's elements has no order, so a lane's consecutive bytes of a row
+// stand for the fragment's elements, of queries and keys alike.
+//
+// 8-bit rows: E4M3 is exact in FP16, and with at most eight query rows so are the
+// queries once each row is scaled by a power of two, unless its elements span
+// more than 2^31.  The codes then take one conversion to a pair, and the blocks'
+// scales are applied to the products of a block.  Else the rows are widened to BF16,
+// in which E4M3 x 2^e is exact.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
-#include "dsa_device.cuh"
+#include <atomic>
+
 #include "e4m3_widen.cuh"
+#include "tile_pipeline.cuh"
 #include "weigh.cuh"
 
 namespace dsa {
@@ -21,10 +31,25 @@ namespace dsa {
 namespace weigh {
 
 using attn::ex2;
-using attn::widen16;
 
 constexpr int kThreads = 256;
-constexpr int kKeys = 32;     // keys of a warp's step
+constexpr int kWarps = kThreads / 32;
+constexpr int kStepBytes = 4096;   // of keys
+constexpr int kSteps = 3;          // in a warp's ring
+
+// Keys of a step.
+template <int D, bool Q8>
+struct Step {
+  static constexpr int kRow = D * (Q8 ? 1 : 2);                           // bytes
+  static constexpr int kKeys = kRow == 256 ? 16 : 32;
+  static constexpr int kUnit = Q8 ? 32 : 64;                              // bytes of a row that four lanes read together
+  // Units of neighbouring rows change places, so that what a quarter (half) of a warp reads at a time is
+  // spread over all banks.
+  static __device__ __forceinline__ uint32_t at(int row, int unit) {
+    const int x = Q8 ? (kRow == 128 ? row & 3 : (row >> 1) & 1) : row & 1;
+    return row * kRow + (unit ^ x) * kUnit;
+  }
+};
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -33,23 +58,34 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A row is read once: not kept in L1.
-__device__ __forceinline__ uint4 load_once(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void mma_16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// First of the groups of kKeys keys of sequence d, in a numbering with room for all of each sequence.
-__device__ __forceinline__ int group_base(const WeighParams& p, int d) { return __ldg(p.cu_k + d) / kKeys + d; }
+// Two E4M3 codes as FP16.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+// First of the steps of sequence d, in a numbering with room for all of each sequence.
+template <int kKeys>
+__device__ __forceinline__ int step_base(const WeighParams& p, int d) {
+  return __ldg(p.cu_k + d) / kKeys + d;
+}
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constant__ WeighParams p) {
-  constexpr int kPieces = Q8 ? D / 64 : D / 32;   // 16-byte pieces of a row to a lane
-  constexpr int kQ = D / 32;                      // of a query row
-  const int tid = threadIdx.x, lane = tid & 31, t = lane & 3, g = lane >> 2;
+  using St = Step<D, Q8>;
+  constexpr int kKeys = St::kKeys;
+  constexpr int kBlocks = D / 32;                 // blocks of 32 elements: of a query row 16 bytes to a lane each
+  extern __shared__ __align__(128) uint8_t ring[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t = lane & 3, g = lane >> 2;
+  const uint32_t sring = smem_u32(ring) + warp * kSteps * kStepBytes;
   int code = 0;
   // Prefixes that fall make rows count for several sequences, or for none: nothing is computed.
   bool falls = false;
@@ -63,177 +99,287 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
   }
   if (tid == 0 && __ldg(p.cu_q + p.num_seqs) > p.total_q) code = DSA_DEV_ERR_INVALID_ARG;
   const bool none = __syncthreads_or(falls);
-  const int n_groups = none ? 0 : group_base(p, p.num_seqs);
-  const int64_t units = (int64_t)n_groups * p.c.n_kv, warps = (int64_t)gridDim.x * (kThreads / 32);
+  const int n_steps = none ? 0 : step_base<kKeys>(p, p.num_seqs);
+  const int64_t units = (int64_t)n_steps * p.c.n_kv, warps = (int64_t)gridDim.x * kWarps;
   const int64_t per = (units + warps - 1) / warps;
-  int64_t u = ((int64_t)blockIdx.x * (kThreads / 32) + (tid >> 5)) * per;
+  int64_t u = ((int64_t)blockIdx.x * kWarps + warp) * per;
   const int64_t u_end = u + per < units ? u + per : units;
 
-  int d = -1, h = -1, base = 0, next_base = 0, n_rows = 0, P0 = 0;
-  Doc doc{};
-  uint4 qf[kQ];        // rows of the first eight (with n_rows <= 8: of every step)
-  float2 bias;
-  auto load_q = [&](int r0) {   // query rows r0 .. r0 + 7 (row r0 + g to this lane), and the biases of rows r0 + 2 t, + 1
-    auto row = [&](int r, int* tok) {
-      *tok = p.group == 1 ? r : (n_rows < 65536 ? (int)__umulhi((uint32_t)r, p.group_mul) : r / p.group);
-      return h * p.group + r - *tok * p.group;
+  while (u < u_end) {
+    // ---- a run: consecutive steps of one sequence and head ----
+    const int h = (int)(u / n_steps), su = (int)(u - (int64_t)h * n_steps);
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (step_base<kKeys>(p, mid) <= su) lo = mid; else hi = mid - 1;
+    }
+    const int d = lo, base = step_base<kKeys>(p, d), next_base = step_base<kKeys>(p, d + 1);
+    Doc doc;
+    doc_info(p, d, &doc);
+    const int64_t run_end = u + (next_base - su) < u_end ? u + (next_base - su) : u_end;
+    const int n_rows = by_steps(p, doc.T) ? doc.T * p.group : 0, P0 = doc.S - doc.T, first = (su - base) * kKeys;
+    int n = (int)(run_end - u);
+    if (n > (doc.S - first + kKeys - 1) / kKeys) n = (doc.S - first + kKeys - 1) / kKeys;
+    u = run_end;
+    if (n_rows == 0 || n <= 0) continue;
+
+    uint4 qf[kBlocks];   // query row r0 + g: elements c * 32 + 8 t ..
+    float2 bias;         // of rows r0 + 2 t and the next one
+    auto load_q = [&](int r0) {
+      int hg;
+      const bool there = r0 + g < n_rows;
+      const int tok = token_of(p, there ? r0 + g : 0, &hg);
+      const uint16_t* src =
+          reinterpret_cast<const uint16_t*>(p.q) + (int64_t)(doc.q0 + tok) * p.q_stride + (int64_t)(h * p.group + hg) * D + 8 * t;
+#pragma unroll
+      for (int c = 0; c < kBlocks; ++c)
+        qf[c] = there ? __ldg(reinterpret_cast<const uint4*>(src + c * 32)) : make_uint4(0, 0, 0, 0);
+      float v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + 2 * t + e;
+        const int tk = token_of(p, r < n_rows ? r : 0, &hg);
+        const float l = __ldg(p.lse + (int64_t)(doc.q0 + tk) * p.n_heads + h * p.group + hg);
+        v[e] = r < n_rows ? bias_of(l) : -INFINITY;
+      }
+      bias = make_float2(v[0], v[1]);
     };
-    int tok;
-    const bool there = r0 + g < n_rows;
-    const int hh = row(there ? r0 + g : 0, &tok);
-    const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (int64_t)(doc.q0 + tok) * p.q_stride + (int64_t)hh * D;
+    if (n_rows <= 8) load_q(0);
+    // FP16 queries, where that loses nothing
+    bool half = false;
+    float2 colscale = make_float2(p.scale_log2, p.scale_log2);
+    if (Q8 && n_rows <= 8) {
+      uint32_t top = 0, low = 0x7FFFu;   // magnitudes of this lane's elements as BF16 bits: largest, smallest but 0
 #pragma unroll
-    for (int c = 0; c < kQ; ++c) {
-      // the elements that this lane's piece of a key row holds
-      const int at = Q8 ? (c >> 1) * 64 + 16 * t + (c & 1) * 8 : c * 32 + 8 * t;
-      qf[c] = there ? __ldg(reinterpret_cast<const uint4*>(src + at)) : make_uint4(0, 0, 0, 0);
-    }
-    float v[2];
+      for (int c = 0; c < kBlocks; ++c) {
+        const uint32_t w[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = r0 + 2 * t + e;
-      int tk;
-      const int hr = row(r < n_rows ? r : 0, &tk);
-      const float l = __ldg(p.lse + (int64_t)(doc.q0 + tk) * p.n_heads + hr);
-      v[e] = r < n_rows && l != -INFINITY ? -l * kLog2e : -INFINITY;   // (a row that sees no key weighs none)
-    }
-    bias = make_float2(v[0], v[1]);
-  };
-  for (; u < u_end; ++u) {
-    const int hu = (int)(u / n_groups), gu = (int)(u - (int64_t)hu * n_groups);
-    if (d < 0 || hu != h || gu >= next_base) {   // another sequence or head
-      int lo = 0, hi = p.num_seqs - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (group_base(p, mid) <= gu) lo = mid; else hi = mid - 1;
-      }
-      d = lo;
-      h = hu;
-      base = group_base(p, d);
-      next_base = group_base(p, d + 1);
-      if (!doc_info(p, d, &doc)) code = DSA_DEV_ERR_INVALID_ARG;
-      n_rows = by_steps(p, doc.T) ? doc.T * p.group : 0;
-      P0 = doc.S - doc.T;
-      if (n_rows > 0 && n_rows <= 8) load_q(0);
-    }
-    const int key0 = (gu - base) * kKeys;
-    if (n_rows == 0 || key0 >= doc.S) {   // to the next sequence
-      u += next_base - 1 - gu;
-      continue;
-    }
-    const int64_t mine = key0 + lane < doc.S ? cache_row(p.c, d, key0 + lane, h) : -1;   // this lane's key
-    if (key0 + lane < doc.S && mine < 0) code = DSA_DEV_ERR_INVALID_ARG;
-    const uint32_t row32 = mine < 0 ? ~0u : (uint32_t)mine;
-    uint32_t a[4][kPieces][Q8 ? 8 : 4];   // keys g, g + 8, g + 16, g + 24 as pairs of BF16
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = __shfl_sync(0xffffffffu, row32, i * 8 + g);
-      if constexpr (Q8) {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(p.c.k) + (size_t)(r == ~0u ? 0 : r) * D + 16 * t;
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          const uint4 v = r == ~0u ? make_uint4(0, 0, 0, 0) : load_once(src + c * 64);
-          a[i][c][0] = v.x; a[i][c][1] = v.y; a[i][c][2] = v.z; a[i][c][3] = v.w;
-          a[i][c][4] = r == ~0u ? 0 : __ldg(p.c.k_scale + (size_t)r * p.c.sw + (p.c.sw == 1 ? 0 : 2 * c + (t >> 1)));
-        }
-      } else {
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(p.c.k) + (size_t)(r == ~0u ? 0 : r) * D + 8 * t;
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          const uint4 v = r == ~0u ? make_uint4(0, 0, 0, 0) : load_once(src + c * 32);
-          a[i][c][0] = v.x; a[i][c][1] = v.y; a[i][c][2] = v.z; a[i][c][3] = v.w;
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t m = (i & 1 ? w[i >> 1] >> 16 : w[i >> 1]) & 0x7FFFu;
+          top = max(top, m);
+          low = min(low, m == 0 ? 0x7FFFu : m);
         }
       }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
+      }
+      // the largest element goes to exponent 14, the least bit of the smallest stays at 2^-24 or above
+      const int e_top = top >> 7, e_low = low >> 7;
+      const bool fits = top == 0 || (e_top >= 15 && e_top < 255 && e_low >= 1 && e_top - e_low <= 31);
+      half = __all_sync(0xffffffffu, fits);
+      if (half) {
+        const float f = top == 0 ? 1.f : __uint_as_float((uint32_t)(14 + 254 - e_top) << 23);   // 2^(14 - (e_top - 127))
+        const float back = top == 0 ? 1.f : __uint_as_float((uint32_t)(e_top - 14) << 23);
+#pragma unroll
+        for (int c = 0; c < kBlocks; ++c) {
+          uint32_t w[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 v = __floats2half2_rn(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+            w[i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          qf[c] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        // of columns 2 t and 2 t + 1 (rows that lanes 8 t and 8 t + 4 hold)
+        const float b0 = __shfl_sync(0xffffffffu, back, 8 * t), b1 = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+        colscale = make_float2(b0 * p.scale_log2, b1 * p.scale_log2);
+      }
     }
-    if constexpr (Q8) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          const uint32_t w4[4] = {a[i][c][0], a[i][c][1], a[i][c][2], a[i][c][3]}, e8 = a[i][c][4];
-          if (e8 <= 134u) widen16<false>(w4, e8, a[i][c]);
-          else widen16<true>(w4, e8, a[i][c]);
+
+    // ---- a lane looks up one key of a step: its row, its scales, its weight so far ----
+    struct Ahead {
+      uint32_t row, scale;
+      float old;
+    };
+    bool bad = false;
+    const int64_t table = (int64_t)d * p.c.max_pages;
+    auto key_of = [&](int i) { return i < n && lane < kKeys ? first + i * kKeys + lane : doc.S; };   // (doc.S: none)
+    auto page_of = [&](int i) {
+      const int key = key_of(i);
+      return key < doc.S ? __ldg(p.c.table + table + (key >> p.c.page_shift)) : 0;
+    };
+    auto fetch = [&](int i, int page) {
+      Ahead a{~0u, 0u, 0.f};
+      const int key = key_of(i);
+      if (key < doc.S) {
+        if ((unsigned)page < (unsigned)p.c.num_pages) {
+          a.row = (uint32_t)((((int64_t)page * p.c.n_kv + h) << p.c.page_shift) + (key & ((1 << p.c.page_shift) - 1)));
+          if (key < P0) a.old = __ldcg(p.weights + a.row);
+          if constexpr (Q8) {   // a byte to each block
+            if (p.c.sw == 1) a.scale = __ldg(p.c.k_scale + a.row) * 0x01010101u;
+            else if constexpr (D == 128) a.scale = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_scale) + a.row);
+            else a.scale = __ldg(reinterpret_cast<const uint16_t*>(p.c.k_scale) + a.row);
+          }
+        } else {
+          bad = true;
         }
       }
-    }
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};   // of keys g, g + 8, g + 16, g + 24
-    const bool edge = key0 + kKeys > P0 + 1;   // some token does not see some key
-    const int r_first = edge && key0 > P0 ? (key0 - P0) * p.group : 0;   // rows before it see none of these keys
-    for (int r0 = r_first & ~7; r0 < n_rows; r0 += 8) {
-      if (n_rows > 8) load_q(r0);
-      float acc[2][4] = {};
+      if (i < n) {
+        constexpr int PPR = St::kRow / 16, RPI = 32 / PPR;   // 16-byte pieces of a row, rows of an instruction
+        const int piece = lane % PPR, rsub = lane / PPR;
+        const uint8_t* const src = reinterpret_cast<const uint8_t*>(p.c.k) + piece * 16;
+        const uint32_t dst = sring + (i % kSteps) * kStepBytes + piece * 16 % St::kUnit;
 #pragma unroll
-      for (int c = 0; c < kQ; ++c) {
-        const uint32_t* const qw = reinterpret_cast<const uint32_t*>(&qf[c]);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int pc = Q8 ? c >> 1 : c, o = Q8 ? (c & 1) * 4 + 2 * s : 2 * s;
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-            mma_16816(acc[m], a[2 * m][pc][o], a[2 * m + 1][pc][o], a[2 * m][pc][o + 1], a[2 * m + 1][pc][o + 1], qw[2 * s],
-                      qw[2 * s + 1]);
+        for (int r = 0; r < kKeys; r += RPI) {
+          const uint32_t row = __shfl_sync(0xffffffffu, a.row, r + rsub);
+          attn::cp_async16(dst + St::at(r + rsub, piece * 16 / St::kUnit), src + (size_t)(row == ~0u ? 0 : row) * St::kRow, row != ~0u);
         }
       }
-      float w[2][4];
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return a;
+    };
+    Ahead a0 = fetch(0, page_of(0)), a1 = fetch(1, page_of(1)), a2 = fetch(2, page_of(2));
+    int page = page_of(3);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSteps - 1) : "memory");
+      __syncwarp();
+      const uint32_t step = sring + (i % kSteps) * kStepBytes;
+      const int key0 = first + i * kKeys;
+      const bool edge = key0 + kKeys > P0 + 1;   // some token does not see some key
+      const int r_first = edge && key0 > P0 ? (key0 - P0) * p.group : 0;   // rows before it see none of these keys
+      float sum[kKeys / 8];   // of keys g, g + 8, ..
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
+      for (int m = 0; m < kKeys / 16; ++m) {
+        const int ra = m * 16 + g, rb = ra + 8;   // this lane's keys
+        float sa = 0.f, sb = 0.f;
+        auto add = [&](const float (&acc)[4], int r0) {
+          float w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[m][e] = ex2(fmaf(acc[m][e], p.scale_log2, e & 1 ? bias.y : bias.x));
-      }
-      if (edge) {
+          for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(acc[e], e & 1 ? colscale.y : colscale.x, e & 1 ? bias.y : bias.x));
+          if (edge) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = r0 + 2 * t + e;
-          const int vis = P0 + (p.group == 1 ? r : (n_rows < 65536 ? (int)__umulhi((uint32_t)r, p.group_mul) : r / p.group));
+            for (int e = 0; e < 2; ++e) {
+              int hg;
+              const int vis = P0 + token_of(p, r0 + 2 * t + e, &hg);
+              if (key0 + ra > vis) w[e] = 0.f;
+              if (key0 + rb > vis) w[2 + e] = 0.f;
+            }
+          }
+          sa += w[0] + w[1];
+          sb += w[2] + w[3];
+        };
+        if (Q8 && half) {
+          const uint32_t ca = __shfl_sync(0xffffffffu, a0.scale, ra), cb = __shfl_sync(0xffffffffu, a0.scale, rb);
+          float total[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if (key0 + m * 16 + g > vis) w[m][e] = 0.f;
-            if (key0 + m * 16 + 8 + g > vis) w[m][2 + e] = 0.f;
+          for (int c = 0; c < kBlocks; ++c) {
+            uint32_t xa[2], xb[2];
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(xa[0]), "=r"(xa[1]) : "r"(step + St::at(ra, c) + 8 * t));
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(xb[0]), "=r"(xb[1]) : "r"(step + St::at(rb, c) + 8 * t));
+            const uint32_t qw[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+              mma_16816_f16(acc, codes_f16(xa[s]), codes_f16(xb[s]), codes_f16(xa[s] >> 16), codes_f16(xb[s] >> 16), qw[2 * s], qw[2 * s + 1]);
+            // 2^(byte - 127) from its bits (byte 0: a subnormal)
+            const float fa = __uint_as_float(max(((ca >> (8 * c)) & 255u) << 23, 0x00400000u));
+            const float fb = __uint_as_float(max(((cb >> (8 * c)) & 255u) << 23, 0x00400000u));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) total[e] = fmaf(acc[e], e < 2 ? fa : fb, total[e]);
+          }
+          add(total, 0);
+        } else {
+          uint32_t a[2][kBlocks][4];   // the two keys as pairs of BF16
+          if constexpr (Q8) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t sc = __shfl_sync(0xffffffffu, a0.scale, k ? rb : ra);
+#pragma unroll
+              for (int c = 0; c < kBlocks; ++c) {
+                uint32_t w2[2];
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w2[0]), "=r"(w2[1]) : "r"(step + St::at(k ? rb : ra, c) + 8 * t));
+                const uint32_t e8 = (sc >> (8 * c)) & 255u;
+                if (e8 <= 134u) attn::widen<false>(w2, e8, a[k][c]);
+                else attn::widen<true>(w2, e8, a[k][c]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+              for (int c = 0; c < kBlocks; ++c) attn::ld_shared_v4(step + St::at(k ? rb : ra, c) + 16 * t, a[k][c]);
+            }
+          }
+          for (int r0 = r_first & ~7; r0 < n_rows; r0 += 8) {
+            if (n_rows > 8) load_q(r0);
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kBlocks; ++c) {
+              const uint32_t qw[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
+#pragma unroll
+              for (int s = 0; s < 2; ++s)
+                mma_16816(acc, a[0][c][2 * s], a[1][c][2 * s], a[0][c][2 * s + 1], a[1][c][2 * s + 1], qw[2 * s], qw[2 * s + 1]);
+            }
+            add(acc, r0);
           }
         }
+        sum[2 * m] = sa;
+        sum[2 * m + 1] = sb;
       }
+      // sums over the four lanes of a row; lane (g, t) ends with key 8 t + g (16 keys: t of 0 and 1)
+      float got;
+      if constexpr (kKeys == 32) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        sum[2 * m] += w[m][0] + w[m][1];
-        sum[2 * m + 1] += w[m][2] + w[m][3];
+        for (int e = 0; e < 2; ++e) {
+          const float give = t & 2 ? sum[e] : sum[e + 2], keep = t & 2 ? sum[e + 2] : sum[e];
+          sum[e] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+        }
+        const float give = t & 1 ? sum[0] : sum[1], keep = t & 1 ? sum[1] : sum[0];
+        got = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+      } else {
+        const float give = t & 1 ? sum[0] : sum[1], keep = t & 1 ? sum[1] : sum[0];
+        got = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+        got += __shfl_xor_sync(0xffffffffu, got, 2);
       }
+      got = __shfl_sync(0xffffffffu, got, (lane & 7) * 4 + (lane >> 3) % (kKeys / 8));   // key `lane`
+      if (a0.row != ~0u) p.weights[a0.row] = a0.old + got;
+      // the next steps (the syncs keep the copies behind every lane's reads)
+      __syncwarp();
+      a0 = a1;
+      a1 = a2;
+      a2 = fetch(i + kSteps, page);
+      page = page_of(i + kSteps + 1);
     }
-    // sums over the four lanes of a row; lane t ends with key group t
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float give = t & 2 ? sum[e] : sum[e + 2], keep = t & 2 ? sum[e + 2] : sum[e];
-      sum[e] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
-    }
-    const float give = t & 1 ? sum[0] : sum[1], keep = t & 1 ? sum[1] : sum[0];
-    const float got = keep + __shfl_xor_sync(0xffffffffu, give, 1);
-    const int mykey = t * 8 + g;
-    const uint32_t r = __shfl_sync(0xffffffffu, row32, mykey);
-    if (r != ~0u) p.weights[r] = key0 + mykey >= P0 ? got : p.weights[r] + got;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+    if (bad) code = DSA_DEV_ERR_INVALID_ARG;
   }
   code = __syncthreads_or(code != 0) ? DSA_DEV_ERR_INVALID_ARG : 0;
   if (tid == 0) put_status(p, blockIdx.x, code);
 }
 
+template <int D, bool Q8>
+cudaError_t launch_steps(const WeighParams& p, int blocks, cudaStream_t stream) {
+  constexpr int kSmem = kWarps * kSteps * kStepBytes;
+  auto kernel = weigh_kernel<D, Q8>;
+  int dev = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready{0};   // devices on which this kernel is set up
+  if (!(ready.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+    ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
+  }
+  kernel<<<blocks, kThreads, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace weigh
 
 int weigh_step_blocks(const WeighParams& p, int sm_count) {
-  // no more blocks than there can be groups of keys
-  const int64_t groups = ((int64_t)p.max_seqlen_k / weigh::kKeys + 1) * p.num_seqs * p.c.n_kv;
-  const int64_t blocks = (groups + weigh::kThreads / 32 - 1) / (weigh::kThreads / 32);
+  // no more blocks than there can be steps (of 16 keys or more)
+  const int64_t steps = ((int64_t)p.max_seqlen_k / 16 + 1) * p.num_seqs * p.c.n_kv;
+  const int64_t blocks = (steps + weigh::kWarps - 1) / weigh::kWarps;
   return (int)(blocks < 2 * sm_count ? blocks : 2 * sm_count);
 }
 
 cudaError_t launch_weigh_steps(const WeighParams& p, int D, int blocks, cudaStream_t stream) {
-  using namespace weigh;
   const bool q8 = p.c.fmt != 0;
-  if (D == 128) {
-    if (q8) weigh_kernel<128, true><<<blocks, kThreads, 0, stream>>>(p);
-    else weigh_kernel<128, false><<<blocks, kThreads, 0, stream>>>(p);
-  } else {
-    if (q8) weigh_kernel<64, true><<<blocks, kThreads, 0, stream>>>(p);
-    else weigh_kernel<64, false><<<blocks, kThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  if (D == 128) return q8 ? weigh::launch_steps<128, true>(p, blocks, stream) : weigh::launch_steps<128, false>(p, blocks, stream);
+  return q8 ? weigh::launch_steps<64, true>(p, blocks, stream) : weigh::launch_steps<64, false>(p, blocks, stream);
 }
 
 }  // namespace dsa

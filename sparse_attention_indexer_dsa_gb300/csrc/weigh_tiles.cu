@@ -30,10 +30,11 @@ using namespace attn;
 
 constexpr int kTileThreads = 512;
 constexpr int kGroups = 64;            // sequences are counted in this many groups
+constexpr int kHalf = kWeighCols / 2;   // columns of a product and of a hand-over
 constexpr int kBiasRing = 4;
 constexpr int kMinTiles = 8;           // query tiles of a part, at least
 // barriers
-enum { K_FULL = 0, K_EMPTY = 2, S_FULL = 4, S_EMPTY = 6, B_FULL = 8, B_EMPTY = B_FULL + kBiasRing, DRAIN = B_EMPTY + kBiasRing,
+enum { K_FULL = 0, K_EMPTY = 2, S_FULL = 4, S_EMPTY = 8, B_FULL = 12, B_EMPTY = B_FULL + kBiasRing, DRAIN = B_EMPTY + kBiasRing,
        Q_FULL, kMaxStages = 4, Q_EMPTY = Q_FULL + kMaxStages, kBars = Q_EMPTY + kMaxStages };
 
 template <int D>
@@ -185,8 +186,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(K_FULL + w), 4);
       mbar_init(bar(K_EMPTY + w), 1);
-      mbar_init(bar(S_FULL + w), 1);
-      mbar_init(bar(S_EMPTY + w), 4);
+    }
+    for (int i = 0; i < 4; ++i) {   // half tiles: 2 w + half
+      mbar_init(bar(S_FULL + i), 1);
+      mbar_init(bar(S_EMPTY + i), 4);
     }
     for (int s = 0; s < kBiasRing; ++s) {
       mbar_init(bar(B_FULL + s), 1);
@@ -230,27 +233,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
       for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
       for (int j = 0; j < x.n; ++j, ++nt) {
         const int slot = nt % kBiasRing;
-        ok = __all_sync(0xffffffffu, wait_bar(bar(S_FULL + w), nt & 1u, abort_flag, status, tmo) &&
-                                         wait_bar(bar(B_FULL + slot), (nt / kBiasRing) & 1u, abort_flag, status, tmo));
-        if (!ok) break;
-        tc_fence_after();
         const int i0 = x.i0 + j * tq, tokens = min(tq, x.T - i0), cols = tokens * p.group;
         const float* const bias = reinterpret_cast<const float*>(smem + L::kOffBias) + slot * kWeighCols;
         const int* const seen = reinterpret_cast<const int*>(smem + L::kOffBias) + (kBiasRing + slot) * kWeighCols;
-        if (wkey <= x.P0 + i0 + tokens - 1 && wkey < x.S) {   // (else no token of the tile sees a key of the warp)
-          // some key that some token does not see, or columns of other sequences' tokens
-          const bool edge = wkey + 31 > x.P0 + i0 || tokens < tq;
+        const bool any = wkey <= x.P0 + i0 + tokens - 1 && wkey < x.S;   // (else no token of the tile sees a key of the warp)
+        // some key that some token does not see, or columns of other sequences' tokens
+        const bool edge = wkey + 31 > x.P0 + i0 || tokens < tq;
+        ok = __all_sync(0xffffffffu, wait_bar(bar(B_FULL + slot), (nt / kBiasRing) & 1u, abort_flag, status, tmo));
 #pragma unroll 1
-          for (int c = 0; c < cols; c += 32) {
-            uint32_t s[32];
-            tmem_ld_x32(t_s + c, s);
-            tmem_ld_wait_tied<32>(s);
-            if (!edge) {
+        for (int half = 0; half < 2 && ok; ++half) {
+          const int c0 = half * kHalf;
+          ok = __all_sync(0xffffffffu, wait_bar(bar(S_FULL + 2 * w + half), nt & 1u, abort_flag, status, tmo));
+          if (!ok) break;
+          tc_fence_after();
+          auto release = [&] {   // the half's columns have been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(S_EMPTY + 2 * w + half));
+          };
+          if (!any || c0 >= cols) {
+            release();
+          } else if (!edge) {
+            // the next 32 columns are on their way while these become weights
+            uint32_t s[2][32];
+            tmem_ld_x32(t_s + c0, s[0]);
+#pragma unroll
+            for (int c = 0; c < kHalf / 32; ++c) {
+              tmem_ld_wait_tied<32>(s[c & 1]);
+              if (c + 1 < kHalf / 32) tmem_ld_x32(t_s + c0 + 32 * (c + 1), s[(c + 1) & 1]);
+              else release();
+              const float* const b32 = bias + c0 + 32 * c;
+              const uint32_t* const v = s[c & 1];
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
-                const float4 b = *reinterpret_cast<const float4*>(bias + c + 2 * i);
-                float2 e0 = ffma2(as_f2(s[2 * i], s[2 * i + 1]), sc2, make_float2(b.x, b.y));
-                float2 e1 = ffma2(as_f2(s[2 * i + 2], s[2 * i + 3]), sc2, make_float2(b.z, b.w));
+                const float4 b = *reinterpret_cast<const float4*>(b32 + 2 * i);
+                float2 e0 = ffma2(as_f2(v[2 * i], v[2 * i + 1]), sc2, make_float2(b.x, b.y));
+                float2 e1 = ffma2(as_f2(v[2 * i + 2], v[2 * i + 3]), sc2, make_float2(b.z, b.w));
                 e0.x = ex2(e0.x);
                 e0.y = ex2(e0.y);
                 e1.x = ex2(e1.x);
@@ -258,21 +276,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
                 sum[i & 2] = __fadd2_rn(sum[i & 2], e0);
                 sum[(i & 2) + 1] = __fadd2_rn(sum[(i & 2) + 1], e1);
               }
-            } else {
+            }
+          } else {
+            const int end = min(cols, c0 + kHalf);
+#pragma unroll 1
+            for (int c = c0; c < end; c += 32) {
+              uint32_t s[32];
+              tmem_ld_x32(t_s + c, s);
+              tmem_ld_wait_tied<32>(s);
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float e = ex2(fmaf(__uint_as_float(s[i]), p.scale_log2, bias[c + i]));
                 sum[(i >> 1) & 3].x += key <= seen[c + i] ? e : 0.f;
               }
             }
+            release();
           }
         }
-        tc_fence_before();
+        if (!ok) break;
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(S_EMPTY + w));
-          mbar_arrive(bar(B_EMPTY + slot));
-        }
+        if (lane == 0) mbar_arrive(bar(B_EMPTY + slot));
       }
       if (!ok) break;
       const float total = ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
@@ -320,8 +343,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
               const int r = (i0 + i) * RPP + rsub;
               const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
               uint32_t o[8];
-              if (e8[i] <= 134u) widen16<false>(w4, e8[i], o);
-              else widen16<true>(w4, e8[i], o);
+              if (e8[i] <= 134u) widen<false>(w4, e8[i], o);
+              else widen<true>(w4, e8[i], o);
               const uint32_t at = dst + (uint32_t)(c >> 2) * (128 * 128) + r * 128;
               st_shared_v4(at + ((((c & 3) * 2) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
               st_shared_v4(at + ((((c & 3) * 2 + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
@@ -411,7 +434,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
   } else if (warp == kMmaWarp) {
     // ======================= products =======================
     if (elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16(128, kWeighCols);
+      constexpr uint32_t idesc = idesc_bf16(128, kHalf);
       uint32_t nt = 0, nk = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
@@ -419,21 +442,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
         for (int j = 0; j < x.n && ok; ++j, ++nt) {
           const uint32_t st = nt % L::kStages;
           ok = wait_bar(bar(Q_FULL + st), (nt / L::kStages) & 1u, abort_flag, status, tmo);
+          const uint64_t q0 = sw128_kmajor_desc(sbase + L::kOffQ + st * L::kQueryTile, 0);
 #pragma unroll 1
-          for (int w = 0; w < 2 && ok; ++w) {
-            if (j == 0) ok = wait_bar(bar(K_FULL + w), nk & 1u, abort_flag, status, tmo);
-            if (ok && nt > 0) ok = wait_bar(bar(S_EMPTY + w), (nt - 1) & 1u, abort_flag, status, tmo);
+          for (int i = 0; i < 4 && ok; ++i) {   // the streams in turn: half i / 2 of stream i % 2
+            const int w = i & 1, half = i >> 1;
+            if (j == 0 && half == 0) ok = wait_bar(bar(K_FULL + w), nk & 1u, abort_flag, status, tmo);
+            if (ok && nt > 0) ok = wait_bar(bar(S_EMPTY + 2 * w + half), (nt - 1) & 1u, abort_flag, status, tmo);
             if (!ok) break;
             tc_fence_after();
-            uint64_t kd = sw128_kmajor_desc(sbase + w * L::kKeyTile, 0);
-            uint64_t qd = sw128_kmajor_desc(sbase + L::kOffQ + st * L::kQueryTile, 0);
+            uint64_t kd = sw128_kmajor_desc(sbase + w * L::kKeyTile, 0), qd = q0 + half * ((kHalf * 128) >> 4);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c, kd += (128 * 128) >> 4, qd += (kWeighCols * 128) >> 4) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_bf16(tmem + w * kWeighCols, kd + 2 * k, qd + 2 * k, idesc, c + k > 0);   // 32 bytes a step
+              for (int k = 0; k < 4; ++k)   // 32 bytes a step
+                mma_bf16(tmem + w * kWeighCols + half * kHalf, kd + 2 * k, qd + 2 * k, idesc, c + k > 0);
             }
-            tc_commit(bar(S_FULL + w));
-            if (j + 1 == x.n) tc_commit(bar(K_EMPTY + w));
+            tc_commit(bar(S_FULL + 2 * w + half));
+            if (j + 1 == x.n && half == 1) tc_commit(bar(K_EMPTY + w));
           }
           if (ok) tc_commit(bar(Q_EMPTY + st));
         }

@@ -142,6 +142,42 @@ def test_weigh_far_scales():
         check_weigh(b, rng, 2, std=1e-6)
 
 
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8", "fp8"])
+@pytest.mark.parametrize("T", [1, 5])
+def test_weigh_queries_of_wide_range(prec, T):
+    """Query elements that span up to 2^100, far from one altogether (the scale brings the logits back)."""
+    rng = np.random.default_rng([39, T])
+    b = Batch(rng, [(T, 77)], 1, 128, 16, prec)
+    for spread, shift in ((1, 0), (20, 80), (31, 0), (31, -100), (33, 0), (60, 0), (100, 80), (100, -100)):
+        x = rng.standard_normal((T, 4, 128)) * 2.0 ** (shift + rng.uniform(-spread, 0, (T, 4, 128)))
+        x[:, 3, ::2] = 0
+        bits, _ = quantise(x, "bf16")
+        q, qd = values(bits, None, "bf16"), bf16_dev(bits)
+        scale = float(np.float32(0.09 * 2.0 ** -shift))
+        lse = true_lse(b, q, 4, scale)
+        w = E.random_weights(rng, b)
+        got = weigh(b, b.cache(dsa), dev(w), qd, dev(lse), scale)
+        close(got, *E.weigh(b, q, lse.astype(np.float64), w, 4, scale), (spread, shift))
+
+
+def test_weigh_lost_bits():
+    """One huge query element against zeros of every key: the others' products must not suffer."""
+    rng = np.random.default_rng(40)
+    for prec in ("mxfp8", "fp8"):
+        b = Batch(rng, [(1, 64)], 1, 64, 16, prec)
+        for nm in ("k",):
+            b.rows[nm][..., 7] = 0
+            b.pages[nm][..., 7] = 0
+        x = rng.standard_normal((1, 2, 64))
+        x[..., 7] = 1e12
+        bits, _ = quantise(x, "bf16")
+        q, qd = values(bits, None, "bf16"), bf16_dev(bits)
+        lse = true_lse(b, q, 2, 0.5)
+        w = np.zeros((b.num_pages, 1, 16), np.float32)
+        got = weigh(b, b.cache(dsa), dev(w), qd, dev(lse), 0.5)
+        close(got, *E.weigh(b, q, lse.astype(np.float64), w, 2, 0.5))
+
+
 def test_weigh_strange_lse():
     """Rows that saw nothing add nothing; scale 0 weighs every row alike."""
     rng = np.random.default_rng(32)
@@ -267,6 +303,16 @@ def test_select_long(page):
     for budget in (200, 4096, 70000):
         check_select(b, w, budget, 4, 64, False)
     check_select(b, E.random_weights(rng, b, True), 5000, 0, 0, True)
+
+
+@pytest.mark.parametrize("lens", [[20000], [5000, 41, 9000], [3000] * 70, [400000]])
+def test_select_clusters(lens):
+    """From one block to a head to eight, and more rows than eight hold."""
+    rng = np.random.default_rng(len(lens))
+    b = Batch(rng, [(0, s) for s in lens], 1, 64, 1024, "fp8", values_too=False)
+    w = E.random_weights(rng, b, True)
+    for budget in (33, 2500):
+        check_select(b, w, budget, 3, 10, False)
 
 
 def test_select_strange_weights():

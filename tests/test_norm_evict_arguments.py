@@ -54,7 +54,7 @@ def test_norm_rope_refuses(lib, want, change):
 @pytest.mark.parametrize("want,change", SHARED_NORM + [
     (BAD, dict(dq=None)), (BAD, dict(dk=None)), (BAD, dict(dq_out=None)), (BAD, dict(dk_out=None)), (BAD, dict(grad_dtype=2)),
     (BAD, dict(dq_out=A + 8)), (BAD, dict(dk_out=A + 8)), (BAD, dict(dq_out_stride=100)), (BAD, dict(dk_out_stride=100)),
-    (BAD, dict(dq_stride=100)), (WS, dict(ws=None)), (WS, dict(ws_bytes=100)), (BAD, dict(ws=A + 64))])
+    (BAD, dict(dq_stride=100)), (BAD, dict(dq_bias=A)), (BAD, dict(dk_bias=A)), (WS, dict(ws=None)), (WS, dict(ws_bytes=100)), (BAD, dict(ws=A + 64))])
 def test_norm_rope_backward_refuses(lib, want, change):
     assert call(lib.dsa_idx_norm_rope_backward, BACK, **change) == want, change
 
