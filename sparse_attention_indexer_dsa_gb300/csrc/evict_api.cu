@@ -18,9 +18,9 @@ size_t dsa_idx_weigh_workspace_size(int total_q, int num_seqs, int max_seqlen_q,
   if (total_q < 0 || num_seqs < 1 || max_seqlen_q < 0 || n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads != 0 ||
       n_heads / n_kv_heads > 128 || (head_dim != 64 && head_dim != 128))
     return 0;
-  // the parts' sums where a sequence may have more query rows than the step kernel takes
+  // the sums of divided units where a sequence may have more query rows than the step kernel takes
   const bool tiles = (int64_t)max_seqlen_q * (n_heads / n_kv_heads) > kWeighStepRows;
-  return DSA_DEV_STATUS_HEADER_BYTES + (tiles ? (size_t)kWeighUnits * kWeighKeys * sizeof(float) : 0);
+  return DSA_DEV_STATUS_HEADER_BYTES + (tiles ? (size_t)kAttnSms * 2 * kWeighKeys * sizeof(float) : 0);
 }
 
 dsa_status_t dsa_idx_cache_weigh(const void* q, int64_t q_stride, const float* lse, const void* k_pages,
@@ -70,12 +70,12 @@ dsa_status_t dsa_idx_cache_weigh(const void* q, int64_t q_stride, const float* l
   // their lengths on the device.
   const bool tiles = total_q > 0 && (int64_t)max_seqlen_q * p.group > kWeighStepRows;
   p.step_blocks = weigh_step_blocks(p, di.sm_count);
-  p.tile_blocks = tiles ? di.sm_count : 0;
+  p.tile_blocks = tiles ? (di.sm_count < kAttnSms ? di.sm_count : kAttnSms) : 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (tiles && (s = make_queries_map(&p.tm_q, q, total_q, q_stride, n_heads, head_dim, p.group, kWeighCols / p.group)) != DSA_OK)
     return s;
   cudaError_t e = launch_weigh_steps(p, head_dim, p.step_blocks, st);
-  if (e == cudaSuccess && tiles) e = launch_weigh_tiles(p, head_dim, di.sm_count, st);
+  if (e == cudaSuccess && tiles) e = launch_weigh_tiles(p, head_dim, st);
   if (e != cudaSuccess) return cuda_fail(e, "cache weigh launch");
   return DSA_OK;
 }

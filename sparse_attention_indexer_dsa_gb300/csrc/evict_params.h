@@ -21,7 +21,7 @@ struct WeighParams {
   float scale_log2;   // sm_scale * log2(e)
   int step_blocks, tile_blocks;
   int* hdr;
-  float* part;        // [kWeighUnits][kWeighKeys] sums over parts of the queries
+  float* part;        // [tile_blocks][2][kWeighKeys] sums of divided units: that a block ends, that it begins
   int fault_inject;
   unsigned long long timeout_ns;
 };
@@ -30,9 +30,6 @@ struct WeighParams {
 constexpr int kWeighStepRows = 64;
 constexpr int kWeighCols = 256;    // query rows of a tile
 constexpr int kWeighKeys = 256;    // keys of a unit
-constexpr int kWeighBalance = 8 * kAttnSms;       // units that a call is divided into, about
-constexpr int kWeighUnits = 2 * kWeighBalance;    // ... and at most, where parts are joined
-
 struct SelectParams {
   const float* weights;
   const int32_t* table;
@@ -59,7 +56,7 @@ struct CompactParams {
 
 int weigh_step_blocks(const WeighParams& p, int sm_count);
 cudaError_t launch_weigh_steps(const WeighParams& p, int D, int blocks, cudaStream_t stream);
-cudaError_t launch_weigh_tiles(const WeighParams& p, int D, int sm_count, cudaStream_t stream);
+cudaError_t launch_weigh_tiles(const WeighParams& p, int D, cudaStream_t stream);
 cudaError_t launch_evict_select(const SelectParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_cache_compact(const CompactParams& p, int sm_count, cudaStream_t stream);
 
