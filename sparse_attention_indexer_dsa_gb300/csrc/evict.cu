@@ -38,6 +38,7 @@ constexpr uint32_t kMust = 0xFFFFFFFFu;   // above every weight's bits
 constexpr int kSelCluster = 8;            // blocks of a cluster, at most
 constexpr int kSelRows = 40 * 1024;       // rows of a block whose bits fit into its shared memory
 constexpr int kSelFixed = 2 * kBins + kLastBins;   // words of the counts
+constexpr int kSelFew = kSelThreads;
 
 // Order-preserving bits of a weight; NaN below everything, -0 as +0.
 __device__ __forceinline__ uint32_t weight_bits(float w) { return w != w ? 0u : orderable_key(w); }
@@ -65,14 +66,17 @@ struct Select {
 };
 
 // Finds the bin of the `want`-th largest entry of the cluster's counts hist[n] and takes off `want` what
-// lies above it.  The whole cluster calls, after its counts are complete; every thread gets the result.
-__device__ __forceinline__ int find_bin(cg::cluster_group& cluster, uint32_t* hist, int n, int* want, int (*scratch)[kSelWarps + 2]) {
+// lies above it; *count: entries of the bin.  The whole cluster calls, after its counts are complete;
+// every thread gets the result.
+__device__ __forceinline__ int find_bin(cg::cluster_group& cluster, uint32_t* hist, int n, int* want, int* count,
+                                        int (*scratch)[kSelWarps + 3]) {
   const int tid = threadIdx.x, lane = tid & 31;
   int c[4] = {0, 0, 0, 0};   // of four bins, from the top down over the threads
   const int top = n - 4 * tid;
+  const unsigned blocks = cluster.num_blocks();
   if (top > 0) {
-    for (unsigned r = 0; r < cluster.num_blocks(); ++r) {
-      const uint4 v = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, r) + top - 4);
+    for (unsigned r = 0; r < blocks; ++r) {
+      const uint4 v = *reinterpret_cast<const uint4*>((blocks > 1 ? cluster.map_shared_rank(hist, r) : hist) + top - 4);
       c[0] += v.w;
       c[1] += v.z;
       c[2] += v.y;
@@ -98,12 +102,14 @@ __device__ __forceinline__ int find_bin(cg::cluster_group& cluster, uint32_t* hi
       if (above < w && above + c[j] >= w) {
         (*scratch)[kSelWarps] = top - 1 - j;
         (*scratch)[kSelWarps + 1] = w - above;
+        (*scratch)[kSelWarps + 2] = c[j];
       }
       above += c[j];
     }
   }
   __syncthreads();
   *want = (*scratch)[kSelWarps + 1];
+  *count = (*scratch)[kSelWarps + 2];
   return (*scratch)[kSelWarps];
 }
 
@@ -111,13 +117,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   extern __shared__ __align__(16) uint32_t sm[];
   uint32_t* const hist[3] = {sm, sm + kBins, sm + 2 * kBins};
   uint32_t* const bits = sm + kSelFixed;     // [p.cached]
-  __shared__ int scratch[3][kSelWarps + 2];
+  __shared__ int scratch[3][kSelWarps + 3];
   __shared__ int counts[2][kSelWarps];
   __shared__ int total[2];
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = p.shared ? 1 : p.n_kv, blocks = cluster.num_blocks(), rank = cluster.block_rank();
   int code = 0;
+  auto sync = [&] {
+    if (blocks > 1) cluster.sync(); else __syncthreads();
+  };
   for (int u = blockIdx.x / blocks; u < p.num_seqs * heads; u += gridDim.x / blocks) {
     const int d = u / heads, h = u - d * heads;
     int32_t* const out = p.kept + (int64_t)u * p.budget;
@@ -138,6 +147,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     Select sel{p, d, h, S};
     auto value = [&](int i) { return cached ? bits[i] : sel.at(lo + i); };
     for (int i = tid; i < kSelFixed; i += kSelThreads) sm[i] = 0;
+    if (tid == 0) total[0] = 0;
     __syncthreads();
     int want = p.budget;
     uint32_t prefix = 0;
@@ -146,7 +156,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     for (int step = 0; step < 3; ++step) {
       const int shift = step == 0 ? 20 : (step == 1 ? 8 : 0), bins = step == 2 ? kLastBins : kBins;
       uint32_t* const count = hist[step];
-      constexpr int U = 4;   // rows of a thread whose loads go together
+      constexpr int U = 8;   // rows of a thread whose loads go together
       for (int i0 = 0; i0 < n; i0 += U * kSelThreads) {
         uint32_t b[U];
 #pragma unroll
@@ -176,8 +186,36 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
           }
         }
       }
-      cluster.sync();
-      prefix = (prefix << (step == 2 ? 8 : 12)) | (uint32_t)find_bin(cluster, count, bins, &want, &scratch[step]);
+      sync();
+      int in_bin;
+      prefix = (prefix << (step == 2 ? 8 : 12)) | (uint32_t)find_bin(cluster, count, bins, &want, &in_bin, &scratch[step]);
+      if (step == 0 && blocks == 1 && in_bin <= kSelFew) {
+        // few rows share the last one's first digit: each is ranked among them at once
+        unsigned long long* const few = reinterpret_cast<unsigned long long*>(hist[1]);
+        for (int i = tid; i < n; i += kSelThreads) {
+          const uint32_t b = value(i);
+          if ((b >> 20) == prefix) few[atomicAdd(&total[0], 1)] = (unsigned long long)(~b) << 32 | (unsigned)i;
+        }
+        __syncthreads();
+        if (tid < in_bin) {
+          const unsigned long long mine = few[tid];
+          int rank = 0, above = 0;
+          for (int i = 0; i < in_bin; ++i) {
+            const unsigned long long other = few[i];
+            rank += other < mine;
+            above += (uint32_t)(other >> 32) < (uint32_t)(mine >> 32);
+          }
+          if (rank == want - 1) {   // the last that stays
+            counts[0][0] = (int)~(uint32_t)(mine >> 32);
+            counts[0][1] = want - above;
+          }
+        }
+        __syncthreads();
+        prefix = (uint32_t)counts[0][0];
+        want = counts[0][1];
+        __syncthreads();
+        break;
+      }
     }
     // `prefix` is the last value that stays, `want` the number of rows of that value that do
     const int wper = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
@@ -200,7 +238,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       total[0] = above + n_above;
       total[1] = equal + n_equal;
     }
-    cluster.sync();
+    sync();
     for (int r = 0; r < rank; ++r) {
       const int* const t = cluster.map_shared_rank(total, r);
       above += t[0];
@@ -218,7 +256,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       equal += __popc(eq);
     }
     if (sel.bad) code = DSA_DEV_ERR_INVALID_ARG;
-    cluster.sync();   // (what other blocks read of this one's shared memory has been read)
+    sync();   // (what other blocks read of this one's shared memory has been read)
   }
   code = __syncthreads_or(code != 0) ? DSA_DEV_ERR_INVALID_ARG : 0;
   if (tid == 0) put_block_status(p.hdr, code);
@@ -366,7 +404,7 @@ __device__ __forceinline__ void move_small(Move& m, T* ks, T* vs, float* w) {
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) cache_compact_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) cache_compact_kernel(const __grid_constant__ CompactParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
   const int tensors = p.c.v ? 2 : 1, parts = tensors * p.slices + 1;   // of one head of one sequence
   const int64_t units = (int64_t)p.num_seqs * p.c.n_kv * parts;
@@ -417,9 +455,9 @@ cudaError_t launch_evict_select(const SelectParams& call, int sm_count, cudaStre
   if (e != cudaSuccess) return e;
   SelectParams p = call;
   const int64_t units = (int64_t)p.num_seqs * (p.shared ? 1 : p.n_kv);
-  // more blocks to a head while there are SMs for them and two rows to a thread, or to hold its rows' bits
+  // more blocks to a head while there are SMs for them and eight rows to a thread, or to hold its rows' bits
   int blocks = 1;
-  while (blocks < kSelCluster && ((units * blocks < sm_count && p.max_seqlen_k / blocks > 2 * kSelThreads) ||
+  while (blocks < kSelCluster && ((units * blocks < sm_count && p.max_seqlen_k / blocks > 8 * kSelThreads) ||
                                   p.max_seqlen_k / blocks > kSelRows))
     blocks *= 2;
   const int64_t rows = ((int64_t)(p.max_seqlen_k + blocks - 1) / blocks + 31) & ~31;

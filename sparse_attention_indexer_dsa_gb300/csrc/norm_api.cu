@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstring>
 
 #include "dsa_idx.h"
 #include "dsa_status_codes.h"
@@ -14,6 +15,13 @@ using namespace dsa;
 namespace {
 
 int elem_bytes(dsa_dtype_t t) { return t == DSA_DTYPE_BF16 ? 2 : 4; }
+
+// A frequency as turns per position, modulo one, in units of 2^-64.
+uint64_t turns_of(double freq) {
+  double turns = freq * 0.15915494309189533577;   // 1 / (2 pi)
+  turns -= std::floor(turns);
+  return turns >= 1.0 ? 0 : (uint64_t)std::ldexp(turns, 64);
+}
 
 // What forward and backward share; y: outputs, or gradients of the inputs.
 dsa_status_t fill(NormRopeParams* p, const void* q, int64_t q_stride, const void* k, int64_t k_stride, dsa_dtype_t in_dtype,
@@ -44,12 +52,22 @@ dsa_status_t fill(NormRopeParams* p, const void* q, int64_t q_stride, const void
     if ((s = check_stride(&k_stride, n_kv_heads, head_dim, elem_bytes(in_dtype), "k")) != DSA_OK) return s;
     if ((s = check_stride(&k_out_stride, n_kv_heads, head_dim, elem_bytes(out_dtype), "k_out")) != DSA_OK) return s;
   }
-  for (int i = 0; i < rope_dim / 2; ++i) {
-    const double f = inv_freq ? inv_freq[i] : std::pow(rope_base, -2.0 * i / (double)rope_dim);
-    if (!std::isfinite(f)) return fail(DSA_ERR_INVALID_ARG, "inv_freq must be finite");
-    double turns = f * 0.15915494309189533577;   // 1 / (2 pi)
-    turns -= std::floor(turns);
-    p->rope.freq[i] = turns >= 1.0 ? 0 : (uint64_t)std::ldexp(turns, 64);
+  if (inv_freq) {
+    for (int i = 0; i < rope_dim / 2; ++i) {
+      if (!std::isfinite(inv_freq[i])) return fail(DSA_ERR_INVALID_ARG, "inv_freq must be finite");
+      p->rope.freq[i] = turns_of(inv_freq[i]);
+    }
+  } else if (rope_dim > 0) {
+    // (a power of a few hundred nanoseconds for each pair: the last table of the thread is kept)
+    static thread_local double base = 0.0;
+    static thread_local int dim = 0;
+    static thread_local uint64_t table[64];
+    if (base != rope_base || dim != rope_dim) {
+      for (int i = 0; i < rope_dim / 2; ++i) table[i] = turns_of(std::pow(rope_base, -2.0 * i / (double)rope_dim));
+      base = rope_base;
+      dim = rope_dim;
+    }
+    std::memcpy(p->rope.freq, table, sizeof(uint64_t) * (rope_dim / 2));
   }
   p->rope.dim = rope_dim;
   p->rope.interleaved = rope_interleaved ? 1 : 0;

@@ -65,44 +65,70 @@ __device__ __forceinline__ void load4(Raw<BF16>& r, const void* base, int64_t el
     r.v = __ldcs(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + elem));
 }
 
+// A lane's eight elements: its two groups of four, as pairs for packed arithmetic.
+struct Elems {
+  float2 v[4];
+};
+
 template <bool BF16>
-__device__ __forceinline__ void widen4(const Raw<BF16>& r, float* x) {
+__device__ __forceinline__ void widen4(const Raw<BF16>& r, float2* x) {
   if constexpr (BF16) {
-    x[0] = __uint_as_float(r.v.x << 16);
-    x[1] = __uint_as_float(r.v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(r.v.y << 16);
-    x[3] = __uint_as_float(r.v.y & 0xFFFF0000u);
+    x[0] = make_float2(__uint_as_float(r.v.x << 16), __uint_as_float(r.v.x & 0xFFFF0000u));
+    x[1] = make_float2(__uint_as_float(r.v.y << 16), __uint_as_float(r.v.y & 0xFFFF0000u));
   } else {
-    x[0] = r.v.x; x[1] = r.v.y; x[2] = r.v.z; x[3] = r.v.w;
+    x[0] = make_float2(r.v.x, r.v.y);
+    x[1] = make_float2(r.v.z, r.v.w);
   }
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store4(void* base, int64_t elem, const float* x) {
+__device__ __forceinline__ Elems widen(const Raw<BF16> (&r)[2]) {
+  Elems x;
+  widen4<BF16>(r[0], x.v);
+  widen4<BF16>(r[1], x.v + 2);
+  return x;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store4(void* base, int64_t elem, const float2* x) {
   if constexpr (BF16) {
-    __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+    __nv_bfloat162 lo = __floats2bfloat162_rn(x[0].x, x[0].y), hi = __floats2bfloat162_rn(x[1].x, x[1].y);
     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(base) + elem) =
         make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
   } else {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + elem) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + elem) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
   }
 }
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // A lane's eight weights (or shifts); `none` where the call has none.
 template <int D>
-__device__ __forceinline__ void load_w(const void* w, int w_bf16, const Lane<D>& at, float none, float (&o)[8]) {
+__device__ __forceinline__ Elems load_w(const void* w, int w_bf16, const Lane<D>& at, float none) {
+  Elems o;
+  if (!w) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int d = (e < 4 ? at.a : at.b) + (e & 3);
-    if (!w) o[e] = none;
-    else if (w_bf16) o[e] = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(w) + d) << 16);
-    else o[e] = __ldg(reinterpret_cast<const float*>(w) + d);
+    for (int i = 0; i < 4; ++i) o.v[i] = both(none);
+  } else if (w_bf16) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(w);
+    Raw<true> r[2];
+    r[0].v = __ldg(reinterpret_cast<const uint2*>(p + at.a));
+    r[1].v = __ldg(reinterpret_cast<const uint2*>(p + at.b));
+    o = widen<true>(r);
+  } else {
+    const float* p = reinterpret_cast<const float*>(w);
+    Raw<false> r[2];
+    r[0].v = __ldg(reinterpret_cast<const float4*>(p + at.a));
+    r[1].v = __ldg(reinterpret_cast<const float4*>(p + at.b));
+    o = widen<false>(r);
   }
+  return o;
 }
 
-// Sum over the lanes of a row.
+// Sum of a lane's elements, over the lanes of a row.
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ float row_sum(float2 a) {
+  float v = a.x + a.y;
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -110,54 +136,62 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // x -> n; returns 1 / std.
 template <int D, bool LAYER>
-__device__ __forceinline__ float normalise(float (&x)[8], float eps) {
+__device__ __forceinline__ float normalise(Elems& x, float eps) {
   constexpr int LPR = D / 8;
   if (LAYER) {
-    const float mean = row_sum<LPR>(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]))) * (1.f / D);
+    const float2 mean = both(row_sum<LPR>(__fadd2_rn(__fadd2_rn(x.v[0], x.v[1]), __fadd2_rn(x.v[2], x.v[3]))) * (-1.f / D));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] -= mean;
+    for (int i = 0; i < 4; ++i) x.v[i] = __fadd2_rn(x.v[i], mean);
   }
-  float s2 = 0.f;
+  float2 s2 = __fmul2_rn(x.v[0], x.v[0]);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s2 = fmaf(x[e], x[e], s2);
-  const float inv = 1.f / sqrtf(row_sum<LPR>(s2) * (1.f / D) + eps);
+  for (int i = 1; i < 4; ++i) s2 = __ffma2_rn(x.v[i], x.v[i], s2);
+  const float inv = rsqrtf(fmaf(row_sum<LPR>(s2), 1.f / D, eps));
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= inv;
+  for (int i = 0; i < 4; ++i) x.v[i] = __fmul2_rn(x.v[i], both(inv));
   return inv;
 }
 
-// The pairs turned by their angles (with sn negated: back).
-__device__ __forceinline__ void turn(float (&y)[8], const float (&cs)[4], const float (&sn)[4], bool interleaved) {
+// The factors of a lane's pairs: of pairs (e, e + 4) side by side, of pairs (2e, 2e + 1) one by one.
+struct Turn {
+  float cs[4], sn[4];
+};
+
+// The pairs turned by their angles (BACK: against them).
+template <bool BACK>
+__device__ __forceinline__ void turn(Elems& y, const Turn& t, bool interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float a = y[2 * e], b = y[2 * e + 1];
-      y[2 * e] = fmaf(a, cs[e], -b * sn[e]);
-      y[2 * e + 1] = fmaf(b, cs[e], a * sn[e]);
+      const float a = y.v[e].x, b = y.v[e].y, s = BACK ? -t.sn[e] : t.sn[e];
+      y.v[e] = make_float2(fmaf(a, t.cs[e], -b * s), fmaf(b, t.cs[e], a * s));
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float a = y[e], b = y[e + 4];
-      y[e] = fmaf(a, cs[e], -b * sn[e]);
-      y[e + 4] = fmaf(b, cs[e], a * sn[e]);
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = y.v[i], b = y.v[i + 2], c = make_float2(t.cs[2 * i], t.cs[2 * i + 1]);
+      const float2 s = make_float2(t.sn[2 * i], t.sn[2 * i + 1]), m = make_float2(-s.x, -s.y);
+      y.v[i] = __ffma2_rn(a, c, __fmul2_rn(b, BACK ? s : m));
+      y.v[i + 2] = __ffma2_rn(b, c, __fmul2_rn(a, BACK ? m : s));
     }
   }
 }
 
 // cos and sin of a lane's pairs at a position.
 template <int D>
-__device__ __forceinline__ void angles(const RopeTable& r, int pos, const Lane<D>& at, float (&cs)[4], float (&sn)[4]) {
+__device__ __forceinline__ Turn angles(const RopeTable& r, int pos, const Lane<D>& at) {
+  Turn t;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    cs[e] = 1.f;
-    sn[e] = 0.f;
+    t.cs[e] = 1.f;
+    t.sn[e] = 0.f;
     if (at.angle[e] >= 0) {
       const uint64_t turns = (uint64_t)(int64_t)pos * r.freq[at.angle[e]];
       // the upper 32 bits as a signed part of a turn; sincospif takes half turns
-      sincospif((float)(int32_t)(uint32_t)(turns >> 32) * 0x1p-31f, &sn[e], &cs[e]);
+      sincospif((float)(int32_t)(uint32_t)(turns >> 32) * 0x1p-31f, &t.sn[e], &t.cs[e]);
     }
   }
+  return t;
 }
 
 // A warp's share of a token: rows [lo, hi) of queries (kind 0) or keys (kind 1).
@@ -180,16 +214,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
   const int tok = (int)(task / p.parts), part = (int)(task - (int64_t)tok * p.parts);
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const Lane<D> at(p.rope, lane % LPR);
-  float cs[4], sn[4];
+  const int pos = p.rope.dim > 0 ? __ldg(p.pos + tok) : 0;
+  Turn tn;
   bool turned = false;
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind) {
     const Share sh(p, part, kind);
     if (sh.lo >= sh.hi) continue;
-    float w[8], b[8];
-    load_w<D>(p.w[kind], p.w_bf16, at, 1.f, w);
-    if (LAYER || p.b[kind]) load_w<D>(p.b[kind], p.w_bf16, at, 0.f, b);
+    const Elems w = load_w<D>(p.w[kind], p.w_bf16, at, 1.f);
     const bool shift = p.b[kind] != nullptr;
+    Elems b;
+    if (shift) b = load_w<D>(p.b[kind], p.w_bf16, at, 0.f);
     const int64_t x0 = (int64_t)tok * p.x_stride[kind], y0 = (int64_t)tok * p.y_stride[kind];
     for (int h0 = sh.lo + sub; h0 - sub < sh.hi; h0 += kBatch * RPS) {
       Raw<IN> raw[kBatch][2];
@@ -200,28 +235,21 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
         load4<IN>(raw[i][1], p.x[kind], e + at.b);
       }
       if (!turned) {
-        angles<D>(p.rope, p.rope.dim > 0 ? __ldg(p.pos + tok) : 0, at, cs, sn);
+        tn = angles<D>(p.rope, pos, at);
         turned = true;
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (h0 - sub + i * RPS >= sh.hi) break;
-        float x[8];
-        widen4<IN>(raw[i][0], x);
-        widen4<IN>(raw[i][1], x + 4);
+        Elems x = widen<IN>(raw[i]);
         normalise<D, LAYER>(x, p.eps);
-        if (shift) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], w[e], b[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= w[e];
-        }
-        turn(x, cs, sn, p.rope.interleaved);
+        for (int e = 0; e < 4; ++e) x.v[e] = shift ? __ffma2_rn(x.v[e], w.v[e], b.v[e]) : __fmul2_rn(x.v[e], w.v[e]);
+        turn<false>(x, tn, p.rope.interleaved);
         const int h = h0 + i * RPS;
         if (h < sh.hi) {
-          store4<OUT>(p.y[kind], y0 + h * D + at.a, x);
-          store4<OUT>(p.y[kind], y0 + h * D + at.b, x + 4);
+          store4<OUT>(p.y[kind], y0 + h * D + at.a, x.v);
+          store4<OUT>(p.y[kind], y0 + h * D + at.b, x.v + 2);
         }
       }
     }
@@ -236,24 +264,24 @@ constexpr int kBackBatch = 2;
 template <int D, bool IN, bool GRAD, bool LAYER>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_back_kernel(const __grid_constant__ NormRopeBackParams q) {
   constexpr int LPR = D / 8, RPS = 32 / LPR, kRows = kNormThreads / LPR;
-  __shared__ float red[kRows * D];
+  __shared__ __align__(16) float red[kRows * D];
   const NormRopeParams& p = q.f;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const Lane<D> at(p.rope, lane % LPR);
-  float dw[2][8], db[2][8];
+  Elems dw[2], db[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = db[0][e] = db[1][e] = 0.f;
+  for (int e = 0; e < 4; ++e) dw[0].v[e] = dw[1].v[e] = db[0].v[e] = db[1].v[e] = both(0.f);
   const int64_t tasks = (int64_t)p.tokens * p.parts, warps = (int64_t)gridDim.x * (kNormThreads / 32);
   for (int64_t task = (int64_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5); task < tasks; task += warps) {
     const int tok = (int)(task / p.parts), part = (int)(task - (int64_t)tok * p.parts);
-    float cs[4], sn[4];
+    const int pos = p.rope.dim > 0 ? __ldg(p.pos + tok) : 0;
+    Turn tn;
     bool turned = false;
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
       const Share sh(p, part, kind);
       if (sh.lo >= sh.hi) continue;
-      float w[8];
-      load_w<D>(p.w[kind], p.w_bf16, at, 1.f, w);
+      const Elems w = load_w<D>(p.w[kind], p.w_bf16, at, 1.f);
       const int64_t x0 = (int64_t)tok * p.x_stride[kind], g0 = (int64_t)tok * q.dy_stride[kind];
       const int64_t y0 = (int64_t)tok * p.y_stride[kind];
       Raw<IN> raw[kBackBatch][2];
@@ -270,19 +298,15 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_back_kernel(const _
       };
       load(sh.lo + sub);
       if (!turned) {
-        angles<D>(p.rope, p.rope.dim > 0 ? __ldg(p.pos + tok) : 0, at, cs, sn);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sn[e] = -sn[e];
+        tn = angles<D>(p.rope, pos, at);
         turned = true;
       }
       for (int h0 = sh.lo + sub; h0 - sub < sh.hi; h0 += kBackBatch * RPS) {
-        float x[kBackBatch][8], g[kBackBatch][8];
+        Elems x[kBackBatch], g[kBackBatch];
 #pragma unroll
         for (int i = 0; i < kBackBatch; ++i) {
-          widen4<IN>(raw[i][0], x[i]);
-          widen4<IN>(raw[i][1], x[i] + 4);
-          widen4<GRAD>(grad[i][0], g[i]);
-          widen4<GRAD>(grad[i][1], g[i] + 4);
+          x[i] = widen<IN>(raw[i]);
+          g[i] = widen<GRAD>(grad[i]);
         }
         load(h0 + kBackBatch * RPS);   // (the next ones are on their way meanwhile; behind the last: the last once more)
 #pragma unroll
@@ -291,25 +315,28 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_back_kernel(const _
           const int h = h0 + i * RPS;
           const bool live = h < sh.hi;
           const float inv = normalise<D, LAYER>(x[i], p.eps);
-          turn(g[i], cs, sn, p.rope.interleaved);
-          float dot = 0.f, sum = 0.f;
+          turn<true>(g[i], tn, p.rope.interleaved);
+          float2 dot, sum;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < 4; ++e) {
             if (live) {
-              dw[kind][e] = fmaf(g[i][e], x[i][e], dw[kind][e]);
-              if (LAYER) db[kind][e] += g[i][e];
+              dw[kind].v[e] = __ffma2_rn(g[i].v[e], x[i].v[e], dw[kind].v[e]);
+              if (LAYER) db[kind].v[e] = __fadd2_rn(db[kind].v[e], g[i].v[e]);
             }
-            g[i][e] *= w[e];
-            dot = fmaf(g[i][e], x[i][e], dot);
-            if (LAYER) sum += g[i][e];
+            g[i].v[e] = __fmul2_rn(g[i].v[e], w.v[e]);
+            dot = e == 0 ? __fmul2_rn(g[i].v[e], x[i].v[e]) : __ffma2_rn(g[i].v[e], x[i].v[e], dot);
+            if (LAYER) sum = e == 0 ? g[i].v[e] : __fadd2_rn(sum, g[i].v[e]);
           }
-          dot = row_sum<LPR>(dot) * (1.f / D);
-          if (LAYER) sum = row_sum<LPR>(sum) * (1.f / D);
+          const float2 md = both(row_sum<LPR>(dot) * (-1.f / D));
+          if (LAYER) sum = both(row_sum<LPR>(sum) * (-1.f / D));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[i][e] = (g[i][e] - (LAYER ? fmaf(x[i][e], dot, sum) : x[i][e] * dot)) * inv;
+          for (int e = 0; e < 4; ++e) {
+            const float2 t = __ffma2_rn(x[i].v[e], md, g[i].v[e]);
+            g[i].v[e] = __fmul2_rn(LAYER ? __fadd2_rn(t, sum) : t, both(inv));
+          }
           if (live) {
-            store4<IN>(p.y[kind], y0 + h * D + at.a, g[i]);
-            store4<IN>(p.y[kind], y0 + h * D + at.b, g[i] + 4);
+            store4<IN>(p.y[kind], y0 + h * D + at.a, g[i].v);
+            store4<IN>(p.y[kind], y0 + h * D + at.b, g[i].v + 2);
           }
         }
       }
@@ -319,10 +346,10 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_back_kernel(const _
   const int row = threadIdx.x / LPR;
 #pragma unroll
   for (int j = 0; j < (LAYER ? 4 : 2); ++j) {
-    const float(&v)[8] = j < 2 ? dw[j & 1] : db[j & 1];
+    const Elems& v = j < 2 ? dw[j & 1] : db[j & 1];
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) red[row * D + (e < 4 ? at.a : at.b) + (e & 3)] = v[e];
+    store4<false>(red, row * D + at.a, v.v);
+    store4<false>(red, row * D + at.b, v.v + 2);
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += kNormThreads) {
       float s = 0.f;

@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
   extern __shared__ __align__(128) uint8_t ring[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t = lane & 3, g = lane >> 2;
   const uint32_t sring = smem_u32(ring) + warp * kSteps * kStepBytes;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the tiles' kernel, where the call has one)
   int code = 0;
   // Prefixes that fall make rows count for several sequences, or for none: nothing is computed.
   bool falls = false;

@@ -39,6 +39,7 @@ constexpr int kGroups = 64;            // sequences are counted in this many gro
 constexpr int kHalf = kWeighCols / 2;  // columns of a product and of a hand-over
 constexpr int kBiasRing = 4;
 constexpr int kUnitCost = 2;           // what a unit's change of keys counts beside its query tiles
+constexpr int kMinPart = 2 * kUnitCost;   // length of a block's part, at least
 // barriers (halves: 2 * stream + half)
 enum { K_FULL = 0, K_EMPTY = 2, S_FULL = 4, S_EMPTY = 8, B_FULL = 12, B_EMPTY = B_FULL + kBiasRing, DRAIN = B_EMPTY + kBiasRing,
        Q_FULL = DRAIN + 2, kMaxStages = 4, Q_EMPTY = Q_FULL + kMaxStages, kBars = Q_EMPTY + kMaxStages };
@@ -47,7 +48,8 @@ enum { K_FULL = 0, K_EMPTY = 2, S_FULL = 4, S_EMPTY = 8, B_FULL = 12, B_EMPTY = 
 // tiles and kUnitCost before them.  The same in every block.
 struct Row {
   long long tab[kGroups + 1];   // where each group of sequences begins
-  long long end;                // ... and all end
+  long long each;               // a part's length: the first `more` are longer by one
+  int parts, more;
   // a block's part begins in this unit, `off` behind its begin
   int d, h, kt, off;
 };
@@ -91,7 +93,10 @@ struct DocUnits {
   }
 };
 
-// Lays the units out in a row; the whole block calls.
+// Where part i begins.
+__device__ __forceinline__ long long part_begin(const Row& r, int i) { return i * r.each + min(i, r.more); }
+
+// Lays the units out in a row and divides it among the call's blocks; the whole block calls.
 __device__ __forceinline__ void lay_out(const WeighParams& p, Row* row) {
   const int tid = threadIdx.x, gsz = (p.num_seqs + kGroups - 1) / kGroups;
   bool falls = false;   // prefixes that fall: nothing is computed
@@ -112,12 +117,18 @@ __device__ __forceinline__ void lay_out(const WeighParams& p, Row* row) {
     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if ((tid & 31) >= o) incl += y;
   }
-  if (tid == 31) row->end = incl;
+  if (tid == 31) row->tab[kGroups] = incl;
   __syncthreads();
-  const long long before = incl - mine + (tid >= 32 ? row->end : 0);
+  const long long before = incl - mine + (tid >= 32 ? row->tab[kGroups] : 0);
   __syncthreads();
   if (tid < kGroups) row->tab[tid] = before;
-  if (tid == kGroups - 1) row->tab[kGroups] = row->end = before + mine;
+  if (tid == kGroups - 1) {
+    const long long end = before + mine, most = (end + kMinPart - 1) / kMinPart;
+    row->tab[kGroups] = end;
+    row->parts = most < p.tile_blocks ? max((int)most, 1) : p.tile_blocks;
+    row->each = end / row->parts;
+    row->more = (int)(end - row->each * row->parts);
+  }
   __syncthreads();
 }
 
@@ -148,10 +159,6 @@ __device__ __forceinline__ void locate(const WeighParams& p, Row* row, long long
     row->off = (int)rem;
     return;
   }
-}
-
-__device__ __forceinline__ long long part_begin(long long end, int block, int blocks) {
-  return (long long)(((unsigned long long)end * (unsigned)block) / (unsigned)blocks);
 }
 
 // A piece of a unit in a block's part.
@@ -244,7 +251,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
   }
   Row* const row = reinterpret_cast<Row*>(smem + L::kOffRow);
   lay_out(p, row);
-  const long long begin = part_begin(row->end, blockIdx.x, gridDim.x), end = part_begin(row->end, blockIdx.x + 1, gridDim.x);
+  const long long begin = (int)blockIdx.x < row->parts ? part_begin(*row, blockIdx.x) : 0;
+  const long long end = (int)blockIdx.x < row->parts ? part_begin(*row, blockIdx.x + 1) : 0;
   if (tid == 0) {
     row->d = row->h = row->kt = row->off = 0;
     if (begin < end) locate(p, row, begin);
@@ -507,6 +515,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
     }
     __syncwarp();
   }
+  // The steps' kernel, whose rows are those of other sequences, is over when this one is; the next may begin.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
   if (tid == 0) put_status(p, p.step_blocks + blockIdx.x, *status);
@@ -516,13 +527,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
 __global__ void __launch_bounds__(kWeighKeys) weigh_join_kernel(const __grid_constant__ WeighParams p) {
   __shared__ Row row;
   lay_out(p, &row);
-  const int parts = p.tile_blocks, b = blockIdx.x + 1;
-  const long long at = part_begin(row.end, b, parts);
-  if (part_begin(row.end, b - 1, parts) == at || at >= row.end) return;   // (an empty part before it divides nothing)
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the tiles' kernel is over
+  const int b = blockIdx.x + 1;
+  if (b >= row.parts) return;
+  const long long at = part_begin(row, b), before = part_begin(row, b - 1);
   if (threadIdx.x == 0) locate(p, &row, at);
   __syncthreads();
   const long long begin = at - row.off;
-  if (row.off == 0 || part_begin(row.end, b - 1, parts) > begin) return;   // not divided, or by an end before it too
+  if (row.off == 0 || before > begin) return;   // not divided, or by an end before it too
   const DocUnits x(p, row.d);
   const long long end = begin + x.length(row.kt);
   const int key = row.kt * kWeighKeys + threadIdx.x;
@@ -530,11 +542,7 @@ __global__ void __launch_bounds__(kWeighKeys) weigh_join_kernel(const __grid_con
   const int64_t r = cache_row(p.c, row.d, key, row.h);
   if (r < 0) return;
   float total = p.part[((int64_t)(b - 1) * 2 + 1) * kWeighKeys + threadIdx.x];
-  for (int i = b; i < parts; ++i) {
-    const long long from = part_begin(row.end, i, parts);
-    if (from >= end) break;
-    if (part_begin(row.end, i + 1, parts) > from) total += p.part[((int64_t)i * 2) * kWeighKeys + threadIdx.x];
-  }
+  for (int i = b; i < row.parts && part_begin(row, i) < end; ++i) total += p.part[((int64_t)i * 2) * kWeighKeys + threadIdx.x];
   p.weights[r] = key >= x.P0 ? total : p.weights[r] + total;
 }
 
@@ -550,10 +558,22 @@ cudaError_t launch_tiles(const WeighParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
   }
-  kernel<<<p.tile_blocks, kTileThreads, Layout<D>::kSmem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.tile_blocks == 1) return e;
-  weigh_join_kernel<<<p.tile_blocks - 1, kWeighKeys, 0, stream>>>(p);
-  return cudaGetLastError();
+  // each may begin while the kernel before it is ending
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(p.tile_blocks);
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = Layout<D>::kSmem;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess || p.tile_blocks == 1) return e;
+  cfg.gridDim = dim3(p.tile_blocks - 1);
+  cfg.blockDim = dim3(kWeighKeys);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, weigh_join_kernel, p);
 }
 
 }  // namespace weigh

@@ -13,6 +13,7 @@ from . import _abi
 from .paged import _arg, _call, _error, _tokens
 
 _NORM = {"rms": _abi.DSA_NORM_RMS, "layer": _abi.DSA_NORM_LAYER}
+_WEIGHTS = ("q_weight", "k_weight", "q_bias", "k_bias")
 _DTYPE = {torch.float32: _abi.DSA_DTYPE_F32, torch.bfloat16: _abi.DSA_DTYPE_BF16}
 
 
@@ -27,39 +28,44 @@ class NormRopeGrads(NamedTuple):
 
 
 def _inputs(q, k, positions, weights, norm, rope_dim, inv_freq):
-    """Checks that forward and backward share."""
+    """Checks that forward and backward share; what they hand on."""
     if q.dim() != 3:
         raise ValueError("q must be [tokens, n_heads, head_dim]")
-    T, H, D = q.shape
-    dev = q.device
+    shape, dev, dt = q.shape, q.device, q.dtype
+    T, H, D = shape
     if not q.is_cuda:
         raise ValueError("q must live on the CUDA device")
     if norm not in _NORM:
         raise ValueError(f"norm must be 'rms' or 'layer', not {norm!r}")
-    Hk = 0
+    qp, qst = _tokens(q, "q", dev, _DTYPE, H, D)
+    kp, kst, Hk = None, 0, 0
     if k is not None:
         if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D:
             raise ValueError(f"k must be [{T}, n_kv_heads, {D}], not {tuple(k.shape)}")
-        if k.dtype != q.dtype:
-            raise ValueError("q and k must have one dtype")
         Hk = k.shape[1]
-    qa, ka = _tokens(q, "q", dev, _DTYPE, H, D), _tokens(k, "k", dev, _DTYPE, Hk, D)
+        kp, kst = _tokens(k, "k", dev, (dt,), Hk, D)
     R = D if rope_dim is None else rope_dim
-    if R and positions is None:
-        raise ValueError("positions are needed unless rope_dim is 0")
-    pos = _arg(positions, "positions", dev, torch.int32, (T,)) if R else None
-    wt = next((w.dtype for w in weights if w is not None), torch.float32)
-    if wt not in _DTYPE:
-        raise ValueError(f"weights: unsupported dtype {wt}")
-    if k is None and any(w is not None for w in weights[1::2]):
-        raise ValueError("k_weight and k_bias belong to k")
-    wp = [_arg(w, n, dev, wt, (D,)) for w, n in zip(weights, ("q_weight", "k_weight", "q_bias", "k_bias"))]
+    pos = None
+    if R:
+        if positions is None:
+            raise ValueError("positions are needed unless rope_dim is 0")
+        pos = _arg(positions, "positions", dev, torch.int32, (T,))
+    wt, wp = None, [None, None, None, None]
+    for i, w in enumerate(weights):
+        if w is not None:
+            if wt is None:
+                wt = w.dtype
+                if wt not in _DTYPE:
+                    raise ValueError(f"weights: unsupported dtype {wt}")
+            if i & 1 and k is None:
+                raise ValueError("k_weight and k_bias belong to k")
+            wp[i] = _arg(w, _WEIGHTS[i], dev, wt, (D,))
     freq = None
     if inv_freq is not None:
         if len(inv_freq) != R // 2:
             raise ValueError(f"inv_freq must have rope_dim / 2 = {R // 2} values")
         freq = (ctypes.c_double * max(1, R // 2))(*[float(f) for f in inv_freq])
-    return dev, T, H, Hk, D, qa, ka, R, pos, wp, _DTYPE[wt], freq
+    return shape, dev, dt, Hk, (qp, qst, kp, kst), R, pos, wp, 0 if wt is None else _DTYPE[wt], freq
 
 
 def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -78,28 +84,32 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[to
     or by the rope_dim / 2 host values inv_freq.  Returns (q_out, k_out or None)
     in out_dtype (default: q's); `out` is such a pair to write into, and may be
     (q, k) itself.  No gradient is recorded: norm_rope_backward gives it."""
-    weights = (q_weight, k_weight, q_bias, k_bias)
-    dev, T, H, Hk, D, (qp, qst), (kp, kst), R, pos, wp, wt, freq = _inputs(q, k, positions, weights, norm, rope_dim, inv_freq)
+    shape, dev, dt, Hk, rows, R, pos, wp, wt, freq = _inputs(q, k, positions, (q_weight, k_weight, q_bias, k_bias), norm,
+                                                            rope_dim, inv_freq)
+    T, H, D = shape
     if out is None:
-        dt = q.dtype if out_dtype is None else out_dtype
-        q_out = torch.empty(q.shape, dtype=dt, device=dev)
-        k_out = None if k is None else torch.empty(k.shape, dtype=dt, device=dev)
+        ot = dt if out_dtype is None else out_dtype
+        if ot not in _DTYPE:
+            raise ValueError(f"out_dtype: unsupported dtype {ot}")
+        q_out, k_out = torch.empty(shape, dtype=ot, device=dev), None
+        qo, qost, ko, kost = q_out.data_ptr() or None, 0, None, 0
+        if k is not None:
+            k_out = torch.empty(k.shape, dtype=ot, device=dev)
+            ko = k_out.data_ptr() or None
     else:
         q_out, k_out = out
-        dt = q_out.dtype
-        if out_dtype not in (None, dt):
+        ot = q_out.dtype
+        if out_dtype not in (None, ot):
             raise ValueError("out has another dtype than out_dtype")
         if (k is None) != (k_out is None):
             raise ValueError("out must be a pair (q_out, k_out), k_out None where k is")
-        if q_out.shape != q.shape or (k is not None and (k_out.shape != k.shape or k_out.dtype != dt)):
-            raise ValueError("out must have the shapes of q and k and one dtype")
-    if dt not in _DTYPE:
-        raise ValueError(f"out: unsupported dtype {dt}")
-    qo, qost = _tokens(q_out, "q_out", dev, _DTYPE, H, D)
-    ko, kost = _tokens(k_out, "k_out", dev, _DTYPE, Hk, D)
+        if q_out.shape != shape or (k is not None and k_out.shape != k.shape):
+            raise ValueError("out must have the shapes of q and k")
+        qo, qost = _tokens(q_out, "q_out", dev, _DTYPE, H, D)
+        ko, kost = _tokens(k_out, "k_out", dev, (ot,), Hk, D)
     code = _call(_abi.load().dsa_idx_norm_rope, dev, (
-        qp, qst, kp, kst, _DTYPE[q.dtype], *wp, wt, _NORM[norm], eps, pos, T, H, Hk, D, R, rope_base, freq,
-        int(rope_interleaved), qo, qost, ko, kost, _DTYPE[dt]))
+        *rows, _DTYPE[dt], *wp, wt, _NORM[norm], eps, pos, T, H, Hk, D, R, rope_base, freq, int(rope_interleaved), qo, qost,
+        ko, kost, _DTYPE[ot]))
     if code:
         raise _error(code, "dsa_idx_norm_rope")
     return q_out, k_out
@@ -126,29 +136,33 @@ def norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: 
     Returns gradients of q and k in their dtype, and in fp32 [head_dim] those of
     the weights (summed over tokens and heads; given or not) and, with norm
     "layer", of the biases."""
-    dev, T, H, Hk, D, (qp, qst), (kp, kst), R, pos, wp, wt, freq = _inputs(
-        q, k, positions, (q_weight, k_weight, None, None), norm, rope_dim, inv_freq)
+    shape, dev, dt, Hk, rows, R, pos, wp, wt, freq = _inputs(q, k, positions, (q_weight, k_weight, None, None), norm, rope_dim,
+                                                            inv_freq)
+    T, H, D = shape
+    gt = dq_out.dtype
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out must both be given or both be None")
-    if dq_out.shape != q.shape or (k is not None and (dk_out.shape != k.shape or dk_out.dtype != dq_out.dtype)):
-        raise ValueError("dq_out and dk_out must have the shapes of q and k and one dtype")
+    if dq_out.shape != shape or (k is not None and dk_out.shape != k.shape):
+        raise ValueError("dq_out and dk_out must have the shapes of q and k")
     gq, gqst = _tokens(dq_out, "dq_out", dev, _DTYPE, H, D)
-    gk, gkst = _tokens(dk_out, "dk_out", dev, _DTYPE, Hk, D)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dk = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=dev)
-    rows = torch.empty((4, D), dtype=torch.float32, device=dev)
-    dqw, dkw, dqb, dkb = rows.unbind(0)
-    if k is None:
-        dkw = dkb = None
-    if norm != "layer":
-        dqb = dkb = None
+    gk, gkst = _tokens(dk_out, "dk_out", dev, (gt,), Hk, D)
+    dq, dk, dkp = torch.empty(shape, dtype=dt, device=dev), None, None
+    if k is not None:
+        dk = torch.empty(k.shape, dtype=dt, device=dev)
+        dkp = dk.data_ptr() or None
+    # gradients of the weights: rows of one tensor (of queries and keys, then of their biases)
+    n, kinds = (2 if norm == "layer" else 1), (1 if k is None else 2)
+    sums = torch.empty((n * kinds, D), dtype=torch.float32, device=dev)
+    at, step, lay = sums.data_ptr(), 4 * D, norm == "layer"
+    sp = (at, at + step if k is not None else None, at + kinds * step if lay else None,
+          at + 3 * step if lay and k is not None else None)
     if ws is None:
         ws = norm_rope_workspace(D, dev)
     code = _call(_abi.load().dsa_idx_norm_rope_backward, dev, (
-        gq, gqst, gk, gkst, _DTYPE[dq_out.dtype], qp, qst, kp, kst, _DTYPE[q.dtype], wp[0], wp[1], wt, _NORM[norm], eps, pos,
-        T, H, Hk, D, R, rope_base, freq, int(rope_interleaved), dq.data_ptr() or None, 0,
-        None if dk is None else dk.data_ptr() or None, 0, *(None if t is None else t.data_ptr() for t in (dqw, dkw, dqb, dkb)),
-        _arg(ws, "ws", dev, torch.uint8), ws.numel()))
+        gq, gqst, gk, gkst, _DTYPE[gt], *rows, _DTYPE[dt], wp[0], wp[1], wt, _NORM[norm], eps, pos, T, H, Hk, D, R, rope_base,
+        freq, int(rope_interleaved), dq.data_ptr() or None, 0, dkp, 0, *sp, _arg(ws, "ws", dev, torch.uint8), ws.numel()))
     if code:
         raise _error(code, "dsa_idx_norm_rope_backward")
-    return NormRopeGrads(dq, dk, dqw, dkw, dqb, dkb)
+    it = iter(sums.unbind(0))
+    return NormRopeGrads(dq, dk, next(it), None if k is None else next(it), next(it) if lay else None,
+                         next(it) if lay and k is not None else None)
