@@ -11,10 +11,15 @@
 // equal ones stay, each block writes its rows behind those of the blocks before.
 //
 // cache_compact: row j takes the place of row kept[j], kept ascending, so that
-// kept[j] >= j: a block moves a part of each row of one head in ascending
-// chunks.  A chunk's rows are read whole before any of them is written, and
+// kept[j] >= j: a cluster of 1 to 8 blocks moves the rows of one head in ascending
+// chunks.  A chunk is read whole by all its blocks before any of them writes, and
 // the rows that later chunks read lie behind everything written before them, so
-// reads run several chunks ahead.
+// reads run two chunks ahead.  One thread looks a row up for all that copy its
+// pieces: at 16 bytes a look-up the instructions, not the memory, took the time.  The
+// rows of 16 sequences, 2048 of some 2200, 8 heads, MXFP8: 27 us = 76 % of the copy
+// rate; 16384 of up to 65536 BF16 rows of 5 sequences: 116 us = 86 %.  (5 stages and
+// two blocks to an SM 28 and 164 us; blocks with a part of each row, no barrier between
+// them and a look-up to every piece 39 and 172.)
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -47,21 +52,44 @@ struct Select {
   const SelectParams& p;
   int d, h, S;
   bool bad = false;
-  __device__ __forceinline__ uint32_t at(int i) {   // of row i
-    if (i < p.sinks || i >= S - p.recent) return kMust;
-    const int page = __ldg(p.table + (int64_t)d * p.max_pages + (i >> p.page_shift));
-    if ((unsigned)page >= (unsigned)p.num_pages) {
-      bad = true;
-      return 0u;
+  // Bits of U rows, kSelThreads apart from row i on; rows from `end` on are not looked at.  The rows' loads
+  // go together: their pages, then head by head their weights.
+  template <int U>
+  __device__ __forceinline__ void load(int i, int end, uint32_t (&b)[U]) {
+    const float* w[U];
+    int page[U];
+    float v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int r = i + k * kSelThreads;
+      page[k] = r < end ? __ldg(p.table + (int64_t)d * p.max_pages + (r >> p.page_shift)) : -1;
     }
-    const int slot = i & ((1 << p.page_shift) - 1);
-    const float* w = p.weights + (((int64_t)page * p.n_kv + h) << p.page_shift) + slot;
-    float v = __ldg(w);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int r = i + k * kSelThreads;
+      const bool there = (unsigned)page[k] < (unsigned)p.num_pages;
+      const bool must = r < p.sinks || r >= S - p.recent;
+      if (r < end && !must && !there) bad = true;
+      b[k] = must ? kMust : 0u;   // (a row on no page: as NaN)
+      w[k] = there && !must ? p.weights + (((int64_t)page[k] * p.n_kv + h) << p.page_shift) + (r & ((1 << p.page_shift) - 1)) : nullptr;
+      v[k] = w[k] ? __ldg(w[k]) : 0.f;
+    }
     if (p.shared) {   // the heads' sum, one after the other
-#pragma unroll 8
-      for (int k = 1; k < p.n_kv; ++k) v += __ldg(w + ((int64_t)k << p.page_shift));
+#pragma unroll 4
+      for (int x = 1; x < p.n_kv; ++x) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) v[k] += w[k] ? __ldg(w[k] + ((int64_t)x << p.page_shift)) : 0.f;
+      }
     }
-    return weight_bits(v);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (w[k]) b[k] = weight_bits(v[k]);
+    }
+  }
+  __device__ __forceinline__ uint32_t at(int i) {   // of row i
+    uint32_t b[1];
+    load<1>(i, S, b);
+    return b[0];
   }
 };
 
@@ -156,16 +184,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     for (int step = 0; step < 3; ++step) {
       const int shift = step == 0 ? 20 : (step == 1 ? 8 : 0), bins = step == 2 ? kLastBins : kBins;
       uint32_t* const count = hist[step];
-      constexpr int U = 8;   // rows of a thread whose loads go together
+      constexpr int U = 4;   // rows of a thread whose loads go together
       for (int i0 = 0; i0 < n; i0 += U * kSelThreads) {
         uint32_t b[U];
+        if (step == 0 || !cached) sel.load<U>(lo + i0 + tid, lo + n, b);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
           const int i = i0 + k * kSelThreads + tid;
-          b[k] = 0;
-          if (i < n) {
-            b[k] = step == 0 ? sel.at(lo + i) : value(i);
-            if (cached && step == 0) bits[i] = b[k];
+          if (cached && i < n) {
+            if (step == 0) bits[i] = b[k];
+            else b[k] = bits[i];
           }
         }
 #pragma unroll
@@ -265,171 +293,153 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 // ---------------------------------------------------------------- moving
 
 constexpr int kMoveThreads = 256;
-constexpr int kMovePer = 2;              // 16-byte pieces of a thread in a chunk
+constexpr int kMovePer = 4;                                          // 16-byte pieces of a thread in a chunk
 constexpr int kMoveChunkBytes = kMoveThreads * kMovePer * 16;
-constexpr int kMoveStages = 6;
+constexpr int kMoveStages = 3;
+constexpr int kMoveRows = kMoveChunkBytes / 64;                      // of a chunk, at most: one to a thread
+constexpr int kMoveCluster = 8;                                      // blocks of a cluster, at most
+static_assert(kMoveRows <= kMoveThreads, "a thread to a row");
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// One head of one sequence.
-struct Move {
-  const CompactParams& p;
-  int d, h, n;
-  const int32_t* kept;
-  bool bad = false;
-  __device__ __forceinline__ int entry(int j) { return j < n ? __ldg(kept + j) : -1; }
-  // Page of position i; -1: not one of the table's.
-  __device__ __forceinline__ int page(int i) {
-    const int pi = i >> p.c.page_shift;
-    return i >= 0 && pi < p.c.max_pages ? __ldg(p.c.table + (int64_t)d * p.c.max_pages + pi) : -1;
-  }
-  // Cache row of position i on its page, ~0: there is none (reported).
-  __device__ __forceinline__ uint32_t row(int i, int page) {
-    if ((unsigned)page >= (unsigned)p.c.num_pages) {
-      bad = true;
-      return ~0u;
-    }
-    return (uint32_t)((((int64_t)page * p.c.n_kv + h) << p.c.page_shift) + (i & ((1 << p.c.page_shift) - 1)));
-  }
-  // Row that row j (< n) comes from, its entry being i; ~0: none, or already there.
-  __device__ __forceinline__ uint32_t source(int j, int i, int page) {
-    if (i < j) {   // not ascending
-      bad = true;
-      return ~0u;
-    }
-    const uint32_t r = row(i, page);
-    return i == j ? ~0u : r;
-  }
+// Shared memory of a block: the chunks' rows, the cache rows that they come from and go to, their weights
+// and the words that hold their scales.
+struct MoveRing {
+  uint4 rows[kMoveStages][kMoveChunkBytes / 16];
+  uint32_t from[kMoveStages + 1][kMoveRows], to[kMoveStages + 1][kMoveRows];
+  uint32_t weight[kMoveStages + 1][kMoveRows], scale[kMoveStages + 1][kMoveRows];
 };
 
-// A part of each row of keys or values.  Looking up where a row is takes two dependent loads: a chunk's
-// entries are requested three steps before its copies, its pages one.
-__device__ __forceinline__ void move_rows(Move& m, uint8_t* base, int row_bytes, int bytes, int off, uint8_t* ring, uint32_t sring) {
-  const int tid = threadIdx.x, pieces = bytes / 16, rows = kMoveThreads / pieces, sub = tid / pieces;
-  off += (tid % pieces) * 16;
-  const int chunks = (m.n + rows * kMovePer - 1) / (rows * kMovePer);
-  auto j_of = [&](int c, int i) { return (c * kMovePer + i) * rows + sub; };
-  int ea[kMovePer], eb[kMovePer], pb[kMovePer], pt[kMovePer];   // entries of chunk f + 1, entries and pages of f; pages written to
-#pragma unroll
-  for (int i = 0; i < kMovePer; ++i) {
-    eb[i] = m.entry(j_of(0, i));
-    ea[i] = m.entry(j_of(1, i));
-    pt[i] = m.page(j_of(0, i));
+// What the cluster's threads have read before it is read before any writes behind it, and the block's shared
+// memory is visible to it.  What has been read is in shared memory or registers by then, so nothing has to
+// be made visible to other blocks: a release would wait for the last chunk's writes (some 1 us a chunk).
+__device__ __forceinline__ void move_barrier(int blocks) {
+  if (blocks > 1) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
   }
-#pragma unroll
-  for (int i = 0; i < kMovePer; ++i) pb[i] = m.page(eb[i]);
-  uint32_t moves = 0;   // a bit for each piece in the ring
-  for (int c = 1 - kMoveStages; c < chunks; ++c) {
-    const int f = c + kMoveStages - 1, stage = f % kMoveStages;
-    if (f < chunks) {
-#pragma unroll
-      for (int i = 0; i < kMovePer; ++i) {
-        const int j = j_of(f, i);
-        const uint32_t src = j < m.n ? m.source(j, eb[i], pb[i]) : ~0u;
-        if (src != ~0u) {
-          cp_async_16(sring + stage * kMoveChunkBytes + (i * kMoveThreads + tid) * 16, base + (size_t)src * row_bytes + off);
-          moves |= 1u << (stage * kMovePer + i);
-        }
-        eb[i] = ea[i];
-        pb[i] = m.page(eb[i]);
-        ea[i] = m.entry(j_of(f + 2, i));
+  __syncthreads();
+}
+
+// Keys or values of one head of one sequence, with their scales (T, null: none) and, with the keys, the
+// rows' weights.  Thread t looks up row t of a chunk: the rows' entries are requested two steps before they
+// are looked up, their pages one; then a chunk's rows are requested, two chunks before they are written.
+template <class T>
+__device__ __forceinline__ bool move_head(const CompactParams& p, int d, int h, int n, uint8_t* base, T* scales, float* weights,
+                                          int blocks, int rank, MoveRing* ring) {
+  const int tid = threadIdx.x, pieces = p.row_bytes / 16, rows = kMoveChunkBytes / p.row_bytes;
+  const int32_t* const kept = p.kept + ((int64_t)d * p.heads + (p.heads > 1 ? h : 0)) * p.width;
+  const int32_t* const table = p.c.table + (int64_t)d * p.c.max_pages;
+  const int chunk = blocks * rows, chunks = (n + chunk - 1) / chunk, mask = (1 << p.c.page_shift) - 1;
+  bool bad = false;
+  const int j0 = rank * rows + tid;   // this thread's row of the first chunk
+  auto entry = [&](int j) { return tid < rows && j < n ? __ldg(kept + j) : -1; };
+  auto page = [&](int i) { return i >= 0 && (i >> p.c.page_shift) < p.c.max_pages ? __ldg(table + (i >> p.c.page_shift)) : -1; };
+  auto row = [&](int i, int page) {   // cache row of position i on its page, ~0: there is none (reported)
+    if ((unsigned)page < (unsigned)p.c.num_pages) return (uint32_t)((((int64_t)page * p.c.n_kv + h) << p.c.page_shift) + (i & mask));
+    bad = true;
+    return ~0u;
+  };
+  int e0 = entry(j0), e1 = entry(j0 + chunk), before = j0 > 0 ? entry(j0 - 1) : -1, before1 = entry(j0 + chunk - 1);
+  int pf = page(e0), pt = page(tid < rows && j0 < n ? j0 : -1);
+  // Looks up this thread's row of chunk f, and requests what the next ones need.
+  auto look_up = [&](int f) {
+    const int j = j0 + f * chunk, slot = f % (kMoveStages + 1);
+    uint32_t from = ~0u, to = ~0u;
+    if (tid < rows && j < n) {
+      if (e0 < j || e0 <= before) {   // not ascending
+        bad = true;
+      } else {
+        from = row(e0, pf);
+        to = row(j, pt);
+        if (from == ~0u || to == ~0u || e0 == j) from = to = ~0u;   // nothing to move
       }
     }
-    cp_commit();
-    if (c < 0) continue;
-    cp_wait<kMoveStages - 1>();
-    __syncthreads();              // the whole chunk has been read
-    const int at = c % kMoveStages;
+    if (from != ~0u) {
+      // (a scale of one or two bytes comes with the word that it is in)
+      if (scales) cp_async_4(smem_u32(&ring->scale[slot][tid]), reinterpret_cast<const uint32_t*>(scales) + from * sizeof(T) / 4);
+      if (weights) cp_async_4(smem_u32(&ring->weight[slot][tid]), weights + from);
+    }
+    if (tid < rows) {
+      ring->from[slot][tid] = from;
+      ring->to[slot][tid] = to;
+    }
+    e0 = e1;
+    before = before1;
+    pf = page(e0);
+    pt = page(tid < rows && j + chunk < n ? j + chunk : -1);
+    e1 = entry(j + 2 * chunk);
+    before1 = entry(j + 2 * chunk - 1);
+  };
+  look_up(0);
+  __syncthreads();
+  for (int c = 1 - kMoveStages; c < chunks; ++c) {
+    const int f = c + kMoveStages - 1;
+    if (f < chunks) {
+      const uint32_t dst = smem_u32(&ring->rows[f % kMoveStages][tid]);
 #pragma unroll
-    for (int i = 0; i < kMovePer; ++i) {
-      const uint32_t bit = 1u << (at * kMovePer + i);
-      const int page = pt[i];
-      pt[i] = m.page(j_of(c + 1, i));
-      if (!(moves & bit)) continue;
-      moves ^= bit;
-      const uint32_t dst = m.row(j_of(c, i), page);
-      if (dst != ~0u)
-        *reinterpret_cast<uint4*>(base + (size_t)dst * row_bytes + off) =
-            *reinterpret_cast<const uint4*>(ring + at * kMoveChunkBytes + (i * kMoveThreads + tid) * 16);
+      for (int s = 0; s < kMovePer; ++s) {
+        const int x = s * kMoveThreads + tid;
+        const uint32_t from = ring->from[f % (kMoveStages + 1)][x / pieces];
+        if (from != ~0u) cp_async_16(dst + s * kMoveThreads * 16, base + (size_t)from * p.row_bytes + (x & (pieces - 1)) * 16);
+      }
+    }
+    cp_commit();        // (with the scales and weights that the last look-up requested)
+    look_up(f + 1);
+    cp_wait<kMoveStages - 1>();
+    move_barrier(blocks);   // the whole chunk c has been read
+    if (c < 0) continue;
+#pragma unroll
+    for (int s = 0; s < kMovePer; ++s) {
+      const int x = s * kMoveThreads + tid;
+      const uint32_t dst = ring->to[c % (kMoveStages + 1)][x / pieces];
+      if (dst != ~0u) *reinterpret_cast<uint4*>(base + (size_t)dst * p.row_bytes + (x & (pieces - 1)) * 16) = ring->rows[c % kMoveStages][x];
+    }
+    const int slot = c % (kMoveStages + 1);
+    const uint32_t to = tid < rows ? ring->to[slot][tid] : ~0u;
+    if (to != ~0u) {
+      if (scales) {
+        const uint32_t from = ring->from[slot][tid], word = ring->scale[slot][tid];
+        scales[to] = (T)(word >> (from * sizeof(T) % 4 * 8));
+      }
+      if (weights) weights[to] = __uint_as_float(ring->weight[slot][tid]);
     }
   }
   cp_wait<0>();
+  __syncthreads();
+  return bad;
 }
 
-// Scales and weights: a chunk of four rows a thread at a time.  Its elements have been read when every
-// thread has reached the barrier, and the next chunk reads behind what this one writes.
-template <class T>
-__device__ __forceinline__ void move_small(Move& m, T* ks, T* vs, float* w) {
-  constexpr int U = 4;
-  for (int j0 = 0; j0 < m.n; j0 += U * kMoveThreads) {
-    int e[U], before[U], page[U];
-    uint32_t src[U];
-    T k[U], v[U];
-    float x[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int j = j0 + i * kMoveThreads + threadIdx.x;
-      e[i] = m.entry(j);
-      before[i] = j > 0 ? m.entry(j - 1) : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) page[i] = m.page(e[i]);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int j = j0 + i * kMoveThreads + threadIdx.x;
-      src[i] = j < m.n ? m.source(j, e[i], page[i]) : ~0u;
-      if (j < m.n && e[i] <= before[i]) m.bad = true;
-      page[i] = m.page(j < m.n ? j : -1);
-      if (src[i] != ~0u) {
-        if (ks) k[i] = *reinterpret_cast<volatile T*>(ks + src[i]);
-        if (vs) v[i] = *reinterpret_cast<volatile T*>(vs + src[i]);
-        if (w) x[i] = *reinterpret_cast<volatile float*>(w + src[i]);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (src[i] == ~0u) continue;
-      const uint32_t dst = m.row(j0 + i * kMoveThreads + threadIdx.x, page[i]);
-      if (dst == ~0u) continue;
-      if (ks) ks[dst] = k[i];
-      if (vs) vs[dst] = v[i];
-      if (w) w[dst] = x[i];
-    }
-  }
-}
-
-__global__ void __launch_bounds__(kMoveThreads, 4) cache_compact_kernel(const __grid_constant__ CompactParams p) {
-  extern __shared__ __align__(16) uint8_t ring[];
-  const int tensors = p.c.v ? 2 : 1, parts = tensors * p.slices + 1;   // of one head of one sequence
-  const int64_t units = (int64_t)p.num_seqs * p.c.n_kv * parts;
-  const uint32_t sring = smem_u32(ring);
+__global__ void __launch_bounds__(kMoveThreads, 3) cache_compact_kernel(const __grid_constant__ CompactParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  MoveRing* const ring = reinterpret_cast<MoveRing*>(smem);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = cluster.num_blocks(), rank = cluster.block_rank(), tensors = p.c.v ? 2 : 1;
+  const int64_t units = (int64_t)p.num_seqs * p.c.n_kv * tensors;
   int code = 0;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int part = (int)(u % parts), dh = (int)(u / parts), d = dh / p.c.n_kv, h = dh - d * p.c.n_kv;
-    const int n = __ldg(p.kept_len + d);
+  for (int64_t u = blockIdx.x / blocks; u < units; u += gridDim.x / blocks) {
+    const bool values = u % tensors != 0;
+    const int dh = (int)(u / tensors), d = dh / p.c.n_kv, h = dh - d * p.c.n_kv, n = __ldg(p.kept_len + d);
     if (n < 0 || n > p.width) {
       code = DSA_DEV_ERR_INVALID_ARG;
       continue;
     }
-    Move m{p, d, h, n, p.kept + ((int64_t)d * p.heads + (p.heads > 1 ? h : 0)) * p.width};
-    if (part > 0) {
-      const int slice = (part - 1) % p.slices, bytes = p.row_bytes / p.slices;
-      move_rows(m, reinterpret_cast<uint8_t*>(part <= p.slices ? p.c.k : p.c.v), p.row_bytes, bytes, slice * bytes, ring, sring);
-    } else if (p.c.sw == 4) {
-      move_small(m, reinterpret_cast<uint32_t*>(p.c.k_scale), reinterpret_cast<uint32_t*>(p.c.v_scale), p.weights);
-    } else if (p.c.sw == 2) {
-      move_small(m, reinterpret_cast<uint16_t*>(p.c.k_scale), reinterpret_cast<uint16_t*>(p.c.v_scale), p.weights);
-    } else {   // (BF16: no scales; the list is looked over here all the same)
-      move_small(m, p.c.sw ? p.c.k_scale : nullptr, p.c.sw ? p.c.v_scale : nullptr, p.weights);
-    }
-    if (m.bad) code = DSA_DEV_ERR_INVALID_ARG;
-    __syncthreads();
+    uint8_t* const base = reinterpret_cast<uint8_t*>(values ? p.c.v : p.c.k);
+    uint8_t* const scales = values ? p.c.v_scale : p.c.k_scale;
+    float* const weights = values ? nullptr : p.weights;
+    bool bad;
+    if (p.c.sw == 4) bad = move_head(p, d, h, n, base, reinterpret_cast<uint32_t*>(scales), weights, blocks, rank, ring);
+    else if (p.c.sw == 2) bad = move_head(p, d, h, n, base, reinterpret_cast<uint16_t*>(scales), weights, blocks, rank, ring);
+    else bad = move_head(p, d, h, n, base, p.c.sw ? scales : nullptr, weights, blocks, rank, ring);
+    if (bad) code = DSA_DEV_ERR_INVALID_ARG;
   }
   code = __syncthreads_or(code != 0) ? DSA_DEV_ERR_INVALID_ARG : 0;
   if (threadIdx.x == 0) put_block_status(p.hdr, code);
@@ -445,6 +455,22 @@ cudaError_t allow_smem(std::atomic<uint64_t>& ready, K kernel, int bytes) {
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
   ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
   return cudaSuccess;
+}
+
+template <class K, class P>
+cudaError_t launch_clusters(K kernel, const P& p, int clusters, int blocks, int threads, int smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = blocks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(clusters * blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
@@ -464,30 +490,21 @@ cudaError_t launch_evict_select(const SelectParams& call, int sm_count, cudaStre
   p.cached = (int)(rows < kSelRows ? rows : kSelRows);
   int64_t clusters = DSA_DEV_STATUS_MAX_BLOCKS / blocks;
   if (clusters > units) clusters = units;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = blocks;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(clusters * blocks));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = (size_t)(kSelFixed + p.cached) * 4;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  return launch_clusters(evict_select_kernel, p, (int)clusters, blocks, kSelThreads, (kSelFixed + p.cached) * 4, stream);
 }
 
-cudaError_t launch_cache_compact(const CompactParams& call, int sm_count, cudaStream_t stream) {
-  constexpr int kSmem = kMoveChunkBytes * kMoveStages;
-  // A row in parts of its own blocks while there are fewer than four blocks to an SM, down to 64 bytes.
-  CompactParams p = call;
-  const int64_t whole = (int64_t)p.num_seqs * p.c.n_kv * (p.c.v ? 2 : 1);
-  for (p.slices = 1; p.row_bytes / p.slices > 64 && whole * p.slices < 4 * sm_count;) p.slices *= 2;
-  const int64_t units = (int64_t)p.num_seqs * p.c.n_kv * ((p.c.v ? 2 : 1) * p.slices + 1);
-  const int64_t grid = units < DSA_DEV_STATUS_MAX_BLOCKS ? units : DSA_DEV_STATUS_MAX_BLOCKS;
-  cache_compact_kernel<<<(unsigned)grid, kMoveThreads, kSmem, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_cache_compact(const CompactParams& p, int sm_count, cudaStream_t stream) {
+  constexpr int kResident = 3;   // blocks of an SM
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(ready, cache_compact_kernel, sizeof(MoveRing));
+  if (e != cudaSuccess) return e;
+  // more blocks to a head while all of them are on the SMs at once
+  const int64_t units = (int64_t)p.num_seqs * p.c.n_kv * (p.c.v ? 2 : 1);
+  int blocks = 1;
+  while (blocks < kMoveCluster && units * blocks * 2 <= kResident * sm_count) blocks *= 2;
+  int64_t clusters = DSA_DEV_STATUS_MAX_BLOCKS / blocks;
+  if (clusters > units) clusters = units;
+  return launch_clusters(cache_compact_kernel, p, (int)clusters, blocks, kMoveThreads, sizeof(MoveRing), stream);
 }
 
 }  // namespace dsa

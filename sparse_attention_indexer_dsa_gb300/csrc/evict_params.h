@@ -50,7 +50,6 @@ struct CompactParams {
   const int32_t* kept_len; // [num_seqs]
   int num_seqs, heads, width;
   int row_bytes;           // of a row of keys or values
-  int slices;              // parts of a row that are moved by blocks of their own
   int* hdr;
 };
 
