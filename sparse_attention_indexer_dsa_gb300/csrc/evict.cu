@@ -3,12 +3,15 @@
 //
 // evict_select: of the S rows of a sequence the `budget` that come first by
 // (sinks and recent rows, weight descending, position ascending), written in
-// ascending order.  A cluster of 1 to 8 blocks takes one head of one sequence
+// ascending order.  A cluster of 1 to 16 blocks takes one head of one sequence
 // (or the sum of its heads), each block a range of the rows, and finds the
-// weight of the last row that stays by digits of its order-preserving bits: 12,
-// 12 and 8 of them, counted in shared memory and added up over the cluster.
-// With the last value known, the number of rows above it and how many of the
-// equal ones stay, each block writes its rows behind those of the blocks before.
+// weight of the last row that stays by the first 12 of its order-preserving
+// bits, counted in shared memory and added up over the cluster; the rows that
+// share them are few as a rule and ranked among one another, else (equal weights)
+// the next 12 and the last 8 bits are counted.  With the last value known, the
+// number of rows above it and how many of the equal ones stay, each block writes its
+// rows behind those of the blocks before.  It is latency that this costs: the rows'
+// loads are some 3 us and every barrier of a cluster 1.  FIGURES
 //
 // cache_compact: row j takes the place of row kept[j], kept ascending, so that
 // kept[j] >= j: a cluster of 1 to 8 blocks moves the rows of one head in ascending
@@ -40,10 +43,11 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 4096;
 constexpr int kLastBins = 256;
 constexpr uint32_t kMust = 0xFFFFFFFFu;   // above every weight's bits
-constexpr int kSelCluster = 8;            // blocks of a cluster, at most
+constexpr int kSelCluster = 16;           // blocks of a cluster, at most
+constexpr int kCoarse = 64;               // counts of as many neighbouring bins each
 constexpr int kSelRows = 40 * 1024;       // rows of a block whose bits fit into its shared memory
 constexpr int kSelFixed = 2 * kBins + kLastBins;   // words of the counts
-constexpr int kSelFew = kSelThreads;
+constexpr int kSelFew = 512;              // rows that are ranked among one another, at most
 
 // Order-preserving bits of a weight; NaN below everything, -0 as +0.
 __device__ __forceinline__ uint32_t weight_bits(float w) { return w != w ? 0u : orderable_key(w); }
@@ -93,61 +97,78 @@ struct Select {
   }
 };
 
-// Finds the bin of the `want`-th largest entry of the cluster's counts hist[n] and takes off `want` what
-// lies above it; *count: entries of the bin.  The whole cluster calls, after its counts are complete;
-// every thread gets the result.
-__device__ __forceinline__ int find_bin(cg::cluster_group& cluster, uint32_t* hist, int n, int* want, int* count,
-                                        int (*scratch)[kSelWarps + 3]) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  int c[4] = {0, 0, 0, 0};   // of four bins, from the top down over the threads
-  const int top = n - 4 * tid;
-  const unsigned blocks = cluster.num_blocks();
-  if (top > 0) {
-    for (unsigned r = 0; r < blocks; ++r) {
-      const uint4 v = *reinterpret_cast<const uint4*>((blocks > 1 ? cluster.map_shared_rank(hist, r) : hist) + top - 4);
-      c[0] += v.w;
-      c[1] += v.z;
-      c[2] += v.y;
-      c[3] += v.x;
-    }
-  }
-  const int mine = (c[0] + c[1]) + (c[2] + c[3]);
-  int incl = mine;
+// What finding a bin leaves for all threads, and what it counts with.
+struct Find {
+  int bin, want, count, here;       // here: it was this block that found it
+  int coarse[3][kCoarse];           // of this block's counts, of each step (others read them until the next but one barrier)
+  int sum[2][kCoarse];              // of the cluster's: coarse, then of one coarse count's bins
+};
+
+// Of 64 counts, from the top down, the one that holds the `want`-th entry; one warp calls.  Lane 0 stores
+// its index, its size and what is left of `want`.
+__device__ __forceinline__ void find_of_64(const int* counts, int want, Find* f) {
+  const int lane = threadIdx.x & 31, a = counts[63 - 2 * lane], b = counts[62 - 2 * lane];
+  int incl = a + b;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) (*scratch)[tid >> 5] = incl;
-  __syncthreads();
-  int before = (*scratch)[lane];
-  before = __reduce_add_sync(0xffffffffu, lane < (tid >> 5) ? before : 0);
-  int above = before + incl - mine;
-  const int w = *want;
-  if (above < w && above + mine >= w) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (above < w && above + c[j] >= w) {
-        (*scratch)[kSelWarps] = top - 1 - j;
-        (*scratch)[kSelWarps + 1] = w - above;
-        (*scratch)[kSelWarps + 2] = c[j];
-      }
-      above += c[j];
-    }
+  const int above = incl - a - b;
+  if (above < want && incl >= want) {
+    const bool first = above + a >= want;
+    f->bin = first ? 63 - 2 * lane : 62 - 2 * lane;
+    f->count = first ? a : b;
+    f->want = first ? want - above : want - above - a;
   }
+}
+
+// Finds the bin of the `want`-th largest entry of the cluster's counts hist[n] and takes off `want` what
+// lies above it; *count: entries of the bin.  The whole cluster calls, each block's counts being complete;
+// every thread gets the result.  Counts of n / 64 neighbouring bins first, so that little is read from
+// other blocks.  f->sum is zero before the unit's first call and after every call.
+__device__ __forceinline__ int find_bin(cg::cluster_group& cluster, uint32_t* hist, int n, int step, int* want, int* count, Find* f) {
+  const int tid = threadIdx.x, blocks = cluster.num_blocks(), fine = n / kCoarse;
+  {
+    const int per = n / kSelThreads > 0 ? n / kSelThreads : 1;   // bins of a thread; threads to a coarse count
+    int c = 0;
+    if (tid * per < n)
+      for (int i = 0; i < per; ++i) c += hist[tid * per + i];
+    for (int o = fine / per / 2; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    if (tid * per < n && tid % (fine / per) == 0) f->coarse[step][tid * per / fine] = c;
+  }
+  if (blocks > 1) cluster.sync(); else __syncthreads();
+  auto gather = [&](int* from, int* to, int size) {   // `size` (at most 64) counts of all blocks
+    if (blocks > 1) {
+      if (tid < size * blocks) {
+        const int v = *(cluster.map_shared_rank(from, tid / size) + tid % size);
+        if (v) atomicAdd(to + tid % size, v);
+      }
+    } else if (tid < size) {
+      to[tid] = from[tid];
+    }
+    __syncthreads();
+  };
+  gather(f->coarse[step], f->sum[0], kCoarse);
+  if (tid < 32) find_of_64(f->sum[0], *want, f);
   __syncthreads();
-  *want = (*scratch)[kSelWarps + 1];
-  *count = (*scratch)[kSelWarps + 2];
-  return (*scratch)[kSelWarps];
+  const int top = f->bin, left = f->want;
+  gather(reinterpret_cast<int*>(hist) + top * fine, f->sum[1], fine);
+  if (tid < 32) find_of_64(f->sum[1], left, f);
+  __syncthreads();
+  if (tid < kCoarse) f->sum[0][tid] = f->sum[1][tid] = 0;
+  *want = f->want;
+  *count = f->count;
+  return top * fine + f->bin;
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ __align__(16) uint32_t sm[];
   uint32_t* const hist[3] = {sm, sm + kBins, sm + 2 * kBins};
   uint32_t* const bits = sm + kSelFixed;     // [p.cached]
-  __shared__ int scratch[3][kSelWarps + 3];
+  __shared__ Find found;
   __shared__ int counts[2][kSelWarps];
-  __shared__ int total[2];
+  __shared__ int total[3];   // few rows collected; rows above and at the last value
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int heads = p.shared ? 1 : p.n_kv, blocks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -175,7 +196,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     Select sel{p, d, h, S};
     auto value = [&](int i) { return cached ? bits[i] : sel.at(lo + i); };
     for (int i = tid; i < kSelFixed; i += kSelThreads) sm[i] = 0;
-    if (tid == 0) total[0] = 0;
+    if (tid == 0) total[0] = found.here = 0;
+    if (tid < kCoarse) found.sum[0][tid] = found.sum[1][tid] = 0;
     __syncthreads();
     int want = p.budget;
     uint32_t prefix = 0;
@@ -214,34 +236,63 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
           }
         }
       }
-      sync();
+      __syncthreads();
       int in_bin;
-      prefix = (prefix << (step == 2 ? 8 : 12)) | (uint32_t)find_bin(cluster, count, bins, &want, &in_bin, &scratch[step]);
-      if (step == 0 && blocks == 1 && in_bin <= kSelFew) {
-        // few rows share the last one's first digit: each is ranked among them at once
-        unsigned long long* const few = reinterpret_cast<unsigned long long*>(hist[1]);
+      prefix = (prefix << (step == 2 ? 8 : 12)) | (uint32_t)find_bin(cluster, count, bins, step, &want, &in_bin, &found);
+      if (step == 0 && in_bin <= kSelFew) {
+        // few rows share the last one's first digit: every block collects its own, then all of them
+        unsigned long long* const own = reinterpret_cast<unsigned long long*>(hist[1]);
+        unsigned long long* const few = blocks > 1 ? own + kSelFew : own;
         for (int i = tid; i < n; i += kSelThreads) {
           const uint32_t b = value(i);
-          if ((b >> 20) == prefix) few[atomicAdd(&total[0], 1)] = (unsigned long long)(~b) << 32 | (unsigned)i;
+          if ((b >> 20) == prefix) own[atomicAdd(&total[0], 1)] = (unsigned long long)(~b) << 32 | (unsigned)(lo + i);
+        }
+        sync();
+        if (blocks > 1) {
+          // of entry `tid`: its block and its place there
+          int end = lane < blocks ? *cluster.map_shared_rank(total, lane) : 0;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += y;
+          }
+          int block = 0, at = tid;
+          for (int r = 0; r < blocks; ++r) {
+            const int e = __shfl_sync(0xffffffffu, end, r);
+            if (tid >= e) {
+              block = r + 1;
+              at = tid - e;
+            }
+          }
+          if (tid < in_bin) few[tid] = cluster.map_shared_rank(own, block)[at];
         }
         __syncthreads();
-        if (tid < in_bin) {
-          const unsigned long long mine = few[tid];
-          int rank = 0, above = 0;
-          for (int i = 0; i < in_bin; ++i) {
+        // a warp ranks one of the block's own among all
+        for (int c = warp; c < total[0]; c += kSelWarps) {
+          const unsigned long long mine = own[c];
+          int before = 0, above = 0;
+          for (int i = lane; i < in_bin; i += 32) {
             const unsigned long long other = few[i];
-            rank += other < mine;
+            before += other < mine;
             above += (uint32_t)(other >> 32) < (uint32_t)(mine >> 32);
           }
-          if (rank == want - 1) {   // the last that stays
-            counts[0][0] = (int)~(uint32_t)(mine >> 32);
-            counts[0][1] = want - above;
+          if (__reduce_add_sync(0xffffffffu, before) == want - 1) {   // the last that stays
+            above = __reduce_add_sync(0xffffffffu, above);
+            if (lane == 0) {
+              found.bin = (int)~(uint32_t)(mine >> 32);
+              found.want = want - above;
+              found.here = 1;
+            }
           }
         }
-        __syncthreads();
-        prefix = (uint32_t)counts[0][0];
-        want = counts[0][1];
-        __syncthreads();
+        sync();
+        const Find* f = &found;
+        if (blocks > 1) {
+          const uint32_t there = __ballot_sync(0xffffffffu, lane < blocks && cluster.map_shared_rank(&found, lane % blocks)->here);
+          f = cluster.map_shared_rank(&found, __ffs(there) - 1);
+        }
+        prefix = (uint32_t)f->bin;
+        want = f->want;
         break;
       }
     }
@@ -263,14 +314,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     int above = __reduce_add_sync(0xffffffffu, lane < warp ? counts[0][lane] : 0);   // before this warp's rows
     int equal = __reduce_add_sync(0xffffffffu, lane < warp ? counts[1][lane] : 0);
     if (tid == kSelThreads - 1) {
-      total[0] = above + n_above;
-      total[1] = equal + n_equal;
+      total[1] = above + n_above;
+      total[2] = equal + n_equal;
     }
     sync();
-    for (int r = 0; r < rank; ++r) {
-      const int* const t = cluster.map_shared_rank(total, r);
-      above += t[0];
-      equal += t[1];
+    if (blocks > 1) {   // rows of the blocks before
+      const int* const t = cluster.map_shared_rank(total, lane < rank ? lane : rank);
+      above += __reduce_add_sync(0xffffffffu, lane < rank ? t[1] : 0);
+      equal += __reduce_add_sync(0xffffffffu, lane < rank ? t[2] : 0);
     }
     for (int i0 = wlo; i0 < whi; i0 += 32) {
       const int i = i0 + lane;
@@ -445,31 +496,37 @@ __global__ void __launch_bounds__(kMoveThreads, 3) cache_compact_kernel(const __
   if (threadIdx.x == 0) put_block_status(p.hdr, code);
 }
 
-// Once per device: the kernel's shared memory beyond the default.
+// Once per device: the kernel's shared memory beyond the default, and clusters of sixteen blocks.
 template <class K>
-cudaError_t allow_smem(std::atomic<uint64_t>& ready, K kernel, int bytes) {
+cudaError_t allow_smem(std::atomic<uint64_t>& ready, K kernel, int bytes, bool sixteen = false) {
   int dev = 0;
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (ready.load(std::memory_order_acquire) >> (dev & 63) & 1) return cudaSuccess;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+  if (sixteen && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
   ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
   return cudaSuccess;
 }
 
-template <class K, class P>
-cudaError_t launch_clusters(K kernel, const P& p, int clusters, int blocks, int threads, int smem, cudaStream_t stream) {
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, int clusters, int blocks, int threads, int smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = blocks;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = blocks;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(clusters * blocks));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cfg.attrs = &attr;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <class K, class P>
+cudaError_t launch_clusters(K kernel, const P& p, int clusters, int blocks, int threads, int smem, cudaStream_t stream) {
+  cudaLaunchAttribute attr{};
+  const cudaLaunchConfig_t cfg = cluster_config(&attr, clusters, blocks, threads, smem, stream);
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -477,15 +534,31 @@ cudaError_t launch_clusters(K kernel, const P& p, int clusters, int blocks, int 
 
 cudaError_t launch_evict_select(const SelectParams& call, int sm_count, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem(ready, evict_select_kernel, (kSelFixed + kSelRows) * 4);
+  cudaError_t e = allow_smem(ready, evict_select_kernel, (kSelFixed + kSelRows) * 4, true);
   if (e != cudaSuccess) return e;
   SelectParams p = call;
   const int64_t units = (int64_t)p.num_seqs * (p.shared ? 1 : p.n_kv);
   // more blocks to a head while there are SMs for them and eight rows to a thread, or to hold its rows' bits
+  // (sixteen of them, which not every cluster of SMs has room for at any time, for few heads alone)
   int blocks = 1;
-  while (blocks < kSelCluster && ((units * blocks < sm_count && p.max_seqlen_k / blocks > 8 * kSelThreads) ||
-                                  p.max_seqlen_k / blocks > kSelRows))
+  while (blocks < kSelCluster / 2 && ((units * blocks * 2 <= sm_count && p.max_seqlen_k / blocks > 8 * kSelThreads) ||
+                                      p.max_seqlen_k / blocks > kSelRows))
     blocks *= 2;
+  static std::atomic<uint64_t> sixteen{0}, asked{0};
+  if (blocks == kSelCluster / 2 && units * kSelCluster <= sm_count / 2 && p.max_seqlen_k / blocks > 4 * kSelThreads) {
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(asked.load(std::memory_order_acquire) & bit)) {   // once per device: whether it has room for one
+      cudaLaunchAttribute attr{};
+      const cudaLaunchConfig_t cfg = cluster_config(&attr, 1, kSelCluster, kSelThreads, (kSelFixed + kSelRows) * 4, stream);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel, &cfg) != cudaSuccess) cudaGetLastError();
+      if (n > 0) sixteen.fetch_or(bit, std::memory_order_release);
+      asked.fetch_or(bit, std::memory_order_release);
+    }
+    if (sixteen.load(std::memory_order_acquire) & bit) blocks = kSelCluster;
+  }
   const int64_t rows = ((int64_t)(p.max_seqlen_k + blocks - 1) / blocks + 31) & ~31;
   p.cached = (int)(rows < kSelRows ? rows : kSelRows);
   int64_t clusters = DSA_DEV_STATUS_MAX_BLOCKS / blocks;
