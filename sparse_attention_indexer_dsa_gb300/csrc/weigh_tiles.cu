@@ -275,9 +275,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
     bool ok = true;
     for (; ok && cur.next(&x); ++nx) {
       const int wkey = x.key0 + w * 128 + quarter * 32, key = wkey + lane;   // the warp's first key, this thread's
-      float2 sum[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
+      float total = 0.f;   // sums of products are added to it: a sum over all columns one by one would lose bits
       for (int j = 0; j < x.n; ++j, ++nt) {
         const int slot = nt % kBiasRing;
         const int i0 = x.i0 + j * tq, tokens = min(tq, x.T - i0), cols = tokens * p.group - c0;   // this half's live columns
@@ -291,6 +289,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
                                          wait_bar(bar(S_FULL + 2 * w + half), nt & 1u, abort_flag, status, tmo));
         if (!ok) break;
         tc_fence_after();
+        float2 sum[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
         auto release = [&] {   // the half's columns have been read
           tc_fence_before();
           __syncwarp();
@@ -334,8 +335,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_EMPTY + slot));
+        total += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
       }
-      float total = ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
       // The halves' sums meet (in two places in turn).  Whatever a warp has waited for in vain, it comes
       // here: both warpgroups leave together.
       if (half == 1) sums[(nx & 1) * 256] = total;
