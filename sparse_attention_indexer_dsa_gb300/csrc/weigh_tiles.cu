@@ -38,7 +38,7 @@ constexpr int kTileThreads = 768;
 constexpr int kGroups = 64;            // sequences are counted in this many groups
 constexpr int kHalf = kWeighCols / 2;  // columns of a product and of a hand-over
 constexpr int kBiasRing = 4;
-constexpr int kUnitCost = 2;           // what a unit's change of keys counts beside its query tiles
+constexpr int kUnitCost = 3;           // what a unit's change of keys counts beside its query tiles
 constexpr int kMinPart = 2 * kUnitCost;   // length of a block's part, at least
 // barriers (halves: 2 * stream + half)
 enum { K_FULL = 0, K_EMPTY = 2, S_FULL = 4, S_EMPTY = 8, B_FULL = 12, B_EMPTY = B_FULL + kBiasRing, DRAIN = B_EMPTY + kBiasRing,
@@ -297,6 +297,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(S_EMPTY + 2 * w + half));
         };
+        // 32 columns, all of whose tokens see all the warp's keys
+        auto weigh32 = [&](const uint32_t (&v)[32], int c) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float4 b = *reinterpret_cast<const float4*>(bias + c + 2 * i);
+            float2 e0 = ffma2(as_f2(v[2 * i], v[2 * i + 1]), sc2, make_float2(b.x, b.y));
+            float2 e1 = ffma2(as_f2(v[2 * i + 2], v[2 * i + 3]), sc2, make_float2(b.z, b.w));
+            e0.x = ex2(e0.x);
+            e0.y = ex2(e0.y);
+            e1.x = ex2(e1.x);
+            e1.y = ex2(e1.y);
+            sum[i & 2] = __fadd2_rn(sum[i & 2], e0);
+            sum[(i & 2) + 1] = __fadd2_rn(sum[(i & 2) + 1], e1);
+          }
+        };
         if (any && !edge) {
 #pragma unroll
           for (int c = 0; c < kHalf; c += 32) {
@@ -304,29 +319,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
             tmem_ld_x32(t_s + c, s);
             tmem_ld_wait_tied<32>(s);
             if (c + 32 == kHalf) release();
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float4 b = *reinterpret_cast<const float4*>(bias + c + 2 * i);
-              float2 e0 = ffma2(as_f2(s[2 * i], s[2 * i + 1]), sc2, make_float2(b.x, b.y));
-              float2 e1 = ffma2(as_f2(s[2 * i + 2], s[2 * i + 3]), sc2, make_float2(b.z, b.w));
-              e0.x = ex2(e0.x);
-              e0.y = ex2(e0.y);
-              e1.x = ex2(e1.x);
-              e1.y = ex2(e1.y);
-              sum[i & 2] = __fadd2_rn(sum[i & 2], e0);
-              sum[(i & 2) + 1] = __fadd2_rn(sum[(i & 2) + 1], e1);
-            }
+            weigh32(s, c);
           }
         } else if (any) {
 #pragma unroll 1
           for (int c = 0; c < min(cols, kHalf); c += 32) {
+            int g;
+            if (wkey > x.P0 + i0 + token_of(p, c0 + c + 31, &g)) continue;   // none of these tokens sees a key of the warp
             uint32_t s[32];
             tmem_ld_x32(t_s + c, s);
             tmem_ld_wait_tied<32>(s);
+            if (c + 32 <= cols && wkey + 31 <= x.P0 + i0 + token_of(p, c0 + c, &g)) {
+              weigh32(s, c);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float e = ex2(fmaf(__uint_as_float(s[i]), p.scale_log2, bias[c + i]));
-              sum[(i >> 1) & 3].x += key <= seen[c + i] ? e : 0.f;
+              for (int i = 0; i < 32; ++i) {
+                const float e = ex2(fmaf(__uint_as_float(s[i]), p.scale_log2, bias[c + i]));
+                sum[(i >> 1) & 3].x += key <= seen[c + i] ? e : 0.f;
+              }
             }
           }
           release();
@@ -358,12 +368,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
     bool ok = true, bad_page = false;
     while (ok && cur.next(&x)) {
       if (x.n == 0) continue;
-#pragma unroll 1
-      for (int w = 0; w < 2 && ok; ++w) {
+      uint32_t rows[2];   // this lane's of either tile
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
         const int key = x.key0 + w * 128 + kw * 32 + lane;
         const int64_t mine = key < x.S ? cache_row(p.c, x.d, key, x.h) : -1;
         if (key < x.S && mine < 0) bad_page = true;
-        const uint32_t row32 = mine < 0 ? ~0u : (uint32_t)mine;
+        rows[w] = mine < 0 ? ~0u : (uint32_t)mine;
+        // on its way to the L2 while the last unit's keys are still in use
+        constexpr int kRowBytes = D * (Q8 ? 1 : 2);
+        if (rows[w] != ~0u) {
+#pragma unroll
+          for (int i = 0; i < kRowBytes; i += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(p.c.k) + (size_t)rows[w] * kRowBytes + i));
+        }
+      }
+#pragma unroll 1
+      for (int w = 0; w < 2 && ok; ++w) {
+        const uint32_t row32 = w ? rows[1] : rows[0];
         const uint32_t dst = sbase + w * L::kKeyTile + kw * 32 * 128;
         auto wait_empty = [&] {
           if (nk > 0) ok = __all_sync(0xffffffffu, wait_bar(bar(K_EMPTY + w), (nk - 1) & 1u, abort_flag, status, tmo));

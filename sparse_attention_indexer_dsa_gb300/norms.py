@@ -10,7 +10,7 @@ from typing import NamedTuple, Optional, Sequence, Tuple
 import torch
 
 from . import _abi
-from .paged import _arg, _call, _error, _tokens
+from .paged import _arg, _call, _error
 
 _NORM = {"rms": _abi.DSA_NORM_RMS, "layer": _abi.DSA_NORM_LAYER}
 _WEIGHTS = ("q_weight", "k_weight", "q_bias", "k_bias")
@@ -27,6 +27,28 @@ class NormRopeGrads(NamedTuple):
     k_bias: Optional[torch.Tensor]
 
 
+def _rows(t: torch.Tensor, name: str):
+    """Address and token stride of a [tokens, heads, head_dim] tensor whose tokens may be apart."""
+    if t.is_contiguous():
+        return t.data_ptr() or None, 0
+    T, H, D = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and H > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if T < 2:
+        return t.data_ptr() or None, 0
+    if s0 < H * D:   # (an expanded tensor's 0 would be taken for packed tokens)
+        raise ValueError(f"{name}: tokens must not share memory (an expanded tensor is copied first)")
+    return t.data_ptr() or None, s0
+
+
+def _like(t: torch.Tensor, name: str, shape, dtype, device):
+    """The same of a tensor that must be of this shape, type and device."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}, not {tuple(t.shape)} {t.dtype} on {t.device}")
+    return _rows(t, name)
+
+
 def _inputs(q, k, positions, weights, norm, rope_dim, inv_freq):
     """Checks that forward and backward share; what they hand on."""
     if q.dim() != 3:
@@ -35,15 +57,17 @@ def _inputs(q, k, positions, weights, norm, rope_dim, inv_freq):
     T, H, D = shape
     if not q.is_cuda:
         raise ValueError("q must live on the CUDA device")
+    if dt not in _DTYPE:
+        raise ValueError(f"q: unsupported dtype {dt}")
     if norm not in _NORM:
         raise ValueError(f"norm must be 'rms' or 'layer', not {norm!r}")
-    qp, qst = _tokens(q, "q", dev, _DTYPE, H, D)
+    qp, qst = _rows(q, "q")
     kp, kst, Hk = None, 0, 0
     if k is not None:
-        if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D:
+        if k.dim() != 3:
             raise ValueError(f"k must be [{T}, n_kv_heads, {D}], not {tuple(k.shape)}")
         Hk = k.shape[1]
-        kp, kst = _tokens(k, "k", dev, (dt,), Hk, D)
+        kp, kst = _like(k, "k", (T, Hk, D), dt, dev)
     R = D if rope_dim is None else rope_dim
     pos = None
     if R:
@@ -103,10 +127,10 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[to
             raise ValueError("out has another dtype than out_dtype")
         if (k is None) != (k_out is None):
             raise ValueError("out must be a pair (q_out, k_out), k_out None where k is")
-        if q_out.shape != shape or (k is not None and k_out.shape != k.shape):
-            raise ValueError("out must have the shapes of q and k")
-        qo, qost = _tokens(q_out, "q_out", dev, _DTYPE, H, D)
-        ko, kost = _tokens(k_out, "k_out", dev, (ot,), Hk, D)
+        if ot not in _DTYPE:
+            raise ValueError(f"q_out: unsupported dtype {ot}")
+        qo, qost = _like(q_out, "q_out", shape, ot, dev)
+        ko, kost = (None, 0) if k is None else _like(k_out, "k_out", k.shape, ot, dev)
     code = _call(_abi.load().dsa_idx_norm_rope, dev, (
         *rows, _DTYPE[dt], *wp, wt, _NORM[norm], eps, pos, T, H, Hk, D, R, rope_base, freq, int(rope_interleaved), qo, qost,
         ko, kost, _DTYPE[ot]))
@@ -142,10 +166,10 @@ def norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: 
     gt = dq_out.dtype
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out must both be given or both be None")
-    if dq_out.shape != shape or (k is not None and dk_out.shape != k.shape):
-        raise ValueError("dq_out and dk_out must have the shapes of q and k")
-    gq, gqst = _tokens(dq_out, "dq_out", dev, _DTYPE, H, D)
-    gk, gkst = _tokens(dk_out, "dk_out", dev, (gt,), Hk, D)
+    if gt not in _DTYPE:
+        raise ValueError(f"dq_out: unsupported dtype {gt}")
+    gq, gqst = _like(dq_out, "dq_out", shape, gt, dev)
+    gk, gkst = (None, 0) if k is None else _like(dk_out, "dk_out", k.shape, gt, dev)
     dq, dk, dkp = torch.empty(shape, dtype=dt, device=dev), None, None
     if k is not None:
         dk = torch.empty(k.shape, dtype=dt, device=dev)

@@ -153,3 +153,30 @@ def test_the_binding_checks_before_the_library():
     with pytest.raises(ValueError):
         dsa.weigh_workspace(1, 1, 1, 3, 2, 64)
     assert set(norms._DTYPE) == {torch.float32, torch.bfloat16}
+
+
+@pytest.mark.parametrize("view", [
+    lambda: torch.zeros((1, 4, 64)).expand(8, 4, 64),
+    lambda: torch.zeros((4, 64)).expand(2, 4, 64),
+    lambda: torch.zeros(64 * 32).as_strided((8, 4, 64), (64, 64, 1)),
+    lambda: torch.zeros((8, 1, 64)).expand(8, 4, 64),
+    lambda: torch.zeros((8, 64, 4)).transpose(1, 2),
+    lambda: torch.zeros((1, 1, 64)).expand(5, 1, 64),
+])
+def test_tokens_that_share_memory_are_refused(view):
+    with pytest.raises(ValueError):
+        norms._rows(view(), "q")
+
+
+def test_token_strides():
+    base = torch.zeros((8, 6, 64))
+    assert norms._rows(base, "q") == (base.data_ptr(), 0)
+    assert norms._rows(base[:, 2:], "q") == (base[:, 2:].data_ptr(), 6 * 64)
+    assert norms._rows(base[::2, 2:], "q") == (base[:, 2:].data_ptr(), 12 * 64)
+    assert norms._rows(base[:1, 2:], "q") == (base[:, 2:].data_ptr(), 0)       # one token has no next one
+    assert norms._rows(base[:0, 2:], "q")[1] == 0
+    one = torch.zeros((8, 1, 128))[:, :, :64]
+    assert norms._rows(one, "q") == (one.data_ptr(), 128)
+    for shape, dt in (((8, 6, 64), torch.bfloat16), ((8, 5, 64), torch.float32)):
+        with pytest.raises(ValueError, match="k must be"):
+            norms._like(base, "k", shape, dt, base.device)
