@@ -11,7 +11,10 @@
 // the next 12 and the last 8 bits are counted.  With the last value known, the
 // number of rows above it and how many of the equal ones stay, each block writes its
 // rows behind those of the blocks before.  It is latency that this costs: the rows'
-// loads are some 3 us and every barrier of a cluster 1.  FIGURES
+// loads take 2 to 5 us, every barrier of a cluster 1.  2048 rows of some 2200, 16
+// sequences of 8 heads, a block each: 10 us; 4096 of up to 65536 by the sums of 8
+// heads, 3 sequences, 16 blocks each: 20 us, with 8 blocks 22, with all digits counted
+// and all counts read from every block 30.
 //
 // cache_compact: row j takes the place of row kept[j], kept ascending, so that
 // kept[j] >= j: a cluster of 1 to 8 blocks moves the rows of one head in ascending
@@ -363,10 +366,13 @@ __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0
 
 // Shared memory of a block: the chunks' rows, the cache rows that they come from and go to, their weights
 // and the words that hold their scales.
+// A chunk is looked up kMoveStages steps before it is written, and a thread may be a step ahead of another's
+// writing: two slots more than lie between.
+constexpr int kMoveSlots = kMoveStages + 2;
 struct MoveRing {
   uint4 rows[kMoveStages][kMoveChunkBytes / 16];
-  uint32_t from[kMoveStages + 1][kMoveRows], to[kMoveStages + 1][kMoveRows];
-  uint32_t weight[kMoveStages + 1][kMoveRows], scale[kMoveStages + 1][kMoveRows];
+  uint32_t from[kMoveSlots][kMoveRows], to[kMoveSlots][kMoveRows];
+  uint32_t weight[kMoveSlots][kMoveRows], scale[kMoveSlots][kMoveRows];
 };
 
 // What the cluster's threads have read before it is read before any writes behind it, and the block's shared
@@ -403,7 +409,7 @@ __device__ __forceinline__ bool move_head(const CompactParams& p, int d, int h, 
   int pf = page(e0), pt = page(tid < rows && j0 < n ? j0 : -1);
   // Looks up this thread's row of chunk f, and requests what the next ones need.
   auto look_up = [&](int f) {
-    const int j = j0 + f * chunk, slot = f % (kMoveStages + 1);
+    const int j = j0 + f * chunk, slot = f % kMoveSlots;
     uint32_t from = ~0u, to = ~0u;
     if (tid < rows && j < n) {
       if (e0 < j || e0 <= before) {   // not ascending
@@ -439,7 +445,7 @@ __device__ __forceinline__ bool move_head(const CompactParams& p, int d, int h, 
 #pragma unroll
       for (int s = 0; s < kMovePer; ++s) {
         const int x = s * kMoveThreads + tid;
-        const uint32_t from = ring->from[f % (kMoveStages + 1)][x / pieces];
+        const uint32_t from = ring->from[f % kMoveSlots][x / pieces];
         if (from != ~0u) cp_async_16(dst + s * kMoveThreads * 16, base + (size_t)from * p.row_bytes + (x & (pieces - 1)) * 16);
       }
     }
@@ -451,10 +457,10 @@ __device__ __forceinline__ bool move_head(const CompactParams& p, int d, int h, 
 #pragma unroll
     for (int s = 0; s < kMovePer; ++s) {
       const int x = s * kMoveThreads + tid;
-      const uint32_t dst = ring->to[c % (kMoveStages + 1)][x / pieces];
+      const uint32_t dst = ring->to[c % kMoveSlots][x / pieces];
       if (dst != ~0u) *reinterpret_cast<uint4*>(base + (size_t)dst * p.row_bytes + (x & (pieces - 1)) * 16) = ring->rows[c % kMoveStages][x];
     }
-    const int slot = c % (kMoveStages + 1);
+    const int slot = c % kMoveSlots;
     const uint32_t to = tid < rows ? ring->to[slot][tid] : ~0u;
     if (to != ~0u) {
       if (scales) {

@@ -94,6 +94,7 @@ dsa_status_t dsa_idx_evict_select(const float* weights, int num_pages, int page_
                                page_table, max_pages, num_seqs, cu_seqlens_k);
   if (s != DSA_OK) return s;
   if (!kept || !kept_len) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if ((int64_t)num_seqs * n_kv_heads >= (int64_t)1 << 30) return fail(DSA_ERR_UNSUPPORTED, "num_seqs * n_kv_heads above 2^30");
   if (max_seqlen_k < 0 || max_seqlen_k > (1 << 30)) return fail(DSA_ERR_INVALID_ARG, "max_seqlen_k must be in [0, 2^30]");
   if (budget < 1 || budget > (1 << 30)) return fail(DSA_ERR_INVALID_ARG, "budget must be in [1, 2^30]");
   if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
@@ -132,6 +133,7 @@ dsa_status_t dsa_idx_cache_compact(void* k_pages, uint8_t* k_page_scale, void* v
                                head_dim, prec, page_table, max_pages, num_seqs, kept_len);
   if (s != DSA_OK) return s;
   if (!kept) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if ((int64_t)num_seqs * n_kv_heads >= (int64_t)1 << 30) return fail(DSA_ERR_UNSUPPORTED, "num_seqs * n_kv_heads above 2^30");
   if (kept_heads != 1 && kept_heads != n_kv_heads) return fail(DSA_ERR_INVALID_ARG, "kept has one head, or the cache's");
   if (kept_width < 1 || kept_width > (1 << 30)) return fail(DSA_ERR_INVALID_ARG, "kept_width must be in [1, 2^30]");
   if (!aligned16(weights)) return fail(DSA_ERR_INVALID_ARG, "weights must be 16-byte aligned");

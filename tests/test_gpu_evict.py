@@ -425,6 +425,29 @@ def test_compact_many_sequences():
     check_compact(b, rng, kept, n, E.random_weights(rng, b))
 
 
+def test_compact_again_and_again():
+    """Many chunks by blocks of threads that are not in step, the same bits every time."""
+    rng = np.random.default_rng(54)
+    for lens, kv, D, prec in (([30000], 2, 128, "bf16"), ([9000] * 3, 8, 128, "mxfp8"), ([2000] * 60, 4, 64, "fp8")):
+        b = Batch(rng, [(0, s) for s in lens], 1, D, 64, prec)
+        kept, n = some_rows(rng, b, 1, max(lens), 0.7)
+        base = b.cache(dsa)
+        full = [None if t is None else t.expand(-1, kv, -1, -1) for t in (base.k, base.k_scale, base.v, base.v_scale)]
+        w = torch.arange(b.num_pages * 64, device="cuda").float().view(-1, 1, 64).expand(-1, kv, -1)
+        want = E.compact(b, tensors_of(b, host(w[:, :1].contiguous())), kept, n)
+        for _ in range(6):
+            c = dsa.PagedCache(*[None if t is None else t.contiguous() for t in full], prec)
+            wd = w.contiguous()
+            dsa.cache_compact(c, dev(kept), dev(n), b.dev("table"), weights=wd)
+            for name, t in (("k", c.k), ("k_scale", c.k_scale), ("v", c.v), ("v_scale", c.v_scale), ("weights", wd)):
+                if t is not None:
+                    first = as_bits(t[:, :1].contiguous())
+                    assert np.array_equal(first, want[name]), (name, lens)
+                    assert torch.equal(t.view(torch.uint8) if t.dtype == torch.bfloat16 else t,
+                                       (t[:, :1].view(torch.uint8) if t.dtype == torch.bfloat16 else t[:, :1]).expand_as(
+                                           t.view(torch.uint8) if t.dtype == torch.bfloat16 else t))
+
+
 def test_compact_shifts_by_one():
     """Every row but one stays: each chunk reads what the one before it has to leave alone."""
     rng = np.random.default_rng(52)

@@ -99,7 +99,7 @@ def test_cache_weigh_refuses(lib, want, change):
 @pytest.mark.parametrize("want,change", PAGES + [
     (BAD, dict(weights=None)), (BAD, dict(cu_k=None)), (BAD, dict(kept=None)), (BAD, dict(kept_len=None)), (BAD, dict(budget=0)),
     (BAD, dict(max_k=-1)), (BAD, dict(sinks=-1)), (BAD, dict(recent=-1)), (BAD, dict(sinks=10, recent=11)),
-    (BAD, dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1)), (BAD, dict(budget=(1 << 30) + 1))])
+    (BAD, dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1)), (BAD, dict(budget=(1 << 30) + 1)), (UNSUP, dict(num_seqs=1 << 29))])
 def test_evict_select_refuses(lib, want, change):
     assert call(lib.dsa_idx_evict_select, SELECT, **change) == want, change
 
@@ -107,7 +107,7 @@ def test_evict_select_refuses(lib, want, change):
 @pytest.mark.parametrize("want,change", PAGES + [
     (BAD, dict(k_pages=None)), (BAD, dict(k_page_scale=None)), (BAD, dict(v_page_scale=None)), (BAD, dict(kept=None)),
     (BAD, dict(kept_len=None)), (BAD, dict(kept_heads=3)), (BAD, dict(kept_heads=0)), (BAD, dict(kept_width=0)), (UNSUP, dict(head_dim=100)),
-    (BAD, dict(k_pages=A + 8)), (BAD, dict(prec=-1))])
+    (BAD, dict(k_pages=A + 8)), (BAD, dict(prec=-1)), (UNSUP, dict(num_seqs=1 << 29))])
 def test_cache_compact_refuses(lib, want, change):
     assert call(lib.dsa_idx_cache_compact, COMPACT, **change) == want, change
 
