@@ -19,7 +19,7 @@ size_t dsa_idx_weigh_workspace_size(int total_q, int num_seqs, int max_seqlen_q,
       n_heads / n_kv_heads > 128 || (head_dim != 64 && head_dim != 128))
     return 0;
   // the sums of divided units where a sequence may have more query rows than the step kernel takes
-  const bool tiles = (int64_t)max_seqlen_q * (n_heads / n_kv_heads) > kWeighStepRows;
+  const bool tiles = (int64_t)max_seqlen_q * (n_heads / n_kv_heads) > kWeighStepRows16;
   return DSA_DEV_STATUS_HEADER_BYTES + (tiles ? (size_t)kAttnSms * 2 * kWeighKeys * sizeof(float) : 0);
 }
 
@@ -72,7 +72,8 @@ dsa_status_t dsa_idx_cache_weigh(const void* q, int64_t q_stride, const float* l
   p.fault_inject = fault_inject_mode();
   // Long chunks have a kernel of their own; each of the two takes the sequences that are its own, by
   // their lengths on the device.
-  const bool tiles = total_q > 0 && (int64_t)max_seqlen_q * p.group > kWeighStepRows;
+  p.step_rows = prec == DSA_PREC_BF16 ? kWeighStepRows16 : kWeighStepRows8;
+  const bool tiles = total_q > 0 && (int64_t)max_seqlen_q * p.group > p.step_rows;
   p.step_blocks = weigh_step_blocks(p, di.sm_count);
   p.tile_blocks = tiles ? (di.sm_count < kAttnSms ? di.sm_count : kAttnSms) : 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

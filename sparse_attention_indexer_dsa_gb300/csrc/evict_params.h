@@ -19,6 +19,7 @@ struct WeighParams {
   int num_seqs, total_q, max_seqlen_q, max_seqlen_k, n_heads, group;
   uint32_t group_mul; // 2^32 / group, rounded up (group 1: not used)
   float scale_log2;   // sm_scale * log2(e)
+  int step_rows;      // query rows of a sequence up to which its keys stream past them
   int step_blocks, tile_blocks;
   int* hdr;
   float* part;        // [tile_blocks][2][kWeighKeys] sums of divided units: that a block ends, that it begins
@@ -26,8 +27,9 @@ struct WeighParams {
   unsigned long long timeout_ns;
 };
 
-// Query rows of a sequence up to which its keys stream past them.
-constexpr int kWeighStepRows = 64;
+// Query rows of a sequence up to which its keys stream past them, 8-bit ones and BF16 ones.
+// (figures: with the kernels)
+constexpr int kWeighStepRows8 = 64, kWeighStepRows16 = 16;
 constexpr int kWeighCols = 256;    // query rows of a tile
 constexpr int kWeighKeys = 256;    // keys of a unit
 struct SelectParams {

@@ -241,28 +241,31 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
       const int key0 = first + i * kKeys;
       const bool edge = key0 + kKeys > P0 + 1;   // some token does not see some key
       const int r_first = edge && key0 > P0 ? (key0 - P0) * p.group : 0;   // rows before it see none of these keys
-      float sum[kKeys / 8];   // of keys g, g + 8, ..
+      constexpr int kTiles = kKeys / 16;
+      float sum[2 * kTiles];   // of keys g, g + 8, ..
 #pragma unroll
-      for (int m = 0; m < kKeys / 16; ++m) {
-        const int ra = m * 16 + g, rb = ra + 8;   // this lane's keys
-        float sa = 0.f, sb = 0.f;
-        auto add = [&](const float (&acc)[4], int r0) {
-          float w[4];
+      for (int m = 0; m < 2 * kTiles; ++m) sum[m] = 0.f;
+      // the weights of keys 16 m + g (and + 8) under query rows r0 + 2 t and the next one
+      auto add = [&](const float (&acc)[4], int m, int r0) {
+        float w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(acc[e], e & 1 ? colscale.y : colscale.x, e & 1 ? bias.y : bias.x));
-          if (edge) {
+        for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(acc[e], e & 1 ? colscale.y : colscale.x, e & 1 ? bias.y : bias.x));
+        if (edge) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              int hg;
-              const int vis = P0 + token_of(p, r0 + 2 * t + e, &hg);
-              if (key0 + ra > vis) w[e] = 0.f;
-              if (key0 + rb > vis) w[2 + e] = 0.f;
-            }
+          for (int e = 0; e < 2; ++e) {
+            int hg;
+            const int vis = P0 + token_of(p, r0 + 2 * t + e, &hg);
+            if (key0 + 16 * m + g > vis) w[e] = 0.f;
+            if (key0 + 16 * m + 8 + g > vis) w[2 + e] = 0.f;
           }
-          sa += w[0] + w[1];
-          sb += w[2] + w[3];
-        };
-        if (Q8 && half) {
+        }
+        sum[2 * m] += w[0] + w[1];
+        sum[2 * m + 1] += w[2] + w[3];
+      };
+      if (Q8 && half) {
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          const int ra = m * 16 + g, rb = ra + 8;   // this lane's keys
           const uint32_t ca = __shfl_sync(0xffffffffu, a0.scale, ra), cb = __shfl_sync(0xffffffffu, a0.scale, rb);
           float total[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -281,44 +284,45 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
 #pragma unroll
             for (int e = 0; e < 4; ++e) total[e] = fmaf(acc[e], e < 2 ? fa : fb, total[e]);
           }
-          add(total, 0);
-        } else {
-          uint32_t a[2][kBlocks][4];   // the two keys as pairs of BF16
+          add(total, m, 0);
+        }
+      } else {
+        uint32_t a[kTiles][2][kBlocks][4];   // the keys as pairs of BF16
+#pragma unroll
+        for (int i = 0; i < 2 * kTiles; ++i) {
+          const int row = i * 8 + g;
           if constexpr (Q8) {
+            const uint32_t sc = __shfl_sync(0xffffffffu, a0.scale, row);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t sc = __shfl_sync(0xffffffffu, a0.scale, k ? rb : ra);
-#pragma unroll
-              for (int c = 0; c < kBlocks; ++c) {
-                uint32_t w2[2];
-                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w2[0]), "=r"(w2[1]) : "r"(step + St::at(k ? rb : ra, c) + 8 * t));
-                const uint32_t e8 = (sc >> (8 * c)) & 255u;
-                if (e8 <= 134u) attn::widen<false>(w2, e8, a[k][c]);
-                else attn::widen<true>(w2, e8, a[k][c]);
-              }
+            for (int c = 0; c < kBlocks; ++c) {
+              uint32_t w2[2];
+              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w2[0]), "=r"(w2[1]) : "r"(step + St::at(row, c) + 8 * t));
+              const uint32_t e8 = (sc >> (8 * c)) & 255u;
+              if (e8 <= 134u) attn::widen<false>(w2, e8, a[i >> 1][i & 1][c]);
+              else attn::widen<true>(w2, e8, a[i >> 1][i & 1][c]);
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-              for (int c = 0; c < kBlocks; ++c) attn::ld_shared_v4(step + St::at(k ? rb : ra, c) + 16 * t, a[k][c]);
-            }
-          }
-          for (int r0 = r_first & ~7; r0 < n_rows; r0 += 8) {
-            if (n_rows > 8) load_q(r0);
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < kBlocks; ++c) {
-              const uint32_t qw[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
-#pragma unroll
-              for (int s = 0; s < 2; ++s)
-                mma_16816(acc, a[0][c][2 * s], a[1][c][2 * s], a[0][c][2 * s + 1], a[1][c][2 * s + 1], qw[2 * s], qw[2 * s + 1]);
-            }
-            add(acc, r0);
+            for (int c = 0; c < kBlocks; ++c) attn::ld_shared_v4(step + St::at(row, c) + 16 * t, a[i >> 1][i & 1][c]);
           }
         }
-        sum[2 * m] = sa;
-        sum[2 * m + 1] = sb;
+        for (int r0 = r_first & ~7; r0 < n_rows; r0 += 8) {
+          if (n_rows > 8) load_q(r0);
+          float acc[kTiles][4] = {};
+#pragma unroll
+          for (int c = 0; c < kBlocks; ++c) {
+            const uint32_t qw[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+              for (int m = 0; m < kTiles; ++m)
+                mma_16816(acc[m], a[m][0][c][2 * s], a[m][1][c][2 * s], a[m][0][c][2 * s + 1], a[m][1][c][2 * s + 1], qw[2 * s],
+                          qw[2 * s + 1]);
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m) add(acc[m], m, r0);
+        }
       }
       // sums over the four lanes of a row; lane (g, t) ends with key 8 t + g (16 keys: t of 0 and 1)
       float got;

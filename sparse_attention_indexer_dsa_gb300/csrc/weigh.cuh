@@ -30,7 +30,7 @@ __device__ __forceinline__ bool doc_info(const WeighParams& p, int d, Doc* o) {
 
 // Whether a sequence's query rows (tokens x heads of the group) are few: its keys then stream past them
 // (weigh.cu), else the queries past tiles of keys (weigh_tiles.cu).
-__device__ __forceinline__ bool by_steps(const WeighParams& p, int T) { return (int64_t)T * p.group <= kWeighStepRows; }
+__device__ __forceinline__ bool by_steps(const WeighParams& p, int T) { return (int64_t)T * p.group <= p.step_rows; }
 
 // Row r of a sequence's query rows: its token, its head of the group.
 __device__ __forceinline__ int token_of(const WeighParams& p, int r, int* g) {
