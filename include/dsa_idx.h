@@ -491,8 +491,8 @@ typedef enum { DSA_NORM_RMS = 0, DSA_NORM_LAYER = 1 } dsa_norm_t;
  *   y = R(pos) (n * weight + bias)
  * in FP32, rounded once.  R turns pair i of the first rope_dim elements (i and
  * i + rope_dim/2, or with rope_interleaved 2i and 2i + 1) by pos * freq_i,
- * freq_i = rope_base^(-2i/rope_dim) or inv_freq[i]; angles are exact to 2^-32
- * of a turn at every position.
+ * freq_i = rope_base^(-2i/rope_dim) or inv_freq[i] in double; angles are within
+ * 2^-25 of a turn of that product at every position.
  *   q, k        device [total_tokens, n_heads (n_kv_heads), head_dim] in_dtype,
  *               16-byte aligned; q_stride ..: elements from one token to the
  *               next (0 = packed; a multiple of 16 bytes), heads packed inside
@@ -555,7 +555,8 @@ size_t dsa_idx_weigh_workspace_size(int total_q, int num_seqs, int max_seqlen_q,
  *               gives it over every visible key; a row of -inf adds nothing
  *   weights     device fp32 [num_pages, n_kv_heads, page_size], 16-byte
  *               aligned: addressed by the page table like the pages' scales
- * Sequences of one call share no pages.  Only keys are read (a cache of keys
+ * Sequences of one call share no pages, and none has a page twice (the weights of
+ * its rows would be unspecified).  Only keys are read (a cache of keys
  * alone will do); they must be finite.  The same inputs give the same bits.
  * T_d > S_d, a prefix that falls, positions and pages that do not fit are
  * reported as by dsa_idx_paged_attention; where a prefix falls nothing is
@@ -599,9 +600,9 @@ dsa_status_t dsa_idx_evict_select(
  *               dsa_idx_evict_select writes it; kept_heads n_kv_heads, or 1: the
  *               same rows for every head (an index cache beside a shared choice)
  *   ws          dsa_idx_cache_workspace_size() bytes
- * Sequences share no pages.  An entry that is not above the one before it or is
- * not a row of the sequence's pages, and a length outside [0, kept_width], are
- * reported in the status; rows 0 .. kept_len[d] - 1 of that head (of that
+ * Sequences share no pages, and none has a page twice.  An entry that is not
+ * above the one before it or is not a row of the sequence's pages, and a length
+ * outside [0, kept_width], are reported in the status; rows 0 .. kept_len[d] - 1 of that head (of that
  * sequence) are then unspecified, and nothing else is touched. */
 dsa_status_t dsa_idx_cache_compact(
     void* k_pages, uint8_t* k_page_scale, void* v_pages, uint8_t* v_page_scale,

@@ -16,11 +16,17 @@ namespace {
 
 int elem_bytes(dsa_dtype_t t) { return t == DSA_DTYPE_BF16 ? 2 : 4; }
 
-// A frequency as turns per position, modulo one, in units of 2^-64.
+// A frequency as turns per position, modulo one, in units of 2^-64.  A position multiplies what is lost
+// here by up to 2^31, so 1 / (2 pi) comes in two parts and the product's rounding is kept.
 uint64_t turns_of(double freq) {
-  double turns = freq * 0.15915494309189533577;   // 1 / (2 pi)
-  turns -= std::floor(turns);
-  return turns >= 1.0 ? 0 : (uint64_t)std::ldexp(turns, 64);
+  constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;
+  auto units = [](double turns) {
+    turns -= std::nearbyint(turns);   // (exact, in [-1/2, 1/2])
+    const double u = std::ldexp(turns, 64);
+    return u < 0x1p63 ? (uint64_t)(int64_t)u : (uint64_t)1 << 63;
+  };
+  const double turns = freq * kHigh;
+  return units(turns) + units(std::fma(freq, kHigh, -turns) + freq * kLow);
 }
 
 // What forward and backward share; y: outputs, or gradients of the inputs.

@@ -14,8 +14,9 @@
 // token's cos and sin itself, each lane those of its pairs, while the first rows
 // are on their way; warps share nothing.
 //
-// An angle is pos * freq in turns, modulo one: 64-bit fixed point, so far
-// positions lose nothing (in FP32 a position of 2^20 would be off by 0.06 rad).
+// An angle is pos * freq in turns, modulo one: 64-bit fixed point, of which the
+// last step alone keeps 24 bits, so far positions lose no more than near ones (in
+// FP32 a position of 2^20 would be off by 0.06 rad).
 #include <cuda_bf16.h>
 
 #include "norm_params.h"

@@ -595,3 +595,63 @@ def test_streams_and_graphs():
     s.synchronize()
     assert torch.equal(got[0], kept) and torch.equal(got[1], n) and torch.equal(w1, w2)
     assert torch.equal(c1.k, c2.k) and torch.equal(c1.v, c2.v) and torch.equal(c1.k_scale, c2.k_scale)
+
+
+def test_two_calls_at_once():
+    """Two streams with caches and workspaces of their own, steps and tiles in one call."""
+    rng = np.random.default_rng(62)
+    b = Batch(rng, [(1, 900), (300, 2000), (40, 700)], 2, 128, 16, "mxfp8")
+    q, qd = queries(rng, b.total_q, 16, 128)
+    lse = dev(true_lse(b, q, 8, 0.1))
+    w0 = E.random_weights(rng, b)
+    args = [b.dev(n) for n in ("cu_q", "cu_k", "table")]
+    streams = [torch.cuda.current_stream(), torch.cuda.Stream(), torch.cuda.Stream()]
+    state = [(b.cache(dsa), dev(w0), dsa.weigh_workspace(b.total_q, 3, 300, 16, 2, 128), dsa.cache_workspace()) for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for (c, w, ws, cw), s in zip(state, streams):
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                dsa.cache_weigh(c, w, qd, lse, *args, 300, 2000, sm_scale=0.1, ws=ws)
+            got.append(dsa.evict_select(w, args[1], args[2], 500, 2000, sinks=2, recent=30, ws=cw))
+            dsa.cache_compact(c, *got[-1], args[2], weights=w, ws=cw)
+        if s is streams[0]:
+            torch.cuda.synchronize()      # the first alone, the others beside one another
+    torch.cuda.synchronize()
+    for i in (1, 2):
+        assert torch.equal(got[i][0], got[0][0]) and torch.equal(got[i][1], got[0][1])
+        assert torch.equal(state[i][1], state[0][1]) and all(
+            torch.equal(getattr(state[i][0], n), getattr(state[0][0], n)) for n in ("k", "v", "k_scale", "v_scale"))
+
+
+@pytest.mark.parametrize("prec,pages", [("bf16", 150000), ("mxfp8", 300000)])
+def test_rows_behind_four_gigabytes(prec, pages):
+    """The same sequences at the end of a cache whose keys are more than 2^32 bytes: the same bits."""
+    rng = np.random.default_rng(63)
+    b = Batch(rng, [(1, 400), (90, 700)], 2, 128, 64, prec)
+    q, qd = queries(rng, b.total_q, 16, 128)
+    lse = dev(true_lse(b, q, 8, 0.1))
+    w0 = dev(E.random_weights(rng, b))
+    cu_q, cu_k, table = (b.dev(n) for n in ("cu_q", "cu_k", "table"))
+
+    def run(c, w, table):
+        dsa.cache_weigh(c, w, qd, lse, cu_q, cu_k, table, 90, 700, sm_scale=0.1)
+        kept = dsa.evict_select(w, cu_k, table, 150, 700, sinks=1, recent=20)
+        dsa.cache_compact(c, *kept, table, weights=w)
+        return kept
+
+    small, w = b.cache(dsa), w0.clone()
+    n = small.k.shape[0]
+    far = dsa.paged_cache(pages, 64, 2, 128, prec)
+    fw = dsa.paged_weights(far)
+    names = [x for x in ("k", "v", "k_scale", "v_scale") if getattr(small, x) is not None]
+    for x in names:
+        getattr(far, x)[-n:] = getattr(small, x)
+    assert far.k[:-n].numel() * far.k.element_size() > 2 ** 32
+    fw[-n:] = w
+    want, got = run(small, w, table), run(far, fw, torch.where(table >= 0, table + (pages - n), table))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(fw[-n:], w)
+    assert not fw[:-n].any()
+    for x in names:
+        a, e = getattr(far, x)[-n:], getattr(small, x)
+        assert torch.equal(a.view(torch.uint8), e.view(torch.uint8)), x   # (unused slots hold NaN)

@@ -239,3 +239,58 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     assert torch.equal(y[0], want[0]) and torch.equal(y[1], want[1])
     assert all(torch.equal(a, b) for a, b in zip(g, gw) if a is not None)
+
+
+def test_angles_of_the_farthest_positions():
+    """Turns from the frequencies' own bits in rational arithmetic: an angle is as good at 2^31 positions as at one."""
+    from fractions import Fraction
+    pi = Fraction(314159265358979323846264338327950288419716939937510582097494459, 10 ** 62)
+    rng = np.random.default_rng(8)
+    at = [0, 1, 2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, 1900000001, -1700000003]
+    q, k, _, w = inputs(rng, len(at), 3, 1, 128, "f32", "rms")
+    pos = torch.tensor(at, dtype=torch.int32, device="cuda")
+    freq = [float(f) for f in np.concatenate([rng.uniform(-1.0, 1.0, 60), [1.0, 1e-9, -1e-9, 1234.567]])]
+    got = dsa.norm_rope(q, k, pos, *w, eps=EPS, inv_freq=freq)
+    ang = np.array([[float((Fraction(f) * p / (2 * pi)) % 1) for f in freq] for p in at]) * (2 * np.pi)
+    for x, y, wi in ((q, got[0], w[0]), (k, got[1], w[1])):
+        a = (host(x), host(wi), None, host(pos))
+        want = R.rotate(R.forward(*a, "rms", EPS, 0, False), ang, 128, False)
+        close(y, want, R.forward_tol(*a, "rms", EPS, 128, False, "f32", want), "far")
+
+
+def test_two_calls_at_once():
+    rng = np.random.default_rng(14)
+    q, k, pos, w = inputs(rng, 3000, 8, 2, 128, "bf16", "layer")
+    d = torch.randn(3000, 10, 128, device="cuda").bfloat16()
+    want, gw = dsa.norm_rope(q, k, pos, *w, norm="layer"), grads(q, k, pos, w, d[:, :8], d[:, 8:], "layer", 128, False)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [dsa.norm_rope_workspace(128) for _ in streams]
+    got = [[] for _ in streams]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((dsa.norm_rope(q, k, pos, *w, norm="layer"),
+                               grads(q, k, pos, w, d[:, :8], d[:, 8:], "layer", 128, False, spaces[i])))
+    torch.cuda.synchronize()
+    for y, g in got[0] + got[1]:
+        assert torch.equal(y[0], want[0]) and torch.equal(y[1], want[1])
+        assert all(torch.equal(a, b) for a, b in zip(g, gw))
+
+
+def test_more_than_32_bits_of_elements():
+    T, H, D = 540000, 64, 128            # 4.4e9 elements
+    rng = np.random.default_rng(15)
+    tail, _, pos, w = inputs(rng, 50, H, 1, D, "bf16", "rms", strided=False)
+    d = torch.randn(50, H, D, device="cuda").bfloat16()
+    q, g = torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda")
+    q[-50:], g[-50:] = tail, d
+    at = torch.zeros(T, dtype=torch.int32, device="cuda")
+    at[-50:] = pos
+    got, _ = dsa.norm_rope(q, None, at, w[0])
+    want, _ = dsa.norm_rope(tail, None, pos, w[0])
+    assert torch.equal(got[-50:], want) and not got[:-50].any()
+    del got
+    a, b = dsa.norm_rope_backward(g, None, q, None, at, w[0]), dsa.norm_rope_backward(d, None, tail, None, pos, w[0])
+    assert torch.equal(a.q[-50:], b.q) and not a.q[:-50].any()
