@@ -27,11 +27,11 @@ struct WeighParams {
   unsigned long long timeout_ns;
 };
 
-// Query rows of a sequence up to which its keys stream past them, 8-bit ones and BF16 ones (a tile kernel widens
-// 8-bit keys on few warps, and its query tiles are empty but for these rows).  Streaming / tiles, us, 32 sequences of
+// Query rows of a sequence up to which its keys stream past them, 8-bit ones and BF16 ones (the tile kernel has to
+// widen 8-bit keys to BF16 first, and its query tiles are empty but for these rows).  Streaming / tiles, us, 32 sequences of
 // 2048 - 8192 keys, 8 key heads of 128 dimensions:
 //   BF16     16 rows  75 / 98     32 rows 128 / 94     64 rows 217 / 97
-//   MXFP8    16 rows  77 / 229    32 rows 103 / 220    64 rows 156 / 220    128 rows 425 / 222
+//   MXFP8    32 rows 103 / 155    64 rows 156 / 157    128 rows 425 / 179
 constexpr int kWeighStepRows8 = 64, kWeighStepRows16 = 16;
 constexpr int kWeighCols = 256;    // query rows of a tile
 constexpr int kWeighKeys = 256;    // keys of a unit

@@ -16,7 +16,11 @@
 // read from the L2 twice as often.)
 //
 // Queries come by TMA (a box of tokens x heads is the tile as the MMA reads it),
-// keys row by row through the page table, 8-bit ones widened on the way.  The
+// keys row by row through the page table, 8-bit ones widened on the way: that takes a
+// warp some 1500 cycles for 32 rows, so eight warps do it, and the warps that weigh keep
+// their 80 registers (ragged chunks over FP8 rows 143 -> 141 us; 8 tokens of each of 32
+// sequences of 2048 - 8192 MXFP8 rows, which change keys all the time, 221 -> 157; four
+// warps of BF16 rows have but copies to issue, 96 us for the latter).  The
 // query tiles of all units in a row are shared out evenly: a block takes a
 // consecutive part, so that it changes keys seldom and all end together.  Where a
 // part's end divides a unit, a second kernel adds the pieces in their order.
@@ -34,7 +38,6 @@ namespace weigh {
 
 using namespace attn;
 
-constexpr int kTileThreads = 768;
 constexpr int kGroups = 64;            // sequences are counted in this many groups
 constexpr int kHalf = kWeighCols / 2;  // columns of a product and of a hand-over
 constexpr int kBiasRing = 4;
@@ -209,8 +212,19 @@ struct Cursor {
   }
 };
 
+// Warps of a block: sixteen turn products into weights, four (BF16) or eight (8-bit keys, which they widen) bring keys,
+// the last four queries, biases and products.
+template <bool Q8>
+struct Roles {
+  static constexpr int kKeyWarps = Q8 ? 8 : 4;
+  static constexpr int kThreads = 32 * (16 + kKeyWarps + 4);
+  // registers of a thread with 8-bit keys, whose warpgroups share them unevenly: 72 each at launch
+  static constexpr int kWeighRegs = 80, kKeyRegs = 64, kRestRegs = 56;
+  static_assert(512 * kWeighRegs + 256 * kKeyRegs + 128 * kRestRegs <= 896 * 72, "no more than the block was launched with");
+};
+
 template <int D, bool Q8>
-__global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
+__global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) weigh_tiles_kernel(const __grid_constant__ WeighParams p) {
   using L = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -220,7 +234,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
   int* const status = ctl;
   volatile int* const abort_flag = ctl + 1;
   auto bar = [&](int i) { return sbase + L::kOffBars + 8u * i; };
-  constexpr int kKeyWarp = 16, kQueryWarp = 20, kBiasWarp = 21, kMmaWarp = 22;
+  using R = Roles<Q8>;
+  constexpr int kThreads = R::kThreads, kKeyWarp = 16, kQueryWarp = kKeyWarp + R::kKeyWarps, kBiasWarp = kQueryWarp + 1;
+  constexpr int kMmaWarp = kQueryWarp + 2;
   if (tid == 0) {
     ctl[0] = (sbase & 1023u) ? DSA_DEV_ERR_BOUNDS : 0;   // the swizzle needs a 1024-byte base
     ctl[1] = (sbase & 1023u) ? 1 : 0;
@@ -245,7 +261,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(ctl + 2), 512);
   if (kWeighCols % p.group != 0) {   // rows that no box covers read as zeros
-    for (uint32_t i = tid * 16; i < L::kStages * L::kQueryTile; i += kTileThreads * 16)
+    for (uint32_t i = tid * 16; i < L::kStages * L::kQueryTile; i += kThreads * 16)
       *reinterpret_cast<uint4*>(smem + L::kOffQ + i) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
@@ -267,6 +283,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
 
   if (warp < 16) {
     // ======================= weights: a key to a thread =======================
+    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kWeighRegs));
     const int w = (warp >> 2) & 1, half = warp >> 3, quarter = warp & 3, c0 = half * kHalf;
     const uint32_t t_s = tmem + (uint32_t)(w * kWeighCols + c0) + ((uint32_t)quarter << 21);
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
@@ -363,30 +380,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
     }
   } else if (warp < kQueryWarp) {
     // ======================= keys =======================
-    const int kw = warp - kKeyWarp;   // a quarter of a tile
+    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kKeyRegs));
+    // a quarter of a tile: of both in turn, or (8-bit keys) of one
+    constexpr int kTiles = Q8 ? 1 : 2;
+    const int kw = (warp - kKeyWarp) & 3, w0 = (warp - kKeyWarp) >> 2;
     uint32_t nk = 0;
     bool ok = true, bad_page = false;
     while (ok && cur.next(&x)) {
       if (x.n == 0) continue;
-      uint32_t rows[2];   // this lane's of either tile
+      uint32_t rows[kTiles];   // this lane's
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int key = x.key0 + w * 128 + kw * 32 + lane;
+      for (int i = 0; i < kTiles; ++i) {
+        const int key = x.key0 + (w0 + i) * 128 + kw * 32 + lane;
         const int64_t mine = key < x.S ? cache_row(p.c, x.d, key, x.h) : -1;
         if (key < x.S && mine < 0) bad_page = true;
-        rows[w] = mine < 0 ? ~0u : (uint32_t)mine;
-        // on its way to the L2 while the last unit's keys are still in use
-        constexpr int kRowBytes = D * (Q8 ? 1 : 2);
-        if (rows[w] != ~0u) {
+        rows[i] = mine < 0 ? ~0u : (uint32_t)mine;
+        if (!Q8 && rows[i] != ~0u) {   // on its way to the L2 while the last unit's keys are still in use
 #pragma unroll
-          for (int i = 0; i < kRowBytes; i += 128)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(p.c.k) + (size_t)rows[w] * kRowBytes + i));
+          for (int o = 0; o < D * 2; o += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(p.c.k) + (size_t)rows[i] * (D * 2) + o));
         }
       }
 #pragma unroll 1
-      for (int w = 0; w < 2 && ok; ++w) {
-        const uint32_t row32 = w ? rows[1] : rows[0];
-        const uint32_t dst = sbase + w * L::kKeyTile + kw * 32 * 128;
+      for (int i = 0; i < kTiles && ok; ++i) {
+        const int w = w0 + i;
+        const uint32_t row32 = kTiles == 2 && i ? rows[kTiles - 1] : rows[0], dst = sbase + w * L::kKeyTile + kw * 32 * 128;
         auto wait_empty = [&] {
           if (nk > 0) ok = __all_sync(0xffffffffu, wait_bar(bar(K_EMPTY + w), (nk - 1) & 1u, abort_flag, status, tmo));
         };
@@ -395,24 +413,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
           constexpr int PPR = D / 16, RPP = 32 / PPR, kPasses = 32 / RPP;
           const int c = lane % PPR, rsub = lane / PPR;
           const uint8_t* const src = reinterpret_cast<const uint8_t*>(p.c.k) + c * 16;
-          const int sc = p.c.sw == 1 ? 0 : c >> 1;
+          uint32_t scales = 0;   // of this lane's row, a byte to each block
+          if (row32 != ~0u) {
+            if (p.c.sw == 1) scales = __ldg(p.c.k_scale + row32) * 0x01010101u;
+            else if constexpr (D == 128) scales = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_scale) + row32);
+            else scales = __ldg(reinterpret_cast<const uint16_t*>(p.c.k_scale) + row32);
+          }
           uint4 v[kPasses];
-          uint32_t e8[kPasses];
 #pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const uint32_t r = __shfl_sync(0xffffffffu, row32, i * RPP + rsub);
-            v[i] = r == ~0u ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * D));
-            e8[i] = r == ~0u ? 0u : __ldg(p.c.k_scale + (size_t)r * p.c.sw + sc);
+          for (int j = 0; j < kPasses; ++j) {
+            const uint32_t r = __shfl_sync(0xffffffffu, row32, j * RPP + rsub);
+            v[j] = r == ~0u ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * D));
           }
           wait_empty();
           if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const int r = i * RPP + rsub;
-            const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          for (int j = 0; j < kPasses; ++j) {
+            const int r = j * RPP + rsub;
+            const uint32_t w4[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
             uint32_t o[8];
-            if (e8[i] <= 134u) widen<false>(w4, e8[i], o);
-            else widen<true>(w4, e8[i], o);
+            const uint32_t e8 = (__shfl_sync(0xffffffffu, scales, r) >> (8 * (c >> 1))) & 255u;
+            if (e8 <= 134u) widen<false>(w4, e8, o);
+            else widen<true>(w4, e8, o);
             const uint32_t at = dst + (uint32_t)(c >> 2) * (128 * 128) + r * 128;
             st_shared_v4(at + ((((c & 3) * 2) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
             st_shared_v4(at + ((((c & 3) * 2 + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
@@ -424,9 +446,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
           wait_empty();
           if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < 32; i += RPP) {
-            const uint32_t e = __shfl_sync(0xffffffffu, row32, i + rsub);
-            const int r = i + rsub;
+          for (int j = 0; j < 32; j += RPP) {
+            const uint32_t e = __shfl_sync(0xffffffffu, row32, j + rsub);
+            const int r = j + rsub;
             cp_async16(dst + (uint32_t)(c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                        src + (size_t)(e == ~0u ? 0 : e) * D, e != ~0u);
           }
@@ -439,104 +461,107 @@ __global__ void __launch_bounds__(kTileThreads, 1) weigh_tiles_kernel(const __gr
       ++nk;
     }
     if (bad_page) set_status(status, DSA_DEV_ERR_INVALID_ARG);
-  } else if (warp == kQueryWarp) {
-    // ======================= queries =======================
-    const uint32_t bytes = (uint32_t)tq * p.group * D * 2;
-    uint32_t nt = 0;
-    bool ok = true;
-    while (ok && cur.next(&x)) {
-      for (int j = 0; j < x.n; ++j, ++nt) {
-        const uint32_t st = nt % L::kStages, round = nt / L::kStages;
-        if (round > 0) ok = __all_sync(0xffffffffu, wait_bar(bar(Q_EMPTY + st), (round - 1) & 1u, abort_flag, status, tmo));
-        if (!ok) break;
-        const bool withheld = p.fault_inject == 1 && nt == 0;   // (tests)
-        if (!withheld && elect_one()) {
-          mbar_arrive_expect_tx(bar(Q_FULL + st), bytes);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sbase + L::kOffQ + st * L::kQueryTile + c * (kWeighCols * 128), &p.tm_q, bar(Q_FULL + st), c * 64,
-                        x.h * p.group, x.q0 + x.i0 + j * tq);
-        }
-        __syncwarp();
-      }
-    }
-    // After an abort: the copies in flight land before the block ends (the last use of every stage).
-    if (*abort_flag && elect_one()) {
-      const uint32_t last = nt < L::kStages ? 0 : nt - L::kStages;
-      for (uint32_t i = last; i < nt; ++i)
-        if (!(p.fault_inject == 1 && i == 0)) drain_wait(bar(Q_FULL + i % L::kStages), (i / L::kStages) & 1u, tmo);
-    }
-    __syncwarp();
-  } else if (warp == kBiasWarp) {
-    // ======================= biases, and the last key that a row sees =======================
-    uint32_t nt = 0;
-    bool ok = true;
-    while (ok && cur.next(&x)) {
-      for (int j = 0; j < x.n; ++j, ++nt) {
-        const uint32_t slot = nt % kBiasRing, round = nt / kBiasRing;
-        const int i0 = x.i0 + j * tq, tokens = min(tq, x.T - i0);
-        float b[kWeighCols / 32];
-        int s[kWeighCols / 32];
-#pragma unroll
-        for (int i = 0; i < kWeighCols / 32; ++i) {
-          int g;
-          const int t = token_of(p, i * 32 + lane, &g);
-          const bool there = t < tokens;
-          b[i] = there ? __ldg(p.lse + (int64_t)(x.q0 + i0 + t) * p.n_heads + x.h * p.group + g) : -INFINITY;
-          s[i] = there ? x.P0 + i0 + t : -1;
-        }
-        if (round > 0) ok = __all_sync(0xffffffffu, wait_bar(bar(B_EMPTY + slot), (round - 1) & 1u, abort_flag, status, tmo));
-        if (!ok) break;
-        float* const bias = reinterpret_cast<float*>(smem + L::kOffBias) + slot * kWeighCols;
-        int* const seen = reinterpret_cast<int*>(smem + L::kOffBias) + (kBiasRing + slot) * kWeighCols;
-#pragma unroll
-        for (int i = 0; i < kWeighCols / 32; ++i) {
-          bias[i * 32 + lane] = bias_of(b[i]);
-          seen[i * 32 + lane] = s[i];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_FULL + slot));
-      }
-    }
   } else {
-    // ======================= products: a warp to a tile of keys =======================
-    const int w = warp - kMmaWarp;
-    if (elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16(128, kHalf);
-      const uint64_t k0 = sw128_kmajor_desc(sbase + w * L::kKeyTile, 0);
-      uint32_t nt = 0, nk = 0;
+    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kRestRegs));
+    if (warp == kQueryWarp) {
+      // ======================= queries =======================
+      const uint32_t bytes = (uint32_t)tq * p.group * D * 2;
+      uint32_t nt = 0;
       bool ok = true;
       while (ok && cur.next(&x)) {
-        for (int j = 0; j < x.n && ok; ++j, ++nt) {
-          const uint32_t st = nt % L::kStages;
-          ok = wait_bar(bar(Q_FULL + st), (nt / L::kStages) & 1u, abort_flag, status, tmo);
-          if (ok && j == 0) ok = wait_bar(bar(K_FULL + w), nk & 1u, abort_flag, status, tmo);
-          const uint64_t q0 = sw128_kmajor_desc(sbase + L::kOffQ + st * L::kQueryTile, 0);
+        for (int j = 0; j < x.n; ++j, ++nt) {
+          const uint32_t st = nt % L::kStages, round = nt / L::kStages;
+          if (round > 0) ok = __all_sync(0xffffffffu, wait_bar(bar(Q_EMPTY + st), (round - 1) & 1u, abort_flag, status, tmo));
+          if (!ok) break;
+          const bool withheld = p.fault_inject == 1 && nt == 0;   // (tests)
+          if (!withheld && elect_one()) {
+            mbar_arrive_expect_tx(bar(Q_FULL + st), bytes);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (ok && nt > 0) ok = wait_bar(bar(S_EMPTY + 2 * w + half), (nt - 1) & 1u, abort_flag, status, tmo);
-            if (!ok) break;
-            tc_fence_after();
-            uint64_t kd = k0, qd = q0 + half * ((kHalf * 128) >> 4);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c, kd += (128 * 128) >> 4, qd += (kWeighCols * 128) >> 4) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)   // 32 bytes a step
-                mma_bf16(tmem + w * kWeighCols + half * kHalf, kd + 2 * k, qd + 2 * k, idesc, c + k > 0);
-            }
-            tc_commit(bar(S_FULL + 2 * w + half));
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(sbase + L::kOffQ + st * L::kQueryTile + c * (kWeighCols * 128), &p.tm_q, bar(Q_FULL + st), c * 64,
+                          x.h * p.group, x.q0 + x.i0 + j * tq);
           }
-          if (ok) tc_commit(bar(Q_EMPTY + st));
-          if (ok && j + 1 == x.n) tc_commit(bar(K_EMPTY + w));
+          __syncwarp();
         }
-        if (x.n > 0) ++nk;
       }
-      if (!ok) {   // what was issued completes before the tensor memory is given back
-        tc_commit(bar(DRAIN + w));
-        drain_wait(bar(DRAIN + w), 0, tmo);
+      // After an abort: the copies in flight land before the block ends (the last use of every stage).
+      if (*abort_flag && elect_one()) {
+        const uint32_t last = nt < L::kStages ? 0 : nt - L::kStages;
+        for (uint32_t i = last; i < nt; ++i)
+          if (!(p.fault_inject == 1 && i == 0)) drain_wait(bar(Q_FULL + i % L::kStages), (i / L::kStages) & 1u, tmo);
       }
+      __syncwarp();
+    } else if (warp == kBiasWarp) {
+      // ======================= biases, and the last key that a row sees =======================
+      uint32_t nt = 0;
+      bool ok = true;
+      while (ok && cur.next(&x)) {
+        for (int j = 0; j < x.n; ++j, ++nt) {
+          const uint32_t slot = nt % kBiasRing, round = nt / kBiasRing;
+          const int i0 = x.i0 + j * tq, tokens = min(tq, x.T - i0);
+          float b[kWeighCols / 32];
+          int s[kWeighCols / 32];
+#pragma unroll
+          for (int i = 0; i < kWeighCols / 32; ++i) {
+            int g;
+            const int t = token_of(p, i * 32 + lane, &g);
+            const bool there = t < tokens;
+            b[i] = there ? __ldg(p.lse + (int64_t)(x.q0 + i0 + t) * p.n_heads + x.h * p.group + g) : -INFINITY;
+            s[i] = there ? x.P0 + i0 + t : -1;
+          }
+          if (round > 0) ok = __all_sync(0xffffffffu, wait_bar(bar(B_EMPTY + slot), (round - 1) & 1u, abort_flag, status, tmo));
+          if (!ok) break;
+          float* const bias = reinterpret_cast<float*>(smem + L::kOffBias) + slot * kWeighCols;
+          int* const seen = reinterpret_cast<int*>(smem + L::kOffBias) + (kBiasRing + slot) * kWeighCols;
+#pragma unroll
+          for (int i = 0; i < kWeighCols / 32; ++i) {
+            bias[i * 32 + lane] = bias_of(b[i]);
+            seen[i * 32 + lane] = s[i];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_FULL + slot));
+        }
+      }
+    } else {
+      // ======================= products: a warp to a tile of keys =======================
+      const int w = warp - kMmaWarp;
+      if (elect_one()) {
+        constexpr uint32_t idesc = idesc_bf16(128, kHalf);
+        const uint64_t k0 = sw128_kmajor_desc(sbase + w * L::kKeyTile, 0);
+        uint32_t nt = 0, nk = 0;
+        bool ok = true;
+        while (ok && cur.next(&x)) {
+          for (int j = 0; j < x.n && ok; ++j, ++nt) {
+            const uint32_t st = nt % L::kStages;
+            ok = wait_bar(bar(Q_FULL + st), (nt / L::kStages) & 1u, abort_flag, status, tmo);
+            if (ok && j == 0) ok = wait_bar(bar(K_FULL + w), nk & 1u, abort_flag, status, tmo);
+            const uint64_t q0 = sw128_kmajor_desc(sbase + L::kOffQ + st * L::kQueryTile, 0);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (ok && nt > 0) ok = wait_bar(bar(S_EMPTY + 2 * w + half), (nt - 1) & 1u, abort_flag, status, tmo);
+              if (!ok) break;
+              tc_fence_after();
+              uint64_t kd = k0, qd = q0 + half * ((kHalf * 128) >> 4);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c, kd += (128 * 128) >> 4, qd += (kWeighCols * 128) >> 4) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)   // 32 bytes a step
+                  mma_bf16(tmem + w * kWeighCols + half * kHalf, kd + 2 * k, qd + 2 * k, idesc, c + k > 0);
+              }
+              tc_commit(bar(S_FULL + 2 * w + half));
+            }
+            if (ok) tc_commit(bar(Q_EMPTY + st));
+            if (ok && j + 1 == x.n) tc_commit(bar(K_EMPTY + w));
+          }
+          if (x.n > 0) ++nk;
+        }
+        if (!ok) {   // what was issued completes before the tensor memory is given back
+          tc_commit(bar(DRAIN + w));
+          drain_wait(bar(DRAIN + w), 0, tmo);
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
   // The steps' kernel, whose rows are those of other sequences, is over when this one is; the next may begin.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -590,7 +615,7 @@ cudaError_t launch_tiles(const WeighParams& p, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(p.tile_blocks);
-  cfg.blockDim = dim3(kTileThreads);
+  cfg.blockDim = dim3(Roles<Q8>::kThreads);
   cfg.dynamicSmemBytes = Layout<D>::kSmem;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess || p.tile_blocks == 1) return e;
   cfg.gridDim = dim3(p.tile_blocks - 1);
