@@ -19,6 +19,8 @@
 // FP32 a position of 2^20 would be off by 0.06 rad).
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "norm_params.h"
 
 namespace dsa {
@@ -264,95 +266,192 @@ __global__ void __launch_bounds__(kNormThreads, Batch<IN>::kBlocks) norm_rope_ke
 
 // Warps take shares in turn and keep the gradients of the weights in registers, each lane those of its
 // own eight columns; what a block has gathered goes to the workspace, and a second kernel adds the
-// blocks' sums in their order, so that the same inputs give the same bits.
-constexpr int kBackBatch = 2;
+// blocks' sums in their order, so that the same inputs give the same bits.  The rows of the steps to come
+// are copied into shared memory of the warp's own, beyond a token's end too.  16384 tokens of 40 heads, BF16:
+// 88 us = 84 % of the copy rate; with the next rows in registers 96, steps of 2 rows to a lane 93, four
+// stages (one block to an SM) 129.
+constexpr int kBackWide = 4;     // rows of a lane in a step, of 16-bit rows
+constexpr int kBackRows = 2;     // of others, and of a share at least
+constexpr int kBackStages = 3;   // steps of a warp in shared memory
+constexpr int kBackBlocks = 2;   // of an SM
+
+// A warp's way through its shares, a step's rows at a time.
+template <int ROWS>
+struct Walk {
+  unsigned tok, dtok;
+  int part, dpart, kind, h, hi;
+  bool live;
+  __device__ __forceinline__ Walk(const NormRopeParams& p, unsigned first, unsigned warps) {
+    tok = first / p.parts;
+    part = (int)(first - tok * p.parts);
+    dtok = warps / p.parts;
+    dpart = (int)(warps - dtok * p.parts);
+    enter(p);
+  }
+  __device__ __forceinline__ void enter(const NormRopeParams& p) {
+    live = tok < (unsigned)p.tokens;
+    const Share s(p, part, 0);
+    kind = 0;
+    h = s.lo;
+    hi = s.hi;
+    if (h >= hi) keys(p);
+  }
+  __device__ __forceinline__ bool keys(const NormRopeParams& p) {
+    const Share s(p, part, 1);
+    kind = 1;
+    h = s.lo;
+    hi = s.hi;
+    return h < hi;
+  }
+  __device__ __forceinline__ void next(const NormRopeParams& p) {
+    h += ROWS;
+    if (h < hi || (kind == 0 && keys(p))) return;
+    tok += dtok;
+    part += dpart;
+    if (part >= p.parts) {
+      part -= p.parts;
+      ++tok;
+    }
+    enter(p);
+  }
+};
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Sizes of a step in shared memory.
+template <int D, bool IN, bool GRAD>
+struct BackStep {
+  static constexpr int kEach = IN && GRAD ? kBackWide : kBackRows;
+  static constexpr int kRows = kEach * 32 / (D / 8);
+  static constexpr int kX = kRows * D * (IN ? 2 : 4), kG = kRows * D * (GRAD ? 2 : 4);
+  static constexpr int kBytes = kX + kG + 16;   // rows, their gradients, the token's position
+  static constexpr int kSmem = kNormThreads / 32 * kBackStages * kBytes;
+  static_assert(kSmem >= kNormThreads * 8 * 4, "the lanes' sums meet in the same place");
+};
+
+template <bool BF16>
+__device__ __forceinline__ void read4(Raw<BF16>& r, const uint8_t* base, int elem) {
+  if constexpr (BF16) r.v = *reinterpret_cast<const uint2*>(base + elem * 2);
+  else r.v = *reinterpret_cast<const float4*>(base + elem * 4);
+}
 
 template <int D, bool IN, bool GRAD, bool LAYER>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_rope_back_kernel(const __grid_constant__ NormRopeBackParams q) {
+__global__ void __launch_bounds__(kNormThreads, kBackBlocks) norm_rope_back_kernel(const __grid_constant__ NormRopeBackParams q) {
+  using St = BackStep<D, IN, GRAD>;
   constexpr int LPR = D / 8, RPS = 32 / LPR, kRows = kNormThreads / LPR;
-  __shared__ __align__(16) float red[kRows * D];
+  extern __shared__ __align__(128) uint8_t ring[];
   const NormRopeParams& p = q.f;
-  const int lane = threadIdx.x & 31, sub = lane / LPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR;
   const Lane<D> at(p.rope, lane % LPR);
-  Elems dw[2], db[2];
+  uint8_t* const own = ring + warp * kBackStages * St::kBytes;
+  const uint32_t sown = (uint32_t)__cvta_generic_to_shared(own);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the sums' kernel waits for this one's end)
+  // sums of the kind of rows at hand, and of the other
+  Elems dw, db, dw2, db2;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) dw[0].v[e] = dw[1].v[e] = db[0].v[e] = db[1].v[e] = both(0.f);
-  const int64_t tasks = (int64_t)p.tokens * p.parts, warps = (int64_t)gridDim.x * (kNormThreads / 32);
-  for (int64_t task = (int64_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5); task < tasks; task += warps) {
-    const int tok = (int)(task / p.parts), part = (int)(task - (int64_t)tok * p.parts);
-    const int pos = p.rope.dim > 0 ? __ldg(p.pos + tok) : 0;
-    Turn tn;
-    bool turned = false;
+  for (int e = 0; e < 4; ++e) dw.v[e] = db.v[e] = dw2.v[e] = db2.v[e] = both(0.f);
+  const unsigned first = blockIdx.x * (kNormThreads / 32) + warp, warps = gridDim.x * (kNormThreads / 32);
+  Walk<St::kRows> ahead(p, first, warps), now = ahead;
+  int put = 0, get = 0;   // slots
+  auto fetch = [&] {
+    if (ahead.live) {
+      const int n = min(St::kRows, ahead.hi - ahead.h) * D;
+      const uint8_t* const x = reinterpret_cast<const uint8_t*>(p.x[ahead.kind]) +
+                               ((int64_t)ahead.tok * p.x_stride[ahead.kind] + ahead.h * D) * (IN ? 2 : 4);
+      const uint8_t* const g = reinterpret_cast<const uint8_t*>(q.dy[ahead.kind]) +
+                               ((int64_t)ahead.tok * q.dy_stride[ahead.kind] + ahead.h * D) * (GRAD ? 2 : 4);
+      const uint32_t dst = sown + put * St::kBytes;
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      const Share sh(p, part, kind);
-      if (sh.lo >= sh.hi) continue;
-      const Elems w = load_w<D>(p.w[kind], p.w_bf16, at, 1.f);
-      const int64_t x0 = (int64_t)tok * p.x_stride[kind], g0 = (int64_t)tok * q.dy_stride[kind];
-      const int64_t y0 = (int64_t)tok * p.y_stride[kind];
-      Raw<IN> raw[kBackBatch][2];
-      Raw<GRAD> grad[kBackBatch][2];
-      auto load = [&](int h0) {
+      for (int o = 0; o < St::kX; o += 512)
+        if (o + lane * 16 < n * (IN ? 2 : 4)) copy_async(dst + o + lane * 16, x + o + lane * 16);
 #pragma unroll
-        for (int i = 0; i < kBackBatch; ++i) {
-          const int h = min(h0 + i * RPS, sh.hi - 1) * D;   // (all lanes take part in the sums)
-          load4<IN>(raw[i][0], p.x[kind], x0 + h + at.a);
-          load4<IN>(raw[i][1], p.x[kind], x0 + h + at.b);
-          load4<GRAD>(grad[i][0], q.dy[kind], g0 + h + at.a);
-          load4<GRAD>(grad[i][1], q.dy[kind], g0 + h + at.b);
+      for (int o = 0; o < St::kG; o += 512)
+        if (o + lane * 16 < n * (GRAD ? 2 : 4)) copy_async(dst + St::kX + o + lane * 16, g + o + lane * 16);
+      if (p.rope.dim > 0 && lane == 0)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + St::kX + St::kG), "l"(p.pos + ahead.tok) : "memory");
+      ahead.next(p);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    put = put + 1 < kBackStages ? put + 1 : 0;
+  };
+#pragma unroll
+  for (int i = 0; i < kBackStages - 1; ++i) fetch();
+  Turn tn;
+  Elems w;
+  int kind = -1;   // whose sums dw and db are
+  unsigned tok = ~0u;
+  while (now.live) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kBackStages - 2) : "memory");
+    __syncwarp();
+    fetch();   // (into the slot that all lanes have read a step ago)
+    const uint8_t* const slot = own + get * St::kBytes;
+    get = get + 1 < kBackStages ? get + 1 : 0;
+    if (now.tok != tok) {
+      tok = now.tok;
+      tn = angles<D>(p.rope, p.rope.dim > 0 ? *reinterpret_cast<const int*>(slot + St::kX + St::kG) : 0, at);
+    }
+    if (now.kind != kind) {   // (at first both are zeros)
+      kind = now.kind;
+      w = load_w<D>(p.w[kind], p.w_bf16, at, 1.f);
+      Elems t = dw;
+      dw = dw2;
+      dw2 = t;
+      t = db;
+      db = db2;
+      db2 = t;
+    }
+    const int64_t y0 = (int64_t)now.tok * p.y_stride[kind];
+#pragma unroll
+    for (int i = 0; i < St::kEach; ++i) {
+      if (now.h + i * RPS >= now.hi) break;
+      const int r = i * RPS + sub, h = now.h + r;
+      const bool there = h < now.hi;   // (else what the slot held before: all lanes take part in the sums)
+      Raw<IN> raw[2];
+      Raw<GRAD> grad[2];
+      read4<IN>(raw[0], slot, r * D + at.a);
+      read4<IN>(raw[1], slot, r * D + at.b);
+      read4<GRAD>(grad[0], slot + St::kX, r * D + at.a);
+      read4<GRAD>(grad[1], slot + St::kX, r * D + at.b);
+      Elems x = widen<IN>(raw), g = widen<GRAD>(grad);
+      const float inv = normalise<D, LAYER>(x, p.eps);
+      turn<true>(g, tn, p.rope.interleaved);
+      float2 dot, sum;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (there) {
+          dw.v[e] = __ffma2_rn(g.v[e], x.v[e], dw.v[e]);
+          if (LAYER) db.v[e] = __fadd2_rn(db.v[e], g.v[e]);
         }
-      };
-      load(sh.lo + sub);
-      if (!turned) {
-        tn = angles<D>(p.rope, pos, at);
-        turned = true;
+        g.v[e] = __fmul2_rn(g.v[e], w.v[e]);
+        dot = e == 0 ? __fmul2_rn(g.v[e], x.v[e]) : __ffma2_rn(g.v[e], x.v[e], dot);
+        if (LAYER) sum = e == 0 ? g.v[e] : __fadd2_rn(sum, g.v[e]);
       }
-      for (int h0 = sh.lo + sub; h0 - sub < sh.hi; h0 += kBackBatch * RPS) {
-        Elems x[kBackBatch], g[kBackBatch];
+      const float2 md = both(row_sum<LPR>(dot) * (-1.f / D));
+      if (LAYER) sum = both(row_sum<LPR>(sum) * (-1.f / D));
 #pragma unroll
-        for (int i = 0; i < kBackBatch; ++i) {
-          x[i] = widen<IN>(raw[i]);
-          g[i] = widen<GRAD>(grad[i]);
-        }
-        load(h0 + kBackBatch * RPS);   // (the next ones are on their way meanwhile; behind the last: the last once more)
-#pragma unroll
-        for (int i = 0; i < kBackBatch; ++i) {
-          if (h0 - sub + i * RPS >= sh.hi) break;
-          const int h = h0 + i * RPS;
-          const bool live = h < sh.hi;
-          const float inv = normalise<D, LAYER>(x[i], p.eps);
-          turn<true>(g[i], tn, p.rope.interleaved);
-          float2 dot, sum;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (live) {
-              dw[kind].v[e] = __ffma2_rn(g[i].v[e], x[i].v[e], dw[kind].v[e]);
-              if (LAYER) db[kind].v[e] = __fadd2_rn(db[kind].v[e], g[i].v[e]);
-            }
-            g[i].v[e] = __fmul2_rn(g[i].v[e], w.v[e]);
-            dot = e == 0 ? __fmul2_rn(g[i].v[e], x[i].v[e]) : __ffma2_rn(g[i].v[e], x[i].v[e], dot);
-            if (LAYER) sum = e == 0 ? g[i].v[e] : __fadd2_rn(sum, g[i].v[e]);
-          }
-          const float2 md = both(row_sum<LPR>(dot) * (-1.f / D));
-          if (LAYER) sum = both(row_sum<LPR>(sum) * (-1.f / D));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 t = __ffma2_rn(x[i].v[e], md, g[i].v[e]);
-            g[i].v[e] = __fmul2_rn(LAYER ? __fadd2_rn(t, sum) : t, both(inv));
-          }
-          if (live) {
-            store4<IN>(p.y[kind], y0 + h * D + at.a, g[i].v);
-            store4<IN>(p.y[kind], y0 + h * D + at.b, g[i].v + 2);
-          }
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float2 t = __ffma2_rn(x.v[e], md, g.v[e]);
+        g.v[e] = __fmul2_rn(LAYER ? __fadd2_rn(t, sum) : t, both(inv));
+      }
+      if (there) {
+        store4<IN>(p.y[kind], y0 + h * D + at.a, g.v);
+        store4<IN>(p.y[kind], y0 + h * D + at.b, g.v + 2);
       }
     }
+    now.next(p);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   // rows of lanes -> one row of columns, in their order
+  float* const red = reinterpret_cast<float*>(ring);
   const int row = threadIdx.x / LPR;
 #pragma unroll
   for (int j = 0; j < (LAYER ? 4 : 2); ++j) {
-    const Elems& v = j < 2 ? dw[j & 1] : db[j & 1];
+    const bool mine = (j & 1) == kind;   // (by kinds: queries' and keys' in turn)
+    Elems v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v.v[e] = j < 2 ? (mine ? dw.v[e] : dw2.v[e]) : (mine ? db.v[e] : db2.v[e]);
     __syncthreads();
     store4<false>(red, row * D + at.a, v.v);
     store4<false>(red, row * D + at.b, v.v + 2);
@@ -376,6 +475,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_rope_join_kernel(const _
   const int j = blockIdx.x, lane = threadIdx.x & 31, c = blockIdx.y * 32 + lane, w = threadIdx.x >> 5;
   float* const out = j < 2 ? q.dw[j & 1] : q.db[j & 1];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && blocks == 0) q.hdr[0] = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the blocks' sums are there
   if (!out) return;
   float s = 0.f;
   for (int i = w; i < blocks; i += kJoinWarps) s += q.part[((int64_t)i * 4 + j) * D + c];
@@ -413,15 +513,27 @@ void run(const NormRopeParams& p, cudaStream_t stream) {
   }
 }
 
-template <int D, bool LAYER>
-void run_back(const NormRopeBackParams& q, int blocks, cudaStream_t stream) {
-  if (q.f.in_bf16) {
-    if (q.dy_bf16) norm_rope_back_kernel<D, true, true, LAYER><<<blocks, kNormThreads, 0, stream>>>(q);
-    else norm_rope_back_kernel<D, true, false, LAYER><<<blocks, kNormThreads, 0, stream>>>(q);
-  } else {
-    if (q.dy_bf16) norm_rope_back_kernel<D, false, true, LAYER><<<blocks, kNormThreads, 0, stream>>>(q);
-    else norm_rope_back_kernel<D, false, false, LAYER><<<blocks, kNormThreads, 0, stream>>>(q);
+template <int D, bool IN, bool GRAD, bool LAYER>
+cudaError_t run_back(const NormRopeBackParams& q, int blocks, cudaStream_t stream) {
+  constexpr int kSmem = BackStep<D, IN, GRAD>::kSmem;
+  auto kernel = norm_rope_back_kernel<D, IN, GRAD, LAYER>;
+  static std::atomic<uint64_t> ready{0};   // devices on which this kernel is set up
+  int dev = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (!(ready.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+    ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
   }
+  kernel<<<blocks, kNormThreads, kSmem, stream>>>(q);
+  return cudaGetLastError();
+}
+
+template <int D, bool LAYER>
+cudaError_t run_back(const NormRopeBackParams& q, int blocks, cudaStream_t stream) {
+  if (q.f.in_bf16)
+    return q.dy_bf16 ? run_back<D, true, true, LAYER>(q, blocks, stream) : run_back<D, true, false, LAYER>(q, blocks, stream);
+  return q.dy_bf16 ? run_back<D, false, true, LAYER>(q, blocks, stream) : run_back<D, false, false, LAYER>(q, blocks, stream);
 }
 
 }  // namespace
@@ -442,24 +554,26 @@ cudaError_t launch_norm_rope(const NormRopeParams& call, int D, int sm_count, cu
 
 cudaError_t launch_norm_rope_back(const NormRopeBackParams& call, int D, int sm_count, cudaStream_t stream) {
   NormRopeBackParams q = call;
-  int cap = 2 * sm_count < kNormBackBlocks ? 2 * sm_count : kNormBackBlocks;
-  divide(&q.f, D, kBackBatch, 2 * cap * (kNormThreads / 32));   // (two shares to a warp: they differ in length)
+  const int cap = kBackBlocks * sm_count < kNormBackBlocks ? kBackBlocks * sm_count : kNormBackBlocks;
+  divide(&q.f, D, kBackRows, 2 * cap * (kNormThreads / 32));   // (two shares to a warp: they differ in length)
   const int64_t tasks = (int64_t)q.f.tokens * q.f.parts;
   int blocks = cap;
   if ((tasks + kNormThreads / 32 - 1) / (kNormThreads / 32) < cap) blocks = (int)((tasks + kNormThreads / 32 - 1) / (kNormThreads / 32));
   if (blocks > 0) {
-    if (D == 128) {
-      if (q.f.layer) run_back<128, true>(q, blocks, stream);
-      else run_back<128, false>(q, blocks, stream);
-    } else {
-      if (q.f.layer) run_back<64, true>(q, blocks, stream);
-      else run_back<64, false>(q, blocks, stream);
-    }
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = D == 128 ? (q.f.layer ? run_back<128, true>(q, blocks, stream) : run_back<128, false>(q, blocks, stream))
+                                   : (q.f.layer ? run_back<64, true>(q, blocks, stream) : run_back<64, false>(q, blocks, stream));
     if (e != cudaSuccess) return e;
   }
-  norm_rope_join_kernel<<<dim3(4, D / 32), 32 * kJoinWarps, 0, stream>>>(q, D, blocks);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = blocks > 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(4, D / 32);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_rope_join_kernel, q, D, blocks);
 }
 
 }  // namespace dsa
