@@ -448,6 +448,15 @@ def test_compact_again_and_again():
                                            t.view(torch.uint8) if t.dtype == torch.bfloat16 else t))
 
 
+@pytest.mark.parametrize("sequences", [10, 14, 18, 22, 28, 36, 50])
+def test_compact_sequences_in_between(sequences):
+    """Numbers of sequences that give a head three to eight blocks, not powers of two alone; ragged last chunks."""
+    rng = np.random.default_rng([55, sequences])
+    b = Batch(rng, [(0, int(s)) for s in rng.integers(300, 1500, sequences)], 2, 64, 16, "mxfp8")
+    kept, n = some_rows(rng, b, 2, 1400, 0.9)
+    check_compact(b, rng, kept, n, E.random_weights(rng, b))
+
+
 def test_compact_shifts_by_one():
     """Every row but one stays: each chunk reads what the one before it has to leave alone."""
     rng = np.random.default_rng(52)
