@@ -20,7 +20,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _abi
-from .paged import _PREC, PagedCache, _arg, _call, _error, _pages, _table, _tokens
+from .paged import _PREC, PagedCache, _arg, _call, _empty, _error, _pages, _table, _tokens
 
 
 def paged_weights(cache: PagedCache) -> torch.Tensor:
@@ -70,7 +70,7 @@ def cache_weigh(cache: PagedCache, weights: torch.Tensor, q: torch.Tensor, lse: 
 def _status_ws(ws: Optional[torch.Tensor], dev: torch.device):
     """Address and size of a workspace that holds the status alone, and the tensor."""
     if ws is None:
-        ws = torch.empty(_abi.DSA_CACHE_WS_BYTES, dtype=torch.uint8, device=dev)
+        ws = _empty((_abi.DSA_CACHE_WS_BYTES,), torch.uint8, dev)
     return _arg(ws, "ws", dev, torch.uint8), ws.numel(), ws
 
 
@@ -98,8 +98,7 @@ def evict_select(weights: torch.Tensor, cu_seqlens_k: torch.Tensor, page_table: 
         raise ValueError("budget must be at least 1")
     shape = (B, 1 if shared else Hk, budget)
     if out is None:
-        kept = torch.empty(shape, dtype=torch.int32, device=dev)
-        kept_len = torch.empty((B,), dtype=torch.int32, device=dev)
+        kept, kept_len = _empty(shape, torch.int32, dev), _empty((B,), torch.int32, dev)
     else:
         kept, kept_len = out
     kp, lp = _arg(kept, "kept", dev, torch.int32, shape), _arg(kept_len, "kept_len", dev, torch.int32, (B,))

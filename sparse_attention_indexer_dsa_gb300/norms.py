@@ -10,7 +10,7 @@ from typing import NamedTuple, Optional, Sequence, Tuple
 import torch
 
 from . import _abi
-from .paged import _arg, _call, _error
+from .paged import _arg, _call, _empty, _error
 
 _NORM = {"rms": _abi.DSA_NORM_RMS, "layer": _abi.DSA_NORM_LAYER}
 _WEIGHTS = ("q_weight", "k_weight", "q_bias", "k_bias")
@@ -115,10 +115,10 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[to
         ot = dt if out_dtype is None else out_dtype
         if ot not in _DTYPE:
             raise ValueError(f"out_dtype: unsupported dtype {ot}")
-        q_out, k_out = torch.empty(shape, dtype=ot, device=dev), None
+        q_out, k_out = _empty((T, H, D), ot, dev), None
         qo, qost, ko, kost = q_out.data_ptr() or None, 0, None, 0
         if k is not None:
-            k_out = torch.empty(k.shape, dtype=ot, device=dev)
+            k_out = _empty((T, Hk, D), ot, dev)
             ko = k_out.data_ptr() or None
     else:
         q_out, k_out = out
@@ -170,23 +170,18 @@ def norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: 
         raise ValueError(f"dq_out: unsupported dtype {gt}")
     gq, gqst = _like(dq_out, "dq_out", shape, gt, dev)
     gk, gkst = (None, 0) if k is None else _like(dk_out, "dk_out", k.shape, gt, dev)
-    dq, dk, dkp = torch.empty(shape, dtype=dt, device=dev), None, None
+    dq, dk, dkp = _empty((T, H, D), dt, dev), None, None
     if k is not None:
-        dk = torch.empty(k.shape, dtype=dt, device=dev)
+        dk = _empty((T, Hk, D), dt, dev)
         dkp = dk.data_ptr() or None
-    # gradients of the weights: rows of one tensor (of queries and keys, then of their biases)
-    n, kinds = (2 if norm == "layer" else 1), (1 if k is None else 2)
-    sums = torch.empty((n * kinds, D), dtype=torch.float32, device=dev)
-    at, step, lay = sums.data_ptr(), 4 * D, norm == "layer"
-    sp = (at, at + step if k is not None else None, at + kinds * step if lay else None,
-          at + 3 * step if lay and k is not None else None)
+    lay = norm == "layer"   # gradients of weights, then of biases, of queries and of keys
+    sums = [_empty((D,), torch.float32, dev) if (lay or i < 2) and (k is not None or i % 2 == 0) else None for i in range(4)]
     if ws is None:
         ws = norm_rope_workspace(D, dev)
     code = _call(_abi.load().dsa_idx_norm_rope_backward, dev, (
         gq, gqst, gk, gkst, _DTYPE[gt], *rows, _DTYPE[dt], wp[0], wp[1], wt, _NORM[norm], eps, pos, T, H, Hk, D, R, rope_base,
-        freq, int(rope_interleaved), dq.data_ptr() or None, 0, dkp, 0, *sp, _arg(ws, "ws", dev, torch.uint8), ws.numel()))
+        freq, int(rope_interleaved), dq.data_ptr() or None, 0, dkp, 0,
+        *[None if s is None else s.data_ptr() for s in sums], _arg(ws, "ws", dev, torch.uint8), ws.numel()))
     if code:
         raise _error(code, "dsa_idx_norm_rope_backward")
-    it = iter(sums.unbind(0))
-    return NormRopeGrads(dq, dk, next(it), None if k is None else next(it), next(it) if lay else None,
-                         next(it) if lay and k is not None else None)
+    return NormRopeGrads(dq, dk, *sums)

@@ -117,6 +117,19 @@ def paged_cache(num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, 
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _empty(shape: tuple, dtype, device: torch.device) -> torch.Tensor:
+    """torch.empty; on the current device without the dispatch around the allocation (two of them before a launch:
+    7.3 us of host time in place of 4.2)."""
+    if _strided is None or _current() != device.index:
+        return torch.empty(shape, dtype=dtype, device=device)
+    strides, n = [1], 1
+    for s in shape[:0:-1]:
+        n *= s
+        strides.append(n)
+    return _strided(shape, tuple(strides[::-1]), dtype)
 
 
 def _call(fn, device: torch.device, args) -> int:
