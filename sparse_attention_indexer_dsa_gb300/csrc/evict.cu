@@ -20,13 +20,14 @@
 // kept[j] >= j: a cluster of 1 to 8 blocks moves the rows of one head in ascending
 // chunks.  A chunk is read whole by all its blocks before any of them writes, and
 // the rows that later chunks read lie behind everything written before them, so
-// reads run two chunks ahead.  One thread looks a row up for all that copy its
+// reads run a chunk ahead.  One thread looks a row up for all that copy its
 // pieces: at 16 bytes a look-up the instructions, not the memory, took the time.  The
-// rows of 16 sequences, 2048 of some 2200, 8 heads, MXFP8: 27 us = 76 % of the copy
-// rate; 16384 of up to 65536 BF16 rows of 5 sequences, clusters of five: 110 us = 91 %.
-// (Clusters of four 116 us; half as long chunks and four blocks to an SM 28 and 118;
-// 5 stages and two blocks 28 and 164; blocks with a part of each row, no barrier between
-// them and a look-up to every piece 39 and 172.)
+// rows of 16 sequences, 2048 of some 2200, 8 heads, MXFP8: 26 us = 80 % of the copy
+// rate; 16384 of up to 65536 BF16 rows of 5 sequences, clusters of seven: 109.5 us =
+// 91 %.  (Chunks of 16 KB, three blocks to an SM, reads a chunk or two ahead 27.4 and
+// 108 or 110, clusters of powers of two alone 116; chunks of 8 KB two ahead 28 and 118; 5
+// stages and two blocks 28 and 164; blocks with a part of each row, no barrier between them
+// and a look-up to every piece 39 and 172.)
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -348,9 +349,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 // ---------------------------------------------------------------- moving
 
 constexpr int kMoveThreads = 256;
-constexpr int kMovePer = 4;                                          // 16-byte pieces of a thread in a chunk
+constexpr int kMovePer = 3;                                          // 16-byte pieces of a thread in a chunk
 constexpr int kMoveChunkBytes = kMoveThreads * kMovePer * 16;
-constexpr int kMoveStages = 3;
+constexpr int kMoveStages = 2;
 constexpr int kMoveRows = kMoveChunkBytes / 64;                      // of a chunk, at most: one to a thread
 constexpr int kMoveCluster = 8;                                      // blocks of a cluster, at most
 static_assert(kMoveRows <= kMoveThreads, "a thread to a row");
@@ -389,7 +390,7 @@ __device__ __forceinline__ void move_barrier(int blocks) {
 
 // Keys or values of one head of one sequence, with their scales (T, null: none) and, with the keys, the
 // rows' weights.  Thread t looks up row t of a chunk: the rows' entries are requested two steps before they
-// are looked up, their pages one; then a chunk's rows are requested, two chunks before they are written.
+// are looked up, their pages one; then a chunk's rows are requested, a chunk before they are written.
 template <class T>
 __device__ __forceinline__ bool move_head(const CompactParams& p, int d, int h, int n, uint8_t* base, T* scales, float* weights,
                                           int blocks, int rank, MoveRing* ring) {
@@ -476,7 +477,7 @@ __device__ __forceinline__ bool move_head(const CompactParams& p, int d, int h, 
   return bad;
 }
 
-__global__ void __launch_bounds__(kMoveThreads, 3) cache_compact_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) cache_compact_kernel(const __grid_constant__ CompactParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   MoveRing* const ring = reinterpret_cast<MoveRing*>(smem);
   cg::cluster_group cluster = cg::this_cluster();
@@ -574,7 +575,7 @@ cudaError_t launch_evict_select(const SelectParams& call, int sm_count, cudaStre
 }
 
 cudaError_t launch_cache_compact(const CompactParams& p, int sm_count, cudaStream_t stream) {
-  constexpr int kResident = 3;   // blocks of an SM
+  constexpr int kResident = 4;   // blocks of an SM
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(ready, cache_compact_kernel, sizeof(MoveRing));
   if (e != cudaSuccess) return e;
