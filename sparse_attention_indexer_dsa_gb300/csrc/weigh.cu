@@ -14,7 +14,7 @@
 // 16384 rows, a token each, 64 heads on 8: 185 us over BF16 rows = 95 % of the copy rate;
 // 109 over MXFP8 ones = 87 %, where the instructions that turn codes into FP16 and apply
 // the scales count too (114 with two halves of a word taken apart by shifts and rows
-// looked up one by one; refilling the ring before the products, 112, gains nothing then).
+// looked up one by one; refilling the ring before the products gains nothing).
 //
 // 8-bit rows: E4M3 is exact in FP16, and with at most eight query rows so are the
 // queries once each row is scaled by a power of two, unless its elements span
