@@ -12,7 +12,7 @@
 // over the head's elements has no order, so a lane's consecutive bytes of a row
 // stand for the fragment's elements, of queries and keys alike.  64 sequences of 2048 -
 // 16384 rows, a token each, 64 heads on 8: 185 us over BF16 rows = 95 % of the copy rate;
-// 109 over MXFP8 ones = 87 %, where the instructions that turn codes into FP16 and apply
+// 110 over MXFP8 ones = 85 %, where the instructions that turn codes into FP16 and apply
 // the scales count too (114 with two halves of a word taken apart by shifts and rows
 // looked up one by one; refilling the ring before the products gains nothing).
 //

@@ -81,6 +81,16 @@ def test_weigh_pages(page, lens):
     check_weigh(b, rng, 4)
 
 
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 128])
+def test_weigh_rows_of_a_page_together(prec, D, page):
+    """Pages of less than a step's rows and of more, last rows anywhere in a page whose other slots hold NaN."""
+    rng = np.random.default_rng([len(prec), D, page])
+    for group, lens in ((8, [(1, 1), (1, 31), (1, 33), (1, 130), (1, 511)]), (5, [(3, 65), (1, 200), (4, 4)])):
+        check_weigh(Batch(rng, lens, 2, D, page, prec), rng, group)
+
+
 @pytest.mark.parametrize("group,T", [(128, 9), (1, 300), (7, 41), (2, 520)])
 def test_weigh_groups(group, T):
     rng = np.random.default_rng([group, T])

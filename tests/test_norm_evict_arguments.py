@@ -180,3 +180,15 @@ def test_token_strides():
     for shape, dt in (((8, 6, 64), torch.bfloat16), ((8, 5, 64), torch.float32)):
         with pytest.raises(ValueError, match="k must be"):
             norms._like(base, "k", shape, dt, base.device)
+
+
+def test_outputs_are_packed(monkeypatch):
+    from sparse_attention_indexer_dsa_gb300 import paged
+    monkeypatch.setattr(paged, "_current", lambda: 0)
+    monkeypatch.setattr(paged, "_strided", lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype))
+    for shape in ((5,), (0,), (3, 4), (0, 2, 64), (7, 1, 128), (2, 3, 4, 5)):
+        t = paged._empty(shape, torch.bfloat16, torch.device("cuda", 0))
+        assert t.shape == shape and t.stride() == torch.empty(shape).stride() and t.dtype is torch.bfloat16
+    assert paged._empty((2, 3), torch.int32, torch.device("cpu")).device.type == "cpu"   # another device: torch.empty
+    monkeypatch.setattr(paged, "_strided", None)
+    assert paged._empty((2, 3), torch.int32, torch.device("cpu")).shape == (2, 3)
