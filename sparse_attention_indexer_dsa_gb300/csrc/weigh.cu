@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
   const bool together = (1 << p.c.page_shift) >= kKeys;   // the rows of a step are one piece of a page
   int code = 0;
   // Prefixes that fall make rows count for several sequences, or for none: nothing is computed.
-  bool falls = false;
+  bool falls = false, any = false;   // any: sequences of this kernel
   for (int d = tid; d < p.num_seqs; d += kThreads) {
     Doc o;
     if (!doc_info(p, d, &o)) {
@@ -102,9 +102,10 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
       falls |= __ldg(p.cu_k + d) < 0 || __ldg(p.cu_k + d + 1) < __ldg(p.cu_k + d) || __ldg(p.cu_q + d) < 0 ||
                __ldg(p.cu_q + d + 1) < __ldg(p.cu_q + d);
     }
+    any |= o.T > 0 && by_steps(p, o.T);
   }
   if (tid == 0 && __ldg(p.cu_q + p.num_seqs) > p.total_q) code = DSA_DEV_ERR_INVALID_ARG;
-  const bool none = __syncthreads_or(falls);
+  const bool none = __syncthreads_or(falls) || !__syncthreads_or(any);
   const int n_steps = none ? 0 : step_base<kKeys>(p, p.num_seqs);
   const int64_t units = (int64_t)n_steps * p.c.n_kv, warps = (int64_t)gridDim.x * kWarps;
   const int64_t per = (units + warps - 1) / warps;
