@@ -89,7 +89,7 @@ def test_frequencies_and_far_positions():
     pos = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1 << 20, 65535, -12345, 7], dtype=torch.int32, device="cuda")
     freq = [float(f) for f in rng.uniform(-1.0, 1.0, 16)]
     got = dsa.norm_rope(q, k, pos, *w, eps=EPS, rope_dim=32, inv_freq=freq)
-    # a frequency in turns is rounded to 2^-54 of a turn: 2^31 positions on, 2^-23 of one
+    # (the reference's own angles in 64 bits lose bits far out: those positions are held to exact ones below)
     near = [i for i in range(9) if abs(int(pos[i])) <= 1 << 20]
     p = pos[near]
     check_forward(q[near], k[near], p, w, (got[0][near], got[1][near]), "rms", 32, False, "f32", inv_freq=freq)
