@@ -555,6 +555,8 @@ size_t dsa_idx_weigh_workspace_size(int total_q, int num_seqs, int max_seqlen_q,
  *               gives it over every visible key; a row of -inf adds nothing
  *   weights     device fp32 [num_pages, n_kv_heads, page_size], 16-byte
  *               aligned: addressed by the page table like the pages' scales
+ * The prefixes may begin above 0: parts of a longer batch's, with that part of its
+ * table.
  * Sequences of one call share no pages, and none has a page twice (the weights of
  * its rows would be unspecified).  Only keys are read (a cache of keys
  * alone will do); they must be finite.  The same inputs give the same bits.

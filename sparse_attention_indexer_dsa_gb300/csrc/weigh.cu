@@ -76,10 +76,11 @@ __device__ __forceinline__ void codes_f16(uint32_t four, uint32_t (&o)[2]) {
       : "r"(four));
 }
 
-// First of the steps of sequence d, in a numbering with room for all of each sequence.
+// First of the steps of sequence d, in a numbering from 0 with room for all of each sequence; k0: the key
+// prefix's first entry (not 0 where it is a part of a longer batch's).
 template <int kKeys>
-__device__ __forceinline__ int step_base(const WeighParams& p, int d) {
-  return __ldg(p.cu_k + d) / kKeys + d;
+__device__ __forceinline__ int step_base(const WeighParams& p, int k0, int d) {
+  return (__ldg(p.cu_k + d) - k0) / kKeys + d;
 }
 
 template <int D, bool Q8>
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
   }
   if (tid == 0 && __ldg(p.cu_q + p.num_seqs) > p.total_q) code = DSA_DEV_ERR_INVALID_ARG;
   const bool none = __syncthreads_or(falls) || !__syncthreads_or(any);
-  const int n_steps = none ? 0 : step_base<kKeys>(p, p.num_seqs);
+  const int k0 = __ldg(p.cu_k), n_steps = none ? 0 : step_base<kKeys>(p, k0, p.num_seqs);
   const int64_t units = (int64_t)n_steps * p.c.n_kv, warps = (int64_t)gridDim.x * kWarps;
   const int64_t per = (units + warps - 1) / warps;
   int64_t u = ((int64_t)blockIdx.x * kWarps + warp) * per;
@@ -118,9 +119,9 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     int lo = 0, hi = p.num_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (step_base<kKeys>(p, mid) <= su) lo = mid; else hi = mid - 1;
+      if (step_base<kKeys>(p, k0, mid) <= su) lo = mid; else hi = mid - 1;
     }
-    const int d = lo, base = step_base<kKeys>(p, d), next_base = step_base<kKeys>(p, d + 1);
+    const int d = lo, base = step_base<kKeys>(p, k0, d), next_base = step_base<kKeys>(p, k0, d + 1);
     Doc doc;
     doc_info(p, d, &doc);
     const int64_t run_end = u + (next_base - su) < u_end ? u + (next_base - su) : u_end;

@@ -674,3 +674,47 @@ def test_rows_behind_four_gigabytes(prec, pages):
     for x in names:
         a, e = getattr(far, x)[-n:], getattr(small, x)
         assert torch.equal(a.view(torch.uint8), e.view(torch.uint8)), x   # (unused slots hold NaN)
+
+
+# ---------------------------------------------------------------- parts of a batch
+
+def part_of(b, lo, hi):
+    """Sequences lo .. hi - 1 as parts of the batch's prefixes and table: the prefixes begin where the part does."""
+    return b.dev("cu_q")[lo:hi + 1], b.dev("cu_k")[lo:hi + 1], b.dev("table")[lo:hi]
+
+
+@pytest.mark.parametrize("prec", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("lens", [[(1, 1000), (1, 100), (1, 200)], [(2, 37), (1, 40), (3, 333), (0, 12), (1, 5)],
+                                  [(1, 600), (60, 300), (1, 90), (130, 131)]])
+def test_weigh_parts_of_a_batch(lens, prec):
+    """Every part by itself: its sequences' weights, and no bit of the others'."""
+    rng = np.random.default_rng([71, len(lens), len(prec)])
+    b = Batch(rng, lens, 2, 128, 16, prec, values_too=False)
+    q, qd = queries(rng, b.total_q, 16, 128)
+    lse = true_lse(b, q, 8, 0.1)
+    w = E.random_weights(rng, b)
+    want, tol = E.weigh(b, q, lse.astype(np.float64), w, 8, 0.1)
+    c, ws = b.cache(dsa), dsa.weigh_workspace(b.total_q, len(lens), max(t for t, _ in lens), 16, 2, 128)
+    for lo in range(len(lens)):
+        for hi in (lo + 1, len(lens)):
+            got = dev(w)
+            cq, ck, table = part_of(b, lo, hi)
+            dsa.cache_weigh(c, got, qd, dev(lse), cq, ck, table, max(t for t, _ in lens), max(s for _, s in lens), sm_scale=0.1, ws=ws)
+            assert dsa.read_status(ws) == 0
+            mine = np.zeros(w.shape, bool)
+            for d in range(lo, hi):
+                page, slot = E.rows_of(b, d)
+                mine[page, :, slot] = True
+            assert np.array_equal(host(got)[~mine], w[~mine]), (lo, hi)
+            close(got[torch.from_numpy(mine).cuda()], want[mine], tol[mine], (lo, hi))
+
+
+def test_select_parts_of_a_batch():
+    rng = np.random.default_rng(72)
+    b = Batch(rng, [(0, 1000), (0, 100), (0, 333)], 2, 64, 16, "bf16", values_too=False)
+    w = E.random_weights(rng, b)
+    want, n = E.select(b, w, 64, 2, 9, False)
+    for lo, hi in ((1, 3), (2, 3), (1, 2)):
+        _, ck, table = part_of(b, lo, hi)
+        kept, got = dsa.evict_select(dev(w), ck, table, 64, 1000, sinks=2, recent=9)
+        assert np.array_equal(host(kept), want[lo:hi]) and np.array_equal(host(got), n[lo:hi])
