@@ -553,6 +553,8 @@ size_t dsa_idx_weigh_workspace_size(int total_q, int num_seqs, int max_seqlen_q,
  * stay as they are.
  *   lse         device fp32 [total_q, n_heads], as dsa_idx_paged_attention
  *               gives it over every visible key; a row of -inf adds nothing
+ *               (logits are summed as the attention sums them: off by at most
+ *               (head_dim + 2) 2^-23 sm_scale sum |q k|, as a rule some 1e-7 short)
  *   weights     device fp32 [num_pages, n_kv_heads, page_size], 16-byte
  *               aligned: addressed by the page table like the pages' scales
  * The prefixes may begin above 0: parts of a longer batch's, with that part of its

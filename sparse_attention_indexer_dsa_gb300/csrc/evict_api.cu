@@ -39,11 +39,12 @@ dsa_status_t dsa_idx_cache_weigh(const void* q, int64_t q_stride, const float* l
     return fail(DSA_ERR_UNSUPPORTED, "n_heads must be a multiple of n_kv_heads, at most 128 heads to one");
   if ((int64_t)total_q * n_heads >= (int64_t)1 << 30) return fail(DSA_ERR_UNSUPPORTED, "total_q * n_heads above 2^30");
   if (max_seqlen_k > (1 << 30)) return fail(DSA_ERR_UNSUPPORTED, "max_seqlen_k is at most 2^30");
-  // The tensor cores' FP32 sums truncate: of 128 products of BF16 values a logit comes out short by 1.0e-7 of
-  // itself on average (N(0, 1) rows with and without outliers, of any size: 1.00 - 1.09e-7; its spread is 6e-8,
-  // that of sums that round 6.5e-8 about 0), which the scale makes up for: a chunk's weights are then 8e-7 off
-  // their formula in place of 2.1e-6.  Products with E4M3 values have fewer bits, and lose none worth it.
-  p.scale_log2 = (float)((double)sm_scale * 1.4426950408889634 * (prec == DSA_PREC_BF16 ? 1.0 + 1.0e-7 : 1.0));
+  // The attention's own scale, so that weights and lse fit together.  The tensor cores' FP32 sums truncate: a logit of
+  // 128 products of BF16 values comes out short by 0.9 - 1.5e-7 of itself on average, one of 64 by 0.4 - 0.8e-7
+  // (mma.sync and tcgen05 alike; rows normal, with outliers, uniform, of one sign).  The attention's lse is short alike:
+  // with it a token's weights add up to its heads within 2e-7 at mean logits up to 30; with the lse of exact
+  // logits they are short by the logit's part (2.7e-6 at 25).
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
   if (!(sm_scale >= 0.f) || std::isinf(p.scale_log2))
     return fail(DSA_ERR_INVALID_ARG, "sm_scale and sm_scale * log2(e) must be finite and >= 0");
   if (!aligned16(q) || !aligned16(weights)) return fail(DSA_ERR_INVALID_ARG, "q and weights must be 16-byte aligned");

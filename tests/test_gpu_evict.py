@@ -718,3 +718,31 @@ def test_select_parts_of_a_batch():
         _, ck, table = part_of(b, lo, hi)
         kept, got = dsa.evict_select(dev(w), ck, table, 64, 1000, sinks=2, recent=9)
         assert np.array_equal(host(kept), want[lo:hi]) and np.array_equal(host(got), n[lo:hi])
+
+
+# ---------------------------------------------------------------- the scale
+
+@pytest.mark.parametrize("T", [1, 40])      # a step, a chunk
+@pytest.mark.parametrize("D", [64, 128])
+def test_weigh_takes_the_scale_as_given(D, T):
+    """One product to a logit, 2^14 and exact, under a scale whose product with log2(e) is 1 in FP32: a weight is
+    2^(2^14 - B) with B = lse log2(e) rounded to FP32, as near as its own arithmetic is (two roundings of at most 2^-24 of an
+    exponent below 2, ex2 at 2^-21, a sum of at most 5 x 40 at 2^-24 each).  One step more of the scale would be 2^-9 off."""
+    group = 5
+    rng = np.random.default_rng([73, D, T])
+    b = Batch(rng, [(T, T + 9)], 1, D, 16, "bf16", values_too=False)
+    b.pages["k"][:] = 0
+    b.pages["k"][..., 3] = 0x4300                       # 128
+    scale = float(np.float32(np.log(2.0)))
+    log2e = np.float32(1.4426950408889634)
+    assert np.float32(scale) * log2e == np.float32(1.0)
+    q = torch.zeros(T, group, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 3] = 128.0
+    lse = (16384 * np.log(2.0) + rng.uniform(-1, 1, (T, group))).astype(np.float32)
+    w = np.zeros((b.num_pages, 1, 16), np.float32)
+    got = weigh(b, b.cache(dsa), dev(w), q, dev(lse), scale)
+    each = np.exp2(16384.0 - (lse * log2e).astype(np.float32).astype(np.float64)).sum(1)
+    want = np.zeros(w.shape)
+    page, slot = E.rows_of(b, 0)
+    want[page, 0, slot] = [each[max(0, s - 9):].sum() for s in range(T + 9)]
+    close(got, want, want * (2.0 ** -20 + 200 * 2.0 ** -24))
