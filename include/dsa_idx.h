@@ -587,7 +587,8 @@ dsa_status_t dsa_idx_cache_weigh(
  *   ws          dsa_idx_cache_workspace_size() bytes
  * sinks + recent <= budget.  A sequence longer than max_seqlen_k, or than its
  * pages, is reported in the status and keeps none (-1, 0); a row on a page that
- * does not exist is reported and weighs NaN. */
+ * does not exist is reported and weighs NaN (one that stays whatever it weighs
+ * stays). */
 dsa_status_t dsa_idx_evict_select(
     const float* weights, int num_pages, int page_size, int n_kv_heads,
     const int32_t* page_table, int max_pages, const int32_t* cu_seqlens_k,

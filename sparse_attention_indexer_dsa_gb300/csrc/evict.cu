@@ -78,7 +78,7 @@ struct Select {
       const int r = i + k * kSelThreads;
       const bool there = (unsigned)page[k] < (unsigned)p.num_pages;
       const bool must = r < p.sinks || r >= S - p.recent;
-      if (r < end && !must && !there) bad = true;
+      if (r < end && !there) bad = true;
       b[k] = must ? kMust : 0u;   // (a row on no page: as NaN)
       w[k] = there && !must ? p.weights + (((int64_t)page[k] * p.n_kv + h) << p.page_shift) + (r & ((1 << p.page_shift) - 1)) : nullptr;
       v[k] = w[k] ? __ldg(w[k]) : 0.f;
@@ -192,6 +192,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     }
     if (h == 0 && tid == 0 && rank == 0) p.kept_len[d] = min(S, p.budget);
     if (S <= p.budget) {
+      if (h == 0) {   // (no weight is read, but a page that does not exist is reported)
+        const int pages = (S + (1 << p.page_shift) - 1) >> p.page_shift;
+        for (int i = rank * kSelThreads + tid; i < pages; i += blocks * kSelThreads)
+          if ((unsigned)__ldg(p.table + (int64_t)d * p.max_pages + i) >= (unsigned)p.num_pages) code = DSA_DEV_ERR_INVALID_ARG;
+      }
       for (int i = rank * kSelThreads + tid; i < p.budget; i += blocks * kSelThreads) out[i] = i < S ? i : -1;
       continue;
     }

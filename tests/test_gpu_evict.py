@@ -746,3 +746,48 @@ def test_weigh_takes_the_scale_as_given(D, T):
     page, slot = E.rows_of(b, 0)
     want[page, 0, slot] = [each[max(0, s - 9):].sum() for s in range(T + 9)]
     close(got, want, want * (2.0 ** -20 + 200 * 2.0 ** -24))
+
+
+# ---------------------------------------------------------------- pages that do not exist
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("where", ["sinks", "recent", "between", "within the budget", "last page"])
+@pytest.mark.parametrize("page", [-7, 1 << 30])
+def test_select_reports_every_missing_page(shared, where, page):
+    """A row that has to stay, or a sequence that keeps all its rows, on a page that does not exist: reported like any
+    other, and the choice is the same as with a page."""
+    rng = np.random.default_rng(74)
+    b = Batch(rng, [(0, 400), (0, 37), (0, 90)], 2, 64, 8, "bf16", values_too=False)
+    w = E.random_weights(rng, b)
+    ws = dsa.cache_workspace()
+
+    def run():
+        kept, n = dsa.evict_select(dev(w), b.dev("cu_k"), b.dev("table"), 64, 400, sinks=8, recent=16, shared=shared, ws=ws)
+        return host(kept), host(n), dsa.read_status(ws)
+
+    want, n, status = run()
+    assert status == 0
+    d, i = {"sinks": (0, 0), "recent": (0, 49), "between": (2, 5), "within the budget": (1, 2), "last page": (1, 4)}[where]
+    b.table[d, i] = page
+    kept, got, status = run()
+    assert status == 1 and np.array_equal(got, n)
+    if where == "between":      # as NaN: those rows go first
+        assert not ((kept[2] >= 40) & (kept[2] < 48)).any()
+        kept[2] = want[2]
+    assert np.array_equal(kept, want)
+
+
+def test_select_reports_a_missing_page_of_a_long_sequence():
+    """Rows by several blocks of a cluster; one page missing under the recent rows, which other blocks hold than report."""
+    rng = np.random.default_rng(75)
+    b = Batch(rng, [(0, 20000)], 1, 64, 64, "fp8", values_too=False)
+    w = E.random_weights(rng, b)
+    ws = dsa.cache_workspace()
+    for at in (0, 312, None):
+        t = b.table.copy()
+        if at is not None:
+            b.table[0, at] = b.num_pages
+        for budget in (4000, 20000):
+            dsa.evict_select(dev(w), b.dev("cu_k"), b.dev("table"), budget, 20000, sinks=64, recent=64, ws=ws)
+            assert dsa.read_status(ws) == (0 if at is None else 1), (at, budget)
+        b.table = t
