@@ -791,3 +791,60 @@ def test_select_reports_a_missing_page_of_a_long_sequence():
             dsa.evict_select(dev(w), b.dev("cu_k"), b.dev("table"), budget, 20000, sinks=64, recent=64, ws=ws)
             assert dsa.read_status(ws) == (0 if at is None else 1), (at, budget)
         b.table = t
+
+
+# ---------------------------------------------------------------- clusters of eight, rows read again
+
+class Long:
+    """Sequences' table and weights alone: what the choice reads."""
+
+    def __init__(self, rng, lens, n_kv, page):
+        need = [-(-s // page) for s in lens]
+        self.lens, self.n_kv, self.page, self.num_pages = [(0, s) for s in lens], n_kv, page, sum(need) + 2
+        order, at = rng.permutation(self.num_pages), 0
+        self.table = np.full((len(lens), max(need)), -1, np.int32)
+        for d, n in enumerate(need):
+            self.table[d, :n] = order[at:at + n]
+            at += n
+        self.cu_k = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+
+    def dev(self, name):
+        return torch.from_numpy(getattr(self, name)).cuda()
+
+
+def choice(b, w, budget, sinks, recent, shared):
+    """As E.select, for weights without NaN, by a sort of arrays."""
+    heads = 1 if shared else b.n_kv
+    kept = np.full((len(b.lens), heads, budget), -1, np.int32)
+    for d, (_, s) in enumerate(b.lens):
+        page, slot = E.rows_of(b, d)
+        x = np.stack([w[page, h, slot] for h in range(b.n_kv)])
+        if shared:
+            total = x[0]
+            for h in range(1, b.n_kv):
+                total = (total + x[h]).astype(np.float32)
+            x = total[None]
+        i = np.arange(s)
+        may = ~((i < sinks) | (i >= s - recent))
+        for h in range(heads):
+            best = np.sort(np.lexsort((i, -x[h], may))[:budget])
+            kept[d, h, :len(best)] = best
+    return kept, np.array([min(s, budget) for _, s in b.lens], np.int32)
+
+
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("lens,kv,shared", [([40000], 5, False), ([40000, 33000, 17, 36000, 9000, 40961], 1, True),
+                                            ([330000, 5000], 5, False), ([700000], 2, True)])
+def test_select_of_eight_blocks_and_of_rows_read_again(lens, kv, shared, ties):
+    """Five heads or more with over 32768 rows: eight blocks to each (fewer heads have sixteen).  Over 327680 rows on
+    eight blocks, or 655360 on sixteen, are not held in shared memory: every pass reads the weights again."""
+    rng = np.random.default_rng([76, len(lens), kv, ties])
+    b = Long(rng, lens, kv, 1024)
+    w = E.random_weights(rng, b, ties)
+    ws = dsa.cache_workspace()
+    for budget, sinks, recent in ((1, 0, 0), (3000, 4, 256), (39999, 0, 7)):
+        kept, n = dsa.evict_select(dev(w), b.dev("cu_k"), b.dev("table"), budget, max(lens), sinks=sinks, recent=recent,
+                                   shared=shared, ws=ws)
+        assert dsa.read_status(ws) == 0
+        want, wn = choice(b, w, budget, sinks, recent, shared)
+        assert np.array_equal(host(n), wn) and np.array_equal(host(kept), want), (budget, sinks, recent)
