@@ -496,7 +496,8 @@ typedef enum { DSA_NORM_RMS = 0, DSA_NORM_LAYER = 1 } dsa_norm_t;
  *   q, k        device [total_tokens, n_heads (n_kv_heads), head_dim] in_dtype,
  *               16-byte aligned; q_stride ..: elements from one token to the
  *               next (0 = packed; a multiple of 16 bytes), heads packed inside
- *   q_weight .. k_bias  device [head_dim] weight_dtype, or NULL: ones (zeros)
+ *   q_weight .. k_bias  device [head_dim] weight_dtype, or NULL: ones (zeros);
+ *               biases of DSA_NORM_RMS always NULL, as their gradients
  *   positions   device int32 [total_tokens] (any value); with rope_dim = 0 NULL
  *   inv_freq    HOST array [rope_dim/2], or NULL
  *   q_out, k_out  as q and k, in out_dtype, with strides of their own; may be q
@@ -520,8 +521,8 @@ size_t dsa_idx_norm_rope_workspace_size(int head_dim);
 
 /* Gradients of dsa_idx_norm_rope: of its inputs (dq, dk, in_dtype, strides of
  * their own) and of its weights and biases (FP32 [head_dim], summed over tokens
- * and heads; NULL: not wanted, biases of DSA_NORM_RMS always NULL), from the
- * gradients dq_out, dk_out of its outputs
+ * and heads; NULL: not wanted, those of biases always NULL with DSA_NORM_RMS,
+ * which takes none), from the gradients dq_out, dk_out of its outputs
  * (grad_dtype) and the forward's inputs; no other statistics are kept.  Weight
  * gradients of a call without weights are those of weights of one.  Outputs
  * share no memory with inputs.  ws as for the cache's operators.  The same

@@ -44,6 +44,7 @@ dsa_status_t fill(NormRopeParams* p, const void* q, int64_t q_stride, const void
   for (dsa_dtype_t t : {in_dtype, out_dtype, weight_dtype})
     if (t != DSA_DTYPE_F32 && t != DSA_DTYPE_BF16) return fail(DSA_ERR_INVALID_ARG, "dtype");
   if (norm != DSA_NORM_RMS && norm != DSA_NORM_LAYER) return fail(DSA_ERR_INVALID_ARG, "norm");
+  if (norm == DSA_NORM_RMS && (q_bias || k_bias)) return fail(DSA_ERR_INVALID_ARG, "an RMS norm takes no biases");
   if (!(eps >= 0.f) || std::isinf(eps)) return fail(DSA_ERR_INVALID_ARG, "eps must be finite and >= 0");
   if (rope_dim < 0 || rope_dim > head_dim || rope_dim % 8 != 0)
     return fail(DSA_ERR_INVALID_ARG, "rope_dim must be a multiple of 8 in [0, head_dim]");

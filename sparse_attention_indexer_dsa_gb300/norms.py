@@ -103,9 +103,10 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[to
     q [tokens, n_heads, head_dim], k [tokens, n_kv_heads, head_dim] or None,
     fp32 or bf16 (views with a token stride, as slices of one projection, are
     taken as they are); positions int32 [tokens]; weights and biases [head_dim],
-    fp32 or bf16, None: ones and zeros.  norm "rms" or "layer".  rope_dim: the
-    first dimensions of a head are rotated (default: all; 0: none), by rope_base
-    or by the rope_dim / 2 host values inv_freq.  Returns (q_out, k_out or None)
+    fp32 or bf16, None: ones and zeros.  norm "rms", which takes no biases (none
+    of its gradients would be theirs), or "layer".  rope_dim: the first
+    dimensions of a head are rotated (default: all; 0: none), by rope_base or by
+    the rope_dim / 2 host values inv_freq.  Returns (q_out, k_out or None)
     in out_dtype (default: q's); `out` is such a pair to write into, and may be
     (q, k) itself.  No gradient is recorded: norm_rope_backward gives it."""
     shape, dev, dt, Hk, rows, R, pos, wp, wt, freq = _inputs(q, k, positions, (q_weight, k_weight, q_bias, k_bias), norm,

@@ -294,3 +294,21 @@ def test_more_than_32_bits_of_elements():
     del got
     a, b = dsa.norm_rope_backward(g, None, q, None, at, w[0]), dsa.norm_rope_backward(d, None, tail, None, pos, w[0])
     assert torch.equal(a.q[-50:], b.q) and not a.q[:-50].any()
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+def test_whatever_the_forward_call_takes_has_a_gradient(norm):
+    rng = np.random.default_rng(16)
+    q, k, pos, _ = inputs(rng, 21, 3, 2, 64, "f32", norm, strided=False)
+    qw, kw, qb, kb = (torch.from_numpy(rng.standard_normal(64)).cuda().float() for _ in range(4))
+    if norm == "rms":
+        for b in (dict(q_bias=qb), dict(k_bias=kb)):
+            with pytest.raises(dsa.DsaError, match="bias"):
+                dsa.norm_rope(q, k, pos, qw, kw, norm=norm, **b)
+        return
+    w = [qw, kw, qb, kb]
+    check_forward(q, k, pos, w, dsa.norm_rope(q, k, pos, *w, norm=norm, eps=EPS), norm, 64, False, "f32")
+    d = torch.from_numpy(rng.standard_normal((21, 5, 64))).cuda().float()
+    g = grads(q, k, pos, w, d[:, :3], d[:, 3:], norm, 64, False)
+    assert all(t is not None for t in g)
+    check_backward(q, k, pos, w, d[:, :3], d[:, 3:], g, norm, 64, False, "f32")

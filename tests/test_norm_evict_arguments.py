@@ -192,3 +192,16 @@ def test_outputs_are_packed(monkeypatch):
     assert paged._empty((2, 3), torch.int32, torch.device("cpu")).device.type == "cpu"   # another device: torch.empty
     monkeypatch.setattr(paged, "_strided", None)
     assert paged._empty((2, 3), torch.int32, torch.device("cpu")).shape == (2, 3)
+
+
+@pytest.mark.parametrize("change", [dict(q_bias=A), dict(k_bias=A), dict(q_bias=A, k_bias=A)])
+def test_an_rms_norm_takes_no_biases(lib, change):
+    """The backward call has no gradient for them, so the forward call refuses them."""
+    assert call(lib.dsa_idx_norm_rope, NORM, **change) == BAD
+    assert b"bias" in lib.dsa_idx_last_error()
+
+
+@pytest.mark.no_device
+def test_a_layer_norm_takes_biases(lib):
+    assert call(lib.dsa_idx_norm_rope, NORM, norm=1, q_bias=A, k_bias=A) not in REFUSED
+    assert call(lib.dsa_idx_norm_rope_backward, BACK, norm=1, dq_bias=A, dk_bias=A) not in REFUSED
