@@ -120,16 +120,33 @@ _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_devi
 _strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
+_modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
+_fills = torch.are_deterministic_algorithms_enabled
+
+
 def _empty(shape: tuple, dtype, device: torch.device) -> torch.Tensor:
     """torch.empty; on the current device without the dispatch around the allocation (two of them before a launch:
-    7.3 us of host time in place of 4.2)."""
-    if _strided is None or _current() != device.index:
+    7.3 us of host time in place of 4.2), unless something wants to see or fill what is allocated.  The function that does
+    it is not torch's public one: where it does not give what torch.empty gives, it is not called again."""
+    global _strided
+    if _strided is None or _modes is None or _modes() or _fills() or _current() != device.index:
         return torch.empty(shape, dtype=dtype, device=device)
-    strides, n = [1], 1
-    for s in shape[:0:-1]:
-        n *= s
-        strides.append(n)
-    return _strided(shape, tuple(strides[::-1]), dtype)
+    if len(shape) == 3:
+        strides = (shape[1] * shape[2], shape[2], 1)
+    else:
+        strides, n = [1], 1
+        for s in shape[:0:-1]:
+            n *= s
+            strides.append(n)
+        strides = tuple(strides[::-1])
+    try:
+        t = _strided(shape, strides, dtype)
+        if t.dtype is dtype and t.shape == shape:
+            return t
+    except (TypeError, AttributeError):   # another signature (what fails else, fails in torch.empty too)
+        pass
+    _strided = None
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _call(fn, device: torch.device, args) -> int:

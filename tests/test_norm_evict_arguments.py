@@ -205,3 +205,50 @@ def test_an_rms_norm_takes_no_biases(lib, change):
 def test_a_layer_norm_takes_biases(lib):
     assert call(lib.dsa_idx_norm_rope, NORM, norm=1, q_bias=A, k_bias=A) not in REFUSED
     assert call(lib.dsa_idx_norm_rope_backward, BACK, norm=1, dq_bias=A, dk_bias=A) not in REFUSED
+
+
+@pytest.mark.parametrize("other", [
+    lambda: torch.zeros(1),                                             # other arguments
+    lambda shape, strides, dtype: None,                                 # another result
+    lambda shape, strides, dtype: torch.zeros(shape, dtype=torch.float64),
+    lambda shape, strides, dtype: torch.zeros((*shape, 1), dtype=dtype),
+])
+def test_an_allocator_of_another_kind_is_left_alone(monkeypatch, other):
+    """torch's own function behind torch.empty may change from one version to the next: outputs then come from
+    torch.empty, from the first call on."""
+    from sparse_attention_indexer_dsa_gb300 import paged
+    cpu, calls = torch.device("cpu"), []
+
+    def strange(*args):
+        calls.append(args)
+        return other(*args)
+    monkeypatch.setattr(paged, "_current", lambda: cpu.index)
+    monkeypatch.setattr(paged, "_strided", strange)
+    for _ in range(3):
+        t = paged._empty((3, 4, 64), torch.bfloat16, cpu)
+        assert t.shape == (3, 4, 64) and t.dtype is torch.bfloat16 and t.is_contiguous()
+    assert len(calls) == 1 and paged._strided is None
+
+
+def test_who_watches_allocations_sees_outputs(monkeypatch):
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    from sparse_attention_indexer_dsa_gb300 import paged
+    cpu, seen = torch.device("cpu"), []
+    monkeypatch.setattr(paged, "_current", lambda: cpu.index)
+    monkeypatch.setattr(paged, "_strided", lambda shape, strides, dtype: torch.zeros(shape, dtype=dtype))
+
+    class Watch(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            seen.append(str(func))
+            return func(*args, **(kwargs or {}))
+    with Watch():
+        paged._empty((3, 4), torch.bfloat16, cpu)
+    assert any("empty" in s for s in seen)
+    monkeypatch.setattr(paged, "_strided", lambda *a: pytest.fail("not under deterministic algorithms"))
+    torch.use_deterministic_algorithms(True)
+    try:
+        t = paged._empty((3, 4), torch.float32, cpu)
+        assert torch.isnan(t).all()       # torch fills what it allocates
+    finally:
+        torch.use_deterministic_algorithms(False)
