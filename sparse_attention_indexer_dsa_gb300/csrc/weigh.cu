@@ -18,9 +18,10 @@
 //
 // 8-bit rows: E4M3 is exact in FP16, and with at most eight query rows so are the
 // queries once each row is scaled by a power of two, unless its elements span
-// more than 2^31.  The codes then take one conversion to a pair, and the blocks'
-// scales are applied to the products of a block.  Else the rows are widened to BF16,
-// in which E4M3 x 2^e is exact (32 query rows, 32 such sequences: 165 us).
+// more than 2^31 or are so far from one that the scaled products could leave FP32.
+// The codes then take one conversion to a pair, and the blocks' scales are applied
+// to the products of a block.  Else the rows are widened to BF16, in which E4M3 x
+// 2^e is exact (32 query rows, 32 such sequences: 165 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -173,13 +174,16 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
         top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
       }
-      // the largest element goes to exponent 14, the least bit of the smallest stays at 2^-24 or above
+      // the largest element goes to exponent 14, the least bit of the smallest stays at 2^-24 or above; and FP32 holds
+      // the scaled products wherever it holds the logit: one that leaves it stands for a logit of 2^24 and more, of
+      // whose weight nothing is left in FP32, and what it loses at its lower end is below 2^-40 of a logit
       const int e_top = top >> 7, e_low = low >> 7;
-      const bool fits = top == 0 || (e_top >= 15 && e_top < 255 && e_low >= 1 && e_top - e_low <= 31);
+      const float back = top == 0 ? 1.f : __uint_as_float((uint32_t)max(e_top - 14, 0) << 23), scale = back * p.scale_log2;
+      const bool fits = (top == 0 || (e_top >= 15 && e_top < 255 && e_low >= 1 && e_top - e_low <= 31)) && scale >= 0x1p-104f &&
+                        scale <= 0x1p104f;
       half = __all_sync(0xffffffffu, fits);
       if (half) {
         const float f = top == 0 ? 1.f : __uint_as_float((uint32_t)(14 + 254 - e_top) << 23);   // 2^(14 - (e_top - 127))
-        const float back = top == 0 ? 1.f : __uint_as_float((uint32_t)(e_top - 14) << 23);
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c) {
           uint32_t w[4] = {qf[c].x, qf[c].y, qf[c].z, qf[c].w};
@@ -191,8 +195,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
           qf[c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         // of columns 2 t and 2 t + 1 (rows that lanes 8 t and 8 t + 4 hold)
-        const float b0 = __shfl_sync(0xffffffffu, back, 8 * t), b1 = __shfl_sync(0xffffffffu, back, 8 * t + 4);
-        colscale = make_float2(b0 * p.scale_log2, b1 * p.scale_log2);
+        colscale = make_float2(__shfl_sync(0xffffffffu, scale, 8 * t), __shfl_sync(0xffffffffu, scale, 8 * t + 4));
       }
     }
 

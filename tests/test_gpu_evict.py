@@ -848,3 +848,15 @@ def test_select_of_eight_blocks_and_of_rows_read_again(lens, kv, shared, ties):
         assert dsa.read_status(ws) == 0
         want, wn = choice(b, w, budget, sinks, recent, shared)
         assert np.array_equal(host(n), wn) and np.array_equal(host(kept), want), (budget, sinks, recent)
+
+
+# ---------------------------------------------------------------- far queries against far keys
+
+@pytest.mark.parametrize("prec", ["mxfp8", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", [-112, -100, -60, 60, 100, 112])
+def test_weigh_far_queries_and_far_keys(prec, D, far):
+    """Query elements around 2^far, keys around 2^-far: their products, and the logits, are ordinary numbers."""
+    rng = np.random.default_rng([77, D, 200 + far])
+    b = Batch(rng, [(1, 130)], 1, D, 16, prec, values_too=False, std=2.0 ** -far)
+    check_weigh(b, rng, 4, std=2.0 ** far, scale=0.1)
