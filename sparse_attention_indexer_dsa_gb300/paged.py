@@ -133,6 +133,8 @@ def _empty(shape: tuple, dtype, device: torch.device) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
     if len(shape) == 3:
         strides = (shape[1] * shape[2], shape[2], 1)
+    elif len(shape) == 1:
+        strides = (1,)
     else:
         strides, n = [1], 1
         for s in shape[:0:-1]:
