@@ -491,8 +491,8 @@ typedef enum { DSA_NORM_RMS = 0, DSA_NORM_LAYER = 1 } dsa_norm_t;
  *   y = R(pos) (n * weight + bias)
  * in FP32, rounded once.  R turns pair i of the first rope_dim elements (i and
  * i + rope_dim/2, or with rope_interleaved 2i and 2i + 1) by pos * freq_i,
- * freq_i = rope_base^(-2i/rope_dim) or inv_freq[i] in double; angles are within
- * 2^-25 of a turn of that product at every position.
+ * freq_i = rope_base^(-2i/rope_dim) or inv_freq[i] in double, at most 2^48 either
+ * way; angles are within 2^-25 of a turn of that product at every position.
  *   q, k        device [total_tokens, n_heads (n_kv_heads), head_dim] in_dtype,
  *               16-byte aligned; q_stride ..: elements from one token to the
  *               next (0 = packed; a multiple of 16 bytes), heads packed inside

@@ -16,6 +16,9 @@ namespace {
 
 int elem_bytes(dsa_dtype_t t) { return t == DSA_DTYPE_BF16 ? 2 : 4; }
 
+// What the parts of 1 / (2 pi) below leave out grows with the frequency: at the farthest position 2^-28 of a turn here.
+constexpr double kMostFreq = 0x1p48;
+
 // A frequency as turns per position, modulo one, in units of 2^-64.  A position multiplies what is lost
 // here by up to 2^31, so 1 / (2 pi) comes in two parts and the product's rounding is kept.
 uint64_t turns_of(double freq) {
@@ -61,7 +64,7 @@ dsa_status_t fill(NormRopeParams* p, const void* q, int64_t q_stride, const void
   }
   if (inv_freq) {
     for (int i = 0; i < rope_dim / 2; ++i) {
-      if (!std::isfinite(inv_freq[i])) return fail(DSA_ERR_INVALID_ARG, "inv_freq must be finite");
+      if (!(std::fabs(inv_freq[i]) <= kMostFreq)) return fail(DSA_ERR_INVALID_ARG, "inv_freq must be finite, and 2^48 at most");
       p->rope.freq[i] = turns_of(inv_freq[i]);
     }
   } else if (rope_dim > 0) {
@@ -70,6 +73,9 @@ dsa_status_t fill(NormRopeParams* p, const void* q, int64_t q_stride, const void
     static thread_local int dim = 0;
     static thread_local uint64_t table[64];
     if (base != rope_base || dim != rope_dim) {
+      // (a base below one: its frequencies rise)
+      if (!(std::pow(rope_base, -2.0 * (rope_dim / 2 - 1) / (double)rope_dim) <= kMostFreq))
+        return fail(DSA_ERR_INVALID_ARG, "rope_base gives frequencies above 2^48");
       for (int i = 0; i < rope_dim / 2; ++i) table[i] = turns_of(std::pow(rope_base, -2.0 * i / (double)rope_dim));
       base = rope_base;
       dim = rope_dim;

@@ -312,3 +312,20 @@ def test_whatever_the_forward_call_takes_has_a_gradient(norm):
     g = grads(q, k, pos, w, d[:, :3], d[:, 3:], norm, 64, False)
     assert all(t is not None for t in g)
     check_backward(q, k, pos, w, d[:, :3], d[:, 3:], g, norm, 64, False, "f32")
+
+
+def test_angles_of_the_highest_frequencies():
+    """As test_angles_of_the_farthest_positions, for frequencies up to their bound."""
+    from fractions import Fraction
+    pi = Fraction(314159265358979323846264338327950288419716939937510582097494459, 10 ** 62)
+    rng = np.random.default_rng(17)
+    at = [0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1234567890]
+    q, k, _, w = inputs(rng, len(at), 3, 1, 64, "f32", "rms")
+    pos = torch.tensor(at, dtype=torch.int32, device="cuda")
+    freq = [float(f) for f in np.concatenate([2.0 ** rng.uniform(20, 48, 28), [2.0 ** 48, -2.0 ** 48, 2.0 ** 47 + 1, 3.0]])]
+    got = dsa.norm_rope(q, k, pos, *w, eps=EPS, inv_freq=freq)
+    ang = np.array([[float((Fraction(f) * p / (2 * pi)) % 1) for f in freq] for p in at]) * (2 * np.pi)
+    for x, y, wi in ((q, got[0], w[0]), (k, got[1], w[1])):
+        a = (host(x), host(wi), None, host(pos))
+        want = R.rotate(R.forward(*a, "rms", EPS, 0, False), ang, 64, False)
+        close(y, want, R.forward_tol(*a, "rms", EPS, 64, False, "f32", want), "high")

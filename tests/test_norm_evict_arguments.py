@@ -252,3 +252,23 @@ def test_who_watches_allocations_sees_outputs(monkeypatch):
         assert torch.isnan(t).all()       # torch fills what it allocates
     finally:
         torch.use_deterministic_algorithms(False)
+
+
+def test_frequencies_have_a_bound(lib):
+    """Beyond it an angle is not what its frequency says."""
+    for f in (2.0 ** 49, -2.0 ** 49, 1.7e308, -1.7e308):
+        a = (ctypes.c_double * 32)(*([0.5] * 31 + [f]))
+        assert call(lib.dsa_idx_norm_rope, NORM, inv_freq=ctypes.addressof(a)) == BAD
+    for base in (1e-300, 5e-324, 1e-20):
+        assert call(lib.dsa_idx_norm_rope, NORM, rope_base=base) == BAD
+        assert call(lib.dsa_idx_norm_rope_backward, BACK, rope_base=base) == BAD
+        assert call(lib.dsa_idx_norm_rope, NORM, rope_base=base) == BAD      # and again
+
+
+@pytest.mark.no_device
+def test_frequencies_up_to_the_bound_are_taken(lib):
+    a = (ctypes.c_double * 32)(*([0.5] * 30 + [2.0 ** 48, -2.0 ** 48]))
+    assert call(lib.dsa_idx_norm_rope, NORM, inv_freq=ctypes.addressof(a)) not in REFUSED
+    for base in (0.5, 1.0, 1e-14, 1e300):
+        assert call(lib.dsa_idx_norm_rope, NORM, rope_base=base) not in REFUSED
+    assert call(lib.dsa_idx_norm_rope, NORM, rope_dim=8, rope_base=1e-18) not in REFUSED
