@@ -85,6 +85,8 @@ def evict_select(weights: torch.Tensor, cu_seqlens_k: torch.Tensor, page_table: 
     weights.  Returns (kept int32 [num_seqs, n_kv_heads or 1, budget],
     ascending, then -1, kept_len int32 [num_seqs]); `out` is such a pair to
     write into.  `ws` from cache_workspace."""
+    if budget >> 31 or max_seqlen_k >> 31 or sinks >> 31 or recent >> 31:   # (ctypes would drop the upper bits)
+        raise ValueError("budget, max_seqlen_k, sinks and recent must be in [0, 2^31)")
     if weights.dim() != 3:
         raise ValueError("weights must be [num_pages, n_kv_heads, page_size]")
     if not weights.is_cuda:

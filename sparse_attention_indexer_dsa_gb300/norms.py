@@ -69,6 +69,8 @@ def _inputs(q, k, positions, weights, norm, rope_dim, inv_freq):
         Hk = k.shape[1]
         kp, kst = _like(k, "k", (T, Hk, D), dt, dev)
     R = D if rope_dim is None else rope_dim
+    if R >> 31:   # (ctypes would drop the upper bits)
+        raise ValueError("rope_dim must be a multiple of 8 in [0, head_dim]")
     pos = None
     if R:
         if positions is None:

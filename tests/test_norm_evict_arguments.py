@@ -272,3 +272,21 @@ def test_frequencies_up_to_the_bound_are_taken(lib):
     for base in (0.5, 1.0, 1e-14, 1e300):
         assert call(lib.dsa_idx_norm_rope, NORM, rope_base=base) not in REFUSED
     assert call(lib.dsa_idx_norm_rope, NORM, rope_dim=8, rope_base=1e-18) not in REFUSED
+
+
+@pytest.mark.parametrize("change", [dict(budget=(1 << 32) + 4), dict(sinks=1 << 32), dict(recent=(1 << 32) + 1), dict(max_seqlen_k=1 << 32),
+                                    dict(sinks=-1), dict(max_seqlen_k=1 << 31)])
+def test_sizes_beyond_32_bits_are_refused(change):
+    """What ctypes hands on is 32 bits: sinks of 2^32 would be none."""
+    w = torch.zeros(3, 2, 16)
+    with pytest.raises(ValueError, match="2.31"):
+        dsa.evict_select(w, None, None, **{**dict(budget=4, max_seqlen_k=10), **change})
+
+
+def test_a_rotation_beyond_32_bits_is_refused(monkeypatch):
+    class Cuda(torch.Tensor):      # a CPU tensor that passes for one on the GPU
+        is_cuda = True
+    q = torch.zeros(4, 2, 64).as_subclass(Cuda)
+    for dim in ((1 << 32) + 64, 1 << 31, -8):
+        with pytest.raises(ValueError, match="multiple of 8"):
+            norms._inputs(q, None, None, (None,) * 4, "rms", dim, None)
