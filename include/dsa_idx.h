@@ -504,8 +504,10 @@ typedef enum { DSA_NORM_RMS = 0, DSA_NORM_LAYER = 1 } dsa_norm_t;
  *               and k themselves (same type and stride), else no shared memory
  * n_kv_heads = 0: queries alone (k, k_out not used).  head_dim 64 or 128, at
  * most 1024 heads each, rope_dim a multiple of 8 in [0, head_dim].  A row of
- * zeros with eps = 0 gives NaN, a non-finite element makes its row non-finite;
- * other rows are not touched by it. */
+ * zeros with eps = 0 gives NaN.  A NaN makes its row NaN, as does an infinite
+ * element with DSA_NORM_LAYER; with DSA_NORM_RMS it becomes NaN (rotated: its
+ * pair) and the row's others zeros, x / inf.  Other rows are not touched by it.  Squares are summed in FP32: a row's largest element (less the
+ * mean, DSA_NORM_LAYER) is at most 2^60, and with eps = 0 at least 2^-60. */
 dsa_status_t dsa_idx_norm_rope(
     const void* q, int64_t q_stride, const void* k, int64_t k_stride,
     dsa_dtype_t in_dtype, const void* q_weight, const void* k_weight,

@@ -32,26 +32,25 @@ namespace dsa {
 
 namespace {
 
-// Where a lane's two groups of four are, and the index of the angle of each of its four pairs
-// ((e, e + 4), or (2e, 2e + 1) interleaved); -1: not rotated.
+// Where a lane's two groups of four are, whether they are rotated (dim is a multiple of 8: all or none) and the index
+// of the angle of the first of its four pairs, (e, e + 4), or (2e, 2e + 1) interleaved.
 template <int D>
 struct Lane {
   int a, b;
-  int angle[4];
+  bool rot;
+  int angle;
   __device__ __forceinline__ Lane(const RopeTable& r, int l) {
     const int half = r.dim / 2;
     if (r.interleaved) {
       a = 8 * l;
       b = a + 4;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) angle[e] = a + 2 * e < r.dim ? a / 2 + e : -1;
+      rot = a < r.dim;
     } else {
-      const bool rot = 4 * l < half;
+      rot = 4 * l < half;
       a = rot ? 4 * l : half + 4 * l;                 // (r.dim + (4 l - half))
       b = rot ? a + half : a + (D - r.dim) / 2;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) angle[e] = rot ? 4 * l + e : -1;
     }
+    angle = 4 * l;
   }
 };
 
@@ -165,22 +164,26 @@ struct Turn {
   float cs[4], sn[4];
 };
 
-// The pairs turned by their angles (BACK: against them).
+__device__ __forceinline__ float keep(float v, uint32_t mask) { return __uint_as_float(__float_as_uint(v) & mask); }
+
+// The pairs turned by their angles (BACK: against them).  mask: all bits, or none where the lane's elements are not
+// rotated (0 times a non-finite element would reach its partner).
 template <bool BACK>
-__device__ __forceinline__ void turn(Elems& y, const Turn& t, bool interleaved) {
+__device__ __forceinline__ void turn(Elems& y, const Turn& t, bool interleaved, uint32_t mask) {
   if (interleaved) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float a = y.v[e].x, b = y.v[e].y, s = BACK ? -t.sn[e] : t.sn[e];
-      y.v[e] = make_float2(fmaf(a, t.cs[e], -b * s), fmaf(b, t.cs[e], a * s));
+      y.v[e] = make_float2(fmaf(a, t.cs[e], -keep(b, mask) * s), fmaf(b, t.cs[e], keep(a, mask) * s));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float2 a = y.v[i], b = y.v[i + 2], c = make_float2(t.cs[2 * i], t.cs[2 * i + 1]);
       const float2 s = make_float2(t.sn[2 * i], t.sn[2 * i + 1]), m = make_float2(-s.x, -s.y);
-      y.v[i] = __ffma2_rn(a, c, __fmul2_rn(b, BACK ? s : m));
-      y.v[i + 2] = __ffma2_rn(b, c, __fmul2_rn(a, BACK ? m : s));
+      const float2 ka = make_float2(keep(a.x, mask), keep(a.y, mask)), kb = make_float2(keep(b.x, mask), keep(b.y, mask));
+      y.v[i] = __ffma2_rn(a, c, __fmul2_rn(kb, BACK ? s : m));
+      y.v[i + 2] = __ffma2_rn(b, c, __fmul2_rn(ka, BACK ? m : s));
     }
   }
 }
@@ -193,8 +196,8 @@ __device__ __forceinline__ Turn angles(const RopeTable& r, int pos, const Lane<D
   for (int e = 0; e < 4; ++e) {
     t.cs[e] = 1.f;
     t.sn[e] = 0.f;
-    if (at.angle[e] >= 0) {
-      const uint64_t turns = (uint64_t)(int64_t)pos * r.freq[at.angle[e]];
+    if (at.rot) {
+      const uint64_t turns = (uint64_t)(int64_t)pos * r.freq[at.angle + e];
       // the upper 32 bits as a signed part of a turn; sincospif takes half turns
       sincospif((float)(int32_t)(uint32_t)(turns >> 32) * 0x1p-31f, &t.sn[e], &t.cs[e]);
     }
@@ -227,6 +230,7 @@ __global__ void __launch_bounds__(kNormThreads, Batch<IN>::kBlocks) norm_rope_ke
   const int tok = (int)(task / p.parts), part = (int)(task - (int64_t)tok * p.parts);
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const Lane<D> at(p.rope, lane % LPR);
+  const uint32_t mask = at.rot ? ~0u : 0u;
   const int pos = p.rope.dim > 0 ? __ldg(p.pos + tok) : 0;
   Turn tn;
   bool turned = false;
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(kNormThreads, Batch<IN>::kBlocks) norm_rope_ke
         normalise<D, LAYER>(x, p.eps);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x.v[e] = shift ? __ffma2_rn(x.v[e], w.v[e], b.v[e]) : __fmul2_rn(x.v[e], w.v[e]);
-        turn<false>(x, tn, p.rope.interleaved);
+        turn<false>(x, tn, p.rope.interleaved, mask);
         const int h = h0 + i * RPS;
         if (h < sh.hi) {
           store4<OUT>(p.y[kind], y0 + h * D + at.a, x.v);
@@ -350,6 +354,7 @@ __global__ void __launch_bounds__(kNormThreads, kBackBlocks) norm_rope_back_kern
   const NormRopeParams& p = q.f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR;
   const Lane<D> at(p.rope, lane % LPR);
+  const uint32_t mask = at.rot ? ~0u : 0u;
   uint8_t* const own = ring + warp * kBackStages * St::kBytes;
   const uint32_t sown = (uint32_t)__cvta_generic_to_shared(own);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the sums' kernel waits for this one's end)
@@ -421,7 +426,7 @@ __global__ void __launch_bounds__(kNormThreads, kBackBlocks) norm_rope_back_kern
       read4<GRAD>(grad[1], slot + St::kX, r * D + at.b);
       Elems x = widen<IN>(raw), g = widen<GRAD>(grad);
       const float inv = normalise<D, LAYER>(x, p.eps);
-      turn<true>(g, tn, p.rope.interleaved);
+      turn<true>(g, tn, p.rope.interleaved, mask);
       float2 dot, sum;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

@@ -329,3 +329,71 @@ def test_angles_of_the_highest_frequencies():
         a = (host(x), host(wi), None, host(pos))
         want = R.rotate(R.forward(*a, "rms", EPS, 0, False), ang, 64, False)
         close(y, want, R.forward_tol(*a, "rms", EPS, 64, False, "f32", want), "high")
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("rope_dim", [0, 64])
+def test_what_a_non_finite_element_does_to_its_row(norm, value, rope_dim):
+    rng = np.random.default_rng(18)
+    q, _, pos, w = inputs(rng, 7, 4, 1, 128, "f32", norm, strided=False)
+    kw = dict(q_bias=w[2], norm=norm, eps=EPS, rope_dim=rope_dim)
+    want, _ = dsa.norm_rope(q, None, pos, w[0], **kw)
+    q2 = q.clone()
+    q2[4, 2, 10] = value
+    got, _ = dsa.norm_rope(q2, None, pos, w[0], **kw)
+    rows = torch.ones(7, 4, dtype=torch.bool, device="cuda")
+    rows[4, 2] = False
+    assert torch.equal(got[rows], want[rows])
+    lost = torch.ones(128, dtype=torch.bool, device="cuda")
+    if norm == "rms" and not np.isnan(value):      # x / inf but for the element, or its pair
+        lost[:] = False
+        lost[[10, 42] if rope_dim else [10]] = True
+        assert (got[4, 2][~lost] == 0).all()
+    assert got[4, 2][lost].isnan().all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rope_dim,at,pair", [(0, 10, 10), (64, 100, 100), (64, 10, None)])
+def test_what_a_non_finite_gradient_does_to_the_sums(norm, inter, value, rope_dim, at, pair):
+    """A weight's gradient is the sum over its own column, and its partner's where the two are rotated."""
+    if pair is None:
+        pair = at ^ 1 if inter else at + 32
+    rng = np.random.default_rng(20)
+    q, k, pos, w = inputs(rng, 40, 3, 2, 128, "f32", norm, strided=False)
+    d = torch.from_numpy(rng.standard_normal((40, 5, 128))).cuda().float()
+    dq, dk = d[:, :3].contiguous(), d[:, 3:].contiguous()
+    want = grads(q, k, pos, w, dq, dk, norm, rope_dim, inter)
+    dq[7, 1, at] = value
+    got = grads(q, k, pos, w, dq, dk, norm, rope_dim, inter)
+    rest = torch.ones(128, dtype=torch.bool, device="cuda")
+    rest[[at, pair]] = False
+    for a, b in ((got.q_weight, want.q_weight), (got.q_bias, want.q_bias)):
+        if a is not None:
+            assert torch.equal(a[rest], b[rest]) and not a[at].isfinite()
+    for a, b in ((got.k, want.k), (got.k_weight, want.k_weight), (got.k_bias, want.k_bias)):
+        assert a is b is None or torch.equal(a, b)
+    rows = torch.ones(40, 3, dtype=torch.bool, device="cuda")
+    rows[7, 1] = False
+    assert torch.equal(got.q[rows], want.q[rows])
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("log2", [-60, 60])
+def test_the_largest_and_smallest_rows(norm, D, log2):
+    """Largest elements of 2^60, of 2^-60 without eps, every element as large or one alone."""
+    rng = np.random.default_rng([19, D])
+    x = np.ldexp(np.where(rng.random((6, 2, D)) < 0.5, -1.0, 1.0), log2)
+    x[3:, :, 1:] *= 2.0 ** -9
+    if norm == "layer":
+        x -= x.mean(-1, keepdims=True)
+        x *= 2.0 ** log2 / np.abs(x).max(-1, keepdims=True)
+        x = x.astype(np.float32).astype(np.float64)
+    q = torch.from_numpy(x).cuda().float()
+    got, _ = dsa.norm_rope(q, None, None, norm=norm, eps=0.0, rope_dim=0)
+    a = (x, None, None, np.zeros(6), norm, 0.0, 0, False)
+    want = R.forward(*a)
+    close(got, want, R.forward_tol(*a, "f32", want), "far")
