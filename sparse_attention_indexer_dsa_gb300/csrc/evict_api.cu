@@ -42,8 +42,8 @@ dsa_status_t dsa_idx_cache_weigh(const void* q, int64_t q_stride, const float* l
   // The attention's own scale, so that weights and lse fit together.  The tensor cores' FP32 sums truncate: a logit of
   // 128 products of BF16 values comes out short by 0.9 - 1.5e-7 of itself on average, one of 64 by 0.4 - 0.8e-7
   // (mma.sync and tcgen05 alike; rows normal, with outliers, uniform, of one sign).  The attention's lse is short alike:
-  // with it a token's weights add up to its heads within 2e-7 at mean logits up to 30; with the lse of exact
-  // logits they are short by the logit's part (2.7e-6 at 25).
+  // with it the weights of a chunk's tokens add up to their heads within 2.5e-7 on average at mean logits up to 30;
+  // with the lse of exact logits they are short by the logit's part (2.7e-6 at 25).
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   if (!(sm_scale >= 0.f) || std::isinf(p.scale_log2))
     return fail(DSA_ERR_INVALID_ARG, "sm_scale and sm_scale * log2(e) must be finite and >= 0");

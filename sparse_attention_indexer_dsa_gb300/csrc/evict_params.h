@@ -29,9 +29,17 @@ struct WeighParams {
 
 // Query rows of a sequence up to which its keys stream past them, 8-bit ones and BF16 ones (the tile kernel has to
 // widen 8-bit keys to BF16 first, and its query tiles are empty but for these rows).  Streaming / tiles, us, 32 sequences of
-// 2048 - 8192 keys, 8 key heads of 128 dimensions:
-//   BF16     16 rows  75 / 98     32 rows 128 / 94     64 rows 217 / 97
-//   MXFP8    32 rows 103 / 155    64 rows 156 / 157    128 rows 425 / 179
+// 2048 - 8192 keys, 8 key heads:
+//   128 elements   16 rows       32 rows       64 rows       128 rows
+//     BF16         75 / 97      127 / 93      218 / 96      403 / 115
+//     MXFP8        78 / 163     104 / 160     158 / 158     266 / 180
+//     FP8          78 / 164     105 / 163     160 / 163     267 / 176
+//   64 elements
+//     BF16         44 / 84       65 / 82      113 / 89      207 / 111
+//     MXFP8        52 / 102      72 / 97      114 / 106     200 / 127
+//     FP8          53 / 102      73 / 97      115 / 106     202 / 127
+// One bound for both sizes of a head: of 64 elements 32 rows of BF16 take 82 in place of 65, 64 8-bit ones 114 in
+// place of 106.
 constexpr int kWeighStepRows8 = 64, kWeighStepRows16 = 16;
 constexpr int kWeighCols = 256;    // query rows of a tile
 constexpr int kWeighKeys = 256;    // keys of a unit

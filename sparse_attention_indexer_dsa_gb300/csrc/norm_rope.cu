@@ -19,8 +19,8 @@
 // FP32 a position of 2^20 would be off by 0.06 rad).
 //
 // Memory bounds both directions where tokens are many: 32768 tokens of 72 heads of 128,
-// BF16, forward 201 us = 89 % of the copy rate, 16384 of 40 backward 87 us = 85 %; 9001 of
-// 25 heads of 64, FP32, 18 us = 71 %, less than two rounds of the GPU's warps.  A few tokens
+// BF16, forward 203 us = 88 % of the copy rate, 16384 of 40 backward 88 us = 84 %; 9001 of
+// 25 heads of 64, FP32, 17.7 us = 72 %, less than two rounds of the GPU's warps.  A few tokens
 // cost a launch, 3.7 us (7.2 backward, with the launch that adds up the blocks' sums).
 #include <cuda_bf16.h>
 
@@ -167,7 +167,8 @@ struct Turn {
 __device__ __forceinline__ float keep(float v, uint32_t mask) { return __uint_as_float(__float_as_uint(v) & mask); }
 
 // The pairs turned by their angles (BACK: against them).  mask: all bits, or none where the lane's elements are not
-// rotated (0 times a non-finite element would reach its partner).
+// rotated (0 times a non-finite element would reach its partner; without masks 201 and 87 us in place of the 203 and
+// 88 above, a branch around the turn 210 and 90).
 template <bool BACK>
 __device__ __forceinline__ void turn(Elems& y, const Turn& t, bool interleaved, uint32_t mask) {
   if (interleaved) {
@@ -216,7 +217,7 @@ struct Share {
 };
 
 // Rows of a lane that are requested together, and blocks of an SM: as many bytes under way either way.  Four and
-// three / two and four: 32768 tokens of 72 heads, BF16, 201 / 208 us; 9001 of 25 narrow ones, FP32, 20.8 / 18.0.
+// three / two and four: 32768 tokens of 72 heads, BF16, 203 / 211 us; 9001 of 25 narrow ones, FP32, 20.7 / 17.6.
 template <bool BF16>
 struct Batch {
   static constexpr int kRows = BF16 ? 4 : 2, kBlocks = BF16 ? 3 : 4;

@@ -20,7 +20,8 @@
 // warp some 1500 cycles for 32 rows, so eight warps do it, and the warps that weigh keep
 // their 80 registers (ragged chunks over FP8 rows 143 -> 141 us; 8 tokens of each of 32
 // sequences of 2048 - 8192 MXFP8 rows, which change keys all the time, 221 -> 157; four
-// warps of BF16 rows have but copies to issue, 96 us for the latter).  The
+// warps of BF16 rows have but copies to issue, 96 us for the latter).  At the 72
+// registers of its launch the form for 8-bit keys spills 96 - 132 bytes.  The
 // query tiles of all units in a row are shared out evenly: a block takes a
 // consecutive part, so that it changes keys seldom and all end together.  Where a
 // part's end divides a unit, a second kernel adds the pieces in their order.
@@ -41,7 +42,10 @@ using namespace attn;
 constexpr int kGroups = 64;            // sequences are counted in this many groups
 constexpr int kHalf = kWeighCols / 2;  // columns of a product and of a hand-over
 constexpr int kBiasRing = 4;
-constexpr int kUnitCost = 3;           // what a unit's change of keys counts beside its query tiles
+// What a unit's change of keys counts beside its query tiles.  1 / 3 / 6 / 12: ragged chunks of 1 - 1500 tokens of six
+// sequences over BF16 131 / 131 / 138 / 145 us, FP8 156 / 140 / 145 / 152, MXFP8 156 / 139 / 145 / 152; heads of 64
+// elements 123 / 129 / 136 / 143, 8-bit 127 / 131 / 140 / 146; 16 tokens of each of 32 sequences the same within 1 %.
+constexpr int kUnitCost = 3;
 constexpr int kMinPart = 2 * kUnitCost;   // length of a block's part, at least
 // barriers (halves: 2 * stream + half)
 enum { K_FULL = 0, K_EMPTY = 2, S_FULL = 4, S_EMPTY = 8, B_FULL = 12, B_EMPTY = B_FULL + kBiasRing, DRAIN = B_EMPTY + kBiasRing,
