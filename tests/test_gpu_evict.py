@@ -860,3 +860,32 @@ def test_weigh_far_queries_and_far_keys(prec, D, far):
     rng = np.random.default_rng([77, D, 200 + far])
     b = Batch(rng, [(1, 130)], 1, D, 16, prec, values_too=False, std=2.0 ** -far)
     check_weigh(b, rng, 4, std=2.0 ** far, scale=0.1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("prec", ["bf16", "fp8"])
+def test_weights_of_the_attentions_lse_add_up_to_the_heads(D, prec):
+    """Logits around 25 under the lse that paged_attention returns: whatever the sums of products lose, logits and lse lose
+    alike, so the weights of all tokens add up to their heads.
+
+    A row's sum is off by one factor: the roundings of lse (2^-24 |lse|), of lse log2(e) (as much) and of the attention's own
+    scaled maximum (as much), any sign, evenly spread at most: a variance of (3 2^-24 lse)^2 / 3.  The mean over N rows is held
+    to six standard deviations, and what does not average out: ex2 here and in the attention 2^-22 each, its log 2^-22."""
+    T, S, kv, group, page = 512, 4096, 2, 8, 64
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(D)
+
+    def rows(*shape):
+        x = torch.randn(shape, generator=gen, device="cuda")
+        return x * torch.where(torch.rand(shape, generator=gen, device="cuda") < 0.01, 8.0, 1.0)
+    c = dsa.paged_cache(S // page, page, kv, D, prec)
+    table = torch.randperm(S // page, generator=gen, device="cuda").to(torch.int32)[None]
+    cu = [torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (S, T)]
+    dsa.cache_write(c, rows(S, kv, D), rows(S, kv, D), cu[0], cu[0], table)
+    q = (2 * rows(T, kv * group, D)).bfloat16()
+    _, lse = dsa.paged_attention(q, c, cu[1], cu[0], table, T, S, return_lse=True)
+    w = dsa.paged_weights(c)
+    dsa.cache_weigh(c, w, q, lse, cu[1], cu[0], table, T, S)
+    off = float(w.double().sum() / (T * kv * group)) - 1
+    deviation = 2.0 ** -24 * float(3 * lse.double().square().mean() / (T * kv * group)) ** 0.5
+    assert abs(off) < 3 * 2.0 ** -22 + 6 * deviation, (off, deviation)
